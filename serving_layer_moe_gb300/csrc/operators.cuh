@@ -1,0 +1,80 @@
+// Declarations shared by the operators of include/moe_operators.h.
+#pragma once
+
+#include "cache.cuh"
+#include "../../include/moe_operators.h"
+
+namespace moe {
+
+// SMs of the current device (looked up once per device).
+int operator_sms();
+
+__device__ __forceinline__ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// expert of a grouped row, or of a row tile: the e with first[e] <= i < first[e + 1]
+__device__ __forceinline__ int expert_of(const int32_t* __restrict__ first, int E, int i) {
+  int lo = 0, hi = E;   // first[lo] <= i < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(first + mid) <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------------------
+// 4-bit blocks
+// ---------------------------------------------------------------------------
+// byte of the scale of block b of padded row r: tiles of 128 rows x 4 blocks
+__host__ __device__ __forceinline__ size_t scale_at(size_t r, int b, int block_groups) {
+  const uint32_t t = (uint32_t)(r & 127);
+  return ((r >> 7) * (size_t)block_groups + (size_t)(b >> 2)) * 512 + (t & 31) * 16 + (t >> 5) * 4 + (b & 3);
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  const uint32_t e = (code >> 3) & 15u, m = code & 7u;
+  if ((code & 127u) == 127u) return __uint_as_float(0x7fffffffu);
+  const float v = e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : (float)m * 0.001953125f;
+  return (code & 128u) ? -v : v;
+}
+// 2^(code - 127); 255 is NaN.  Code 0 is the subnormal 2^-127.
+__device__ __forceinline__ float e8m0_value(uint32_t code) {
+  return code == 255u ? __uint_as_float(0x7fffffffu) : code ? __uint_as_float(code << 23) : __uint_as_float(0x00400000u);
+}
+// nearest e4m3, ties to even, at most 448; x >= 0 or NaN (which gives the code of NaN)
+__device__ __forceinline__ uint32_t to_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(x));
+  return r & 0xffu;
+}
+// two e2m1 codes, lo in the low nibble: nearest, ties to even, at most 6
+__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// value of an e2m1 code (bit 3: sign)
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  const uint32_t m = c & 7u;
+  const float v = m < 2u ? 0.5f * (float)m : __uint_as_float((((m >> 1) + 126u) << 23) | ((m & 1u) << 22));
+  return (c & 8u) ? -v : v;
+}
+
+// Scale code of a block and the value of one step, from the bits of its largest |x|.
+template <bool NV>
+__device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float g, float& step) {
+  if (NV) {
+    if (amax_bits > 0x7f800000u) { step = 0.0f; return 0x7fu; }
+    const uint32_t code = to_e4m3(__fdiv_rn(__fdiv_rn(__uint_as_float(amax_bits), 6.0f), g));
+    step = e4m3_value(code) * g;
+    return code;
+  }
+  if (amax_bits > 0x7f800000u) { step = 0.0f; return 255u; }
+  const int x = amax_bits ? max((int)(amax_bits >> 23) - 129, -127) : 0;
+  step = e8m0_value((uint32_t)(x + 127));
+  return (uint32_t)(x + 127);
+}
+// what a value is multiplied by (MXFP4: 2^-X, exact) -- NVFP4 divides by the step
+__device__ __forceinline__ float e8m0_inverse(uint32_t code) { return e8m0_value(254u - code); }
+
+}  // namespace moe
