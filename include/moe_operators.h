@@ -39,7 +39,8 @@
  * rows past the matrix's end pad their tile; blocks pad with scale 0.  A stack of
  * G matrices of N rows starts every matrix on a new row tile; rows grouped by
  * expert start every expert on a new one (tile tiles[e]).  NVFP4: block 16, e4m3
- * scale, and one fp32 scale g per matrix; MXFP4: block 32, e8m0 scale, no g.
+ * scale, and one fp32 scale g per matrix; MXFP4: block 32, e8m0 scale.  Products and
+ * dequantisation multiply MXFP4 values by a g too if one is given; quantising takes none.
  */
 #ifndef MOE_OPERATORS_H
 #define MOE_OPERATORS_H

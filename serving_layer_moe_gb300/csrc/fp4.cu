@@ -73,21 +73,6 @@ __device__ __forceinline__ void load16(const X* p, float (&v)[16]) {
   }
 }
 
-// 16 values -> 8 bytes of codes
-template <bool NV>
-__device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t code, float step) {
-  uint32_t w[2] = {0u, 0u};
-  const bool none = !(step > 0.0f);
-  const float inv = NV ? 0.0f : e8m0_inverse(code);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float lo = NV ? __fdiv_rn(v[2 * i], step) : v[2 * i] * inv;
-    const float hi = NV ? __fdiv_rn(v[2 * i + 1], step) : v[2 * i + 1] * inv;
-    w[i >> 2] |= to_e2m1x2(lo, hi) << (8 * (i & 3));
-  }
-  return none ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
-}
-
 template <typename X, bool NV>
 __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(QuantArgs a) {
   __shared__ RowAt at[Q_ROWS];
@@ -146,7 +131,7 @@ __global__ void __launch_bounds__(Q_THREADS) dequantize_kernel(QuantArgs a, O* _
       } else {
         const uint2 q = __ldg(reinterpret_cast<const uint2*>(a.codes + (size_t)(r0 + r) * (a.K / 2) + c * 8));
         const uint32_t sc = a.scales[scale_at((size_t)o.pad, NV ? c : c >> 1, a.block_groups)];
-        const float step = NV ? e4m3_value(sc) * (a.g ? __ldg(a.g + o.g) : 1.0f) : e8m0_value(sc);
+        const float step = (NV ? e4m3_value(sc) : e8m0_value(sc)) * (a.g ? __ldg(a.g + o.g) : 1.0f);
 #pragma unroll
         for (int i = 0; i < 16; ++i) res[i] = (O)(e2m1_value(((i < 8 ? q.x : q.y) >> (4 * (i & 7))) & 15u) * step);
       }
@@ -196,7 +181,6 @@ moe_status check_fp4(int32_t G, int32_t N, int32_t K, int32_t dtype, int32_t wdt
   if (K < 32 || K % 32) return fail(MOE_EINVAL, "K = %d is not a multiple of 32", K);
   if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_EINVAL, "dtype must be MOE_F32 or MOE_BF16");
   if (wdtype != MOE_NVFP4 && wdtype != MOE_MXFP4) return fail(MOE_EINVAL, "wdtype must be MOE_NVFP4 or MOE_MXFP4");
-  if (g && wdtype == MOE_MXFP4) return fail(MOE_EINVAL, "MXFP4 has no matrix scale");
   if (g && g_count != 1 && g_count != G) return fail(MOE_EINVAL, "g_count must be 1 or G = %d, is %d", G, g_count);
   return MOE_OK;
 }
@@ -237,6 +221,7 @@ extern "C" moe_status moe_quantize_fp4(int32_t G, int32_t N, int32_t K, int32_t 
                                        void* stream) {
   moe_status st = check_fp4(G, N, K, dtype, wdtype, g, g_count);
   if (st != MOE_OK) return st;
+  if (g && wdtype == MOE_MXFP4) return fail(MOE_EINVAL, "MXFP4 has no matrix scale");
   if (offsets && (G != 1 || !tiles || (N > 0 && !order) || E < 1 || k < 1))
     return fail(MOE_EINVAL, "grouped rows need G = 1, tiles, order, E >= 1 and k >= 1");
   if (G == 0 || N == 0) return MOE_OK;

@@ -1,10 +1,33 @@
 // Products grouped by expert (include/moe_operators.h: moe_grouped_matmul,
 // moe_grouped_matmul_fp4).
 //
-// A block computes 64 rows of one expert's 128-row tile against 64 columns (with
-// SwiGLU: 64 gate columns and their 64 up columns) on the CUDA cores, from fp32 copies of
-// 32-deep slices in shared memory.
+// The product is computed transposed: the weights are the M operand, the tokens the N
+// operand, D[feature, token].  A CTA (CG = 1) or a pair of CTAs (CG = 2) multiplies 128 or
+// 256 weight rows by up to 128 or 256 tokens of one expert.  An expert's last, ragged
+// tile then costs only the columns it has (N is a multiple of 16 or 32 per
+// instruction), and one decoded token costs 16 columns, not 128 rows.
+//
+// Persistent kernel, one CTA per SM:
+//   warp 0     TMA: weight tiles, token tiles (or rows gathered four at a time by index),
+//              4-bit scale tiles, into a ring of K slices of 128 bytes a row
+//   warp 1     one thread issues tcgen05.mma: kind::f16 (bf16) or the block-scaled 4-bit
+//              kinds, whose scales go from shared memory to TMEM by tcgen05.cp first
+//   warp 2     4-bit SwiGLU: moves the weights' scales into the order of the rows (below)
+//   warps 4-11 epilogue, two warps to a quarter of the TMEM lanes
+// The accumulators are double-buffered in TMEM where they fit beside the scales (bf16:
+// 2 x 256 columns; 4-bit: 2 x 128, or one of 256), so the epilogue of a tile runs under
+// the products of the next.
+//
+// SwiGLU: the weight rows of a tile alternate 16 gate rows and the 16 up rows of the same
+// features (one 5-dimensional tensor map does it), so lanes l and l + 16 of a warp hold
+// gate and up of one feature, and one shuffle for two tokens brings them together.  A
+// 16- or 32-element block of the result is requantised after a turn through shared memory.
+//
+// Every wait is bounded; one that runs out sets the flag moe_operators_check() reads.
 #include "operators.cuh"
+#include "tc.cuh"
+
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 
@@ -12,137 +35,530 @@ namespace moe {
 
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 32;
+using namespace tc;
+
+__device__ uint32_t g_operator_err;
+
+constexpr int THREADS = 384;
+constexpr int FIRST_EPI = 4, EPI_WARPS = 8;
+constexpr int A_BYTES = 128 * 128;             // 128 weight rows, 128 bytes of K each
+constexpr int SCALE_A = 2048, SCALE_B = 2048;  // scales of 128 rows and one K slice (of every 128 tokens: CG of them)
+constexpr int MAX_STAGES = 12;
+constexpr int TMEM_COLS = 512, TMEM_SCALES = 256;
+constexpr int QUANT_STRIDE = 80;               // floats a token's 64 features take in the requantising buffer
+constexpr int QUANT_BYTES = 2 * 32 * QUANT_STRIDE * 4;
+constexpr int SMEM_LIMIT = 227 * 1024;
+constexpr int SF_DEPTH = 3;                    // K slices of scales in flight (warp 2); at most the ring's stages
 
 struct ProductArgs {
-  int P, E, N, K, k, cols, block_groups, gw_count, act;
-  const void* x;             // bf16 rows or codes
-  const uint8_t* x_scales;
-  const void* w;
+  int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant;
+  int m_blocks, kslices, stages, stage_bytes, b_rows, b_box, w_tiles;
   const uint8_t* w_scales;
   const float *gx, *gw, *g_out;
-  const int32_t *offsets, *tiles, *order;
+  const int32_t *offsets, *order;
   void* out;
   uint8_t *out_codes, *out_scales;
+  const int32_t* tiles;
 };
 
-// element of a 4-bit matrix: row r of `codes`, padded row `pad` of `scales`
-template <int FMT>
-__device__ __forceinline__ float fp4_at(const uint8_t* codes, const uint8_t* scales, size_t r, size_t pad, int c, int K, int groups) {
-  const uint32_t q = codes[r * (size_t)(K / 2) + (c >> 1)] >> (4 * (c & 1));
-  const uint32_t s = scales[scale_at(pad, FMT == MOE_NVFP4 ? c >> 4 : c >> 5, groups)];
-  return e2m1_value(q & 15u) * (FMT == MOE_NVFP4 ? e4m3_value(s) : e8m0_value(s));
+struct Item { int e, row0, n, mb, tile; };   // expert, first grouped row, rows, weight block, scale tile of row0
+
+template <int FMT, int CG>
+struct Shape4 {
+  static constexpr bool FP4 = FMT != MOE_BF16, NV = FMT == MOE_NVFP4;
+  static constexpr int NMAX = 128 * CG;                 // tokens of a tile
+  static constexpr int KS = FP4 ? 256 : 64;             // K of a slice
+  static constexpr int KI = FP4 ? 64 : 16;              // K of an instruction
+  static constexpr int GS = NV ? 4 : 2;                 // scale groups of a slice
+  static constexpr int NACC = FP4 && CG == 2 ? 1 : 2;
+  static constexpr int ACC_COLS = CG == 2 ? 256 : 128;
+};
+
+template <int FMT, int CG>
+__device__ __forceinline__ Item item_at(const ProductArgs& a, const int32_t* first, int it) {
+  using S = Shape4<FMT, CG>;
+  Item o;
+  const int tt = it / a.m_blocks;
+  o.mb = it - tt * a.m_blocks;
+  int lo = 0, hi = a.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= tt) lo = mid;
+    else hi = mid;
+  }
+  o.e = lo;
+  const int j = tt - first[lo], r0 = __ldg(a.offsets + lo), n = __ldg(a.offsets + lo + 1) - r0;
+  int chunk = S::NMAX;
+  if constexpr (!S::FP4) {
+    // even shares; 4-bit tiles start on their scales' 128-row tiles
+    const int nt = first[lo + 1] - first[lo];
+    chunk = ((n + nt - 1) / nt + 16 * CG - 1) / (16 * CG) * (16 * CG);
+  }
+  o.row0 = r0 + j * chunk;
+  o.n = min(chunk, n - j * chunk);
+  o.tile = S::FP4 ? __ldg(a.tiles + lo) + j * CG : 0;
+  return o;
 }
 
-// OUT: MOE_BF16, MOE_F32, or -1 = 4-bit rows of FMT
-template <int FMT, int OUT, bool SWIGLU>
-__global__ void __launch_bounds__(256) product_kernel(ProductArgs a) {
-  constexpr int NB = SWIGLU ? 2 : 1;
-  __shared__ float xs[TK][TM + 1], ws[NB][TK][TN + 1];
-  __shared__ float hs[OUT < 0 ? TM : 1][TN + 1];
-  const int tile = blockIdx.y >> 1;
-  if (tile >= __ldg(a.tiles + a.E)) return;
-  const int e = expert_of(a.tiles, a.E, tile);
-  const int in_e = (tile - __ldg(a.tiles + e)) * 128 + (blockIdx.y & 1) * TM;
-  const int row0 = __ldg(a.offsets + e) + in_e, row1 = __ldg(a.offsets + e + 1);
-  if (row0 >= row1) return;
-  const int col0 = blockIdx.x * TN;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const size_t wpad = (size_t)e * (size_t)(ceil_div64(a.N, 128) * 128), xpad = (size_t)tile * 128 + (blockIdx.y & 1) * TM;
-  float acc[NB][4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += TK) {
-    for (int i = threadIdx.x; i < TM * TK; i += 256) {
-      const int r = i / TK, c = i % TK;
-      float v = 0.0f;
-      if (row0 + r < row1 && k0 + c < a.K) {
-        if constexpr (FMT == MOE_BF16) {
-          const size_t src = a.order ? (size_t)(__ldg(a.order + row0 + r) / a.k) : (size_t)(row0 + r);
-          v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.x)[src * a.K + k0 + c]);
-        } else {
-          v = fp4_at<FMT>(static_cast<const uint8_t*>(a.x), a.x_scales, row0 + r, xpad + r, k0 + c, a.K, a.block_groups);
-        }
-      }
-      xs[c][r] = v;
+template <int FMT, int CG>
+__global__ void __launch_bounds__(THREADS, 1)
+product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+               const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX, const ProductArgs a) {
+  using S = Shape4<FMT, CG>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const uint32_t ring = smem_u32(smem);
+  uint8_t* tail = smem + (size_t)a.stages * a.stage_bytes;
+  float* qbuf = reinterpret_cast<float*>(tail);
+  if (a.quant) tail += QUANT_BYTES;
+  const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, tfull = empty + 8 * MAX_STAGES, tempty = tfull + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 16 * MAX_STAGES + 32);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int32_t* first = reinterpret_cast<int32_t*>(tmem_slot + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const bool sf_warp = S::FP4 && a.act;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) {
+      mbar_init(full + 8 * s, 1 + (sf_warp ? CG : 0));
+      mbar_init(empty + 8 * s, 1);
     }
-    for (int b = 0; b < NB; ++b)
-      for (int i = threadIdx.x; i < TN * TK; i += 256) {
-        const int r = i / TK, c = i % TK;
-        float v = 0.0f;
-        if (col0 + r < a.cols && k0 + c < a.K) {
-          const int n = col0 + r + b * a.cols;
-          if constexpr (FMT == MOE_BF16)
-            v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.w)[((size_t)e * a.N + n) * a.K + k0 + c]);
-          else
-            v = fp4_at<FMT>(static_cast<const uint8_t*>(a.w), a.w_scales, (size_t)e * a.N + n, wpad + n, k0 + c, a.K, a.block_groups);
-        }
-        ws[b][c][r] = v;
-      }
-    __syncthreads();
-#pragma unroll 8
-    for (int c = 0; c < TK; ++c)
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[b][i][j] = fmaf(xs[c][ty * 4 + i], ws[b][c][tx + 16 * j], acc[b][i][j]);
-    __syncthreads();
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(tfull + 8 * s, 1);
+      mbar_init(tempty + 8 * s, EPI_WARPS * CG);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  float g = 1.0f;
-  if (FMT != MOE_BF16) g = (a.gx ? *a.gx : 1.0f) * (a.gw ? a.gw[a.gw_count > 1 ? e : 0] : 1.0f);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = row0 + ty * 4 + i, c = col0 + tx + 16 * j;
-      float v = acc[0][i][j] * g;
-      if (SWIGLU) v = v / (1.0f + expf(-v)) * (acc[NB - 1][i][j] * g);
-      if constexpr (OUT < 0) hs[ty * 4 + i][tx + 16 * j] = v;
-      else if (r < row1 && c < a.cols) {
-        if constexpr (OUT == MOE_F32) static_cast<float*>(a.out)[(size_t)r * a.cols + c] = v;
-        else static_cast<__nv_bfloat16*>(a.out)[(size_t)r * a.cols + c] = __float2bfloat16_rn(v);
+  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), TMEM_COLS);
+  if (warp == 2) {   // token tiles before each expert
+    int run = 0;
+    for (int b = 0; b < a.E; b += 32) {
+      const int e = b + lane;
+      const int c = e < a.E ? (__ldg(a.offsets + e + 1) - __ldg(a.offsets + e) + S::NMAX - 1) / S::NMAX : 0;
+      int x = c;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += v;
+      }
+      if (e < a.E) first[e] = run + x - c;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) first[a.E] = run;
+  }
+  fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int total = first[a.E] * a.m_blocks;
+  const int step = gridDim.x / CG, it0 = blockIdx.x / CG;
+
+  if (warp == 0) {
+    // ---------------- loads ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = it0; it < total && ok; it += step) {
+      const Item o = item_at<FMT, CG>(a, first, it);
+      const int ncols = (o.n + 16 * CG - 1) / (16 * CG) * (16 * CG), mine = ncols / CG;   // token columns; those this CTA loads
+      const int boxes = (mine + a.b_box - 1) / a.b_box;
+      const int row0 = o.row0 + (int)rank * mine;
+      const int m = o.mb * CG + (int)rank;      // 128-row weight tile (64 gate + 64 up with SwiGLU)
+      const int chunks = S::FP4 ? (o.n + 127) / 128 : 0;
+      uint32_t bytes = (uint32_t)CG * (A_BYTES + 128u * (a.gather ? mine : boxes * a.b_box));
+      if (S::FP4) bytes += (uint32_t)CG * 512u * S::GS * (chunks + (a.act ? 0 : 1));
+      int4 idx = make_int4(0, 0, 0, 0);   // sources of this CTA's rows 4 * lane ..; past the end: the last again
+      if (a.gather && 4 * lane < mine) {
+        const int last = o.row0 + o.n - 1, r = row0 + 4 * lane;
+        idx = make_int4(__ldg(a.order + min(r, last)) / a.k, __ldg(a.order + min(r + 1, last)) / a.k,
+                        __ldg(a.order + min(r + 2, last)) / a.k, __ldg(a.order + min(r + 3, last)) / a.k);
+      }
+      for (int ks = 0; ks < a.kslices; ++ks) {
+        if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+        const uint32_t sa = ring + stage * a.stage_bytes, sb = sa + A_BYTES;
+        uint32_t bar = full + 8 * stage;
+        if (CG == 2) bar = in_rank(bar, 0);
+        if (lane == 0) {
+          if (rank == 0) mbar_expect(full + 8 * stage, bytes);
+          const int x = ks * (S::FP4 ? 128 : 64);
+          // weights: rows of one expert (dimensions K, row, expert), or with SwiGLU (K, 16 rows, gate / up, block of 16, expert)
+          if (a.act) tma_5d<CG>(&tmW, bar, sa, x, 0, 0, 4 * m, o.e);
+          else tma_5d<CG>(&tmW, bar, sa, x, 128 * m, 0, 0, o.e);
+          if (!a.gather)
+            for (int b = 0; b < boxes; ++b) tma_2d<CG>(&tmX, bar, sb + b * a.b_box * 128, x, row0 + b * a.b_box);
+          if (S::FP4) {
+            const uint32_t ss = sb + a.b_rows * 128;
+            if (!a.act) tma_2d<CG>(&tmSW, bar, ss, 0, (o.e * a.w_tiles + m) * a.groups + ks * S::GS);
+            for (int c = 0; c < chunks; ++c)
+              tma_2d<CG>(&tmSX, bar, ss + SCALE_A + c * SCALE_B, 0, (o.tile + c) * a.groups + ks * S::GS);
+          }
+        }
+        if (a.gather) {
+          __syncwarp();
+          if (4 * lane < mine) tma_gather4<CG>(&tmX, bar, sb + 4 * lane * 128, ks * 64, idx);
+        }
+        if (++stage == a.stages) { stage = 0; phase ^= 1u; }
       }
     }
-  if constexpr (OUT < 0) {
-    __syncthreads();
-    constexpr bool NV = FMT == MOE_NVFP4;
-    constexpr int B = NV ? 16 : 32;
-    const int og = (a.cols + 4 * B - 1) / (4 * B);
-    const float go = NV && a.g_out ? *a.g_out : 1.0f;
-    for (int u = threadIdx.x; u < TM * (TN / B); u += 256) {
-      const int r = u / (TN / B), b = u % (TN / B), c = col0 + b * B;
-      if (row0 + r >= row1 || c >= a.cols) continue;
-      uint32_t m = 0u;
-      for (int i = 0; i < B; ++i) m = max(m, __float_as_uint(hs[r][b * B + i]) & 0x7fffffffu);
-      float step;
-      const uint32_t code = block_scale<NV>(m, go, step);
-      const float inv = NV ? 0.0f : e8m0_inverse(code);
-      for (int i = 0; i < B; i += 2) {
-        const float lo = hs[r][b * B + i], hi = hs[r][b * B + i + 1];
-        const uint32_t q = !(step > 0.0f) ? 0u : NV ? to_e2m1x2(__fdiv_rn(lo, step), __fdiv_rn(hi, step)) : to_e2m1x2(lo * inv, hi * inv);
-        a.out_codes[(size_t)(row0 + r) * (a.cols / 2) + (c + i) / 2] = (uint8_t)q;
+    if (!ok) {
+      if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
+      // copies in flight land long before this bound
+      const unsigned long long t0 = gtimer();
+      while (gtimer() - t0 < 1000000ull) {
       }
-      uint8_t* s = a.out_scales + scale_at(xpad + r, c / B, og);
-      *s = (uint8_t)code;
-      if (c + B >= a.cols)
-        for (int i = 1; i < 4 - ((c / B) & 3); ++i) s[i] = 0;
     }
+    // every slice has been used, and no arrival on this CTA's barriers is outstanding, before it ends
+    for (int i = 0; i < a.stages && ok; ++i) {
+      ok = mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag);
+      if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+    }
+  } else if (warp == 1) {
+    // ---------------- products ----------------
+    if (lane == 0 && rank == 0) {
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int it = it0; it < total && ok; it += step) {
+        const Item o = item_at<FMT, CG>(a, first, it);
+        const int ncols = (o.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        if (!mbar_wait(tempty + 8 * acc, acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+        fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * S::ACC_COLS);
+        // D fp32; bf16 operands, or e2m1 with e4m3 / e8m0 scales; both K-major; N; M = 128 CG
+        const uint32_t idesc = ((uint32_t)(ncols >> 3) << 17) | ((uint32_t)(8 * CG) << 24) |
+                               (S::FP4 ? (1u << 7) | (1u << 10) | (S::NV ? 0u : 1u << 23) : (1u << 4) | (1u << 7) | (1u << 10));
+        for (int ks = 0; ks < a.kslices; ++ks) {
+          if (!mbar_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
+          fence_after();
+          const uint32_t sa = ring + stage * a.stage_bytes, sb = sa + A_BYTES;
+          const int left = a.K - ks * S::KS;
+          if constexpr (S::FP4) {
+            const uint32_t ss = sb + a.b_rows * 128, tsa = tmem + TMEM_SCALES, tsb = tsa + 16;
+            const int chunks = (o.n + 127) / 128;
+#pragma unroll
+            for (int g = 0; g < S::GS; ++g) {
+              if (g * (S::KS / S::GS) >= left) break;
+              copy_scales<CG>(tsa + 4 * g, desc_scales(ss + 512 * g));
+              for (int c = 0; c < chunks; ++c) copy_scales<CG>(tsb + 8 * g + 4 * c, desc_scales(ss + SCALE_A + c * SCALE_B + 512 * g));
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk * S::KI >= left) break;
+              const uint32_t g = S::NV ? kk : kk >> 1, id = S::NV ? 0u : 2u * (kk & 1);
+              mma_fp4<CG, S::NV>(d, desc_sw128(sa + kk * 32), desc_sw128(sb + kk * 32), idesc | (id << 4) | (id << 29), tsa + 4 * g,
+                                 tsb + 8 * g, (ks | kk) != 0);
+            }
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk * S::KI >= left) break;
+              mma_bf16<CG>(d, desc_sw128(sa + kk * 32), desc_sw128(sb + kk * 32), idesc, (ks | kk) != 0);
+            }
+          }
+          commit<CG>(empty + 8 * stage);
+          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok) break;
+        commit<CG>(tfull + 8 * acc);
+        if (++acc == S::NACC) { acc = 0; acc_phase ^= 1u; }
+      }
+      if (!ok) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
+    }
+  } else if (warp == 2) {
+    // ---------------- 4-bit SwiGLU: the weights' scales, in the order of the tile's rows ----------------
+    if constexpr (S::FP4) {
+      if (sf_warp) {
+        int stage = 0, done_stage = 0, pending = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const int I = a.cols;
+        auto finish = [&]() {   // the oldest slice's copies have landed: hand it over
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2) mbar_arrive_cluster(in_rank(full + 8 * done_stage, 0));
+            else mbar_arrive(full + 8 * done_stage);
+          }
+          if (++done_stage == a.stages) done_stage = 0;
+          --pending;
+        };
+        for (int it = it0; it < total && ok; it += step) {
+          const Item o = item_at<FMT, CG>(a, first, it);
+          const int m = o.mb * CG + (int)rank;
+          const uint8_t* src[4];   // this lane's four rows: lane + 32 j of the tile
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int row = min((lane >> 4) * I + m * 64 + j * 16 + (lane & 15), a.N - 1);
+            src[j] = a.w_scales + ((size_t)o.e * a.w_tiles + (row >> 7)) * a.groups * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+          }
+          for (int ks = 0; ks < a.kslices; ++ks) {
+            if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+            const uint32_t dst = ring + stage * a.stage_bytes + A_BYTES + a.b_rows * 128 + lane * 16;
+#pragma unroll
+            for (int g = 0; g < S::GS; ++g) {
+              const int at = ks * S::GS + g;
+              if (at >= a.groups) break;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + g * 512 + 4 * j), "l"(src[j] + (size_t)at * 512) : "memory");
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (++pending == SF_DEPTH) {
+              asm volatile("cp.async.wait_group %0;" ::"n"(SF_DEPTH - 1) : "memory");
+              finish();
+            }
+            if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+          }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        while (pending) finish();
+        if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
+      }
+    }
+  } else if (warp >= FIRST_EPI) {
+    // ---------------- epilogue: a TMEM lane is a weight row, a column a token ----------------
+    const int q = warp & 3, part = (warp - FIRST_EPI) >> 2;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int it = it0; it < total; it += step) {
+      const Item o = item_at<FMT, CG>(a, first, it);
+      const bool ok = mbar_wait(tfull + 8 * acc, acc_phase, abort_flag);
+      if (!named_and(1 + part, 128, ok)) {
+        if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
+        break;
+      }
+      fence_after();
+      const int m = o.mb * CG + (int)rank;
+      float g = 1.0f;
+      if (S::FP4) g = (a.gx ? __ldg(a.gx) : 1.0f) * (a.gw ? __ldg(a.gw + (a.gw_count > 1 ? o.e : 0)) : 1.0f);
+      const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * S::ACC_COLS);
+#pragma unroll 1
+      for (int c = 32 * part; c < o.n; c += 64) {
+        uint32_t v[32];
+        tmem_ld32(tbase + c, v);
+        tmem_ld_wait();
+        const int left = o.n - c;
+        if (!a.act) {
+          const int f = m * 128 + 32 * q + lane;
+          if (f < a.cols) {
+            const size_t at = (size_t)(o.row0 + c) * a.cols + f;
+            if (a.out_f32) {
+              float* p = static_cast<float*>(a.out) + at;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < left) p[(size_t)i * a.cols] = __uint_as_float(v[i]) * g;
+            } else {
+              __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + at;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < left) p[(size_t)i * a.cols] = __float2bfloat16_rn(__uint_as_float(v[i]) * g);
+            }
+          }
+          continue;
+        }
+        // lanes 0-15: gate of 16 features, lanes 16-31: up; two tokens at a time, one to each half
+        const int half = lane >> 4;
+        const int f = m * 64 + 16 * q + (lane & 15);
+        float h[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float t0 = __uint_as_float(v[2 * i]), t1 = __uint_as_float(v[2 * i + 1]);
+          const float got = __shfl_xor_sync(0xffffffffu, half ? t0 : t1, 16);
+          const float gate = (half ? got : t0) * g, up = (half ? t1 : got) * g;
+          h[i] = gate / (1.0f + expf(-gate)) * up;     // token c + 2 i + half
+        }
+        if (!a.quant) {
+          if (f < a.cols) {
+            const size_t at = (size_t)(o.row0 + c + half) * a.cols + f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (2 * i + half < left) {
+                if (a.out_f32) static_cast<float*>(a.out)[at + (size_t)(2 * i) * a.cols] = h[i];
+                else static_cast<__nv_bfloat16*>(a.out)[at + (size_t)(2 * i) * a.cols] = __float2bfloat16_rn(h[i]);
+              }
+          }
+          continue;
+        }
+        if constexpr (S::FP4) {
+          float* buf = qbuf + part * 32 * QUANT_STRIDE;
+          named_sync(1 + part, 128);      // the last round has been read
+#pragma unroll
+          for (int i = 0; i < 16; ++i) buf[(2 * i + half) * QUANT_STRIDE + 16 * q + (lane & 15)] = h[i];
+          named_sync(1 + part, 128);
+          const int t = (threadIdx.x & 127) >> 2, b = threadIdx.x & 3;   // token, 16 of the 64 features
+          float x[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 w = *reinterpret_cast<const float4*>(buf + t * QUANT_STRIDE + 16 * b + 4 * i);
+            x[4 * i] = w.x; x[4 * i + 1] = w.y; x[4 * i + 2] = w.z; x[4 * i + 3] = w.w;
+          }
+          uint32_t top = 0u;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+          if (!S::NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          float st;
+          uint32_t code = block_scale<S::NV>(top, S::NV && a.g_out ? __ldg(a.g_out) : 1.0f, st);
+          const uint2 codes = encode16<S::NV>(x, code, st);
+          const int fb = m * 64 + 16 * b;
+          const int og = (a.cols + (S::NV ? 63 : 127)) / (S::NV ? 64 : 128);
+          const size_t pad = ((size_t)__ldg(a.tiles + o.e) << 7) + (o.row0 - __ldg(a.offsets + o.e)) + c + t;
+          const bool live = t < left && fb < a.cols;
+          if (live) *reinterpret_cast<uint2*>(a.out_codes + (size_t)(o.row0 + c + t) * (a.cols / 2) + fb / 2) = codes;
+          if (!(fb < a.cols)) code = 0u;        // blocks past the end pad their group
+          if (S::NV) {
+            code |= __shfl_xor_sync(0xffffffffu, code, 1) << 8;
+            code |= __shfl_xor_sync(0xffffffffu, code, 2) << 16;
+            if (b == 0 && live) *reinterpret_cast<uint32_t*>(a.out_scales + scale_at(pad, fb / 16, og)) = code;
+          } else {
+            code |= __shfl_xor_sync(0xffffffffu, code, 2) << 8;
+            if (b == 0 && live) {
+              uint8_t* s = a.out_scales + scale_at(pad, fb / 32, og);
+              *reinterpret_cast<uint16_t*>(s) = (uint16_t)code;
+              if (m * 64 + 64 >= a.cols && (m & 1) == 0) *reinterpret_cast<uint16_t*>(s + 2) = 0;
+            }
+          }
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2) mbar_arrive_cluster(in_rank(tempty + 8 * acc, 0));
+        else mbar_arrive(tempty + 8 * acc);
+      }
+      if (++acc == S::NACC) { acc = 0; acc_phase ^= 1u; }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 1) {
+    fence_after();
+    tmem_free<CG>(tmem, TMEM_COLS);
   }
 }
 
-template <int FMT>
-moe_status launch_product(const ProductArgs& a, int out_dtype, cudaStream_t s) {
-  const dim3 grid((a.cols + TN - 1) / TN, (unsigned)(2 * moe_grouped_tiles(a.P, a.E)));
-  if (grid.y > 65535) return fail(MOE_EINVAL, "P = %d rows are too many", a.P);
-  if (!a.out) {
-    if constexpr (FMT != MOE_BF16) product_kernel<FMT, -1, true><<<grid, 256, 0, s>>>(a);
-  } else if (a.act) {
-    if (out_dtype == MOE_F32) product_kernel<FMT, MOE_F32, true><<<grid, 256, 0, s>>>(a);
-    else product_kernel<FMT, MOE_BF16, true><<<grid, 256, 0, s>>>(a);
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box, bool swizzle) {
+  auto enc = get_encode();
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return enc && enc(m, type, rank, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct ProductMem { const void *x, *w, *x_scales, *w_scales; int x_rows; };
+
+template <int FMT, int CG>
+moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
+  using S = Shape4<FMT, CG>;
+  const uint64_t row_bytes = S::FP4 ? (uint64_t)a.K / 2 : (uint64_t)a.K * 2;
+  const uint64_t row_elems = S::FP4 ? (uint64_t)a.K / 2 : (uint64_t)a.K;
+  const CUtensorMapDataType type = S::FP4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint32_t kbox = S::FP4 ? 128 : 64;
+  a.m_blocks = (int)ceil_div64(a.act ? a.cols : a.N, (a.act ? 64 : 128) * CG);
+  a.kslices = (a.K + S::KS - 1) / S::KS;
+  a.w_tiles = (a.N + 127) / 128;
+  // rows of the token area: what the largest tile of P rows can need
+  a.b_box = CG == 2 ? 32 : 16;
+  a.b_rows = std::min(128, (a.P + 15) / 16 * 16);
+  if (CG == 2) a.b_rows = 128;
+  a.stage_bytes = A_BYTES + a.b_rows * 128 + (S::FP4 ? SCALE_A + CG * SCALE_B : 0);
+  const int fixed = 1024 + (a.quant ? QUANT_BYTES : 0) + 16 * MAX_STAGES + 32 + 8 + 4 * (a.E + 1) + 16;
+  a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
+  const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
+
+  CUtensorMap tw, tx, tsw, tsx;
+  bool ok;
+  if (a.act) {
+    const cuuint64_t dims[5] = {row_elems, 16, 2, (cuuint64_t)a.cols / 16, (cuuint64_t)a.E};
+    const cuuint64_t strides[4] = {row_bytes, row_bytes * a.cols, row_bytes * 16, row_bytes * a.N};
+    const cuuint32_t box[5] = {kbox, 16, 2, 4, 1};
+    ok = make_map(&tw, type, 5, mem.w, dims, strides, box, true);
   } else {
-    if (out_dtype == MOE_F32) product_kernel<FMT, MOE_F32, false><<<grid, 256, 0, s>>>(a);
-    else product_kernel<FMT, MOE_BF16, false><<<grid, 256, 0, s>>>(a);
+    const cuuint64_t dims[5] = {row_elems, (cuuint64_t)a.N, 1, 1, (cuuint64_t)a.E};
+    const cuuint64_t strides[4] = {row_bytes, row_bytes * a.N, row_bytes * a.N, row_bytes * a.N};
+    const cuuint32_t box[5] = {kbox, 128, 1, 1, 1};
+    ok = make_map(&tw, type, 5, mem.w, dims, strides, box, true);
   }
-  CK(cudaGetLastError());
+  {
+    const cuuint64_t dims[2] = {row_elems, (cuuint64_t)mem.x_rows};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {kbox, a.gather ? 1u : (cuuint32_t)a.b_box};
+    ok = ok && make_map(&tx, type, 2, mem.x, dims, strides, box, true);
+  }
+  tsw = tsx = tx;
+  if (S::FP4) {
+    const cuuint64_t strides[1] = {512};
+    const cuuint32_t box[2] = {128, (cuuint32_t)S::GS};
+    const cuuint64_t dw[2] = {128, (cuuint64_t)a.E * a.w_tiles * a.groups};
+    const cuuint64_t dx[2] = {128, (cuuint64_t)moe_grouped_tiles(a.P, a.E) * a.groups};
+    ok = ok && make_map(&tsw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, mem.w_scales, dw, strides, box, false) &&
+         make_map(&tsx, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, mem.x_scales, dx, strides, box, false);
+  }
+  if (!ok) return fail(MOE_ECUDA, "cuTensorMapEncodeTiled failed");
+
+  // at most every token tile the rows can make, on every weight block
+  if (a.stages < SF_DEPTH) return fail(MOE_EINVAL, "E = %d experts leave too little shared memory", a.E);
+  const int64_t most = (a.P + (int64_t)(S::NMAX - 1) * std::min(a.P, a.E)) / S::NMAX * a.m_blocks;
+  CK(cudaFuncSetAttribute(product_kernel<FMT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT));
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG == 2 ? 1 : 0;
+  // every unit of a persistent grid has to be resident: as many pairs as the device's clusters allow
+  int resident = operator_sms();
+  if (CG == 2) {
+    static int pairs[64] = {};
+    int dev = 0;
+    CK(cudaGetDevice(&dev));
+    if (dev < 0 || dev >= 64) return fail(MOE_EINVAL, "device %d is out of range", dev);
+    if (!pairs[dev]) {
+      int n = 0;
+      cfg.gridDim = dim3(operator_sms() / 2 * 2);
+      cfg.dynamicSmemBytes = SMEM_LIMIT;
+      CK(cudaOccupancyMaxActiveClusters(&n, product_kernel<FMT, CG>, &cfg));
+      if (n < 1) return fail(MOE_ECUDA, "no CTA pair fits the device");
+      pairs[dev] = n;
+      cfg.dynamicSmemBytes = smem;
+    }
+    resident = pairs[dev];
+  }
+  const int units = (int)std::min<int64_t>(most, resident);
+  cfg.gridDim = dim3(units * CG);
+  CK(cudaLaunchKernelEx(&cfg, product_kernel<FMT, CG>, tw, tx, tsw, tsx, a));
   return MOE_OK;
+}
+
+// Pairs of CTAs halve what each SM reads of the tokens; single CTAs give small calls twice the units of work.
+template <int FMT>
+moe_status launch_product(const ProductArgs& a, const ProductMem& mem, cudaStream_t s) {
+  if (a.P >= 64 * (int64_t)a.E) return launch_tiles<FMT, 2>(a, mem, s);
+  return launch_tiles<FMT, 1>(a, mem, s);
 }
 
 moe_status check_product(int32_t P, int32_t E, int32_t N, int32_t K, int32_t quantum, const int32_t* offsets,
@@ -170,12 +586,12 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
   if (st != MOE_OK) return st;
   if (order && (k < 1 || !aligned_to(order, 4))) return fail(MOE_EINVAL, "order needs k >= 1 and 4-byte alignment");
   if (P == 0) return MOE_OK;
-  if (!x || !w || !out || x_rows < 1) return fail(MOE_EINVAL, "x, w and out must not be NULL and x must hold rows");
+  if (!x || !w || !out || x_rows < (order ? 1 : P)) return fail(MOE_EINVAL, "x, w and out must not be NULL and x must hold its rows");
   if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(out, 16)) return fail(MOE_EINVAL, "x, w and out must be 16-byte aligned");
   ProductArgs a{};
-  a.P = P; a.E = E; a.N = N; a.K = K; a.k = k; a.act = act; a.cols = act ? N / 2 : N;
-  a.x = x; a.w = w; a.order = order; a.offsets = offsets; a.tiles = tiles; a.out = out;
-  return launch_product<MOE_BF16>(a, out_dtype, static_cast<cudaStream_t>(stream));
+  a.P = P; a.E = E; a.N = N; a.K = K; a.k = k; a.act = act; a.cols = act ? N / 2 : N; a.gather = order != nullptr;
+  a.out_f32 = out_dtype == MOE_F32; a.order = order; a.offsets = offsets; a.tiles = tiles; a.out = out;
+  return launch_product<MOE_BF16>(a, ProductMem{x, w, nullptr, nullptr, x_rows}, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, int32_t K, int32_t wdtype,
@@ -187,7 +603,7 @@ extern "C" moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, in
   moe_status st = check_product(P, E, N, K, 32, offsets, tiles, act, out_dtype);
   if (st != MOE_OK) return st;
   if (wdtype != MOE_NVFP4 && wdtype != MOE_MXFP4) return fail(MOE_EINVAL, "wdtype must be MOE_NVFP4 or MOE_MXFP4");
-  if (wdtype == MOE_MXFP4 && (gx || gw || g_out)) return fail(MOE_EINVAL, "MXFP4 has no matrix scale");
+  if (wdtype == MOE_MXFP4 && g_out) return fail(MOE_EINVAL, "an MXFP4 result has no matrix scale");
   if (gw && gw_count != 1 && gw_count != E) return fail(MOE_EINVAL, "gw_count must be 1 or E = %d, is %d", E, gw_count);
   if (P == 0) return MOE_OK;
   if (!x_codes || !x_scales || !w_codes || !w_scales) return fail(MOE_EINVAL, "codes and scales must not be NULL");
@@ -203,14 +619,23 @@ extern "C" moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, in
   }
   ProductArgs a{};
   a.P = P; a.E = E; a.N = N; a.K = K; a.k = 1; a.act = act; a.cols = act ? N / 2 : N;
-  a.block_groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
-  a.x = x_codes; a.x_scales = x_scales; a.gx = gx; a.w = w_codes; a.w_scales = w_scales; a.gw = gw; a.gw_count = gw_count;
+  a.groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
+  a.quant = !out; a.out_f32 = out_dtype == MOE_F32;
+  a.w_scales = w_scales; a.gx = gx; a.gw = gw; a.gw_count = gw_count;
   a.offsets = offsets; a.tiles = tiles; a.out = out; a.out_codes = out_codes; a.out_scales = out_scales; a.g_out = g_out;
+  const ProductMem mem{x_codes, w_codes, x_scales, w_scales, P};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return wdtype == MOE_NVFP4 ? launch_product<MOE_NVFP4>(a, out_dtype, s) : launch_product<MOE_MXFP4>(a, out_dtype, s);
+  return wdtype == MOE_NVFP4 ? launch_product<MOE_NVFP4>(a, mem, s) : launch_product<MOE_MXFP4>(a, mem, s);
 }
 
 extern "C" moe_status moe_operators_check(void* stream) {
-  CK(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)));
-  return MOE_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint32_t err = 0;
+  CK(cudaMemcpyFromSymbolAsync(&err, g_operator_err, sizeof(err), 0, cudaMemcpyDeviceToHost, s));
+  CK(cudaStreamSynchronize(s));
+  if (!err) return MOE_OK;
+  err = 0;
+  CK(cudaMemcpyToSymbolAsync(g_operator_err, &err, sizeof(err), 0, cudaMemcpyHostToDevice, s));
+  CK(cudaStreamSynchronize(s));
+  return fail(MOE_EDEVICE, "a wait inside an operator kernel ran out");
 }

@@ -9,7 +9,7 @@ namespace moe {
 // SMs of the current device (looked up once per device).
 int operator_sms();
 
-__device__ __forceinline__ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // expert of a grouped row, or of a row tile: the e with first[e] <= i < first[e + 1]
 __device__ __forceinline__ int expert_of(const int32_t* __restrict__ first, int E, int i) {
@@ -76,5 +76,20 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float g, flo
 }
 // what a value is multiplied by (MXFP4: 2^-X, exact) -- NVFP4 divides by the step
 __device__ __forceinline__ float e8m0_inverse(uint32_t code) { return e8m0_value(254u - code); }
+
+// 16 values -> 8 bytes of codes
+template <bool NV>
+__device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t code, float step) {
+  uint32_t w[2] = {0u, 0u};
+  const bool none = !(step > 0.0f);
+  const float inv = NV ? 0.0f : e8m0_inverse(code);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float lo = NV ? __fdiv_rn(v[2 * i], step) : v[2 * i] * inv;
+    const float hi = NV ? __fdiv_rn(v[2 * i + 1], step) : v[2 * i + 1] * inv;
+    w[i >> 2] |= to_e2m1x2(lo, hi) << (8 * (i & 3));
+  }
+  return none ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
+}
 
 }  // namespace moe

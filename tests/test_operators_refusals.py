@@ -99,19 +99,19 @@ def test_quantize_refuses(lib, kw, word):
     ((1, 4, 64, NVFP4, A, B, None, 0, 0, None, None, NVFP4, C), b"dtype"),
     ((1, 4, 64, NVFP4, A, B, None, 0, 0, None, None, BF16, None), b"NULL"),
     ((1, 4, 64, NVFP4, A, B, None, 0, 4, D, None, BF16, C), b"grouped"),
-    ((1, 4, 64, MXFP4, A, B, D, 1, 0, None, None, BF16, C), b"no matrix scale")])
+    ((3, 4, 64, MXFP4, A, B, D, 2, 0, None, None, BF16, C), b"g_count")])
 def test_dequantize_refuses(lib, args, word):
     refused(lib, lib.moe_dequantize_fp4(*args, None), word)
 
 
-def matmul(lib, P_=8, E=2, N=64, K=64, x=A, rows=4, order=None, k=2, w=B, off=C, til=D, act=0, od=BF16, out=F):
+def matmul(lib, P_=8, E=2, N=64, K=64, x=A, rows=8, order=None, k=2, w=B, off=C, til=D, act=0, od=BF16, out=F):
     return lib.moe_grouped_matmul(P_, E, N, K, x, rows, order, k, w, off, til, act, od, out, None)
 
 
 @pytest.mark.parametrize("kw,word", [
     (dict(P_=-1), b"P >= 0"), (dict(E=0), b"E"), (dict(E=4097), b"4096"), (dict(N=0), b"N"), (dict(K=12), b"multiple of 8"), (dict(act=2), b"act"),
     (dict(act=1, N=48), b"multiple of 32"), (dict(od=3), b"out_dtype"), (dict(off=None), b"offsets"), (dict(x=None), b"NULL"),
-    (dict(x=P(0x10008)), b"16-byte"), (dict(w=P(0x10002)), b"16-byte"), (dict(order=G, k=0), b"order"), (dict(rows=0), b"rows")])
+    (dict(x=P(0x10008)), b"16-byte"), (dict(w=P(0x10002)), b"16-byte"), (dict(order=G, k=0), b"order"), (dict(rows=0), b"rows"), (dict(rows=7), b"rows")])
 def test_grouped_matmul_refuses(lib, kw, word):
     refused(lib, matmul(lib, **kw), word)
 
@@ -122,7 +122,7 @@ def matmul_fp4(lib, P_=8, E=2, N=64, K=64, wd=NVFP4, xc=A, xs=B, gx=None, wc=C, 
 
 
 @pytest.mark.parametrize("kw,word", [
-    (dict(K=72), b"multiple of 32"), (dict(wd=BF16), b"wdtype"), (dict(wd=MXFP4, gx=A), b"no matrix scale"), (dict(gw=A, gwc=3), b"gw_count"),
+    (dict(K=72), b"multiple of 32"), (dict(wd=BF16), b"wdtype"), (dict(wd=MXFP4, act=1, N=128, out=None, oc=A, os_=B, go=C), b"no matrix scale"), (dict(gw=A, gwc=3), b"gw_count"),
     (dict(xc=None), b"NULL"), (dict(ws=P(0x10008)), b"16-byte"), (dict(out=None), b"act = 1"), (dict(out=None, act=1, N=96), b"multiple of 32"),
     (dict(out=None, act=1, N=128), b"out_codes"), (dict(out=P(0x10002)), b"16-byte"), (dict(gx=P(0x10002)), b"4-byte")])
 def test_grouped_matmul_fp4_refuses(lib, kw, word):
