@@ -8,11 +8,12 @@
 // instruction), and one decoded token costs 16 columns, not 128 rows.
 //
 // Persistent kernel, one CTA per SM:
-//   warp 0     TMA: weight tiles, token tiles (or rows gathered four at a time by index),
-//              4-bit scale tiles, into a ring of K slices of 128 bytes a row
+//   warp 0     TMA: weight tiles, token tiles, 4-bit scale tiles, into a ring of K slices of
+//              128 bytes a row
 //   warp 1     one thread issues tcgen05.mma: kind::f16 (bf16) or the block-scaled 4-bit
 //              kinds, whose scales go from shared memory to TMEM by tcgen05.cp first
-//   warp 2     4-bit SwiGLU: moves the weights' scales into the order of the rows (below)
+//   warps 2, 3 what TMA does not place: bf16 token rows gathered by index, and with 4-bit
+//              SwiGLU the weights' scales in the order of the rows (below), by cp.async
 //   warps 4-11 epilogue, two warps to a quarter of the TMEM lanes
 // The accumulators are double-buffered in TMEM where they fit beside the scales (bf16:
 // 2 x 256 columns; 4-bit: 2 x 128, or one of 256), so the epilogue of a tile runs under
@@ -48,11 +49,12 @@ constexpr int TMEM_COLS = 512, TMEM_SCALES = 256;
 constexpr int QUANT_STRIDE = 80;               // floats a token's 64 features take in the requantising buffer
 constexpr int QUANT_BYTES = 2 * 32 * QUANT_STRIDE * 4;
 constexpr int SMEM_LIMIT = 227 * 1024;
-constexpr int SF_DEPTH = 3;                    // K slices of scales in flight (warp 2); at most the ring's stages
+constexpr int DEPTH = 3;                       // K slices whose copies warps 2 and 3 have in flight; at most the ring's stages
 
 struct ProductArgs {
   int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant;
   int m_blocks, kslices, stages, stage_bytes, b_rows, b_box, w_tiles;
+  const __nv_bfloat16* x;      // rows to gather
   const uint8_t* w_scales;
   const float *gx, *gw, *g_out;
   const int32_t *offsets, *order;
@@ -100,6 +102,36 @@ __device__ __forceinline__ Item item_at(const ProductArgs& a, const int32_t* fir
   return o;
 }
 
+// The products of one K slice (descriptors da, db, ds of its weights, tokens and scales); `left`: the K that is there
+// when the slice is not FULL.  The scales of even and odd slices go to their own TMEM columns.
+template <int FMT, int CG, bool FULL>
+__device__ __forceinline__ void issue_slice(uint32_t d, uint32_t tmem, uint64_t da, uint64_t db, uint64_t ds, uint32_t idesc, int chunks,
+                                            int ks, int left) {
+  using S = Shape4<FMT, CG>;
+  if constexpr (S::FP4) {
+    const uint32_t tsa = tmem + TMEM_SCALES + 48u * (ks & 1), tsb = tsa + 16;
+#pragma unroll
+    for (int g = 0; g < S::GS; ++g) {
+      if (!FULL && g * (S::KS / S::GS) >= left) break;
+      copy_scales<CG>(tsa + 4 * g, ds + 32 * g);
+      copy_scales<CG>(tsb + 8 * g, ds + (SCALE_A >> 4) + 32 * g);
+      if (CG == 2 && chunks == 2) copy_scales<CG>(tsb + 8 * g + 4, ds + ((SCALE_A + SCALE_B) >> 4) + 32 * g);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      if (!FULL && kk * S::KI >= left) break;
+      const uint32_t g = S::NV ? kk : kk >> 1, id = S::NV ? 0u : 2u * (kk & 1);
+      mma_fp4<CG, S::NV>(d, da + 2 * kk, db + 2 * kk, idesc | (id << 4) | (id << 29), tsa + 4 * g, tsb + 8 * g, (ks | kk) != 0);
+    }
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      if (!FULL && kk * S::KI >= left) break;
+      mma_bf16<CG>(d, da + 2 * kk, db + 2 * kk, idesc, (ks | kk) != 0);
+    }
+  }
+}
+
 template <int FMT, int CG>
 __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -119,10 +151,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-  const bool sf_warp = S::FP4 && a.act;
+  const bool helped = S::FP4 ? (bool)a.act : (bool)a.gather;   // warps 2 and 3 fill part of every slice
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(full + 8 * s, 1 + (sf_warp ? CG : 0));
+      mbar_init(full + 8 * s, 1 + (helped ? 2 * CG : 0));
       mbar_init(empty + 8 * s, 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -168,14 +200,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       const int row0 = o.row0 + (int)rank * mine;
       const int m = o.mb * CG + (int)rank;      // 128-row weight tile (64 gate + 64 up with SwiGLU)
       const int chunks = S::FP4 ? (o.n + 127) / 128 : 0;
-      uint32_t bytes = (uint32_t)CG * (A_BYTES + 128u * (a.gather ? mine : boxes * a.b_box));
+      uint32_t bytes = (uint32_t)CG * (A_BYTES + (a.gather ? 0u : 128u * boxes * a.b_box));
       if (S::FP4) bytes += (uint32_t)CG * 512u * S::GS * (chunks + (a.act ? 0 : 1));
-      int4 idx = make_int4(0, 0, 0, 0);   // sources of this CTA's rows 4 * lane ..; past the end: the last again
-      if (a.gather && 4 * lane < mine) {
-        const int last = o.row0 + o.n - 1, r = row0 + 4 * lane;
-        idx = make_int4(__ldg(a.order + min(r, last)) / a.k, __ldg(a.order + min(r + 1, last)) / a.k,
-                        __ldg(a.order + min(r + 2, last)) / a.k, __ldg(a.order + min(r + 3, last)) / a.k);
-      }
       for (int ks = 0; ks < a.kslices; ++ks) {
         if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
         const uint32_t sa = ring + stage * a.stage_bytes, sb = sa + A_BYTES;
@@ -195,10 +221,6 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             for (int c = 0; c < chunks; ++c)
               tma_2d<CG>(&tmSX, bar, ss + SCALE_A + c * SCALE_B, 0, (o.tile + c) * a.groups + ks * S::GS);
           }
-        }
-        if (a.gather) {
-          __syncwarp();
-          if (4 * lane < mine) tma_gather4<CG>(&tmX, bar, sb + 4 * lane * 128, ks * 64, idx);
         }
         if (++stage == a.stages) { stage = 0; phase ^= 1u; }
       }
@@ -221,6 +243,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
+      const uint64_t da = desc_sw128(ring), db = desc_sw128(ring + A_BYTES), ds = desc_scales(ring + A_BYTES + a.b_rows * 128);
       for (int it = it0; it < total && ok; it += step) {
         const Item o = item_at<FMT, CG>(a, first, it);
         const int ncols = (o.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
@@ -230,34 +253,13 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         // D fp32; bf16 operands, or e2m1 with e4m3 / e8m0 scales; both K-major; N; M = 128 CG
         const uint32_t idesc = ((uint32_t)(ncols >> 3) << 17) | ((uint32_t)(8 * CG) << 24) |
                                (S::FP4 ? (1u << 7) | (1u << 10) | (S::NV ? 0u : 1u << 23) : (1u << 4) | (1u << 7) | (1u << 10));
+        const int chunks = (o.n + 127) / 128;
         for (int ks = 0; ks < a.kslices; ++ks) {
           if (!mbar_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
           fence_after();
-          const uint32_t sa = ring + stage * a.stage_bytes, sb = sa + A_BYTES;
-          const int left = a.K - ks * S::KS;
-          if constexpr (S::FP4) {
-            const uint32_t ss = sb + a.b_rows * 128, tsa = tmem + TMEM_SCALES, tsb = tsa + 16;
-            const int chunks = (o.n + 127) / 128;
-#pragma unroll
-            for (int g = 0; g < S::GS; ++g) {
-              if (g * (S::KS / S::GS) >= left) break;
-              copy_scales<CG>(tsa + 4 * g, desc_scales(ss + 512 * g));
-              for (int c = 0; c < chunks; ++c) copy_scales<CG>(tsb + 8 * g + 4 * c, desc_scales(ss + SCALE_A + c * SCALE_B + 512 * g));
-            }
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk * S::KI >= left) break;
-              const uint32_t g = S::NV ? kk : kk >> 1, id = S::NV ? 0u : 2u * (kk & 1);
-              mma_fp4<CG, S::NV>(d, desc_sw128(sa + kk * 32), desc_sw128(sb + kk * 32), idesc | (id << 4) | (id << 29), tsa + 4 * g,
-                                 tsb + 8 * g, (ks | kk) != 0);
-            }
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (kk * S::KI >= left) break;
-              mma_bf16<CG>(d, desc_sw128(sa + kk * 32), desc_sw128(sb + kk * 32), idesc, (ks | kk) != 0);
-            }
-          }
+          const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
+          if (a.K - ks * S::KS >= S::KS) issue_slice<FMT, CG, true>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, 0);
+          else issue_slice<FMT, CG, false>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, a.K - ks * S::KS);
           commit<CG>(empty + 8 * stage);
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
@@ -267,56 +269,81 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       }
       if (!ok) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
     }
-  } else if (warp == 2) {
-    // ---------------- 4-bit SwiGLU: the weights' scales, in the order of the tile's rows ----------------
-    if constexpr (S::FP4) {
-      if (sf_warp) {
-        int stage = 0, done_stage = 0, pending = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        const int I = a.cols;
-        auto finish = [&]() {   // the oldest slice's copies have landed: hand it over
-          fence_async_proxy();
-          __syncwarp();
-          if (lane == 0) {
-            if (CG == 2) mbar_arrive_cluster(in_rank(full + 8 * done_stage, 0));
-            else mbar_arrive(full + 8 * done_stage);
-          }
-          if (++done_stage == a.stages) done_stage = 0;
-          --pending;
-        };
-        for (int it = it0; it < total && ok; it += step) {
-          const Item o = item_at<FMT, CG>(a, first, it);
-          const int m = o.mb * CG + (int)rank;
-          const uint8_t* src[4];   // this lane's four rows: lane + 32 j of the tile
+  } else if (warp < FIRST_EPI) {
+    // ---------------- warps 2 and 3: what TMA does not place ----------------
+    // 4-bit SwiGLU: the weights' scales, in the order of the tile's rows; bf16: token rows by index.  Asynchronous
+    // copies of a few slices are in flight; a landed slice is made visible to the tensor cores and handed over.
+    if (helped) {
+      const int hw = warp - 2;
+      int stage = 0, done_stage = 0, pending = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto finish = [&]() {
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2) mbar_arrive_cluster(in_rank(full + 8 * done_stage, 0));
+          else mbar_arrive(full + 8 * done_stage);
+        }
+        if (++done_stage == a.stages) done_stage = 0;
+        --pending;
+      };
+      for (int it = it0; it < total && ok; it += step) {
+        const Item o = item_at<FMT, CG>(a, first, it);
+        const int m = o.mb * CG + (int)rank;
+        const uint8_t* src[2];     // scales: rows lane + 32 (2 hw + j) of the tile
+        uint32_t tok[16];          // tokens: sources of rows 64 hw + 4 i + lane / 8
+        const int ncols = (o.n + 16 * CG - 1) / (16 * CG) * (16 * CG), mine = ncols / CG;
+        if constexpr (S::FP4) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = min((lane >> 4) * I + m * 64 + j * 16 + (lane & 15), a.N - 1);
+          for (int j = 0; j < 2; ++j) {
+            const int row = min((lane >> 4) * a.cols + m * 64 + (2 * hw + j) * 16 + (lane & 15), a.N - 1);
             src[j] = a.w_scales + ((size_t)o.e * a.w_tiles + (row >> 7)) * a.groups * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
           }
-          for (int ks = 0; ks < a.kslices; ++ks) {
-            if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
-            const uint32_t dst = ring + stage * a.stage_bytes + A_BYTES + a.b_rows * 128 + lane * 16;
+        } else {
+          const int last = o.row0 + o.n - 1;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r = 64 * hw + 4 * i + (lane >> 3);   // past the end: the last row again
+            tok[i] = r < mine ? (uint32_t)(__ldg(a.order + min(o.row0 + (int)rank * mine + r, last)) / a.k) : 0u;
+          }
+        }
+        for (int ks = 0; ks < a.kslices; ++ks) {
+          if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+          const uint32_t sb = ring + stage * a.stage_bytes + A_BYTES;
+          if constexpr (S::FP4) {
+            const uint32_t dst = sb + a.b_rows * 128 + lane * 16 + 8 * hw;
 #pragma unroll
             for (int g = 0; g < S::GS; ++g) {
               const int at = ks * S::GS + g;
               if (at >= a.groups) break;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
+              for (int j = 0; j < 2; ++j)
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + g * 512 + 4 * j), "l"(src[j] + (size_t)at * 512) : "memory");
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (++pending == SF_DEPTH) {
-              asm volatile("cp.async.wait_group %0;" ::"n"(SF_DEPTH - 1) : "memory");
-              finish();
+          } else {
+            const int col = ks * 64 + (lane & 7) * 8;
+            const uint32_t there = col < a.K ? 16u : 0u;   // past K: zeros
+            const __nv_bfloat16* x = a.x + (there ? col : 0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = 64 * hw + 4 * i + (lane >> 3);
+              if (r < mine)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
+                             "l"(x + (size_t)tok[i] * a.K), "r"(there) : "memory");
             }
-            if (++stage == a.stages) { stage = 0; phase ^= 1u; }
           }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (++pending == DEPTH) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+            finish();
+          }
+          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        while (pending) finish();
-        if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      while (pending) finish();
+      if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
     }
   } else if (warp >= FIRST_EPI) {
     // ---------------- epilogue: a TMEM lane is a weight row, a column a token ----------------
@@ -502,7 +529,7 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   {
     const cuuint64_t dims[2] = {row_elems, (cuuint64_t)mem.x_rows};
     const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {kbox, a.gather ? 1u : (cuuint32_t)a.b_box};
+    const cuuint32_t box[2] = {kbox, (cuuint32_t)a.b_box};
     ok = ok && make_map(&tx, type, 2, mem.x, dims, strides, box, true);
   }
   tsw = tsx = tx;
@@ -517,9 +544,16 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   if (!ok) return fail(MOE_ECUDA, "cuTensorMapEncodeTiled failed");
 
   // at most every token tile the rows can make, on every weight block
-  if (a.stages < SF_DEPTH) return fail(MOE_EINVAL, "E = %d experts leave too little shared memory", a.E);
+  if (a.stages < DEPTH) return fail(MOE_EINVAL, "E = %d experts leave too little shared memory", a.E);
   const int64_t most = (a.P + (int64_t)(S::NMAX - 1) * std::min(a.P, a.E)) / S::NMAX * a.m_blocks;
-  CK(cudaFuncSetAttribute(product_kernel<FMT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT));
+  static bool allowed[64] = {};   // the kernel's shared memory, once per device
+  int dev = 0;
+  CK(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(MOE_EINVAL, "device %d is out of range", dev);
+  if (!allowed[dev]) {
+    CK(cudaFuncSetAttribute(product_kernel<FMT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT));
+    allowed[dev] = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
@@ -534,9 +568,6 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   int resident = operator_sms();
   if (CG == 2) {
     static int pairs[64] = {};
-    int dev = 0;
-    CK(cudaGetDevice(&dev));
-    if (dev < 0 || dev >= 64) return fail(MOE_EINVAL, "device %d is out of range", dev);
     if (!pairs[dev]) {
       int n = 0;
       cfg.gridDim = dim3(operator_sms() / 2 * 2);
@@ -590,6 +621,7 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
   if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(out, 16)) return fail(MOE_EINVAL, "x, w and out must be 16-byte aligned");
   ProductArgs a{};
   a.P = P; a.E = E; a.N = N; a.K = K; a.k = k; a.act = act; a.cols = act ? N / 2 : N; a.gather = order != nullptr;
+  a.x = static_cast<const __nv_bfloat16*>(x);
   a.out_f32 = out_dtype == MOE_F32; a.order = order; a.offsets = offsets; a.tiles = tiles; a.out = out;
   return launch_product<MOE_BF16>(a, ProductMem{x, w, nullptr, nullptr, x_rows}, static_cast<cudaStream_t>(stream));
 }

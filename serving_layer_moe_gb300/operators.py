@@ -9,6 +9,9 @@
 Argument checks, output tensors and pointers only: the work is in the library's kernels, there is no
 fallback.  Everything is enqueued on `stream` (torch's current stream if None); outputs are allocated for
 that stream.  Wrong arguments raise ValueError before anything is enqueued.
+
+One decoded token runs all five calls in the time of a few launches, so the calls are kept short: a whole
+argument is checked in one expression, and only a failed one is looked at again for its message.
 """
 from __future__ import annotations
 
@@ -26,6 +29,7 @@ SCORING = {"softmax": 0, "sigmoid": 1}
 ACTS = {None: 0, "none": 0, "swiglu": 1}
 FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
 _FLOATS = {torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"]}
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 _lib = None
 
@@ -58,33 +62,40 @@ def _operators():
 
 
 class _On:
-    """The device and stream that a call runs on, with both current inside the block."""
+    """A stream other than torch's current one, or another device: both current inside the block."""
 
-    __slots__ = ("handle", "_ctx")
-
-    def __init__(self, device, stream):
-        self._ctx = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self._ctx.append(torch.cuda.device(device))
-        if stream is None:
-            self.handle = None
-        else:
+    def __init__(self, index, stream):
+        self.ctx = []
+        if index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(index))
+        if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
-            self._ctx.append(torch.cuda.stream(stream))
-            self.handle = stream.cuda_stream
+                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
+            self.ctx.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        for c in self._ctx:
+        for c in self.ctx:
             c.__enter__()
-        if self.handle is None:
-            self.handle = torch.cuda.current_stream().cuda_stream
-        return self.handle
 
     def __exit__(self, *exc):
-        for c in reversed(self._ctx):
+        for c in reversed(self.ctx):
             c.__exit__(*exc)
         return False
+
+
+def _elsewhere(index, stream):
+    """Whether a call for tensors of device `index` has to make another stream or device current first."""
+    return stream is not None or index != torch.cuda.current_device()
+
+
+def _stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+try:    # the same without building Stream objects, where this torch has it
+    _stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    pass
 
 
 def _need(ok, what):
@@ -92,99 +103,139 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _tensor(t, name, dtypes, dim, device=None):
+def _bad(t, name, dtypes, dim, index=None):
+    """Raise what is wrong with an argument that should be a contiguous CUDA tensor."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != dim or not t.is_contiguous():
         got = f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}" if isinstance(t, torch.Tensor) else type(t)
         raise ValueError(f"{name} must be a contiguous {dim}-dimensional tensor of {' or '.join(map(str, dtypes))}, got {got}")
-    if device is None:
-        _need(t.device.type == "cuda", f"{name} must be on a CUDA device, is on {t.device}")
-    else:
-        _need(t.device == device, f"{name} is on {t.device}, the other arguments on {device}")
+    _need(t.is_cuda, f"{name} must be on a CUDA device, is on {t.device}")
+    raise ValueError(f"{name} is on {t.device}, the other arguments on cuda:{index}")
+
+
+def _floats(t, name, dim, index=None):
+    """dtype code of a contiguous fp32 or bf16 CUDA tensor of `dim` dimensions (of device `index`)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in _FLOATS and t.dim() == dim and t.is_contiguous() and t.is_cuda
+            and (index is None or t.get_device() == index)):
+        _bad(t, name, tuple(_FLOATS), dim, index)
+    return _FLOATS[t.dtype]
+
+
+def _typed(t, name, dtype, dim, index=None):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == dim and t.is_contiguous() and t.is_cuda
+            and (index is None or t.get_device() == index)):
+        _bad(t, name, (dtype,), dim, index)
     return t
 
 
-def _scale_arg(g, name, counts, device):
+def _scale_ptr(g, name, most, index):
+    """Pointer and count of an fp32 matrix scale of 1 or `most` values (None: no scale)."""
     if g is None:
         return None, 0
-    _tensor(g, name, (torch.float32,), 1, device)
-    _need(g.numel() in counts, f"{name} must hold {' or '.join(map(str, sorted(set(counts))))} values, holds {g.numel()}")
-    return g.data_ptr(), g.numel()
-
-
-_I32 = (torch.int32,)
+    _typed(g, name, _F32, 1, index)
+    n = g.numel()
+    _need(n == 1 or n == most, f"{name} must hold {'1' if most == 1 else f'1 or {most}'} values, holds {n}")
+    return g.data_ptr(), n
 
 
 class ExpertGroups:
     """The (token, expert) pairs of a call in expert order: offsets and tiles [E + 1], order [T * k] and
-    place [T, k], all int32 (include/moe_operators.h, "Expert order")."""
+    place [T, k], all int32 (include/moe_operators.h, "Expert order").  Checked here, once, and not changed after."""
 
-    __slots__ = ("offsets", "tiles", "order", "place")
+    __slots__ = ("E", "P", "T", "k", "_index", "_ptrs", "_all", "_views")
 
     def __init__(self, offsets, tiles, order, place):
-        self.offsets, self.tiles, self.order, self.place = offsets, tiles, order, place
+        _typed(offsets, "offsets", _I32, 1)
+        i = offsets.get_device()
+        _typed(tiles, "tiles", _I32, 1, i)
+        _typed(order, "order", _I32, 1, i)
+        _typed(place, "place", _I32, 2, i)
+        self.E, self.P, self._index = offsets.numel() - 1, order.numel(), i
+        self.T, self.k = place.shape
+        _need(1 <= self.E <= 4096 and tiles.numel() == self.E + 1,
+              f"offsets and tiles must hold E + 1 values each (1 <= E <= 4096), hold {offsets.numel()} and {tiles.numel()}")
+        _need(self.T * self.k == self.P, f"order holds {self.P} pairs, place {self.T * self.k}")
+        self._ptrs = (offsets.data_ptr(), tiles.data_ptr(), order.data_ptr(), place.data_ptr())
+        self._views = [offsets, tiles, order, place]
+        self._all = None
 
-    @property
-    def E(self):
-        return self.offsets.numel() - 1
-
-    @property
-    def P(self):
-        return self.order.numel()
-
-    @property
-    def k(self):
-        return self.place.shape[1]
-
-    def _checked(self, device=None):
-        _tensor(self.offsets, "groups.offsets", _I32, 1, device)
-        device = self.offsets.device
-        _tensor(self.tiles, "groups.tiles", _I32, 1, device)
-        _tensor(self.order, "groups.order", _I32, 1, device)
-        _tensor(self.place, "groups.place", _I32, 2, device)
-        _need(self.offsets.numel() >= 2 and self.tiles.numel() == self.offsets.numel(),
-              f"groups.offsets and groups.tiles must hold E + 1 values each, hold {self.offsets.numel()} and {self.tiles.numel()}")
-        _need(self.place.numel() == self.order.numel(),
-              f"groups.order holds {self.order.numel()} pairs, groups.place {self.place.numel()}")
+    @classmethod
+    def _empty(cls, T, k, E, like):
+        """Room for the grouping of T tokens, on the device of `like`."""
+        self = cls.__new__(cls)
+        P = T * k
+        self.E, self.P, self.T, self.k, self._index = E, P, T, k, like.get_device()
+        self._all = like.new_empty(2 * (E + 1) + 2 * P, dtype=_I32)
+        p = self._all.data_ptr()
+        self._ptrs = (p, p + 4 * (E + 1), p + 8 * (E + 1), p + 8 * (E + 1) + 4 * P)
+        self._views = None
         return self
+
+    def _view(self, i):
+        if self._views is None:
+            e = self.E + 1
+            v = list(self._all.split((e, e, self.P, self.P)))
+            v[3] = v[3].view(self.T, self.k)
+            self._views = v
+        return self._views[i]
+
+    offsets = property(lambda self: self._view(0))
+    tiles = property(lambda self: self._view(1))
+    order = property(lambda self: self._view(2))
+    place = property(lambda self: self._view(3))
+
+
+def _groups_on(groups, index):
+    if not isinstance(groups, ExpertGroups):
+        raise ValueError(f"groups must be ExpertGroups, is {type(groups)}")
+    _need(groups._index == index, f"groups are on cuda:{groups._index}, the other arguments on cuda:{index}")
+    return groups
 
 
 class FP4Rows:
     """4-bit matrices: codes uint8 [..., K/2] and scale tiles uint8 [row tiles, block groups, 512]
     (include/moe_operators.h, "4-bit matrices"), wdtype "nvfp4" or "mxfp4", g the fp32 matrix scales (1 or one
-    per matrix; None = 1).  groups: of rows in expert order; None for a stack of matrices [G, N, K] or one [N, K]."""
+    per matrix; None = 1).  groups: of rows in expert order; None for a stack of matrices [G, N, K] or one [N, K].
+    Checked here, once, and not changed after."""
 
-    __slots__ = ("codes", "scales", "wdtype", "g", "groups")
+    __slots__ = ("codes", "scales", "wdtype", "g", "groups", "shape", "K", "_stack", "_index", "_ptrs")
 
     def __init__(self, codes, scales, wdtype, g=None, groups=None):
-        self.codes, self.scales, self.wdtype, self.g, self.groups = codes, scales, wdtype, g, groups
-
-    @property
-    def K(self):
-        return 2 * self.codes.shape[-1]
-
-    @property
-    def shape(self):
-        return (*self.codes.shape[:-1], self.K)
-
-    def _checked(self, name, dims, device=None):
-        _need(self.wdtype in FP4_BLOCK, f"{name}.wdtype must be 'nvfp4' or 'mxfp4', is {self.wdtype!r}")
-        dim = self.codes.dim() if isinstance(self.codes, torch.Tensor) else dims[0]
-        _tensor(self.codes, f"{name}.codes", (torch.uint8,), dim if dim in dims else dims[0], device)
-        _tensor(self.scales, f"{name}.scales", (torch.uint8,), 3, self.codes.device)
-        _need(self.K > 0 and self.K % 32 == 0, f"{name}: K must be a multiple of 32, is {self.K}")
-        if self.groups is not None:
-            n = _grouped_tiles(self.codes.shape[0], self.groups.E)
+        _need(wdtype in FP4_BLOCK, f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
+        dim = 2 if groups is not None or not isinstance(codes, torch.Tensor) or codes.dim() != 3 else 3
+        _typed(codes, "codes", _U8, dim)
+        i = codes.get_device()
+        _typed(scales, "scales", _U8, 3, i)
+        K = 2 * codes.shape[-1]
+        _need(K > 0 and K % 32 == 0, f"K must be a multiple of 32, is {K}")
+        if groups is not None:
+            _groups_on(groups, i)
+            _need(codes.shape[0] == groups.P, f"codes hold {codes.shape[0]} rows, groups {groups.P} pairs")
+            n = _grouped_tiles(groups.P, groups.E)
+            self._stack = (1, groups.P)
         else:
-            G, N = self._stack()
-            n = G * -(-N // 128)
-        want = (n, _block_groups(self.wdtype, self.K), 512)
-        _need(tuple(self.scales.shape) == want, f"{name}.scales must be {want}, is {tuple(self.scales.shape)}")
-        _need(self.codes.data_ptr() % 16 == 0 and self.scales.data_ptr() % 16 == 0,
-              f"{name}: codes and scales must be 16-byte aligned")
-        return self
+            self._stack = (1, codes.shape[0]) if dim == 2 else (codes.shape[0], codes.shape[1])
+            n = self._stack[0] * -(-self._stack[1] // 128)
+        want = (n, _block_groups(wdtype, K), 512)
+        _need(tuple(scales.shape) == want, f"scales must be {want}, is {tuple(scales.shape)}")
+        cp, sp = codes.data_ptr(), scales.data_ptr()
+        _need((cp | sp) % 16 == 0, "codes and scales must be 16-byte aligned")
+        gp, gn = _scale_ptr(g, "g", self._stack[0], i)
+        self.codes, self.scales, self.wdtype, self.g, self.groups = codes, scales, wdtype, g, groups
+        self.K, self._index, self._ptrs = K, i, (cp, sp, gp, gn)
+        self.shape = (*codes.shape[:-1], K)
 
-    def _stack(self):
-        return (1, self.codes.shape[0]) if self.codes.dim() == 2 else (self.codes.shape[0], self.codes.shape[1])
+    @classmethod
+    def _empty(cls, shape, wdtype, g, gp, groups, stack, like):
+        """Room for rows of `shape`, on the device of `like`; gp: pointer and count of g."""
+        self = cls.__new__(cls)
+        K = shape[-1]
+        n = _grouped_tiles(groups.P, groups.E) if groups is not None else stack[0] * -(-stack[1] // 128)
+        self.codes = like.new_empty((*shape[:-1], K // 2), dtype=_U8)
+        self.scales = like.new_empty((n, _block_groups(wdtype, K), 512), dtype=_U8)
+        self.wdtype, self.g, self.groups, self.shape, self.K, self._stack = wdtype, g, groups, shape, K, stack
+        self._index = like.get_device()
+        self._ptrs = (self.codes.data_ptr(), self.scales.data_ptr(), *gp)
+        return self
 
 
 def _block_groups(wdtype, K):
@@ -195,15 +246,9 @@ def _grouped_tiles(P, E):
     return (P + 127 * min(P, E)) // 128
 
 
-def _workspace(T, k, E, device):
-    n = int(_operators().moe_group_workspace(T, k, E))
-    return torch.empty(n, dtype=torch.uint8, device=device), n
-
-
-def _empty_groups(T, k, E, device):
-    e = E + 1
-    ints = torch.empty(2 * e + 2 * T * k, dtype=torch.int32, device=device)
-    return ExpertGroups(ints[:e], ints[e:2 * e], ints[2 * e:2 * e + T * k], ints[2 * e + T * k:].view(T, k))
+def _workspace(T, k, E, like):
+    n = _operators().moe_group_workspace(T, k, E)
+    return like.new_empty(n, dtype=_U8), n
 
 
 def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=1, renormalize=True, scale=1.0,
@@ -211,57 +256,65 @@ def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=
     """Experts and gates of each token: (topk_ids int32 [T, k], topk_w fp32 [T, k]), or with groups=True also the
     ExpertGroups of the picked pairs.  logits [T, E] fp32 or bf16; scoring "softmax" (by logit) or "sigmoid"
     (with an optional selection bias [E] and topk_group of n_group expert groups): moe_route."""
-    _tensor(logits, "logits", tuple(_FLOATS), 2)
+    dt = _floats(logits, "logits", 2)
     T, E = logits.shape
-    k, dev = int(top_k), logits.device
+    k, index = int(top_k), logits.get_device()
     _need(scoring in SCORING, f"scoring must be 'softmax' or 'sigmoid', is {scoring!r}")
-    _need(1 <= E <= 4096 and 1 <= k <= E, f"1 <= top_k <= E <= 4096 is needed, got top_k {k}, E {E}")
-    if scoring == "softmax":
-        _need(bias is None and n_group == 1, "softmax scoring takes no bias and no expert groups")
+    if not 1 <= k <= E <= 4096:
+        raise ValueError(f"1 <= top_k <= E <= 4096 is needed, got top_k {k}, E {E}")
+    sc = SCORING[scoring]
+    _need(sc or (bias is None and n_group == 1), "softmax scoring takes no bias and no expert groups")
     if bias is not None:
-        _tensor(bias, "bias", (torch.float32,), 1, dev)
+        _typed(bias, "bias", _F32, 1, index)
         _need(bias.numel() == E, f"bias must hold E = {E} values, holds {bias.numel()}")
-    _need(1 <= n_group <= 32 and E % n_group == 0 and 1 <= topk_group <= n_group and topk_group * (E // n_group) >= k,
-          f"n_group (1 to 32) must divide E and topk_group groups must hold top_k experts, got n_group {n_group}, "
-          f"topk_group {topk_group}, E {E}, top_k {k}")
-    with _On(dev, stream) as s:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-        w = torch.empty((T, k), dtype=torch.float32, device=dev)
-        gr, ws, n = None, None, 0
-        if groups:
-            gr = _empty_groups(T, k, E, dev)
-            ws, n = _workspace(T, k, E, dev)
-        _check(_operators().moe_route(
-            T, E, k, _FLOATS[logits.dtype], logits.data_ptr(), SCORING[scoring],
-            None if bias is None else bias.data_ptr(), n_group, topk_group, 1 if renormalize else 0, scale,
-            ids.data_ptr(), w.data_ptr(), *((gr.offsets.data_ptr(), gr.tiles.data_ptr(), gr.order.data_ptr(),
-                                            gr.place.data_ptr(), ws.data_ptr()) if groups else (None,) * 5), n, s))
+    if n_group != 1 or topk_group != 1:
+        _need(1 <= n_group <= 32 and E % n_group == 0 and 1 <= topk_group <= n_group and topk_group * (E // n_group) >= k,
+              f"n_group (1 to 32) must divide E and topk_group groups must hold top_k experts, got n_group {n_group}, "
+              f"topk_group {topk_group}, E {E}, top_k {k}")
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return route(logits, k, scoring=scoring, bias=bias, n_group=n_group, topk_group=topk_group,
+                         renormalize=renormalize, scale=scale, groups=groups)
+    ids = logits.new_empty((T, k), dtype=_I32)
+    w = logits.new_empty((T, k), dtype=_F32)
+    if groups:
+        gr = ExpertGroups._empty(T, k, E, logits)
+        ws, n = _workspace(T, k, E, logits)
+        rest = (*gr._ptrs, ws.data_ptr(), n)
+    else:
+        rest = (None, None, None, None, None, 0)
+    _check(_operators().moe_route(T, E, k, dt, logits.data_ptr(), sc, None if bias is None else bias.data_ptr(), n_group,
+                                  topk_group, 1 if renormalize else 0, scale, ids.data_ptr(), w.data_ptr(), *rest, _stream(index)))
     return (ids, w, gr) if groups else (ids, w)
 
 
 def group_pairs(topk_ids, n_experts, *, stream=None):
     """ExpertGroups of topk_ids int32 [T, k]; pairs whose id is outside [0, n_experts) are dropped (place -1)."""
-    _tensor(topk_ids, "topk_ids", _I32, 2)
+    _typed(topk_ids, "topk_ids", _I32, 2)
     T, k = topk_ids.shape
-    E, dev = int(n_experts), topk_ids.device
+    E, index = int(n_experts), topk_ids.get_device()
     _need(1 <= E <= 4096 and k >= 1, f"1 <= n_experts <= 4096 and k >= 1 are needed, got {E} and {k}")
-    with _On(dev, stream) as s:
-        gr = _empty_groups(T, k, E, dev)
-        ws, n = _workspace(T, k, E, dev)
-        _check(_operators().moe_group_pairs(T, E, k, topk_ids.data_ptr(), gr.offsets.data_ptr(), gr.tiles.data_ptr(),
-                                            gr.order.data_ptr(), gr.place.data_ptr(), ws.data_ptr(), n, s))
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return group_pairs(topk_ids, E)
+    gr = ExpertGroups._empty(T, k, E, topk_ids)
+    ws, n = _workspace(T, k, E, topk_ids)
+    _check(_operators().moe_group_pairs(T, E, k, topk_ids.data_ptr(), *gr._ptrs, ws.data_ptr(), n, _stream(index)))
     return gr
 
 
 def fp4_scale(x, *, stream=None):
     """NVFP4 matrix scales: max |x| / (6 * 448) of x [N, K] or of each matrix of x [G, N, K]; fp32 [1] or [G]."""
     dim = 3 if isinstance(x, torch.Tensor) and x.dim() == 3 else 2
-    _tensor(x, "x", tuple(_FLOATS), dim)
-    _need(x.numel() > 0, f"x is empty: {tuple(x.shape)}")
+    dt = _floats(x, "x", dim)
+    index, n = x.get_device(), x.numel()
+    _need(n > 0, f"x is empty: {tuple(x.shape)}")
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return fp4_scale(x)
     G = x.shape[0] if dim == 3 else 1
-    with _On(x.device, stream) as s:
-        g = torch.empty(G, dtype=torch.float32, device=x.device)
-        _check(_operators().moe_fp4_scale(G, x.numel() // G, _FLOATS[x.dtype], x.data_ptr(), g.data_ptr(), s))
+    g = x.new_empty(G, dtype=_F32)
+    _check(_operators().moe_fp4_scale(G, n // G, dt, x.data_ptr(), g.data_ptr(), _stream(index)))
     return g
 
 
@@ -271,82 +324,82 @@ def quantize_fp4(x, wdtype, *, g=None, groups=None, stream=None):
     for "nvfp4" (None = 1)."""
     _need(wdtype in FP4_BLOCK, f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
     dim = 2 if groups is not None or not isinstance(x, torch.Tensor) or x.dim() != 3 else 3
-    _tensor(x, "x", tuple(_FLOATS), dim)
-    dev, K = x.device, x.shape[-1]
+    dt = _floats(x, "x", dim)
+    index, K, xp = x.get_device(), x.shape[-1], x.data_ptr()
     _need(K > 0 and K % 32 == 0, f"K must be a multiple of 32, is {K}")
-    _need(x.data_ptr() % 16 == 0, "x must be 16-byte aligned")
+    _need(xp % 16 == 0, "x must be 16-byte aligned")
     _need(g is None or wdtype == "nvfp4", "only nvfp4 takes a matrix scale g")
-    G, N = (x.shape[0], x.shape[1]) if dim == 3 else (1, x.shape[0])
-    gp, gn = _scale_arg(g, "g", (1, G), dev)
     if groups is not None:
-        groups._checked(dev)
-        _need(groups.place.shape[0] == N, f"x has {N} rows, groups hold {groups.place.shape[0]} tokens")
-        N = groups.P
-        nt, shape = _grouped_tiles(N, groups.E), (N, K // 2)
+        _groups_on(groups, index)
+        _need(groups.T == x.shape[0], f"x has {x.shape[0]} rows, groups hold {groups.T} tokens")
+        stack, shape = (1, groups.P), (groups.P, K)
+        rest = (groups.E, groups.k, *groups._ptrs[:3])
     else:
-        nt, shape = G * -(-N // 128), (*x.shape[:-1], K // 2)
-    with _On(dev, stream) as s:
-        codes = torch.empty(shape, dtype=torch.uint8, device=dev)
-        scales = torch.empty((nt, _block_groups(wdtype, K), 512), dtype=torch.uint8, device=dev)
-        if groups is None:
-            rest = (0, 0, None, None, None)
-        else:
-            rest = (groups.E, groups.k, groups.offsets.data_ptr(), groups.tiles.data_ptr(), groups.order.data_ptr())
-        _check(_operators().moe_quantize_fp4(G, N, K, _FLOATS[x.dtype], x.data_ptr(), DTYPES[wdtype], gp, gn, *rest,
-                                             codes.data_ptr(), scales.data_ptr(), s))
-    return FP4Rows(codes, scales, wdtype, g, groups)
+        stack = (x.shape[0], x.shape[1]) if dim == 3 else (1, x.shape[0])
+        shape, rest = tuple(x.shape), (0, 0, None, None, None)
+    gp = _scale_ptr(g, "g", stack[0], index)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return quantize_fp4(x, wdtype, g=g, groups=groups)
+    q = FP4Rows._empty(shape, wdtype, g, gp, groups, stack, x)
+    _check(_operators().moe_quantize_fp4(*stack, K, dt, xp, DTYPES[wdtype], *gp, *rest, *q._ptrs[:2], _stream(index)))
+    return q
+
+
+def _rows(q, name):
+    if not isinstance(q, FP4Rows):
+        raise ValueError(f"{name} must be FP4Rows, is {type(q)}")
+    return q
 
 
 def dequantize_fp4(q, *, out_dtype=torch.bfloat16, stream=None):
     """The values that q stands for, in q.shape; rows that no pair fills are zero (moe_dequantize_fp4)."""
-    _need(isinstance(q, FP4Rows), f"q must be FP4Rows, is {type(q)}")
-    q._checked("q", (2,) if q.groups is not None else (2, 3))
+    _rows(q, "q")
     _need(out_dtype in _FLOATS, f"out_dtype must be float32 or bfloat16, is {out_dtype}")
-    dev = q.codes.device
-    G, N = q._stack()
-    gp, gn = _scale_arg(q.g, "q.g", (1, G), dev)
-    rest = (0, None, None)
-    if q.groups is not None:
-        q.groups._checked(dev)
-        _need(q.groups.P == N, f"q has {N} rows, its groups hold {q.groups.P} pairs")
-        rest = (q.groups.E, q.groups.offsets.data_ptr(), q.groups.tiles.data_ptr())
-    with _On(dev, stream) as s:
-        out = torch.empty(q.shape, dtype=out_dtype, device=dev)
-        _check(_operators().moe_dequantize_fp4(G, N, q.K, DTYPES[q.wdtype], q.codes.data_ptr(), q.scales.data_ptr(),
-                                               gp, gn, *rest, _FLOATS[out_dtype], out.data_ptr(), s))
+    index = q._index
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return dequantize_fp4(q, out_dtype=out_dtype)
+    rest = (0, None, None) if q.groups is None else (q.groups.E, *q.groups._ptrs[:2])
+    out = q.codes.new_empty(q.shape, dtype=out_dtype)
+    _check(_operators().moe_dequantize_fp4(*q._stack, q.K, DTYPES[q.wdtype], *q._ptrs, *rest, _FLOATS[out_dtype],
+                                           out.data_ptr(), _stream(index)))
     return out
 
 
-def _product_args(groups, E, N, act, out_dtype, dev):
-    _need(isinstance(groups, ExpertGroups), f"groups must be ExpertGroups, is {type(groups)}")
-    groups._checked(dev)
+def _columns(groups, E, N, act, out_dtype):
     _need(groups.E == E, f"w holds {E} experts, groups {groups.E}")
     _need(act in ACTS, f"act must be 'none' or 'swiglu', is {act!r}")
     _need(out_dtype in _FLOATS, f"out_dtype must be float32 or bfloat16, is {out_dtype}")
-    if ACTS[act]:
-        _need(N % 32 == 0, f"swiglu needs w rows a multiple of 32, got {N}")
-        return N // 2
-    return N
+    if not ACTS[act]:
+        return N
+    _need(N % 32 == 0, f"swiglu needs w rows a multiple of 32, got {N}")
+    return N // 2
 
 
 def grouped_matmul(x, w, groups, *, act="none", gather=False, out_dtype=torch.bfloat16, stream=None):
     """Row i of expert e: x[i] @ w[e].T, w [E, N, K] bf16, x bf16 [P, K] in expert order, or with gather=True
     [T, K] and grouped row i reads x[order[i] // k].  act="swiglu": w holds gate rows, then up rows, and the
     result has N/2 columns.  K a multiple of 8 (moe_grouped_matmul).  Rows that no pair fills are undefined."""
-    _tensor(x, "x", (torch.bfloat16,), 2)
-    dev = x.device
-    _tensor(w, "w", (torch.bfloat16,), 3, dev)
+    _typed(w, "w", _BF16, 3)
+    index = w.get_device()
+    _typed(x, "x", _BF16, 2, index)
+    _groups_on(groups, index)
     E, N, K = w.shape
-    cols = _product_args(groups, E, N, act, out_dtype, dev)
+    cols = _columns(groups, E, N, act, out_dtype)
     _need(N > 0 and K > 0 and K % 8 == 0, f"w must be [E, N, K] with K a multiple of 8, is {tuple(w.shape)}")
-    rows = groups.place.shape[0] if gather else groups.P
-    _need(tuple(x.shape) == (rows, K), f"x must be {(rows, K)}, is {tuple(x.shape)}")
-    _need(x.data_ptr() % 16 == 0 and w.data_ptr() % 16 == 0, "x and w must be 16-byte aligned")
-    with _On(dev, stream) as s:
-        out = torch.empty((groups.P, cols), dtype=out_dtype, device=dev)
-        _check(_operators().moe_grouped_matmul(
-            groups.P, E, N, K, x.data_ptr(), rows, groups.order.data_ptr() if gather else None, groups.k, w.data_ptr(),
-            groups.offsets.data_ptr(), groups.tiles.data_ptr(), ACTS[act], _FLOATS[out_dtype], out.data_ptr(), s))
+    rows = groups.T if gather else groups.P
+    if x.shape[0] != rows or x.shape[1] != K:
+        raise ValueError(f"x must be {(rows, K)}, is {tuple(x.shape)}")
+    xp, wp = x.data_ptr(), w.data_ptr()
+    _need((xp | wp) % 16 == 0, "x and w must be 16-byte aligned")
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return grouped_matmul(x, w, groups, act=act, gather=gather, out_dtype=out_dtype)
+    off, til, order, _ = groups._ptrs
+    out = x.new_empty((groups.P, cols), dtype=out_dtype)
+    _check(_operators().moe_grouped_matmul(groups.P, E, N, K, xp, rows, order if gather else None, groups.k, wp, off, til,
+                                           ACTS[act], _FLOATS[out_dtype], out.data_ptr(), _stream(index)))
     return out
 
 
@@ -354,52 +407,52 @@ def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, 
     """grouped_matmul of 4-bit rows x (FP4Rows in expert order) and 4-bit weights w (FP4Rows [E, N, K]) of one
     format.  quantize=True (act="swiglu" only): the result as FP4Rows of that format with the matrix scale g_out
     [1] (None = 1; "nvfp4" only), rounded from the fp32 values (moe_grouped_matmul_fp4)."""
-    _need(isinstance(x, FP4Rows) and isinstance(w, FP4Rows), "x and w must be FP4Rows")
-    w._checked("w", (3,))
-    dev = w.codes.device
+    _rows(x, "x")
+    _rows(w, "w")
+    index = w._index
+    _groups_on(groups, index)
+    _need(len(w.shape) == 3 and w.groups is None, f"w must be [E, N, K], is {w.shape}")
     E, N, K = w.shape
-    cols = _product_args(groups, E, N, act, out_dtype, dev)
-    _need(x.groups is not None and x.groups.E == E and N > 0, "x must hold rows in the expert order of w's experts")
-    x._checked("x", (2,), dev)
+    cols = _columns(groups, E, N, act, out_dtype)
+    _need(x.groups is not None and x._index == index and x.groups.E == E and N > 0,
+          "x must hold rows in the order of w's experts, on the same device")
     _need(x.wdtype == w.wdtype, f"x is {x.wdtype}, w is {w.wdtype}")
     _need(x.shape == (groups.P, K), f"x must be {(groups.P, K)}, is {x.shape}")
     _need(not quantize or (ACTS[act] and cols % 32 == 0), "quantize needs act='swiglu' and w rows a multiple of 64")
     _need(g_out is None or (quantize and x.wdtype == "nvfp4"), "g_out goes with quantize=True and nvfp4")
-    gx, _ = _scale_arg(x.g, "x.g", (1,), dev)
-    gw, gwn = _scale_arg(w.g, "w.g", (1, E), dev)
-    go, _ = _scale_arg(g_out, "g_out", (1,), dev)
-    with _On(dev, stream) as s:
-        if quantize:
-            out, op = None, None
-            codes = torch.empty((groups.P, cols // 2), dtype=torch.uint8, device=dev)
-            scales = torch.empty((_grouped_tiles(groups.P, E), _block_groups(x.wdtype, cols), 512), dtype=torch.uint8, device=dev)
-            cp, sp = codes.data_ptr(), scales.data_ptr()
-        else:
-            out = torch.empty((groups.P, cols), dtype=out_dtype, device=dev)
-            op, cp, sp = out.data_ptr(), None, None
-        _check(_operators().moe_grouped_matmul_fp4(
-            groups.P, E, N, K, DTYPES[x.wdtype], x.codes.data_ptr(), x.scales.data_ptr(), gx, w.codes.data_ptr(),
-            w.scales.data_ptr(), gw, gwn, groups.offsets.data_ptr(), groups.tiles.data_ptr(), ACTS[act],
-            _FLOATS[out_dtype], op, cp, sp, go, s))
-    return FP4Rows(codes, scales, x.wdtype, g_out, groups) if quantize else out
+    go = _scale_ptr(g_out, "g_out", 1, index)
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return grouped_matmul_fp4(x, w, groups, act=act, quantize=quantize, g_out=g_out, out_dtype=out_dtype)
+    if quantize:
+        out = FP4Rows._empty((groups.P, cols), x.wdtype, g_out, go, groups, (1, groups.P), x.codes)
+        dst = (None, out._ptrs[0], out._ptrs[1], go[0])
+    else:
+        out = x.codes.new_empty((groups.P, cols), dtype=out_dtype)
+        dst = (out.data_ptr(), None, None, None)
+    _check(_operators().moe_grouped_matmul_fp4(groups.P, E, N, K, DTYPES[x.wdtype], *x._ptrs[:3], *w._ptrs, *groups._ptrs[:2],
+                                               ACTS[act], _FLOATS[out_dtype], *dst, _stream(index)))
+    return out
 
 
 def combine(y, groups, topk_w, *, out_dtype=torch.float32, stream=None):
     """out[t] = sum_j topk_w[t, j] * y[place[t, j]], y [P, N] bf16 or fp32 in expert order; pairs dropped from the
     groups contribute nothing (moe_combine)."""
-    _tensor(y, "y", tuple(_FLOATS), 2)
-    dev, N = y.device, y.shape[1]
-    _need(isinstance(groups, ExpertGroups), f"groups must be ExpertGroups, is {type(groups)}")
-    groups._checked(dev)
-    _tensor(topk_w, "topk_w", (torch.float32,), 2, dev)
-    _need(topk_w.shape == groups.place.shape, f"topk_w must be {tuple(groups.place.shape)}, is {tuple(topk_w.shape)}")
+    dt = _floats(y, "y", 2)
+    index = y.get_device()
+    _groups_on(groups, index)
+    _typed(topk_w, "topk_w", _F32, 2, index)
+    T, k, N = groups.T, groups.k, y.shape[1]
+    if topk_w.shape[0] != T or topk_w.shape[1] != k:
+        raise ValueError(f"topk_w must be {(T, k)}, is {tuple(topk_w.shape)}")
     _need(y.shape[0] == groups.P and N > 0, f"y must be [{groups.P}, N], is {tuple(y.shape)}")
     _need(out_dtype in _FLOATS, f"out_dtype must be float32 or bfloat16, is {out_dtype}")
-    T, k = topk_w.shape
-    with _On(dev, stream) as s:
-        out = torch.empty((T, N), dtype=out_dtype, device=dev)
-        _check(_operators().moe_combine(T, k, N, _FLOATS[y.dtype], y.data_ptr(), groups.place.data_ptr(),
-                                        topk_w.data_ptr(), _FLOATS[out_dtype], out.data_ptr(), s))
+    if _elsewhere(index, stream):
+        with _On(index, stream):
+            return combine(y, groups, topk_w, out_dtype=out_dtype)
+    out = y.new_empty((T, N), dtype=out_dtype)
+    _check(_operators().moe_combine(T, k, N, dt, y.data_ptr(), groups._ptrs[3], topk_w.data_ptr(), _FLOATS[out_dtype],
+                                    out.data_ptr(), _stream(index)))
     return out
 
 
