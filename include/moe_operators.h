@@ -124,10 +124,13 @@ moe_status moe_dequantize_fp4(int32_t G, int32_t N, int32_t K, int32_t wdtype, c
  *   out[i] = silu(gate) * up, N/2 columns.
  *   out [P, N or N/2] in out_dtype (MOE_BF16 or MOE_F32); rows from offsets[E] on are
  *   left as they are.  Sums are fp32, rounded once.
+ *   workspace: moe_grouped_matmul_workspace(P, E, K, order != NULL) bytes (0 or the rows
+ *   gathered, for many rows per expert), 16-byte aligned.
  */
+int64_t moe_grouped_matmul_workspace(int32_t P, int32_t E, int32_t K, int32_t gather);
 moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const void* x, int32_t x_rows, const int32_t* order,
                               int32_t k, const void* w, const int32_t* offsets, const int32_t* tiles, int32_t act,
-                              int32_t out_dtype, void* out, void* stream);
+                              int32_t out_dtype, void* out, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * The same with 4-bit rows and weights of one format (K a multiple of 32).  Products of

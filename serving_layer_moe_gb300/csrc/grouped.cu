@@ -8,13 +8,15 @@
 // instruction), and one decoded token costs 16 columns, not 128 rows.
 //
 // Persistent kernel, one CTA per SM:
-//   warp 0     TMA: weight tiles, token tiles, 4-bit scale tiles, into a ring of K slices of
-//              128 bytes a row
+//   warp 0     TMA: weight tiles, into a ring of K slices of 128 bytes a row
 //   warp 1     one thread issues tcgen05.mma: kind::f16 (bf16) or the block-scaled 4-bit
 //              kinds, whose scales go from shared memory to TMEM by tcgen05.cp first
-//   warps 2, 3 what TMA does not place: bf16 token rows gathered by index, and with 4-bit
-//              SwiGLU the weights' scales in the order of the rows (below), by cp.async
-//   warps 4-11 epilogue, two warps to a quarter of the TMEM lanes
+//   warp 2     TMA: token tiles, or rows gathered four at a time by index
+//   warp 3     TMA: 4-bit scale tiles.  (One thread takes 35 to 55 ns to issue a load; all
+//              of a 4-bit slice's from one thread took 620 ns, longer than its products.)
+//   warps 2-5  with 4-bit SwiGLU, the weights' scales in the order of the rows (below), by
+//              cp.async
+//   warps 6-13 epilogue, two warps to a quarter of the TMEM lanes
 // The accumulators are double-buffered in TMEM where they fit beside the scales (bf16:
 // 2 x 256 columns; 4-bit: 2 x 128, or one of 256), so the epilogue of a tile runs under
 // the products of the next.
@@ -40,21 +42,20 @@ using namespace tc;
 
 __device__ uint32_t g_operator_err;
 
-constexpr int THREADS = 384;
-constexpr int FIRST_EPI = 4, EPI_WARPS = 8;
+constexpr int HELPERS = 4, FIRST_EPI = 2 + HELPERS, EPI_WARPS = 8;
+constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
 constexpr int A_BYTES = 128 * 128;             // 128 weight rows, 128 bytes of K each
 constexpr int SCALE_A = 2048, SCALE_B = 2048;  // scales of 128 rows and one K slice (of every 128 tokens: CG of them)
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512, TMEM_SCALES = 256;
-constexpr int QUANT_STRIDE = 80;               // floats a token's 64 features take in the requantising buffer
-constexpr int QUANT_BYTES = 2 * 32 * QUANT_STRIDE * 4;
+constexpr int QUANT_STRIDE = 80;               // floats a token's 64 features take in the epilogue's buffer when requantising
+constexpr int ROW_STRIDE = 272;                // bytes a token's 128 (SwiGLU: 64) bf16 features take in it otherwise
+constexpr int EPI_BYTES = 2 * 32 * QUANT_STRIDE * 4;   // 32 tokens for each half of the epilogue
 constexpr int SMEM_LIMIT = 227 * 1024;
-constexpr int DEPTH = 3;                       // K slices whose copies warps 2 and 3 have in flight; at most the ring's stages
 
 struct ProductArgs {
-  int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant;
-  int m_blocks, kslices, stages, stage_bytes, b_rows, b_box, w_tiles;
-  const __nv_bfloat16* x;      // rows to gather
+  int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant, wide;
+  int m_blocks, kslices, stages, stage_bytes, b_rows, w_tiles;
   const uint8_t* w_scales;
   const float *gx, *gw, *g_out;
   const int32_t *offsets, *order;
@@ -74,6 +75,7 @@ struct Shape4 {
   static constexpr int GS = NV ? 4 : 2;                 // scale groups of a slice
   static constexpr int NACC = FP4 && CG == 2 ? 1 : 2;
   static constexpr int ACC_COLS = CG == 2 ? 256 : 128;
+  static constexpr int BOX = 16 * CG;                   // token rows of a small load; a tile's 128 rows take one
 };
 
 template <int FMT, int CG>
@@ -102,6 +104,17 @@ __device__ __forceinline__ Item item_at(const ProductArgs& a, const int32_t* fir
   return o;
 }
 
+// token columns of a tile, and the rows of them that one CTA loads
+template <int CG>
+__device__ __forceinline__ int columns(int n) { return (n + 16 * CG - 1) / (16 * CG) * (16 * CG); }
+template <int FMT, int CG>
+__device__ __forceinline__ int token_rows(const ProductArgs& a, const Item& o) {
+  using S = Shape4<FMT, CG>;
+  const int mine = columns<CG>(o.n) / CG;
+  if (a.gather) return mine;
+  return a.b_rows == 128 && mine > 3 * S::BOX ? 128 : (mine + S::BOX - 1) / S::BOX * S::BOX;
+}
+
 // The products of one K slice (descriptors da, db, ds of its weights, tokens and scales); `left`: the K that is there
 // when the slice is not FULL.  The scales of even and odd slices go to their own TMEM columns.
 template <int FMT, int CG, bool FULL>
@@ -115,7 +128,7 @@ __device__ __forceinline__ void issue_slice(uint32_t d, uint32_t tmem, uint64_t 
       if (!FULL && g * (S::KS / S::GS) >= left) break;
       copy_scales<CG>(tsa + 4 * g, ds + 32 * g);
       copy_scales<CG>(tsb + 8 * g, ds + (SCALE_A >> 4) + 32 * g);
-      if (CG == 2 && chunks == 2) copy_scales<CG>(tsb + 8 * g + 4, ds + ((SCALE_A + SCALE_B) >> 4) + 32 * g);
+      if (CG == 2 && chunks == 2) copy_scales<CG>(tsb + 8 * g + 4, ds + ((SCALE_A + S::GS * 512) >> 4) + 32 * g);
     }
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
@@ -135,27 +148,29 @@ __device__ __forceinline__ void issue_slice(uint32_t d, uint32_t tmem, uint64_t 
 template <int FMT, int CG>
 __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-               const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX, const ProductArgs a) {
+               const __grid_constant__ CUtensorMap tmXall, const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX, const ProductArgs a) {
   using S = Shape4<FMT, CG>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const uint32_t ring = smem_u32(smem);
   uint8_t* tail = smem + (size_t)a.stages * a.stage_bytes;
-  float* qbuf = reinterpret_cast<float*>(tail);
-  if (a.quant) tail += QUANT_BYTES;
-  const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, tfull = empty + 8 * MAX_STAGES, tempty = tfull + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 16 * MAX_STAGES + 32);
+  uint8_t* ebuf = tail;
+  tail += EPI_BYTES;
+  const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, landed = empty + 8 * MAX_STAGES, tfull = landed + 8 * MAX_STAGES,
+                 tempty = tfull + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 24 * MAX_STAGES + 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* first = reinterpret_cast<int32_t*>(tmem_slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-  const bool helped = S::FP4 ? (bool)a.act : (bool)a.gather;   // warps 2 and 3 fill part of every slice
+  const bool helped = S::FP4 && a.act;   // warps 2 to 5 copy part of every slice
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(full + 8 * s, 1 + (helped ? 2 * CG : 0));
+      mbar_init(full + 8 * s, 1 + (helped ? CG - 1 : 0));   // the loads' bytes; the second CTA's copies
       mbar_init(empty + 8 * s, 1);
+      mbar_init(landed + 8 * s, 32 * HELPERS);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(tfull + 8 * s, 1);
@@ -195,32 +210,16 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     bool ok = true;
     for (int it = it0; it < total && ok; it += step) {
       const Item o = item_at<FMT, CG>(a, first, it);
-      const int ncols = (o.n + 16 * CG - 1) / (16 * CG) * (16 * CG), mine = ncols / CG;   // token columns; those this CTA loads
-      const int boxes = (mine + a.b_box - 1) / a.b_box;
-      const int row0 = o.row0 + (int)rank * mine;
       const int m = o.mb * CG + (int)rank;      // 128-row weight tile (64 gate + 64 up with SwiGLU)
-      const int chunks = S::FP4 ? (o.n + 127) / 128 : 0;
-      uint32_t bytes = (uint32_t)CG * (A_BYTES + (a.gather ? 0u : 128u * boxes * a.b_box));
-      if (S::FP4) bytes += (uint32_t)CG * 512u * S::GS * (chunks + (a.act ? 0 : 1));
+      uint32_t bytes = (uint32_t)CG * (A_BYTES + 128u * token_rows<FMT, CG>(a, o));
+      if (S::FP4) bytes += (uint32_t)CG * 512u * S::GS * (CG + (a.act ? 0 : 1));
       for (int ks = 0; ks < a.kslices; ++ks) {
         if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
-        const uint32_t sa = ring + stage * a.stage_bytes, sb = sa + A_BYTES;
-        uint32_t bar = full + 8 * stage;
-        if (CG == 2) bar = in_rank(bar, 0);
         if (lane == 0) {
+          const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
           if (rank == 0) mbar_expect(full + 8 * stage, bytes);
-          const int x = ks * (S::FP4 ? 128 : 64);
-          // weights: rows of one expert (dimensions K, row, expert), or with SwiGLU (K, 16 rows, gate / up, block of 16, expert)
-          if (a.act) tma_5d<CG>(&tmW, bar, sa, x, 0, 0, 4 * m, o.e);
-          else tma_5d<CG>(&tmW, bar, sa, x, 128 * m, 0, 0, o.e);
-          if (!a.gather)
-            for (int b = 0; b < boxes; ++b) tma_2d<CG>(&tmX, bar, sb + b * a.b_box * 128, x, row0 + b * a.b_box);
-          if (S::FP4) {
-            const uint32_t ss = sb + a.b_rows * 128;
-            if (!a.act) tma_2d<CG>(&tmSW, bar, ss, 0, (o.e * a.w_tiles + m) * a.groups + ks * S::GS);
-            for (int c = 0; c < chunks; ++c)
-              tma_2d<CG>(&tmSX, bar, ss + SCALE_A + c * SCALE_B, 0, (o.tile + c) * a.groups + ks * S::GS);
-          }
+          // rows of one expert (dimensions K, row, expert), or with SwiGLU (K, 16 rows, gate / up, block of 16, expert)
+          tma_5d<CG>(&tmW, bar, ring + stage * a.stage_bytes, ks * (S::FP4 ? 128 : 64), a.act ? 0 : 128 * m, 0, a.act ? 4 * m : 0, o.e);
         }
         if (++stage == a.stages) { stage = 0; phase ^= 1u; }
       }
@@ -246,7 +245,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       const uint64_t da = desc_sw128(ring), db = desc_sw128(ring + A_BYTES), ds = desc_scales(ring + A_BYTES + a.b_rows * 128);
       for (int it = it0; it < total && ok; it += step) {
         const Item o = item_at<FMT, CG>(a, first, it);
-        const int ncols = (o.n + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        const int ncols = columns<CG>(o.n);
         if (!mbar_wait(tempty + 8 * acc, acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * S::ACC_COLS);
@@ -256,6 +255,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const int chunks = (o.n + 127) / 128;
         for (int ks = 0; ks < a.kslices; ++ks) {
           if (!mbar_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
+          if (helped) {
+            if (!mbar_wait(landed + 8 * stage, phase, abort_flag)) { ok = false; break; }
+            fence_async_proxy();
+          }
           fence_after();
           const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
           if (a.K - ks * S::KS >= S::KS) issue_slice<FMT, CG, true>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, 0);
@@ -268,81 +271,76 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         if (++acc == S::NACC) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
-    }
-  } else if (warp < FIRST_EPI) {
-    // ---------------- warps 2 and 3: what TMA does not place ----------------
-    // 4-bit SwiGLU: the weights' scales, in the order of the tile's rows; bf16: token rows by index.  Asynchronous
-    // copies of a few slices are in flight; a landed slice is made visible to the tensor cores and handed over.
-    if (helped) {
-      const int hw = warp - 2;
-      int stage = 0, done_stage = 0, pending = 0;
+    } else if (lane == 0 && helped) {
+      // second CTA of a pair: its copies have landed and are visible to the tensor cores
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      auto finish = [&]() {
-        fence_async_proxy();
-        __syncwarp();
-        if (lane == 0) {
-          if (CG == 2) mbar_arrive_cluster(in_rank(full + 8 * done_stage, 0));
-          else mbar_arrive(full + 8 * done_stage);
+      for (int it = it0; it < total && ok; it += step)
+        for (int ks = 0; ks < a.kslices; ++ks) {
+          if (!mbar_wait(landed + 8 * stage, phase, abort_flag)) { ok = false; break; }
+          fence_async_proxy();
+          mbar_arrive_cluster(in_rank(full + 8 * stage, 0));
+          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
-        if (++done_stage == a.stages) done_stage = 0;
-        --pending;
-      };
+      if (!ok) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
+    }
+  } else if (warp < FIRST_EPI) {
+    // ---------------- tokens (warp 2), scales (warp 3), and with 4-bit SwiGLU the weights' scales (warps 2 to 5) ----------------
+    // Those arrive on `landed` by themselves.  The fence that shows them to the tensor cores is left to warp 1: in these
+    // warps it would wait for every copy still in flight.
+    const int hw = warp - 2;
+    if (helped || hw == 0 || (S::FP4 && hw == 1)) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
       for (int it = it0; it < total && ok; it += step) {
         const Item o = item_at<FMT, CG>(a, first, it);
         const int m = o.mb * CG + (int)rank;
-        const uint8_t* src[2];     // scales: rows lane + 32 (2 hw + j) of the tile
-        uint32_t tok[16];          // tokens: sources of rows 64 hw + 4 i + lane / 8
-        const int ncols = (o.n + 16 * CG - 1) / (16 * CG) * (16 * CG), mine = ncols / CG;
+        const int mine = columns<CG>(o.n) / CG, row0 = o.row0 + (int)rank * mine, rows = token_rows<FMT, CG>(a, o);
+        const uint8_t* src = nullptr;   // scales of row lane + 32 hw of the weight tile
+        int4 idx = make_int4(0, 0, 0, 0);   // sources of token rows 4 * lane ..; past the end: the last again
         if constexpr (S::FP4) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int row = min((lane >> 4) * a.cols + m * 64 + (2 * hw + j) * 16 + (lane & 15), a.N - 1);
-            src[j] = a.w_scales + ((size_t)o.e * a.w_tiles + (row >> 7)) * a.groups * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
-          }
-        } else {
-          const int last = o.row0 + o.n - 1;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = 64 * hw + 4 * i + (lane >> 3);   // past the end: the last row again
-            tok[i] = r < mine ? (uint32_t)(__ldg(a.order + min(o.row0 + (int)rank * mine + r, last)) / a.k) : 0u;
-          }
+          const int row = min((lane >> 4) * a.cols + m * 64 + hw * 16 + (lane & 15), a.N - 1);
+          src = a.w_scales + ((size_t)o.e * a.w_tiles + (row >> 7)) * a.groups * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+        } else if (a.gather && 4 * lane < mine) {
+          const int last = o.row0 + o.n - 1, r = row0 + 4 * lane;
+          idx = make_int4(__ldg(a.order + min(r, last)) / a.k, __ldg(a.order + min(r + 1, last)) / a.k,
+                          __ldg(a.order + min(r + 2, last)) / a.k, __ldg(a.order + min(r + 3, last)) / a.k);
         }
         for (int ks = 0; ks < a.kslices; ++ks) {
           if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
-          const uint32_t sb = ring + stage * a.stage_bytes + A_BYTES;
-          if constexpr (S::FP4) {
-            const uint32_t dst = sb + a.b_rows * 128 + lane * 16 + 8 * hw;
-#pragma unroll
-            for (int g = 0; g < S::GS; ++g) {
-              const int at = ks * S::GS + g;
-              if (at >= a.groups) break;
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + g * 512 + 4 * j), "l"(src[j] + (size_t)at * 512) : "memory");
-            }
-          } else {
-            const int col = ks * 64 + (lane & 7) * 8;
-            const uint32_t there = col < a.K ? 16u : 0u;   // past K: zeros
-            const __nv_bfloat16* x = a.x + (there ? col : 0);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = 64 * hw + 4 * i + (lane >> 3);
-              if (r < mine)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sb + r * 128 + (((lane & 7) ^ (r & 7)) << 4)),
-                             "l"(x + (size_t)tok[i] * a.K), "r"(there) : "memory");
+          const uint32_t sb = ring + stage * a.stage_bytes + A_BYTES, ss = sb + a.b_rows * 128;
+          const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
+          const int x = ks * (S::FP4 ? 128 : 64);
+          if (hw == 0) {
+            if (!S::FP4 && a.gather) {
+              if (4 * lane < mine) tma_gather4<CG>(&tmX, bar, sb + 512 * lane, x, idx);
+            } else if (lane == 0) {
+              if (a.b_rows == 128 && rows == 128) tma_2d<CG>(&tmXall, bar, sb, x, row0);
+              else
+                for (int r = 0; r < rows; r += S::BOX) tma_2d<CG>(&tmX, bar, sb + r * 128, x, row0 + r);
             }
           }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (++pending == DEPTH) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-            finish();
+          if constexpr (S::FP4) {
+            if (hw == 1 && lane == 0) {
+              tma_3d<CG>(&tmSX, bar, ss + SCALE_A, 0, ks * S::GS, o.tile);
+              if (!a.act) tma_3d<CG>(&tmSW, bar, ss, 0, ks * S::GS, o.e * a.w_tiles + m);
+            }
+            if (helped) {
+#pragma unroll
+              for (int g = 0; g < S::GS; ++g) {
+                const int at = ks * S::GS + g;
+                if (at >= a.groups) break;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ss + g * 512 + lane * 16 + 4 * hw), "l"(src + (size_t)at * 512) : "memory");
+              }
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(landed + 8 * stage) : "memory");
+            }
           }
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      while (pending) finish();
+      asm volatile("cp.async.wait_all;" ::: "memory");
       if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
     }
   } else if (warp >= FIRST_EPI) {
@@ -368,6 +366,22 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         tmem_ld32(tbase + c, v);
         tmem_ld_wait();
         const int left = o.n - c;
+        uint8_t* buf = ebuf + part * (EPI_BYTES / 2);
+        if (!a.act && a.wide) {
+          // bf16: 32 tokens of 128 features through shared memory, 16 bytes a thread to memory
+          named_sync(1 + part, 128);      // the last round has been read
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            *reinterpret_cast<__nv_bfloat16*>(buf + i * ROW_STRIDE + (32 * q + lane) * 2) = __float2bfloat16_rn(__uint_as_float(v[i]) * g);
+          named_sync(1 + part, 128);
+          const int t = (threadIdx.x - 32 * FIRST_EPI) & 127, f = m * 128 + (t & 15) * 8;
+#pragma unroll
+          for (int r = t >> 4; r < 32; r += 8)
+            if (r < left && f < a.cols)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c + r) * a.cols + f) =
+                  *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + (t & 15) * 16);
+          continue;
+        }
         if (!a.act) {
           const int f = m * 128 + 32 * q + lane;
           if (f < a.cols) {
@@ -397,6 +411,20 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           const float gate = (half ? got : t0) * g, up = (half ? t1 : got) * g;
           h[i] = gate / (1.0f + expf(-gate)) * up;     // token c + 2 i + half
         }
+        if (a.wide) {
+          named_sync(1 + part, 128);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<__nv_bfloat16*>(buf + (2 * i + half) * ROW_STRIDE + (16 * q + (lane & 15)) * 2) = __float2bfloat16_rn(h[i]);
+          named_sync(1 + part, 128);
+          const int t = (threadIdx.x - 32 * FIRST_EPI) & 127, fw = m * 64 + (t & 7) * 8;
+#pragma unroll
+          for (int r = t >> 3; r < 32; r += 16)
+            if (r < left && fw < a.cols)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c + r) * a.cols + fw) =
+                  *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + (t & 7) * 16);
+          continue;
+        }
         if (!a.quant) {
           if (f < a.cols) {
             const size_t at = (size_t)(o.row0 + c + half) * a.cols + f;
@@ -410,16 +438,16 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           continue;
         }
         if constexpr (S::FP4) {
-          float* buf = qbuf + part * 32 * QUANT_STRIDE;
+          float* hb = reinterpret_cast<float*>(buf);
           named_sync(1 + part, 128);      // the last round has been read
 #pragma unroll
-          for (int i = 0; i < 16; ++i) buf[(2 * i + half) * QUANT_STRIDE + 16 * q + (lane & 15)] = h[i];
+          for (int i = 0; i < 16; ++i) hb[(2 * i + half) * QUANT_STRIDE + 16 * q + (lane & 15)] = h[i];
           named_sync(1 + part, 128);
-          const int t = (threadIdx.x & 127) >> 2, b = threadIdx.x & 3;   // token, 16 of the 64 features
+          const int t = ((threadIdx.x - 32 * FIRST_EPI) & 127) >> 2, b = threadIdx.x & 3;   // token, 16 of the 64 features
           float x[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 w = *reinterpret_cast<const float4*>(buf + t * QUANT_STRIDE + 16 * b + 4 * i);
+            const float4 w = *reinterpret_cast<const float4*>(hb + t * QUANT_STRIDE + 16 * b + 4 * i);
             x[4 * i] = w.x; x[4 * i + 1] = w.y; x[4 * i + 2] = w.z; x[4 * i + 3] = w.w;
           }
           uint32_t top = 0u;
@@ -504,16 +532,16 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   a.m_blocks = (int)ceil_div64(a.act ? a.cols : a.N, (a.act ? 64 : 128) * CG);
   a.kslices = (a.K + S::KS - 1) / S::KS;
   a.w_tiles = (a.N + 127) / 128;
+  a.wide = !a.quant && !a.out_f32 && a.cols % 8 == 0;   // rows of out start on 16 bytes
   // rows of the token area: what the largest tile of P rows can need
-  a.b_box = CG == 2 ? 32 : 16;
   a.b_rows = std::min(128, (a.P + 15) / 16 * 16);
   if (CG == 2) a.b_rows = 128;
   a.stage_bytes = A_BYTES + a.b_rows * 128 + (S::FP4 ? SCALE_A + CG * SCALE_B : 0);
-  const int fixed = 1024 + (a.quant ? QUANT_BYTES : 0) + 16 * MAX_STAGES + 32 + 8 + 4 * (a.E + 1) + 16;
+  const int fixed = 1024 + EPI_BYTES + 24 * MAX_STAGES + 32 + 8 + 4 * (a.E + 1) + 16;
   a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 
-  CUtensorMap tw, tx, tsw, tsx;
+  CUtensorMap tw, tx, txall, tsw, tsx;
   bool ok;
   if (a.act) {
     const cuuint64_t dims[5] = {row_elems, 16, 2, (cuuint64_t)a.cols / 16, (cuuint64_t)a.E};
@@ -529,22 +557,21 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   {
     const cuuint64_t dims[2] = {row_elems, (cuuint64_t)mem.x_rows};
     const cuuint64_t strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {kbox, (cuuint32_t)a.b_box};
-    ok = ok && make_map(&tx, type, 2, mem.x, dims, strides, box, true);
+    const cuuint32_t box[2] = {kbox, a.gather ? 1u : (cuuint32_t)S::BOX}, all[2] = {kbox, 128};
+    ok = ok && make_map(&tx, type, 2, mem.x, dims, strides, box, true) && make_map(&txall, type, 2, mem.x, dims, strides, all, true);
   }
   tsw = tsx = tx;
   if (S::FP4) {
-    const cuuint64_t strides[1] = {512};
-    const cuuint32_t box[2] = {128, (cuuint32_t)S::GS};
-    const cuuint64_t dw[2] = {128, (cuuint64_t)a.E * a.w_tiles * a.groups};
-    const cuuint64_t dx[2] = {128, (cuuint64_t)moe_grouped_tiles(a.P, a.E) * a.groups};
-    ok = ok && make_map(&tsw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, mem.w_scales, dw, strides, box, false) &&
-         make_map(&tsx, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, mem.x_scales, dx, strides, box, false);
+    const cuuint64_t strides[2] = {512, 512ull * a.groups};
+    const cuuint32_t bw[3] = {128, (cuuint32_t)S::GS, 1}, bx[3] = {128, (cuuint32_t)S::GS, CG};
+    const cuuint64_t dw[3] = {128, (cuuint64_t)a.groups, (cuuint64_t)a.E * a.w_tiles};
+    const cuuint64_t dx[3] = {128, (cuuint64_t)a.groups, (cuuint64_t)moe_grouped_tiles(a.P, a.E)};
+    ok = ok && make_map(&tsw, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, mem.w_scales, dw, strides, bw, false) &&
+         make_map(&tsx, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, mem.x_scales, dx, strides, bx, false);
   }
   if (!ok) return fail(MOE_ECUDA, "cuTensorMapEncodeTiled failed");
 
   // at most every token tile the rows can make, on every weight block
-  if (a.stages < DEPTH) return fail(MOE_EINVAL, "E = %d experts leave too little shared memory", a.E);
   const int64_t most = (a.P + (int64_t)(S::NMAX - 1) * std::min(a.P, a.E)) / S::NMAX * a.m_blocks;
   static bool allowed[64] = {};   // the kernel's shared memory, once per device
   int dev = 0;
@@ -581,15 +608,29 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   }
   const int units = (int)std::min<int64_t>(most, resident);
   cfg.gridDim = dim3(units * CG);
-  CK(cudaLaunchKernelEx(&cfg, product_kernel<FMT, CG>, tw, tx, tsw, tsx, a));
+  CK(cudaLaunchKernelEx(&cfg, product_kernel<FMT, CG>, tw, tx, txall, tsw, tsx, a));
   return MOE_OK;
 }
 
 // Pairs of CTAs halve what each SM reads of the tokens; single CTAs give small calls twice the units of work.
+bool use_pairs(int64_t P, int64_t E) { return P >= 64 * E; }
+
 template <int FMT>
 moe_status launch_product(const ProductArgs& a, const ProductMem& mem, cudaStream_t s) {
-  if (a.P >= 64 * (int64_t)a.E) return launch_tiles<FMT, 2>(a, mem, s);
-  return launch_tiles<FMT, 1>(a, mem, s);
+  return use_pairs(a.P, a.E) ? launch_tiles<FMT, 2>(a, mem, s) : launch_tiles<FMT, 1>(a, mem, s);
+}
+
+// xs[i] = x[order[i] / k]: 16 bytes a thread.  A pair's token tile gathered inside the product, once for every weight
+// block, costs more than this pass: 8192 tokens, 8 of 128 experts, K 2048, N 1536 take 343 us from rows in order and
+// 950 (TMA gather) or 700 us (cp.async) by index.
+__global__ void __launch_bounds__(256)
+gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ order, int P, int row16, int k, uint4* __restrict__ xs) {
+  const int64_t units = (int64_t)P * row16;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+    const int i = (int)(u / row16), c = (int)(u - (int64_t)i * row16);
+    const int p = __ldg(order + i);
+    if (p >= 0) xs[u] = __ldg(x + (size_t)(p / k) * row16 + c);
+  }
 }
 
 moe_status check_product(int32_t P, int32_t E, int32_t N, int32_t K, int32_t quantum, const int32_t* offsets,
@@ -610,9 +651,14 @@ moe_status check_product(int32_t P, int32_t E, int32_t N, int32_t K, int32_t qua
 
 using namespace moe;
 
+extern "C" int64_t moe_grouped_matmul_workspace(int32_t P, int32_t E, int32_t K, int32_t gather) {
+  return gather && P > 0 && use_pairs(P, E) ? (int64_t)P * K * 2 : 0;
+}
+
 extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const void* x, int32_t x_rows,
                                          const int32_t* order, int32_t k, const void* w, const int32_t* offsets,
-                                         const int32_t* tiles, int32_t act, int32_t out_dtype, void* out, void* stream) {
+                                         const int32_t* tiles, int32_t act, int32_t out_dtype, void* out, void* workspace,
+                                         int64_t workspace_bytes, void* stream) {
   moe_status st = check_product(P, E, N, K, 8, offsets, tiles, act, out_dtype);
   if (st != MOE_OK) return st;
   if (order && (k < 1 || !aligned_to(order, 4))) return fail(MOE_EINVAL, "order needs k >= 1 and 4-byte alignment");
@@ -621,8 +667,19 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
   if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(out, 16)) return fail(MOE_EINVAL, "x, w and out must be 16-byte aligned");
   ProductArgs a{};
   a.P = P; a.E = E; a.N = N; a.K = K; a.k = k; a.act = act; a.cols = act ? N / 2 : N; a.gather = order != nullptr;
-  a.x = static_cast<const __nv_bfloat16*>(x);
   a.out_f32 = out_dtype == MOE_F32; a.order = order; a.offsets = offsets; a.tiles = tiles; a.out = out;
+  const int64_t need = moe_grouped_matmul_workspace(P, E, K, a.gather);
+  if (need) {
+    if (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))
+      return fail(MOE_EINVAL, "workspace must hold %lld bytes, 16-byte aligned, holds %lld", (long long)need, (long long)workspace_bytes);
+    const int64_t units = (int64_t)P * (K / 8);
+    const int grid = (int)std::min<int64_t>((units + 255) / 256, (int64_t)operator_sms() * 16);
+    gather_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<const uint4*>(x), order, P, K / 8, k, static_cast<uint4*>(workspace));
+    CK(cudaGetLastError());
+    a.gather = 0;
+    x = workspace;
+    x_rows = P;
+  }
   return launch_product<MOE_BF16>(a, ProductMem{x, w, nullptr, nullptr, x_rows}, static_cast<cudaStream_t>(stream));
 }
 

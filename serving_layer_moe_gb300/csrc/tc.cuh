@@ -78,6 +78,27 @@ __device__ __forceinline__ void tma_2d(const CUtensorMap* m, uint32_t bar, uint3
                      dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 template <int CG>
+__device__ __forceinline__ void tma_3d(const CUtensorMap* m, uint32_t bar, uint32_t dst, int x, int y, int z) {
+  if constexpr (CG == 1)
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+                 "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+  else
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                     dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+// four rows of a map whose box is one row high
+template <int CG>
+__device__ __forceinline__ void tma_gather4(const CUtensorMap* m, uint32_t bar, uint32_t dst, int x, int4 r) {
+  if constexpr (CG == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            dst), "l"(m), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar) : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], "
+        "[%7];" ::"r"(dst), "l"(m), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar) : "memory");
+}
+template <int CG>
 __device__ __forceinline__ void tma_5d(const CUtensorMap* m, uint32_t bar, uint32_t dst, int x, int a, int b, int c, int d) {
   if constexpr (CG == 1)
     asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(

@@ -22,7 +22,8 @@ import torch
 from .binding import DTYPES, _check, load_library
 
 OPERATOR_SYMBOLS = ("moe_grouped_tiles", "moe_group_workspace", "moe_route", "moe_group_pairs", "moe_fp4_scale",
-                    "moe_quantize_fp4", "moe_dequantize_fp4", "moe_grouped_matmul", "moe_grouped_matmul_fp4",
+                    "moe_quantize_fp4", "moe_dequantize_fp4", "moe_grouped_matmul_workspace", "moe_grouped_matmul",
+                    "moe_grouped_matmul_fp4",
                     "moe_combine", "moe_operators_check")
 
 SCORING = {"softmax": 0, "sigmoid": 1}
@@ -48,7 +49,8 @@ def _operators():
             "moe_fp4_scale": [I32, I64, I32, P, P, P],
             "moe_quantize_fp4": [I32, I32, I32, I32, P, I32, P, I32, I32, I32, P, P, P, P, P, P],
             "moe_dequantize_fp4": [I32, I32, I32, I32, P, P, P, I32, I32, P, P, I32, P, P],
-            "moe_grouped_matmul": [I32, I32, I32, I32, P, I32, P, I32, P, P, P, I32, I32, P, P],
+            "moe_grouped_matmul_workspace": [I32, I32, I32, I32],
+            "moe_grouped_matmul": [I32, I32, I32, I32, P, I32, P, I32, P, P, P, I32, I32, P, P, I64, P],
             "moe_grouped_matmul_fp4": [I32, I32, I32, I32, I32, P, P, P, P, P, P, I32, P, P, I32, I32, P, P, P, P, P],
             "moe_combine": [I32, I32, I32, I32, P, P, P, I32, P, P],
             "moe_operators_check": [P],
@@ -56,7 +58,7 @@ def _operators():
         for name, args in sig.items():
             fn = getattr(lib, name)
             fn.argtypes = args
-            fn.restype = ctypes.c_int64 if name in ("moe_grouped_tiles", "moe_group_workspace") else ctypes.c_int
+            fn.restype = ctypes.c_int64 if name == "moe_grouped_tiles" or name.endswith("_workspace") else ctypes.c_int
         _lib = lib
     return _lib
 
@@ -398,8 +400,13 @@ def grouped_matmul(x, w, groups, *, act="none", gather=False, out_dtype=torch.bf
             return grouped_matmul(x, w, groups, act=act, gather=gather, out_dtype=out_dtype)
     off, til, order, _ = groups._ptrs
     out = x.new_empty((groups.P, cols), dtype=out_dtype)
-    _check(_operators().moe_grouped_matmul(groups.P, E, N, K, xp, rows, order if gather else None, groups.k, wp, off, til,
-                                           ACTS[act], _FLOATS[out_dtype], out.data_ptr(), _stream(index)))
+    ops, ws, n = _operators(), None, 0
+    if gather:
+        n = ops.moe_grouped_matmul_workspace(groups.P, E, K, 1)
+        if n:
+            ws = x.new_empty(n, dtype=_U8)
+    _check(ops.moe_grouped_matmul(groups.P, E, N, K, xp, rows, order if gather else None, groups.k, wp, off, til, ACTS[act],
+                                  _FLOATS[out_dtype], out.data_ptr(), ws.data_ptr() if n else None, n, _stream(index)))
     return out
 
 
