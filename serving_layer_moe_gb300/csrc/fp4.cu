@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(QuantArgs a) {
       float step;
       const float g = NV && a.g ? __ldg(a.g + o.g) : 1.0f;
       const uint32_t code = block_scale<NV>(m, g, step);
-      const uint2 q = encode16<NV>(v, code, step);
+      const uint2 q = encode16<NV>(v, m, code, step);
       if (u >= units || o.src < 0) continue;
       *reinterpret_cast<uint2*>(a.codes + (size_t)(r0 + r) * (a.K / 2) + c * 8) = q;
       const int b = NV ? c : c >> 1;

@@ -17,9 +17,9 @@
 //   warps 2-5  with 4-bit SwiGLU, the weights' scales in the order of the rows (below), by
 //              cp.async
 //   warps 6-13 epilogue, two warps to a quarter of the TMEM lanes
-// The accumulators are double-buffered in TMEM where they fit beside the scales (bf16:
-// 2 x 256 columns; 4-bit: 2 x 128, or one of 256), so the epilogue of a tile runs under
-// the products of the next.
+// Two accumulators in TMEM let the epilogue of a tile run under the products of the next.
+// Two of 256 columns leave no room for 4-bit scales, so those of 4-bit pairs overlap by 64
+// columns, which the epilogue reads first and then lets the next tile begin.
 //
 // SwiGLU: the weight rows of a tile alternate 16 gate rows and the 16 up rows of the same
 // features (one 5-dimensional tensor map does it), so lanes l and l + 16 of a warp hold
@@ -47,7 +47,8 @@ constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
 constexpr int A_BYTES = 128 * 128;             // 128 weight rows, 128 bytes of K each
 constexpr int SCALE_A = 2048, SCALE_B = 2048;  // scales of 128 rows and one K slice (of every 128 tokens: CG of them)
 constexpr int MAX_STAGES = 12;
-constexpr int TMEM_COLS = 512, TMEM_SCALES = 256;
+constexpr int TMEM_COLS = 512, TMEM_SCALES = 448;
+constexpr int SCALE_SLOTS = 5;                 // 12-column slots of block scales, one group of 4 blocks each, used in turn
 constexpr int QUANT_STRIDE = 80;               // floats a token's 64 features take in the epilogue's buffer when requantising
 constexpr int ROW_STRIDE = 272;                // bytes a token's 128 (SwiGLU: 64) bf16 features take in it otherwise
 constexpr int EPI_BYTES = 2 * 32 * QUANT_STRIDE * 4;   // 32 tokens for each half of the epilogue
@@ -73,8 +74,9 @@ struct Shape4 {
   static constexpr int KS = FP4 ? 256 : 64;             // K of a slice
   static constexpr int KI = FP4 ? 64 : 16;              // K of an instruction
   static constexpr int GS = NV ? 4 : 2;                 // scale groups of a slice
-  static constexpr int NACC = FP4 && CG == 2 ? 1 : 2;
-  static constexpr int ACC_COLS = CG == 2 ? 256 : 128;
+  // TMEM column of the second accumulator.  4-bit pairs: the two overlap in 64 columns, to leave room for the scales
+  static constexpr int ACC_COLS = CG == 1 ? 128 : FP4 ? 192 : 256;
+  static constexpr bool OVERLAP = FP4 && CG == 2;
   static constexpr int BOX = 16 * CG;                   // token rows of a small load; a tile's 128 rows take one
 };
 
@@ -116,25 +118,27 @@ __device__ __forceinline__ int token_rows(const ProductArgs& a, const Item& o) {
 }
 
 // The products of one K slice (descriptors da, db, ds of its weights, tokens and scales); `left`: the K that is there
-// when the slice is not FULL.  The scales of even and odd slices go to their own TMEM columns.
+// when the slice is not FULL.  Scales take the next of the TMEM slots, so that copies do not wait for the last products.
 template <int FMT, int CG, bool FULL>
 __device__ __forceinline__ void issue_slice(uint32_t d, uint32_t tmem, uint64_t da, uint64_t db, uint64_t ds, uint32_t idesc, int chunks,
-                                            int ks, int left) {
+                                            int ks, int left, uint32_t& slot) {
   using S = Shape4<FMT, CG>;
   if constexpr (S::FP4) {
-    const uint32_t tsa = tmem + TMEM_SCALES + 48u * (ks & 1), tsb = tsa + 16;
+    uint32_t ts[S::GS];   // scales of the weights; of the tokens 4 columns on
 #pragma unroll
     for (int g = 0; g < S::GS; ++g) {
       if (!FULL && g * (S::KS / S::GS) >= left) break;
-      copy_scales<CG>(tsa + 4 * g, ds + 32 * g);
-      copy_scales<CG>(tsb + 8 * g, ds + (SCALE_A >> 4) + 32 * g);
-      if (CG == 2 && chunks == 2) copy_scales<CG>(tsb + 8 * g + 4, ds + ((SCALE_A + S::GS * 512) >> 4) + 32 * g);
+      ts[g] = tmem + TMEM_SCALES + 12u * slot;
+      if (++slot == SCALE_SLOTS) slot = 0;
+      copy_scales<CG>(ts[g], ds + 32 * g);
+      copy_scales<CG>(ts[g] + 4, ds + (SCALE_A >> 4) + 32 * g);
+      if (CG == 2 && chunks == 2) copy_scales<CG>(ts[g] + 8, ds + ((SCALE_A + S::GS * 512) >> 4) + 32 * g);
     }
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       if (!FULL && kk * S::KI >= left) break;
       const uint32_t g = S::NV ? kk : kk >> 1, id = S::NV ? 0u : 2u * (kk & 1);
-      mma_fp4<CG, S::NV>(d, da + 2 * kk, db + 2 * kk, idesc | (id << 4) | (id << 29), tsa + 4 * g, tsb + 8 * g, (ks | kk) != 0);
+      mma_fp4<CG, S::NV>(d, da + 2 * kk, db + 2 * kk, idesc | (id << 4) | (id << 29), ts[g], ts[g] + 4, (ks | kk) != 0);
     }
   } else {
 #pragma unroll
@@ -240,13 +244,14 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     // ---------------- products ----------------
     if (lane == 0 && rank == 0) {
       int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t phase = 0, acc_phase = 0, slot = 0;
       bool ok = true;
       const uint64_t da = desc_sw128(ring), db = desc_sw128(ring + A_BYTES), ds = desc_scales(ring + A_BYTES + a.b_rows * 128);
       for (int it = it0; it < total && ok; it += step) {
         const Item o = item_at<FMT, CG>(a, first, it);
         const int ncols = columns<CG>(o.n);
-        if (!mbar_wait(tempty + 8 * acc, acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+        // overlapping accumulators: the tile before this one has let go of the overlap; otherwise: the one before that is read
+        if (!mbar_wait(tempty + (S::OVERLAP ? 0 : 8 * acc), S::OVERLAP ? (uint32_t)acc ^ 1u : acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * S::ACC_COLS);
         // D fp32; bf16 operands, or e2m1 with e4m3 / e8m0 scales; both K-major; N; M = 128 CG
@@ -261,14 +266,14 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           }
           fence_after();
           const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
-          if (a.K - ks * S::KS >= S::KS) issue_slice<FMT, CG, true>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, 0);
-          else issue_slice<FMT, CG, false>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, a.K - ks * S::KS);
+          if (a.K - ks * S::KS >= S::KS) issue_slice<FMT, CG, true>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, 0, slot);
+          else issue_slice<FMT, CG, false>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, a.K - ks * S::KS, slot);
           commit<CG>(empty + 8 * stage);
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
         commit<CG>(tfull + 8 * acc);
-        if (++acc == S::NACC) { acc = 0; acc_phase ^= 1u; }
+        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
     } else if (lane == 0 && helped) {
@@ -360,11 +365,30 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       float g = 1.0f;
       if (S::FP4) g = (a.gx ? __ldg(a.gx) : 1.0f) * (a.gw ? __ldg(a.gw + (a.gw_count > 1 ? o.e : 0)) : 1.0f);
       const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * S::ACC_COLS);
+      bool released = false;
+      auto release = [&]() {   // the accumulator (or the part the next one needs) has been read
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t bar = tempty + (S::OVERLAP ? 0 : 8 * acc);
+          if (CG == 2) mbar_arrive_cluster(in_rank(bar, 0));
+          else mbar_arrive(bar);
+        }
+      };
+      // 64 columns a round; the overlap of the accumulators, columns 192 on of the first and 0 on of the second, first
 #pragma unroll 1
-      for (int c = 32 * part; c < o.n; c += 64) {
+      for (int round = 0; round < S::NMAX / 64; ++round) {
+        const int c = 32 * part + (S::OVERLAP && acc == 0 ? (round + 3) % 4 : round) * 64;
         uint32_t v[32];
-        tmem_ld32(tbase + c, v);
-        tmem_ld_wait();
+        const bool some = c < o.n;
+        if (some) {
+          tmem_ld32(tbase + c, v);
+          tmem_ld_wait();
+        }
+        if (S::OVERLAP ? round == 0 : (round + 1) * 64 >= o.n || round + 1 == S::NMAX / 64) {
+          if (S::OVERLAP || !released) { release(); released = true; }
+        }
+        if (!some) continue;
         const int left = o.n - c;
         uint8_t* buf = ebuf + part * (EPI_BYTES / 2);
         if (!a.act && a.wide) {
@@ -409,7 +433,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           const float t0 = __uint_as_float(v[2 * i]), t1 = __uint_as_float(v[2 * i + 1]);
           const float got = __shfl_xor_sync(0xffffffffu, half ? t0 : t1, 16);
           const float gate = (half ? got : t0) * g, up = (half ? t1 : got) * g;
-          h[i] = gate / (1.0f + expf(-gate)) * up;     // token c + 2 i + half
+          h[i] = __fdividef(gate, 1.0f + expf(-gate)) * up;     // token c + 2 i + half; the division is good to 2 units
         }
         if (a.wide) {
           named_sync(1 + part, 128);
@@ -456,7 +480,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           if (!S::NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           float st;
           uint32_t code = block_scale<S::NV>(top, S::NV && a.g_out ? __ldg(a.g_out) : 1.0f, st);
-          const uint2 codes = encode16<S::NV>(x, code, st);
+          const uint2 codes = encode16<S::NV>(x, top, code, st);
           const int fb = m * 64 + 16 * b;
           const int og = (a.cols + (S::NV ? 63 : 127)) / (S::NV ? 64 : 128);
           const size_t pad = ((size_t)__ldg(a.tiles + o.e) << 7) + (o.row0 - __ldg(a.offsets + o.e)) + c + t;
@@ -477,13 +501,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           }
         }
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 2) mbar_arrive_cluster(in_rank(tempty + 8 * acc, 0));
-        else mbar_arrive(tempty + 8 * acc);
-      }
-      if (++acc == S::NACC) { acc = 0; acc_phase ^= 1u; }
+      if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
     }
   }
   __syncwarp();

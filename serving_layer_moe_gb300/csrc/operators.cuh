@@ -77,19 +77,33 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float g, flo
 // what a value is multiplied by (MXFP4: 2^-X, exact) -- NVFP4 divides by the step
 __device__ __forceinline__ float e8m0_inverse(uint32_t code) { return e8m0_value(254u - code); }
 
-// 16 values -> 8 bytes of codes
+// 16 values -> 8 bytes of codes.  NVFP4's x / step is the correctly rounded quotient without a division an element
+// (Markstein 1990): with r = 1 / step rounded to nearest and q = x r, the remainder x - q step is exact in one fma, and
+// q + remainder * r rounds to the quotient.  That holds away from the ends of the exponent range; outside it (and for
+// infinities) the elements are divided.
 template <bool NV>
-__device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t code, float step) {
+__device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t amax_bits, uint32_t code, float step) {
   uint32_t w[2] = {0u, 0u};
-  const bool none = !(step > 0.0f);
-  const float inv = NV ? 0.0f : e8m0_inverse(code);
+  if (!(step > 0.0f)) return make_uint2(0u, 0u);
+  if (!NV) {
+    const float inv = e8m0_inverse(code);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float lo = NV ? __fdiv_rn(v[2 * i], step) : v[2 * i] * inv;
-    const float hi = NV ? __fdiv_rn(v[2 * i + 1], step) : v[2 * i + 1] * inv;
-    w[i >> 2] |= to_e2m1x2(lo, hi) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= to_e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
   }
-  return none ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
+  const float r = __frcp_rn(step);
+  if (step > 1e-24f && step < 1e24f && __uint_as_float(amax_bits) * r < 1e30f) {
+    auto quotient = [&](float x) {
+      const float q = x * r;
+      return copysignf(fmaf(fmaf(-q, step, x), r, q), x);   // a zero keeps its sign
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= to_e2m1x2(quotient(v[2 * i]), quotient(v[2 * i + 1])) << (8 * (i & 3));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= to_e2m1x2(__fdiv_rn(v[2 * i], step), __fdiv_rn(v[2 * i + 1], step)) << (8 * (i & 3));
+  }
+  return make_uint2(w[0], w[1]);
 }
 
 }  // namespace moe

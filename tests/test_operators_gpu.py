@@ -118,13 +118,15 @@ def test_group_pairs_drops_foreign_ids(moe, T, E, k):
 # 4-bit quantisation
 # ---------------------------------------------------------------------------------------------------------
 def special_rows(K):
-    x = np.zeros((7, K), np.float32)
+    x = np.zeros((9, K), np.float32)
     x[1] = 1e-40
     x[2, ::3] = np.inf
     x[3, 5] = np.nan
     x[4] = np.finfo(np.float32).max
     x[5] = np.resize([0.25, -0.75, 1.25, -1.75, 2.5, -3.5, 5.0, 6.0], K)      # ties
     x[6] = np.resize([-0.0, 1e-30, 3e38, -2.0], K)
+    x[7] = np.resize([-0.0, 1.0, 0.0, -0.5], K)
+    x[8] = np.resize([-3e37, 2.0, -1e30, 1e37], K)                            # far past the largest scale, both signs
     return x
 
 
@@ -134,7 +136,7 @@ def special_rows(K):
 def test_quantize_stack_bit_for_bit(moe, wdtype, dtype, G, N, K):
     rng = np.random.default_rng(G * N + K)
     x = (rng.standard_normal((G * N, K)) * np.exp(rng.standard_normal((G * N, 1)) * 3)).astype(np.float32)
-    x[: min(7, G * N)] = special_rows(K)[: min(7, G * N)]
+    x[: min(9, G * N)] = special_rows(K)[: min(9, G * N)]
     if dtype == torch.bfloat16:
         x = bf16(x)
     g = np.exp(rng.standard_normal(G) - 6).astype(np.float32) if wdtype == "nvfp4" else None
