@@ -8,15 +8,16 @@
 // instruction), and one decoded token costs 16 columns, not 128 rows.
 //
 // Persistent kernel, one CTA per SM:
-//   warp 0     TMA: weight tiles, into a ring of K slices of 128 bytes a row
-//   warp 1     one thread issues tcgen05.mma: kind::f16 (bf16) or the block-scaled 4-bit
-//              kinds, whose scales go from shared memory to TMEM by tcgen05.cp first
-//   warp 2     TMA: token tiles, or rows gathered four at a time by index
-//   warp 3     TMA: 4-bit scale tiles.  (One thread takes 35 to 55 ns to issue a load; all
-//              of a 4-bit slice's from one thread took 620 ns, longer than its products.)
-//   warps 2-5  with 4-bit SwiGLU, the weights' scales in the order of the rows (below), by
-//              cp.async
-//   warps 6-13 epilogue, two warps to a quarter of the TMEM lanes
+//   warp 0       TMA: weight tiles, into a ring of K slices of 128 bytes a row
+//   warp 1       one lane issues tcgen05.mma: kind::f16 (bf16) or the block-scaled 4-bit
+//                kinds, whose scales go from shared memory to TMEM by tcgen05.cp first
+//   warp 2       TMA: token tiles, or rows gathered four at a time by index
+//   warp 3       TMA: 4-bit scale tiles
+//   warps 4-7    with 4-bit SwiGLU, the weights' scales into the order of the rows (below)
+//   warps 8-15   epilogue, two warps to a quarter of the TMEM lanes
+// The issuing lane is picked by elect.sync in a converged warp: where the compiler has to
+// allow for several lanes it issues each load, copy and product through a loop over lanes
+// (16384 rows of 32 experts, K 7168, N 4096, NVFP4: 391 us from lane 0, 196 elected).
 // Two accumulators in TMEM let the epilogue of a tile run under the products of the next.
 // Two of 256 columns leave no room for 4-bit scales, so those of 4-bit pairs overlap by 64
 // columns, which the epilogue reads first and then lets the next tile begin.
@@ -42,13 +43,13 @@ using namespace tc;
 
 __device__ uint32_t g_operator_err;
 
-constexpr int HELPERS = 4, FIRST_EPI = 2 + HELPERS, EPI_WARPS = 8;
+constexpr int FIRST_SORT = 4, FIRST_EPI = 8, EPI_WARPS = 8;
 constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
 constexpr int A_BYTES = 128 * 128;             // 128 weight rows, 128 bytes of K each
-constexpr int SCALE_A = 2048, SCALE_B = 2048;  // scales of 128 rows and one K slice (of every 128 tokens: CG of them)
 constexpr int MAX_STAGES = 12;
-constexpr int TMEM_COLS = 512, TMEM_SCALES = 448;
-constexpr int SCALE_SLOTS = 5;                 // 12-column slots of block scales, one group of 4 blocks each, used in turn
+constexpr int TMEM_COLS = 512;
+constexpr int TMEM_SCALES = 448, SCALE_SLOTS = 5;   // 12-column slots of block scales, a group of 4 blocks each, used in turn:
+                                               // 4 columns of the weights' (128 rows), 8 of the tokens'
 constexpr int QUANT_STRIDE = 80;               // floats a token's 64 features take in the epilogue's buffer when requantising
 constexpr int ROW_STRIDE = 272;                // bytes a token's 128 (SwiGLU: 64) bf16 features take in it otherwise
 constexpr int EPI_BYTES = 2 * 32 * QUANT_STRIDE * 4;   // 32 tokens for each half of the epilogue
@@ -56,8 +57,7 @@ constexpr int SMEM_LIMIT = 227 * 1024;
 
 struct ProductArgs {
   int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant, wide;
-  int m_blocks, kslices, stages, stage_bytes, b_rows, w_tiles;
-  const uint8_t* w_scales;
+  int m_blocks, kslices, stages, stage_bytes, b_rows, w_tiles, w_parts;   // w_parts: scale tiles one weight tile's rows are in
   const float *gx, *gw, *g_out;
   const int32_t *offsets, *order;
   void* out;
@@ -74,6 +74,7 @@ struct Shape4 {
   static constexpr int KS = FP4 ? 256 : 64;             // K of a slice
   static constexpr int KI = FP4 ? 64 : 16;              // K of an instruction
   static constexpr int GS = NV ? 4 : 2;                 // scale groups of a slice
+  static constexpr int TILE_SCALES = GS * 512;          // bytes of a slice's scales of 128 rows
   // TMEM column of the second accumulator.  4-bit pairs: the two overlap in 64 columns, to leave room for the scales
   static constexpr int ACC_COLS = CG == 1 ? 128 : FP4 ? 192 : 256;
   static constexpr bool OVERLAP = FP4 && CG == 2;
@@ -117,34 +118,34 @@ __device__ __forceinline__ int token_rows(const ProductArgs& a, const Item& o) {
   return a.b_rows == 128 && mine > 3 * S::BOX ? 128 : (mine + S::BOX - 1) / S::BOX * S::BOX;
 }
 
-// The products of one K slice (descriptors da, db, ds of its weights, tokens and scales); `left`: the K that is there
-// when the slice is not FULL.  Scales take the next of the TMEM slots, so that copies do not wait for the last products.
+// The products of one K slice (descriptors da, db, ds of its weights, tokens and scales); `left`: the K that is there when
+// the slice is not FULL.  Scales take the TMEM slots from `slot` on, so that copies do not wait for the last products.
 template <int FMT, int CG, bool FULL>
-__device__ __forceinline__ void issue_slice(uint32_t d, uint32_t tmem, uint64_t da, uint64_t db, uint64_t ds, uint32_t idesc, int chunks,
-                                            int ks, int left, uint32_t& slot) {
+__device__ __forceinline__ void issue_slice(uint32_t d, uint32_t tmem, uint64_t da, uint64_t db, uint64_t ds, uint32_t idesc, bool second,
+                                            uint32_t acc, int left, uint32_t slot) {
   using S = Shape4<FMT, CG>;
   if constexpr (S::FP4) {
-    uint32_t ts[S::GS];   // scales of the weights; of the tokens 4 columns on
+    uint32_t ts[S::GS];
 #pragma unroll
     for (int g = 0; g < S::GS; ++g) {
       if (!FULL && g * (S::KS / S::GS) >= left) break;
       ts[g] = tmem + TMEM_SCALES + 12u * slot;
       if (++slot == SCALE_SLOTS) slot = 0;
-      copy_scales<CG>(ts[g], ds + 32 * g);
-      copy_scales<CG>(ts[g] + 4, ds + (SCALE_A >> 4) + 32 * g);
-      if (CG == 2 && chunks == 2) copy_scales<CG>(ts[g] + 8, ds + ((SCALE_A + S::GS * 512) >> 4) + 32 * g);
+      copy_scales<CG>(ts[g], ds + ((CG * S::TILE_SCALES) >> 4) + 32 * g);
+      copy_scales<CG>(ts[g] + 4, ds + 32 * g);
+      if (CG == 2 && second) copy_scales<CG>(ts[g] + 8, ds + (S::TILE_SCALES >> 4) + 32 * g);
     }
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       if (!FULL && kk * S::KI >= left) break;
       const uint32_t g = S::NV ? kk : kk >> 1, id = S::NV ? 0u : 2u * (kk & 1);
-      mma_fp4<CG, S::NV>(d, da + 2 * kk, db + 2 * kk, idesc | (id << 4) | (id << 29), ts[g], ts[g] + 4, (ks | kk) != 0);
+      mma_fp4<CG, S::NV>(d, da + 2 * kk, db + 2 * kk, idesc | (id << 4) | (id << 29), ts[g], ts[g] + 4, acc | (uint32_t)kk);
     }
   } else {
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       if (!FULL && kk * S::KI >= left) break;
-      mma_bf16<CG>(d, da + 2 * kk, db + 2 * kk, idesc, (ks | kk) != 0);
+      mma_bf16<CG>(d, da + 2 * kk, db + 2 * kk, idesc, acc | (uint32_t)kk);
     }
   }
 }
@@ -161,20 +162,21 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
   uint8_t* tail = smem + (size_t)a.stages * a.stage_bytes;
   uint8_t* ebuf = tail;
   tail += EPI_BYTES;
-  const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, landed = empty + 8 * MAX_STAGES, tfull = landed + 8 * MAX_STAGES,
+  const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, sfull = empty + 8 * MAX_STAGES, tfull = sfull + 8 * MAX_STAGES,
                  tempty = tfull + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 24 * MAX_STAGES + 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* first = reinterpret_cast<int32_t*>(tmem_slot + 2);
+  int32_t* gathered = reinterpret_cast<int32_t*>(tail + 24 * MAX_STAGES + 48);   // sources of a tile's 128 token rows
+  int32_t* first = gathered + 128;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
-  const bool helped = S::FP4 && a.act;   // warps 2 to 5 copy part of every slice
+  const bool sorts = S::FP4 && a.act;   // warps 4 on sort the weights' scales
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(full + 8 * s, 1 + (helped ? CG - 1 : 0));   // the loads' bytes; the second CTA's copies
+      mbar_init(full + 8 * s, 1 + (sorts ? CG * S::GS : 0));
       mbar_init(empty + 8 * s, 1);
-      mbar_init(landed + 8 * s, 32 * HELPERS);
+      mbar_init(sfull + 8 * s, 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(tfull + 8 * s, 1);
@@ -215,11 +217,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     for (int it = it0; it < total && ok; it += step) {
       const Item o = item_at<FMT, CG>(a, first, it);
       const int m = o.mb * CG + (int)rank;      // 128-row weight tile (64 gate + 64 up with SwiGLU)
-      uint32_t bytes = (uint32_t)CG * (A_BYTES + 128u * token_rows<FMT, CG>(a, o));
-      if (S::FP4) bytes += (uint32_t)CG * 512u * S::GS * (CG + (a.act ? 0 : 1));
+      const uint32_t bytes = (uint32_t)CG * (A_BYTES + 128u * token_rows<FMT, CG>(a, o) + (S::FP4 ? (uint32_t)S::TILE_SCALES * (CG + (a.act ? 0 : 1)) : 0u));
       for (int ks = 0; ks < a.kslices; ++ks) {
-        if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
-        if (lane == 0) {
+        if (!warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+        if (elect_one()) {
           const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
           if (rank == 0) mbar_expect(full + 8 * stage, bytes);
           // rows of one expert (dimensions K, row, expert), or with SwiGLU (K, 16 rows, gate / up, block of 16, expert)
@@ -237,12 +238,12 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     }
     // every slice has been used, and no arrival on this CTA's barriers is outstanding, before it ends
     for (int i = 0; i < a.stages && ok; ++i) {
-      ok = mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag);
+      ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag);
       if (++stage == a.stages) { stage = 0; phase ^= 1u; }
     }
   } else if (warp == 1) {
     // ---------------- products ----------------
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0, slot = 0;
       bool ok = true;
@@ -251,101 +252,128 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const Item o = item_at<FMT, CG>(a, first, it);
         const int ncols = columns<CG>(o.n);
         // overlapping accumulators: the tile before this one has let go of the overlap; otherwise: the one before that is read
-        if (!mbar_wait(tempty + (S::OVERLAP ? 0 : 8 * acc), S::OVERLAP ? (uint32_t)acc ^ 1u : acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+        if (!warp_wait(tempty + (S::OVERLAP ? 0 : 8 * acc), S::OVERLAP ? (uint32_t)acc ^ 1u : acc_phase ^ 1u, abort_flag)) { ok = false; break; }
         fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * S::ACC_COLS);
         // D fp32; bf16 operands, or e2m1 with e4m3 / e8m0 scales; both K-major; N; M = 128 CG
         const uint32_t idesc = ((uint32_t)(ncols >> 3) << 17) | ((uint32_t)(8 * CG) << 24) |
                                (S::FP4 ? (1u << 7) | (1u << 10) | (S::NV ? 0u : 1u << 23) : (1u << 4) | (1u << 7) | (1u << 10));
-        const int chunks = (o.n + 127) / 128;
         for (int ks = 0; ks < a.kslices; ++ks) {
-          if (!mbar_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
-          if (helped) {
-            if (!mbar_wait(landed + 8 * stage, phase, abort_flag)) { ok = false; break; }
-            fence_async_proxy();
-          }
+          if (!warp_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
           fence_after();
           const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
-          if (a.K - ks * S::KS >= S::KS) issue_slice<FMT, CG, true>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, 0, slot);
-          else issue_slice<FMT, CG, false>(d, tmem, da + at, db + at, ds + at, idesc, chunks, ks, a.K - ks * S::KS, slot);
-          commit<CG>(empty + 8 * stage);
+          const int left = a.K - ks * S::KS;
+          if (elect_one()) {
+            if (left >= S::KS) issue_slice<FMT, CG, true>(d, tmem, da + at, db + at, ds + at, idesc, o.n > 128, ks, 0, slot);
+            else issue_slice<FMT, CG, false>(d, tmem, da + at, db + at, ds + at, idesc, o.n > 128, ks, left, slot);
+            commit<CG>(empty + 8 * stage);
+          }
+          __syncwarp();
+          slot = (slot + S::GS) % SCALE_SLOTS;
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
-        commit<CG>(tfull + 8 * acc);
+        if (elect_one()) commit<CG>(tfull + 8 * acc);
+        __syncwarp();
         if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
-      if (!ok) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
-    } else if (lane == 0 && helped) {
-      // second CTA of a pair: its copies have landed and are visible to the tensor cores
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int it = it0; it < total && ok; it += step)
-        for (int ks = 0; ks < a.kslices; ++ks) {
-          if (!mbar_wait(landed + 8 * stage, phase, abort_flag)) { ok = false; break; }
-          fence_async_proxy();
-          mbar_arrive_cluster(in_rank(full + 8 * stage, 0));
-          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
-        }
-      if (!ok) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
+      if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
     }
+  } else if (warp == 2) {
+    // ---------------- tokens ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = it0; it < total && ok; it += step) {
+      const Item o = item_at<FMT, CG>(a, first, it);
+      const int mine = columns<CG>(o.n) / CG, row0 = o.row0 + (int)rank * mine, rows = token_rows<FMT, CG>(a, o);
+      if (!S::FP4 && a.gather) {
+        const int last = o.row0 + o.n - 1;   // past the end: the last again
+        __syncwarp();
+        for (int r = lane; r < mine; r += 32) gathered[r] = __ldg(a.order + min(row0 + r, last)) / a.k;
+        __syncwarp();
+      }
+      for (int ks = 0; ks < a.kslices; ++ks) {
+        if (!warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+        const uint32_t sb = ring + stage * a.stage_bytes + A_BYTES;
+        const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
+        const int x = ks * (S::FP4 ? 128 : 64);
+        if (!S::FP4 && a.gather) {
+          if (elect_one()) {
+#pragma unroll 4
+            for (int r = 0; r < mine; r += 4)
+              tma_gather4<CG>(&tmX, bar, sb + 128 * r, x, *reinterpret_cast<const int4*>(gathered + r));
+          }
+        } else if (elect_one()) {
+          if (a.b_rows == 128 && rows == 128) tma_2d<CG>(&tmXall, bar, sb, x, row0);
+          else
+            for (int r = 0; r < rows; r += S::BOX) tma_2d<CG>(&tmX, bar, sb + r * 128, x, row0 + r);
+        }
+        if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
+  } else if (S::FP4 && warp == 3) {
+    // ---------------- scale tiles: the tokens' (CG of them), then the weights' ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = it0; it < total && ok; it += step) {
+      const Item o = item_at<FMT, CG>(a, first, it);
+      const int m = o.mb * CG + (int)rank;
+      const int wt = o.e * a.w_tiles + (a.act ? m >> 1 : m), ut = o.e * a.w_tiles + ((a.cols + 64 * m) >> 7);
+      for (int ks = 0; ks < a.kslices; ++ks) {
+        if (!warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
+        if (elect_one()) {
+          const uint32_t ss = ring + stage * a.stage_bytes + A_BYTES + a.b_rows * 128, sw = ss + CG * S::TILE_SCALES;
+          const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
+          tma_3d<CG>(&tmSX, bar, ss, 0, ks * S::GS, o.tile);
+          if (!a.act) {
+            tma_3d<CG>(&tmSW, bar, sw, 0, ks * S::GS, wt);
+          } else {   // the tile of the gate rows, and the one or two of the up rows
+            mbar_expect(sfull + 8 * stage, a.w_parts * S::TILE_SCALES);
+            tma_3d<1>(&tmSW, sfull + 8 * stage, sw, 0, ks * S::GS, wt);
+            for (int i = 1; i < a.w_parts; ++i) tma_3d<1>(&tmSW, sfull + 8 * stage, sw + i * S::TILE_SCALES, 0, ks * S::GS, ut + i - 1);
+          }
+        }
+        if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+      }
+    }
+    if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
   } else if (warp < FIRST_EPI) {
-    // ---------------- tokens (warp 2), scales (warp 3), and with 4-bit SwiGLU the weights' scales (warps 2 to 5) ----------------
-    // Those arrive on `landed` by themselves.  The fence that shows them to the tensor cores is left to warp 1: in these
-    // warps it would wait for every copy still in flight.
-    const int hw = warp - 2;
-    if (helped || hw == 0 || (S::FP4 && hw == 1)) {
+    // ---------------- 4-bit SwiGLU: a group of blocks a warp, the weights' scales in the order of the tile's rows ----------------
+    const int grp = warp - FIRST_SORT;
+    if (sorts && grp >= 0 && grp < S::GS) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int it = it0; it < total && ok; it += step) {
         const Item o = item_at<FMT, CG>(a, first, it);
         const int m = o.mb * CG + (int)rank;
-        const int mine = columns<CG>(o.n) / CG, row0 = o.row0 + (int)rank * mine, rows = token_rows<FMT, CG>(a, o);
-        const uint8_t* src = nullptr;   // scales of row lane + 32 hw of the weight tile
-        int4 idx = make_int4(0, 0, 0, 0);   // sources of token rows 4 * lane ..; past the end: the last again
-        if constexpr (S::FP4) {
-          const int row = min((lane >> 4) * a.cols + m * 64 + hw * 16 + (lane & 15), a.N - 1);
-          src = a.w_scales + ((size_t)o.e * a.w_tiles + (row >> 7)) * a.groups * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
-        } else if (a.gather && 4 * lane < mine) {
-          const int last = o.row0 + o.n - 1, r = row0 + 4 * lane;
-          idx = make_int4(__ldg(a.order + min(r, last)) / a.k, __ldg(a.order + min(r + 1, last)) / a.k,
-                          __ldg(a.order + min(r + 2, last)) / a.k, __ldg(a.order + min(r + 3, last)) / a.k);
+        uint32_t src[4];   // where the scales of row lane + 32 j of the weight tile are
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = (lane >> 4) * a.cols + m * 64 + 16 * j + (lane & 15);
+          const int part = lane < 16 ? 0 : 1 + (row >> 7) - ((a.cols + 64 * m) >> 7);
+          src[j] = part * S::TILE_SCALES + (row & 31) * 16 + ((row >> 5) & 3) * 4;
         }
         for (int ks = 0; ks < a.kslices; ++ks) {
-          if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
-          const uint32_t sb = ring + stage * a.stage_bytes + A_BYTES, ss = sb + a.b_rows * 128;
-          const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
-          const int x = ks * (S::FP4 ? 128 : 64);
-          if (hw == 0) {
-            if (!S::FP4 && a.gather) {
-              if (4 * lane < mine) tma_gather4<CG>(&tmX, bar, sb + 512 * lane, x, idx);
-            } else if (lane == 0) {
-              if (a.b_rows == 128 && rows == 128) tma_2d<CG>(&tmXall, bar, sb, x, row0);
-              else
-                for (int r = 0; r < rows; r += S::BOX) tma_2d<CG>(&tmX, bar, sb + r * 128, x, row0 + r);
-            }
-          }
-          if constexpr (S::FP4) {
-            if (hw == 1 && lane == 0) {
-              tma_3d<CG>(&tmSX, bar, ss + SCALE_A, 0, ks * S::GS, o.tile);
-              if (!a.act) tma_3d<CG>(&tmSW, bar, ss, 0, ks * S::GS, o.e * a.w_tiles + m);
-            }
-            if (helped) {
+          if (!warp_wait(sfull + 8 * stage, phase, abort_flag)) { ok = false; break; }
+          const uint32_t sw = ring + stage * a.stage_bytes + A_BYTES + a.b_rows * 128 + CG * S::TILE_SCALES + 512 * grp;
+          uint32_t r[4];
 #pragma unroll
-              for (int g = 0; g < S::GS; ++g) {
-                const int at = ks * S::GS + g;
-                if (at >= a.groups) break;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ss + g * 512 + lane * 16 + 4 * hw), "l"(src + (size_t)at * 512) : "memory");
-              }
-              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(landed + 8 * stage) : "memory");
-            }
+          for (int j = 0; j < 4; ++j) r[j] = lds32(sw + src[j]);
+          __syncwarp();   // in place: the group's 512 bytes of the first tile have been read
+          sts128(sw + 16 * lane, r);
+          fence_async_proxy();
+          __syncwarp();
+          if (lane == 0) {
+            if (CG == 2) mbar_arrive_cluster(in_rank(full + 8 * stage, 0));
+            else mbar_arrive(full + 8 * stage);
           }
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
       if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
     }
   } else if (warp >= FIRST_EPI) {
@@ -355,7 +383,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint32_t acc_phase = 0;
     for (int it = it0; it < total; it += step) {
       const Item o = item_at<FMT, CG>(a, first, it);
-      const bool ok = mbar_wait(tfull + 8 * acc, acc_phase, abort_flag);
+      const bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
       if (!named_and(1 + part, 128, ok)) {
         if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
         break;
@@ -375,7 +403,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           else mbar_arrive(bar);
         }
       };
-      // 64 columns a round; the overlap of the accumulators, columns 192 on of the first and 0 on of the second, first
+      // 64 columns a round; the overlap of the accumulators, columns 192 on of the first and 0 to 63 of the second, first
 #pragma unroll 1
       for (int round = 0; round < S::NMAX / 64; ++round) {
         const int c = 32 * part + (S::OVERLAP && acc == 0 ? (round + 3) % 4 : round) * 64;
@@ -554,8 +582,10 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   // rows of the token area: what the largest tile of P rows can need
   a.b_rows = std::min(128, (a.P + 15) / 16 * 16);
   if (CG == 2) a.b_rows = 128;
-  a.stage_bytes = A_BYTES + a.b_rows * 128 + (S::FP4 ? SCALE_A + CG * SCALE_B : 0);
-  const int fixed = 1024 + EPI_BYTES + 24 * MAX_STAGES + 32 + 8 + 4 * (a.E + 1) + 16;
+  // SwiGLU: the 64 gate rows of a tile lie in one scale tile, the 64 up rows in one or two
+  a.w_parts = !a.act ? 1 : a.cols % 64 ? 3 : 2;
+  a.stage_bytes = A_BYTES + a.b_rows * 128 + (S::FP4 ? (CG + a.w_parts) * S::TILE_SCALES : 0);
+  const int fixed = 1024 + EPI_BYTES + 24 * MAX_STAGES + 48 + 512 + 4 * (a.E + 1);
   a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 
@@ -728,7 +758,7 @@ extern "C" moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, in
   a.P = P; a.E = E; a.N = N; a.K = K; a.k = 1; a.act = act; a.cols = act ? N / 2 : N;
   a.groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
   a.quant = !out; a.out_f32 = out_dtype == MOE_F32;
-  a.w_scales = w_scales; a.gx = gx; a.gw = gw; a.gw_count = gw_count;
+  a.gx = gx; a.gw = gw; a.gw_count = gw_count;
   a.offsets = offsets; a.tiles = tiles; a.out = out; a.out_codes = out_codes; a.out_scales = out_scales; a.g_out = g_out;
   const ProductMem mem{x_codes, w_codes, x_scales, w_scales, P};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
