@@ -96,8 +96,8 @@ moe_status moe_fp4_scale(int32_t G, int64_t count, int32_t dtype, const void* x,
 /*
  * Quantise to 4 bits.  x in dtype MOE_BF16 or MOE_F32, K a multiple of 32.
  *   offsets NULL: x is a stack of G matrices [N, K]; row i of the output is row i of x.
- *   otherwise (G = 1): N = number of pairs; grouped row i is row order[i] / k of x
- *   [rows of x, K], laid out by offsets / tiles [E + 1].  Rows without a pair are skipped.
+ *   otherwise (G = 1): x [N / k, K], N = number of pairs; row t of x becomes the rows
+ *   place[t, 0 .. k - 1] (none where -1), laid out by offsets / tiles [E + 1].
  * Per block, a = max |x|:
  *   NVFP4  block scale s = e4m3(a / 6 / g), nearest even, at most 448; code = e2m1(x / (s * g)).
  *   MXFP4  scale 2^X, X = floor(log2 a) - 2 within [-127, 127], 0 for a block of zeros;
@@ -108,7 +108,7 @@ moe_status moe_fp4_scale(int32_t G, int64_t count, int32_t dtype, const void* x,
  */
 moe_status moe_quantize_fp4(int32_t G, int32_t N, int32_t K, int32_t dtype, const void* x, int32_t wdtype,
                             const float* g, int32_t g_count, int32_t E, int32_t k, const int32_t* offsets,
-                            const int32_t* tiles, const int32_t* order, uint8_t* codes, uint8_t* scales, void* stream);
+                            const int32_t* tiles, const int32_t* place, uint8_t* codes, uint8_t* scales, void* stream);
 
 /* The values e2m1(code) * (scale * g), in fp32, stored in dtype (MOE_BF16 or MOE_F32).
  * out [G, N, K], or [N, K] in expert order (offsets, tiles given; rows past offsets[E] are zero). */

@@ -4,9 +4,12 @@
 // A thread holds 16 consecutive elements of a row: one NVFP4 block, or half an MXFP4
 // block, whose largest value it shares with its neighbour.  The largest |x| is taken
 // over the bit patterns, so NaN shows up above infinity.  Rounding is the format's:
-// NVFP4 divides by the step in correctly rounded 32-bit divisions, MXFP4 multiplies by
-// a power of two, which is exact.  Scales go straight into the tile order that the
-// tensor cores take.
+// NVFP4 takes the correctly rounded quotient by the step, MXFP4 multiplies by a power of
+// two, which is exact.  Scales go straight into the tile order that the tensor cores
+// take, a word for each row's group of four blocks.
+//
+// Rows for the experts are read and converted once a token and stored once an expert
+// (converting once a pair took 95 us for 8192 tokens, 8 experts each, K 2048).
 //
 // Bound by memory: 2 bytes read and 0.53 or 0.56 written an element (bf16), the other way
 // round for the inverse.
@@ -19,53 +22,59 @@ namespace moe {
 namespace {
 
 constexpr int Q_THREADS = 256;
-constexpr int Q_ROWS = 8;       // rows of one step of a block
-
-// where an output row comes from and which padded row holds its scales; src < 0: no pair
-struct RowAt { int64_t src, pad; int g; };
+constexpr int Q_UNITS = 1024;   // 16-element units of one step of a block, about
+constexpr int Q_PLACES = 256;   // output rows of one step, at most
 
 struct QuantArgs {
-  int64_t rows;      // output rows
-  int N, K, E, k, block_groups, g_count;
+  int64_t rows;      // input rows
+  int N, K, E, k, block_groups, g_count, step_rows;
   const void* x;
   const float* g;
-  const int32_t *offsets, *tiles, *order;   // NULL: a stack of matrices
+  const int32_t *offsets, *tiles, *place;   // NULL: a stack of matrices
   uint8_t *codes, *scales;
 };
 
+// an output row, the padded row of its scales, its matrix's scale; row < 0: none
+struct RowAt { int64_t row, pad; float g; };
+
 __device__ __forceinline__ RowAt row_at(const QuantArgs& a, int64_t r) {
-  RowAt o;
+  RowAt o{r, 0, 1.0f};
   if (a.offsets) {
-    o.g = 0;
-    const int i = (int)r;
-    if (i >= __ldg(a.offsets + a.E)) { o.src = -1; o.pad = 0; return o; }
-    const int e = expert_of(a.offsets, a.E, i);
-    o.src = a.order ? __ldg(a.order + i) / a.k : i;
+    const int i = (int)r, e = expert_of(a.offsets, a.E, i);
     o.pad = (int64_t)__ldg(a.tiles + e) * 128 + (i - __ldg(a.offsets + e));
-    return o;
+    if (a.g) o.g = __ldg(a.g);
+  } else {
+    const int64_t m = r / a.N;
+    o.pad = m * (ceil_div64(a.N, 128) * 128) + (r - m * a.N);
+    if (a.g) o.g = __ldg(a.g + (a.g_count > 1 ? m : 0));
   }
-  const int64_t m = r / a.N;
-  o.src = r;
-  o.pad = m * (ceil_div64(a.N, 128) * 128) + (r - m * a.N);
-  o.g = a.g_count > 1 ? (int)m : 0;
   return o;
 }
 
+// 16 elements of a row; a row of K starts on 16 elements' bytes from its 16-byte aligned matrix
 template <typename X>
 __device__ __forceinline__ void load16(const X* p, float (&v)[16]) {
-  if constexpr (sizeof(X) == 4) {
+  constexpr int W = sizeof(X) == 4 ? 4 : 2;   // 16-byte words
+  uint4 q[W];
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {   // 32 bytes an instruction
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
-      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
-    }
+    for (int i = 0; i < W / 2; ++i)
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(q[2 * i].x), "=r"(q[2 * i].y), "=r"(q[2 * i].z), "=r"(q[2 * i].w), "=r"(q[2 * i + 1].x), "=r"(q[2 * i + 1].y),
+                     "=r"(q[2 * i + 1].z), "=r"(q[2 * i + 1].w)
+                   : "l"(reinterpret_cast<const uint4*>(p) + 2 * i));
   } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
-      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+    for (int i = 0; i < W; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+  for (int i = 0; i < W; ++i) {
+    const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(X) == 4) {
+        v[4 * i + j] = __uint_as_float(u[j]);
+      } else {
         v[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
         v[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
       }
@@ -75,69 +84,93 @@ __device__ __forceinline__ void load16(const X* p, float (&v)[16]) {
 
 template <typename X, bool NV>
 __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(QuantArgs a) {
-  __shared__ RowAt at[Q_ROWS];
-  const int per_row = a.K / 16;
-  for (int64_t r0 = (int64_t)blockIdx.x * Q_ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * Q_ROWS) {
-    const int n = (int)min((int64_t)Q_ROWS, a.rows - r0);
-    __syncthreads();
-    if (threadIdx.x < n) at[threadIdx.x] = row_at(a, r0 + threadIdx.x);
-    __syncthreads();
-    // units past the last one do the last again, so that a warp's shuffles are whole
-    const int units = n * per_row, padded = (units + 31) & ~31;
-    for (int u = threadIdx.x; u < padded; u += Q_THREADS) {
-      const int uu = min(u, units - 1);
-      const int r = uu / per_row, c = uu - r * per_row;
-      const RowAt o = at[r];
-      float v[16];
-      load16(static_cast<const X*>(a.x) + (size_t)max(o.src, (int64_t)0) * a.K + c * 16, v);
-      uint32_t m = 0u;
+  __shared__ RowAt at[Q_PLACES];
+  pdl_wait();
+  pdl_trigger();
+  constexpr int G = NV ? 4 : 8;                       // units of a group of four blocks
+  const int units_row = a.K / 16, per_row = (units_row + G - 1) / G * G;
+  const int kk = min(a.k, Q_PLACES / a.step_rows);    // copies of a row handled at a time
+  for (int64_t r0 = (int64_t)blockIdx.x * a.step_rows; r0 < a.rows; r0 += (int64_t)gridDim.x * a.step_rows) {
+    const int n = (int)min((int64_t)a.step_rows, a.rows - r0);
+    for (int j0 = 0; j0 < a.k; j0 += kk) {
+      const int nj = min(kk, a.k - j0);
+      __syncthreads();
+      for (int i = threadIdx.x; i < n * nj; i += Q_THREADS) {
+        const int64_t r = r0 + i / nj;
+        const int64_t row = a.place ? (int64_t)__ldg(a.place + r * a.k + j0 + i % nj) : r;
+        at[i] = row < 0 ? RowAt{-1, 0, 1.0f} : row_at(a, row);
+      }
+      __syncthreads();
+      // whole groups a row, so that four (eight) neighbouring lanes make a group's word of scales; past the row's end: no block
+      for (int u0 = 0; u0 < n * per_row; u0 += Q_THREADS) {
+        const int u = u0 + threadIdx.x;
+        const bool some = u < n * per_row;
+        const int r = some ? u / per_row : 0, c = some ? u - r * per_row : 0;
+        const bool live = some && c < units_row;
+        float v[16];
+        uint32_t m = 0u, code = 0u;
+        uint2 q = make_uint2(0u, 0u);
+        if (live) {
+          load16(static_cast<const X*>(a.x) + (size_t)(r0 + r) * a.K + c * 16, v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-      if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));   // per_row is even: the pair is one block
-      float step;
-      const float g = NV && a.g ? __ldg(a.g + o.g) : 1.0f;
-      const uint32_t code = block_scale<NV>(m, g, step);
-      const uint2 q = encode16<NV>(v, m, code, step);
-      if (u >= units || o.src < 0) continue;
-      *reinterpret_cast<uint2*>(a.codes + (size_t)(r0 + r) * (a.K / 2) + c * 8) = q;
-      const int b = NV ? c : c >> 1;
-      if (NV || !(c & 1)) {
-        uint8_t* s = a.scales + scale_at((size_t)o.pad, b, a.block_groups);
-        *s = (uint8_t)code;
-        // the row's last block also pads its group
-        if (b == (NV ? per_row : per_row / 2) - 1)
-          for (int i = 1; i < 4 - (b & 3); ++i) s[i] = 0;
+          for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        }
+        if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        if (live) {
+          float step;
+          code = block_scale<NV>(m, a.place ? (a.g ? __ldg(a.g) : 1.0f) : at[r].g, step);
+          q = encode16<NV>(v, m, code, step);
+        }
+        if (NV) {
+          code |= __shfl_xor_sync(0xffffffffu, code, 1) << 8;      // lane 0 of 4: bytes of lanes 0, 1
+          code |= __shfl_xor_sync(0xffffffffu, code, 2) << 16;
+        } else {
+          code |= __shfl_xor_sync(0xffffffffu, code, 2) << 8;
+          code |= __shfl_xor_sync(0xffffffffu, code, 4) << 16;
+        }
+        if (!some) continue;
+        for (int j = 0; j < nj; ++j) {
+          const RowAt o = at[r * nj + j];
+          if (o.row < 0) continue;
+          if (live) *reinterpret_cast<uint2*>(a.codes + (size_t)o.row * (a.K / 2) + c * 8) = q;
+          if (c % G == 0) *reinterpret_cast<uint32_t*>(a.scales + scale_at((size_t)o.pad, c / (G / 4), a.block_groups)) = code;
+        }
       }
     }
   }
 }
 
+// 8 values a thread: 16 bytes of bf16
 template <typename O, bool NV>
 __global__ void __launch_bounds__(Q_THREADS) dequantize_kernel(QuantArgs a, O* __restrict__ out) {
-  __shared__ RowAt at[Q_ROWS];
-  const int per_row = a.K / 16;
-  for (int64_t r0 = (int64_t)blockIdx.x * Q_ROWS; r0 < a.rows; r0 += (int64_t)gridDim.x * Q_ROWS) {
-    const int n = (int)min((int64_t)Q_ROWS, a.rows - r0);
+  __shared__ RowAt at[Q_PLACES];
+  pdl_wait();
+  pdl_trigger();
+  const int per_row = a.K / 8;
+  for (int64_t r0 = (int64_t)blockIdx.x * a.step_rows; r0 < a.rows; r0 += (int64_t)gridDim.x * a.step_rows) {
+    const int n = (int)min((int64_t)a.step_rows, a.rows - r0);
     __syncthreads();
-    if (threadIdx.x < n) at[threadIdx.x] = row_at(a, r0 + threadIdx.x);
+    for (int i = threadIdx.x; i < n; i += Q_THREADS) {
+      at[i] = a.offsets && r0 + i >= __ldg(a.offsets + a.E) ? RowAt{-1, 0, 1.0f} : row_at(a, r0 + i);
+    }
     __syncthreads();
     for (int u = threadIdx.x; u < n * per_row; u += Q_THREADS) {
       const int r = u / per_row, c = u - r * per_row;
       const RowAt o = at[r];
-      O res[16];
-      if (o.src < 0) {
+      O res[8];
+      if (o.row < 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) res[i] = (O)0.0f;
+        for (int i = 0; i < 8; ++i) res[i] = (O)0.0f;
       } else {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(a.codes + (size_t)(r0 + r) * (a.K / 2) + c * 8));
-        const uint32_t sc = a.scales[scale_at((size_t)o.pad, NV ? c : c >> 1, a.block_groups)];
-        const float step = (NV ? e4m3_value(sc) : e8m0_value(sc)) * (a.g ? __ldg(a.g + o.g) : 1.0f);
+        const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (size_t)o.row * (a.K / 2)) + c);
+        const uint32_t sc = __ldg(a.scales + scale_at((size_t)o.pad, NV ? c >> 1 : c >> 2, a.block_groups));
+        const float step = (NV ? e4m3_value(sc) : e8m0_value(sc)) * o.g;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) res[i] = (O)(e2m1_value(((i < 8 ? q.x : q.y) >> (4 * (i & 7))) & 15u) * step);
+        for (int i = 0; i < 8; ++i) res[i] = (O)(e2m1_value((q >> (4 * i)) & 15u) * step);
       }
-      uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(r0 + r) * a.K + c * 16);
+      uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(r0 + r) * a.K + c * 8);
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(O); ++i) dst[i] = reinterpret_cast<const uint4*>(res)[i];
+      for (int i = 0; i < (int)sizeof(O) / 2; ++i) dst[i] = reinterpret_cast<const uint4*>(res)[i];
     }
   }
 }
@@ -185,7 +218,15 @@ moe_status check_fp4(int32_t G, int32_t N, int32_t K, int32_t dtype, int32_t wdt
   return MOE_OK;
 }
 
-int row_grid(int64_t rows) { return (int)std::min<int64_t>((rows + Q_ROWS - 1) / Q_ROWS, (int64_t)operator_sms() * 8); }
+// rows of a step of a block, and the blocks
+void set_steps(QuantArgs& a, int unit) {
+  const int64_t share = a.rows / ((int64_t)operator_sms() * 4) + 1;   // small calls: a few rows a block, on every SM
+  const int most = std::min({Q_PLACES / std::min(a.k, Q_PLACES), Q_UNITS * 16 / unit / std::max(1, a.K / unit), 64});
+  a.step_rows = (int)std::max<int64_t>(1, std::min<int64_t>(most, share));
+}
+int steps_grid(const QuantArgs& a) {
+  return (int)std::min<int64_t>((a.rows + a.step_rows - 1) / a.step_rows, (int64_t)operator_sms() * 8);
+}
 
 }  // namespace
 
@@ -217,31 +258,31 @@ extern "C" moe_status moe_fp4_scale(int32_t G, int64_t count, int32_t dtype, con
 
 extern "C" moe_status moe_quantize_fp4(int32_t G, int32_t N, int32_t K, int32_t dtype, const void* x, int32_t wdtype,
                                        const float* g, int32_t g_count, int32_t E, int32_t k, const int32_t* offsets,
-                                       const int32_t* tiles, const int32_t* order, uint8_t* codes, uint8_t* scales,
+                                       const int32_t* tiles, const int32_t* place, uint8_t* codes, uint8_t* scales,
                                        void* stream) {
   moe_status st = check_fp4(G, N, K, dtype, wdtype, g, g_count);
   if (st != MOE_OK) return st;
   if (g && wdtype == MOE_MXFP4) return fail(MOE_EINVAL, "MXFP4 has no matrix scale");
-  if (offsets && (G != 1 || !tiles || (N > 0 && !order) || E < 1 || k < 1))
-    return fail(MOE_EINVAL, "grouped rows need G = 1, tiles, order, E >= 1 and k >= 1");
+  if (offsets && (G != 1 || !tiles || (N > 0 && !place) || E < 1 || k < 1 || N % k))
+    return fail(MOE_EINVAL, "grouped rows need G = 1, tiles, place, E >= 1 and N pairs of k a row");
   if (G == 0 || N == 0) return MOE_OK;
   if (!x || !codes || !scales) return fail(MOE_EINVAL, "x, codes and scales must not be NULL");
   if (!aligned_to(x, 16) || !aligned_to(codes, 16) || !aligned_to(scales, 16) || !aligned_to(g, 4))
     return fail(MOE_EINVAL, "x, codes and scales must be 16-byte aligned, g 4-byte aligned");
-  if (!aligned_to(offsets, 4) || !aligned_to(tiles, 4) || !aligned_to(order, 4))
-    return fail(MOE_EINVAL, "offsets, tiles and order must be 4-byte aligned");
+  if (!aligned_to(offsets, 4) || !aligned_to(tiles, 4) || !aligned_to(place, 4))
+    return fail(MOE_EINVAL, "offsets, tiles and place must be 4-byte aligned");
   QuantArgs a{};
-  a.rows = (int64_t)G * N; a.N = N; a.K = K; a.E = E; a.k = k; a.g_count = g_count; a.x = x; a.g = g;
+  a.k = offsets ? k : 1;
+  a.rows = offsets ? N / k : (int64_t)G * N; a.N = N; a.K = K; a.E = E; a.g_count = g_count; a.x = x; a.g = g;
   a.block_groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
-  a.offsets = offsets; a.tiles = tiles; a.order = order; a.codes = codes; a.scales = scales;
+  a.offsets = offsets; a.tiles = tiles; a.place = offsets ? place : nullptr; a.codes = codes; a.scales = scales;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid = row_grid(a.rows);
+  set_steps(a, 16);
+  const dim3 grid(steps_grid(a)), block(Q_THREADS);
   const bool f32 = dtype == MOE_F32, nv = wdtype == MOE_NVFP4;
-  if (f32 && nv) quantize_kernel<float, true><<<grid, Q_THREADS, 0, s>>>(a);
-  else if (f32) quantize_kernel<float, false><<<grid, Q_THREADS, 0, s>>>(a);
-  else if (nv) quantize_kernel<__nv_bfloat16, true><<<grid, Q_THREADS, 0, s>>>(a);
-  else quantize_kernel<__nv_bfloat16, false><<<grid, Q_THREADS, 0, s>>>(a);
-  CK(cudaGetLastError());
+  CK(f32 ? (nv ? launch_pdl(quantize_kernel<float, true>, grid, block, 0, s, a) : launch_pdl(quantize_kernel<float, false>, grid, block, 0, s, a))
+         : (nv ? launch_pdl(quantize_kernel<__nv_bfloat16, true>, grid, block, 0, s, a)
+               : launch_pdl(quantize_kernel<__nv_bfloat16, false>, grid, block, 0, s, a)));
   return MOE_OK;
 }
 
@@ -263,12 +304,13 @@ extern "C" moe_status moe_dequantize_fp4(int32_t G, int32_t N, int32_t K, int32_
   a.offsets = offsets; a.tiles = tiles;
   a.codes = const_cast<uint8_t*>(codes); a.scales = const_cast<uint8_t*>(scales);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int grid = row_grid(a.rows);
+  set_steps(a, 8);
+  const dim3 grid(steps_grid(a)), block(Q_THREADS);
   const bool f32 = dtype == MOE_F32, nv = wdtype == MOE_NVFP4;
-  if (f32 && nv) dequantize_kernel<float, true><<<grid, Q_THREADS, 0, s>>>(a, static_cast<float*>(out));
-  else if (f32) dequantize_kernel<float, false><<<grid, Q_THREADS, 0, s>>>(a, static_cast<float*>(out));
-  else if (nv) dequantize_kernel<__nv_bfloat16, true><<<grid, Q_THREADS, 0, s>>>(a, static_cast<__nv_bfloat16*>(out));
-  else dequantize_kernel<__nv_bfloat16, false><<<grid, Q_THREADS, 0, s>>>(a, static_cast<__nv_bfloat16*>(out));
-  CK(cudaGetLastError());
+  float* of = static_cast<float*>(out);
+  __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(out);
+  CK(f32 ? (nv ? launch_pdl(dequantize_kernel<float, true>, grid, block, 0, s, a, of) : launch_pdl(dequantize_kernel<float, false>, grid, block, 0, s, a, of))
+         : (nv ? launch_pdl(dequantize_kernel<__nv_bfloat16, true>, grid, block, 0, s, a, ob)
+               : launch_pdl(dequantize_kernel<__nv_bfloat16, false>, grid, block, 0, s, a, ob)));
   return MOE_OK;
 }

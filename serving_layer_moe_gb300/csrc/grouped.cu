@@ -186,6 +186,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), TMEM_COLS);
+  pdl_wait();
+  pdl_trigger();
   if (warp == 2) {   // token tiles before each expert
     int run = 0;
     for (int b = 0; b < a.E; b += 32) {
@@ -633,12 +635,14 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
+  cfg.numAttrs = CG;
   // every unit of a persistent grid has to be resident: as many pairs as the device's clusters allow
   int resident = operator_sms();
   if (CG == 2) {
@@ -673,6 +677,8 @@ moe_status launch_product(const ProductArgs& a, const ProductMem& mem, cudaStrea
 // 950 (TMA gather) or 700 us (cp.async) by index.
 __global__ void __launch_bounds__(256)
 gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ order, int P, int row16, int k, uint4* __restrict__ xs) {
+  pdl_wait();
+  pdl_trigger();
   const int64_t units = (int64_t)P * row16;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
     const int i = (int)(u / row16), c = (int)(u - (int64_t)i * row16);
@@ -722,8 +728,8 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
       return fail(MOE_EINVAL, "workspace must hold %lld bytes, 16-byte aligned, holds %lld", (long long)need, (long long)workspace_bytes);
     const int64_t units = (int64_t)P * (K / 8);
     const int grid = (int)std::min<int64_t>((units + 255) / 256, (int64_t)operator_sms() * 16);
-    gather_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<const uint4*>(x), order, P, K / 8, k, static_cast<uint4*>(workspace));
-    CK(cudaGetLastError());
+    CK(launch_pdl(gather_kernel, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), order, P, K / 8, k,
+                  static_cast<uint4*>(workspace)));
     a.gather = 0;
     x = workspace;
     x_rows = P;

@@ -7,12 +7,12 @@
 // a minimum over the indices that hold it, so equal scores go to the lower index
 // and the result is the same on every run.
 //
-// Grouping is a stable counting sort of the T*k pairs by expert in at most two
-// launches: blocks of tokens count their pairs per expert (the router's blocks count
-// what they have just picked), then each block adds up the counts of the blocks
-// before it and ranks its own pairs, 32 at a time by match.  Ranks follow the pair
-// index, so no atomic decides an order.  Calls whose pairs fit one block do all of
-// it, router included, in one launch.
+// Grouping is a stable counting sort of the T*k pairs by expert in three launches: the
+// router's blocks count the pairs they have just picked per expert, one warp per expert
+// turns the counts of all blocks into starts, and blocks rank their own pairs, 32 at a
+// time by match.  Ranks follow the pair index, so no atomic decides an order.  Calls of at
+// most 256 pairs do all of it, router included, in one block, where a pair counts the
+// pairs before it in expert order.
 //
 // Bounds: a prompt chunk of 8192 tokens and 256 experts reads 8.4 MB of logits; one
 // decoded token is one launch's latency.
@@ -26,9 +26,10 @@ namespace {
 
 constexpr int ROUTE_THREADS = 256;          // 8 warps, a token each at a time
 constexpr int ROUTE_WARPS = ROUTE_THREADS / 32;
-constexpr int PLACE_THREADS = 512;          // 256 above 1024 experts: a count per warp and expert in shared memory
-constexpr int kMaxBlocks = 304;             // two blocks on each of 152 SMs
-constexpr int kOneBlockTokens = 32;         // up to here one block routes and groups
+constexpr int PLACE_THREADS = 256;          // 8 warps rank a segment of pairs each
+constexpr int PLACE_WARPS = PLACE_THREADS / 32;
+constexpr int kMaxBlocks = 1024;            // counting blocks: what one warp adds up per expert
+constexpr int kSmallPairs = 256;            // up to here one block routes and groups
 
 struct RouteArgs {
   int T, E, k, scoring, n_group, topk_group, renorm, tokens_per_block;
@@ -38,7 +39,7 @@ struct RouteArgs {
   int32_t* ids;
   float* w;
   int32_t *offsets, *tiles, *order, *place;   // NULL: no grouping
-  int32_t* counts;                            // [blocks, E + 1]
+  int32_t* counts;                            // [E + 1, blocks] pairs of each block of each expert; row E: dropped ones
 };
 
 // larger float <=> larger integer; -0 and +0 are one value; NaN is below -inf
@@ -184,57 +185,14 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int logits_bf16,
   }
 }
 
-// Rank the pairs of one block of tokens: pairs p0 .. p1 - 1, experts `ids`.  base[e]
-// (shared, E + 1) is the row of the block's first pair of expert e; bin E holds the pairs whose id is
-// out of range.  Warps take consecutive segments, so ranks follow the pair index.
-__device__ __forceinline__ void count_segments(const int32_t* __restrict__ ids, int p0, int p1, int E, int32_t* cnt,
-                                               int warps) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int seg = ((p1 - p0 + warps - 1) / warps + 31) & ~31;
-  int32_t* mine = cnt + warp * (E + 1);
-  const int s0 = p0 + warp * seg, s1 = min(p1, s0 + seg);
-  for (int p = s0; p < s1; p += 32) {
-    const int q = p + lane;
-    const bool live = q < s1;
-    int e = live ? ids[q] : -2;
-    if (live && (unsigned)e >= (unsigned)E) e = E;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (live && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-  }
-}
-
-__device__ __forceinline__ void place_segments(const int32_t* __restrict__ ids, int p0, int p1, int E, int32_t* cnt,
-                                               int warps, int32_t* __restrict__ order, int32_t* __restrict__ place) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int seg = ((p1 - p0 + warps - 1) / warps + 31) & ~31;
-  int32_t* mine = cnt + warp * (E + 1);
-  const int s0 = p0 + warp * seg, s1 = min(p1, s0 + seg);
-  for (int p = s0; p < s1; p += 32) {
-    const int q = p + lane;
-    const bool live = q < s1;
-    int e = live ? ids[q] : -2;
-    if (live && (unsigned)e >= (unsigned)E) e = E;
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (live) {
-      const int row = mine[e] + __popc(same & ((1u << lane) - 1u));
-      order[row] = e < E ? q : -1;
-      place[q] = e < E ? row : -1;
-    }
-    __syncwarp();
-    if (live && lane == __ffs(same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-  }
-}
-
-// exclusive prefix over E + 1 bins of shared `total` into `first` and, for tiles, of ceil(total / 128); one warp
-__device__ __forceinline__ void scan_bins(const int32_t* total, int E, int32_t* first, int32_t* offsets, int32_t* tiles,
-                                          bool write) {
+// exclusive prefixes over E + 1 bins: of the counts into `first` (and `offsets`), of ceil(count / 128) into `tiles`; one warp.
+// Bin E, the dropped pairs, comes last, so first[E] is the number of rows.
+__device__ __forceinline__ void scan_bins(const int32_t* count, int E, int32_t* first, int32_t* offsets, int32_t* tiles) {
   const int lane = threadIdx.x & 31;
   int run = 0, trun = 0;
   for (int b = 0; b <= E; b += 32) {
     const int e = b + lane;
-    const int c = e <= E ? total[e] : 0;
+    const int c = e <= E ? count[e] : 0;
     const int tl = (c + 127) >> 7;
     int x = c, y = tl;
     for (int o = 1; o < 32; o <<= 1) {
@@ -243,89 +201,66 @@ __device__ __forceinline__ void scan_bins(const int32_t* total, int E, int32_t* 
     }
     if (e <= E) {
       first[e] = run + x - c;
-      if (write) { offsets[e] = run + x - c; tiles[e] = trun + y - tl; }
+      if (offsets) { offsets[e] = run + x - c; tiles[e] = trun + y - tl; }
     }
     run += __shfl_sync(0xffffffffu, x, 31);
     trun += __shfl_sync(0xffffffffu, y, 31);
   }
 }
 
-// Ranks the pairs of block `b` of `blocks`; smem: total[E+1], first[E+1], cnt[warps][E+1].
-__device__ __forceinline__ void place_block(const int32_t* __restrict__ ids, int p0, int p1, int E, int b, int blocks,
-                                            const int32_t* __restrict__ counts, int32_t* offsets, int32_t* tiles,
+// Groups at most kSmallPairs pairs in one block.  smem: ids [kSmallPairs], count and first [E + 1].
+__device__ __forceinline__ void group_small(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* tiles,
                                             int32_t* order, int32_t* place, int32_t* smem) {
-  const int nt = blockDim.x, tid = threadIdx.x, warps = nt >> 5, bins = E + 1;
-  int32_t* total = smem;
-  int32_t* first = total + bins;
-  int32_t* before = first + bins;
-  int32_t* cnt = before + bins;
-  for (int i = tid; i < (3 + warps) * bins; i += nt) smem[i] = 0;
+  int32_t* id = smem;
+  int32_t* count = id + kSmallPairs;
+  int32_t* first = count + E + 1;
+  for (int e = threadIdx.x; e <= E; e += blockDim.x) count[e] = 0;
   __syncthreads();
-  count_segments(ids, p0, p1, E, cnt, warps);
-  if (blocks > 1) {
-    // the other blocks' counts: `parts` threads to a bin
-    const int parts = max(1, nt / bins);
-    for (int i = tid; i < parts * bins; i += nt) {
-      const int e = i % bins, part = i / bins;
-      int all = 0, bef = 0;
-      for (int r = part; r < blocks; r += parts) {
-        const int c = __ldcg(counts + (size_t)r * bins + e);
-        all += c;
-        if (r < b) bef += c;
-      }
-      atomicAdd(&total[e], all);
-      if (bef) atomicAdd(&before[e], bef);
-    }
-    __syncthreads();
-  } else {
-    __syncthreads();
-    for (int e = tid; e < bins; e += nt) {
-      int c = 0;
-      for (int w = 0; w < warps; ++w) c += cnt[w * bins + e];
-      total[e] = c;
-    }
-    __syncthreads();
-  }
-  if (tid < 32) scan_bins(total, E, first, offsets, tiles, b == 0);
-  __syncthreads();
-  for (int e = tid; e < bins; e += nt) {
-    int run = first[e] + before[e];
-    for (int w = 0; w < warps; ++w) {
-      const int c = cnt[w * bins + e];
-      cnt[w * bins + e] = run;
-      run += c;
-    }
+  const int p = threadIdx.x;      // blockDim.x >= kSmallPairs
+  int mine = -1;
+  if (p < P) {
+    const int e = ids[p];
+    mine = (unsigned)e < (unsigned)E ? e : E;
+    id[p] = mine;
+    atomicAdd(&count[mine], 1);
   }
   __syncthreads();
-  place_segments(ids, p0, p1, E, cnt, warps, order, place);
+  if (p < P) {
+    int row = 0;
+    for (int i = 0; i < P; ++i) row += id[i] < mine || (id[i] == mine && i < p);
+    order[row] = mine < E ? p : -1;
+    place[p] = mine < E ? row : -1;
+  }
+  if (threadIdx.x < 32) scan_bins(count, E, first, offsets, tiles);
 }
-
-int place_threads(int E) { return E <= 1024 ? PLACE_THREADS : 256; }
-size_t place_smem(int E, int threads) { return (size_t)(3 + threads / 32) * (E + 1) * 4; }
 
 template <int NPL>
 __global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(RouteArgs a, int logits_bf16) {
   extern __shared__ int32_t smem[];
+  pdl_wait();
+  pdl_trigger();
   const int warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * a.tokens_per_block, t1 = min(a.T, t0 + a.tokens_per_block);
   float* scratch = reinterpret_cast<float*>(smem) + (size_t)warp * (a.E + a.E / 32 + 1);
   for (int t = t0 + warp; t < t1; t += ROUTE_WARPS) route_token<NPL>(a, logits_bf16, t, scratch);
   if (!a.offsets) return;
   __syncthreads();   // this block's ids are written, the scratch is free
-  if (gridDim.x == 1) {
-    place_block(a.ids, 0, a.T * a.k, a.E, 0, 1, nullptr, a.offsets, a.tiles, a.order, a.place, smem);
+  if (!a.counts) {
+    group_small(a.ids, a.T * a.k, a.E, a.offsets, a.tiles, a.order, a.place, smem);
     return;
   }
   for (int i = threadIdx.x; i <= a.E; i += ROUTE_THREADS) smem[i] = 0;
   __syncthreads();
   for (int p = t0 * a.k + threadIdx.x; p < t1 * a.k; p += ROUTE_THREADS) atomicAdd(&smem[a.ids[p]], 1);
   __syncthreads();
-  for (int i = threadIdx.x; i <= a.E; i += ROUTE_THREADS) a.counts[(size_t)blockIdx.x * (a.E + 1) + i] = smem[i];
+  for (int i = threadIdx.x; i <= a.E; i += ROUTE_THREADS) a.counts[(size_t)i * gridDim.x + blockIdx.x] = smem[i];
 }
 
 __global__ void __launch_bounds__(ROUTE_THREADS)
 count_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int32_t* __restrict__ counts) {
   extern __shared__ int32_t smem[];
+  pdl_wait();
+  pdl_trigger();
   for (int i = threadIdx.x; i <= E; i += ROUTE_THREADS) smem[i] = 0;
   __syncthreads();
   const int p0 = blockIdx.x * per_block, p1 = min(P, p0 + per_block);
@@ -334,15 +269,96 @@ count_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int32
     atomicAdd(&smem[(unsigned)e < (unsigned)E ? e : E], 1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i <= E; i += ROUTE_THREADS) counts[(size_t)blockIdx.x * (E + 1) + i] = smem[i];
+  for (int i = threadIdx.x; i <= E; i += ROUTE_THREADS) counts[(size_t)i * gridDim.x + blockIdx.x] = smem[i];
 }
 
-__global__ void __launch_bounds__(PLACE_THREADS)
-place_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, const int32_t* __restrict__ counts,
-             int32_t* offsets, int32_t* tiles, int32_t* order, int32_t* place) {
+__global__ void __launch_bounds__(ROUTE_THREADS)
+group_small_kernel(const int32_t* __restrict__ ids, int P, int E, int32_t* offsets, int32_t* tiles, int32_t* order, int32_t* place) {
   extern __shared__ int32_t smem[];
-  const int p0 = blockIdx.x * per_block, p1 = min(P, p0 + per_block);
-  place_block(ids, p0, p1, E, blockIdx.x, gridDim.x, counts, offsets, tiles, order, place, smem);
+  pdl_wait();
+  pdl_trigger();
+  group_small(ids, P, E, offsets, tiles, order, place, smem);
+}
+
+// counts [E + 1, blocks] -> what comes before each block, in place, and each expert's total; a warp per expert
+__global__ void __launch_bounds__(256) starts_kernel(int32_t* __restrict__ counts, int E, int blocks, int32_t* __restrict__ total) {
+  pdl_wait();
+  pdl_trigger();
+  const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (e > E) return;
+  int32_t* row = counts + (size_t)e * blocks;
+  constexpr int MOST = kMaxBlocks / 32;
+  int c[MOST];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) c[i] = i * 32 + lane < blocks ? row[i * 32 + lane] : 0;
+  int run = 0;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    if (i * 32 >= blocks) break;
+    int x = c[i];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += u;
+    }
+    if (i * 32 + lane < blocks) row[i * 32 + lane] = run + x - c[i];
+    run += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) total[e] = run;
+}
+
+// Ranks the pairs of `per` counting blocks; warps take consecutive segments.  smem: start [E + 1], total [E + 1], a count per
+// warp and bin.
+__global__ void __launch_bounds__(PLACE_THREADS)
+place_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int per, int blocks, const int32_t* __restrict__ starts,
+             const int32_t* __restrict__ totals, int32_t* offsets, int32_t* tiles, int32_t* __restrict__ order, int32_t* __restrict__ place) {
+  extern __shared__ int32_t smem[];
+  const int bins = E + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* start = smem;
+  int32_t* total = start + bins;
+  int32_t* cnt = total + bins;
+  for (int i = threadIdx.x; i < PLACE_WARPS * bins; i += PLACE_THREADS) cnt[i] = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int p0 = blockIdx.x * per * per_block, p1 = min(P, p0 + per * per_block);
+  const int seg = ((p1 - p0 + PLACE_WARPS - 1) / PLACE_WARPS + 31) & ~31;
+  const int s0 = p0 + warp * seg, s1 = min(p1, s0 + seg);
+  int32_t* mine = cnt + warp * bins;
+  for (int e = threadIdx.x; e < bins; e += PLACE_THREADS) total[e] = totals[e];
+  __syncthreads();
+  if (warp == 0) scan_bins(total, E, start, blockIdx.x == 0 ? offsets : nullptr, tiles);
+  for (int p = s0; p < s1; p += 32) {
+    const int q = p + lane;
+    int e = q < s1 ? __ldg(ids + q) : -2;
+    if (q < s1 && (unsigned)e >= (unsigned)E) e = E;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (q < s1 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < bins; e += PLACE_THREADS) {
+    int run = start[e] + starts[(size_t)e * blocks + blockIdx.x * per];
+#pragma unroll
+    for (int w = 0; w < PLACE_WARPS; ++w) {
+      const int c = cnt[w * bins + e];
+      cnt[w * bins + e] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  for (int p = s0; p < s1; p += 32) {
+    const int q = p + lane;
+    int e = q < s1 ? __ldg(ids + q) : -2;
+    if (q < s1 && (unsigned)e >= (unsigned)E) e = E;
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (q < s1) {
+      const int row = mine[e] + __popc(same & ((1u << lane) - 1u));
+      order[row] = e < E ? q : -1;
+      place[q] = e < E ? row : -1;
+    }
+    __syncwarp();
+    if (q < s1 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+  }
 }
 
 // out[t, n] = sum_j w[t, j] y[place[t, j], n]: V columns a thread
@@ -350,6 +366,8 @@ template <typename Y, typename O, int V>
 __global__ void __launch_bounds__(256)
 combine_kernel(int T, int k, int N, const Y* __restrict__ y, const int32_t* __restrict__ place,
                const float* __restrict__ w, O* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
   const int cols = N / V;
   const int64_t units = (int64_t)T * cols;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
@@ -395,18 +413,13 @@ cudaError_t launch_combine_rows(int T, int k, int N, const void* y, const int32_
   const bool wide = N % 8 == 0;   // every row of y and out starts on 16 bytes
   const int64_t units = (int64_t)T * (wide ? N / 8 : N);
   const int grid = (int)std::min<int64_t>((units + 255) / 256, (int64_t)operator_sms() * 32);
-  if (wide)
-    combine_kernel<Y, O, 8><<<grid, 256, 0, s>>>(T, k, N, (const Y*)y, place, w, (O*)out);
-  else
-    combine_kernel<Y, O, 1><<<grid, 256, 0, s>>>(T, k, N, (const Y*)y, place, w, (O*)out);
-  return cudaGetLastError();
+  return wide ? launch_pdl(combine_kernel<Y, O, 8>, dim3(grid), dim3(256), 0, s, T, k, N, (const Y*)y, place, w, (O*)out)
+              : launch_pdl(combine_kernel<Y, O, 1>, dim3(grid), dim3(256), 0, s, T, k, N, (const Y*)y, place, w, (O*)out);
 }
 
-// tokens of one block when T tokens are spread over at most kMaxBlocks
-int tokens_per_block(int T) {
-  const int want = (T + kMaxBlocks - 1) / kMaxBlocks;
-  return std::max(ROUTE_WARPS, (want + ROUTE_WARPS - 1) / ROUTE_WARPS * ROUTE_WARPS);
-}
+// tokens of one counting block when T tokens are spread over at most kMaxBlocks
+int tokens_per_block(int T) { return ROUTE_WARPS * std::max(1, (T + ROUTE_WARPS * kMaxBlocks - 1) / (ROUTE_WARPS * kMaxBlocks)); }
+bool small_group(int64_t T, int64_t k) { return T * k <= kSmallPairs; }
 
 moe_status check_group_args(int32_t T, int32_t E, int32_t k, const void* offsets, const void* tiles, const void* order,
                             const void* place, const void* ws, int64_t ws_bytes) {
@@ -431,22 +444,34 @@ cudaError_t allow_smem(const void* fn, size_t bytes) {
   return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+size_t small_smem(int E) { return (size_t)(kSmallPairs + 2 * (E + 1)) * 4; }
+
 template <int NPL>
 moe_status run_route(const RouteArgs& a, int bf16, int blocks, cudaStream_t s) {
   size_t smem = a.n_group > 1 ? (size_t)ROUTE_WARPS * (a.E + a.E / 32 + 1) * 4 : 0;
-  if (a.offsets) smem = std::max(smem, blocks == 1 ? place_smem(a.E, ROUTE_THREADS) : (size_t)(a.E + 1) * 4);
+  if (a.offsets) smem = std::max(smem, small_smem(a.E));
   CK(allow_smem((const void*)route_kernel<NPL>, smem));
-  route_kernel<NPL><<<blocks, ROUTE_THREADS, smem, s>>>(a, bf16);
-  CK(cudaGetLastError());
+  CK(launch_pdl(route_kernel<NPL>, dim3(blocks), dim3(ROUTE_THREADS), smem, s, a, bf16));
   return MOE_OK;
 }
 
-moe_status run_place(const int32_t* ids, int P, int E, int per_block, int blocks, const int32_t* counts, int32_t* offsets,
-                     int32_t* tiles, int32_t* order, int32_t* place, cudaStream_t s) {
-  const size_t smem = place_smem(E, place_threads(E));
+// counts [E + 1, blocks] of the blocks' pairs -> the grouping; the totals follow the counts in the workspace
+moe_status run_place(const int32_t* ids, int P, int E, int per_block, int blocks, int32_t* counts, int32_t* offsets, int32_t* tiles,
+                     int32_t* order, int32_t* place, cudaStream_t s) {
+  int32_t* total = counts + (size_t)(E + 1) * blocks;
+  CK(launch_pdl(starts_kernel, dim3((E + 8) / 8), dim3(256), 0, s, counts, E, blocks, total));
+  const size_t smem = (size_t)(2 + PLACE_WARPS) * (E + 1) * 4;
   CK(allow_smem((const void*)place_kernel, smem));
-  place_kernel<<<blocks, place_threads(E), smem, s>>>(ids, P, E, per_block, counts, offsets, tiles, order, place);
-  CK(cudaGetLastError());
+  const int per = std::max(1, PLACE_THREADS / per_block);   // about a pair a thread
+  CK(launch_pdl(place_kernel, dim3((blocks + per - 1) / per), dim3(PLACE_THREADS), smem, s, ids, P, E, per_block, per, blocks,
+                (const int32_t*)counts, (const int32_t*)total, offsets, tiles, order, place));
+  return MOE_OK;
+}
+
+moe_status run_small(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* tiles, int32_t* order, int32_t* place, cudaStream_t s) {
+  const size_t smem = small_smem(E);
+  CK(allow_smem((const void*)group_small_kernel, smem));
+  CK(launch_pdl(group_small_kernel, dim3(1), dim3(ROUTE_THREADS), smem, s, ids, P, E, offsets, tiles, order, place));
   return MOE_OK;
 }
 
@@ -471,10 +496,9 @@ using namespace moe;
 extern "C" int64_t moe_grouped_tiles(int64_t P, int32_t E) { return P < 0 || E < 0 ? 0 : (P + 127 * std::min<int64_t>(P, E)) / 128; }
 
 extern "C" int64_t moe_group_workspace(int32_t T, int32_t k, int32_t E) {
-  (void)k;
-  if (T < 0 || E < 0) return 0;
-  const int64_t blocks = T ? (T + tokens_per_block(T) - 1) / tokens_per_block(T) : 1;
-  return blocks * ((int64_t)E + 1) * 4;
+  if (T <= 0 || k < 0 || E < 0 || small_group(T, k)) return 0;
+  const int64_t blocks = (T + tokens_per_block(T) - 1) / tokens_per_block(T);
+  return (blocks + 1) * ((int64_t)E + 1) * 4;
 }
 
 extern "C" moe_status moe_route(int32_t T, int32_t E, int32_t k, int32_t logits_dtype, const void* logits, int32_t scoring,
@@ -497,21 +521,21 @@ extern "C" moe_status moe_route(int32_t T, int32_t E, int32_t k, int32_t logits_
   if (!aligned_to(logits, logits_dtype == MOE_F32 ? 4 : 2) || !aligned_to(bias, 4) || !aligned_to(ids, 4) || !aligned_to(w, 4))
     return fail(MOE_EINVAL, "logits, bias, topk_ids and topk_w must be aligned to their element size");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T == 0)
-    return group ? run_place(nullptr, 0, E, 1, 1, nullptr, offsets, tiles, order, place, s) : MOE_OK;
+  if (T == 0) return group ? run_small(nullptr, 0, E, offsets, tiles, order, place, s) : MOE_OK;
   RouteArgs a{};
   a.T = T; a.E = E; a.k = k; a.scoring = scoring; a.n_group = n_group; a.topk_group = topk_group;
   a.renorm = renormalize != 0; a.scale = scale; a.logits = logits; a.bias = bias; a.ids = ids; a.w = w;
   a.offsets = offsets; a.tiles = tiles; a.order = order; a.place = place;
-  a.counts = static_cast<int32_t*>(workspace);
-  a.tokens_per_block = group && T <= kOneBlockTokens ? T : tokens_per_block(T);
+  const bool small = group && small_group(T, k);
+  a.counts = group && !small ? static_cast<int32_t*>(workspace) : nullptr;
+  a.tokens_per_block = small ? T : tokens_per_block(T);
   const int blocks = (T + a.tokens_per_block - 1) / a.tokens_per_block;
   const int bf16 = logits_dtype == MOE_BF16;
   const int npl = (E + 31) / 32;
   st = npl <= 2 ? run_route<2>(a, bf16, blocks, s) : npl <= 4 ? run_route<4>(a, bf16, blocks, s)
        : npl <= 8 ? run_route<8>(a, bf16, blocks, s) : npl <= 16 ? run_route<16>(a, bf16, blocks, s)
        : npl <= 32 ? run_route<32>(a, bf16, blocks, s) : run_route<128>(a, bf16, blocks, s);
-  if (st != MOE_OK || !group || blocks == 1) return st;
+  if (st != MOE_OK || !a.counts) return st;
   return run_place(ids, T * k, E, a.tokens_per_block * k, blocks, a.counts, offsets, tiles, order, place, s);
 }
 
@@ -523,13 +547,11 @@ extern "C" moe_status moe_group_pairs(int32_t T, int32_t E, int32_t k, const int
   if (T > 0 && !ids) return fail(MOE_EINVAL, "topk_ids must not be NULL");
   if (!aligned_to(ids, 4)) return fail(MOE_EINVAL, "topk_ids must be 4-byte aligned");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T <= kOneBlockTokens)
-    return run_place(ids, T * k, E, std::max(1, T * k), 1, nullptr, offsets, tiles, order, place, s);
+  if (small_group(T, k)) return run_small(ids, T * k, E, offsets, tiles, order, place, s);
   const int tpb = tokens_per_block(T), blocks = (T + tpb - 1) / tpb;
   int32_t* counts = static_cast<int32_t*>(workspace);
   const size_t smem = (size_t)(E + 1) * 4;
-  count_kernel<<<blocks, ROUTE_THREADS, smem, s>>>(ids, T * k, E, tpb * k, counts);
-  CK(cudaGetLastError());
+  CK(launch_pdl(count_kernel, dim3(blocks), dim3(ROUTE_THREADS), smem, s, ids, T * k, E, tpb * k, counts));
   return run_place(ids, T * k, E, tpb * k, blocks, counts, offsets, tiles, order, place, s);
 }
 

@@ -100,17 +100,13 @@ except AttributeError:
     pass
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
 def _bad(t, name, dtypes, dim, index=None):
     """Raise what is wrong with an argument that should be a contiguous CUDA tensor."""
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dim() != dim or not t.is_contiguous():
         got = f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}" if isinstance(t, torch.Tensor) else type(t)
         raise ValueError(f"{name} must be a contiguous {dim}-dimensional tensor of {' or '.join(map(str, dtypes))}, got {got}")
-    _need(t.is_cuda, f"{name} must be on a CUDA device, is on {t.device}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, is on {t.device}")
     raise ValueError(f"{name} is on {t.device}, the other arguments on cuda:{index}")
 
 
@@ -135,7 +131,8 @@ def _scale_ptr(g, name, most, index):
         return None, 0
     _typed(g, name, _F32, 1, index)
     n = g.numel()
-    _need(n == 1 or n == most, f"{name} must hold {'1' if most == 1 else f'1 or {most}'} values, holds {n}")
+    if not (n == 1 or n == most):
+        raise ValueError(f"{name} must hold {'1' if most == 1 else f'1 or {most}'} values, holds {n}")
     return g.data_ptr(), n
 
 
@@ -153,29 +150,32 @@ class ExpertGroups:
         _typed(place, "place", _I32, 2, i)
         self.E, self.P, self._index = offsets.numel() - 1, order.numel(), i
         self.T, self.k = place.shape
-        _need(1 <= self.E <= 4096 and tiles.numel() == self.E + 1,
-              f"offsets and tiles must hold E + 1 values each (1 <= E <= 4096), hold {offsets.numel()} and {tiles.numel()}")
-        _need(self.T * self.k == self.P, f"order holds {self.P} pairs, place {self.T * self.k}")
+        if not (1 <= self.E <= 4096 and tiles.numel() == self.E + 1):
+            raise ValueError(f"offsets and tiles must hold E + 1 values each (1 <= E <= 4096), hold {offsets.numel()} and {tiles.numel()}")
+        if self.T * self.k != self.P:
+            raise ValueError(f"order holds {self.P} pairs, place {self.T * self.k}")
         self._ptrs = (offsets.data_ptr(), tiles.data_ptr(), order.data_ptr(), place.data_ptr())
         self._views = [offsets, tiles, order, place]
         self._all = None
 
     @classmethod
     def _empty(cls, T, k, E, like):
-        """Room for the grouping of T tokens, on the device of `like`."""
+        """Room for the grouping of T tokens, on the device of `like`, and the call's arguments for it."""
         self = cls.__new__(cls)
         P = T * k
         self.E, self.P, self.T, self.k, self._index = E, P, T, k, like.get_device()
-        self._all = like.new_empty(2 * (E + 1) + 2 * P, dtype=_I32)
+        ws = _operators().moe_group_workspace(T, k, E)
+        n = 2 * (E + 1) + 2 * P
+        self._all = torch.empty(n + ws // 4, dtype=_I32, device=like.device)     # the workspace last
         p = self._all.data_ptr()
         self._ptrs = (p, p + 4 * (E + 1), p + 8 * (E + 1), p + 8 * (E + 1) + 4 * P)
         self._views = None
-        return self
+        return self, (*self._ptrs, p + 4 * n if ws else None, ws)
 
     def _view(self, i):
         if self._views is None:
             e = self.E + 1
-            v = list(self._all.split((e, e, self.P, self.P)))
+            v = list(self._all[:2 * (e + self.P)].split((e, e, self.P, self.P)))
             v[3] = v[3].view(self.T, self.k)
             self._views = v
         return self._views[i]
@@ -189,7 +189,8 @@ class ExpertGroups:
 def _groups_on(groups, index):
     if not isinstance(groups, ExpertGroups):
         raise ValueError(f"groups must be ExpertGroups, is {type(groups)}")
-    _need(groups._index == index, f"groups are on cuda:{groups._index}, the other arguments on cuda:{index}")
+    if groups._index != index:
+        raise ValueError(f"groups are on cuda:{groups._index}, the other arguments on cuda:{index}")
     return groups
 
 
@@ -202,25 +203,30 @@ class FP4Rows:
     __slots__ = ("codes", "scales", "wdtype", "g", "groups", "shape", "K", "_stack", "_index", "_ptrs")
 
     def __init__(self, codes, scales, wdtype, g=None, groups=None):
-        _need(wdtype in FP4_BLOCK, f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
+        if wdtype not in FP4_BLOCK:
+            raise ValueError(f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
         dim = 2 if groups is not None or not isinstance(codes, torch.Tensor) or codes.dim() != 3 else 3
         _typed(codes, "codes", _U8, dim)
         i = codes.get_device()
         _typed(scales, "scales", _U8, 3, i)
         K = 2 * codes.shape[-1]
-        _need(K > 0 and K % 32 == 0, f"K must be a multiple of 32, is {K}")
+        if not (K > 0 and K % 32 == 0):
+            raise ValueError(f"K must be a multiple of 32, is {K}")
         if groups is not None:
             _groups_on(groups, i)
-            _need(codes.shape[0] == groups.P, f"codes hold {codes.shape[0]} rows, groups {groups.P} pairs")
+            if codes.shape[0] != groups.P:
+                raise ValueError(f"codes hold {codes.shape[0]} rows, groups {groups.P} pairs")
             n = _grouped_tiles(groups.P, groups.E)
             self._stack = (1, groups.P)
         else:
             self._stack = (1, codes.shape[0]) if dim == 2 else (codes.shape[0], codes.shape[1])
             n = self._stack[0] * -(-self._stack[1] // 128)
         want = (n, _block_groups(wdtype, K), 512)
-        _need(tuple(scales.shape) == want, f"scales must be {want}, is {tuple(scales.shape)}")
+        if tuple(scales.shape) != want:
+            raise ValueError(f"scales must be {want}, is {tuple(scales.shape)}")
         cp, sp = codes.data_ptr(), scales.data_ptr()
-        _need((cp | sp) % 16 == 0, "codes and scales must be 16-byte aligned")
+        if (cp | sp) % 16:
+            raise ValueError("codes and scales must be 16-byte aligned")
         gp, gn = _scale_ptr(g, "g", self._stack[0], i)
         self.codes, self.scales, self.wdtype, self.g, self.groups = codes, scales, wdtype, g, groups
         self.K, self._index, self._ptrs = K, i, (cp, sp, gp, gn)
@@ -232,8 +238,8 @@ class FP4Rows:
         self = cls.__new__(cls)
         K = shape[-1]
         n = _grouped_tiles(groups.P, groups.E) if groups is not None else stack[0] * -(-stack[1] // 128)
-        self.codes = like.new_empty((*shape[:-1], K // 2), dtype=_U8)
-        self.scales = like.new_empty((n, _block_groups(wdtype, K), 512), dtype=_U8)
+        self.codes = torch.empty((*shape[:-1], K // 2), dtype=_U8, device=like.device)
+        self.scales = torch.empty((n, _block_groups(wdtype, K), 512), dtype=_U8, device=like.device)
         self.wdtype, self.g, self.groups, self.shape, self.K, self._stack = wdtype, g, groups, shape, K, stack
         self._index = like.get_device()
         self._ptrs = (self.codes.data_ptr(), self.scales.data_ptr(), *gp)
@@ -248,11 +254,6 @@ def _grouped_tiles(P, E):
     return (P + 127 * min(P, E)) // 128
 
 
-def _workspace(T, k, E, like):
-    n = _operators().moe_group_workspace(T, k, E)
-    return like.new_empty(n, dtype=_U8), n
-
-
 def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=1, renormalize=True, scale=1.0,
           groups=False, stream=None):
     """Experts and gates of each token: (topk_ids int32 [T, k], topk_w fp32 [T, k]), or with groups=True also the
@@ -261,28 +262,29 @@ def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=
     dt = _floats(logits, "logits", 2)
     T, E = logits.shape
     k, index = int(top_k), logits.get_device()
-    _need(scoring in SCORING, f"scoring must be 'softmax' or 'sigmoid', is {scoring!r}")
+    if scoring not in SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', is {scoring!r}")
     if not 1 <= k <= E <= 4096:
         raise ValueError(f"1 <= top_k <= E <= 4096 is needed, got top_k {k}, E {E}")
     sc = SCORING[scoring]
-    _need(sc or (bias is None and n_group == 1), "softmax scoring takes no bias and no expert groups")
+    if not (sc or (bias is None and n_group == 1)):
+        raise ValueError("softmax scoring takes no bias and no expert groups")
     if bias is not None:
         _typed(bias, "bias", _F32, 1, index)
-        _need(bias.numel() == E, f"bias must hold E = {E} values, holds {bias.numel()}")
+        if bias.numel() != E:
+            raise ValueError(f"bias must hold E = {E} values, holds {bias.numel()}")
     if n_group != 1 or topk_group != 1:
-        _need(1 <= n_group <= 32 and E % n_group == 0 and 1 <= topk_group <= n_group and topk_group * (E // n_group) >= k,
-              f"n_group (1 to 32) must divide E and topk_group groups must hold top_k experts, got n_group {n_group}, "
-              f"topk_group {topk_group}, E {E}, top_k {k}")
+        if not (1 <= n_group <= 32 and E % n_group == 0 and 1 <= topk_group <= n_group and topk_group * (E // n_group) >= k):
+            raise ValueError(f"n_group (1 to 32) must divide E and topk_group groups must hold top_k experts, got n_group {n_group}, "
+                                 f"topk_group {topk_group}, E {E}, top_k {k}")
     if _elsewhere(index, stream):
         with _On(index, stream):
             return route(logits, k, scoring=scoring, bias=bias, n_group=n_group, topk_group=topk_group,
                          renormalize=renormalize, scale=scale, groups=groups)
-    ids = logits.new_empty((T, k), dtype=_I32)
-    w = logits.new_empty((T, k), dtype=_F32)
+    ids = torch.empty((T, k), dtype=_I32, device=logits.device)
+    w = torch.empty((T, k), dtype=_F32, device=logits.device)
     if groups:
-        gr = ExpertGroups._empty(T, k, E, logits)
-        ws, n = _workspace(T, k, E, logits)
-        rest = (*gr._ptrs, ws.data_ptr(), n)
+        gr, rest = ExpertGroups._empty(T, k, E, logits)
     else:
         rest = (None, None, None, None, None, 0)
     _check(_operators().moe_route(T, E, k, dt, logits.data_ptr(), sc, None if bias is None else bias.data_ptr(), n_group,
@@ -295,13 +297,13 @@ def group_pairs(topk_ids, n_experts, *, stream=None):
     _typed(topk_ids, "topk_ids", _I32, 2)
     T, k = topk_ids.shape
     E, index = int(n_experts), topk_ids.get_device()
-    _need(1 <= E <= 4096 and k >= 1, f"1 <= n_experts <= 4096 and k >= 1 are needed, got {E} and {k}")
+    if not (1 <= E <= 4096 and k >= 1):
+        raise ValueError(f"1 <= n_experts <= 4096 and k >= 1 are needed, got {E} and {k}")
     if _elsewhere(index, stream):
         with _On(index, stream):
             return group_pairs(topk_ids, E)
-    gr = ExpertGroups._empty(T, k, E, topk_ids)
-    ws, n = _workspace(T, k, E, topk_ids)
-    _check(_operators().moe_group_pairs(T, E, k, topk_ids.data_ptr(), *gr._ptrs, ws.data_ptr(), n, _stream(index)))
+    gr, rest = ExpertGroups._empty(T, k, E, topk_ids)
+    _check(_operators().moe_group_pairs(T, E, k, topk_ids.data_ptr(), *rest, _stream(index)))
     return gr
 
 
@@ -310,12 +312,13 @@ def fp4_scale(x, *, stream=None):
     dim = 3 if isinstance(x, torch.Tensor) and x.dim() == 3 else 2
     dt = _floats(x, "x", dim)
     index, n = x.get_device(), x.numel()
-    _need(n > 0, f"x is empty: {tuple(x.shape)}")
+    if n == 0:
+        raise ValueError(f"x is empty: {tuple(x.shape)}")
     if _elsewhere(index, stream):
         with _On(index, stream):
             return fp4_scale(x)
     G = x.shape[0] if dim == 3 else 1
-    g = x.new_empty(G, dtype=_F32)
+    g = torch.empty(G, dtype=_F32, device=x.device)
     _check(_operators().moe_fp4_scale(G, n // G, dt, x.data_ptr(), g.data_ptr(), _stream(index)))
     return g
 
@@ -324,18 +327,24 @@ def quantize_fp4(x, wdtype, *, g=None, groups=None, stream=None):
     """x in 4 bits (moe_quantize_fp4).  Without groups: x [N, K] or a stack [G, N, K], g fp32 [1] or [G].  With
     groups: x [T, K], and the result holds row order[i] // k of x at grouped row i.  K a multiple of 32; g only
     for "nvfp4" (None = 1)."""
-    _need(wdtype in FP4_BLOCK, f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
+    if wdtype not in FP4_BLOCK:
+        raise ValueError(f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
     dim = 2 if groups is not None or not isinstance(x, torch.Tensor) or x.dim() != 3 else 3
     dt = _floats(x, "x", dim)
     index, K, xp = x.get_device(), x.shape[-1], x.data_ptr()
-    _need(K > 0 and K % 32 == 0, f"K must be a multiple of 32, is {K}")
-    _need(xp % 16 == 0, "x must be 16-byte aligned")
-    _need(g is None or wdtype == "nvfp4", "only nvfp4 takes a matrix scale g")
+    if not (K > 0 and K % 32 == 0):
+        raise ValueError(f"K must be a multiple of 32, is {K}")
+    if xp % 16:
+        raise ValueError("x must be 16-byte aligned")
+    if not (g is None or wdtype == "nvfp4"):
+        raise ValueError("only nvfp4 takes a matrix scale g")
     if groups is not None:
         _groups_on(groups, index)
-        _need(groups.T == x.shape[0], f"x has {x.shape[0]} rows, groups hold {groups.T} tokens")
+        if groups.T != x.shape[0]:
+            raise ValueError(f"x has {x.shape[0]} rows, groups hold {groups.T} tokens")
         stack, shape = (1, groups.P), (groups.P, K)
-        rest = (groups.E, groups.k, *groups._ptrs[:3])
+        off, til, _, place = groups._ptrs
+        rest = (groups.E, groups.k, off, til, place)
     else:
         stack = (x.shape[0], x.shape[1]) if dim == 3 else (1, x.shape[0])
         shape, rest = tuple(x.shape), (0, 0, None, None, None)
@@ -357,25 +366,30 @@ def _rows(q, name):
 def dequantize_fp4(q, *, out_dtype=torch.bfloat16, stream=None):
     """The values that q stands for, in q.shape; rows that no pair fills are zero (moe_dequantize_fp4)."""
     _rows(q, "q")
-    _need(out_dtype in _FLOATS, f"out_dtype must be float32 or bfloat16, is {out_dtype}")
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
     index = q._index
     if _elsewhere(index, stream):
         with _On(index, stream):
             return dequantize_fp4(q, out_dtype=out_dtype)
     rest = (0, None, None) if q.groups is None else (q.groups.E, *q.groups._ptrs[:2])
-    out = q.codes.new_empty(q.shape, dtype=out_dtype)
+    out = torch.empty(q.shape, dtype=out_dtype, device=q.codes.device)
     _check(_operators().moe_dequantize_fp4(*q._stack, q.K, DTYPES[q.wdtype], *q._ptrs, *rest, _FLOATS[out_dtype],
                                            out.data_ptr(), _stream(index)))
     return out
 
 
 def _columns(groups, E, N, act, out_dtype):
-    _need(groups.E == E, f"w holds {E} experts, groups {groups.E}")
-    _need(act in ACTS, f"act must be 'none' or 'swiglu', is {act!r}")
-    _need(out_dtype in _FLOATS, f"out_dtype must be float32 or bfloat16, is {out_dtype}")
+    if groups.E != E:
+        raise ValueError(f"w holds {E} experts, groups {groups.E}")
+    if act not in ACTS:
+        raise ValueError(f"act must be 'none' or 'swiglu', is {act!r}")
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
     if not ACTS[act]:
         return N
-    _need(N % 32 == 0, f"swiglu needs w rows a multiple of 32, got {N}")
+    if N % 32:
+        raise ValueError(f"swiglu needs w rows a multiple of 32, got {N}")
     return N // 2
 
 
@@ -389,22 +403,24 @@ def grouped_matmul(x, w, groups, *, act="none", gather=False, out_dtype=torch.bf
     _groups_on(groups, index)
     E, N, K = w.shape
     cols = _columns(groups, E, N, act, out_dtype)
-    _need(N > 0 and K > 0 and K % 8 == 0, f"w must be [E, N, K] with K a multiple of 8, is {tuple(w.shape)}")
+    if not (N > 0 and K > 0 and K % 8 == 0):
+        raise ValueError(f"w must be [E, N, K] with K a multiple of 8, is {tuple(w.shape)}")
     rows = groups.T if gather else groups.P
     if x.shape[0] != rows or x.shape[1] != K:
         raise ValueError(f"x must be {(rows, K)}, is {tuple(x.shape)}")
     xp, wp = x.data_ptr(), w.data_ptr()
-    _need((xp | wp) % 16 == 0, "x and w must be 16-byte aligned")
+    if (xp | wp) % 16:
+        raise ValueError("x and w must be 16-byte aligned")
     if _elsewhere(index, stream):
         with _On(index, stream):
             return grouped_matmul(x, w, groups, act=act, gather=gather, out_dtype=out_dtype)
     off, til, order, _ = groups._ptrs
-    out = x.new_empty((groups.P, cols), dtype=out_dtype)
+    out = torch.empty((groups.P, cols), dtype=out_dtype, device=x.device)
     ops, ws, n = _operators(), None, 0
     if gather:
         n = ops.moe_grouped_matmul_workspace(groups.P, E, K, 1)
         if n:
-            ws = x.new_empty(n, dtype=_U8)
+            ws = torch.empty(n, dtype=_U8, device=x.device)
     _check(ops.moe_grouped_matmul(groups.P, E, N, K, xp, rows, order if gather else None, groups.k, wp, off, til, ACTS[act],
                                   _FLOATS[out_dtype], out.data_ptr(), ws.data_ptr() if n else None, n, _stream(index)))
     return out
@@ -418,15 +434,20 @@ def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, 
     _rows(w, "w")
     index = w._index
     _groups_on(groups, index)
-    _need(len(w.shape) == 3 and w.groups is None, f"w must be [E, N, K], is {w.shape}")
+    if not (len(w.shape) == 3 and w.groups is None):
+        raise ValueError(f"w must be [E, N, K], is {w.shape}")
     E, N, K = w.shape
     cols = _columns(groups, E, N, act, out_dtype)
-    _need(x.groups is not None and x._index == index and x.groups.E == E and N > 0,
-          "x must hold rows in the order of w's experts, on the same device")
-    _need(x.wdtype == w.wdtype, f"x is {x.wdtype}, w is {w.wdtype}")
-    _need(x.shape == (groups.P, K), f"x must be {(groups.P, K)}, is {x.shape}")
-    _need(not quantize or (ACTS[act] and cols % 32 == 0), "quantize needs act='swiglu' and w rows a multiple of 64")
-    _need(g_out is None or (quantize and x.wdtype == "nvfp4"), "g_out goes with quantize=True and nvfp4")
+    if not (x.groups is not None and x._index == index and x.groups.E == E and N > 0):
+        raise ValueError("x must hold rows in the order of w's experts, on the same device")
+    if x.wdtype != w.wdtype:
+        raise ValueError(f"x is {x.wdtype}, w is {w.wdtype}")
+    if not (x.shape == (groups.P, K)):
+        raise ValueError(f"x must be {(groups.P, K)}, is {x.shape}")
+    if not (not quantize or (ACTS[act] and cols % 32 == 0)):
+        raise ValueError("quantize needs act='swiglu' and w rows a multiple of 64")
+    if not (g_out is None or (quantize and x.wdtype == "nvfp4")):
+        raise ValueError("g_out goes with quantize=True and nvfp4")
     go = _scale_ptr(g_out, "g_out", 1, index)
     if _elsewhere(index, stream):
         with _On(index, stream):
@@ -435,7 +456,7 @@ def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, 
         out = FP4Rows._empty((groups.P, cols), x.wdtype, g_out, go, groups, (1, groups.P), x.codes)
         dst = (None, out._ptrs[0], out._ptrs[1], go[0])
     else:
-        out = x.codes.new_empty((groups.P, cols), dtype=out_dtype)
+        out = torch.empty((groups.P, cols), dtype=out_dtype, device=x.codes.device)
         dst = (out.data_ptr(), None, None, None)
     _check(_operators().moe_grouped_matmul_fp4(groups.P, E, N, K, DTYPES[x.wdtype], *x._ptrs[:3], *w._ptrs, *groups._ptrs[:2],
                                                ACTS[act], _FLOATS[out_dtype], *dst, _stream(index)))
@@ -452,12 +473,14 @@ def combine(y, groups, topk_w, *, out_dtype=torch.float32, stream=None):
     T, k, N = groups.T, groups.k, y.shape[1]
     if topk_w.shape[0] != T or topk_w.shape[1] != k:
         raise ValueError(f"topk_w must be {(T, k)}, is {tuple(topk_w.shape)}")
-    _need(y.shape[0] == groups.P and N > 0, f"y must be [{groups.P}, N], is {tuple(y.shape)}")
-    _need(out_dtype in _FLOATS, f"out_dtype must be float32 or bfloat16, is {out_dtype}")
+    if not (y.shape[0] == groups.P and N > 0):
+        raise ValueError(f"y must be [{groups.P}, N], is {tuple(y.shape)}")
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
     if _elsewhere(index, stream):
         with _On(index, stream):
             return combine(y, groups, topk_w, out_dtype=out_dtype)
-    out = y.new_empty((T, N), dtype=out_dtype)
+    out = torch.empty((T, N), dtype=out_dtype, device=y.device)
     _check(_operators().moe_combine(T, k, N, dt, y.data_ptr(), groups._ptrs[3], topk_w.data_ptr(), _FLOATS[out_dtype],
                                     out.data_ptr(), _stream(index)))
     return out

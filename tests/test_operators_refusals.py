@@ -43,7 +43,7 @@ def test_sizes_without_a_device(lib):
     assert lib.moe_grouped_tiles(8, 128) == 8           # eight experts of one row each
     assert lib.moe_grouped_tiles(256, 2) == 3           # 1 + 255 rows
     assert lib.moe_grouped_tiles(1 << 40, 4096) == ((1 << 40) + 127 * 4096) // 128
-    assert lib.moe_group_workspace(0, 8, 128) >= 129 * 4
+    assert lib.moe_group_workspace(0, 8, 128) == 0 and lib.moe_group_workspace(32, 8, 128) == 0     # one block, no counts
     assert lib.moe_group_workspace(8192, 8, 256) >= 257 * 4
 
 
@@ -58,8 +58,8 @@ def route(lib, T=4, E=16, k=2, dt=F32, logits=A, scoring=0, bias=None, ng=1, tg=
     (dict(ng=2, tg=2), b"softmax"), (dict(scoring=1, ng=3, tg=3), b"n_group"), (dict(scoring=1, ng=8, tg=0), b"topk_group"),
     (dict(scoring=1, ng=8, tg=9), b"topk_group"), (dict(scoring=1, ng=16, tg=1), b"k = 2"), (dict(logits=None), b"NULL"),
     (dict(ids=None), b"NULL"), (dict(logits=P(0x10002)), b"aligned"), (dict(w=P(0x10001)), b"aligned"),
-    (dict(off=D), b"all needed"), (dict(off=D, til=F, order=G, place=H), b"workspace"),
-    (dict(off=D, til=F, order=G, place=H, ws=A, n=16), b"workspace"),
+    (dict(off=D), b"all needed"), (dict(T=64, k=8, off=D, til=F, order=G, place=H), b"workspace"),
+    (dict(T=64, k=8, off=D, til=F, order=G, place=H, ws=A, n=16), b"workspace"),
     (dict(off=D, til=F, order=P(0x10002), place=H, ws=A, n=1 << 20), b"aligned")])
 def test_route_refuses(lib, kw, word):
     refused(lib, route(lib, **kw), word)
@@ -68,7 +68,7 @@ def test_route_refuses(lib, kw, word):
 @pytest.mark.parametrize("args,word", [
     ((-1, 4, 2, A, B, C, D, F, G, 1 << 20), b"T >= 0"), ((4, 0, 2, A, B, C, D, F, G, 1 << 20), b"E"),
     ((4, 4, 2, None, B, C, D, F, G, 1 << 20), b"NULL"), ((4, 4, 2, A, None, C, D, F, G, 1 << 20), b"all needed"),
-    ((4, 4, 2, A, B, C, D, F, None, 0), b"workspace"), ((4, 4, 2, P(0x10001), B, C, D, F, G, 1 << 20), b"aligned")])
+    ((400, 4, 2, A, B, C, D, F, None, 0), b"workspace"), ((4, 4, 2, P(0x10001), B, C, D, F, G, 1 << 20), b"aligned")])
 def test_group_pairs_refuses(lib, args, word):
     refused(lib, lib.moe_group_pairs(*args, None), word)
 
