@@ -4,8 +4,8 @@
 // A thread holds 16 consecutive elements of a row: one NVFP4 block, or half an MXFP4
 // block, whose largest value it shares with its neighbour.  The largest |x| is taken
 // over the bit patterns, so NaN shows up above infinity.  Rounding is the format's:
-// NVFP4 takes the correctly rounded quotient by the step, MXFP4 multiplies by a power of
-// two, which is exact.  Scales go straight into the tile order that the tensor cores
+// NVFP4's codes are those of the correctly rounded quotient by the step, MXFP4 multiplies by a
+// power of two, which is exact.  Scales go straight into the tile order that the tensor cores
 // take, a word for each row's group of four blocks.
 //
 // Rows for the experts are read and converted once a token and stored once an expert
@@ -16,161 +16,185 @@
 #include "operators.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 
 namespace {
 
 constexpr int Q_THREADS = 256;
-constexpr int Q_UNITS = 1024;   // 16-element units of one step of a block, about
-constexpr int Q_PLACES = 256;   // output rows of one step, at most
+constexpr int Q_WARPS = Q_THREADS / 32;
+// A warp takes a segment of a row (blockIdx.y): a unit of 16 elements a lane when quantising, four of 8 when dequantising,
+// loaded before any is used.  Rows, segments and matrices (blockIdx.z) come from the grid: 64-bit divisions were half of
+// the instructions (391 us for 805 MB of bf16, against 152 of its bytes).
+constexpr int Q_SEG = 32, D_SEG = 128;
 
 struct QuantArgs {
-  int64_t rows;      // input rows
-  int N, K, E, k, block_groups, g_count, step_rows;
+  int64_t rows;      // input rows (of each matrix)
+  int K, E, k, block_groups, g_count;
   const void* x;
   const float* g;
   const int32_t *offsets, *tiles, *place;   // NULL: a stack of matrices
   uint8_t *codes, *scales;
 };
 
-// an output row, the padded row of its scales, its matrix's scale; row < 0: none
-struct RowAt { int64_t row, pad; float g; };
+struct RowAt { int64_t row, pad; };   // an output row and the padded row of its scales; row < 0: none
 
-__device__ __forceinline__ RowAt row_at(const QuantArgs& a, int64_t r) {
-  RowAt o{r, 0, 1.0f};
-  if (a.offsets) {
-    const int i = (int)r, e = expert_of(a.offsets, a.E, i);
-    o.pad = (int64_t)__ldg(a.tiles + e) * 128 + (i - __ldg(a.offsets + e));
-    if (a.g) o.g = __ldg(a.g);
-  } else {
-    const int64_t m = r / a.N;
-    o.pad = m * (ceil_div64(a.N, 128) * 128) + (r - m * a.N);
-    if (a.g) o.g = __ldg(a.g + (a.g_count > 1 ? m : 0));
-  }
-  return o;
+// row i of the rows in expert order
+__device__ __forceinline__ RowAt grouped_row(const QuantArgs& a, int i) {
+  if (i < 0) return RowAt{-1, 0};
+  const int e = expert_of(a.offsets, a.E, i);
+  return RowAt{i, (int64_t)__ldg(a.tiles + e) * 128 + (i - __ldg(a.offsets + e))};
 }
 
-// 16 elements of a row; a row of K starts on 16 elements' bytes from its 16-byte aligned matrix
+// 16 elements of a row as they are; a row of K starts on 16 elements' bytes from its 16-byte aligned matrix
 template <typename X>
-__device__ __forceinline__ void load16(const X* p, float (&v)[16]) {
-  constexpr int W = sizeof(X) == 4 ? 4 : 2;   // 16-byte words
-  uint4 q[W];
-  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {   // 32 bytes an instruction
+struct Raw16 {
+  static constexpr int W = sizeof(X) == 4 ? 16 : 8;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const X* p) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p);
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {   // 32 bytes an instruction
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i)
-      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(q[2 * i].x), "=r"(q[2 * i].y), "=r"(q[2 * i].z), "=r"(q[2 * i].w), "=r"(q[2 * i + 1].x), "=r"(q[2 * i + 1].y),
-                     "=r"(q[2 * i + 1].z), "=r"(q[2 * i + 1].w)
-                   : "l"(reinterpret_cast<const uint4*>(p) + 2 * i));
-  } else {
+      for (int i = 0; i < W; i += 8)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]), "=r"(w[i + 6]), "=r"(w[i + 7])
+                     : "l"(src + i));
+    } else {
 #pragma unroll
-    for (int i = 0; i < W; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-  }
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(X) == 4) {
-        v[4 * i + j] = __uint_as_float(u[j]);
-      } else {
-        v[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
-        v[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      for (int i = 0; i < W; i += 4) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + i));
+        w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
       }
     }
   }
-}
+  // bits of the largest |x| as fp32
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0u;
+    if constexpr (sizeof(X) == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) m = max(m, w[i] & 0x7fffffffu);
+    } else {   // two at a time: bf16 patterns without their signs order like the values
+#pragma unroll
+      for (int i = 0; i < W; i += 2) m = __vimax3_u16x2(m, w[i] & 0x7fff7fffu, w[i + 1] & 0x7fff7fffu);
+      m = max(m << 16, m & 0xffff0000u);
+    }
+    return m;
+  }
+  __device__ __forceinline__ void values(float (&v)[16]) const {
+    if constexpr (sizeof(X) == 4) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+};
 
-template <typename X, bool NV>
-__global__ void __launch_bounds__(Q_THREADS) quantize_kernel(QuantArgs a) {
-  __shared__ RowAt at[Q_PLACES];
+// GROUPED: rows become the rows of their pairs in expert order; otherwise a stack of matrices
+template <typename X, bool NV, bool GROUPED>
+__global__ void __launch_bounds__(Q_THREADS, sizeof(X) == 4 ? 3 : 4) quantize_kernel(QuantArgs a) {
+  __shared__ RowAt places[Q_WARPS][GROUPED ? 32 : 1];
   pdl_wait();
   pdl_trigger();
   constexpr int G = NV ? 4 : 8;                       // units of a group of four blocks
-  const int units_row = a.K / 16, per_row = (units_row + G - 1) / G * G;
-  const int kk = min(a.k, Q_PLACES / a.step_rows);    // copies of a row handled at a time
-  for (int64_t r0 = (int64_t)blockIdx.x * a.step_rows; r0 < a.rows; r0 += (int64_t)gridDim.x * a.step_rows) {
-    const int n = (int)min((int64_t)a.step_rows, a.rows - r0);
-    for (int j0 = 0; j0 < a.k; j0 += kk) {
-      const int nj = min(kk, a.k - j0);
-      __syncthreads();
-      for (int i = threadIdx.x; i < n * nj; i += Q_THREADS) {
-        const int64_t r = r0 + i / nj;
-        const int64_t row = a.place ? (int64_t)__ldg(a.place + r * a.k + j0 + i % nj) : r;
-        at[i] = row < 0 ? RowAt{-1, 0, 1.0f} : row_at(a, row);
-      }
-      __syncthreads();
-      // whole groups a row, so that four (eight) neighbouring lanes make a group's word of scales; past the row's end: no block
-      for (int u0 = 0; u0 < n * per_row; u0 += Q_THREADS) {
-        const int u = u0 + threadIdx.x;
-        const bool some = u < n * per_row;
-        const int r = some ? u / per_row : 0, c = some ? u - r * per_row : 0;
-        const bool live = some && c < units_row;
-        float v[16];
-        uint32_t m = 0u, code = 0u;
-        uint2 q = make_uint2(0u, 0u);
-        if (live) {
-          load16(static_cast<const X*>(a.x) + (size_t)(r0 + r) * a.K + c * 16, v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-        }
-        if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        if (live) {
-          float step;
-          code = block_scale<NV>(m, a.place ? (a.g ? __ldg(a.g) : 1.0f) : at[r].g, step);
-          q = encode16<NV>(v, m, code, step);
-        }
-        if (NV) {
-          code |= __shfl_xor_sync(0xffffffffu, code, 1) << 8;      // lane 0 of 4: bytes of lanes 0, 1
-          code |= __shfl_xor_sync(0xffffffffu, code, 2) << 16;
-        } else {
-          code |= __shfl_xor_sync(0xffffffffu, code, 2) << 8;
-          code |= __shfl_xor_sync(0xffffffffu, code, 4) << 16;
-        }
-        if (!some) continue;
-        for (int j = 0; j < nj; ++j) {
-          const RowAt o = at[r * nj + j];
-          if (o.row < 0) continue;
-          if (live) *reinterpret_cast<uint2*>(a.codes + (size_t)o.row * (a.K / 2) + c * 8) = q;
-          if (c % G == 0) *reinterpret_cast<uint32_t*>(a.scales + scale_at((size_t)o.pad, c / (G / 4), a.block_groups)) = code;
-        }
+  const int units = a.K / 16, padded = (units + G - 1) / G * G;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = (int)blockIdx.y * Q_SEG + lane;
+  const bool live = c < units, word = c % G == 0 && c < padded;
+  const int64_t m = blockIdx.z;
+  const float g = NV && a.g ? __ldg(a.g + (a.g_count > 1 ? m : 0)) : 1.0f, rg = __frcp_rn(g);
+  const size_t word_at = ((size_t)(c / (G / 4)) >> 2) * 512;
+  auto store = [&](int64_t row, int64_t pad, uint2 q, uint32_t code) {
+    if (live) *reinterpret_cast<uint2*>(a.codes + (size_t)row * (a.K / 2) + c * 8) = q;
+    if (word) *reinterpret_cast<uint32_t*>(a.scales + scale_at((size_t)pad, 0, a.block_groups) + word_at) = code;
+  };
+  for (int64_t r = (int64_t)blockIdx.x * Q_WARPS + warp; r < a.rows; r += (int64_t)gridDim.x * Q_WARPS) {
+    Raw16<X> x;
+    if (live) x.load(static_cast<const X*>(a.x) + (size_t)(m * a.rows + r) * a.K + c * 16);
+    uint32_t top = live ? x.top() : 0u, code = 0u;
+    uint2 q = make_uint2(0u, 0u);
+    if (!NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    if (live) {
+      float step, v[16];
+      x.values(v);
+      code = block_scale<NV>(top, g, rg, step);
+      q = encode16<NV>(v, top, code, step);
+    }
+    // four (eight) neighbouring lanes make a group's word of scales; past the row's end there is no block
+    code |= __shfl_xor_sync(0xffffffffu, code, NV ? 1 : 2) << 8;
+    code |= __shfl_xor_sync(0xffffffffu, code, NV ? 2 : 4) << 16;
+    if constexpr (!GROUPED) {
+      store(m * a.rows + r, m * ((a.rows + 127) & ~127ll) + r, q, code);
+    } else {
+      RowAt* at = places[warp];
+      for (int j0 = 0; j0 < a.k; j0 += 32) {
+        const int nj = min(32, a.k - j0);
+        __syncwarp();
+        if (lane < nj) at[lane] = grouped_row(a, __ldg(a.place + r * a.k + j0 + lane));
+        __syncwarp();
+        for (int j = 0; j < nj; ++j)
+          if (at[j].row >= 0) store(at[j].row, at[j].pad, q, code);
       }
     }
   }
 }
 
-// 8 values a thread: 16 bytes of bf16
+// two e2m1 codes (low nibble first) as fp16 values, exact
+__device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
+  uint32_t h;
+  asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 template <typename O, bool NV>
 __global__ void __launch_bounds__(Q_THREADS) dequantize_kernel(QuantArgs a, O* __restrict__ out) {
-  __shared__ RowAt at[Q_PLACES];
   pdl_wait();
   pdl_trigger();
-  const int per_row = a.K / 8;
-  for (int64_t r0 = (int64_t)blockIdx.x * a.step_rows; r0 < a.rows; r0 += (int64_t)gridDim.x * a.step_rows) {
-    const int n = (int)min((int64_t)a.step_rows, a.rows - r0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += Q_THREADS) {
-      at[i] = a.offsets && r0 + i >= __ldg(a.offsets + a.E) ? RowAt{-1, 0, 1.0f} : row_at(a, r0 + i);
-    }
-    __syncthreads();
-    for (int u = threadIdx.x; u < n * per_row; u += Q_THREADS) {
-      const int r = u / per_row, c = u - r * per_row;
-      const RowAt o = at[r];
-      O res[8];
-      if (o.row < 0) {
+  const int units = a.K / 8, lane = threadIdx.x & 31;
+  const int c0 = (int)blockIdx.y * D_SEG + lane;
+  const int64_t m = blockIdx.z;
+  const float g = a.g ? __ldg(a.g + (a.g_count > 1 ? m : 0)) : 1.0f;
+  for (int64_t r = (int64_t)blockIdx.x * Q_WARPS + (threadIdx.x >> 5); r < a.rows; r += (int64_t)gridDim.x * Q_WARPS) {
+    const bool none = a.offsets && r >= __ldg(a.offsets + a.E);   // no pair fills the row
+    const int64_t row = m * a.rows + r;
+    const int64_t pad = none ? 0 : a.offsets ? grouped_row(a, (int)r).pad : m * ((a.rows + 127) & ~127ll) + r;
+    uint32_t q[D_SEG / 32], sc[D_SEG / 32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) res[i] = (O)0.0f;
-      } else {
-        const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (size_t)o.row * (a.K / 2)) + c);
-        const uint32_t sc = __ldg(a.scales + scale_at((size_t)o.pad, NV ? c >> 1 : c >> 2, a.block_groups));
-        const float step = (NV ? e4m3_value(sc) : e8m0_value(sc)) * o.g;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) res[i] = (O)(e2m1_value((q >> (4 * i)) & 15u) * step);
+    for (int h = 0; h < D_SEG / 32; ++h) {
+      const int c = c0 + 32 * h;
+      q[h] = sc[h] = 0u;
+      if (c < units && !none) {
+        q[h] = __ldg(reinterpret_cast<const uint32_t*>(a.codes + (size_t)row * (a.K / 2)) + c);
+        sc[h] = __ldg(a.scales + scale_at((size_t)pad, NV ? c >> 1 : c >> 2, a.block_groups));
       }
-      uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(r0 + r) * a.K + c * 8);
+    }
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(O) / 2; ++i) dst[i] = reinterpret_cast<const uint4*>(res)[i];
+    for (int h = 0; h < D_SEG / 32; ++h) {
+      const int c = c0 + 32 * h;
+      if (c >= units) continue;
+      const float step = none ? 0.0f : (NV ? e4m3_value(sc[h]) : e8m0_value(sc[h])) * g;
+      O res[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = e2m1x2_values((q[h] >> (8 * i)) & 255u);
+        res[2 * i] = (O)(x.x * step);
+        res[2 * i + 1] = (O)(x.y * step);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(out + (size_t)row * a.K + c * 8);
+      const uint4* src = reinterpret_cast<const uint4*>(res);
+      if (sizeof(O) == 4 && (reinterpret_cast<uintptr_t>(dst) & 31) == 0) {   // 32 bytes an instruction
+        asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(src[0].x), "r"(src[0].y), "r"(src[0].z), "r"(src[0].w),
+                     "r"(src[sizeof(O) / 4].x), "r"(src[sizeof(O) / 4].y), "r"(src[sizeof(O) / 4].z), "r"(src[sizeof(O) / 4].w), "l"(dst)
+                     : "memory");
+      } else {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(O) / 2; ++i) dst[i] = src[i];
+      }
     }
   }
 }
@@ -210,22 +234,19 @@ __global__ void finish_scale_kernel(int G, float* g) {
 }
 
 moe_status check_fp4(int32_t G, int32_t N, int32_t K, int32_t dtype, int32_t wdtype, const float* g, int32_t g_count) {
-  if (G < 0 || N < 0) return fail(MOE_EINVAL, "G and N must not be negative, got %d and %d", G, N);
-  if (K < 32 || K % 32) return fail(MOE_EINVAL, "K = %d is not a multiple of 32", K);
+  if (G < 0 || G > 65535 || N < 0) return fail(MOE_EINVAL, "G (at most 65535) and N must not be negative, got %d and %d", G, N);
+  if (K < 32 || K % 32 || K > 1 << 24) return fail(MOE_EINVAL, "K = %d is not a multiple of 32 (at most 2^24)", K);
   if (dtype != MOE_F32 && dtype != MOE_BF16) return fail(MOE_EINVAL, "dtype must be MOE_F32 or MOE_BF16");
   if (wdtype != MOE_NVFP4 && wdtype != MOE_MXFP4) return fail(MOE_EINVAL, "wdtype must be MOE_NVFP4 or MOE_MXFP4");
   if (g && g_count != 1 && g_count != G) return fail(MOE_EINVAL, "g_count must be 1 or G = %d, is %d", G, g_count);
   return MOE_OK;
 }
 
-// rows of a step of a block, and the blocks
-void set_steps(QuantArgs& a, int unit) {
-  const int64_t share = a.rows / ((int64_t)operator_sms() * 4) + 1;   // small calls: a few rows a block, on every SM
-  const int most = std::min({Q_PLACES / std::min(a.k, Q_PLACES), Q_UNITS * 16 / unit / std::max(1, a.K / unit), 64});
-  a.step_rows = (int)std::max<int64_t>(1, std::min<int64_t>(most, share));
-}
-int steps_grid(const QuantArgs& a) {
-  return (int)std::min<int64_t>((a.rows + a.step_rows - 1) / a.step_rows, (int64_t)operator_sms() * 8);
+// blocks: rows in x, a row's segments in y, matrices in z
+dim3 segment_grid(const QuantArgs& a, int G, int units, int seg) {
+  const int segs = (units + seg - 1) / seg;
+  const int64_t most = std::max<int64_t>(1, (int64_t)operator_sms() * 64 / segs / G);
+  return dim3((unsigned)std::min<int64_t>((a.rows + Q_WARPS - 1) / Q_WARPS, most), (unsigned)segs, (unsigned)G);
 }
 
 }  // namespace
@@ -273,16 +294,19 @@ extern "C" moe_status moe_quantize_fp4(int32_t G, int32_t N, int32_t K, int32_t 
     return fail(MOE_EINVAL, "offsets, tiles and place must be 4-byte aligned");
   QuantArgs a{};
   a.k = offsets ? k : 1;
-  a.rows = offsets ? N / k : (int64_t)G * N; a.N = N; a.K = K; a.E = E; a.g_count = g_count; a.x = x; a.g = g;
+  a.rows = offsets ? N / k : N; a.K = K; a.E = E; a.g_count = g_count; a.x = x; a.g = g;
   a.block_groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
   a.offsets = offsets; a.tiles = tiles; a.place = offsets ? place : nullptr; a.codes = codes; a.scales = scales;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  set_steps(a, 16);
-  const dim3 grid(steps_grid(a)), block(Q_THREADS);
+  const dim3 grid = segment_grid(a, G, (K / 16 + 7) / 8 * 8, Q_SEG), block(Q_THREADS);   // whole groups of blocks
   const bool f32 = dtype == MOE_F32, nv = wdtype == MOE_NVFP4;
-  CK(f32 ? (nv ? launch_pdl(quantize_kernel<float, true>, grid, block, 0, s, a) : launch_pdl(quantize_kernel<float, false>, grid, block, 0, s, a))
-         : (nv ? launch_pdl(quantize_kernel<__nv_bfloat16, true>, grid, block, 0, s, a)
-               : launch_pdl(quantize_kernel<__nv_bfloat16, false>, grid, block, 0, s, a)));
+  auto run = [&](auto dtype_of, auto nvfp4) {
+    using X = decltype(dtype_of);
+    constexpr bool NV = decltype(nvfp4)::value;
+    return offsets ? launch_pdl(quantize_kernel<X, NV, true>, grid, block, 0, s, a) : launch_pdl(quantize_kernel<X, NV, false>, grid, block, 0, s, a);
+  };
+  CK(f32 ? (nv ? run(float{}, std::true_type{}) : run(float{}, std::false_type{}))
+         : (nv ? run(__nv_bfloat16{}, std::true_type{}) : run(__nv_bfloat16{}, std::false_type{})));
   return MOE_OK;
 }
 
@@ -299,13 +323,12 @@ extern "C" moe_status moe_dequantize_fp4(int32_t G, int32_t N, int32_t K, int32_
     return fail(MOE_EINVAL, "codes, scales and out must be 16-byte aligned, g 4-byte aligned");
   if (!aligned_to(offsets, 4) || !aligned_to(tiles, 4)) return fail(MOE_EINVAL, "offsets and tiles must be 4-byte aligned");
   QuantArgs a{};
-  a.rows = (int64_t)G * N; a.N = N; a.K = K; a.E = E; a.k = 1; a.g_count = g_count; a.g = g;
+  a.rows = N; a.K = K; a.E = E; a.k = 1; a.g_count = g_count; a.g = g;
   a.block_groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
   a.offsets = offsets; a.tiles = tiles;
   a.codes = const_cast<uint8_t*>(codes); a.scales = const_cast<uint8_t*>(scales);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  set_steps(a, 8);
-  const dim3 grid(steps_grid(a)), block(Q_THREADS);
+  const dim3 grid = segment_grid(a, G, K / 8, D_SEG), block(Q_THREADS);
   const bool f32 = dtype == MOE_F32, nv = wdtype == MOE_NVFP4;
   float* of = static_cast<float*>(out);
   __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(out);

@@ -394,6 +394,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       const int m = o.mb * CG + (int)rank;
       float g = 1.0f;
       if (S::FP4) g = (a.gx ? __ldg(a.gx) : 1.0f) * (a.gw ? __ldg(a.gw + (a.gw_count > 1 ? o.e : 0)) : 1.0f);
+      const float go = S::NV && a.quant && a.g_out ? __ldg(a.g_out) : 1.0f, rgo = __frcp_rn(go);
       const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * S::ACC_COLS);
       bool released = false;
       auto release = [&]() {   // the accumulator (or the part the next one needs) has been read
@@ -509,7 +510,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
           if (!S::NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           float st;
-          uint32_t code = block_scale<S::NV>(top, S::NV && a.g_out ? __ldg(a.g_out) : 1.0f, st);
+          uint32_t code = block_scale<S::NV>(top, go, rgo, st);
           const uint2 codes = encode16<S::NV>(x, top, code, st);
           const int fb = m * 64 + 16 * b;
           const int og = (a.cols + (S::NV ? 63 : 127)) / (S::NV ? 64 : 128);
