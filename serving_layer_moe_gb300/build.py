@@ -1,7 +1,8 @@
-"""Build libmoecache.so in-tree with nvcc for sm_103a (no torch extension, no cmake).
+"""Build libmoecache.so in-tree with nvcc for sm_103a, and _operators.so, which takes torch
+tensors to its operators, with g++ (no cmake).
 
-Each .cu file compiles to an object in parallel, then one link.  The output
-sits next to this file so the in-tree library is the one that loads.
+Each source compiles to an object in parallel, then one link each.  The outputs
+sit next to this file so the in-tree libraries are the ones that load.
 """
 from __future__ import annotations
 
@@ -10,12 +11,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoecache.so")
+HOST = os.path.join(HERE, "_operators.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-DNDEBUG"]
@@ -44,14 +47,35 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    def compile_host() -> str:
+        from torch.utils.cpp_extension import include_paths
+        obj = os.path.join(BUILD, "operators_host.o")
+        inc = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(cc)), "include")]
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-w", *(f"-I{i}" for i in inc), "-c",
+               os.path.join(CSRC, "operators_host.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for operators_host.cpp:\n{r.stderr}")
+        return obj
+
+    with ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
+        host = ex.submit(compile_host)
         objs = list(ex.map(compile_one, srcs))
+        host_obj = host.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    from torch.utils.cpp_extension import library_paths
+    libs = [f"-L{p}" for p in library_paths()]
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", HOST + ".tmp", host_obj, f"-L{HERE}", "-l:libmoecache.so", "-Wl,-rpath,$ORIGIN",
+           *libs, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(HOST + ".tmp", HOST)
     return LIB
 
 

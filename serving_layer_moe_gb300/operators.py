@@ -10,8 +10,9 @@ Argument checks, output tensors and pointers only: the work is in the library's 
 fallback.  Everything is enqueued on `stream` (torch's current stream if None); outputs are allocated for
 that stream.  Wrong arguments raise ValueError before anything is enqueued.
 
-One decoded token runs all five calls in the time of a few launches, so the calls are kept short: a whole
-argument is checked in one expression, and only a failed one is looked at again for its message.
+One decoded token runs all five calls in the time of a few launches, so the ordinary call goes straight to
+csrc/operators_host.cpp, which checks, allocates and launches.  What that leaves alone (it returns None) is
+looked at here: a wrong argument raises, another device or stream is made current and the call made again.
 """
 from __future__ import annotations
 
@@ -33,6 +34,22 @@ _FLOATS = {torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"]}
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 _lib = None
+_host_module = None
+
+
+def _host():
+    """The C++ side of the binding (_operators.so)."""
+    global _host_module
+    if _host_module is None:
+        _operators()
+        try:
+            import importlib
+            host = importlib.import_module("._operators", __package__)
+        except ImportError as e:
+            raise RuntimeError(f"_operators.so is not built ({e}); build it with serving_layer_moe_gb300.build.build()") from e
+        host.init(_check)
+        _host_module = host
+    return _host_module
 
 
 def _operators():
@@ -85,19 +102,16 @@ class _On:
         return False
 
 
-def _elsewhere(index, stream):
-    """Whether a call for tensors of device `index` has to make another stream or device current first."""
-    return stream is not None or index != torch.cuda.current_device()
-
-
 def _stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
-try:    # the same without building Stream objects, where this torch has it
-    _stream = torch._C._cuda_getCurrentRawStream
-except AttributeError:
-    pass
+def _again(call, index, stream):
+    """Make a call that was left alone again, on its own device and stream, now that its arguments are right."""
+    if stream is None and index == torch.cuda.current_device():
+        raise RuntimeError("the call was not made: its arguments pass every check here")
+    with _On(index, stream):
+        return call()
 
 
 def _bad(t, name, dtypes, dim, index=None):
@@ -125,61 +139,50 @@ def _typed(t, name, dtype, dim, index=None):
     return t
 
 
-def _scale_ptr(g, name, most, index):
-    """Pointer and count of an fp32 matrix scale of 1 or `most` values (None: no scale)."""
-    if g is None:
-        return None, 0
-    _typed(g, name, _F32, 1, index)
-    n = g.numel()
-    if not (n == 1 or n == most):
-        raise ValueError(f"{name} must hold {'1' if most == 1 else f'1 or {most}'} values, holds {n}")
-    return g.data_ptr(), n
+def _scale(g, name, most, index):
+    """An fp32 matrix scale of 1 or `most` values (None: no scale)."""
+    if g is not None:
+        _typed(g, name, _F32, 1, index)
+        if g.numel() != 1 and g.numel() != most:
+            raise ValueError(f"{name} must hold {'1' if most == 1 else f'1 or {most}'} values, holds {g.numel()}")
 
 
 class ExpertGroups:
     """The (token, expert) pairs of a call in expert order: offsets and tiles [E + 1], order [T * k] and
     place [T, k], all int32 (include/moe_operators.h, "Expert order").  Checked here, once, and not changed after."""
 
-    __slots__ = ("E", "P", "T", "k", "_index", "_ptrs", "_all", "_views")
+    __slots__ = ("_c", "_buffer", "_views")
 
     def __init__(self, offsets, tiles, order, place):
-        _typed(offsets, "offsets", _I32, 1)
-        i = offsets.get_device()
-        _typed(tiles, "tiles", _I32, 1, i)
-        _typed(order, "order", _I32, 1, i)
-        _typed(place, "place", _I32, 2, i)
-        self.E, self.P, self._index = offsets.numel() - 1, order.numel(), i
-        self.T, self.k = place.shape
-        if not (1 <= self.E <= 4096 and tiles.numel() == self.E + 1):
-            raise ValueError(f"offsets and tiles must hold E + 1 values each (1 <= E <= 4096), hold {offsets.numel()} and {tiles.numel()}")
-        if self.T * self.k != self.P:
-            raise ValueError(f"order holds {self.P} pairs, place {self.T * self.k}")
-        self._ptrs = (offsets.data_ptr(), tiles.data_ptr(), order.data_ptr(), place.data_ptr())
-        self._views = [offsets, tiles, order, place]
-        self._all = None
+        self._c = _host().groups_of(offsets, tiles, order, place)
+        if self._c is None:
+            _typed(offsets, "offsets", _I32, 1)
+            i = offsets.get_device()
+            _typed(tiles, "tiles", _I32, 1, i)
+            _typed(order, "order", _I32, 1, i)
+            _typed(place, "place", _I32, 2, i)
+            if tiles.numel() != offsets.numel() or not 2 <= offsets.numel() <= 4097:
+                raise ValueError(f"offsets and tiles must hold E + 1 values each (1 <= E <= 4096), hold {offsets.numel()} and {tiles.numel()}")
+            raise ValueError(f"order holds {order.numel()} pairs, place {place.numel()}")
+        self._buffer, self._views = None, (offsets, tiles, order, place)
 
     @classmethod
-    def _empty(cls, T, k, E, like):
-        """Room for the grouping of T tokens, on the device of `like`, and the call's arguments for it."""
+    def _of(cls, buffer, c):
+        """Of one buffer that holds all four, and the host module's tuple."""
         self = cls.__new__(cls)
-        P = T * k
-        self.E, self.P, self.T, self.k, self._index = E, P, T, k, like.get_device()
-        ws = _operators().moe_group_workspace(T, k, E)
-        n = 2 * (E + 1) + 2 * P
-        self._all = torch.empty(n + ws // 4, dtype=_I32, device=like.device)     # the workspace last
-        p = self._all.data_ptr()
-        self._ptrs = (p, p + 4 * (E + 1), p + 8 * (E + 1), p + 8 * (E + 1) + 4 * P)
-        self._views = None
-        return self, (*self._ptrs, p + 4 * n if ws else None, ws)
+        self._buffer, self._c, self._views = buffer, c, None
+        return self
 
     def _view(self, i):
         if self._views is None:
-            e = self.E + 1
-            v = list(self._all[:2 * (e + self.P)].split((e, e, self.P, self.P)))
-            v[3] = v[3].view(self.T, self.k)
-            self._views = v
+            self._views = _host().views(self._buffer, self._c)
         return self._views[i]
 
+    _index = property(lambda self: self._c[0])
+    E = property(lambda self: self._c[1])
+    P = property(lambda self: self._c[2])
+    T = property(lambda self: self._c[3])
+    k = property(lambda self: self._c[4])
     offsets = property(lambda self: self._view(0))
     tiles = property(lambda self: self._view(1))
     order = property(lambda self: self._view(2))
@@ -200,58 +203,49 @@ class FP4Rows:
     per matrix; None = 1).  groups: of rows in expert order; None for a stack of matrices [G, N, K] or one [N, K].
     Checked here, once, and not changed after."""
 
-    __slots__ = ("codes", "scales", "wdtype", "g", "groups", "shape", "K", "_stack", "_index", "_ptrs")
+    __slots__ = ("codes", "scales", "wdtype", "g", "groups", "_c")
 
     def __init__(self, codes, scales, wdtype, g=None, groups=None):
         if wdtype not in FP4_BLOCK:
             raise ValueError(f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
+        self._c = _host().rows_of(codes, scales, DTYPES[wdtype], g, groups._c if isinstance(groups, ExpertGroups) else groups)
+        if self._c is None:
+            self._refuse(codes, scales, wdtype, g, groups)
+        self.codes, self.scales, self.wdtype, self.g, self.groups = codes, scales, wdtype, g, groups
+
+    @staticmethod
+    def _refuse(codes, scales, wdtype, g, groups):
         dim = 2 if groups is not None or not isinstance(codes, torch.Tensor) or codes.dim() != 3 else 3
         _typed(codes, "codes", _U8, dim)
         i = codes.get_device()
         _typed(scales, "scales", _U8, 3, i)
         K = 2 * codes.shape[-1]
-        if not (K > 0 and K % 32 == 0):
+        if K == 0 or K % 32:
             raise ValueError(f"K must be a multiple of 32, is {K}")
         if groups is not None:
             _groups_on(groups, i)
             if codes.shape[0] != groups.P:
                 raise ValueError(f"codes hold {codes.shape[0]} rows, groups {groups.P} pairs")
-            n = _grouped_tiles(groups.P, groups.E)
-            self._stack = (1, groups.P)
+            G, n = 1, (groups.P + 127 * min(groups.P, groups.E)) // 128
         else:
-            self._stack = (1, codes.shape[0]) if dim == 2 else (codes.shape[0], codes.shape[1])
-            n = self._stack[0] * -(-self._stack[1] // 128)
-        want = (n, _block_groups(wdtype, K), 512)
+            G, N = (1, codes.shape[0]) if dim == 2 else codes.shape[:2]
+            n = G * -(-N // 128)
+        want = (n, -(-K // (4 * FP4_BLOCK[wdtype])), 512)
         if tuple(scales.shape) != want:
             raise ValueError(f"scales must be {want}, is {tuple(scales.shape)}")
-        cp, sp = codes.data_ptr(), scales.data_ptr()
-        if (cp | sp) % 16:
-            raise ValueError("codes and scales must be 16-byte aligned")
-        gp, gn = _scale_ptr(g, "g", self._stack[0], i)
-        self.codes, self.scales, self.wdtype, self.g, self.groups = codes, scales, wdtype, g, groups
-        self.K, self._index, self._ptrs = K, i, (cp, sp, gp, gn)
-        self.shape = (*codes.shape[:-1], K)
+        _scale(g, "g", G, i)
+        raise ValueError("codes and scales must be 16-byte aligned")
 
     @classmethod
-    def _empty(cls, shape, wdtype, g, gp, groups, stack, like):
-        """Room for rows of `shape`, on the device of `like`; gp: pointer and count of g."""
+    def _of(cls, codes, scales, wdtype, g, groups, c):
+        """Of what the host module has allocated and described."""
         self = cls.__new__(cls)
-        K = shape[-1]
-        n = _grouped_tiles(groups.P, groups.E) if groups is not None else stack[0] * -(-stack[1] // 128)
-        self.codes = torch.empty((*shape[:-1], K // 2), dtype=_U8, device=like.device)
-        self.scales = torch.empty((n, _block_groups(wdtype, K), 512), dtype=_U8, device=like.device)
-        self.wdtype, self.g, self.groups, self.shape, self.K, self._stack = wdtype, g, groups, shape, K, stack
-        self._index = like.get_device()
-        self._ptrs = (self.codes.data_ptr(), self.scales.data_ptr(), *gp)
+        self.codes, self.scales, self.wdtype, self.g, self.groups, self._c = codes, scales, wdtype, g, groups, c
         return self
 
-
-def _block_groups(wdtype, K):
-    return -(-K // (4 * FP4_BLOCK[wdtype]))
-
-
-def _grouped_tiles(P, E):
-    return (P + 127 * min(P, E)) // 128
+    _index = property(lambda self: self._c[0])
+    K = property(lambda self: self._c[3])
+    shape = property(lambda self: (*self.codes.shape[:-1], self._c[3]))
 
 
 def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=1, renormalize=True, scale=1.0,
@@ -259,37 +253,29 @@ def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=
     """Experts and gates of each token: (topk_ids int32 [T, k], topk_w fp32 [T, k]), or with groups=True also the
     ExpertGroups of the picked pairs.  logits [T, E] fp32 or bf16; scoring "softmax" (by logit) or "sigmoid"
     (with an optional selection bias [E] and topk_group of n_group expert groups): moe_route."""
-    dt = _floats(logits, "logits", 2)
-    T, E = logits.shape
-    k, index = int(top_k), logits.get_device()
+    if stream is None:
+        r = (_host_module or _host()).route(logits, top_k, SCORING.get(scoring, -1), bias, n_group, topk_group, renormalize, scale, groups)
+        if r is not None:
+            return (r[0], r[1], ExpertGroups._of(*r[2])) if groups else r[:2]
+    _floats(logits, "logits", 2)
+    E, k, index = logits.shape[1], int(top_k), logits.get_device()
     if scoring not in SCORING:
         raise ValueError(f"scoring must be 'softmax' or 'sigmoid', is {scoring!r}")
     if not 1 <= k <= E <= 4096:
         raise ValueError(f"1 <= top_k <= E <= 4096 is needed, got top_k {k}, E {E}")
-    sc = SCORING[scoring]
-    if not (sc or (bias is None and n_group == 1)):
+    if scoring == "softmax" and (bias is not None or n_group != 1):
         raise ValueError("softmax scoring takes no bias and no expert groups")
     if bias is not None:
         _typed(bias, "bias", _F32, 1, index)
         if bias.numel() != E:
             raise ValueError(f"bias must hold E = {E} values, holds {bias.numel()}")
-    if n_group != 1 or topk_group != 1:
-        if not (1 <= n_group <= 32 and E % n_group == 0 and 1 <= topk_group <= n_group and topk_group * (E // n_group) >= k):
-            raise ValueError(f"n_group (1 to 32) must divide E and topk_group groups must hold top_k experts, got n_group {n_group}, "
-                                 f"topk_group {topk_group}, E {E}, top_k {k}")
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return route(logits, k, scoring=scoring, bias=bias, n_group=n_group, topk_group=topk_group,
-                         renormalize=renormalize, scale=scale, groups=groups)
-    ids = torch.empty((T, k), dtype=_I32, device=logits.device)
-    w = torch.empty((T, k), dtype=_F32, device=logits.device)
-    if groups:
-        gr, rest = ExpertGroups._empty(T, k, E, logits)
-    else:
-        rest = (None, None, None, None, None, 0)
-    _check(_operators().moe_route(T, E, k, dt, logits.data_ptr(), sc, None if bias is None else bias.data_ptr(), n_group,
-                                  topk_group, 1 if renormalize else 0, scale, ids.data_ptr(), w.data_ptr(), *rest, _stream(index)))
-    return (ids, w, gr) if groups else (ids, w)
+    if not (1 <= n_group <= 32 and E % n_group == 0 and 1 <= topk_group <= n_group and topk_group * (E // n_group) >= k):
+        raise ValueError(f"n_group (1 to 32) must divide E and topk_group groups must hold top_k experts, got n_group {n_group}, "
+                         f"topk_group {topk_group}, E {E}, top_k {k}")
+    if logits.shape[0] * k >= 1 << 31:
+        raise ValueError(f"{logits.shape[0]} tokens of {k} experts are more than 2^31 pairs")
+    return _again(lambda: route(logits, k, scoring=scoring, bias=bias, n_group=n_group, topk_group=topk_group, renormalize=renormalize,
+                                scale=scale, groups=groups), index, stream)
 
 
 def group_pairs(topk_ids, n_experts, *, stream=None):
@@ -299,12 +285,17 @@ def group_pairs(topk_ids, n_experts, *, stream=None):
     E, index = int(n_experts), topk_ids.get_device()
     if not (1 <= E <= 4096 and k >= 1):
         raise ValueError(f"1 <= n_experts <= 4096 and k >= 1 are needed, got {E} and {k}")
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return group_pairs(topk_ids, E)
-    gr, rest = ExpertGroups._empty(T, k, E, topk_ids)
-    _check(_operators().moe_group_pairs(T, E, k, topk_ids.data_ptr(), *rest, _stream(index)))
-    return gr
+    if stream is not None or index != torch.cuda.current_device():
+        return _again(lambda: group_pairs(topk_ids, E), index, stream)
+    ops = _operators()
+    ws, P = ops.moe_group_workspace(T, k, E), T * k
+    buffer = torch.empty(2 * (E + 1 + P) + ws // 4, dtype=_I32, device=topk_ids.device)      # the workspace last
+    off = buffer.data_ptr()
+    til = off + 4 * (E + 1)
+    order = til + 4 * (E + 1)
+    place = order + 4 * P
+    _check(ops.moe_group_pairs(T, E, k, topk_ids.data_ptr(), off, til, order, place, place + 4 * P if ws else None, ws, _stream(index)))
+    return ExpertGroups._of(buffer, (index, E, P, T, k, off, til, order, place))
 
 
 def fp4_scale(x, *, stream=None):
@@ -314,9 +305,8 @@ def fp4_scale(x, *, stream=None):
     index, n = x.get_device(), x.numel()
     if n == 0:
         raise ValueError(f"x is empty: {tuple(x.shape)}")
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return fp4_scale(x)
+    if stream is not None or index != torch.cuda.current_device():
+        return _again(lambda: fp4_scale(x), index, stream)
     G = x.shape[0] if dim == 3 else 1
     g = torch.empty(G, dtype=_F32, device=x.device)
     _check(_operators().moe_fp4_scale(G, n // G, dt, x.data_ptr(), g.data_ptr(), _stream(index)))
@@ -329,32 +319,25 @@ def quantize_fp4(x, wdtype, *, g=None, groups=None, stream=None):
     for "nvfp4" (None = 1)."""
     if wdtype not in FP4_BLOCK:
         raise ValueError(f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
+    if stream is None:
+        r = (_host_module or _host()).quantize(x, DTYPES[wdtype], g, groups._c if isinstance(groups, ExpertGroups) else groups)
+        if r is not None:
+            return FP4Rows._of(r[0], r[1], wdtype, g, groups, r[2])
     dim = 2 if groups is not None or not isinstance(x, torch.Tensor) or x.dim() != 3 else 3
-    dt = _floats(x, "x", dim)
-    index, K, xp = x.get_device(), x.shape[-1], x.data_ptr()
-    if not (K > 0 and K % 32 == 0):
+    _floats(x, "x", dim)
+    index, K = x.get_device(), x.shape[-1]
+    if K == 0 or K % 32:
         raise ValueError(f"K must be a multiple of 32, is {K}")
-    if xp % 16:
+    if x.data_ptr() % 16:
         raise ValueError("x must be 16-byte aligned")
-    if not (g is None or wdtype == "nvfp4"):
+    if g is not None and wdtype != "nvfp4":
         raise ValueError("only nvfp4 takes a matrix scale g")
     if groups is not None:
         _groups_on(groups, index)
         if groups.T != x.shape[0]:
             raise ValueError(f"x has {x.shape[0]} rows, groups hold {groups.T} tokens")
-        stack, shape = (1, groups.P), (groups.P, K)
-        off, til, _, place = groups._ptrs
-        rest = (groups.E, groups.k, off, til, place)
-    else:
-        stack = (x.shape[0], x.shape[1]) if dim == 3 else (1, x.shape[0])
-        shape, rest = tuple(x.shape), (0, 0, None, None, None)
-    gp = _scale_ptr(g, "g", stack[0], index)
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return quantize_fp4(x, wdtype, g=g, groups=groups)
-    q = FP4Rows._empty(shape, wdtype, g, gp, groups, stack, x)
-    _check(_operators().moe_quantize_fp4(*stack, K, dt, xp, DTYPES[wdtype], *gp, *rest, *q._ptrs[:2], _stream(index)))
-    return q
+    _scale(g, "g", x.shape[0] if dim == 3 else 1, index)
+    return _again(lambda: quantize_fp4(x, wdtype, g=g, groups=groups), index, stream)
 
 
 def _rows(q, name):
@@ -368,15 +351,11 @@ def dequantize_fp4(q, *, out_dtype=torch.bfloat16, stream=None):
     _rows(q, "q")
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
-    index = q._index
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return dequantize_fp4(q, out_dtype=out_dtype)
-    rest = (0, None, None) if q.groups is None else (q.groups.E, *q.groups._ptrs[:2])
-    out = torch.empty(q.shape, dtype=out_dtype, device=q.codes.device)
-    _check(_operators().moe_dequantize_fp4(*q._stack, q.K, DTYPES[q.wdtype], *q._ptrs, *rest, _FLOATS[out_dtype],
-                                           out.data_ptr(), _stream(index)))
-    return out
+    if stream is None:
+        out = _host().dequantize(q._c, None if q.groups is None else q.groups._c, q.codes.dim() == 3, _FLOATS[out_dtype])
+        if out is not None:
+            return out
+    return _again(lambda: dequantize_fp4(q, out_dtype=out_dtype), q._index, stream)
 
 
 def _columns(groups, E, N, act, out_dtype):
@@ -386,44 +365,33 @@ def _columns(groups, E, N, act, out_dtype):
         raise ValueError(f"act must be 'none' or 'swiglu', is {act!r}")
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
-    if not ACTS[act]:
-        return N
-    if N % 32:
+    if ACTS[act] and N % 32:
         raise ValueError(f"swiglu needs w rows a multiple of 32, got {N}")
-    return N // 2
+    return N // 2 if ACTS[act] else N
 
 
 def grouped_matmul(x, w, groups, *, act="none", gather=False, out_dtype=torch.bfloat16, stream=None):
     """Row i of expert e: x[i] @ w[e].T, w [E, N, K] bf16, x bf16 [P, K] in expert order, or with gather=True
     [T, K] and grouped row i reads x[order[i] // k].  act="swiglu": w holds gate rows, then up rows, and the
     result has N/2 columns.  K a multiple of 8 (moe_grouped_matmul).  Rows that no pair fills are undefined."""
+    if stream is None and isinstance(groups, ExpertGroups) and act in ACTS and out_dtype in _FLOATS:
+        out = (_host_module or _host()).matmul(x, w, groups._c, ACTS[act], gather, _FLOATS[out_dtype])
+        if out is not None:
+            return out
     _typed(w, "w", _BF16, 3)
     index = w.get_device()
     _typed(x, "x", _BF16, 2, index)
     _groups_on(groups, index)
     E, N, K = w.shape
-    cols = _columns(groups, E, N, act, out_dtype)
-    if not (N > 0 and K > 0 and K % 8 == 0):
+    _columns(groups, E, N, act, out_dtype)
+    if N == 0 or K == 0 or K % 8:
         raise ValueError(f"w must be [E, N, K] with K a multiple of 8, is {tuple(w.shape)}")
     rows = groups.T if gather else groups.P
-    if x.shape[0] != rows or x.shape[1] != K:
+    if tuple(x.shape) != (rows, K):
         raise ValueError(f"x must be {(rows, K)}, is {tuple(x.shape)}")
-    xp, wp = x.data_ptr(), w.data_ptr()
-    if (xp | wp) % 16:
+    if (x.data_ptr() | w.data_ptr()) % 16:
         raise ValueError("x and w must be 16-byte aligned")
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return grouped_matmul(x, w, groups, act=act, gather=gather, out_dtype=out_dtype)
-    off, til, order, _ = groups._ptrs
-    out = torch.empty((groups.P, cols), dtype=out_dtype, device=x.device)
-    ops, ws, n = _operators(), None, 0
-    if gather:
-        n = ops.moe_grouped_matmul_workspace(groups.P, E, K, 1)
-        if n:
-            ws = torch.empty(n, dtype=_U8, device=x.device)
-    _check(ops.moe_grouped_matmul(groups.P, E, N, K, xp, rows, order if gather else None, groups.k, wp, off, til, ACTS[act],
-                                  _FLOATS[out_dtype], out.data_ptr(), ws.data_ptr() if n else None, n, _stream(index)))
-    return out
+    return _again(lambda: grouped_matmul(x, w, groups, act=act, gather=gather, out_dtype=out_dtype), index, stream)
 
 
 def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, out_dtype=torch.bfloat16, stream=None):
@@ -432,58 +400,49 @@ def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, 
     [1] (None = 1; "nvfp4" only), rounded from the fp32 values (moe_grouped_matmul_fp4)."""
     _rows(x, "x")
     _rows(w, "w")
+    if stream is None and x.groups is not None and isinstance(groups, ExpertGroups) and act in ACTS and out_dtype in _FLOATS and \
+            w.codes.dim() == 3 and w.groups is None and (quantize or g_out is None):
+        out = (_host_module or _host()).matmul_fp4(x._c, w._c, x.groups._c, groups._c, ACTS[act], g_out if quantize else False, _FLOATS[out_dtype])
+        if out is not None:
+            return FP4Rows._of(out[0], out[1], x.wdtype, g_out, groups, out[2]) if quantize else out
     index = w._index
     _groups_on(groups, index)
-    if not (len(w.shape) == 3 and w.groups is None):
+    if w.codes.dim() != 3 or w.groups is not None:
         raise ValueError(f"w must be [E, N, K], is {w.shape}")
     E, N, K = w.shape
     cols = _columns(groups, E, N, act, out_dtype)
-    if not (x.groups is not None and x._index == index and x.groups.E == E and N > 0):
+    if x.groups is None or x._index != index or x.groups.E != E or N == 0:
         raise ValueError("x must hold rows in the order of w's experts, on the same device")
     if x.wdtype != w.wdtype:
         raise ValueError(f"x is {x.wdtype}, w is {w.wdtype}")
-    if not (x.shape == (groups.P, K)):
+    if x.shape != (groups.P, K):
         raise ValueError(f"x must be {(groups.P, K)}, is {x.shape}")
-    if not (not quantize or (ACTS[act] and cols % 32 == 0)):
+    if quantize and not (ACTS[act] and cols % 32 == 0):
         raise ValueError("quantize needs act='swiglu' and w rows a multiple of 64")
-    if not (g_out is None or (quantize and x.wdtype == "nvfp4")):
+    if g_out is not None and not (quantize and x.wdtype == "nvfp4"):
         raise ValueError("g_out goes with quantize=True and nvfp4")
-    go = _scale_ptr(g_out, "g_out", 1, index)
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return grouped_matmul_fp4(x, w, groups, act=act, quantize=quantize, g_out=g_out, out_dtype=out_dtype)
-    if quantize:
-        out = FP4Rows._empty((groups.P, cols), x.wdtype, g_out, go, groups, (1, groups.P), x.codes)
-        dst = (None, out._ptrs[0], out._ptrs[1], go[0])
-    else:
-        out = torch.empty((groups.P, cols), dtype=out_dtype, device=x.codes.device)
-        dst = (out.data_ptr(), None, None, None)
-    _check(_operators().moe_grouped_matmul_fp4(groups.P, E, N, K, DTYPES[x.wdtype], *x._ptrs[:3], *w._ptrs, *groups._ptrs[:2],
-                                               ACTS[act], _FLOATS[out_dtype], *dst, _stream(index)))
-    return out
+    _scale(g_out, "g_out", 1, index)
+    return _again(lambda: grouped_matmul_fp4(x, w, groups, act=act, quantize=quantize, g_out=g_out, out_dtype=out_dtype), index, stream)
 
 
 def combine(y, groups, topk_w, *, out_dtype=torch.float32, stream=None):
     """out[t] = sum_j topk_w[t, j] * y[place[t, j]], y [P, N] bf16 or fp32 in expert order; pairs dropped from the
     groups contribute nothing (moe_combine)."""
-    dt = _floats(y, "y", 2)
+    if stream is None and isinstance(groups, ExpertGroups) and out_dtype in _FLOATS:
+        out = (_host_module or _host()).combine(y, groups._c, topk_w, _FLOATS[out_dtype])
+        if out is not None:
+            return out
+    _floats(y, "y", 2)
     index = y.get_device()
     _groups_on(groups, index)
     _typed(topk_w, "topk_w", _F32, 2, index)
-    T, k, N = groups.T, groups.k, y.shape[1]
-    if topk_w.shape[0] != T or topk_w.shape[1] != k:
-        raise ValueError(f"topk_w must be {(T, k)}, is {tuple(topk_w.shape)}")
-    if not (y.shape[0] == groups.P and N > 0):
+    if tuple(topk_w.shape) != (groups.T, groups.k):
+        raise ValueError(f"topk_w must be {(groups.T, groups.k)}, is {tuple(topk_w.shape)}")
+    if y.shape[0] != groups.P or y.shape[1] == 0:
         raise ValueError(f"y must be [{groups.P}, N], is {tuple(y.shape)}")
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
-    if _elsewhere(index, stream):
-        with _On(index, stream):
-            return combine(y, groups, topk_w, out_dtype=out_dtype)
-    out = torch.empty((T, N), dtype=out_dtype, device=y.device)
-    _check(_operators().moe_combine(T, k, N, dt, y.data_ptr(), groups._ptrs[3], topk_w.data_ptr(), _FLOATS[out_dtype],
-                                    out.data_ptr(), _stream(index)))
-    return out
+    return _again(lambda: combine(y, groups, topk_w, out_dtype=out_dtype), index, stream)
 
 
 def check_operators(stream=None):
