@@ -23,8 +23,8 @@
 // columns, which the epilogue reads first and then lets the next tile begin.
 //
 // SwiGLU: the weight rows of a tile alternate 16 gate rows and the 16 up rows of the same
-// features (one 5-dimensional tensor map does it), so lanes l and l + 16 of a warp hold
-// gate and up of one feature, and one shuffle for two tokens brings them together.  A
+// features (one 5-dimensional tensor map does it), so the two halves of a warp's TMEM lanes
+// hold gate and up of one feature, and tcgen05.ld gives both to one thread.  A
 // 16- or 32-element block of the result is requantised after a turn through shared memory.
 //
 // Every wait is bounded; one that runs out sets the flag moe_operators_check() reads.
@@ -43,16 +43,15 @@ using namespace tc;
 
 __device__ uint32_t g_operator_err;
 
-constexpr int FIRST_SORT = 4, FIRST_EPI = 8, EPI_WARPS = 8;
-constexpr int THREADS = 32 * (FIRST_EPI + EPI_WARPS);
+constexpr int FIRST_SORT = 4, FIRST_EPI = 8, EW = 8;           // EW epilogue warps (16 lose a stage of the ring and are slower)
+constexpr int THREADS = 32 * (FIRST_EPI + EW);
 constexpr int A_BYTES = 128 * 128;             // 128 weight rows, 128 bytes of K each
 constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
 constexpr int TMEM_SCALES = 448, SCALE_SLOTS = 5;   // 12-column slots of block scales, a group of 4 blocks each, used in turn:
                                                // 4 columns of the weights' (128 rows), 8 of the tokens'
-constexpr int QUANT_STRIDE = 80;               // floats a token's 64 features take in the epilogue's buffer when requantising
-constexpr int ROW_STRIDE = 272;                // bytes a token's 128 (SwiGLU: 64) bf16 features take in it otherwise
-constexpr int EPI_BYTES = 2 * 32 * QUANT_STRIDE * 4;   // 32 tokens for each half of the epilogue
+constexpr int ROW_STRIDE = 272;                // bytes a token's 128 (SwiGLU: 64) bf16 features take in the epilogue's buffer
+constexpr int EPI_PART = 32 * ROW_STRIDE;      // 32 tokens of four epilogue warps; requantising: 64 fp32 features a token
 constexpr int SMEM_LIMIT = 227 * 1024;
 
 struct ProductArgs {
@@ -150,6 +149,32 @@ __device__ __forceinline__ void issue_slice(uint32_t d, uint32_t tmem, uint64_t 
   }
 }
 
+// h[j] = silu(gate[j] g) * up[j] g of two values; e = -g log2 e.  exp by ex2.approx and one rcp.approx for both quotients
+// (1 / a = b / (a b); the special function unit is what an epilogue of short K waits for).  Two units each, and the rounded
+// argument adds |gate g| units: far inside bf16 and 4-bit results, 2e-6 at most where fp32 ones matter (|gate g| < 32).
+// Past 2^60 the exponential stays there: silu is then below 1e-16 of the gate.
+__device__ __forceinline__ void swiglu2(uint32_t gate0, uint32_t gate1, uint32_t up0, uint32_t up1, float g, float e, float& h0, float& h1) {
+  const float a = __uint_as_float(gate0), b = __uint_as_float(gate1);
+  float x, y, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(x) : "f"(fminf(a * e, 60.0f)));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(fminf(b * e, 60.0f)));
+  x += 1.0f;
+  y += 1.0f;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x * y));
+  h0 = a * g * (r * y) * (__uint_as_float(up0) * g);
+  h1 = b * g * (r * x) * (__uint_as_float(up1) * g);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_bf16(uint32_t a, uint32_t b, float g) { return pack_bf16(__uint_as_float(a) * g, __uint_as_float(b) * g); }
+__device__ __forceinline__ void store_one(const ProductArgs& a, size_t at, float v) {
+  if (a.out_f32) static_cast<float*>(a.out)[at] = v;
+  else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+}
+
 template <int FMT, int CG>
 __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -161,7 +186,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
   const uint32_t ring = smem_u32(smem);
   uint8_t* tail = smem + (size_t)a.stages * a.stage_bytes;
   uint8_t* ebuf = tail;
-  tail += EPI_BYTES;
+  tail += EW / 4 * EPI_PART;
   const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, sfull = empty + 8 * MAX_STAGES, tfull = sfull + 8 * MAX_STAGES,
                  tempty = tfull + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 24 * MAX_STAGES + 32);
@@ -180,7 +205,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(tfull + 8 * s, 1);
-      mbar_init(tempty + 8 * s, EPI_WARPS * CG);
+      mbar_init(tempty + 8 * s, EW * CG);
     }
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -380,7 +405,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     }
   } else if (warp >= FIRST_EPI) {
     // ---------------- epilogue: a TMEM lane is a weight row, a column a token ----------------
+    // quarter of the TMEM lanes; which 32 columns of each round; a round's columns
     const int q = warp & 3, part = (warp - FIRST_EPI) >> 2;
+    constexpr int RC = 8 * EW, ROUNDS = S::NMAX / RC;
+    const int tid = (threadIdx.x - 32 * FIRST_EPI) & 127;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int it = it0; it < total; it += step) {
@@ -406,103 +434,93 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           else mbar_arrive(bar);
         }
       };
-      // 64 columns a round; the overlap of the accumulators, columns 192 on of the first and 0 to 63 of the second, first
+      const int64_t pad0 = S::FP4 && a.quant ? (int64_t)__ldg(a.tiles + o.e) * 128 + (o.row0 - __ldg(a.offsets + o.e)) : 0;
+      // The overlap of the accumulators, columns 192 on of the first and 0 to 63 of the second, first.  A thread gets, of the
+      // 16 rows of its quarter's first half (lo) and second half (hi), rows lane / 4 and 8 on, columns 2 (lane % 4) and 1 on of
+      // every 8: [4 k + 2 (row >= 8) + column].
 #pragma unroll 1
-      for (int round = 0; round < S::NMAX / 64; ++round) {
-        const int c = 32 * part + (S::OVERLAP && acc == 0 ? (round + 3) % 4 : round) * 64;
-        uint32_t v[32];
+      for (int round = 0; round < ROUNDS; ++round) {
+        const int c = 32 * part + (S::OVERLAP && acc == 0 ? ROUNDS - 1 - round : round) * RC;
+        uint32_t lo[16], hi[16];
         const bool some = c < o.n;
         if (some) {
-          tmem_ld32(tbase + c, v);
-          tmem_ld_wait();
+          tmem_ld16x4(tbase + c, lo);
+          tmem_ld16x4(tbase + (16u << 16) + c, hi);
+          tmem_ld_wait(lo, hi);
         }
-        if (S::OVERLAP ? round == 0 : (round + 1) * 64 >= o.n || round + 1 == S::NMAX / 64) {
-          if (S::OVERLAP || !released) { release(); released = true; }
-        }
+        if (S::OVERLAP ? round == 0 : !released && ((round + 1) * RC >= o.n || round + 1 == ROUNDS)) { release(); released = true; }
         if (!some) continue;
         const int left = o.n - c;
-        uint8_t* buf = ebuf + part * (EPI_BYTES / 2);
-        if (!a.act && a.wide) {
-          // bf16: 32 tokens of 128 features through shared memory, 16 bytes a thread to memory
-          named_sync(1 + part, 128);      // the last round has been read
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            *reinterpret_cast<__nv_bfloat16*>(buf + i * ROW_STRIDE + (32 * q + lane) * 2) = __float2bfloat16_rn(__uint_as_float(v[i]) * g);
-          named_sync(1 + part, 128);
-          const int t = (threadIdx.x - 32 * FIRST_EPI) & 127, f = m * 128 + (t & 15) * 8;
-#pragma unroll
-          for (int r = t >> 4; r < 32; r += 8)
-            if (r < left && f < a.cols)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c + r) * a.cols + f) =
-                  *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + (t & 15) * 16);
-          continue;
-        }
+        uint8_t* buf = ebuf + part * EPI_PART;
+        const int tok = 2 * (lane & 3), feat = lane >> 2;    // token and row of register 0
         if (!a.act) {
-          const int f = m * 128 + 32 * q + lane;
-          if (f < a.cols) {
-            const size_t at = (size_t)(o.row0 + c) * a.cols + f;
-            if (a.out_f32) {
-              float* p = static_cast<float*>(a.out) + at;
+          if (a.wide) {
+            // bf16: 32 tokens of 128 features through shared memory, transposed 8 x 8 by stmatrix, 16 bytes a thread to memory
+            named_sync(1 + part, 128);      // the last round has been read
+            const uint32_t to = smem_u32(buf) + (lane & 7) * ROW_STRIDE + (32 * q + 8 * (lane >> 3)) * 2;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < left) p[(size_t)i * a.cols] = __uint_as_float(v[i]) * g;
-            } else {
-              __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out) + at;
+            for (int k = 0; k < 4; ++k)
+              stmatrix4_trans(to + 8 * k * ROW_STRIDE, pack_bf16(lo[4 * k], lo[4 * k + 1], g), pack_bf16(lo[4 * k + 2], lo[4 * k + 3], g),
+                              pack_bf16(hi[4 * k], hi[4 * k + 1], g), pack_bf16(hi[4 * k + 2], hi[4 * k + 3], g));
+            named_sync(1 + part, 128);
+            const int f = m * 128 + (tid & 15) * 8;
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < left) p[(size_t)i * a.cols] = __float2bfloat16_rn(__uint_as_float(v[i]) * g);
+            for (int r = tid >> 4; r < 32; r += 8)
+              if (r < left && f < a.cols)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c + r) * a.cols + f) =
+                    *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + (tid & 15) * 16);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t v = i < 16 ? lo[i & 15] : hi[i & 15];
+              const int t = tok + 8 * ((i & 15) >> 2) + (i & 1), f = m * 128 + 32 * q + feat + (i & 16) + 4 * (i & 2);
+              if (t < left && f < a.cols) store_one(a, (size_t)(o.row0 + c + t) * a.cols + f, __uint_as_float(v) * g);
             }
           }
           continue;
         }
-        // lanes 0-15: gate of 16 features, lanes 16-31: up; two tokens at a time, one to each half
-        const int half = lane >> 4;
-        const int f = m * 64 + 16 * q + (lane & 15);
+        // lo: gate rows, hi: the up rows of the same 16 features
         float h[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float t0 = __uint_as_float(v[2 * i]), t1 = __uint_as_float(v[2 * i + 1]);
-          const float got = __shfl_xor_sync(0xffffffffu, half ? t0 : t1, 16);
-          const float gate = (half ? got : t0) * g, up = (half ? t1 : got) * g;
-          h[i] = __fdividef(gate, 1.0f + expf(-gate)) * up;     // token c + 2 i + half; the division is good to 2 units
-        }
+        for (int i = 0; i < 16; i += 2) swiglu2(lo[i], lo[i + 1], hi[i], hi[i + 1], g, -1.44269504f * g, h[i], h[i + 1]);
         if (a.wide) {
           named_sync(1 + part, 128);
+          // matrices: features 0-7 and 8-15 of eight tokens, then of the next eight
+          const uint32_t to = smem_u32(buf) + ((lane & 7) + 8 * (lane >> 4)) * ROW_STRIDE + (16 * q + (lane & 8)) * 2;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<__nv_bfloat16*>(buf + (2 * i + half) * ROW_STRIDE + (16 * q + (lane & 15)) * 2) = __float2bfloat16_rn(h[i]);
+          for (int k = 0; k < 4; k += 2)
+            stmatrix4_trans(to + 8 * k * ROW_STRIDE, pack_bf16(h[4 * k], h[4 * k + 1]), pack_bf16(h[4 * k + 2], h[4 * k + 3]),
+                            pack_bf16(h[4 * k + 4], h[4 * k + 5]), pack_bf16(h[4 * k + 6], h[4 * k + 7]));
           named_sync(1 + part, 128);
-          const int t = (threadIdx.x - 32 * FIRST_EPI) & 127, fw = m * 64 + (t & 7) * 8;
+          const int f = m * 64 + (tid & 7) * 8;
 #pragma unroll
-          for (int r = t >> 3; r < 32; r += 16)
-            if (r < left && fw < a.cols)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c + r) * a.cols + fw) =
-                  *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + (t & 7) * 16);
+          for (int r = tid >> 3; r < 32; r += 16)
+            if (r < left && f < a.cols)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c + r) * a.cols + f) =
+                  *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + (tid & 7) * 16);
           continue;
         }
         if (!a.quant) {
-          if (f < a.cols) {
-            const size_t at = (size_t)(o.row0 + c + half) * a.cols + f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (2 * i + half < left) {
-                if (a.out_f32) static_cast<float*>(a.out)[at + (size_t)(2 * i) * a.cols] = h[i];
-                else static_cast<__nv_bfloat16*>(a.out)[at + (size_t)(2 * i) * a.cols] = __float2bfloat16_rn(h[i]);
-              }
+          for (int i = 0; i < 16; ++i) {
+            const int t = tok + 8 * (i >> 2) + (i & 1), f = m * 64 + 16 * q + feat + 4 * (i & 2);
+            if (t < left && f < a.cols) store_one(a, (size_t)(o.row0 + c + t) * a.cols + f, h[i]);
           }
           continue;
         }
         if constexpr (S::FP4) {
+          // through shared memory so that a thread has 16 features of a token; eights of features change places by token, so
+          // that a warp writes to all banks
           float* hb = reinterpret_cast<float*>(buf);
           named_sync(1 + part, 128);      // the last round has been read
 #pragma unroll
-          for (int i = 0; i < 16; ++i) hb[(2 * i + half) * QUANT_STRIDE + 16 * q + (lane & 15)] = h[i];
+          for (int i = 0; i < 16; ++i) hb[(tok + 8 * (i >> 2) + (i & 1)) * 64 + ((16 * q + feat + 4 * (i & 2)) ^ ((lane & 3) << 3))] = h[i];
           named_sync(1 + part, 128);
-          const int t = ((threadIdx.x - 32 * FIRST_EPI) & 127) >> 2, b = threadIdx.x & 3;   // token, 16 of the 64 features
+          const int t = tid >> 2, b = tid & 3;   // token, 16 of the 64 features
           float x[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 w = *reinterpret_cast<const float4*>(hb + t * QUANT_STRIDE + 16 * b + 4 * i);
+            const float4 w = *reinterpret_cast<const float4*>(hb + t * 64 + ((16 * b + 8 * (i >> 1)) ^ (((t >> 1) & 3) << 3)) + 4 * (i & 1));
             x[4 * i] = w.x; x[4 * i + 1] = w.y; x[4 * i + 2] = w.z; x[4 * i + 3] = w.w;
           }
           uint32_t top = 0u;
@@ -510,14 +528,14 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
           if (!S::NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           float st;
-          uint32_t code = block_scale<S::NV>(top, go, rgo, st);
-          const uint2 codes = encode16<S::NV>(x, top, code, st);
+          uint32_t code = block_scale<S::NV, false>(top, go, rgo, st);
+          const uint2 codes = encode16<S::NV, false>(x, top, code, st);
           const int fb = m * 64 + 16 * b;
           const int og = (a.cols + (S::NV ? 63 : 127)) / (S::NV ? 64 : 128);
-          const size_t pad = ((size_t)__ldg(a.tiles + o.e) << 7) + (o.row0 - __ldg(a.offsets + o.e)) + c + t;
           const bool live = t < left && fb < a.cols;
           if (live) *reinterpret_cast<uint2*>(a.out_codes + (size_t)(o.row0 + c + t) * (a.cols / 2) + fb / 2) = codes;
           if (!(fb < a.cols)) code = 0u;        // blocks past the end pad their group
+          const size_t pad = (size_t)(pad0 + c + t);
           if (S::NV) {
             code |= __shfl_xor_sync(0xffffffffu, code, 1) << 8;
             code |= __shfl_xor_sync(0xffffffffu, code, 2) << 16;
@@ -588,7 +606,7 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   // SwiGLU: the 64 gate rows of a tile lie in one scale tile, the 64 up rows in one or two
   a.w_parts = !a.act ? 1 : a.cols % 64 ? 3 : 2;
   a.stage_bytes = A_BYTES + a.b_rows * 128 + (S::FP4 ? (CG + a.w_parts) * S::TILE_SCALES : 0);
-  const int fixed = 1024 + EPI_BYTES + 24 * MAX_STAGES + 48 + 512 + 4 * (a.E + 1);
+  const int fixed = 1024 + EW / 4 * EPI_PART + 24 * MAX_STAGES + 48 + 512 + 4 * (a.E + 1);
   a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 

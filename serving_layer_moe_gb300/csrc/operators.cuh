@@ -71,11 +71,18 @@ __device__ __forceinline__ float quotient(float x, float d, float r) {
 __device__ __forceinline__ bool regular(float most, float d, float r) { return d > 1e-24f && d < 1e24f && most * r < 1e30f; }
 
 // Scale code of a block and the value of one step, from the bits of its largest |x|; rg = 1 / g rounded.
-template <bool NV>
+// EXACT: as the format defines them, by correctly rounded divisions.  Otherwise (values that carry rounding errors of their
+// own) by multiplications, good to three units.
+template <bool NV, bool EXACT = true>
 __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float g, float rg, float& step) {
   if (NV) {
     if (amax_bits > 0x7f800000u) { step = 0.0f; return 0x7fu; }
     const float a = __uint_as_float(amax_bits);
+    if (!EXACT) {
+      const uint32_t code = to_e4m3(a * 0.16666667f * rg);
+      step = e4m3_value(code) * g;
+      return code;
+    }
     const bool fast = a > 1e-20f && a < 1e30f && regular(a, g, rg);
     const uint32_t code = to_e4m3(fast ? quotient(quotient(a, 6.0f, 0.16666667f), g, rg) : __fdiv_rn(__fdiv_rn(a, 6.0f), g));
     step = e4m3_value(code) * g;
@@ -90,7 +97,7 @@ __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float g, flo
 __device__ __forceinline__ float e8m0_inverse(uint32_t code) { return e8m0_value(254u - code); }
 
 // 16 values -> 8 bytes of codes
-template <bool NV>
+template <bool NV, bool EXACT = true>
 __device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t amax_bits, uint32_t code, float step) {
   if (!(step > 0.0f)) return make_uint2(0u, 0u);
   auto words = [&](auto of) {
@@ -100,7 +107,7 @@ __device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t amax_bi
     return make_uint2(w[0], w[1]);
   };
   const float r = NV ? __frcp_rn(step) : e8m0_inverse(code);
-  if (!NV) return words([&](float x) { return x * r; });
+  if (!NV || (!EXACT && r < 1e38f)) return words([&](float x) { return x * r; });
   // (comparing the codes of quotients rounded down and up first, and doing this only where they differ, is no faster where
   // the matrix scale comes from the same bf16 values: ties are common there, 259 against 240 us for 805 MB)
   if (regular(__uint_as_float(amax_bits), step, r))
