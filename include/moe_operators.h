@@ -87,8 +87,9 @@ moe_status moe_group_pairs(int32_t T, int32_t E, int32_t k, const int32_t* topk_
                            int32_t* order, int32_t* place, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
- * Matrix scales for NVFP4: g[i] = max |x_i| / (6 * 448) of each of G matrices of
- * `count` elements (x in dtype MOE_BF16 or MOE_F32); 1 for a matrix of zeros.  NaN or
+ * Matrix scales for NVFP4: g[i] = max |x_i| times the fp32 nearest to 1 / (6 * 448), of
+ * each of G matrices of `count` elements (x in dtype MOE_BF16 or MOE_F32); 1 for a matrix
+ * of zeros.  NaN or
  * infinity in a matrix gives that g.
  */
 moe_status moe_fp4_scale(int32_t G, int64_t count, int32_t dtype, const void* x, float* g, void* stream);
@@ -99,12 +100,13 @@ moe_status moe_fp4_scale(int32_t G, int64_t count, int32_t dtype, const void* x,
  *   otherwise (G = 1): x [N / k, K], N = number of pairs; row t of x becomes the rows
  *   place[t, 0 .. k - 1] (none where -1), laid out by offsets / tiles [E + 1].
  * Per block, a = max |x|:
- *   NVFP4  block scale s = e4m3(a / 6 / g), nearest even, at most 448; code = e2m1(x / (s * g)).
+ *   NVFP4  block scale s = e4m3(a * r / g), r the fp32 nearest to 1 / 6, nearest even, at most
+ *          448; code = e2m1(x / (s * g)).
  *   MXFP4  scale 2^X, X = floor(log2 a) - 2 within [-127, 127], 0 for a block of zeros;
  *          code = e2m1(x / 2^X).
  * Codes round to nearest, ties to even, and saturate at +-6 (infinities too).  A block
- * with a NaN gets the scale NaN.  Where s * g is 0 the codes are 0.  Every division is
- * a correctly rounded 32-bit one.  g: g_count = 1 or G fp32 scales, NULL = 1.
+ * with a NaN gets the scale NaN.  Where s * g is 0 the codes are 0.  Every product and
+ * division is a correctly rounded 32-bit one.  g: g_count = 1 or G fp32 scales, NULL = 1.
  */
 moe_status moe_quantize_fp4(int32_t G, int32_t N, int32_t K, int32_t dtype, const void* x, int32_t wdtype,
                             const float* g, int32_t g_count, int32_t E, int32_t k, const int32_t* offsets,

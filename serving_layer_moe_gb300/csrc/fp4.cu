@@ -230,7 +230,7 @@ __global__ void finish_scale_kernel(int G, float* g) {
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= G) return;
   const float a = g[i];
-  g[i] = a == 0.0f ? 1.0f : __fdiv_rn(a, 2688.0f);
+  g[i] = a == 0.0f ? 1.0f : a * (1.0f / 2688.0f);
 }
 
 moe_status check_fp4(int32_t G, int32_t N, int32_t K, int32_t dtype, int32_t wdtype, const float* g, int32_t g_count) {

@@ -77,14 +77,8 @@ template <bool NV, bool EXACT = true>
 __device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float g, float rg, float& step) {
   if (NV) {
     if (amax_bits > 0x7f800000u) { step = 0.0f; return 0x7fu; }
-    const float a = __uint_as_float(amax_bits);
-    if (!EXACT) {
-      const uint32_t code = to_e4m3(a * 0.16666667f * rg);
-      step = e4m3_value(code) * g;
-      return code;
-    }
-    const bool fast = a > 1e-20f && a < 1e30f && regular(a, g, rg);
-    const uint32_t code = to_e4m3(fast ? quotient(quotient(a, 6.0f, 0.16666667f), g, rg) : __fdiv_rn(__fdiv_rn(a, 6.0f), g));
+    const float a = __uint_as_float(amax_bits) * 0.16666667f;   // the fp32 nearest to 1 / 6
+    const uint32_t code = to_e4m3(!EXACT ? a * rg : a > 1e-20f && regular(a, g, rg) ? quotient(a, g, rg) : __fdiv_rn(a, g));
     step = e4m3_value(code) * g;
     return code;
   }

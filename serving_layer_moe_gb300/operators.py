@@ -299,7 +299,7 @@ def group_pairs(topk_ids, n_experts, *, stream=None):
 
 
 def fp4_scale(x, *, stream=None):
-    """NVFP4 matrix scales: max |x| / (6 * 448) of x [N, K] or of each matrix of x [G, N, K]; fp32 [1] or [G]."""
+    """NVFP4 matrix scales: max |x| times 1 / (6 * 448), of x [N, K] or of each matrix of x [G, N, K]; fp32 [1] or [G]."""
     dim = 3 if isinstance(x, torch.Tensor) and x.dim() == 3 else 2
     dt = _floats(x, "x", dim)
     index, n = x.get_device(), x.numel()

@@ -70,7 +70,7 @@ def quantize(x, wdtype, g=1.0):
         nan = np.isnan(xb).any(axis=2)
         amax = np.where(nan, np.float32(0), np.abs(np.where(np.isnan(xb), np.float32(0), xb)).max(axis=2))
         if wdtype == "nvfp4":
-            t = (amax / np.float32(6) / g).astype(np.float32)
+            t = (amax * np.float32(1 / 6) / g).astype(np.float32)
             sc = f32_to_e4m3_codes(np.minimum(t, np.float32(448)))
             step = (E4M3_TABLE[sc].astype(np.float32) * g).astype(np.float32)
             m = np.where(step[:, :, None] > 0, xb / np.where(step > 0, step, np.float32(1))[:, :, None], np.float32(0))

@@ -168,7 +168,7 @@ def test_quantize_is_the_bank_layouts_conversion(moe):
     w = (rng.standard_normal((200, 256)) * 0.02).astype(np.float32)
     packed, sc, g = _nvfp4(w)
     got = moe.fp4_scale(dev(w))
-    assert host(got)[0] == np.float32(np.abs(w).max()) / np.float32(2688)
+    assert host(got)[0] == np.abs(w).max() * np.float32(1 / 2688)
     q = moe.quantize_fp4(dev(w), "nvfp4", g=dev(np.array([g])))
     assert np.array_equal(host(q.codes), packed)
     assert np.array_equal(ref.untile(host(q.scales), np.arange(200), 16), sc)
@@ -186,7 +186,7 @@ def test_fp4_scale(moe, dtype, G, count):
     if G > 1:
         x[1, 0, count // 2] = -np.inf
     got = host(moe.fp4_scale(dev(x, dtype)))
-    want = (np.abs(x).max(axis=(1, 2)) / np.float32(2688)).astype(np.float32)
+    want = (np.abs(x).max(axis=(1, 2)) * np.float32(1 / 2688)).astype(np.float32)
     want[0] = 1
     assert np.array_equal(got, want)
 
