@@ -52,10 +52,11 @@ constexpr int TMEM_SCALES = 448, SCALE_SLOTS = 5;   // 12-column slots of block 
                                                // 4 columns of the weights' (128 rows), 8 of the tokens'
 constexpr int ROW_STRIDE = 272;                // bytes a token's 128 (SwiGLU: 64) bf16 features take in the epilogue's buffer
 constexpr int EPI_PART = 32 * ROW_STRIDE;      // 32 tokens of four epilogue warps; requantising: 64 fp32 features a token
+constexpr int SUM_SLICES = 4;                  // fp32 results: K slices summed in TMEM before they are added in registers
 constexpr int SMEM_LIMIT = 227 * 1024;
 
 struct ProductArgs {
-  int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant, wide;
+  int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant, wide, exact;
   int m_blocks, kslices, stages, stage_bytes, b_rows, w_tiles, w_parts;   // w_parts: scale tiles one weight tile's rows are in
   const float *gx, *gw, *g_out;
   const int32_t *offsets, *order;
@@ -77,6 +78,7 @@ struct Shape4 {
   // TMEM column of the second accumulator.  4-bit pairs: the two overlap in 64 columns, to leave room for the scales
   static constexpr int ACC_COLS = CG == 1 ? 128 : FP4 ? 192 : 256;
   static constexpr bool OVERLAP = FP4 && CG == 2;
+  static constexpr bool EXACT = !FP4 && CG == 1;        // has the form for fp32 results
   static constexpr int BOX = 16 * CG;                   // token rows of a small load; a tile's 128 rows take one
 };
 
@@ -173,6 +175,56 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t a, uint32_t b, float g) {
 __device__ __forceinline__ void store_one(const ProductArgs& a, size_t at, float v) {
   if (a.out_f32) static_cast<float*>(a.out)[at] = v;
   else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+}
+
+// The epilogue of fp32 results.  The tensor cores truncate what they add to an accumulator: over K = 1944 the result is 2e-6 off,
+// where fp32 additions that round leave 1e-7.  So an accumulator holds SUM_SLICES slices only (16 additions), and this adds them
+// up in registers: 64 columns a warp, with the registers of the single-CTA form's 128.  false: a wait has run out.
+__device__ __forceinline__ bool exact_tile(const ProductArgs& a, const Item& o, uint32_t tmem, uint32_t tfull, uint32_t tempty, int& acc, uint32_t& acc_phase,
+                                           volatile int* abort_flag, int q, int part) {
+  const int lane = threadIdx.x & 31;
+  float lo[2][16] = {}, hi[2][16] = {};
+  for (int k0 = 0; k0 < a.kslices; k0 += SUM_SLICES) {
+    const bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
+    if (!named_and(1 + part, 128, ok)) {
+      if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
+      return false;
+    }
+    fence_after();
+    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * 128 + 64 * part);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (64 * part + 32 * h >= o.n) continue;
+      uint32_t x[16], y[16];
+      tmem_ld16x4(tbase + 32 * h, x);
+      tmem_ld16x4(tbase + (16u << 16) + 32 * h, y);
+      tmem_ld_wait(x, y);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) { lo[h][i] += __uint_as_float(x[i]); hi[h][i] += __uint_as_float(y[i]); }
+    }
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(tempty + 8 * acc);
+    if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int t = 64 * part + 32 * h + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
+      if (t >= o.n) continue;
+      float* out = static_cast<float*>(a.out) + (size_t)(o.row0 + t) * a.cols;
+      const int f = (lane >> 2) + 4 * (i & 2);
+      if (a.act) {
+        const int c = o.mb * 64 + 16 * q + f;
+        if (c < a.cols) out[c] = lo[h][i] / (1.0f + expf(-lo[h][i])) * hi[h][i];
+      } else {
+        const int c = o.mb * 128 + 32 * q + f;
+        if (c < a.cols) out[c] = lo[h][i];
+        if (c + 16 < a.cols) out[c + 16] = hi[h][i];
+      }
+    }
+  return true;
 }
 
 template <int FMT, int CG>
@@ -274,35 +326,39 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0, slot = 0;
       bool ok = true;
+      const int sum = S::EXACT && a.exact ? SUM_SLICES : a.kslices;   // slices of an accumulator
       const uint64_t da = desc_sw128(ring), db = desc_sw128(ring + A_BYTES), ds = desc_scales(ring + A_BYTES + a.b_rows * 128);
       for (int it = it0; it < total && ok; it += step) {
         const Item o = item_at<FMT, CG>(a, first, it);
         const int ncols = columns<CG>(o.n);
-        // overlapping accumulators: the tile before this one has let go of the overlap; otherwise: the one before that is read
-        if (!warp_wait(tempty + (S::OVERLAP ? 0 : 8 * acc), S::OVERLAP ? (uint32_t)acc ^ 1u : acc_phase ^ 1u, abort_flag)) { ok = false; break; }
-        fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * S::ACC_COLS);
         // D fp32; bf16 operands, or e2m1 with e4m3 / e8m0 scales; both K-major; N; M = 128 CG
         const uint32_t idesc = ((uint32_t)(ncols >> 3) << 17) | ((uint32_t)(8 * CG) << 24) |
                                (S::FP4 ? (1u << 7) | (1u << 10) | (S::NV ? 0u : 1u << 23) : (1u << 4) | (1u << 7) | (1u << 10));
-        for (int ks = 0; ks < a.kslices; ++ks) {
-          if (!warp_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
+        for (int k0 = 0; k0 < a.kslices && ok; k0 += sum) {
+          // overlapping accumulators: the tile before this one has let go of the overlap; otherwise: the one before that is read
+          if (!warp_wait(tempty + (S::OVERLAP ? 0 : 8 * acc), S::OVERLAP ? (uint32_t)acc ^ 1u : acc_phase ^ 1u, abort_flag)) { ok = false; break; }
           fence_after();
-          const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
-          const int left = a.K - ks * S::KS;
-          if (elect_one()) {
-            if (left >= S::KS) issue_slice<FMT, CG, true>(d, tmem, da + at, db + at, ds + at, idesc, o.n > 128, ks, 0, slot);
-            else issue_slice<FMT, CG, false>(d, tmem, da + at, db + at, ds + at, idesc, o.n > 128, ks, left, slot);
-            commit<CG>(empty + 8 * stage);
+          const uint32_t d = tmem + (uint32_t)(acc * S::ACC_COLS);
+          const int k1 = min(a.kslices, k0 + sum);
+          for (int ks = k0; ks < k1; ++ks) {
+            if (!warp_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
+            fence_after();
+            const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
+            const int left = a.K - ks * S::KS;
+            if (elect_one()) {
+              if (left >= S::KS) issue_slice<FMT, CG, true>(d, tmem, da + at, db + at, ds + at, idesc, o.n > 128, ks - k0, 0, slot);
+              else issue_slice<FMT, CG, false>(d, tmem, da + at, db + at, ds + at, idesc, o.n > 128, ks - k0, left, slot);
+              commit<CG>(empty + 8 * stage);
+            }
+            __syncwarp();
+            slot = (slot + S::GS) % SCALE_SLOTS;
+            if (++stage == a.stages) { stage = 0; phase ^= 1u; }
           }
+          if (!ok) break;
+          if (elect_one()) commit<CG>(tfull + 8 * acc);
           __syncwarp();
-          slot = (slot + S::GS) % SCALE_SLOTS;
-          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+          if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
-        if (!ok) break;
-        if (elect_one()) commit<CG>(tfull + 8 * acc);
-        __syncwarp();
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
       }
       if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
     }
@@ -413,6 +469,12 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint32_t acc_phase = 0;
     for (int it = it0; it < total; it += step) {
       const Item o = item_at<FMT, CG>(a, first, it);
+      if constexpr (S::EXACT) {
+        if (a.exact) {
+          if (!exact_tile(a, o, tmem, tfull, tempty, acc, acc_phase, abort_flag, q, part)) break;
+          continue;
+        }
+      }
       const bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
       if (!named_and(1 + part, 128, ok)) {
         if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
@@ -683,12 +745,13 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   return MOE_OK;
 }
 
-// Pairs of CTAs halve what each SM reads of the tokens; single CTAs give small calls twice the units of work.
-bool use_pairs(int64_t P, int64_t E) { return P >= 64 * E; }
+// Pairs of CTAs halve what each SM reads of the tokens; single CTAs give small calls twice the units of work.  fp32 results of bf16
+// products take single CTAs (exact_tile).
+bool use_pairs(int64_t P, int64_t E, bool exact) { return !exact && P >= 64 * E; }
 
 template <int FMT>
 moe_status launch_product(const ProductArgs& a, const ProductMem& mem, cudaStream_t s) {
-  return use_pairs(a.P, a.E) ? launch_tiles<FMT, 2>(a, mem, s) : launch_tiles<FMT, 1>(a, mem, s);
+  return use_pairs(a.P, a.E, a.exact) ? launch_tiles<FMT, 2>(a, mem, s) : launch_tiles<FMT, 1>(a, mem, s);
 }
 
 // xs[i] = x[order[i] / k]: 16 bytes a thread.  A pair's token tile gathered inside the product, once for every weight
@@ -725,7 +788,8 @@ moe_status check_product(int32_t P, int32_t E, int32_t N, int32_t K, int32_t qua
 using namespace moe;
 
 extern "C" int64_t moe_grouped_matmul_workspace(int32_t P, int32_t E, int32_t K, int32_t gather) {
-  return gather && P > 0 && use_pairs(P, E) ? (int64_t)P * K * 2 : 0;
+  // many rows of an expert are gathered once, before the product
+  return gather && P > 0 && use_pairs(P, E, false) ? (int64_t)P * K * 2 : 0;
 }
 
 extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const void* x, int32_t x_rows,
@@ -740,7 +804,7 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
   if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(out, 16)) return fail(MOE_EINVAL, "x, w and out must be 16-byte aligned");
   ProductArgs a{};
   a.P = P; a.E = E; a.N = N; a.K = K; a.k = k; a.act = act; a.cols = act ? N / 2 : N; a.gather = order != nullptr;
-  a.out_f32 = out_dtype == MOE_F32; a.order = order; a.offsets = offsets; a.tiles = tiles; a.out = out;
+  a.out_f32 = a.exact = out_dtype == MOE_F32; a.order = order; a.offsets = offsets; a.tiles = tiles; a.out = out;
   const int64_t need = moe_grouped_matmul_workspace(P, E, K, a.gather);
   if (need) {
     if (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))
