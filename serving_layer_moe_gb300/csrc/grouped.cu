@@ -50,8 +50,9 @@ constexpr int MAX_STAGES = 12;
 constexpr int TMEM_COLS = 512;
 constexpr int TMEM_SCALES = 448, SCALE_SLOTS = 5;   // 12-column slots of block scales, a group of 4 blocks each, used in turn:
                                                // 4 columns of the weights' (128 rows), 8 of the tokens'
-constexpr int ROW_STRIDE = 272;                // bytes a token's 128 (SwiGLU: 64) bf16 features take in the epilogue's buffer
-constexpr int EPI_PART = 32 * ROW_STRIDE;      // 32 tokens of four epilogue warps; requantising: 64 fp32 features a token
+// An epilogue warp's buffer, 32 tokens: rows of 32 bf16 features, or 16 (SwiGLU), or 16 fp32 ones (requantising), with strides
+// that reach all banks.  A warp needs no other, so that it waits for none.
+constexpr int EPI_WARP = 32 * 80, ROW32 = 80, ROW16 = 48, ROW16F = 20 /* floats */;
 constexpr int SUM_SLICES = 4;                  // fp32 results: K slices summed in TMEM before they are added in registers
 constexpr int SMEM_LIMIT = 227 * 1024;
 
@@ -185,8 +186,7 @@ __device__ __forceinline__ bool exact_tile(const ProductArgs& a, const Item& o, 
   const int lane = threadIdx.x & 31;
   float lo[2][16] = {}, hi[2][16] = {};
   for (int k0 = 0; k0 < a.kslices; k0 += SUM_SLICES) {
-    const bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
-    if (!named_and(1 + part, 128, ok)) {
+    if (!warp_wait(tfull + 8 * acc, acc_phase, abort_flag)) {
       if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
       return false;
     }
@@ -238,7 +238,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
   const uint32_t ring = smem_u32(smem);
   uint8_t* tail = smem + (size_t)a.stages * a.stage_bytes;
   uint8_t* ebuf = tail;
-  tail += EW / 4 * EPI_PART;
+  tail += EW * EPI_WARP + 1024;   // and the block maxima of requantised MXFP4
   const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, sfull = empty + 8 * MAX_STAGES, tfull = sfull + 8 * MAX_STAGES,
                  tempty = tfull + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 24 * MAX_STAGES + 32);
@@ -464,7 +464,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     // quarter of the TMEM lanes; which 32 columns of each round; a round's columns
     const int q = warp & 3, part = (warp - FIRST_EPI) >> 2;
     constexpr int RC = 8 * EW, ROUNDS = S::NMAX / RC;
-    const int tid = (threadIdx.x - 32 * FIRST_EPI) & 127;
+    uint8_t* const buf = ebuf + (4 * part + q) * EPI_WARP;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int it = it0; it < total; it += step) {
@@ -475,8 +475,9 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           continue;
         }
       }
-      const bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
-      if (!named_and(1 + part, 128, ok)) {
+      bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
+      if (S::FP4 && !S::NV && a.quant) ok = named_and(1 + part, 128, ok);   // these four warps wait for one another below
+      if (!ok) {
         if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err, 1u); }
         break;
       }
@@ -513,24 +514,23 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         if (S::OVERLAP ? round == 0 : !released && ((round + 1) * RC >= o.n || round + 1 == ROUNDS)) { release(); released = true; }
         if (!some) continue;
         const int left = o.n - c;
-        uint8_t* buf = ebuf + part * EPI_PART;
         const int tok = 2 * (lane & 3), feat = lane >> 2;    // token and row of register 0
+        __syncwarp();                                        // the last round's buffer has been read
         if (!a.act) {
           if (a.wide) {
-            // bf16: 32 tokens of 128 features through shared memory, transposed 8 x 8 by stmatrix, 16 bytes a thread to memory
-            named_sync(1 + part, 128);      // the last round has been read
-            const uint32_t to = smem_u32(buf) + (lane & 7) * ROW_STRIDE + (32 * q + 8 * (lane >> 3)) * 2;
+            // bf16: 32 tokens of 32 features through shared memory, transposed 8 x 8 by stmatrix, 16 bytes a lane to memory
+            const uint32_t to = smem_u32(buf) + (lane & 7) * ROW32 + (lane >> 3) * 16;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              stmatrix4_trans(to + 8 * k * ROW_STRIDE, pack_bf16(lo[4 * k], lo[4 * k + 1], g), pack_bf16(lo[4 * k + 2], lo[4 * k + 3], g),
+              stmatrix4_trans(to + 8 * k * ROW32, pack_bf16(lo[4 * k], lo[4 * k + 1], g), pack_bf16(lo[4 * k + 2], lo[4 * k + 3], g),
                               pack_bf16(hi[4 * k], hi[4 * k + 1], g), pack_bf16(hi[4 * k + 2], hi[4 * k + 3], g));
-            named_sync(1 + part, 128);
-            const int f = m * 128 + (tid & 15) * 8;
+            __syncwarp();
+            const int f = m * 128 + 32 * q + (lane & 3) * 8;
 #pragma unroll
-            for (int r = tid >> 4; r < 32; r += 8)
+            for (int r = lane >> 2; r < 32; r += 8)
               if (r < left && f < a.cols)
                 *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c + r) * a.cols + f) =
-                    *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + (tid & 15) * 16);
+                    *reinterpret_cast<const uint4*>(buf + r * ROW32 + (lane & 3) * 16);
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -546,20 +546,19 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 16; i += 2) swiglu2(lo[i], lo[i + 1], hi[i], hi[i + 1], g, -1.44269504f * g, h[i], h[i + 1]);
         if (a.wide) {
-          named_sync(1 + part, 128);
           // matrices: features 0-7 and 8-15 of eight tokens, then of the next eight
-          const uint32_t to = smem_u32(buf) + ((lane & 7) + 8 * (lane >> 4)) * ROW_STRIDE + (16 * q + (lane & 8)) * 2;
+          const uint32_t to = smem_u32(buf) + ((lane & 7) + 8 * (lane >> 4)) * ROW16 + (lane & 8) * 2;
 #pragma unroll
           for (int k = 0; k < 4; k += 2)
-            stmatrix4_trans(to + 8 * k * ROW_STRIDE, pack_bf16(h[4 * k], h[4 * k + 1]), pack_bf16(h[4 * k + 2], h[4 * k + 3]),
+            stmatrix4_trans(to + 8 * k * ROW16, pack_bf16(h[4 * k], h[4 * k + 1]), pack_bf16(h[4 * k + 2], h[4 * k + 3]),
                             pack_bf16(h[4 * k + 4], h[4 * k + 5]), pack_bf16(h[4 * k + 6], h[4 * k + 7]));
-          named_sync(1 + part, 128);
-          const int f = m * 64 + (tid & 7) * 8;
+          __syncwarp();
+          const int f = m * 64 + 16 * q + (lane & 1) * 8;
 #pragma unroll
-          for (int r = tid >> 3; r < 32; r += 16)
+          for (int r = lane >> 1; r < 32; r += 16)
             if (r < left && f < a.cols)
               *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c + r) * a.cols + f) =
-                  *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + (tid & 7) * 16);
+                  *reinterpret_cast<const uint4*>(buf + r * ROW16 + (lane & 1) * 16);
           continue;
         }
         if (!a.quant) {
@@ -571,43 +570,41 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           continue;
         }
         if constexpr (S::FP4) {
-          // through shared memory so that a thread has 16 features of a token; eights of features change places by token, so
-          // that a warp writes to all banks
+          // Through shared memory, so that a lane has a token's 16 features: an NVFP4 block, or half an MXFP4 one, whose other
+          // half another warp of the four has.
           float* hb = reinterpret_cast<float*>(buf);
-          named_sync(1 + part, 128);      // the last round has been read
 #pragma unroll
-          for (int i = 0; i < 16; ++i) hb[(tok + 8 * (i >> 2) + (i & 1)) * 64 + ((16 * q + feat + 4 * (i & 2)) ^ ((lane & 3) << 3))] = h[i];
-          named_sync(1 + part, 128);
-          const int t = tid >> 2, b = tid & 3;   // token, 16 of the 64 features
+          for (int i = 0; i < 16; ++i) hb[(tok + 8 * (i >> 2) + (i & 1)) * ROW16F + feat + 4 * (i & 2)] = h[i];
+          __syncwarp();
           float x[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 w = *reinterpret_cast<const float4*>(hb + t * 64 + ((16 * b + 8 * (i >> 1)) ^ (((t >> 1) & 3) << 3)) + 4 * (i & 1));
+            const float4 w = *reinterpret_cast<const float4*>(hb + lane * ROW16F + 4 * i);
             x[4 * i] = w.x; x[4 * i + 1] = w.y; x[4 * i + 2] = w.z; x[4 * i + 3] = w.w;
           }
           uint32_t top = 0u;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-          if (!S::NV) top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          for (int i = 0; i < 16; i += 2)
+            top = __vimax3_u32(top, __float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(x[i + 1]) & 0x7fffffffu);
+          if constexpr (!S::NV) {
+            uint32_t* tops = reinterpret_cast<uint32_t*>(ebuf + EW * EPI_WARP) + part * 128;
+            tops[32 * q + lane] = top;
+            named_sync(1 + part, 128);
+            top = max(top, tops[32 * (q ^ 1) + lane]);
+            named_sync(1 + part, 128);
+          }
           float st;
           uint32_t code = block_scale<S::NV, false>(top, go, rgo, st);
           const uint2 codes = encode16<S::NV, false>(x, top, code, st);
-          const int fb = m * 64 + 16 * b;
-          const int og = (a.cols + (S::NV ? 63 : 127)) / (S::NV ? 64 : 128);
-          const bool live = t < left && fb < a.cols;
-          if (live) *reinterpret_cast<uint2*>(a.out_codes + (size_t)(o.row0 + c + t) * (a.cols / 2) + fb / 2) = codes;
-          if (!(fb < a.cols)) code = 0u;        // blocks past the end pad their group
-          const size_t pad = (size_t)(pad0 + c + t);
-          if (S::NV) {
-            code |= __shfl_xor_sync(0xffffffffu, code, 1) << 8;
-            code |= __shfl_xor_sync(0xffffffffu, code, 2) << 16;
-            if (b == 0 && live) *reinterpret_cast<uint32_t*>(a.out_scales + scale_at(pad, fb / 16, og)) = code;
-          } else {
-            code |= __shfl_xor_sync(0xffffffffu, code, 2) << 8;
-            if (b == 0 && live) {
-              uint8_t* s = a.out_scales + scale_at(pad, fb / 32, og);
-              *reinterpret_cast<uint16_t*>(s) = (uint16_t)code;
-              if (m * 64 + 64 >= a.cols && (m & 1) == 0) *reinterpret_cast<uint16_t*>(s + 2) = 0;
+          const int f = m * 64 + 16 * q, og = (a.cols + (S::NV ? 63 : 127)) / (S::NV ? 64 : 128);
+          if (lane < left) {
+            if (f < a.cols) *reinterpret_cast<uint2*>(a.out_codes + (size_t)(o.row0 + c + lane) * (a.cols / 2) + f / 2) = codes;
+            // blocks past the end pad their group
+            const int block = S::NV ? f / 16 : f / 32;
+            if (block < 4 * og && (S::NV || !(q & 1))) {
+              uint8_t* s = a.out_scales + scale_at((size_t)(pad0 + c + lane), block, og);
+              *s = (uint8_t)(f < a.cols ? code : 0u);
+              if (!S::NV && f + 64 >= a.cols && !(m & 1)) s[2] = 0;      // the group's second half has no tile of its own
             }
           }
         }
@@ -668,7 +665,7 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   // SwiGLU: the 64 gate rows of a tile lie in one scale tile, the 64 up rows in one or two
   a.w_parts = !a.act ? 1 : a.cols % 64 ? 3 : 2;
   a.stage_bytes = A_BYTES + a.b_rows * 128 + (S::FP4 ? (CG + a.w_parts) * S::TILE_SCALES : 0);
-  const int fixed = 1024 + EW / 4 * EPI_PART + 24 * MAX_STAGES + 48 + 512 + 4 * (a.E + 1);
+  const int fixed = 1024 + EW * EPI_WARP + 1024 + 24 * MAX_STAGES + 48 + 512 + 4 * (a.E + 1);
   a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 
