@@ -120,8 +120,8 @@ moe_status moe_dequantize_fp4(int32_t G, int32_t N, int32_t K, int32_t wdtype, c
 
 /*
  * Products grouped by expert: out[i] = x_row(i) * w[e]^T for the rows i of each expert e.
- *   w [E, N, K] bf16; x [P, K] bf16 in expert order, or, with `order` given, [rows, K]
- *   and grouped row i reads row order[i] / k.  K a multiple of 8.
+ *   w [E, N, K] bf16; x [P, K] bf16 in expert order, or, with `order` and `place` given,
+ *   [P / k, K] and grouped row i reads row order[i] / k.  K a multiple of 8.
  *   act 1: SwiGLU; w holds N/2 gate rows, then N/2 up rows (N a multiple of 32);
  *   out[i] = silu(gate) * up, N/2 columns.
  *   out [P, N or N/2] in out_dtype (MOE_BF16 or MOE_F32); rows from offsets[E] on are
@@ -131,7 +131,7 @@ moe_status moe_dequantize_fp4(int32_t G, int32_t N, int32_t K, int32_t wdtype, c
  */
 int64_t moe_grouped_matmul_workspace(int32_t P, int32_t E, int32_t K, int32_t gather);
 moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const void* x, int32_t x_rows, const int32_t* order,
-                              int32_t k, const void* w, const int32_t* offsets, const int32_t* tiles, int32_t act,
+                              const int32_t* place, int32_t k, const void* w, const int32_t* offsets, const int32_t* tiles, int32_t act,
                               int32_t out_dtype, void* out, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*

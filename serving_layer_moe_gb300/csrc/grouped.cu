@@ -79,7 +79,7 @@ struct Shape4 {
   // TMEM column of the second accumulator.  4-bit pairs: the two overlap in 64 columns, to leave room for the scales
   static constexpr int ACC_COLS = CG == 1 ? 128 : FP4 ? 192 : 256;
   static constexpr bool OVERLAP = FP4 && CG == 2;
-  static constexpr bool EXACT = !FP4 && CG == 1;        // has the form for fp32 results
+  static constexpr bool EXACT = !FP4 && CG == 1;        // has the forms for fp32 results and for gathered rows
   static constexpr int BOX = 16 * CG;                   // token rows of a small load; a tile's 128 rows take one
 };
 
@@ -116,7 +116,7 @@ template <int FMT, int CG>
 __device__ __forceinline__ int token_rows(const ProductArgs& a, const Item& o) {
   using S = Shape4<FMT, CG>;
   const int mine = columns<CG>(o.n) / CG;
-  if (a.gather) return mine;
+  if (S::EXACT && a.gather) return (o.n + 3) & ~3;   // single CTAs; the columns past the rows are not used
   return a.b_rows == 128 && mine > 3 * S::BOX ? 128 : (mine + S::BOX - 1) / S::BOX * S::BOX;
 }
 
@@ -369,11 +369,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     bool ok = true;
     for (int it = it0; it < total && ok; it += step) {
       const Item o = item_at<FMT, CG>(a, first, it);
-      const int mine = columns<CG>(o.n) / CG, row0 = o.row0 + (int)rank * mine, rows = token_rows<FMT, CG>(a, o);
-      if (!S::FP4 && a.gather) {
-        const int last = o.row0 + o.n - 1;   // past the end: the last again
+      const int row0 = o.row0 + (int)rank * (columns<CG>(o.n) / CG), rows = token_rows<FMT, CG>(a, o);
+      if (S::EXACT && a.gather) {
         __syncwarp();
-        for (int r = lane; r < mine; r += 32) gathered[r] = __ldg(a.order + min(row0 + r, last)) / a.k;
+        for (int r = lane; r < rows; r += 32) gathered[r] = __ldg(a.order + row0 + min(r, o.n - 1)) / a.k;
         __syncwarp();
       }
       for (int ks = 0; ks < a.kslices; ++ks) {
@@ -381,10 +380,10 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const uint32_t sb = ring + stage * a.stage_bytes + A_BYTES;
         const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
         const int x = ks * (S::FP4 ? 128 : 64);
-        if (!S::FP4 && a.gather) {
+        if (S::EXACT && a.gather) {
           if (elect_one()) {
 #pragma unroll 4
-            for (int r = 0; r < mine; r += 4)
+            for (int r = 0; r < rows; r += 4)
               tma_gather4<CG>(&tmX, bar, sb + 128 * r, x, *reinterpret_cast<const int4*>(gathered + r));
           }
         } else if (elect_one()) {
@@ -475,6 +474,11 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           continue;
         }
       }
+      // what the tile needs from memory, on its way while the products run
+      float g = 1.0f;
+      if (S::FP4) g = (a.gx ? __ldg(a.gx) : 1.0f) * (a.gw ? __ldg(a.gw + (a.gw_count > 1 ? o.e : 0)) : 1.0f);
+      const float go = S::NV && a.quant && a.g_out ? __ldg(a.g_out) : 1.0f, rgo = __frcp_rn(go);
+      const int64_t pad0 = S::FP4 && a.quant ? (int64_t)__ldg(a.tiles + o.e) * 128 + (o.row0 - __ldg(a.offsets + o.e)) : 0;
       bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
       if (S::FP4 && !S::NV && a.quant) ok = named_and(1 + part, 128, ok);   // these four warps wait for one another below
       if (!ok) {
@@ -483,9 +487,6 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       }
       fence_after();
       const int m = o.mb * CG + (int)rank;
-      float g = 1.0f;
-      if (S::FP4) g = (a.gx ? __ldg(a.gx) : 1.0f) * (a.gw ? __ldg(a.gw + (a.gw_count > 1 ? o.e : 0)) : 1.0f);
-      const float go = S::NV && a.quant && a.g_out ? __ldg(a.g_out) : 1.0f, rgo = __frcp_rn(go);
       const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * S::ACC_COLS);
       bool released = false;
       auto release = [&]() {   // the accumulator (or the part the next one needs) has been read
@@ -497,7 +498,6 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           else mbar_arrive(bar);
         }
       };
-      const int64_t pad0 = S::FP4 && a.quant ? (int64_t)__ldg(a.tiles + o.e) * 128 + (o.row0 - __ldg(a.offsets + o.e)) : 0;
       // The overlap of the accumulators, columns 192 on of the first and 0 to 63 of the second, first.  A thread gets, of the
       // 16 rows of its quarter's first half (lo) and second half (hi), rows lane / 4 and 8 on, columns 2 (lane % 4) and 1 on of
       // every 8: [4 k + 2 (row >= 8) + column].
@@ -751,25 +751,34 @@ moe_status launch_product(const ProductArgs& a, const ProductMem& mem, cudaStrea
   return use_pairs(a.P, a.E, a.exact) ? launch_tiles<FMT, 2>(a, mem, s) : launch_tiles<FMT, 1>(a, mem, s);
 }
 
-// xs[i] = x[order[i] / k]: 16 bytes a thread.  A pair's token tile gathered inside the product, once for every weight
-// block, costs more than this pass: 8192 tokens, 8 of 128 experts, K 2048, N 1536 take 343 us from rows in order and
-// 950 (TMA gather) or 700 us (cp.async) by index.
-__global__ void __launch_bounds__(256)
-gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ order, int P, int row16, int k, uint4* __restrict__ xs) {
+// xs[place[t, j]] = x[t]: a row is read once and stored k times, two 16-byte units a lane of a warp's segment.  A pair's token
+// tile gathered inside the product, once for every weight block, costs more than this pass: 8192 tokens, 8 of 128 experts, K 2048,
+// N 1536 take 277 us from rows in order, 820 gathered by TMA and 710 by cp.async.
+constexpr int GATHER_THREADS = 256, GATHER_SEG = 64;
+__global__ void __launch_bounds__(GATHER_THREADS)
+gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ place, int T, int row16, int k, uint4* __restrict__ xs) {
   pdl_wait();
   pdl_trigger();
-  const int64_t units = (int64_t)P * row16;
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-    const int i = (int)(u / row16), c = (int)(u - (int64_t)i * row16);
-    const int p = __ldg(order + i);
-    if (p >= 0) xs[u] = __ldg(x + (size_t)(p / k) * row16 + c);
+  const int lane = threadIdx.x & 31, c = blockIdx.y * GATHER_SEG + lane;
+  for (int t = blockIdx.x * (GATHER_THREADS / 32) + (threadIdx.x >> 5); t < T; t += gridDim.x * (GATHER_THREADS / 32)) {
+    uint4 v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (c + 32 * h < row16) v[h] = __ldg(x + (size_t)t * row16 + c + 32 * h);
+    for (int j = 0; j < k; ++j) {
+      const int row = __ldg(place + (size_t)t * k + j);
+      if (row < 0) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (c + 32 * h < row16) xs[(size_t)row * row16 + c + 32 * h] = v[h];
+    }
   }
 }
 
 moe_status check_product(int32_t P, int32_t E, int32_t N, int32_t K, int32_t quantum, const int32_t* offsets,
                          const int32_t* tiles, int32_t act, int32_t out_dtype) {
   if (P < 0 || E < 1 || E > kMaxExperts || N < 1) return fail(MOE_EINVAL, "P >= 0, 1 <= E <= %d and N >= 1 are needed, got P %d, E %d, N %d", kMaxExperts, P, E, N);
-  if (K < 1 || K % quantum) return fail(MOE_EINVAL, "K = %d is not a multiple of %d", K, quantum);
+  if (K < 1 || K > 1 << 24 || K % quantum) return fail(MOE_EINVAL, "K = %d is not a multiple of %d", K, quantum);
   if (act != 0 && act != 1) return fail(MOE_EINVAL, "act must be 0 (none) or 1 (SwiGLU)");
   if (act == 1 && N % 32) return fail(MOE_EINVAL, "SwiGLU needs N a multiple of 32, got %d", N);
   if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return fail(MOE_EINVAL, "out_dtype must be MOE_F32 or MOE_BF16");
@@ -790,14 +799,15 @@ extern "C" int64_t moe_grouped_matmul_workspace(int32_t P, int32_t E, int32_t K,
 }
 
 extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const void* x, int32_t x_rows,
-                                         const int32_t* order, int32_t k, const void* w, const int32_t* offsets,
+                                         const int32_t* order, const int32_t* place, int32_t k, const void* w, const int32_t* offsets,
                                          const int32_t* tiles, int32_t act, int32_t out_dtype, void* out, void* workspace,
                                          int64_t workspace_bytes, void* stream) {
   moe_status st = check_product(P, E, N, K, 8, offsets, tiles, act, out_dtype);
   if (st != MOE_OK) return st;
-  if (order && (k < 1 || !aligned_to(order, 4))) return fail(MOE_EINVAL, "order needs k >= 1 and 4-byte alignment");
+  if (order && (!place || k < 1 || P % k || !aligned_to(order, 4) || !aligned_to(place, 4)))
+    return fail(MOE_EINVAL, "order needs place, k >= 1 that divides P, and 4-byte alignment");
   if (P == 0) return MOE_OK;
-  if (!x || !w || !out || x_rows < (order ? 1 : P)) return fail(MOE_EINVAL, "x, w and out must not be NULL and x must hold its rows");
+  if (!x || !w || !out || x_rows < (order ? P / k : P)) return fail(MOE_EINVAL, "x, w and out must not be NULL and x must hold its rows");
   if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(out, 16)) return fail(MOE_EINVAL, "x, w and out must be 16-byte aligned");
   ProductArgs a{};
   a.P = P; a.E = E; a.N = N; a.K = K; a.k = k; a.act = act; a.cols = act ? N / 2 : N; a.gather = order != nullptr;
@@ -806,9 +816,9 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
   if (need) {
     if (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))
       return fail(MOE_EINVAL, "workspace must hold %lld bytes, 16-byte aligned, holds %lld", (long long)need, (long long)workspace_bytes);
-    const int64_t units = (int64_t)P * (K / 8);
-    const int grid = (int)std::min<int64_t>((units + 255) / 256, (int64_t)operator_sms() * 16);
-    CK(launch_pdl(gather_kernel, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), order, P, K / 8, k,
+    const int T = P / k, warps = GATHER_THREADS / 32, segs = (K / 8 + GATHER_SEG - 1) / GATHER_SEG;
+    const dim3 grid(std::min((T + warps - 1) / warps, std::max(1, operator_sms() * 64 / segs)), segs);
+    CK(launch_pdl(gather_kernel, grid, dim3(GATHER_THREADS), 0, static_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), place, T, K / 8, k,
                   static_cast<uint4*>(workspace)));
     a.gather = 0;
     x = workspace;

@@ -264,7 +264,7 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t wb = moe_grouped_matmul_workspace((int32_t)g.P, (int32_t)E, (int32_t)K, gather);
   if (wb) ws = empty({wb}, ScalarType::Byte, g.index);
   const moe_status st = moe_grouped_matmul((int32_t)g.P, (int32_t)E, (int32_t)N, (int32_t)K, x->data_ptr(), (int32_t)rows, gather ? ptr<int32_t>(g.order) : nullptr,
-                                           (int32_t)g.k, w->data_ptr(), ptr<int32_t>(g.offsets), ptr<int32_t>(g.tiles), (int32_t)act, (int32_t)od, out.data_ptr(),
+                                           gather ? ptr<int32_t>(g.place) : nullptr, (int32_t)g.k, w->data_ptr(), ptr<int32_t>(g.offsets), ptr<int32_t>(g.tiles), (int32_t)act, (int32_t)od, out.data_ptr(),
                                            wb ? ws.data_ptr() : nullptr, wb, s);
   if (st != MOE_OK) return raise(st);
   return THPVariable_Wrap(out);

@@ -140,40 +140,52 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int logits_bf16,
         live |= 1u << (who / sub);
         if (lane == (int)who) gkey = 0u;
       }
+      const float per = 1.0f / (float)gs;
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
         const int e = i * 32 + lane;
-        if (e < a.E && !((live >> (e / gs)) & 1u)) key[i] = 0u;
+        // e / gs: e < 4096 and half a unit away from the next quotient
+        if (e < a.E && !((live >> (int)(((float)e + 0.5f) * per)) & 1u)) key[i] = 0u;
       }
       __syncwarp();
     }
   }
 
-  // the k picks; lane j % 32 keeps pick j's id, its weight term goes to w
-  float sum = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) m = max(m, key[i]);
-    const uint32_t best = __reduce_max_sync(0xffffffffu, m);
-    uint32_t at = 0xffffffffu;
+  // The k picks: the warp's largest key and the lowest index that has it.  A lane keeps its own largest and looks for the next
+  // only when it has lost it.  Lane j % 32 keeps pick j.
+  uint32_t m = 0u, at_m = 0u;
+  auto rescan = [&]() {
+    m = 0u;
 #pragma unroll
     for (int i = NPL - 1; i >= 0; --i)
-      if (key[i] == best) at = (uint32_t)(i * 32 + lane);
-    at = __reduce_min_sync(0xffffffffu, at);
-    float term = 0.0f;
+      if (key[i] >= m) { m = key[i]; at_m = (uint32_t)(i * 32 + lane); }
+  };
+  rescan();
+  float sum = 0.0f;
+  for (int j0 = 0; j0 < a.k; j0 += 32) {
+    const int nj = min(32, a.k - j0);
+    uint32_t my_at = 0u;
+    float my_v = 0.0f;
+    for (int j = 0; j < nj; ++j) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, m);
+      const uint32_t at = __reduce_min_sync(0xffffffffu, m == best ? at_m : 0xffffffffu);
+      float val = 0.0f;
+      if (at == at_m && m == best) {   // the lane that has it
 #pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (at == (uint32_t)(i * 32 + lane)) {
-        key[i] = 0u;
-        term = a.scoring == 0 ? softmax_term(v[i], top) : v[i];
+        for (int i = 0; i < NPL; ++i)
+          if (at == (uint32_t)(i * 32 + lane)) { key[i] = 0u; val = v[i]; }
+        rescan();
       }
-    term = __shfl_sync(0xffffffffu, term, (int)(at & 31u));
-    sum += term;
-    if (lane == 0) {
-      a.ids[(size_t)t * a.k + j] = (int32_t)at;
-      a.w[(size_t)t * a.k + j] = term;
+      val = __shfl_sync(0xffffffffu, val, (int)(at & 31u));
+      if (lane == j) { my_at = at; my_v = val; }
     }
+    float term = 0.0f;
+    if (lane < nj) {
+      term = a.scoring == 0 ? softmax_term(my_v, top) : my_v;
+      a.ids[(size_t)t * a.k + j0 + lane] = (int32_t)my_at;
+      a.w[(size_t)t * a.k + j0 + lane] = term;
+    }
+    sum += warp_sum(term);
   }
   if (a.renorm) denom = sum;
   __syncwarp();

@@ -67,7 +67,7 @@ def _operators():
             "moe_quantize_fp4": [I32, I32, I32, I32, P, I32, P, I32, I32, I32, P, P, P, P, P, P],
             "moe_dequantize_fp4": [I32, I32, I32, I32, P, P, P, I32, I32, P, P, I32, P, P],
             "moe_grouped_matmul_workspace": [I32, I32, I32, I32],
-            "moe_grouped_matmul": [I32, I32, I32, I32, P, I32, P, I32, P, P, P, I32, I32, P, P, I64, P],
+            "moe_grouped_matmul": [I32, I32, I32, I32, P, I32, P, P, I32, P, P, P, I32, I32, P, P, I64, P],
             "moe_grouped_matmul_fp4": [I32, I32, I32, I32, I32, P, P, P, P, P, P, I32, P, P, I32, I32, P, P, P, P, P],
             "moe_combine": [I32, I32, I32, I32, P, P, P, I32, P, P],
             "moe_operators_check": [P],

@@ -104,15 +104,15 @@ def test_dequantize_refuses(lib, args, word):
     refused(lib, lib.moe_dequantize_fp4(*args, None), word)
 
 
-def matmul(lib, P_=8, E=2, N=64, K=64, x=A, rows=8, order=None, k=2, w=B, off=C, til=D, act=0, od=BF16, out=F, ws=None, n=0):
-    return lib.moe_grouped_matmul(P_, E, N, K, x, rows, order, k, w, off, til, act, od, out, ws, n, None)
+def matmul(lib, P_=8, E=2, N=64, K=64, x=A, rows=8, order=None, place=None, k=2, w=B, off=C, til=D, act=0, od=BF16, out=F, ws=None, n=0):
+    return lib.moe_grouped_matmul(P_, E, N, K, x, rows, order, place, k, w, off, til, act, od, out, ws, n, None)
 
 
 @pytest.mark.parametrize("kw,word", [
     (dict(P_=-1), b"P >= 0"), (dict(E=0), b"E"), (dict(E=4097), b"4096"), (dict(N=0), b"N"), (dict(K=12), b"multiple of 8"), (dict(act=2), b"act"),
     (dict(act=1, N=48), b"multiple of 32"), (dict(od=3), b"out_dtype"), (dict(off=None), b"offsets"), (dict(x=None), b"NULL"),
-    (dict(x=P(0x10008)), b"16-byte"), (dict(w=P(0x10002)), b"16-byte"), (dict(order=G, k=0), b"order"), (dict(rows=0), b"rows"), (dict(rows=7), b"rows"),
-    (dict(P_=128, rows=64, order=G), b"workspace"), (dict(P_=128, rows=64, order=G, ws=P(0x10008), n=1 << 20), b"workspace")])
+    (dict(x=P(0x10008)), b"16-byte"), (dict(w=P(0x10002)), b"16-byte"), (dict(order=G, place=H, k=0), b"order"), (dict(order=G), b"place"), (dict(order=G, place=H, k=3), b"divides"), (dict(rows=0), b"rows"), (dict(rows=7), b"rows"),
+    (dict(P_=128, rows=64, order=G, place=H), b"workspace"), (dict(P_=128, rows=64, order=G, place=H, ws=P(0x10008), n=1 << 20), b"workspace")])
 def test_grouped_matmul_refuses(lib, kw, word):
     refused(lib, matmul(lib, **kw), word)
 
