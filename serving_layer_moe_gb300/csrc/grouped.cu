@@ -66,7 +66,8 @@ struct ProductArgs {
   const int32_t* tiles;
 };
 
-struct Item { int e, row0, n, mb, tile; };   // expert, first grouped row, rows, weight block, scale tile of row0
+// expert, first grouped row, rows, weight block, scale tile of row0; tt: token tile, of all experts
+struct Item { int e, row0, n, mb, tile, tt; };
 
 template <int FMT, int CG>
 struct Shape4 {
@@ -83,12 +84,14 @@ struct Shape4 {
   static constexpr int BOX = 16 * CG;                   // token rows of a small load; a tile's 128 rows take one
 };
 
+// item `it` into o, which holds the one before (tt = -1: none)
 template <int FMT, int CG>
-__device__ __forceinline__ Item item_at(const ProductArgs& a, const int32_t* first, int it) {
+__device__ __forceinline__ void item_at(const ProductArgs& a, const int32_t* first, int it, Item& o) {
   using S = Shape4<FMT, CG>;
-  Item o;
   const int tt = it / a.m_blocks;
   o.mb = it - tt * a.m_blocks;
+  if (tt == o.tt) return;
+  o.tt = tt;
   int lo = 0, hi = a.E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -106,7 +109,6 @@ __device__ __forceinline__ Item item_at(const ProductArgs& a, const int32_t* fir
   o.row0 = r0 + j * chunk;
   o.n = min(chunk, n - j * chunk);
   o.tile = S::FP4 ? __ldg(a.tiles + lo) + j * CG : 0;
-  return o;
 }
 
 // token columns of a tile, and the rows of them that one CTA loads
@@ -286,15 +288,21 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
   fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = first[a.E] * a.m_blocks;
-  const int step = gridDim.x / CG, it0 = blockIdx.x / CG;
+  // Pairs take every so many-th item, which mixes long and short tiles.  Single CTAs, whose items cost their weights, take a run
+  // of them: mostly weight blocks of one token tile.
+  const int units = gridDim.x / CG, unit = blockIdx.x / CG, share = total / units, more = total % units;
+  const int step = CG == 2 ? units : 1, it0 = CG == 2 ? unit : unit * share + min(unit, more);
+  const int it1 = CG == 2 ? total : it0 + share + (unit < more);
+  Item o;
+  o.tt = -1;
 
   if (warp == 0) {
     // ---------------- loads ----------------
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int it = it0; it < total && ok; it += step) {
-      const Item o = item_at<FMT, CG>(a, first, it);
+    for (int it = it0; it < it1 && ok; it += step) {
+      item_at<FMT, CG>(a, first, it, o);
       const int m = o.mb * CG + (int)rank;      // 128-row weight tile (64 gate + 64 up with SwiGLU)
       const uint32_t bytes = (uint32_t)CG * (A_BYTES + 128u * token_rows<FMT, CG>(a, o) + (S::FP4 ? (uint32_t)S::TILE_SCALES * (CG + (a.act ? 0 : 1)) : 0u));
       for (int ks = 0; ks < a.kslices; ++ks) {
@@ -328,8 +336,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       bool ok = true;
       const int sum = S::EXACT && a.exact ? SUM_SLICES : a.kslices;   // slices of an accumulator
       const uint64_t da = desc_sw128(ring), db = desc_sw128(ring + A_BYTES), ds = desc_scales(ring + A_BYTES + a.b_rows * 128);
-      for (int it = it0; it < total && ok; it += step) {
-        const Item o = item_at<FMT, CG>(a, first, it);
+      for (int it = it0; it < it1 && ok; it += step) {
+        item_at<FMT, CG>(a, first, it, o);
         const int ncols = columns<CG>(o.n);
         // D fp32; bf16 operands, or e2m1 with e4m3 / e8m0 scales; both K-major; N; M = 128 CG
         const uint32_t idesc = ((uint32_t)(ncols >> 3) << 17) | ((uint32_t)(8 * CG) << 24) |
@@ -367,8 +375,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int it = it0; it < total && ok; it += step) {
-      const Item o = item_at<FMT, CG>(a, first, it);
+    for (int it = it0; it < it1 && ok; it += step) {
+      item_at<FMT, CG>(a, first, it, o);
       const int row0 = o.row0 + (int)rank * (columns<CG>(o.n) / CG), rows = token_rows<FMT, CG>(a, o);
       if (S::EXACT && a.gather) {
         __syncwarp();
@@ -400,8 +408,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int it = it0; it < total && ok; it += step) {
-      const Item o = item_at<FMT, CG>(a, first, it);
+    for (int it = it0; it < it1 && ok; it += step) {
+      item_at<FMT, CG>(a, first, it, o);
       const int m = o.mb * CG + (int)rank;
       const int wt = o.e * a.w_tiles + (a.act ? m >> 1 : m), ut = o.e * a.w_tiles + ((a.cols + 64 * m) >> 7);
       for (int ks = 0; ks < a.kslices; ++ks) {
@@ -429,8 +437,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int it = it0; it < total && ok; it += step) {
-        const Item o = item_at<FMT, CG>(a, first, it);
+      for (int it = it0; it < it1 && ok; it += step) {
+        item_at<FMT, CG>(a, first, it, o);
         const int m = o.mb * CG + (int)rank;
         uint32_t src[4];   // where the scales of row lane + 32 j of the weight tile are
 #pragma unroll
@@ -466,8 +474,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint8_t* const buf = ebuf + (4 * part + q) * EPI_WARP;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int it = it0; it < total; it += step) {
-      const Item o = item_at<FMT, CG>(a, first, it);
+    for (int it = it0; it < it1; it += step) {
+      item_at<FMT, CG>(a, first, it, o);
       if constexpr (S::EXACT) {
         if (a.exact) {
           if (!exact_tile(a, o, tmem, tfull, tempty, acc, acc_phase, abort_flag, q, part)) break;
