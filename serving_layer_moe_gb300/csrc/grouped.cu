@@ -709,6 +709,7 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
 
   // at most every token tile the rows can make, on every weight block
   const int64_t most = (a.P + (int64_t)(S::NMAX - 1) * std::min(a.P, a.E)) / S::NMAX * a.m_blocks;
+  if (most > 0x7fffffff) return fail(MOE_EINVAL, "P = %d rows of N = %d columns are too many tiles", a.P, a.N);
   static bool allowed[64] = {};   // the kernel's shared memory, once per device
   int dev = 0;
   CK(cudaGetDevice(&dev));
@@ -785,7 +786,8 @@ gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ place, in
 
 moe_status check_product(int32_t P, int32_t E, int32_t N, int32_t K, int32_t quantum, const int32_t* offsets,
                          const int32_t* tiles, int32_t act, int32_t out_dtype) {
-  if (P < 0 || E < 1 || E > kMaxExperts || N < 1) return fail(MOE_EINVAL, "P >= 0, 1 <= E <= %d and N >= 1 are needed, got P %d, E %d, N %d", kMaxExperts, P, E, N);
+  if (P < 0 || P > kMaxPairs || E < 1 || E > kMaxExperts || N < 1)
+    return fail(MOE_EINVAL, "P >= 0 (at most %lld), 1 <= E <= %d and N >= 1 are needed, got P %d, E %d, N %d", (long long)kMaxPairs, kMaxExperts, P, E, N);
   if (K < 1 || K > 1 << 24 || K % quantum) return fail(MOE_EINVAL, "K = %d is not a multiple of %d", K, quantum);
   if (act != 0 && act != 1) return fail(MOE_EINVAL, "act must be 0 (none) or 1 (SwiGLU)");
   if (act == 1 && N % 32) return fail(MOE_EINVAL, "SwiGLU needs N a multiple of 32, got %d", N);

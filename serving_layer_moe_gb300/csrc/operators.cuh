@@ -6,6 +6,8 @@
 
 namespace moe {
 
+constexpr int64_t kMaxPairs = 0x70000000;   // T * k: row numbers, and those a block past them, fit 31 bits
+
 // SMs of the current device (looked up once per device).
 int operator_sms();
 

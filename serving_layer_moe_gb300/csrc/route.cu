@@ -197,26 +197,32 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int logits_bf16,
   }
 }
 
-// exclusive prefixes over E + 1 bins: of the counts into `first` (and `offsets`), of ceil(count / 128) into `tiles`; one warp.
-// Bin E, the dropped pairs, comes last, so first[E] is the number of rows.
+// Exclusive prefixes over the E + 1 bins of `count` by a block of 256 threads: of the counts into `first` (and `offsets`), of
+// ceil(count / 128) into `tiles`.  A thread adds up a run of bins, the threads' sums are scanned by shuffles.  Bin E, the
+// dropped pairs, comes last, so first[E] is the number of rows.
 __device__ __forceinline__ void scan_bins(const int32_t* count, int E, int32_t* first, int32_t* offsets, int32_t* tiles) {
-  const int lane = threadIdx.x & 31;
-  int run = 0, trun = 0;
-  for (int b = 0; b <= E; b += 32) {
-    const int e = b + lane;
-    const int c = e <= E ? count[e] : 0;
-    const int tl = (c + 127) >> 7;
-    int x = c, y = tl;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-      if (lane >= o) { x += u; y += v; }
-    }
-    if (e <= E) {
-      first[e] = run + x - c;
-      if (offsets) { offsets[e] = run + x - c; tiles[e] = trun + y - tl; }
-    }
-    run += __shfl_sync(0xffffffffu, x, 31);
-    trun += __shfl_sync(0xffffffffu, y, 31);
+  __shared__ int2 warps[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (E + 1 + 255) / 256, e0 = threadIdx.x * per, e1 = min(E + 1, e0 + per);
+  int c = 0, t = 0;
+  for (int e = e0; e < e1; ++e) { c += count[e]; t += (count[e] + 127) >> 7; }
+  int x = c, y = t;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) { x += u; y += v; }
+  }
+  if (lane == 31) warps[warp] = make_int2(x, y);
+  __syncthreads();
+  x -= c;
+  y -= t;
+#pragma unroll
+  for (int w = 0; w < 8; ++w)
+    if (w < warp) { x += warps[w].x; y += warps[w].y; }
+  for (int e = e0; e < e1; ++e) {
+    first[e] = x;
+    if (offsets) { offsets[e] = x; tiles[e] = y; }
+    x += count[e];
+    y += (count[e] + 127) >> 7;
   }
 }
 
@@ -243,7 +249,7 @@ __device__ __forceinline__ void group_small(const int32_t* ids, int P, int E, in
     order[row] = mine < E ? p : -1;
     place[p] = mine < E ? row : -1;
   }
-  if (threadIdx.x < 32) scan_bins(count, E, first, offsets, tiles);
+  scan_bins(count, E, first, offsets, tiles);
 }
 
 template <int NPL>
@@ -299,21 +305,24 @@ __global__ void __launch_bounds__(256) starts_kernel(int32_t* __restrict__ count
   const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (e > E) return;
   int32_t* row = counts + (size_t)e * blocks;
-  constexpr int MOST = kMaxBlocks / 32;
-  int c[MOST];
-#pragma unroll
-  for (int i = 0; i < MOST; ++i) c[i] = i * 32 + lane < blocks ? row[i * 32 + lane] : 0;
+  // 32 blocks a step: loads and scans of eight steps do not wait for one another
   int run = 0;
+  for (int b0 = 0; b0 < blocks; b0 += 256) {
+    int c[8], x[8];
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) {
-    if (i * 32 >= blocks) break;
-    int x = c[i];
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += u;
+    for (int i = 0; i < 8; ++i) c[i] = x[i] = b0 + 32 * i + lane < blocks ? row[b0 + 32 * i + lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int u = __shfl_up_sync(0xffffffffu, x[i], o);
+        if (lane >= o) x[i] += u;
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (b0 + 32 * i + lane < blocks) row[b0 + 32 * i + lane] = run + x[i] - c[i];
+      run += __shfl_sync(0xffffffffu, x[i], 31);
     }
-    if (i * 32 + lane < blocks) row[i * 32 + lane] = run + x - c[i];
-    run += __shfl_sync(0xffffffffu, x, 31);
   }
   if (lane == 0) total[e] = run;
 }
@@ -337,7 +346,7 @@ place_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int p
   int32_t* mine = cnt + warp * bins;
   for (int e = threadIdx.x; e < bins; e += PLACE_THREADS) total[e] = totals[e];
   __syncthreads();
-  if (warp == 0) scan_bins(total, E, start, blockIdx.x == 0 ? offsets : nullptr, tiles);
+  scan_bins(total, E, start, blockIdx.x == 0 ? offsets : nullptr, tiles);
   for (int p = s0; p < s1; p += 32) {
     const int q = p + lane;
     int e = q < s1 ? __ldg(ids + q) : -2;
@@ -447,7 +456,7 @@ moe_status check_group_args(int32_t T, int32_t E, int32_t k, const void* offsets
 
 moe_status check_sizes(int32_t T, int32_t E, int32_t k) {
   if (T < 0 || E < 1 || E > kMaxExperts || k < 1) return fail(MOE_EINVAL, "T >= 0, 1 <= E <= %d and k >= 1 are needed, got T %d, E %d, k %d", kMaxExperts, T, E, k);
-  if ((int64_t)T * k > 0x7fffff00ll) return fail(MOE_EINVAL, "T * k = %lld pairs do not fit 31 bits", (long long)T * k);
+  if ((int64_t)T * k > kMaxPairs) return fail(MOE_EINVAL, "T * k = %lld pairs do not fit 31 bits with room for a block", (long long)T * k);
   return MOE_OK;
 }
 
@@ -569,8 +578,8 @@ extern "C" moe_status moe_group_pairs(int32_t T, int32_t E, int32_t k, const int
 
 extern "C" moe_status moe_combine(int32_t T, int32_t k, int32_t N, int32_t y_dtype, const void* y, const int32_t* place,
                                   const float* w, int32_t out_dtype, void* out, void* stream) {
-  if (T < 0 || k < 1 || N < 1 || (int64_t)T * k > 0x7fffff00ll)
-    return fail(MOE_EINVAL, "T >= 0, k >= 1, N >= 1 and at most 2^31 pairs are needed, got T %d, k %d, N %d", T, k, N);
+  if (T < 0 || k < 1 || N < 1 || (int64_t)T * k > kMaxPairs)
+    return fail(MOE_EINVAL, "T >= 0, k >= 1, N >= 1 and at most %lld pairs are needed, got T %d, k %d, N %d", (long long)kMaxPairs, T, k, N);
   if ((y_dtype != MOE_F32 && y_dtype != MOE_BF16) || (out_dtype != MOE_F32 && out_dtype != MOE_BF16))
     return fail(MOE_EINVAL, "y_dtype and out_dtype must be MOE_F32 or MOE_BF16");
   if (T == 0) return MOE_OK;

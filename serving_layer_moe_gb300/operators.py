@@ -272,8 +272,8 @@ def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=
     if not (1 <= n_group <= 32 and E % n_group == 0 and 1 <= topk_group <= n_group and topk_group * (E // n_group) >= k):
         raise ValueError(f"n_group (1 to 32) must divide E and topk_group groups must hold top_k experts, got n_group {n_group}, "
                          f"topk_group {topk_group}, E {E}, top_k {k}")
-    if logits.shape[0] * k >= 1 << 31:
-        raise ValueError(f"{logits.shape[0]} tokens of {k} experts are more than 2^31 pairs")
+    if logits.shape[0] * k > 0x70000000:
+        raise ValueError(f"{logits.shape[0]} tokens of {k} experts are more pairs than row numbers")
     return _again(lambda: route(logits, k, scoring=scoring, bias=bias, n_group=n_group, topk_group=topk_group, renormalize=renormalize,
                                 scale=scale, groups=groups), index, stream)
 

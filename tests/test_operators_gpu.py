@@ -481,3 +481,14 @@ def test_binding_refusals(moe, small_layer):
     ]:
         with pytest.raises(ValueError, match=word):
             call()
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_example_layer(fmt):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import routed_layer
+    r = routed_layer.run(tokens=300, hidden=512, inter=256, experts=16, top_k=4, fmt=fmt)
+    # a 4-bit value is up to 1/6 of its block's largest off; three of them multiply up to a result
+    assert 0.01 < r["distance"] < 0.4, r
