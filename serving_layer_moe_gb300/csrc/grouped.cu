@@ -57,7 +57,7 @@ constexpr int SUM_SLICES = 4;                  // fp32 results: K slices summed 
 constexpr int SMEM_LIMIT = 227 * 1024;
 
 struct ProductArgs {
-  int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant, wide, exact;
+  int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant, wide, exact, few;
   int m_blocks, kslices, stages, stage_bytes, b_rows, w_tiles, w_parts;   // w_parts: scale tiles one weight tile's rows are in
   const float *gx, *gw, *g_out;
   const int32_t *offsets, *order;
@@ -288,11 +288,13 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
   fence_after();
   const uint32_t tmem = *tmem_slot;
   const int total = first[a.E] * a.m_blocks;
-  // Pairs take every so many-th item, which mixes long and short tiles.  Single CTAs, whose items cost their weights, take a run
-  // of them: mostly weight blocks of one token tile.
+  // Every so many-th item, which mixes long and short tiles and lets neighbours share a token tile.  With few rows an expert, when
+  // an item costs its weights: a run of items, mostly weight blocks of one token tile (16 tokens, K 768: 17.7 -> 15.2 us; with
+  // 512 rows an expert runs read the weights again for every token tile, 500 -> 1090 us).
   const int units = gridDim.x / CG, unit = blockIdx.x / CG, share = total / units, more = total % units;
-  const int step = CG == 2 ? units : 1, it0 = CG == 2 ? unit : unit * share + min(unit, more);
-  const int it1 = CG == 2 ? total : it0 + share + (unit < more);
+  const bool runs = CG == 1 && a.few;
+  const int step = runs ? 1 : units, it0 = runs ? unit * share + min(unit, more) : unit;
+  const int it1 = runs ? it0 + share + (unit < more) : total;
   Item o;
   o.tt = -1;
 
@@ -753,10 +755,12 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
 
 // Pairs of CTAs halve what each SM reads of the tokens; single CTAs give small calls twice the units of work.  fp32 results of bf16
 // products take single CTAs (exact_tile).
-bool use_pairs(int64_t P, int64_t E, bool exact) { return !exact && P >= 64 * E; }
+bool few_rows(int64_t P, int64_t E) { return P < 64 * E; }
+bool use_pairs(int64_t P, int64_t E, bool exact) { return !exact && !few_rows(P, E); }
 
 template <int FMT>
-moe_status launch_product(const ProductArgs& a, const ProductMem& mem, cudaStream_t s) {
+moe_status launch_product(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
+  a.few = few_rows(a.P, a.E);
   return use_pairs(a.P, a.E, a.exact) ? launch_tiles<FMT, 2>(a, mem, s) : launch_tiles<FMT, 1>(a, mem, s);
 }
 

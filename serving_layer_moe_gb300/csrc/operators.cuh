@@ -33,11 +33,11 @@ __host__ __device__ __forceinline__ size_t scale_at(size_t r, int b, int block_g
   return ((r >> 7) * (size_t)block_groups + (size_t)(b >> 2)) * 512 + (t & 31) * 16 + (t >> 5) * 4 + (b & 3);
 }
 
+// value of an e4m3 code, exact in fp16
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
-  const uint32_t e = (code >> 3) & 15u, m = code & 7u;
-  if ((code & 127u) == 127u) return __uint_as_float(0x7fffffffu);
-  const float v = e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : (float)m * 0.001953125f;
-  return (code & 128u) ? -v : v;
+  uint32_t h;
+  asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(h) : "r"(code));
+  return __low2float(*reinterpret_cast<const __half2*>(&h));
 }
 // 2^(code - 127); 255 is NaN.  Code 0 is the subnormal 2^-127.
 __device__ __forceinline__ float e8m0_value(uint32_t code) {
@@ -102,7 +102,10 @@ __device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t amax_bi
     for (int i = 0; i < 8; ++i) w[i >> 2] |= to_e2m1x2(of(v[2 * i]), of(v[2 * i + 1])) << (8 * (i & 3));
     return make_uint2(w[0], w[1]);
   };
-  const float r = NV ? __frcp_rn(step) : e8m0_inverse(code);
+  float r;
+  if (!NV) r = e8m0_inverse(code);
+  else if (EXACT) r = __frcp_rn(step);
+  else asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(step));
   if (!NV || (!EXACT && r < 1e38f)) return words([&](float x) { return x * r; });
   // (comparing the codes of quotients rounded down and up first, and doing this only where they differ, is no faster where
   // the matrix scale comes from the same bf16 values: ties are common there, 259 against 240 us for 805 MB)
