@@ -753,15 +753,17 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   return MOE_OK;
 }
 
-// Pairs of CTAs halve what each SM reads of the tokens; single CTAs give small calls twice the units of work.  fp32 results of bf16
-// products take single CTAs (exact_tile).
-bool few_rows(int64_t P, int64_t E) { return P < 64 * E; }
-bool use_pairs(int64_t P, int64_t E, bool exact) { return !exact && !few_rows(P, E); }
+// Pairs of CTAs load half of the tokens each and fewer, larger slices; single CTAs start sooner and have twice the units of work.
+// us of gate/up (K 2048, N 1536, 128 experts), single and in pairs, by rows an expert: bf16 1 row 75.9 / 73.7, 4 rows 114.3 / 109.1,
+// 64 rows 178.9 / 138.4; rows gathered (before the product for pairs, in it otherwise) 1 row 75.9 / 80.2, 4 rows 119.0 / 118.6,
+// 16 rows 249.7 / 136.0; NVFP4 4 rows 38.0 / 40.1, 64 rows 49.1 / 50.4, 128 rows 66.8 / 56.2 (K 7168, N 4096, 64 rows 32.7 / 28.5).
+// fp32 results of bf16 products take single CTAs (exact_tile).
+bool use_pairs(int64_t P, int64_t E, bool fp4, bool exact) { return !exact && P >= (fp4 ? 64 : 4) * E; }
 
 template <int FMT>
 moe_status launch_product(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
-  a.few = few_rows(a.P, a.E);
-  return use_pairs(a.P, a.E, a.exact) ? launch_tiles<FMT, 2>(a, mem, s) : launch_tiles<FMT, 1>(a, mem, s);
+  a.few = a.P < 64 * (int64_t)a.E;
+  return use_pairs(a.P, a.E, FMT != MOE_BF16, a.exact) ? launch_tiles<FMT, 2>(a, mem, s) : launch_tiles<FMT, 1>(a, mem, s);
 }
 
 // xs[place[t, j]] = x[t]: a row is read once and stored k times, two 16-byte units a lane of a warp's segment.  A pair's token
@@ -809,7 +811,7 @@ using namespace moe;
 
 extern "C" int64_t moe_grouped_matmul_workspace(int32_t P, int32_t E, int32_t K, int32_t gather) {
   // many rows of an expert are gathered once, before the product
-  return gather && P > 0 && use_pairs(P, E, false) ? (int64_t)P * K * 2 : 0;
+  return gather && P > 0 && use_pairs(P, E, false, false) ? (int64_t)P * K * 2 : 0;
 }
 
 extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const void* x, int32_t x_rows,
