@@ -69,6 +69,16 @@ bool here(int64_t index, void** stream) {
 at::Tensor empty(at::IntArrayRef shape, ScalarType type, int64_t index) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)index));
 }
+// `bytes` of memory for several tensors of one call: an allocation costs more than the tensors on it
+at::Tensor room(int64_t bytes, int64_t index) { return empty({bytes}, ScalarType::Byte, index); }
+// a contiguous tensor at byte `at` of b's memory, without as_strided's way through the dispatcher (2 us)
+at::Tensor on(const at::Tensor& b, int64_t at, at::IntArrayRef shape, ScalarType type) {
+  const auto meta = c10::scalarTypeToTypeMeta(type);
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(b.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), meta);
+  t.unsafeGetTensorImpl()->set_storage_offset(at / (int64_t)meta.itemsize());
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
 PyObject* raise(moe_status st) {
   PyObject* r = PyObject_CallFunction(g_raise, "i", (int)st);
   Py_XDECREF(r);
@@ -91,6 +101,16 @@ int64_t block_of(int64_t wdtype) { return wdtype == MOE_NVFP4 ? 16 : 32; }
 int64_t block_groups(int64_t wdtype, int64_t K) { return (K + 4 * block_of(wdtype) - 1) / (4 * block_of(wdtype)); }
 int64_t row_tiles(const Rows& r, const Groups* g) {
   return g ? moe_grouped_tiles(g->P, (int32_t)g->E) : r.G * ((r.N + 127) / 128);
+}
+
+// room for the rows r describes
+void make_rows(Rows& r, const Groups* g, bool stacked, at::Tensor& codes, at::Tensor& scales) {
+  const int64_t cb = (r.G * r.N * (r.K / 2) + 15) / 16 * 16, tiles = row_tiles(r, g), groups = block_groups(r.wdtype, r.K);
+  const at::Tensor b = room(cb + tiles * groups * 512, r.index);
+  codes = stacked ? on(b, 0, {r.G, r.N, r.K / 2}, ScalarType::Byte) : on(b, 0, {r.N, r.K / 2}, ScalarType::Byte);
+  scales = on(b, cb, {tiles, groups, 512}, ScalarType::Byte);
+  r.codes = address(b);
+  r.scales = r.codes + cb;
 }
 
 #define OTHERWISE Py_RETURN_NONE
@@ -170,22 +190,16 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bias = typed(a[3], ScalarType::Float, 1, index);
     if (!bias || bias->numel() != E) OTHERWISE;
   }
-  at::Tensor ids = empty({T, k}, ScalarType::Int, index), w = empty({T, k}, ScalarType::Float, index), buf;
+  // ids, gates, and with groups their four arrays and the workspace
+  const int64_t pairs = 4 * T * k, bins = 4 * (E + 1), wb = group ? moe_group_workspace((int32_t)T, (int32_t)k, (int32_t)E) : 0;
+  const at::Tensor buf = room(2 * pairs + (group ? 2 * bins + 2 * pairs + wb : 0), index);
+  const at::Tensor ids = on(buf, 0, {T, k}, ScalarType::Int), w = on(buf, pairs, {T, k}, ScalarType::Float);
+  const int64_t base = address(buf);
   Groups g{};
-  void* ws = nullptr;
-  int64_t wb = 0;
-  if (group) {
-    wb = moe_group_workspace((int32_t)T, (int32_t)k, (int32_t)E);
-    const int64_t words = 2 * (E + 1) + 2 * T * k;
-    buf = empty({words + wb / 4}, ScalarType::Int, index);
-    g = Groups{index, E, T * k, T, k, address(buf), 0, 0, 0};
-    g.tiles = g.offsets + 4 * (E + 1);
-    g.order = g.tiles + 4 * (E + 1);
-    g.place = g.order + 4 * T * k;
-    if (wb) ws = ptr<void>(g.offsets + 4 * words);
-  }
+  if (group) g = Groups{index, E, T * k, T, k, base + 2 * pairs, base + 2 * pairs + bins, base + 2 * pairs + 2 * bins, base + 3 * pairs + 2 * bins};
+  void* ws = wb ? ptr<void>(base + 4 * pairs + 2 * bins) : nullptr;
   const moe_status st = moe_route((int32_t)T, (int32_t)E, (int32_t)k, dt, x->data_ptr(), (int32_t)sc, bias ? bias->data_ptr<float>() : nullptr, (int32_t)ng,
-                                  (int32_t)tg, renorm, (float)scale, ids.data_ptr<int32_t>(), w.data_ptr<float>(), ptr<int32_t>(g.offsets), ptr<int32_t>(g.tiles),
+                                  (int32_t)tg, renorm, (float)scale, ptr<int32_t>(base), ptr<float>(base + pairs), ptr<int32_t>(g.offsets), ptr<int32_t>(g.tiles),
                                   ptr<int32_t>(g.order), ptr<int32_t>(g.place), ws, wb, s);
   if (st != MOE_OK) return raise(st);
   PyObject* third = Py_None;
@@ -216,10 +230,8 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (dt < 0 || r.K <= 0 || r.K % 32 || (grouped && x->size(0) != gr.T) || !aligned(x->data_ptr(), 16) || (a[2] != Py_None && r.wdtype != MOE_NVFP4) ||
       !fits(r.N) || !scale_of(a[2], r.G, r.index, &r.g, &r.g_count) || !here(r.index, &s))
     OTHERWISE;
-  at::Tensor codes = dim == 3 ? empty({r.G, r.N, r.K / 2}, ScalarType::Byte, r.index) : empty({r.N, r.K / 2}, ScalarType::Byte, r.index);
-  at::Tensor scales = empty({row_tiles(r, grouped ? &gr : nullptr), block_groups(r.wdtype, r.K), 512}, ScalarType::Byte, r.index);
-  r.codes = address(codes);
-  r.scales = address(scales);
+  at::Tensor codes, scales;
+  make_rows(r, grouped ? &gr : nullptr, dim == 3, codes, scales);
   const moe_status st =
       moe_quantize_fp4((int32_t)r.G, (int32_t)r.N, (int32_t)r.K, dt, x->data_ptr(), (int32_t)r.wdtype, ptr<float>(r.g), (int32_t)r.g_count, (int32_t)gr.E,
                        (int32_t)gr.k, ptr<int32_t>(gr.offsets), ptr<int32_t>(gr.tiles), ptr<int32_t>(gr.place), ptr<uint8_t>(r.codes), ptr<uint8_t>(r.scales), s);
@@ -288,10 +300,7 @@ PyObject* matmul_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Rows r{w.index, 1, g.P, cols, w.wdtype, 0, 0, 0, 0};
   if (quant) {
     if ((a[5] != Py_None && w.wdtype != MOE_NVFP4) || !scale_of(a[5], 1, w.index, &r.g, &r.g_count)) OTHERWISE;
-    codes = empty({g.P, cols / 2}, ScalarType::Byte, w.index);
-    scales = empty({row_tiles(r, &g), block_groups(w.wdtype, cols), 512}, ScalarType::Byte, w.index);
-    r.codes = address(codes);
-    r.scales = address(scales);
+    make_rows(r, &g, false, codes, scales);
   } else {
     out = empty({g.P, cols}, float_type(od), w.index);
   }
@@ -324,23 +333,16 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CATCH
 }
 
-// views(buffer, groups) -> (offsets, tiles, order, place) of a buffer that route() allocated
+// views(buffer, groups) -> (offsets, tiles, order, place) of the buffer that holds them
 PyObject* views(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
   Groups g{};
   if (n != 2 || !nine(a[1], &g)) OTHERWISE;
-  const at::Tensor* b = typed(a[0], ScalarType::Int, 1, g.index);
+  const at::Tensor* b = tensor(a[0], 1, g.index);
   if (!b) OTHERWISE;
-  // tensors of the buffer's storage, without as_strided's way through the dispatcher (2 us each)
-  int64_t at0 = b->storage_offset();
-  auto part = [&](at::IntArrayRef shape, int64_t n) {
-    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(b->storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA), b->dtype());
-    t.unsafeGetTensorImpl()->set_storage_offset(at0);
-    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-    at0 += n;
-    return THPVariable_Wrap(t);
-  };
-  PyObject *off = part({g.E + 1}, g.E + 1), *til = part({g.E + 1}, g.E + 1), *order = part({g.P}, g.P), *place = part({g.T, g.k}, g.P);
+  const int64_t base = (int64_t)(uintptr_t)b->storage().data();
+  auto part = [&](int64_t p, at::IntArrayRef shape) { return THPVariable_Wrap(on(*b, p - base, shape, ScalarType::Int)); };
+  PyObject *off = part(g.offsets, {g.E + 1}), *til = part(g.tiles, {g.E + 1}), *order = part(g.order, {g.P}), *place = part(g.place, {g.T, g.k});
   return Py_BuildValue("(NNNN)", off, til, order, place);
   CATCH
 }
