@@ -2,23 +2,23 @@
 // sum of the experts' rows (include/moe_operators.h: moe_route, moe_group_pairs,
 // moe_combine).
 //
-// Router: one warp per token.  A lane holds E / 32 scores in registers as order-
-// preserving integers; each of the k picks is a warp-wide integer maximum and then
-// a minimum over the indices that hold it, so equal scores go to the lower index
-// and the result is the same on every run.
+// Router: one warp per token.  A lane holds E / 32 neighbouring scores in registers as
+// order-preserving integers, and its two best; each of the k picks is a warp-wide integer
+// maximum, and the lowest lane that holds it gives it up, so equal scores go to the lower
+// index and the result is the same on every run.
 //
 // Grouping is a stable counting sort of the T*k pairs by expert in three launches: the
-// router's blocks count the pairs they have just picked per expert, one warp per expert
-// turns the counts of all blocks into starts, and blocks rank their own pairs, 32 at a
-// time by match.  Ranks follow the pair index, so no atomic decides an order.  Calls of at
-// most 256 pairs do all of it, router included, in one block, where a pair counts the
-// pairs before it in expert order.
+// router's blocks count the pairs they pick per expert, those counts become starts, and
+// blocks rank their own pairs, 32 at a time by match.  Ranks follow the pair index, so no
+// atomic decides an order.  Calls of at most 256 pairs do all of it, router included, in
+// one block, where a pair counts the pairs before it in expert order.
 //
 // Bounds: a prompt chunk of 8192 tokens and 256 experts reads 8.4 MB of logits; one
 // decoded token is one launch's latency.
 #include "operators.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 
@@ -28,34 +28,30 @@ constexpr int ROUTE_THREADS = 256;          // 8 warps, a token each at a time
 constexpr int ROUTE_WARPS = ROUTE_THREADS / 32;
 constexpr int PLACE_THREADS = 256;          // 8 warps rank a segment of pairs each
 constexpr int PLACE_WARPS = PLACE_THREADS / 32;
-constexpr int kMaxBlocks = 1024;            // counting blocks: what one warp adds up per expert
+constexpr int kMaxBlocks = 1024;            // counting blocks
 constexpr int kSmallPairs = 256;            // up to here one block routes and groups
 
 struct RouteArgs {
-  int T, E, k, scoring, n_group, topk_group, renorm, tokens_per_block;
+  int T, E, k, scoring, n_group, topk_group, renorm, tokens_per_block, bf16;
   float scale;
   const void* logits;
   const float* bias;
   int32_t* ids;
   float* w;
   int32_t *offsets, *tiles, *order, *place;   // NULL: no grouping
-  int32_t* counts;                            // [E + 1, blocks] pairs of each block of each expert; row E: dropped ones
+  int32_t* counts;                            // [blocks, E + 1] pairs of each block of each expert; bin E: dropped ones
 };
 
 // larger float <=> larger integer; -0 and +0 are one value; NaN is below -inf
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 1u;
   const uint32_t b = __float_as_uint(x + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
@@ -66,135 +62,197 @@ __device__ __forceinline__ float softmax_term(float l, float top) {
   if (!(l > -INFINITY)) return 0.0f;
   return expf(fminf(l, 3.402823466e38f) - top);
 }
-__device__ __forceinline__ float sigmoid_of(float l) { return l != l ? 0.0f : 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-template <int NPL>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int logits_bf16, int t, float* group_scratch) {
-  const int lane = threadIdx.x & 31;
-  float v[NPL];
-  uint32_t key[NPL];
+// a row's logit e
+__device__ __forceinline__ float logit_at(const RouteArgs& a, size_t at) {
+  return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
+}
+
+// Routes token t; lane j % 32 hands pick j to `found(j, expert)`.  FULL: NPL experts to every lane, on addresses that hold
+// logits and bias four (or two) at a time.  scratch [E + E / 32 + 1]: the warp's, where not FULL or the groups are not whole lanes.
+template <int NPL, bool FULL, typename F>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int t, float* scratch, F found) {
+  constexpr int U = NPL >= 4 ? 4 : 2;
+  const int lane = threadIdx.x & 31, per = FULL ? NPL : (a.E + 31) / 32, e0 = lane * per;
+  const size_t row = (size_t)t * a.E;
+  auto has = [&](int i) { return FULL || (i < per && e0 + i < a.E); };
+  alignas(16) float v[NPL];
+  if constexpr (FULL) {
+    if (a.bf16) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.logits) + row + e0;
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = i * 32 + lane;
-    const size_t at = (size_t)t * a.E + e;
-    v[i] = e >= a.E ? -INFINITY
-           : logits_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.logits)[at])
-                         : static_cast<const float*>(a.logits)[at];
-  }
-  float top = -INFINITY, denom = 0.0f;
-  if (a.scoring == 0) {
+      for (int i = 0; i < NPL; i += U) {
+        alignas(8) __nv_bfloat16 x[U];
+        if constexpr (U == 4) *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(src + i);
+        else *reinterpret_cast<uint32_t*>(x) = *reinterpret_cast<const uint32_t*>(src + i);
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      key[i] = i * 32 + lane < a.E ? order_key(v[i]) : 0u;
-      top = fmaxf(top, v[i]);   // fmaxf passes NaN over
-    }
-    top = fminf(warp_max(top), 3.402823466e38f);
-    if (!a.renorm) {
+        for (int u = 0; u < U; ++u) v[i + u] = __bfloat162float(x[u]);
+      }
+    } else {
+      const float* src = static_cast<const float*>(a.logits) + row + e0;
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) denom += softmax_term(v[i], top);
-      denom = warp_sum(denom);
+      for (int i = 0; i < NPL; i += U) {
+        if constexpr (U == 4) *reinterpret_cast<float4*>(v + i) = *reinterpret_cast<const float4*>(src + i);
+        else *reinterpret_cast<float2*>(v + i) = *reinterpret_cast<const float2*>(src + i);
+      }
     }
   } else {
+    for (int e = lane; e < a.E; e += 32) scratch[e + (e >> 5)] = logit_at(a, row + e);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = has(i) ? scratch[e0 + i + ((e0 + i) >> 5)] : 0.0f;
+    __syncwarp();
+  }
+
+  uint32_t key[NPL];   // 0: no expert, or one that may not be picked
+  if (a.scoring != 0) {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = sigmoid_of(v[i]);
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < NPL; i += U) {
+        alignas(16) float b[U];
+        if constexpr (!FULL) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) b[u] = has(i + u) ? __ldg(a.bias + e0 + i + u) : 0.0f;
+        } else if constexpr (U == 4) {
+          *reinterpret_cast<float4*>(b) = __ldg(reinterpret_cast<const float4*>(a.bias + e0 + i));
+        } else {
+          *reinterpret_cast<float2*>(b) = __ldg(reinterpret_cast<const float2*>(a.bias + e0 + i));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[i + u] += b[u];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) key[i] = has(i) ? order_key(v[i]) : 0u;
+
+  // a group is a power of two of whole lanes: its two best come from the lanes' own two best, below
+  const bool lanes = a.n_group > 1 && a.E == 32 * per && !(a.n_group & (a.n_group - 1));
+  // score of a group: the sum of its two best; a NaN (key 1) or an absent second value adds nothing, a group of NaN ranks last
+  auto live_groups = [&](int sub, uint32_t b1, uint32_t b2) {
+    for (int o = 1; o < sub; o <<= 1) {
+      const uint32_t c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
+      b2 = max(min(b1, c1), max(b2, c2));
+      b1 = max(b1, c1);
+    }
+    uint32_t gkey = 0u, live = 0u;
+    if (lane / sub < a.n_group && lane % sub == 0)
+      gkey = b1 <= 1u ? 1u : order_key(b2 <= 1u ? key_value(b1) : key_value(b1) + key_value(b2));
+    for (int r = 0; r < a.topk_group; ++r) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, gkey);
+      const int who = __ffs(__ballot_sync(0xffffffffu, gkey == best)) - 1;
+      live |= 1u << (who / sub);
+      if (lane == who) gkey = 0u;
+    }
+    return live;
+  };
+  if (a.n_group > 1 && !lanes) {
+    // a power of two of lanes looks through each group
+    const int gs = a.E / a.n_group;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)
+      if (has(i)) scratch[e0 + i + ((e0 + i) >> 5)] = __uint_as_float(key[i]);
+    __syncwarp();
+    int sub = 1;
+    while (2 * sub * a.n_group <= 32) sub *= 2;
+    const int g = lane / sub;
+    uint32_t b1 = 0u, b2 = 0u;
+    if (g < a.n_group)
+      for (int i = lane % sub; i < gs; i += sub) {
+        const int e = g * gs + i;
+        const uint32_t x = __float_as_uint(scratch[e + (e >> 5)]);
+        b2 = max(min(b1, x), b2);
+        b1 = max(b1, x);
+      }
+    const uint32_t live = live_groups(sub, b1, b2);
+    const float step = 1.0f / (float)gs;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i)   // e / gs: e < 4096 and half a unit away from the next quotient
+      if (!((live >> (min((int)(((float)(e0 + i) + 0.5f) * step), 31))) & 1u)) key[i] = 0u;
+    __syncwarp();
+  }
+
+  // A lane keeps its two best, m1 at i1 and m2 at i2 (the lower index where they are equal), of its experts that come after
+  // (last, at_last) in that order: what it has lost needs no mark, and it looks through its keys again only after two losses.
+  uint32_t m1, m2;
+  int i1, i2, kept;
+  auto best_two = [&](auto all, uint32_t last, int at_last) {
+    m1 = m2 = 0u;
+    i1 = i2 = 0;
+    kept = 2;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
-      const int e = i * 32 + lane;
-      const bool nan = v[i] != v[i];
-      v[i] = sigmoid_of(v[i]);
-      const float s = a.bias && e < a.E ? v[i] + a.bias[e] : v[i];
-      key[i] = e >= a.E ? 0u : nan ? 1u : order_key(s);
+      const uint32_t x = decltype(all)::value || key[i] < last || (key[i] == last && i > at_last) ? key[i] : 0u;
+      const bool first = x > m1, second = x > m2;
+      i2 = first ? i1 : second ? i : i2;
+      m2 = max(min(m1, x), m2);
+      i1 = first ? i : i1;
+      m1 = max(m1, x);
     }
-    if (a.n_group > 1) {
-      // score of a group: the sum of its two best; a power of two of lanes looks through each group
-      const int gs = a.E / a.n_group;
+  };
+  best_two(std::true_type{}, 0u, 0);
+  if (lanes) {
+    const int sub = 32 / a.n_group;
+    if (!((live_groups(sub, m1, m2) >> (lane / sub)) & 1u)) m1 = 0u;
+  }
+
+  // the largest score of a softmax row is the first pick's
+  float top = 0.0f, denom = 0.0f, sum = 0.0f;
+  auto term_of = [&](uint32_t x) { return x <= 1u ? 0.0f : softmax_term(key_value(x), top); };
+  if (a.scoring == 0) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, m1);
+    top = best <= 1u ? 0.0f : fminf(key_value(best), 3.402823466e38f);
+    if (!a.renorm) {
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int e = i * 32 + lane;
-        if (e < a.E) group_scratch[e + (e >> 5)] = __uint_as_float(key[i]);
-      }
-      __syncwarp();
-      int sub = 1;
-      while (2 * sub * a.n_group <= 32) sub *= 2;
-      const int g = lane / sub, j = lane % sub;
-      uint32_t b1 = 0u, b2 = 0u;
-      if (g < a.n_group) {
-        for (int i = j; i < gs; i += sub) {
-          const int e = g * gs + i;
-          const uint32_t x = __float_as_uint(group_scratch[e + (e >> 5)]);
-          if (x > b1) { b2 = b1; b1 = x; }
-          else if (x > b2) b2 = x;
-        }
-      }
-      for (int o = 1; o < sub; o <<= 1) {
-        const uint32_t c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
-        b2 = b1 > c1 ? max(b2, c1) : max(b1, c2);
-        b1 = max(b1, c1);
-      }
-      // a NaN (key 1) or an absent second value adds nothing; a group of NaN ranks last
-      uint32_t gkey = 0u;
-      if (g < a.n_group && j == 0)
-        gkey = b1 <= 1u ? 1u : order_key(b2 <= 1u ? key_value(b1) : key_value(b1) + key_value(b2));
-      uint32_t live = 0u;
-      for (int r = 0; r < a.topk_group; ++r) {
-        const uint32_t best = __reduce_max_sync(0xffffffffu, gkey);
-        const uint32_t who = __reduce_min_sync(0xffffffffu, gkey == best && gkey ? (uint32_t)lane : 0xffu);
-        live |= 1u << (who / sub);
-        if (lane == (int)who) gkey = 0u;
-      }
-      const float per = 1.0f / (float)gs;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int e = i * 32 + lane;
-        // e / gs: e < 4096 and half a unit away from the next quotient
-        if (e < a.E && !((live >> (int)(((float)e + 0.5f) * per)) & 1u)) key[i] = 0u;
-      }
-      __syncwarp();
+      for (int i = 0; i < NPL; ++i) denom += term_of(key[i]);
+      denom = warp_sum(denom);
     }
   }
 
-  // The k picks: the warp's largest key and the lowest index that has it.  A lane keeps its own largest and looks for the next
-  // only when it has lost it.  Lane j % 32 keeps pick j.
-  uint32_t m = 0u, at_m = 0u;
-  auto rescan = [&]() {
-    m = 0u;
-#pragma unroll
-    for (int i = NPL - 1; i >= 0; --i)
-      if (key[i] >= m) { m = key[i]; at_m = (uint32_t)(i * 32 + lane); }
-  };
-  rescan();
-  float sum = 0.0f;
+  // The k picks: the warp's largest key, of the lowest lane that has it.  Lane j % 32 keeps pick j.
+  int32_t* ids = a.ids + (size_t)t * a.k;
+  float* w = a.w + (size_t)t * a.k;
+  const bool divide = a.renorm || a.scoring == 0;
+  auto gate = [&](float x) { return (divide ? (denom > 0.0f ? x / denom : 0.0f) : x) * a.scale; };
   for (int j0 = 0; j0 < a.k; j0 += 32) {
     const int nj = min(32, a.k - j0);
-    uint32_t my_at = 0u;
-    float my_v = 0.0f;
+    int my_at = 0;
+    uint32_t my_key = 0u;
     for (int j = 0; j < nj; ++j) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, m);
-      const uint32_t at = __reduce_min_sync(0xffffffffu, m == best ? at_m : 0xffffffffu);
-      float val = 0.0f;
-      if (at == at_m && m == best) {   // the lane that has it
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-          if (at == (uint32_t)(i * 32 + lane)) { key[i] = 0u; val = v[i]; }
-        rescan();
+      const uint32_t best = __reduce_max_sync(0xffffffffu, m1);
+      const int who = __ffs(__ballot_sync(0xffffffffu, m1 == best)) - 1;
+      const int at = __shfl_sync(0xffffffffu, e0 + i1, who);
+      if (lane == j) { my_at = at; my_key = best; }
+      if (lane == who) {
+        if (--kept == 0) {
+          best_two(std::false_type{}, best, i1);
+        } else {
+          m1 = m2;
+          i1 = i2;
+        }
       }
-      val = __shfl_sync(0xffffffffu, val, (int)(at & 31u));
-      if (lane == j) { my_at = at; my_v = val; }
     }
     float term = 0.0f;
     if (lane < nj) {
-      term = a.scoring == 0 ? softmax_term(my_v, top) : my_v;
-      a.ids[(size_t)t * a.k + j0 + lane] = (int32_t)my_at;
-      a.w[(size_t)t * a.k + j0 + lane] = term;
+      if (a.scoring == 0) term = term_of(my_key);
+      else if (!a.bias) term = my_key <= 1u ? 0.0f : key_value(my_key);
+      else if (const float l = logit_at(a, row + my_at); l == l) term = sigmoid_of(l);   // the gate has no bias in it
+      ids[j0 + lane] = my_at;
+      found(j0 + lane, my_at);
     }
-    sum += warp_sum(term);
+    if (a.renorm) sum += warp_sum(term);
+    if (a.k <= 32) {
+      if (a.renorm) denom = sum;
+      if (lane < nj) w[lane] = gate(term);
+      return;
+    }
+    if (lane < nj) w[j0 + lane] = term;
   }
   if (a.renorm) denom = sum;
-  __syncwarp();
-  const bool divide = a.renorm || a.scoring == 0;
-  for (int j = lane; j < a.k; j += 32) {
-    float* w = a.w + (size_t)t * a.k + j;
-    const float x = *w;
-    *w = (divide ? (denom > 0.0f ? x / denom : 0.0f) : x) * a.scale;
-  }
+  for (int j = lane; j < a.k; j += 32) w[j] = gate(w[j]);   // its own picks
 }
 
 // Exclusive prefixes over the E + 1 bins of `count` by a block of 256 threads: of the counts into `first` (and `offsets`), of
@@ -226,24 +284,15 @@ __device__ __forceinline__ void scan_bins(const int32_t* count, int E, int32_t* 
   }
 }
 
-// Groups at most kSmallPairs pairs in one block.  smem: ids [kSmallPairs], count and first [E + 1].
-__device__ __forceinline__ void group_small(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* tiles,
-                                            int32_t* order, int32_t* place, int32_t* smem) {
-  int32_t* id = smem;
-  int32_t* count = id + kSmallPairs;
-  int32_t* first = count + E + 1;
-  for (int e = threadIdx.x; e <= E; e += blockDim.x) count[e] = 0;
-  __syncthreads();
+// Groups at most kSmallPairs pairs in one block.  smem: the pairs' bins [kSmallPairs], count [E + 1], room for starts [E + 1].
+__device__ __forceinline__ void group_small(int P, int E, int32_t* offsets, int32_t* tiles, int32_t* order, int32_t* place,
+                                            int32_t* smem) {
+  const int32_t* id = smem;
+  const int32_t* count = id + kSmallPairs;
+  int32_t* first = smem + kSmallPairs + E + 1;
   const int p = threadIdx.x;      // blockDim.x >= kSmallPairs
-  int mine = -1;
   if (p < P) {
-    const int e = ids[p];
-    mine = (unsigned)e < (unsigned)E ? e : E;
-    id[p] = mine;
-    atomicAdd(&count[mine], 1);
-  }
-  __syncthreads();
-  if (p < P) {
+    const int mine = id[p];
     int row = 0;
     for (int i = 0; i < P; ++i) row += id[i] < mine || (id[i] == mine && i < p);
     order[row] = mine < E ? p : -1;
@@ -252,34 +301,41 @@ __device__ __forceinline__ void group_small(const int32_t* ids, int P, int E, in
   scan_bins(count, E, first, offsets, tiles);
 }
 
-template <int NPL>
-__global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(RouteArgs a, int logits_bf16) {
+// Registers for 5 blocks an SM (3 with 16 scores a lane): 8192 tokens of 256 experts in 4 of 8 groups take 10.7 us, 11.4 without a
+// bound, 10.9 with 6 blocks; 8192 tokens of 384 experts 13.7, 17.1 with 2.
+template <int NPL, bool FULL>
+__global__ void __launch_bounds__(ROUTE_THREADS, NPL <= 8 ? 5 : NPL == 16 ? 3 : 1) route_kernel(RouteArgs a, int scratch_at) {
   extern __shared__ int32_t smem[];
+  // the block's own pairs by expert; a block that groups them all keeps their bins before that
+  const bool small = a.offsets && !a.counts;
+  int32_t* count = smem + (small ? kSmallPairs : 0);
+  if (a.offsets)
+    for (int i = threadIdx.x; i <= a.E; i += ROUTE_THREADS) count[i] = 0;
   pdl_wait();
   pdl_trigger();
+  __syncthreads();
   const int warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * a.tokens_per_block, t1 = min(a.T, t0 + a.tokens_per_block);
-  float* scratch = reinterpret_cast<float*>(smem) + (size_t)warp * (a.E + a.E / 32 + 1);
-  for (int t = t0 + warp; t < t1; t += ROUTE_WARPS) route_token<NPL>(a, logits_bf16, t, scratch);
+  float* scratch = reinterpret_cast<float*>(smem + scratch_at) + (size_t)warp * (a.E + a.E / 32 + 1);
+  for (int t = t0 + warp; t < t1; t += ROUTE_WARPS)
+    route_token<NPL, FULL>(a, t, scratch, [&](int j, int e) {
+      if (!a.offsets) return;
+      atomicAdd(&count[e], 1);
+      if (small) smem[t * a.k + j] = e;
+    });
   if (!a.offsets) return;
-  __syncthreads();   // this block's ids are written, the scratch is free
-  if (!a.counts) {
-    group_small(a.ids, a.T * a.k, a.E, a.offsets, a.tiles, a.order, a.place, smem);
-    return;
-  }
-  for (int i = threadIdx.x; i <= a.E; i += ROUTE_THREADS) smem[i] = 0;
   __syncthreads();
-  for (int p = t0 * a.k + threadIdx.x; p < t1 * a.k; p += ROUTE_THREADS) atomicAdd(&smem[a.ids[p]], 1);
-  __syncthreads();
-  for (int i = threadIdx.x; i <= a.E; i += ROUTE_THREADS) a.counts[(size_t)i * gridDim.x + blockIdx.x] = smem[i];
+  if (small) group_small(a.T * a.k, a.E, a.offsets, a.tiles, a.order, a.place, smem);
+  else
+    for (int i = threadIdx.x; i <= a.E; i += ROUTE_THREADS) a.counts[(size_t)blockIdx.x * (a.E + 1) + i] = count[i];
 }
 
 __global__ void __launch_bounds__(ROUTE_THREADS)
 count_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int32_t* __restrict__ counts) {
   extern __shared__ int32_t smem[];
+  for (int i = threadIdx.x; i <= E; i += ROUTE_THREADS) smem[i] = 0;
   pdl_wait();
   pdl_trigger();
-  for (int i = threadIdx.x; i <= E; i += ROUTE_THREADS) smem[i] = 0;
   __syncthreads();
   const int p0 = blockIdx.x * per_block, p1 = min(P, p0 + per_block);
   for (int p = p0 + threadIdx.x; p < p1; p += ROUTE_THREADS) {
@@ -287,50 +343,63 @@ count_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int32
     atomicAdd(&smem[(unsigned)e < (unsigned)E ? e : E], 1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i <= E; i += ROUTE_THREADS) counts[(size_t)i * gridDim.x + blockIdx.x] = smem[i];
+  for (int i = threadIdx.x; i <= E; i += ROUTE_THREADS) counts[(size_t)blockIdx.x * (E + 1) + i] = smem[i];
 }
 
 __global__ void __launch_bounds__(ROUTE_THREADS)
 group_small_kernel(const int32_t* __restrict__ ids, int P, int E, int32_t* offsets, int32_t* tiles, int32_t* order, int32_t* place) {
   extern __shared__ int32_t smem[];
+  int32_t* count = smem + kSmallPairs;
+  for (int e = threadIdx.x; e <= E; e += ROUTE_THREADS) count[e] = 0;
   pdl_wait();
   pdl_trigger();
-  group_small(ids, P, E, offsets, tiles, order, place, smem);
+  __syncthreads();
+  if (threadIdx.x < P) {
+    const int e = ids[threadIdx.x], bin = (unsigned)e < (unsigned)E ? e : E;
+    smem[threadIdx.x] = bin;
+    atomicAdd(&count[bin], 1);
+  }
+  __syncthreads();
+  group_small(P, E, offsets, tiles, order, place, smem);
 }
 
-// counts [E + 1, blocks] -> what comes before each block, in place, and each expert's total; a warp per expert
-__global__ void __launch_bounds__(256) starts_kernel(int32_t* __restrict__ counts, int E, int blocks, int32_t* __restrict__ total) {
+// counts [blocks, E + 1] -> what comes before each block, in place, and each expert's total.  A block of 1024 threads takes 8
+// bins, a sector of each row; a thread holds the counts of a run of at most kMaxBlocks / 128 blocks.
+__global__ void __launch_bounds__(1024) starts_kernel(int32_t* __restrict__ counts, int E, int blocks, int32_t* __restrict__ total) {
+  constexpr int ROWS = kMaxBlocks / 128;
+  __shared__ int32_t sums[32][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bin = lane & 7, e = blockIdx.x * 8 + bin;
+  const int rows = (blocks + 127) / 128, r0 = (int)(threadIdx.x >> 3) * rows, n = e <= E ? min(rows, blocks - r0) : 0;
+  int32_t* at = counts + (size_t)r0 * (E + 1) + e;
   pdl_wait();
   pdl_trigger();
-  const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (e > E) return;
-  int32_t* row = counts + (size_t)e * blocks;
-  // 32 blocks a step: loads and scans of eight steps do not wait for one another
-  int run = 0;
-  for (int b0 = 0; b0 < blocks; b0 += 256) {
-    int c[8], x[8];
+  int c[ROWS], sum = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = x[i] = b0 + 32 * i + lane < blocks ? row[b0 + 32 * i + lane] : 0;
+  for (int r = 0; r < ROWS; ++r) c[r] = r < n ? at[(size_t)r * (E + 1)] : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int u = __shfl_up_sync(0xffffffffu, x[i], o);
-        if (lane >= o) x[i] += u;
-      }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (b0 + 32 * i + lane < blocks) row[b0 + 32 * i + lane] = run + x[i] - c[i];
-      run += __shfl_sync(0xffffffffu, x[i], 31);
-    }
+  for (int r = 0; r < ROWS; ++r) sum += c[r];
+  int run = sum;   // over the warp's four runs of the bin
+  for (int o = 8; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += u;
   }
-  if (lane == 0) total[e] = run;
+  if (lane >= 24) sums[warp][bin] = run;
+  __syncthreads();
+  run -= sum;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) run += w < warp ? sums[w][bin] : 0;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    if (r < n) at[(size_t)r * (E + 1)] = run;
+    run += c[r];
+  }
+  if (threadIdx.x >= 1016 && e <= E) total[e] = run;
 }
 
 // Ranks the pairs of `per` counting blocks; warps take consecutive segments.  smem: start [E + 1], total [E + 1], a count per
 // warp and bin.
 __global__ void __launch_bounds__(PLACE_THREADS)
-place_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int per, int blocks, const int32_t* __restrict__ starts,
+place_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int per, const int32_t* __restrict__ starts,
              const int32_t* __restrict__ totals, int32_t* offsets, int32_t* tiles, int32_t* __restrict__ order, int32_t* __restrict__ place) {
   extern __shared__ int32_t smem[];
   const int bins = E + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -357,7 +426,7 @@ place_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int p
   }
   __syncthreads();
   for (int e = threadIdx.x; e < bins; e += PLACE_THREADS) {
-    int run = start[e] + starts[(size_t)e * blocks + blockIdx.x * per];
+    int run = start[e] + starts[(size_t)blockIdx.x * per * bins + e];
 #pragma unroll
     for (int w = 0; w < PLACE_WARPS; ++w) {
       const int c = cnt[w * bins + e];
@@ -401,7 +470,7 @@ combine_kernel(int T, int k, int N, const Y* __restrict__ y, const int32_t* __re
       if (row < 0) continue;
       const float g = __ldg(w + (size_t)t * k + j);
       const Y* src = y + (size_t)row * N + c;
-      Y tmp[V];
+      alignas(16) Y tmp[V];
       if constexpr (sizeof(Y) * V == 16) *reinterpret_cast<uint4*>(tmp) = __ldg(reinterpret_cast<const uint4*>(src));
       else if constexpr (sizeof(Y) * V == 32) {
         reinterpret_cast<uint4*>(tmp)[0] = __ldg(reinterpret_cast<const uint4*>(src));
@@ -413,7 +482,7 @@ combine_kernel(int T, int k, int N, const Y* __restrict__ y, const int32_t* __re
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] = fmaf(g, (float)tmp[i], acc[i]);
     }
-    O res[V];
+    alignas(16) O res[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) res[i] = (O)acc[i];
     O* dst = out + (size_t)t * N + c;
@@ -468,23 +537,27 @@ cudaError_t allow_smem(const void* fn, size_t bytes) {
 size_t small_smem(int E) { return (size_t)(kSmallPairs + 2 * (E + 1)) * 4; }
 
 template <int NPL>
-moe_status run_route(const RouteArgs& a, int bf16, int blocks, cudaStream_t s) {
-  size_t smem = a.n_group > 1 ? (size_t)ROUTE_WARPS * (a.E + a.E / 32 + 1) * 4 : 0;
-  if (a.offsets) smem = std::max(smem, small_smem(a.E));
-  CK(allow_smem((const void*)route_kernel<NPL>, smem));
-  CK(launch_pdl(route_kernel<NPL>, dim3(blocks), dim3(ROUTE_THREADS), smem, s, a, bf16));
+moe_status run_route(const RouteArgs& a, int blocks, cudaStream_t s) {
+  constexpr int U = NPL >= 4 ? 4 : 2;
+  const bool full = a.E == 32 * NPL && aligned_to(a.logits, U * (a.bf16 ? 2 : 4)) && aligned_to(a.bias, 4 * U);
+  const bool whole_lanes = a.n_group == 1 || (a.E % 32 == 0 && !(a.n_group & (a.n_group - 1)));
+  const size_t bins = !a.offsets ? 0 : a.counts ? (size_t)(a.E + 1) * 4 : small_smem(a.E);
+  const size_t smem = bins + (full && whole_lanes ? 0 : (size_t)ROUTE_WARPS * (a.E + a.E / 32 + 1) * 4);
+  const auto kernel = full ? route_kernel<NPL, true> : route_kernel<NPL, false>;
+  CK(allow_smem((const void*)kernel, smem));
+  CK(launch_pdl(kernel, dim3(blocks), dim3(ROUTE_THREADS), smem, s, a, (int)(bins / 4)));
   return MOE_OK;
 }
 
-// counts [E + 1, blocks] of the blocks' pairs -> the grouping; the totals follow the counts in the workspace
+// counts [blocks, E + 1] of the blocks' pairs -> the grouping; the totals follow the counts in the workspace
 moe_status run_place(const int32_t* ids, int P, int E, int per_block, int blocks, int32_t* counts, int32_t* offsets, int32_t* tiles,
                      int32_t* order, int32_t* place, cudaStream_t s) {
   int32_t* total = counts + (size_t)(E + 1) * blocks;
-  CK(launch_pdl(starts_kernel, dim3((E + 8) / 8), dim3(256), 0, s, counts, E, blocks, total));
+  CK(launch_pdl(starts_kernel, dim3((E + 8) / 8), dim3(1024), 0, s, counts, E, blocks, total));
   const size_t smem = (size_t)(2 + PLACE_WARPS) * (E + 1) * 4;
   CK(allow_smem((const void*)place_kernel, smem));
   const int per = std::max(1, PLACE_THREADS / per_block);   // about a pair a thread
-  CK(launch_pdl(place_kernel, dim3((blocks + per - 1) / per), dim3(PLACE_THREADS), smem, s, ids, P, E, per_block, per, blocks,
+  CK(launch_pdl(place_kernel, dim3((blocks + per - 1) / per), dim3(PLACE_THREADS), smem, s, ids, P, E, per_block, per,
                 (const int32_t*)counts, (const int32_t*)total, offsets, tiles, order, place));
   return MOE_OK;
 }
@@ -551,11 +624,11 @@ extern "C" moe_status moe_route(int32_t T, int32_t E, int32_t k, int32_t logits_
   a.counts = group && !small ? static_cast<int32_t*>(workspace) : nullptr;
   a.tokens_per_block = small ? T : tokens_per_block(T);
   const int blocks = (T + a.tokens_per_block - 1) / a.tokens_per_block;
-  const int bf16 = logits_dtype == MOE_BF16;
+  a.bf16 = logits_dtype == MOE_BF16;
   const int npl = (E + 31) / 32;
-  st = npl <= 2 ? run_route<2>(a, bf16, blocks, s) : npl <= 4 ? run_route<4>(a, bf16, blocks, s)
-       : npl <= 8 ? run_route<8>(a, bf16, blocks, s) : npl <= 16 ? run_route<16>(a, bf16, blocks, s)
-       : npl <= 32 ? run_route<32>(a, bf16, blocks, s) : run_route<128>(a, bf16, blocks, s);
+  st = npl <= 2 ? run_route<2>(a, blocks, s) : npl <= 4 ? run_route<4>(a, blocks, s) : npl <= 8 ? run_route<8>(a, blocks, s)
+       : npl <= 16 ? run_route<16>(a, blocks, s) : npl <= 32 ? run_route<32>(a, blocks, s)
+       : npl <= 64 ? run_route<64>(a, blocks, s) : run_route<128>(a, blocks, s);
   if (st != MOE_OK || !a.counts) return st;
   return run_place(ids, T * k, E, a.tokens_per_block * k, blocks, a.counts, offsets, tiles, order, place, s);
 }
