@@ -451,7 +451,9 @@ place_kernel(const int32_t* __restrict__ ids, int P, int E, int per_block, int p
   }
 }
 
-// out[t, n] = sum_j w[t, j] y[place[t, j], n]: V columns a thread
+// out[t, n] = sum_j w[t, j] y[place[t, j], n], in j order: V columns a thread.  Four rows' loads are in flight before the first is
+// used: 4096 tokens, 8 experts, N 7168 in bf16 take 89 us a row at a time, 81 so, 102 by eights, whose registers cost warps.
+constexpr int COMBINE_ROWS = 4;
 template <typename Y, typename O, int V>
 __global__ void __launch_bounds__(256)
 combine_kernel(int T, int k, int N, const Y* __restrict__ y, const int32_t* __restrict__ place,
@@ -461,26 +463,38 @@ combine_kernel(int T, int k, int N, const Y* __restrict__ y, const int32_t* __re
   const int cols = N / V;
   const int64_t units = (int64_t)T * cols;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
-    const int t = (int)(u / cols), c = (int)(u % cols) * V;
+    // a 64-bit division only where it is needed (4 us of 85)
+    const int t = units <= 0x7fffffff ? (int)((uint32_t)u / (uint32_t)cols) : (int)(u / cols), c = (int)(u - (int64_t)t * cols) * V;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const int row = __ldg(place + (size_t)t * k + j);
-      if (row < 0) continue;
-      const float g = __ldg(w + (size_t)t * k + j);
-      const Y* src = y + (size_t)row * N + c;
-      alignas(16) Y tmp[V];
-      if constexpr (sizeof(Y) * V == 16) *reinterpret_cast<uint4*>(tmp) = __ldg(reinterpret_cast<const uint4*>(src));
-      else if constexpr (sizeof(Y) * V == 32) {
-        reinterpret_cast<uint4*>(tmp)[0] = __ldg(reinterpret_cast<const uint4*>(src));
-        reinterpret_cast<uint4*>(tmp)[1] = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-      } else {
+    for (int j0 = 0; j0 < k; j0 += COMBINE_ROWS) {
+      alignas(16) Y tmp[COMBINE_ROWS][V];
+      int row[COMBINE_ROWS];
+      float g[COMBINE_ROWS];
 #pragma unroll
-        for (int i = 0; i < V; ++i) tmp[i] = src[i];
+      for (int j = 0; j < COMBINE_ROWS; ++j) {
+        row[j] = j0 + j < k ? __ldg(place + (size_t)t * k + j0 + j) : -1;
+        g[j] = j0 + j < k ? __ldg(w + (size_t)t * k + j0 + j) : 0.0f;
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = fmaf(g, (float)tmp[i], acc[i]);
+      for (int j = 0; j < COMBINE_ROWS; ++j) {
+        if (row[j] < 0) continue;
+        const Y* src = y + (size_t)row[j] * N + c;
+        if constexpr (sizeof(Y) * V % 16 == 0) {
+#pragma unroll
+          for (int i = 0; i < (int)sizeof(Y) * V / 16; ++i) reinterpret_cast<uint4*>(tmp[j])[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) tmp[j][i] = src[i];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < COMBINE_ROWS; ++j) {
+        if (row[j] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(g[j], (float)tmp[j][i], acc[i]);
+      }
     }
     alignas(16) O res[V];
 #pragma unroll
