@@ -55,12 +55,6 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
   asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// value of an e2m1 code (bit 3: sign)
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t m = c & 7u;
-  const float v = m < 2u ? 0.5f * (float)m : __uint_as_float((((m >> 1) + 126u) << 23) | ((m & 1u) << 22));
-  return (c & 8u) ? -v : v;
-}
 
 // Correctly rounded x / d from r = 1 / d rounded to nearest, without a division (Markstein 1990): with q = x r, the
 // remainder x - q d is exact in one fma, and q + remainder * r rounds to the quotient.  Away from the ends of the exponent
