@@ -106,6 +106,48 @@ def test_sigmoid_route_with_groups(moe, T, E, k, n_group, topk_group, bias):
     check_groups(gr, host(ids), E)
 
 
+@pytest.mark.parametrize("E", [32, 64, 96, 128, 256, 384, 512, 1024, 2048, 4096])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("skip", [0, 1])
+def test_route_widths_and_where_the_picks_lie(moe, E, dtype, skip):
+    """Whole and partial lanes, rows that start off 16 bytes, and picks that lie together, apart, or are equal."""
+    rng = np.random.default_rng(E)
+    k = min(E, 40)
+    z = bf16(rng.standard_normal((14, E)))
+    z[0] = np.maximum(-np.arange(E), -255) / 4                     # the first ones in order: exact in bf16
+    z[1] = z[0, ::-1]                                              # the last ones
+    z[2] = 0.5
+    z[3] = np.repeat(rng.permutation(E // 2) % 16, 2)              # equal neighbours
+    z[4, ::3], z[4, 1] = np.nan, np.inf
+    z[5] = np.nan
+    z[6] = -np.inf
+    z[7], z[7, E // 2:E // 2 + 3] = -np.inf, [1, np.nan, 1]
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = torch.empty(z.size + skip, dtype=t, device="cuda")[skip:].view(z.shape)
+    x.copy_(dev(z, t))
+    ids, w, gr = moe.route(x, k, groups=True)
+    rid, rw = ref.route(z, k)
+    assert np.array_equal(host(ids), rid)
+    # as above; picks lie within 10 of the largest, or their terms below 1e-30 come from a row of -inf
+    assert np.allclose(host(w), rw, rtol=(k + 32) * 2 * EPS, atol=1e-30)
+    check_groups(gr, rid, E)
+
+
+@pytest.mark.parametrize("E,n_group", [(256, 8), (256, 32), (64, 2), (60, 6), (160, 8), (512, 16)])
+def test_sigmoid_groups_with_equal_and_missing_scores(moe, E, n_group):
+    rng = np.random.default_rng(E + n_group)
+    z = rng.choice(np.array([-np.inf, 0, np.inf], np.float32), (24, E))    # scores 0, 0.5 and 1
+    z[rng.random(z.shape) < 0.05] = np.nan
+    gs, keep = E // n_group, max(1, n_group // 2)
+    z[:, ::gs], z[:, 1::gs] = 0, 0                                         # no group is short of two scores, but for
+    z[0:8, gs:2 * gs] = np.nan                                             # one that has none
+    z[8] = np.nan
+    ids, w = moe.route(dev(z), 4, scoring="sigmoid", n_group=n_group, topk_group=keep)
+    rid, rw = ref.route(z, 4, "sigmoid", None, n_group, keep)
+    assert np.array_equal(host(ids), rid)
+    assert np.allclose(host(w), rw, rtol=64 * EPS)
+
+
 @pytest.mark.parametrize("T,E,k", [(0, 4, 2), (1, 1, 1), (3, 5, 2), (100, 7, 3), (33, 4096, 4), (5000, 256, 8), (20000, 3, 2), (1300, 1024, 1)])
 def test_group_pairs_drops_foreign_ids(moe, T, E, k):
     rng = np.random.default_rng(T + E)
