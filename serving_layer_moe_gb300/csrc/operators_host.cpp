@@ -124,6 +124,7 @@ void make_rows(Rows& r, const Groups* g, bool stacked, at::Tensor& codes, at::Te
 
 // groups_of(offsets, tiles, order, place) -> tuple
 PyObject* groups_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  TRY
   if (n != 4) OTHERWISE;
   const at::Tensor* off = typed(a[0], ScalarType::Int, 1, -1);
   if (!off) OTHERWISE;
@@ -142,10 +143,12 @@ PyObject* groups_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.order = address(*order);
   g.place = address(*place);
   return as_nine(&g);
+  CATCH
 }
 
 // rows_of(codes, scales, wdtype, g, groups) -> tuple
 PyObject* rows_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  TRY
   if (n != 5 || !THPVariable_Check(a[0])) OTHERWISE;
   Groups gr{};
   const bool grouped = a[4] != Py_None;
@@ -167,6 +170,7 @@ PyObject* rows_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.scales = address(*scales);
   if ((r.codes | r.scales) % 16 || !scale_of(a[3], r.G, r.index, &r.g, &r.g_count)) OTHERWISE;
   return as_nine(&r);
+  CATCH
 }
 
 // route(logits, k, scoring, bias, n_group, topk_group, renormalize, scale, groups) -> (ids, w, None) or (ids, w, (buffer, tuple))

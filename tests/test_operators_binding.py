@@ -1,0 +1,50 @@
+"""The operators' binding, as far as it goes without a GPU: what it raises, what it keeps, what it needs."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from serving_layer_moe_gb300 import build as b
+    if not (os.path.exists(b.LIB) and os.path.exists(b.HOST)):
+        b.build()
+
+
+def run(script, *args):
+    """A script in a process of its own, so that an abort fails one test; its output's last line."""
+    r = subprocess.run([sys.executable, "-c", script, *args], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+    return r.stdout.strip().splitlines()[-1]
+
+
+# Tensors that say they are on a GPU and have no memory: the constructors' own checks pass, reading an address throws.
+WITHOUT_MEMORY = """
+import sys, torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+import serving_layer_moe_gb300 as moe
+moe.operators._host()
+with FakeTensorMode(allow_non_fake_inputs=True):
+    i = lambda *s: torch.empty(3, *s, dtype=torch.int32, device="cuda")
+    u = lambda *s: torch.empty(3, *s, dtype=torch.uint8, device="cuda")
+    def groups(a, b, c, d):
+        moe.ExpertGroups(a, b, c, d)
+    def rows(a, b):
+        moe.FP4Rows(a, b, "mxfp4")
+    try:
+        if sys.argv[1] == "groups":
+            torch.vmap(groups)(i(5), i(5), i(6), i(3, 2))
+        else:
+            torch.vmap(rows)(u(4, 16), u(1, 1, 512))
+    except RuntimeError as e:
+        print("raised", type(e).__name__)
+"""
+
+
+@pytest.mark.parametrize("what", ["groups", "rows"])
+def test_constructors_raise_on_tensors_without_memory(what):
+    assert run(WITHOUT_MEMORY, what).startswith("raised")
