@@ -189,6 +189,11 @@ class ExpertGroups:
     place = property(lambda self: self._view(3))
 
 
+def _described(groups):
+    """What the host module takes for groups: their tuple, None, or False for anything else (which it leaves alone)."""
+    return None if groups is None else groups._c if isinstance(groups, ExpertGroups) else False
+
+
 def _groups_on(groups, index):
     if not isinstance(groups, ExpertGroups):
         raise ValueError(f"groups must be ExpertGroups, is {type(groups)}")
@@ -208,7 +213,7 @@ class FP4Rows:
     def __init__(self, codes, scales, wdtype, g=None, groups=None):
         if wdtype not in FP4_BLOCK:
             raise ValueError(f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
-        self._c = _host().rows_of(codes, scales, DTYPES[wdtype], g, groups._c if isinstance(groups, ExpertGroups) else groups)
+        self._c = _host().rows_of(codes, scales, DTYPES[wdtype], g, _described(groups))
         if self._c is None:
             self._refuse(codes, scales, wdtype, g, groups)
         self.codes, self.scales, self.wdtype, self.g, self.groups = codes, scales, wdtype, g, groups
@@ -320,7 +325,7 @@ def quantize_fp4(x, wdtype, *, g=None, groups=None, stream=None):
     if wdtype not in FP4_BLOCK:
         raise ValueError(f"wdtype must be 'nvfp4' or 'mxfp4', is {wdtype!r}")
     if stream is None:
-        r = (_host_module or _host()).quantize(x, DTYPES[wdtype], g, groups._c if isinstance(groups, ExpertGroups) else groups)
+        r = (_host_module or _host()).quantize(x, DTYPES[wdtype], g, _described(groups))
         if r is not None:
             return FP4Rows._of(r[0], r[1], wdtype, g, groups, r[2])
     dim = 2 if groups is not None or not isinstance(x, torch.Tensor) or x.dim() != 3 else 3

@@ -48,3 +48,22 @@ with FakeTensorMode(allow_non_fake_inputs=True):
 @pytest.mark.parametrize("what", ["groups", "rows"])
 def test_constructors_raise_on_tensors_without_memory(what):
     assert run(WITHOUT_MEMORY, what).startswith("raised")
+
+
+# Nine integers look like the description that the binding keeps of groups; as an argument they are nobody's addresses.
+NINE_INTEGERS = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+import serving_layer_moe_gb300 as moe
+nine = (0, 8, 4, 2, 2, 4096, 8192, 12288, 16384)
+with FakeTensorMode(allow_non_fake_inputs=True):
+    u = lambda *s: torch.empty(*s, dtype=torch.uint8, device="cuda")
+    try:
+        moe.FP4Rows(u(4, 16), u(4, 1, 512), "mxfp4", groups=nine)
+    except ValueError as e:
+        print("refused", e)
+"""
+
+
+def test_integers_are_not_groups():
+    assert run(NINE_INTEGERS).startswith("refused groups must be ExpertGroups")
