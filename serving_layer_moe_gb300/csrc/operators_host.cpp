@@ -6,9 +6,11 @@
 // ordinary (a wrong argument, another device or stream) it leaves to operators.py by returning None, which looks again and
 // raises what is wrong.  A status other than MOE_OK goes to the function given to init().
 //
-// Groups and 4-bit rows come as tuples of integers that operators.py keeps with the tensors:
-//   groups  (device, E, P, T, k, offsets, tiles, order, place)
-//   rows    (device, G, N, K, wdtype, codes, scales, g, number of g)
+// Groups and 4-bit rows come as the tuples that operators.py keeps of them, integers and tensors:
+//   groups  (device, E, P, T, k, offsets, tiles, order, place), or (device, E, P, T, k, buffer, byte, None, None) with the four
+//           one after another from that byte of a buffer of the library's own
+//   rows    (device, G, N, K, wdtype, codes, scales, g or None, number of g)
+// Addresses are read from the tensors at each call: a copy has its own memory, and a resized tensor other memory than before.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -29,16 +31,6 @@ struct Groups { int64_t index, E, P, T, k, offsets, tiles, order, place; };
 struct Rows { int64_t index, G, N, K, wdtype, codes, scales, g, g_count; };
 static_assert(sizeof(Groups) == 9 * 8 && sizeof(Rows) == 9 * 8, "nine integers each");
 
-bool nine(PyObject* o, void* to) {
-  if (!PyTuple_CheckExact(o) || PyTuple_GET_SIZE(o) != 9) return false;
-  for (int i = 0; i < 9; ++i) static_cast<int64_t*>(to)[i] = (int64_t)PyLong_AsUnsignedLongLongMask(PyTuple_GET_ITEM(o, i));
-  return true;
-}
-PyObject* as_nine(const void* from) {
-  PyObject* t = PyTuple_New(9);
-  for (int i = 0; t && i < 9; ++i) PyTuple_SET_ITEM(t, i, PyLong_FromLongLong(static_cast<const int64_t*>(from)[i]));
-  return t;
-}
 template <typename T> T* ptr(int64_t p) { return reinterpret_cast<T*>((uintptr_t)p); }
 
 // a contiguous CUDA tensor of `dim` dimensions on device `index` (any where -1), or NULL
@@ -87,6 +79,42 @@ PyObject* raise(moe_status st) {
 }
 int64_t address(const at::Tensor& t) { return (int64_t)(uintptr_t)t.data_ptr(); }
 
+// the first n integers of a tuple of nine
+bool integers(PyObject* o, int n, int64_t* to) {
+  if (!PyTuple_CheckExact(o) || PyTuple_GET_SIZE(o) != 9) return false;
+  for (int i = 0; i < n; ++i) to[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(o, i));
+  return !PyErr_Occurred();
+}
+// bytes of t's memory from its first element on
+int64_t bytes_from(const at::Tensor& t) { return (int64_t)t.storage().nbytes() - t.storage_offset() * (int64_t)t.itemsize(); }
+// where a tensor of a tuple is now; false if it is no longer the one that was checked
+bool held(PyObject* o, ScalarType type, int64_t index, int64_t numel, int64_t* p) {
+  if (!THPVariable_Check(o)) return false;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda() || t.get_device() != index || t.scalar_type() != type || t.numel() != numel || !t.is_contiguous() ||
+      bytes_from(t) < numel * (int64_t)t.itemsize())
+    return false;
+  *p = address(t);
+  return true;
+}
+bool groups_in(PyObject* o, Groups& g) {
+  if (!integers(o, 5, &g.index)) return false;
+  PyObject *first = PyTuple_GET_ITEM(o, 5), *second = PyTuple_GET_ITEM(o, 6);
+  if (PyLong_Check(second)) {
+    const int64_t at = PyLong_AsLongLong(second), bins = 4 * (g.E + 1);
+    if (!THPVariable_Check(first)) return false;
+    const at::Tensor& b = THPVariable_Unpack(first);
+    if (!b.is_cuda() || b.get_device() != g.index || bytes_from(b) < at + 2 * bins + 8 * g.P) return false;
+    g.offsets = address(b) + at;
+    g.tiles = g.offsets + bins;
+    g.order = g.tiles + bins;
+    g.place = g.order + 4 * g.P;
+    return true;
+  }
+  return held(first, ScalarType::Int, g.index, g.E + 1, &g.offsets) && held(second, ScalarType::Int, g.index, g.E + 1, &g.tiles) &&
+         held(PyTuple_GET_ITEM(o, 7), ScalarType::Int, g.index, g.P, &g.order) && held(PyTuple_GET_ITEM(o, 8), ScalarType::Int, g.index, g.P, &g.place);
+}
+
 // one fp32 scale, or `most`: pointer and number, 0 and 0 for None
 bool scale_of(PyObject* o, int64_t most, int64_t index, int64_t* p, int64_t* n) {
   *p = *n = 0;
@@ -101,6 +129,21 @@ int64_t block_of(int64_t wdtype) { return wdtype == MOE_NVFP4 ? 16 : 32; }
 int64_t block_groups(int64_t wdtype, int64_t K) { return (K + 4 * block_of(wdtype) - 1) / (4 * block_of(wdtype)); }
 int64_t row_tiles(const Rows& r, const Groups* g) {
   return g ? moe_grouped_tiles(g->P, (int32_t)g->E) : r.G * ((r.N + 127) / 128);
+}
+
+// rows with the groups that they are laid out by (NULL: matrices)
+bool rows_in(PyObject* o, const Groups* g, Rows& r) {
+  if (!integers(o, 5, &r.index)) return false;
+  PyObject *scale = PyTuple_GET_ITEM(o, 7), *count = PyTuple_GET_ITEM(o, 8);
+  r.g_count = PyLong_AsLongLong(count);
+  r.g = 0;
+  return held(PyTuple_GET_ITEM(o, 5), ScalarType::Byte, r.index, r.G * r.N * (r.K / 2), &r.codes) &&
+         held(PyTuple_GET_ITEM(o, 6), ScalarType::Byte, r.index, row_tiles(r, g) * block_groups(r.wdtype, r.K) * 512, &r.scales) &&
+         (scale == Py_None || held(scale, ScalarType::Float, r.index, r.g_count, &r.g));
+}
+// a new tuple of rows; takes codes and scales
+PyObject* rows_tuple(const Rows& r, PyObject* codes, PyObject* scales, PyObject* g) {
+  return Py_BuildValue("(LLLLLNNOL)", (long long)r.index, (long long)r.G, (long long)r.N, (long long)r.K, (long long)r.wdtype, codes, scales, g, (long long)r.g_count);
 }
 
 // room for the rows r describes
@@ -138,11 +181,8 @@ PyObject* groups_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.T = place->size(0);
   g.k = place->size(1);
   if (g.E < 1 || g.E > 4096 || til->numel() != g.E + 1 || g.T * g.k != g.P) OTHERWISE;
-  g.offsets = address(*off);
-  g.tiles = address(*til);
-  g.order = address(*order);
-  g.place = address(*place);
-  return as_nine(&g);
+  for (const at::Tensor* t : {off, til, order, place}) (void)address(*t);   // throws where there is no memory
+  return Py_BuildValue("(LLLLLOOOO)", (long long)g.index, (long long)g.E, (long long)g.P, (long long)g.T, (long long)g.k, a[0], a[1], a[2], a[3]);
   CATCH
 }
 
@@ -152,7 +192,7 @@ PyObject* rows_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 5 || !THPVariable_Check(a[0])) OTHERWISE;
   Groups gr{};
   const bool grouped = a[4] != Py_None;
-  if (grouped && !nine(a[4], &gr)) OTHERWISE;
+  if (grouped && !groups_in(a[4], gr)) OTHERWISE;
   const int dim = grouped || THPVariable_Unpack(a[0]).dim() != 3 ? 2 : 3;
   const at::Tensor* codes = typed(a[0], ScalarType::Byte, dim, grouped ? gr.index : -1);
   if (!codes) OTHERWISE;
@@ -169,11 +209,13 @@ PyObject* rows_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.codes = address(*codes);
   r.scales = address(*scales);
   if ((r.codes | r.scales) % 16 || !scale_of(a[3], r.G, r.index, &r.g, &r.g_count)) OTHERWISE;
-  return as_nine(&r);
+  Py_INCREF(a[0]);
+  Py_INCREF(a[1]);
+  return rows_tuple(r, a[0], a[1], a[3]);
   CATCH
 }
 
-// route(logits, k, scoring, bias, n_group, topk_group, renormalize, scale, groups) -> (ids, w, None) or (ids, w, (buffer, tuple))
+// route(logits, k, scoring, bias, n_group, topk_group, renormalize, scale, groups) -> (ids, w, None or groups)
 PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
   if (n != 9) OTHERWISE;
@@ -207,19 +249,20 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                   ptr<int32_t>(g.order), ptr<int32_t>(g.place), ws, wb, s);
   if (st != MOE_OK) return raise(st);
   PyObject* third = Py_None;
-  if (group) third = Py_BuildValue("(NN)", THPVariable_Wrap(buf), as_nine(&g));
+  if (group)
+    third = Py_BuildValue("(LLLLLNLOO)", (long long)index, (long long)E, (long long)g.P, (long long)T, (long long)k, THPVariable_Wrap(buf), (long long)(2 * pairs), Py_None, Py_None);
   else Py_INCREF(third);
   return Py_BuildValue("(NNN)", THPVariable_Wrap(ids), THPVariable_Wrap(w), third);
   CATCH
 }
 
-// quantize(x, wdtype, g, groups) -> (codes, scales, tuple)
+// quantize(x, wdtype, g, groups) -> rows
 PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
   if (n != 4 || !THPVariable_Check(a[0])) OTHERWISE;
   Groups gr{};
   const bool grouped = a[3] != Py_None;
-  if (grouped && !nine(a[3], &gr)) OTHERWISE;
+  if (grouped && !groups_in(a[3], gr)) OTHERWISE;
   const int dim = grouped || THPVariable_Unpack(a[0]).dim() != 3 ? 2 : 3;
   const at::Tensor* x = tensor(a[0], dim, grouped ? gr.index : -1);
   if (!x) OTHERWISE;
@@ -240,7 +283,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       moe_quantize_fp4((int32_t)r.G, (int32_t)r.N, (int32_t)r.K, dt, x->data_ptr(), (int32_t)r.wdtype, ptr<float>(r.g), (int32_t)r.g_count, (int32_t)gr.E,
                        (int32_t)gr.k, ptr<int32_t>(gr.offsets), ptr<int32_t>(gr.tiles), ptr<int32_t>(gr.place), ptr<uint8_t>(r.codes), ptr<uint8_t>(r.scales), s);
   if (st != MOE_OK) return raise(st);
-  return Py_BuildValue("(NNN)", THPVariable_Wrap(codes), THPVariable_Wrap(scales), as_nine(&r));
+  return rows_tuple(r, THPVariable_Wrap(codes), THPVariable_Wrap(scales), a[2]);
   CATCH
 }
 
@@ -249,7 +292,8 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
   Rows r{};
   Groups gr{};
-  if (n != 4 || !nine(a[0], &r) || (a[1] != Py_None && !nine(a[1], &gr))) OTHERWISE;
+  const bool grouped = n == 4 && a[1] != Py_None;
+  if (n != 4 || (grouped && !groups_in(a[1], gr)) || !rows_in(a[0], grouped ? &gr : nullptr, r)) OTHERWISE;
   const long od = PyLong_AsLong(a[3]);
   void* s;
   if (!here(r.index, &s)) OTHERWISE;
@@ -266,7 +310,7 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
   Groups g{};
-  if (n != 6 || !nine(a[2], &g)) OTHERWISE;
+  if (n != 6 || !groups_in(a[2], g)) OTHERWISE;
   const at::Tensor *x = typed(a[0], ScalarType::BFloat16, 2, g.index), *w = typed(a[1], ScalarType::BFloat16, 3, g.index);
   if (!x || !w) OTHERWISE;
   const long act = PyLong_AsLong(a[3]), od = PyLong_AsLong(a[5]);
@@ -287,12 +331,12 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CATCH
 }
 
-// matmul_fp4(x rows, w rows, x's groups, groups, act, g_out or False, out dtype) -> tensor, or with a g_out (None = 1) (codes, scales, tuple)
+// matmul_fp4(x rows, w rows, x's groups, groups, act, g_out or False, out dtype) -> tensor, or with a g_out (None = 1) rows
 PyObject* matmul_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
   Rows x{}, w{};
   Groups xg{}, g{};
-  if (n != 7 || !nine(a[0], &x) || !nine(a[1], &w) || !nine(a[2], &xg) || !nine(a[3], &g)) OTHERWISE;
+  if (n != 7 || !groups_in(a[2], xg) || !groups_in(a[3], g) || !rows_in(a[0], &xg, x) || !rows_in(a[1], nullptr, w)) OTHERWISE;
   const long act = PyLong_AsLong(a[4]), od = PyLong_AsLong(a[6]);
   const bool quant = a[5] != Py_False;
   const int64_t cols = act ? w.N / 2 : w.N;
@@ -314,7 +358,7 @@ PyObject* matmul_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
       quant ? nullptr : out.data_ptr(), ptr<uint8_t>(r.codes), ptr<uint8_t>(r.scales), ptr<float>(r.g), s);
   if (st != MOE_OK) return raise(st);
   if (!quant) return THPVariable_Wrap(out);
-  return Py_BuildValue("(NNN)", THPVariable_Wrap(codes), THPVariable_Wrap(scales), as_nine(&r));
+  return rows_tuple(r, THPVariable_Wrap(codes), THPVariable_Wrap(scales), a[5]);
   CATCH
 }
 
@@ -322,7 +366,7 @@ PyObject* matmul_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
   Groups g{};
-  if (n != 4 || !nine(a[1], &g)) OTHERWISE;
+  if (n != 4 || !groups_in(a[1], g)) OTHERWISE;
   const at::Tensor *y = tensor(a[0], 2, g.index), *w = typed(a[2], ScalarType::Float, 2, g.index);
   if (!y || !w) OTHERWISE;
   const int dt = float_code(*y);
@@ -337,15 +381,14 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CATCH
 }
 
-// views(buffer, groups) -> (offsets, tiles, order, place) of the buffer that holds them
+// views(groups) -> (offsets, tiles, order, place) of groups whose buffer holds them
 PyObject* views(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
   Groups g{};
-  if (n != 2 || !nine(a[1], &g)) OTHERWISE;
-  const at::Tensor* b = tensor(a[0], 1, g.index);
-  if (!b) OTHERWISE;
-  const int64_t base = (int64_t)(uintptr_t)b->storage().data();
-  auto part = [&](int64_t p, at::IntArrayRef shape) { return THPVariable_Wrap(on(*b, p - base, shape, ScalarType::Int)); };
+  if (n != 1 || !groups_in(a[0], g) || !PyLong_Check(PyTuple_GET_ITEM(a[0], 6))) OTHERWISE;
+  const at::Tensor& b = THPVariable_Unpack(PyTuple_GET_ITEM(a[0], 5));
+  const int64_t base = (int64_t)(uintptr_t)b.storage().data();
+  auto part = [&](int64_t p, at::IntArrayRef shape) { return THPVariable_Wrap(on(b, p - base, shape, ScalarType::Int)); };
   PyObject *off = part(g.offsets, {g.E + 1}), *til = part(g.tiles, {g.E + 1}), *order = part(g.order, {g.P}), *place = part(g.place, {g.T, g.k});
   return Py_BuildValue("(NNNN)", off, til, order, place);
   CATCH

@@ -109,7 +109,7 @@ def _stream(index):
 def _again(call, index, stream):
     """Make a call that was left alone again, on its own device and stream, now that its arguments are right."""
     if stream is None and index == torch.cuda.current_device():
-        raise RuntimeError("the call was not made: its arguments pass every check here")
+        raise ValueError("the call was not made: tensors that its groups or 4-bit rows hold were resized, moved or replaced since")
     with _On(index, stream):
         return call()
 
@@ -149,9 +149,10 @@ def _scale(g, name, most, index):
 
 class ExpertGroups:
     """The (token, expert) pairs of a call in expert order: offsets and tiles [E + 1], order [T * k] and
-    place [T, k], all int32 (include/moe_operators.h, "Expert order").  Checked here, once, and not changed after."""
+    place [T, k], all int32 (include/moe_operators.h, "Expert order").  Types and sizes are checked here; the tensors
+    cannot be exchanged after.  What they hold is not looked at: it has to be a grouping, such as route and group_pairs make."""
 
-    __slots__ = ("_c", "_buffer", "_views")
+    __slots__ = ("_c", "_views")
 
     def __init__(self, offsets, tiles, order, place):
         self._c = _host().groups_of(offsets, tiles, order, place)
@@ -164,18 +165,18 @@ class ExpertGroups:
             if tiles.numel() != offsets.numel() or not 2 <= offsets.numel() <= 4097:
                 raise ValueError(f"offsets and tiles must hold E + 1 values each (1 <= E <= 4096), hold {offsets.numel()} and {tiles.numel()}")
             raise ValueError(f"order holds {order.numel()} pairs, place {place.numel()}")
-        self._buffer, self._views = None, (offsets, tiles, order, place)
+        self._views = self._c[5:]
 
     @classmethod
-    def _of(cls, buffer, c):
-        """Of one buffer that holds all four, and the host module's tuple."""
+    def _of(cls, c):
+        """Of the host module's tuple, with all four in one buffer."""
         self = cls.__new__(cls)
-        self._buffer, self._c, self._views = buffer, c, None
+        self._c, self._views = c, None
         return self
 
     def _view(self, i):
         if self._views is None:
-            self._views = _host().views(self._buffer, self._c)
+            self._views = _host().views(self._c)
         return self._views[i]
 
     _index = property(lambda self: self._c[0])
@@ -206,9 +207,9 @@ class FP4Rows:
     """4-bit matrices: codes uint8 [..., K/2] and scale tiles uint8 [row tiles, block groups, 512]
     (include/moe_operators.h, "4-bit matrices"), wdtype "nvfp4" or "mxfp4", g the fp32 matrix scales (1 or one
     per matrix; None = 1).  groups: of rows in expert order; None for a stack of matrices [G, N, K] or one [N, K].
-    Checked here, once, and not changed after."""
+    Types and sizes are checked here; the tensors cannot be exchanged after."""
 
-    __slots__ = ("codes", "scales", "wdtype", "g", "groups", "_c")
+    __slots__ = ("_wdtype", "_groups", "_c")
 
     def __init__(self, codes, scales, wdtype, g=None, groups=None):
         if wdtype not in FP4_BLOCK:
@@ -216,7 +217,7 @@ class FP4Rows:
         self._c = _host().rows_of(codes, scales, DTYPES[wdtype], g, _described(groups))
         if self._c is None:
             self._refuse(codes, scales, wdtype, g, groups)
-        self.codes, self.scales, self.wdtype, self.g, self.groups = codes, scales, wdtype, g, groups
+        self._wdtype, self._groups = wdtype, groups
 
     @staticmethod
     def _refuse(codes, scales, wdtype, g, groups):
@@ -242,13 +243,18 @@ class FP4Rows:
         raise ValueError("codes and scales must be 16-byte aligned")
 
     @classmethod
-    def _of(cls, codes, scales, wdtype, g, groups, c):
-        """Of what the host module has allocated and described."""
+    def _of(cls, wdtype, groups, c):
+        """Of the host module's tuple."""
         self = cls.__new__(cls)
-        self.codes, self.scales, self.wdtype, self.g, self.groups, self._c = codes, scales, wdtype, g, groups, c
+        self._wdtype, self._groups, self._c = wdtype, groups, c
         return self
 
     _index = property(lambda self: self._c[0])
+    codes = property(lambda self: self._c[5])
+    scales = property(lambda self: self._c[6])
+    wdtype = property(lambda self: self._wdtype)
+    g = property(lambda self: self._c[7])
+    groups = property(lambda self: self._groups)
     K = property(lambda self: self._c[3])
     shape = property(lambda self: (*self.codes.shape[:-1], self._c[3]))
 
@@ -261,7 +267,7 @@ def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=
     if stream is None:
         r = (_host_module or _host()).route(logits, top_k, SCORING.get(scoring, -1), bias, n_group, topk_group, renormalize, scale, groups)
         if r is not None:
-            return (r[0], r[1], ExpertGroups._of(*r[2])) if groups else r[:2]
+            return (r[0], r[1], ExpertGroups._of(r[2])) if groups else r[:2]
     _floats(logits, "logits", 2)
     E, k, index = logits.shape[1], int(top_k), logits.get_device()
     if scoring not in SCORING:
@@ -300,7 +306,7 @@ def group_pairs(topk_ids, n_experts, *, stream=None):
     order = til + 4 * (E + 1)
     place = order + 4 * P
     _check(ops.moe_group_pairs(T, E, k, topk_ids.data_ptr(), off, til, order, place, place + 4 * P if ws else None, ws, _stream(index)))
-    return ExpertGroups._of(buffer, (index, E, P, T, k, off, til, order, place))
+    return ExpertGroups._of((index, E, P, T, k, buffer, 0, None, None))
 
 
 def fp4_scale(x, *, stream=None):
@@ -327,7 +333,7 @@ def quantize_fp4(x, wdtype, *, g=None, groups=None, stream=None):
     if stream is None:
         r = (_host_module or _host()).quantize(x, DTYPES[wdtype], g, _described(groups))
         if r is not None:
-            return FP4Rows._of(r[0], r[1], wdtype, g, groups, r[2])
+            return FP4Rows._of(wdtype, groups, r)
     dim = 2 if groups is not None or not isinstance(x, torch.Tensor) or x.dim() != 3 else 3
     _floats(x, "x", dim)
     index, K = x.get_device(), x.shape[-1]
@@ -409,7 +415,7 @@ def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, 
             w.codes.dim() == 3 and w.groups is None and (quantize or g_out is None):
         out = (_host_module or _host()).matmul_fp4(x._c, w._c, x.groups._c, groups._c, ACTS[act], g_out if quantize else False, _FLOATS[out_dtype])
         if out is not None:
-            return FP4Rows._of(out[0], out[1], x.wdtype, g_out, groups, out[2]) if quantize else out
+            return FP4Rows._of(x.wdtype, groups, out) if quantize else out
     index = w._index
     _groups_on(groups, index)
     if w.codes.dim() != 3 or w.groups is not None:

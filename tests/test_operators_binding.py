@@ -67,3 +67,46 @@ with FakeTensorMode(allow_non_fake_inputs=True):
 
 def test_integers_are_not_groups():
     assert run(NINE_INTEGERS).startswith("refused groups must be ExpertGroups")
+
+
+def cpu_rows(groups=None):
+    """FP4Rows as the binding makes them, of CPU memory that no kernel sees."""
+    import torch
+
+    import serving_layer_moe_gb300 as moe
+    codes, scales, g = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(1, 1, 512, dtype=torch.uint8), torch.ones(1)
+    return moe.FP4Rows._of("nvfp4", groups, (0, 1, 4, 64, 3, codes, scales, g, 1))
+
+
+def test_copies_of_rows_and_groups_have_their_own_memory():
+    """No address is kept: all that a copy holds is its own tensors."""
+    import copy
+    import pickle
+
+    import torch
+
+    import serving_layer_moe_gb300 as moe
+    gr = moe.ExpertGroups._of((0, 4, 4, 2, 2, torch.zeros(18, dtype=torch.int32), 0, None, None))
+    q = cpu_rows(gr)
+    for d in (copy.deepcopy(q), pickle.loads(pickle.dumps(q))):
+        mine = [q.codes, q.scales, q.g, q.groups._c[5]]
+        theirs = [d.codes, d.scales, d.g, d.groups._c[5]]
+        assert {t.data_ptr() for t in mine}.isdisjoint(t.data_ptr() for t in theirs)
+        addresses = {t.data_ptr() for t in mine}
+        assert not addresses & {v for v in (*d._c, *d.groups._c) if isinstance(v, int)}
+        assert all(any(v is t for v in (*d._c, *d.groups._c)) for t in theirs)
+        assert (d.wdtype, d.shape, d.groups.E) == ("nvfp4", (4, 64), 4)
+
+
+def test_rows_and_groups_do_not_change():
+    import torch
+
+    import serving_layer_moe_gb300 as moe
+    q = cpu_rows()
+    for name in ("codes", "scales", "wdtype", "g", "groups", "K", "shape"):
+        with pytest.raises(AttributeError):
+            setattr(q, name, None)
+    gr = moe.ExpertGroups._of((0, 4, 4, 2, 2, torch.zeros(18, dtype=torch.int32), 0, None, None))
+    for name in ("offsets", "tiles", "order", "place", "E", "P", "T", "k"):
+        with pytest.raises(AttributeError):
+            setattr(gr, name, None)
