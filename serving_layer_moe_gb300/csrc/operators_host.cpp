@@ -236,21 +236,24 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bias = typed(a[3], ScalarType::Float, 1, index);
     if (!bias || bias->numel() != E) OTHERWISE;
   }
-  // ids, gates, and with groups their four arrays and the workspace
+  // ids, gates, and with groups their four arrays: in one allocation where there are few pairs.  Otherwise the groups have one of
+  // their own, so that keeping or saving ids does not keep them, and the workspace goes when the call returns.
   const int64_t pairs = 4 * T * k, bins = 4 * (E + 1), wb = group ? moe_group_workspace((int32_t)T, (int32_t)k, (int32_t)E) : 0;
-  const at::Tensor buf = room(2 * pairs + (group ? 2 * bins + 2 * pairs + wb : 0), index);
-  const at::Tensor ids = on(buf, 0, {T, k}, ScalarType::Int), w = on(buf, pairs, {T, k}, ScalarType::Float);
-  const int64_t base = address(buf);
+  const int64_t many = group ? 2 * bins + 2 * pairs : 0;
+  const at::Tensor both = room(2 * pairs + (wb ? 0 : many), index), buf = wb ? room(many, index) : both;
+  at::Tensor ws;
+  if (wb) ws = room(wb, index);
+  const at::Tensor ids = on(both, 0, {T, k}, ScalarType::Int), w = on(both, pairs, {T, k}, ScalarType::Float);
+  const int64_t from = wb ? 0 : 2 * pairs, base = address(buf) + from;
   Groups g{};
-  if (group) g = Groups{index, E, T * k, T, k, base + 2 * pairs, base + 2 * pairs + bins, base + 2 * pairs + 2 * bins, base + 3 * pairs + 2 * bins};
-  void* ws = wb ? ptr<void>(base + 4 * pairs + 2 * bins) : nullptr;
+  if (group) g = Groups{index, E, T * k, T, k, base, base + bins, base + 2 * bins, base + 2 * bins + pairs};
   const moe_status st = moe_route((int32_t)T, (int32_t)E, (int32_t)k, dt, x->data_ptr(), (int32_t)sc, bias ? bias->data_ptr<float>() : nullptr, (int32_t)ng,
-                                  (int32_t)tg, renorm, (float)scale, ptr<int32_t>(base), ptr<float>(base + pairs), ptr<int32_t>(g.offsets), ptr<int32_t>(g.tiles),
-                                  ptr<int32_t>(g.order), ptr<int32_t>(g.place), ws, wb, s);
+                                  (int32_t)tg, renorm, (float)scale, ids.data_ptr<int32_t>(), w.data_ptr<float>(), ptr<int32_t>(g.offsets), ptr<int32_t>(g.tiles),
+                                  ptr<int32_t>(g.order), ptr<int32_t>(g.place), wb ? ws.data_ptr() : nullptr, wb, s);
   if (st != MOE_OK) return raise(st);
   PyObject* third = Py_None;
   if (group)
-    third = Py_BuildValue("(LLLLLNLOO)", (long long)index, (long long)E, (long long)g.P, (long long)T, (long long)k, THPVariable_Wrap(buf), (long long)(2 * pairs), Py_None, Py_None);
+    third = Py_BuildValue("(LLLLLNLOO)", (long long)index, (long long)E, (long long)g.P, (long long)T, (long long)k, THPVariable_Wrap(buf), (long long)from, Py_None, Py_None);
   else Py_INCREF(third);
   return Py_BuildValue("(NNN)", THPVariable_Wrap(ids), THPVariable_Wrap(w), third);
   CATCH

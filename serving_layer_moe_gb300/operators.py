@@ -263,7 +263,8 @@ def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=
           groups=False, stream=None):
     """Experts and gates of each token: (topk_ids int32 [T, k], topk_w fp32 [T, k]), or with groups=True also the
     ExpertGroups of the picked pairs.  logits [T, E] fp32 or bf16; scoring "softmax" (by logit) or "sigmoid"
-    (with an optional selection bias [E] and topk_group of n_group expert groups): moe_route."""
+    (with an optional selection bias [E] and topk_group of n_group expert groups): moe_route.  ids and
+    gates share an allocation, with the groups too up to 256 pairs."""
     if stream is None:
         r = (_host_module or _host()).route(logits, top_k, SCORING.get(scoring, -1), bias, n_group, topk_group, renormalize, scale, groups)
         if r is not None:
@@ -300,12 +301,14 @@ def group_pairs(topk_ids, n_experts, *, stream=None):
         return _again(lambda: group_pairs(topk_ids, E), index, stream)
     ops = _operators()
     ws, P = ops.moe_group_workspace(T, k, E), T * k
-    buffer = torch.empty(2 * (E + 1 + P) + ws // 4, dtype=_I32, device=topk_ids.device)      # the workspace last
+    buffer = torch.empty(2 * (E + 1 + P), dtype=_I32, device=topk_ids.device)
+    scratch = torch.empty(ws // 4, dtype=_I32, device=topk_ids.device) if ws else None
     off = buffer.data_ptr()
     til = off + 4 * (E + 1)
     order = til + 4 * (E + 1)
     place = order + 4 * P
-    _check(ops.moe_group_pairs(T, E, k, topk_ids.data_ptr(), off, til, order, place, place + 4 * P if ws else None, ws, _stream(index)))
+    _check(ops.moe_group_pairs(T, E, k, topk_ids.data_ptr(), off, til, order, place, scratch.data_ptr() if ws else None, ws,
+                                _stream(index)))
     return ExpertGroups._of((index, E, P, T, k, buffer, 0, None, None))
 
 

@@ -59,3 +59,15 @@ def test_resized_tensors_are_found_or_refused(moe):
     y = torch.zeros(gr.P, 8, device="cuda")
     with pytest.raises(ValueError, match="resized"):
         moe.combine(y, held, gates)
+
+
+@pytest.mark.parametrize("T,E,k", [(40, 200, 2), (2000, 256, 8)])
+def test_results_keep_their_own_memory_only(moe, T, E, k):
+    """No result of route or group_pairs keeps the grouping's scratch; ids and gates of many pairs
+    do not keep the groups."""
+    ids, w, gr = moe.route(torch.randn(T, E, device="cuda"), k, groups=True)
+    P, four = T * k, 4 * 2 * (E + 1 + T * k)
+    most = {ids: 8 * P, w: 8 * P, gr.order: four} if P > 256 else {ids: 8 * P + four, w: 8 * P + four, gr.order: 8 * P + four}
+    for t, n in most.items():
+        assert t.untyped_storage().nbytes() == n, (tuple(t.shape), t.untyped_storage().nbytes(), n)
+    assert moe.group_pairs(ids, E).order.untyped_storage().nbytes() == four
