@@ -57,7 +57,7 @@ constexpr int SUM_SLICES = 4;                  // fp32 results: K slices summed 
 constexpr int SMEM_LIMIT = 227 * 1024;
 
 struct ProductArgs {
-  int P, E, N, K, k, cols, groups, gw_count, act, gather, out_f32, quant, wide, exact, few;
+  int P, E, N, K, k, cols, groups, gw_count, act, gather, quant, wide, few;
   int m_blocks, kslices, stages, stage_bytes, b_rows, w_tiles, w_parts;   // w_parts: scale tiles one weight tile's rows are in
   const float *gx, *gw, *g_out;
   const int32_t *offsets, *order;
@@ -80,7 +80,7 @@ struct Shape4 {
   // TMEM column of the second accumulator.  4-bit pairs: the two overlap in 64 columns, to leave room for the scales
   static constexpr int ACC_COLS = CG == 1 ? 128 : FP4 ? 192 : 256;
   static constexpr bool OVERLAP = FP4 && CG == 2;
-  static constexpr bool EXACT = !FP4 && CG == 1;        // has the forms for fp32 results and for gathered rows
+  static constexpr bool GATHER = !FP4 && CG == 1;       // has the form for gathered rows
   static constexpr int BOX = 16 * CG;                   // token rows of a small load; a tile's 128 rows take one
 };
 
@@ -118,7 +118,7 @@ template <int FMT, int CG>
 __device__ __forceinline__ int token_rows(const ProductArgs& a, const Item& o) {
   using S = Shape4<FMT, CG>;
   const int mine = columns<CG>(o.n) / CG;
-  if (S::EXACT && a.gather) return (o.n + 3) & ~3;   // single CTAs; the columns past the rows are not used
+  if (S::GATHER && a.gather) return (o.n + 3) & ~3;   // single CTAs; the columns past the rows are not used
   return a.b_rows == 128 && mine > 3 * S::BOX ? 128 : (mine + S::BOX - 1) / S::BOX * S::BOX;
 }
 
@@ -156,7 +156,7 @@ __device__ __forceinline__ void issue_slice(uint32_t d, uint32_t tmem, uint64_t 
 
 // h[j] = silu(gate[j] g) * up[j] g of two values; e = -g log2 e.  exp by ex2.approx and one rcp.approx for both quotients
 // (1 / a = b / (a b); the special function unit is what an epilogue of short K waits for).  Two units each, and the rounded
-// argument adds |gate g| units: far inside bf16 and 4-bit results, 2e-6 at most where fp32 ones matter (|gate g| < 32).
+// argument adds |gate g| units: far inside bf16 and 4-bit results (fp32 ones: silu below).
 // Past 2^60 the exponential stays there: silu is then below 1e-16 of the gate.
 __device__ __forceinline__ void swiglu2(uint32_t gate0, uint32_t gate1, uint32_t up0, uint32_t up1, float g, float e, float& h0, float& h1) {
   const float a = __uint_as_float(gate0), b = __uint_as_float(gate1);
@@ -170,21 +170,31 @@ __device__ __forceinline__ void swiglu2(uint32_t gate0, uint32_t gate1, uint32_t
   h1 = b * g * (r * x) * (__uint_as_float(up1) * g);
 }
 
+// silu(x) = x / (1 + exp(-x)) of fp32 results, within ten half units.  exp(-x) = 2^t 2^r with t the rounded product -x log2 e and r
+// what the rounding and log2 e's own have left out, |r| < 2^-17: 2^r = 1 + r ln 2.  (65536 rows of 128 experts, K 768, N 2048,
+// MXFP4, fp32 results: 195 us, with expf and a division 293.)  Past -128 the exponential is infinite all the same.
+__device__ __forceinline__ float silu(float x) {
+  const float c = fmaxf(x, -128.0f), t = c * -1.44269502f, r = fmaf(c, -1.44269502f, -t) - c * 1.92596303e-8f;
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+  if (e < INFINITY) e = fmaf(e, r * 0.693147181f, e);
+  return __fdividef(x, 1.0f + e);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ uint32_t pack_bf16(uint32_t a, uint32_t b, float g) { return pack_bf16(__uint_as_float(a) * g, __uint_as_float(b) * g); }
-__device__ __forceinline__ void store_one(const ProductArgs& a, size_t at, float v) {
-  if (a.out_f32) static_cast<float*>(a.out)[at] = v;
-  else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
-}
+__device__ __forceinline__ void store_one(const ProductArgs& a, size_t at, float v) { static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v); }
 
-// The epilogue of fp32 results.  The tensor cores truncate what they add to an accumulator: over K = 1944 the result is 2e-6 off,
-// where fp32 additions that round leave 1e-7.  So an accumulator holds SUM_SLICES slices only (16 additions), and this adds them
-// up in registers: 64 columns a warp, with the registers of the single-CTA form's 128.  false: a wait has run out.
-__device__ __forceinline__ bool exact_tile(const ProductArgs& a, const Item& o, uint32_t tmem, uint32_t tfull, uint32_t tempty, int& acc, uint32_t& acc_phase,
-                                           volatile int* abort_flag, int q, int part) {
+// The epilogue of fp32 results, times g.  The tensor cores truncate what they add to an accumulator: bf16 operands over K = 1944 are
+// 2e-6 off, where fp32 additions that round leave 1e-7; 4-bit ones whose block scales vary by e^2 are 3e-6 off over K = 7168.  So an
+// accumulator holds SUM_SLICES slices only (16 additions), and this adds them up in registers: 64 columns a warp, with the
+// registers of the single-CTA form's 128.  false: a wait has run out.
+template <bool FP4>
+__device__ __forceinline__ bool exact_tile(const ProductArgs& a, const Item& o, float g, uint32_t tmem, uint32_t tfull, uint32_t tempty, int& acc,
+                                           uint32_t& acc_phase, volatile int* abort_flag, int q, int part) {
   const int lane = threadIdx.x & 31;
   float lo[2][16] = {}, hi[2][16] = {};
   for (int k0 = 0; k0 < a.kslices; k0 += SUM_SLICES) {
@@ -212,24 +222,30 @@ __device__ __forceinline__ bool exact_tile(const ProductArgs& a, const Item& o, 
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int t = 64 * part + 32 * h + 8 * (i >> 2) + 2 * (lane & 3) + (i & 1);
-      if (t >= o.n) continue;
-      float* out = static_cast<float*>(a.out) + (size_t)(o.row0 + t) * a.cols;
-      const int f = (lane >> 2) + 4 * (i & 2);
-      if (a.act) {
-        const int c = o.mb * 64 + 16 * q + f;
-        if (c < a.cols) out[c] = lo[h][i] / (1.0f + expf(-lo[h][i])) * hi[h][i];
-      } else {
-        const int c = o.mb * 128 + 32 * q + f;
-        if (c < a.cols) out[c] = lo[h][i];
-        if (c + 16 < a.cols) out[c + 16] = hi[h][i];
+    for (int i0 = 0; i0 < 16; i0 += 4) {
+      const int t0 = 64 * part + 32 * h + 2 * i0;
+      if (t0 >= o.n) continue;   // eight tokens, of all lanes
+#pragma unroll
+      for (int i = i0; i < i0 + 4; ++i) {
+        const int t = t0 + 2 * (lane & 3) + (i & 1), f = (lane >> 2) + 4 * (i & 2);
+        float* out = static_cast<float*>(a.out) + (size_t)(o.row0 + t) * a.cols;
+        const float x = FP4 ? lo[h][i] * g : lo[h][i], y = FP4 ? hi[h][i] * g : hi[h][i];
+        if (a.act) {
+          const int c = o.mb * 64 + 16 * q + f;
+          const float v = silu(x) * y;
+          if (t < o.n && c < a.cols) out[c] = v;
+        } else {
+          const int c = o.mb * 128 + 32 * q + f;
+          if (t < o.n && c < a.cols) out[c] = x;
+          if (t < o.n && c + 16 < a.cols) out[c + 16] = y;
+        }
       }
     }
   return true;
 }
 
-template <int FMT, int CG>
+// EXACT (CG = 1): fp32 results
+template <int FMT, int CG, bool EXACT>
 __global__ void __launch_bounds__(THREADS, 1)
 product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                const __grid_constant__ CUtensorMap tmXall, const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX, const ProductArgs a) {
@@ -336,7 +352,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0, slot = 0;
       bool ok = true;
-      const int sum = S::EXACT && a.exact ? SUM_SLICES : a.kslices;   // slices of an accumulator
+      const int sum = EXACT ? SUM_SLICES : a.kslices;   // slices of an accumulator
       const uint64_t da = desc_sw128(ring), db = desc_sw128(ring + A_BYTES), ds = desc_scales(ring + A_BYTES + a.b_rows * 128);
       for (int it = it0; it < it1 && ok; it += step) {
         item_at<FMT, CG>(a, first, it, o);
@@ -380,7 +396,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     for (int it = it0; it < it1 && ok; it += step) {
       item_at<FMT, CG>(a, first, it, o);
       const int row0 = o.row0 + (int)rank * (columns<CG>(o.n) / CG), rows = token_rows<FMT, CG>(a, o);
-      if (S::EXACT && a.gather) {
+      if (S::GATHER && a.gather) {
         __syncwarp();
         for (int r = lane; r < rows; r += 32) gathered[r] = __ldg(a.order + row0 + min(r, o.n - 1)) / a.k;
         __syncwarp();
@@ -390,7 +406,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const uint32_t sb = ring + stage * a.stage_bytes + A_BYTES;
         const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
         const int x = ks * (S::FP4 ? 128 : 64);
-        if (S::EXACT && a.gather) {
+        if (S::GATHER && a.gather) {
           if (elect_one()) {
 #pragma unroll 4
             for (int r = 0; r < rows; r += 4)
@@ -478,15 +494,13 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     uint32_t acc_phase = 0;
     for (int it = it0; it < it1; it += step) {
       item_at<FMT, CG>(a, first, it, o);
-      if constexpr (S::EXACT) {
-        if (a.exact) {
-          if (!exact_tile(a, o, tmem, tfull, tempty, acc, acc_phase, abort_flag, q, part)) break;
-          continue;
-        }
-      }
       // what the tile needs from memory, on its way while the products run
       float g = 1.0f;
       if (S::FP4) g = (a.gx ? __ldg(a.gx) : 1.0f) * (a.gw ? __ldg(a.gw + (a.gw_count > 1 ? o.e : 0)) : 1.0f);
+      if constexpr (EXACT) {
+        if (!exact_tile<S::FP4>(a, o, g, tmem, tfull, tempty, acc, acc_phase, abort_flag, q, part)) break;
+        continue;
+      }
       const float go = S::NV && a.quant && a.g_out ? __ldg(a.g_out) : 1.0f, rgo = __frcp_rn(go);
       const int64_t pad0 = S::FP4 && a.quant ? (int64_t)__ldg(a.tiles + o.e) * 128 + (o.row0 - __ldg(a.offsets + o.e)) : 0;
       bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
@@ -658,7 +672,7 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* ba
 
 struct ProductMem { const void *x, *w, *x_scales, *w_scales; int x_rows; };
 
-template <int FMT, int CG>
+template <int FMT, int CG, bool EXACT>
 moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   using S = Shape4<FMT, CG>;
   const uint64_t row_bytes = S::FP4 ? (uint64_t)a.K / 2 : (uint64_t)a.K * 2;
@@ -668,7 +682,7 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   a.m_blocks = (int)ceil_div64(a.act ? a.cols : a.N, (a.act ? 64 : 128) * CG);
   a.kslices = (a.K + S::KS - 1) / S::KS;
   a.w_tiles = (a.N + 127) / 128;
-  a.wide = !a.quant && !a.out_f32 && a.cols % 8 == 0;   // rows of out start on 16 bytes
+  a.wide = !a.quant && !EXACT && a.cols % 8 == 0;   // rows of out start on 16 bytes
   // rows of the token area: what the largest tile of P rows can need
   a.b_rows = std::min(128, (a.P + 15) / 16 * 16);
   if (CG == 2) a.b_rows = 128;
@@ -717,7 +731,7 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   CK(cudaGetDevice(&dev));
   if (dev < 0 || dev >= 64) return fail(MOE_EINVAL, "device %d is out of range", dev);
   if (!allowed[dev]) {
-    CK(cudaFuncSetAttribute(product_kernel<FMT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT));
+    CK(cudaFuncSetAttribute(product_kernel<FMT, CG, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT));
     allowed[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
@@ -740,7 +754,7 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
       int n = 0;
       cfg.gridDim = dim3(operator_sms() / 2 * 2);
       cfg.dynamicSmemBytes = SMEM_LIMIT;
-      CK(cudaOccupancyMaxActiveClusters(&n, product_kernel<FMT, CG>, &cfg));
+      CK(cudaOccupancyMaxActiveClusters(&n, product_kernel<FMT, CG, EXACT>, &cfg));
       if (n < 1) return fail(MOE_ECUDA, "no CTA pair fits the device");
       pairs[dev] = n;
       cfg.dynamicSmemBytes = smem;
@@ -749,7 +763,7 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   }
   const int units = (int)std::min<int64_t>(most, resident);
   cfg.gridDim = dim3(units * CG);
-  CK(cudaLaunchKernelEx(&cfg, product_kernel<FMT, CG>, tw, tx, txall, tsw, tsx, a));
+  CK(cudaLaunchKernelEx(&cfg, product_kernel<FMT, CG, EXACT>, tw, tx, txall, tsw, tsx, a));
   return MOE_OK;
 }
 
@@ -757,13 +771,15 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
 // us of gate/up (K 2048, N 1536, 128 experts), single and in pairs, by rows an expert: bf16 1 row 75.9 / 73.7, 4 rows 114.3 / 109.1,
 // 64 rows 178.9 / 138.4; rows gathered (before the product for pairs, in it otherwise) 1 row 75.9 / 80.2, 4 rows 119.0 / 118.6,
 // 16 rows 249.7 / 136.0; NVFP4 4 rows 38.0 / 40.1, 64 rows 49.1 / 50.4, 128 rows 66.8 / 56.2 (K 7168, N 4096, 64 rows 32.7 / 28.5).
-// fp32 results of bf16 products take single CTAs (exact_tile).
-bool use_pairs(int64_t P, int64_t E, bool fp4, bool exact) { return !exact && P >= (fp4 ? 64 : 4) * E; }
+// fp32 results take single CTAs (exact_tile): NVFP4, 65536 rows of 128 experts, K 2048, N 1536 184 us, in pairs without the short
+// sums 199; 16384 rows of 32 experts, K 7168, N 4096 327 and 195.
+bool use_pairs(int64_t P, int64_t E, bool fp4) { return P >= (fp4 ? 64 : 4) * E; }
 
 template <int FMT>
-moe_status launch_product(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
+moe_status launch_product(ProductArgs a, const ProductMem& mem, bool exact, cudaStream_t s) {
   a.few = a.P < 64 * (int64_t)a.E;
-  return use_pairs(a.P, a.E, FMT != MOE_BF16, a.exact) ? launch_tiles<FMT, 2>(a, mem, s) : launch_tiles<FMT, 1>(a, mem, s);
+  if (exact) return launch_tiles<FMT, 1, true>(a, mem, s);
+  return use_pairs(a.P, a.E, FMT != MOE_BF16) ? launch_tiles<FMT, 2, false>(a, mem, s) : launch_tiles<FMT, 1, false>(a, mem, s);
 }
 
 // xs[place[t, j]] = x[t]: a row is read once and stored k times, two 16-byte units a lane of a warp's segment.  A pair's token
@@ -811,7 +827,7 @@ using namespace moe;
 
 extern "C" int64_t moe_grouped_matmul_workspace(int32_t P, int32_t E, int32_t K, int32_t gather) {
   // many rows of an expert are gathered once, before the product
-  return gather && P > 0 && use_pairs(P, E, false, false) ? (int64_t)P * K * 2 : 0;
+  return gather && P > 0 && use_pairs(P, E, false) ? (int64_t)P * K * 2 : 0;
 }
 
 extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const void* x, int32_t x_rows,
@@ -827,7 +843,7 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
   if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(out, 16)) return fail(MOE_EINVAL, "x, w and out must be 16-byte aligned");
   ProductArgs a{};
   a.P = P; a.E = E; a.N = N; a.K = K; a.k = k; a.act = act; a.cols = act ? N / 2 : N; a.gather = order != nullptr;
-  a.out_f32 = a.exact = out_dtype == MOE_F32; a.order = order; a.offsets = offsets; a.tiles = tiles; a.out = out;
+  a.order = order; a.offsets = offsets; a.tiles = tiles; a.out = out;
   const int64_t need = moe_grouped_matmul_workspace(P, E, K, a.gather);
   if (need) {
     if (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))
@@ -840,7 +856,7 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
     x = workspace;
     x_rows = P;
   }
-  return launch_product<MOE_BF16>(a, ProductMem{x, w, nullptr, nullptr, x_rows}, static_cast<cudaStream_t>(stream));
+  return launch_product<MOE_BF16>(a, ProductMem{x, w, nullptr, nullptr, x_rows}, out_dtype == MOE_F32, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, int32_t K, int32_t wdtype,
@@ -869,12 +885,13 @@ extern "C" moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, in
   ProductArgs a{};
   a.P = P; a.E = E; a.N = N; a.K = K; a.k = 1; a.act = act; a.cols = act ? N / 2 : N;
   a.groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
-  a.quant = !out; a.out_f32 = out_dtype == MOE_F32;
+  a.quant = !out;
   a.gx = gx; a.gw = gw; a.gw_count = gw_count;
   a.offsets = offsets; a.tiles = tiles; a.out = out; a.out_codes = out_codes; a.out_scales = out_scales; a.g_out = g_out;
   const ProductMem mem{x_codes, w_codes, x_scales, w_scales, P};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return wdtype == MOE_NVFP4 ? launch_product<MOE_NVFP4>(a, mem, s) : launch_product<MOE_MXFP4>(a, mem, s);
+  const bool exact = out && out_dtype == MOE_F32;
+  return wdtype == MOE_NVFP4 ? launch_product<MOE_NVFP4>(a, mem, exact, s) : launch_product<MOE_MXFP4>(a, mem, exact, s);
 }
 
 extern "C" moe_status moe_operators_check(void* stream) {

@@ -3,6 +3,9 @@ import numpy as np
 import pytest
 import torch
 
+from tests import operators_reference as ref
+from tests.test_operators_gpu import EPS, bf16, dev, host, make_ids
+
 pytestmark = pytest.mark.gpu
 
 
@@ -71,3 +74,74 @@ def test_results_keep_their_own_memory_only(moe, T, E, k):
     for t, n in most.items():
         assert t.untyped_storage().nbytes() == n, (tuple(t.shape), t.untyped_storage().nbytes(), n)
     assert moe.group_pairs(ids, E).order.untyped_storage().nbytes() == four
+
+
+# ---------------------------------------------------------------------------------------------------------
+# fp32 results
+# ---------------------------------------------------------------------------------------------------------
+def distance(got, want):
+    return np.linalg.norm(got - want) / np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("K", [1944, 7168])
+@pytest.mark.parametrize("counts", [[70, 80, 75, 75], [3, 1, 2, 4]])
+def test_fp32_results_of_bf16_products_add_up(moe, counts, K):
+    """An accumulator that truncates, by half a unit (2^-24 of the sum or less) on average, takes 16 additions to a sum that grows
+    to its size: 16 * 0.75 * 2^-24 * 2/3 = 4.8e-7 of it.  All of K = 1944 in one, 122 additions: 3.6e-6."""
+    rng = np.random.default_rng(K)
+    ids = make_ids(rng, counts, sum(counts), 1)
+    gr, (offsets, _, _, _) = moe.group_pairs(dev(ids), len(counts)), ref.groups(ids, len(counts))
+    x, w = bf16(rng.standard_normal((sum(counts), K))), bf16(rng.standard_normal((len(counts), 96, K)))
+    y, _ = ref.product(x.astype(np.float64), w.astype(np.float64), offsets)
+    got = host(moe.grouped_matmul(dev(x, torch.bfloat16), dev(w, torch.bfloat16), gr, out_dtype=torch.float32))
+    assert distance(got, y) < 5e-7
+
+
+def rows_of_uneven_blocks(rng, wdtype, R, K, rows, tiles):
+    """Rows whose blocks' sizes differ by a factor of e^2 (one standard deviation), 4-bit: packed codes, tiles, g, values."""
+    B = ref.BLOCK[wdtype]
+    size = np.repeat(np.exp(2 * rng.standard_normal((R, K // B))), B, axis=1)
+    x = (rng.standard_normal((R, K)) * size).astype(np.float32)
+    g = np.float32(np.abs(x).max() / 2688) if wdtype == "nvfp4" else np.float32(1)
+    codes, sc = ref.quantize(x, wdtype, g)
+    return dev(codes[:, 0::2] | (codes[:, 1::2] << 4)), dev(ref.tile(sc, rows, tiles)), g, ref.values(codes, sc, wdtype, g)
+
+
+@pytest.mark.parametrize("wdtype", ["nvfp4", "mxfp4"])
+def test_fp32_results_of_4bit_products_add_up(moe, wdtype):
+    """Few large blocks and many small ones: once a sum is large, each addition to it is truncated.  16 of them take 16 * 0.75 * 2^-24
+    = 7.2e-7 of it at most on average, all 112 of K = 7168 seven times that."""
+    rng = np.random.default_rng(11)
+    counts, N, K = [70, 80, 75, 75], 96, 7168
+    P, E = sum(counts), len(counts)
+    ids = make_ids(rng, counts, P, 1)
+    gr, (offsets, tiles, _, _) = moe.group_pairs(dev(ids), E), ref.groups(ids, E)
+    xc, xs, xg, xv = rows_of_uneven_blocks(rng, wdtype, P, K, ref.padded_rows(offsets, tiles), (P + 127 * E) // 128)
+    wc, ws, wg, wv = rows_of_uneven_blocks(rng, wdtype, E * N, K, np.arange(E * N) // N * 128 + np.arange(E * N) % N, E)
+    one = lambda g: dev(np.array([g])) if wdtype == "nvfp4" else None  # noqa: E731
+    got = host(moe.grouped_matmul_fp4(moe.FP4Rows(xc, xs, wdtype, one(xg), gr), moe.FP4Rows(wc.view(E, N, K // 2), ws, wdtype, one(wg)), gr,
+                                      out_dtype=torch.float32))
+    y, _ = ref.product(xv, wv.reshape(E, N, K), offsets)
+    assert distance(got, y) < 1e-6
+
+
+@pytest.mark.parametrize("kind", ["bf16", "nvfp4", "mxfp4"])
+def test_fp32_swiglu(moe, kind):
+    """Of exact sums: silu within ten half units, one more for the product with up."""
+    from tests.test_operators_many_items_gpu import fp4_operands, product
+    rng = np.random.default_rng(4)
+    counts, N, K = [5, 9, 100, 64], 512, 544
+    if kind == "bf16":
+        P, E = sum(counts), len(counts)
+        ids = make_ids(rng, counts, P, 1)
+        gr, (offsets, _, _, _) = moe.group_pairs(dev(ids), E), ref.groups(ids, E)
+        x, w = rng.integers(-2, 3, (P, K)).astype(np.float32), rng.integers(-2, 3, (E, N, K)).astype(np.float32) * 0.5
+        y, _ = product(x, w, offsets)
+        got = moe.grouped_matmul(dev(x, torch.bfloat16), dev(w, torch.bfloat16), gr, act="swiglu", out_dtype=torch.float32)
+    else:
+        x, w, gr, y, _, _, _ = fp4_operands(moe, rng, kind, counts, N, K, 1.0, 0.5)
+        got = moe.grouped_matmul_fp4(x, w, gr, act="swiglu", out_dtype=torch.float32)
+    assert y.min() < -40 and y.max() > 40
+    h = ref.swiglu(y)
+    bad = np.abs(host(got) - h) > 12 * EPS * np.abs(h) + 1e-33      # a gate below -87 leaves less than 1e-36 of itself
+    assert not bad.any(), (y[:, :N // 2][bad][:5], host(got)[bad][:5], h[bad][:5])
