@@ -239,7 +239,7 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, float* sc
     if (lane < nj) {
       if (a.scoring == 0) term = term_of(my_key);
       else if (!a.bias) term = my_key <= 1u ? 0.0f : key_value(my_key);
-      else if (const float l = logit_at(a, row + my_at); l == l) term = sigmoid_of(l);   // the gate has no bias in it
+      else if (my_key > 1u) term = sigmoid_of(logit_at(a, row + my_at));   // the gate has no bias in it
       ids[j0 + lane] = my_at;
       found(j0 + lane, my_at);
     }

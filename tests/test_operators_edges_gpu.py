@@ -145,3 +145,25 @@ def test_fp32_swiglu(moe, kind):
     h = ref.swiglu(y)
     bad = np.abs(host(got) - h) > 12 * EPS * np.abs(h) + 1e-33      # a gate below -87 leaves less than 1e-36 of itself
     assert not bad.any(), (y[:, :N // 2][bad][:5], host(got)[bad][:5], h[bad][:5])
+
+
+# ---------------------------------------------------------------------------------------------------------
+# NaN in the router
+# ---------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("E", [8, 64, 100, 256])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_a_nan_score_has_no_gate(moe, E, renorm):
+    """Three experts of finite score, k = 5: the other two picks have NaN for a bias, or for a logit, and weigh nothing."""
+    z, b = np.full((2, E), -1, np.float32), np.full(E, np.nan, np.float32)
+    good = [1, 3, E - 1]
+    b[good] = [0.5, 0.25, 0.0]
+    z[1, good[0]] = np.nan                                 # in the second row only two are left
+    ids, w = moe.route(dev(z), 5, scoring="sigmoid", bias=dev(b), renormalize=renorm)
+    rest = [e for e in range(E) if e not in good]
+    assert host(ids)[0].tolist() == good + rest[:2]
+    assert host(ids)[1].tolist() == good[1:] + sorted(rest + good[:1])[:3]
+    s = 1 / (1 + np.exp(1.0))
+    want = np.array([[s] * 3 + [0] * 2, [s] * 2 + [0] * 3])
+    if renorm:
+        want /= want.sum(axis=1, keepdims=True)
+    assert np.allclose(host(w), want, rtol=16 * EPS, atol=0)
