@@ -66,7 +66,8 @@ int64_t moe_group_workspace(int32_t T, int32_t k, int32_t E);
  *              NULL); w = s, over the sum of the k picked when renormalize = 1.
  *              n_group > 1: E / n_group consecutive experts form a group, scored by
  *              the sum of its two best s + bias; only the topk_group best groups
- *              compete (DeepSeek-V3's routing).
+ *              compete (DeepSeek-V3's routing).  A NaN adds nothing to its group's score, so
+ *              that of one number and NaN is the number; a group of NaN alone ranks last.
  *   Every w is then multiplied by scale.  A NaN logit (or NaN score) ranks below
  *   -inf and has w = 0, -inf has w = 0, +inf counts as the largest finite value; a
  *   row with no finite logit gets w = 0 throughout, and ids that are still distinct.

@@ -167,3 +167,24 @@ def test_a_nan_score_has_no_gate(moe, E, renorm):
     if renorm:
         want /= want.sum(axis=1, keepdims=True)
     assert np.allclose(host(w), want, rtol=16 * EPS, atol=0)
+
+
+@pytest.mark.parametrize("size", [2, 3, 8, 32])
+def test_a_nan_adds_nothing_to_its_groups_score(moe, size):
+    """Eight groups: one of a single number and NaN, one of NaN alone, the others of numbers; three compete."""
+    E = 8 * size
+    z = np.full((1, 8, size), -3, np.float32)
+    z[0, 2] = np.nan
+    z[0, 4], z[0, 4, size - 1] = np.nan, 3                  # scores sigmoid(3) = 0.95
+    z[0, 5] = 0                                            # 1
+    z[0, 7] = -0.5                                         # 0.76
+    ids, w = moe.route(dev(z.reshape(1, E)), 3, scoring="sigmoid", n_group=8, topk_group=3)
+    assert host(ids)[0].tolist() == [4 * size + size - 1, 5 * size, 5 * size + 1]
+    # with one group more, and all of their experts picked, the NaN of group 4 come after the numbers
+    ids, w = moe.route(dev(z.reshape(1, E)), 4 * size, scoring="sigmoid", n_group=8, topk_group=4, renormalize=False)
+    numbers = 3 * size + 1
+    nan = [4 * size + i for i in range(size - 1)]
+    assert host(ids)[0, numbers:].tolist() == nan and not host(w)[0, numbers:].any() and host(w)[0, :numbers].all()
+    # all eight: the group of NaN alone is in
+    ids, _ = moe.route(dev(z.reshape(1, E)), E, scoring="sigmoid", n_group=8, topk_group=8)
+    assert host(ids)[0, E - size - len(nan):].tolist() == list(range(2 * size, 3 * size)) + nan
