@@ -344,7 +344,8 @@ PyObject* matmul_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool quant = a[5] != Py_False;
   const int64_t cols = act ? w.N / 2 : w.N;
   void* s;
-  if (w.G != g.E || xg.E != g.E || x.index != w.index || g.index != w.index || x.wdtype != w.wdtype || x.N != g.P || x.K != w.K || x.g_count > 1 || w.N < 1 ||
+  // x's scale tiles lie by its own groups: they have to be these, or of the same tensors
+  if (w.G != g.E || xg.offsets != g.offsets || xg.tiles != g.tiles || xg.E != g.E || x.index != w.index || g.index != w.index || x.wdtype != w.wdtype || x.N != g.P || x.K != w.K || x.g_count > 1 || w.N < 1 ||
       !fits(w.N) || !fits(g.P) || (act && w.N % 32) || (quant && (!act || cols % 32)) || !here(w.index, &s))
     OTHERWISE;
   at::Tensor out, codes, scales;

@@ -409,7 +409,7 @@ def grouped_matmul(x, w, groups, *, act="none", gather=False, out_dtype=torch.bf
 
 
 def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, out_dtype=torch.bfloat16, stream=None):
-    """grouped_matmul of 4-bit rows x (FP4Rows in expert order) and 4-bit weights w (FP4Rows [E, N, K]) of one
+    """grouped_matmul of 4-bit rows x (FP4Rows laid out by these groups) and 4-bit weights w (FP4Rows [E, N, K]) of one
     format.  quantize=True (act="swiglu" only): the result as FP4Rows of that format with the matrix scale g_out
     [1] (None = 1; "nvfp4" only), rounded from the fp32 values (moe_grouped_matmul_fp4)."""
     _rows(x, "x")
@@ -431,6 +431,8 @@ def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, 
         raise ValueError(f"x is {x.wdtype}, w is {w.wdtype}")
     if x.shape != (groups.P, K):
         raise ValueError(f"x must be {(groups.P, K)}, is {x.shape}")
+    if x.groups.offsets.data_ptr() != groups.offsets.data_ptr() or x.groups.tiles.data_ptr() != groups.tiles.data_ptr():
+        raise ValueError("x is laid out by other groups than the call's")
     if quantize and not (ACTS[act] and cols % 32 == 0):
         raise ValueError("quantize needs act='swiglu' and w rows a multiple of 64")
     if g_out is not None and not (quantize and x.wdtype == "nvfp4"):

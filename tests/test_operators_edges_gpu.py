@@ -188,3 +188,14 @@ def test_a_nan_adds_nothing_to_its_groups_score(moe, size):
     # all eight: the group of NaN alone is in
     ids, _ = moe.route(dev(z.reshape(1, E)), E, scoring="sigmoid", n_group=8, topk_group=8)
     assert host(ids)[0, E - size - len(nan):].tolist() == list(range(2 * size, 3 * size)) + nan
+
+
+def test_rows_of_other_groups_are_refused(moe):
+    """The rows of one routing under the groups of another, of the same sizes: their scales lie elsewhere."""
+    x, w, ids, gates, gr, q = small_case(moe)
+    want = moe.grouped_matmul_fp4(q, w, gr)
+    other = moe.group_pairs((ids + 1) % gr.E, gr.E)
+    with pytest.raises(ValueError, match="other groups"):
+        moe.grouped_matmul_fp4(q, w, other)
+    same = moe.ExpertGroups(gr.offsets, gr.tiles, gr.order, gr.place)
+    assert torch.equal(moe.grouped_matmul_fp4(q, w, same), want)
