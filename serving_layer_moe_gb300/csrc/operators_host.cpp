@@ -377,7 +377,9 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const long od = PyLong_AsLong(a[3]);
   const int64_t N = y->size(1);
   void* s;
-  if (dt < 0 || w->size(0) != g.T || w->size(1) != g.k || y->size(0) != g.P || N < 1 || !fits(N) || !fits(g.P) || !here(g.index, &s)) OTHERWISE;
+  if (dt < 0 || w->size(0) != g.T || w->size(1) != g.k || y->size(0) != g.P || N < 1 || !fits(N) || !fits(g.P) ||
+      (N % 8 == 0 && !aligned(y->data_ptr(), 16)) || !here(g.index, &s))
+    OTHERWISE;
   at::Tensor out = empty({g.T, N}, float_type(od), g.index);
   const moe_status st = moe_combine((int32_t)g.T, (int32_t)g.k, (int32_t)N, dt, y->data_ptr(), ptr<int32_t>(g.place), w->data_ptr<float>(), (int32_t)od, out.data_ptr(), s);
   if (st != MOE_OK) return raise(st);

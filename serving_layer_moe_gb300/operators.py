@@ -456,6 +456,8 @@ def combine(y, groups, topk_w, *, out_dtype=torch.float32, stream=None):
         raise ValueError(f"topk_w must be {(groups.T, groups.k)}, is {tuple(topk_w.shape)}")
     if y.shape[0] != groups.P or y.shape[1] == 0:
         raise ValueError(f"y must be [{groups.P}, N], is {tuple(y.shape)}")
+    if y.shape[1] % 8 == 0 and y.data_ptr() % 16:
+        raise ValueError("y must be 16-byte aligned where its rows are multiples of 16 bytes")
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
     return _again(lambda: combine(y, groups, topk_w, out_dtype=out_dtype), index, stream)

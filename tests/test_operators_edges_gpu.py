@@ -199,3 +199,13 @@ def test_rows_of_other_groups_are_refused(moe):
         moe.grouped_matmul_fp4(q, w, other)
     same = moe.ExpertGroups(gr.offsets, gr.tiles, gr.order, gr.place)
     assert torch.equal(moe.grouped_matmul_fp4(q, w, same), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_combine_refuses_rows_off_16_bytes_as_a_value(moe, dtype):
+    x, w, ids, gates, gr, q = small_case(moe)
+    room = torch.randn(gr.P * 16 + 1, device="cuda").to(dtype)
+    with pytest.raises(ValueError, match="16-byte aligned"):
+        moe.combine(room[1:].view(gr.P, 16), gr, gates)
+    odd = room[1:gr.P * 9 + 1].view(gr.P, 9)               # rows of nine start anywhere
+    assert torch.equal(moe.combine(odd, gr, gates), moe.combine(odd.clone(), gr, gates))
