@@ -50,6 +50,9 @@ int float_code(const at::Tensor& t) {
 }
 ScalarType float_type(long code) { return code == MOE_F32 ? ScalarType::Float : ScalarType::BFloat16; }
 bool fits(int64_t v) { return v >= 0 && v <= 0x7fffffff; }
+// the library's limits: pairs of a call, matrices of a stack, K
+bool pairs_fit(int64_t T, int64_t k) { return T <= 0x70000000 / (k > 0 ? k : 1); }
+bool matrices_fit(int64_t G, int64_t N, int64_t K) { return G <= 65535 && fits(N) && K <= 1 << 24; }
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // the current stream, when `index` is the current device
@@ -180,7 +183,7 @@ PyObject* groups_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g.P = order->numel();
   g.T = place->size(0);
   g.k = place->size(1);
-  if (g.E < 1 || g.E > 4096 || til->numel() != g.E + 1 || g.T * g.k != g.P) OTHERWISE;
+  if (g.E < 1 || g.E > 4096 || til->numel() != g.E + 1 || g.T * g.k != g.P || !pairs_fit(g.P, 1)) OTHERWISE;
   for (const at::Tensor* t : {off, til, order, place}) (void)address(*t);   // throws where there is no memory
   return Py_BuildValue("(LLLLLOOOO)", (long long)g.index, (long long)g.E, (long long)g.P, (long long)g.T, (long long)g.k, a[0], a[1], a[2], a[3]);
   CATCH
@@ -204,7 +207,7 @@ PyObject* rows_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.G = dim == 3 ? codes->size(0) : 1;
   r.N = codes->size(dim - 2);
   r.K = 2 * codes->size(dim - 1);
-  if (r.K <= 0 || r.K % 32 || (grouped && r.N != gr.P)) OTHERWISE;
+  if (r.K <= 0 || r.K % 32 || !matrices_fit(r.G, r.N, r.K) || (grouped && r.N != gr.P)) OTHERWISE;
   if (scales->size(0) != row_tiles(r, grouped ? &gr : nullptr) || scales->size(1) != block_groups(r.wdtype, r.K) || scales->size(2) != 512) OTHERWISE;
   r.codes = address(*codes);
   r.scales = address(*scales);
@@ -228,7 +231,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double scale = PyFloat_AsDouble(a[7]);
   if (PyErr_Occurred()) return nullptr;
   void* s;
-  if (dt < 0 || (sc != 0 && sc != 1) || k < 1 || k > E || E > 4096 || !fits(T * k) || (sc == 0 && (a[3] != Py_None || ng != 1)) || ng < 1 || ng > 32 || E % ng || tg < 1 ||
+  if (dt < 0 || (sc != 0 && sc != 1) || k < 1 || k > E || E > 4096 || !pairs_fit(T, k) || (sc == 0 && (a[3] != Py_None || ng != 1)) || ng < 1 || ng > 32 || E % ng || tg < 1 ||
       tg > ng || tg * (E / ng) < k || !here(index, &s))
     OTHERWISE;
   const at::Tensor* bias = nullptr;
@@ -277,8 +280,8 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.N = grouped ? gr.P : x->size(dim - 2);
   r.K = x->size(dim - 1);
   void* s;
-  if (dt < 0 || r.K <= 0 || r.K % 32 || (grouped && x->size(0) != gr.T) || !aligned(x->data_ptr(), 16) || (a[2] != Py_None && r.wdtype != MOE_NVFP4) ||
-      !fits(r.N) || !scale_of(a[2], r.G, r.index, &r.g, &r.g_count) || !here(r.index, &s))
+  if (dt < 0 || r.K <= 0 || r.K % 32 || !matrices_fit(r.G, r.N, r.K) || (grouped && x->size(0) != gr.T) || !aligned(x->data_ptr(), 16) ||
+      (a[2] != Py_None && r.wdtype != MOE_NVFP4) || !scale_of(a[2], r.G, r.index, &r.g, &r.g_count) || !here(r.index, &s))
     OTHERWISE;
   at::Tensor codes, scales;
   make_rows(r, grouped ? &gr : nullptr, dim == 3, codes, scales);
@@ -320,7 +323,7 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int gather = PyObject_IsTrue(a[4]);
   const int64_t E = w->size(0), N = w->size(1), K = w->size(2), rows = gather ? g.T : g.P;
   void* s;
-  if (E != g.E || N < 1 || K < 1 || K % 8 || (act && N % 32) || x->size(0) != rows || x->size(1) != K || !fits(N) || !fits(K) || !fits(g.P) ||
+  if (E != g.E || N < 1 || K < 1 || K % 8 || (act && N % 32) || x->size(0) != rows || x->size(1) != K || !matrices_fit(E, N, K) || !fits(g.P) ||
       !aligned(x->data_ptr(), 16) || !aligned(w->data_ptr(), 16) || !here(g.index, &s))
     OTHERWISE;
   at::Tensor out = empty({g.P, act ? N / 2 : N}, float_type(od), g.index), ws;

@@ -31,6 +31,7 @@ SCORING = {"softmax": 0, "sigmoid": 1}
 ACTS = {None: 0, "none": 0, "swiglu": 1}
 FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
 _FLOATS = {torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"]}
+_MOST_PAIRS, _MOST_MATRICES, _MOST_ROWS, _MOST_K = 0x70000000, 65535, 0x7FFFFFFF, 1 << 24       # the library's limits
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 _lib = None
@@ -139,6 +140,14 @@ def _typed(t, name, dtype, dim, index=None):
     return t
 
 
+def _matrices(G, N, K, multiple):
+    """Sizes of a stack of matrices."""
+    if K == 0 or K % multiple or K > _MOST_K:
+        raise ValueError(f"K must be a multiple of {multiple}, {_MOST_K} at most, is {K}")
+    if G > _MOST_MATRICES or N > _MOST_ROWS:
+        raise ValueError(f"at most {_MOST_MATRICES} matrices of {_MOST_ROWS} rows are taken, got {G} of {N}")
+
+
 def _scale(g, name, most, index):
     """An fp32 matrix scale of 1 or `most` values (None: no scale)."""
     if g is not None:
@@ -164,7 +173,7 @@ class ExpertGroups:
             _typed(place, "place", _I32, 2, i)
             if tiles.numel() != offsets.numel() or not 2 <= offsets.numel() <= 4097:
                 raise ValueError(f"offsets and tiles must hold E + 1 values each (1 <= E <= 4096), hold {offsets.numel()} and {tiles.numel()}")
-            raise ValueError(f"order holds {order.numel()} pairs, place {place.numel()}")
+            raise ValueError(f"order and place must hold the same number of pairs, {_MOST_PAIRS} at most, hold {order.numel()} and {place.numel()}")
         self._views = self._c[5:]
 
     @classmethod
@@ -226,8 +235,7 @@ class FP4Rows:
         i = codes.get_device()
         _typed(scales, "scales", _U8, 3, i)
         K = 2 * codes.shape[-1]
-        if K == 0 or K % 32:
-            raise ValueError(f"K must be a multiple of 32, is {K}")
+        _matrices(*((1, *codes.shape) if dim == 2 else codes.shape)[:2], K, 32)
         if groups is not None:
             _groups_on(groups, i)
             if codes.shape[0] != groups.P:
@@ -259,6 +267,11 @@ class FP4Rows:
     shape = property(lambda self: (*self.codes.shape[:-1], self._c[3]))
 
 
+def _pairs(T, k):
+    if T * k > _MOST_PAIRS:
+        raise ValueError(f"{T} tokens of {k} experts are more than {_MOST_PAIRS} pairs")
+
+
 def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=1, renormalize=True, scale=1.0,
           groups=False, stream=None):
     """Experts and gates of each token: (topk_ids int32 [T, k], topk_w fp32 [T, k]), or with groups=True also the
@@ -284,8 +297,7 @@ def route(logits, top_k, *, scoring="softmax", bias=None, n_group=1, topk_group=
     if not (1 <= n_group <= 32 and E % n_group == 0 and 1 <= topk_group <= n_group and topk_group * (E // n_group) >= k):
         raise ValueError(f"n_group (1 to 32) must divide E and topk_group groups must hold top_k experts, got n_group {n_group}, "
                          f"topk_group {topk_group}, E {E}, top_k {k}")
-    if logits.shape[0] * k > 0x70000000:
-        raise ValueError(f"{logits.shape[0]} tokens of {k} experts are more pairs than row numbers")
+    _pairs(logits.shape[0], k)
     return _again(lambda: route(logits, k, scoring=scoring, bias=bias, n_group=n_group, topk_group=topk_group, renormalize=renormalize,
                                 scale=scale, groups=groups), index, stream)
 
@@ -297,6 +309,7 @@ def group_pairs(topk_ids, n_experts, *, stream=None):
     E, index = int(n_experts), topk_ids.get_device()
     if not (1 <= E <= 4096 and k >= 1):
         raise ValueError(f"1 <= n_experts <= 4096 and k >= 1 are needed, got {E} and {k}")
+    _pairs(T, k)
     if stream is not None or index != torch.cuda.current_device():
         return _again(lambda: group_pairs(topk_ids, E), index, stream)
     ops = _operators()
@@ -319,6 +332,8 @@ def fp4_scale(x, *, stream=None):
     index, n = x.get_device(), x.numel()
     if n == 0:
         raise ValueError(f"x is empty: {tuple(x.shape)}")
+    if dim == 3 and x.shape[0] > _MOST_ROWS:
+        raise ValueError(f"at most {_MOST_ROWS} matrices are taken, got {x.shape[0]}")
     if stream is not None or index != torch.cuda.current_device():
         return _again(lambda: fp4_scale(x), index, stream)
     G = x.shape[0] if dim == 3 else 1
@@ -340,8 +355,7 @@ def quantize_fp4(x, wdtype, *, g=None, groups=None, stream=None):
     dim = 2 if groups is not None or not isinstance(x, torch.Tensor) or x.dim() != 3 else 3
     _floats(x, "x", dim)
     index, K = x.get_device(), x.shape[-1]
-    if K == 0 or K % 32:
-        raise ValueError(f"K must be a multiple of 32, is {K}")
+    _matrices(*((1, *x.shape) if dim == 2 else x.shape)[:2], K, 32)
     if x.data_ptr() % 16:
         raise ValueError("x must be 16-byte aligned")
     if g is not None and wdtype != "nvfp4":
@@ -398,8 +412,9 @@ def grouped_matmul(x, w, groups, *, act="none", gather=False, out_dtype=torch.bf
     _groups_on(groups, index)
     E, N, K = w.shape
     _columns(groups, E, N, act, out_dtype)
-    if N == 0 or K == 0 or K % 8:
-        raise ValueError(f"w must be [E, N, K] with K a multiple of 8, is {tuple(w.shape)}")
+    if N == 0:
+        raise ValueError(f"w must be [E, N, K], is {tuple(w.shape)}")
+    _matrices(E, N, K, 8)
     rows = groups.T if gather else groups.P
     if tuple(x.shape) != (rows, K):
         raise ValueError(f"x must be {(rows, K)}, is {tuple(x.shape)}")

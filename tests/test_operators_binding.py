@@ -110,3 +110,42 @@ def test_rows_and_groups_do_not_change():
     for name in ("offsets", "tiles", "order", "place", "E", "P", "T", "k"):
         with pytest.raises(AttributeError):
             setattr(gr, name, None)
+
+
+# Sizes past the library's limits, of tensors that take no memory.  Nothing may be cut to 32 bits on the way.
+TOO_LARGE = """
+import sys, torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+import serving_layer_moe_gb300 as moe
+moe.operators._host()
+with FakeTensorMode(allow_non_fake_inputs=True):
+    t = lambda dtype, *s: torch.empty(*s, dtype=dtype, device="cuda")
+    i32, u8, bf16 = torch.int32, torch.uint8, torch.bfloat16
+    big = 1 << 32
+    groups = lambda: moe.ExpertGroups(t(i32, 2), t(i32, 2), t(i32, 4), t(i32, 4, 1))
+    calls = {
+        "route": lambda: moe.route(t(bf16, 950_000_000, 2), 2),
+        "group_pairs": lambda: moe.group_pairs(t(i32, big + 1, 2), 4),
+        "groups": lambda: moe.ExpertGroups(t(i32, 5), t(i32, 5), t(i32, 1 << 31), t(i32, 1 << 30, 2)),
+        "scale": lambda: moe.fp4_scale(t(bf16, big + 1, 1, 1)),
+        "quantize_K": lambda: moe.quantize_fp4(t(bf16, 1, big + 32), "mxfp4"),
+        "quantize_N": lambda: moe.quantize_fp4(t(bf16, big + 1, 32), "mxfp4"),
+        "quantize_G": lambda: moe.quantize_fp4(t(bf16, 70000, 1, 32), "mxfp4"),
+        "rows_K": lambda: moe.FP4Rows(t(u8, 1, big // 2 + 16), t(u8, 1, big // 128 + 1, 512), "mxfp4"),
+        "rows_N": lambda: moe.FP4Rows(t(u8, big + 1, 16), t(u8, big // 128 + 1, 1, 512), "mxfp4"),
+        "rows_G": lambda: moe.FP4Rows(t(u8, 70000, 1, 16), t(u8, 70000, 1, 512), "mxfp4"),
+        "matmul_K": lambda: moe.grouped_matmul(t(bf16, 4, big + 8), t(bf16, 1, 8, big + 8), groups()),
+        "matmul_N": lambda: moe.grouped_matmul(t(bf16, 4, 8), t(bf16, 1, big + 8, 8), groups()),
+    }
+    try:
+        calls[sys.argv[1]]()
+    except ValueError as e:
+        print("refused", e)
+"""
+
+
+@pytest.mark.parametrize("call", ["route", "group_pairs", "groups", "scale", "quantize_K", "quantize_N", "quantize_G", "rows_K", "rows_N", "rows_G",
+                                  "matmul_K", "matmul_N"])
+def test_sizes_past_the_limits_are_refused_as_values(call):
+    line = run(TOO_LARGE, call)
+    assert line.startswith("refused") and "most" in line or "more than" in line, line

@@ -209,3 +209,12 @@ def test_combine_refuses_rows_off_16_bytes_as_a_value(moe, dtype):
         moe.combine(room[1:].view(gr.P, 16), gr, gates)
     odd = room[1:gr.P * 9 + 1].view(gr.P, 9)               # rows of nine start anywhere
     assert torch.equal(moe.combine(odd, gr, gates), moe.combine(odd.clone(), gr, gates))
+
+
+def test_too_many_matrices_are_refused_as_values(moe):
+    x = torch.zeros(65536, 1, 32, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="65535"):
+        moe.quantize_fp4(x, "mxfp4")
+    assert torch.equal(moe.fp4_scale(x), torch.ones(65536, device="cuda"))        # no stack of 4-bit matrices
+    q = moe.quantize_fp4(x[:65535], "mxfp4")
+    assert q.shape == (65535, 1, 32) and not moe.dequantize_fp4(q).any()
