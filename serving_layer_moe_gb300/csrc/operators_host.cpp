@@ -321,6 +321,7 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!x || !w) OTHERWISE;
   const long act = PyLong_AsLong(a[3]), od = PyLong_AsLong(a[5]);
   const int gather = PyObject_IsTrue(a[4]);
+  if (PyErr_Occurred()) return nullptr;
   const int64_t E = w->size(0), N = w->size(1), K = w->size(2), rows = gather ? g.T : g.P;
   void* s;
   if (E != g.E || N < 1 || K < 1 || K % 8 || (act && N % 32) || x->size(0) != rows || x->size(1) != K || !matrices_fit(E, N, K) || !fits(g.P) ||

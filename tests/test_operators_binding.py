@@ -149,3 +149,26 @@ with FakeTensorMode(allow_non_fake_inputs=True):
 def test_sizes_past_the_limits_are_refused_as_values(call):
     line = run(TOO_LARGE, call)
     assert line.startswith("refused") and "most" in line or "more than" in line, line
+
+
+# An argument whose truth value raises: that error, not the interpreter's own about a result with an error set.
+NO_TRUTH = """
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+import serving_layer_moe_gb300 as moe
+class No:
+    def __bool__(self):
+        raise KeyError("no truth")
+with FakeTensorMode(allow_non_fake_inputs=True):
+    t = lambda dtype, *s: torch.empty(*s, dtype=dtype, device="cuda")
+    i32, bf16 = torch.int32, torch.bfloat16
+    gr = moe.ExpertGroups(t(i32, 2), t(i32, 2), t(i32, 4), t(i32, 4, 1))
+    try:
+        moe.grouped_matmul(t(bf16, 3, 8), t(bf16, 1, 8, 8), gr, gather=No())
+    except KeyError as e:
+        print("raised", e)
+"""
+
+
+def test_an_argument_without_a_truth_value_raises_its_own_error():
+    assert run(NO_TRUTH).startswith("raised")
