@@ -501,7 +501,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         if (!exact_tile<S::FP4>(a, o, g, tmem, tfull, tempty, acc, acc_phase, abort_flag, q, part)) break;
         continue;
       }
-      const float go = S::NV && a.quant && a.g_out ? __ldg(a.g_out) : 1.0f, rgo = __frcp_rn(go);
+      const float go = S::NV && a.quant && a.g_out ? __ldg(a.g_out) : 1.0f, up = fabsf(go) < 1e-30f ? 0x1p64f : 1.0f;
+      const float rgo = __frcp_rn(go * up), sixth = kSixth * up;
       const int64_t pad0 = S::FP4 && a.quant ? (int64_t)__ldg(a.tiles + o.e) * 128 + (o.row0 - __ldg(a.offsets + o.e)) : 0;
       bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
       if (S::FP4 && !S::NV && a.quant) ok = named_and(1 + part, 128, ok);   // these four warps wait for one another below
@@ -618,7 +619,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
             named_sync(1 + part, 128);
           }
           float st;
-          uint32_t code = block_scale<S::NV, false>(top, go, rgo, st);
+          uint32_t code = block_scale<S::NV, false>(top, go, rgo, st, sixth);
           const uint2 codes = encode16<S::NV, false>(x, top, code, st);
           const int f = m * 64 + 16 * q, og = (a.cols + (S::NV ? 63 : 127)) / (S::NV ? 64 : 128);
           if (lane < left) {

@@ -84,12 +84,13 @@ __device__ __forceinline__ bool regular(float most, float d, float r) { return d
 
 // Scale code of a block and the value of one step, from the bits of its largest |x|; rg = 1 / g rounded.
 // EXACT: as the format defines them, by correctly rounded divisions.  Otherwise (values that carry rounding errors of their
-// own) by multiplications, good to three units.
+// own) by multiplications, good to three units; rg is then 1 / (g up) and sixth is up / 6 for an `up` that keeps 1 / g finite.
+constexpr float kSixth = 0.16666667f;   // the fp32 nearest to 1 / 6
 template <bool NV, bool EXACT = true>
-__device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float g, float rg, float& step) {
+__device__ __forceinline__ uint32_t block_scale(uint32_t amax_bits, float g, float rg, float& step, float sixth = kSixth) {
   if (NV) {
     if (amax_bits > 0x7f800000u) { step = 0.0f; return 0x7fu; }
-    const float a = __uint_as_float(amax_bits) * 0.16666667f;   // the fp32 nearest to 1 / 6
+    const float a = __uint_as_float(amax_bits) * sixth;
     const uint32_t code = to_e4m3(!EXACT ? a * rg : a > 1e-20f && regular(a, g, rg) ? quotient(a, g, rg) : __fdiv_rn(a, g));
     step = e4m3_value(code) * g;
     return code;

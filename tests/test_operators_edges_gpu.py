@@ -218,3 +218,18 @@ def test_too_many_matrices_are_refused_as_values(moe):
     assert torch.equal(moe.fp4_scale(x), torch.ones(65536, device="cuda"))        # no stack of 4-bit matrices
     q = moe.quantize_fp4(x[:65535], "mxfp4")
     assert q.shape == (65535, 1, 32) and not moe.dequantize_fp4(q).any()
+
+
+@pytest.mark.parametrize("g", [1e-39, 2e-45, 1.0])
+def test_requantised_zeros_under_a_subnormal_matrix_scale(moe, g):
+    """1 / g is infinite below 2^-128, 0 / g is not: a block of zeros has scale and codes 0."""
+    E, H, I = 2, 64, 64
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.randn(E, 2 * I, H, device="cuda", generator=gen).bfloat16()
+    w[:, I:I + 32] = 0                                     # the first 32 features of every result are zero
+    gr = moe.group_pairs(torch.tensor([[0], [1], [1]], dtype=torch.int32, device="cuda"), E)
+    x = moe.quantize_fp4(torch.randn(3, H, device="cuda", generator=gen).bfloat16(), "nvfp4", groups=gr)
+    g = torch.tensor([g], device="cuda")
+    q = moe.grouped_matmul_fp4(x, moe.quantize_fp4(w, "nvfp4"), gr, act="swiglu", quantize=True, g_out=g)
+    v = host(moe.dequantize_fp4(q, out_dtype=torch.float32))
+    assert not v[:, :32].any() and np.isfinite(v).all()
