@@ -172,3 +172,31 @@ with FakeTensorMode(allow_non_fake_inputs=True):
 
 def test_an_argument_without_a_truth_value_raises_its_own_error():
     assert run(NO_TRUTH).startswith("raised")
+
+
+WITHOUT_TORCH = """
+import sys
+sys.modules["torch"] = None                      # importing it raises, as where it is not installed
+import serving_layer_moe_gb300 as moe
+from serving_layer_moe_gb300 import *
+assert MoECache is moe.MoECache and "moe_layer_decode" in moe.SYMBOLS
+moe.load_library()
+try:
+    moe.route
+except ImportError:
+    print("needs torch")
+"""
+
+LATER = """
+import sys
+import serving_layer_moe_gb300 as moe
+assert "torch" not in sys.modules and "route" in dir(moe) and not hasattr(moe, "nothing")
+from serving_layer_moe_gb300 import *
+assert route is moe.route is moe.operators.route and combine is moe.combine and "moe_route" in OPERATOR_SYMBOLS
+print("later")
+"""
+
+
+@pytest.mark.parametrize("script,last", [(WITHOUT_TORCH, "needs torch"), (LATER, "later")])
+def test_the_package_needs_torch_for_the_operators_only(script, last):
+    assert run(script) == last
