@@ -2,11 +2,14 @@
 tensors to its operators, with g++ (no cmake).
 
 Each source compiles to an object in parallel, then one link each.  The outputs
-sit next to this file so the in-tree libraries are the ones that load.
+sit next to this file so the in-tree libraries are the ones that load.  Where torch
+is not installed there is nothing for _operators.so to take, and it is left out;
+libmoecache.so needs no torch and is there even if _operators.so fails.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -58,16 +61,21 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
             raise RuntimeError(f"g++ failed for operators_host.cpp:\n{r.stderr}")
         return obj
 
+    torch = importlib.util.find_spec("torch") is not None
     with ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
-        host = ex.submit(compile_host)
+        host = ex.submit(compile_host) if torch else None
         objs = list(ex.map(compile_one, srcs))
-        host_obj = host.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    if not torch:
+        if os.path.exists(HOST):
+            os.remove(HOST)        # another library's
+        return LIB
+    host_obj = host.result()
     from torch.utils.cpp_extension import library_paths
     libs = [f"-L{p}" for p in library_paths()]
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", HOST + ".tmp", host_obj, f"-L{HERE}", "-l:libmoecache.so", "-Wl,-rpath,$ORIGIN",

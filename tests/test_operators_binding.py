@@ -200,3 +200,34 @@ print("later")
 @pytest.mark.parametrize("script,last", [(WITHOUT_TORCH, "needs torch"), (LATER, "later")])
 def test_the_package_needs_torch_for_the_operators_only(script, last):
     assert run(script) == last
+
+
+# The build with stand-ins for the compilers, in a folder of its own: what is asked of them, not what they make.
+BUILD = """
+import os, sys
+here, torch = sys.argv[1:]
+if torch == "no":
+    sys.modules["torch"] = None
+sys.path.insert(0, here)
+import build as b
+open(b.HOST, "w").close()                        # left from another build
+try:
+    print("built", b.build() == b.LIB, os.path.exists(b.LIB), os.path.exists(b.HOST))
+except RuntimeError as e:
+    print("raised", os.path.exists(b.LIB), str(e).split()[0])
+"""
+
+
+@pytest.mark.parametrize("torch,last", [("no", "built True True False"), ("yes", "raised True g++")])
+def test_the_library_builds_without_the_operators_binding(tmp_path, monkeypatch, torch, last):
+    """Without torch _operators.so is left out; where its compiler fails, libmoecache.so is there all the same."""
+    import shutil
+    shutil.copy(os.path.join(ROOT, "serving_layer_moe_gb300", "build.py"), tmp_path)
+    (tmp_path / "csrc").mkdir()
+    (tmp_path / "csrc" / "one.cu").touch()
+    nvcc = tmp_path / "nvcc"
+    nvcc.write_text('#!/bin/sh\nwhile [ "$1" != -o ]; do shift; done\ntouch "$2"\n')
+    nvcc.chmod(0o755)
+    monkeypatch.setenv("NVCC", str(nvcc))
+    monkeypatch.setenv("CXX", "false")
+    assert run(BUILD, str(tmp_path), torch) == last
