@@ -239,15 +239,16 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     bias = typed(a[3], ScalarType::Float, 1, index);
     if (!bias || bias->numel() != E) OTHERWISE;
   }
-  // ids, gates, and with groups their four arrays: in one allocation where there are few pairs.  Otherwise the groups have one of
-  // their own, so that keeping or saving ids does not keep them, and the workspace goes when the call returns.
+  // ids, gates, and with groups their four arrays: in one allocation up to 256 pairs.  Otherwise the groups have one of
+  // their own, so that keeping or saving ids does not keep them.  The workspace goes when the call returns.
   const int64_t pairs = 4 * T * k, bins = 4 * (E + 1), wb = group ? moe_group_workspace((int32_t)T, (int32_t)k, (int32_t)E) : 0;
   const int64_t many = group ? 2 * bins + 2 * pairs : 0;
-  const at::Tensor both = room(2 * pairs + (wb ? 0 : many), index), buf = wb ? room(many, index) : both;
+  const bool few = T * k <= 256;
+  const at::Tensor both = room(2 * pairs + (few ? many : 0), index), buf = few || !group ? both : room(many, index);
   at::Tensor ws;
   if (wb) ws = room(wb, index);
   const at::Tensor ids = on(both, 0, {T, k}, ScalarType::Int), w = on(both, pairs, {T, k}, ScalarType::Float);
-  const int64_t from = wb ? 0 : 2 * pairs, base = address(buf) + from;
+  const int64_t from = few ? 2 * pairs : 0, base = address(buf) + from;
   Groups g{};
   if (group) g = Groups{index, E, T * k, T, k, base, base + bins, base + 2 * bins, base + 2 * bins + pairs};
   const moe_status st = moe_route((int32_t)T, (int32_t)E, (int32_t)k, dt, x->data_ptr(), (int32_t)sc, bias ? bias->data_ptr<float>() : nullptr, (int32_t)ng,

@@ -10,8 +10,9 @@
 // Grouping is a stable counting sort of the T*k pairs by expert in three launches: the
 // router's blocks count the pairs they pick per expert, those counts become starts, and
 // blocks rank their own pairs, 32 at a time by match.  Ranks follow the pair index, so no
-// atomic decides an order.  Calls of at most 256 pairs do all of it, router included, in
-// one block, where a pair counts the pairs before it in expert order.
+// atomic decides an order.  Calls of at most 256 pairs of 32 tokens do all of it, router
+// included, in one block, where a pair counts the pairs before it in expert order; pairs
+// that come with their ids up to 256, whatever their tokens.
 //
 // Bounds: a prompt chunk of 8192 tokens and 256 experts reads 8.4 MB of logits; one
 // decoded token is one launch's latency.
@@ -29,7 +30,10 @@ constexpr int ROUTE_WARPS = ROUTE_THREADS / 32;
 constexpr int PLACE_THREADS = 256;          // 8 warps rank a segment of pairs each
 constexpr int PLACE_WARPS = PLACE_THREADS / 32;
 constexpr int kMaxBlocks = 1024;            // counting blocks
-constexpr int kSmallPairs = 256;            // up to here one block routes and groups
+// Up to here one block groups; and routes, up to kSmallTokens, four a warp.  us of one block / of three launches: top-8 of 128
+// experts, 1 token 2.8 / 5.8, 16 tokens 5.3 / 7.0, 32 tokens 9.8 / 7.3; best of 128, 32 tokens 5.0 / 5.9, 64 tokens 8.8 / 5.9, 256
+// tokens 32 / 6.4; best of 4096, 32 tokens 31 / 25, 256 tokens 146 / 27.
+constexpr int kSmallPairs = 256, kSmallTokens = 32;
 
 struct RouteArgs {
   int T, E, k, scoring, n_group, topk_group, renorm, tokens_per_block, bf16;
@@ -524,14 +528,14 @@ cudaError_t launch_combine_rows(int T, int k, int N, const void* y, const int32_
 // tokens of one counting block when T tokens are spread over at most kMaxBlocks
 int tokens_per_block(int T) { return ROUTE_WARPS * std::max(1, (T + ROUTE_WARPS * kMaxBlocks - 1) / (ROUTE_WARPS * kMaxBlocks)); }
 bool small_group(int64_t T, int64_t k) { return T * k <= kSmallPairs; }
+bool small_route(int64_t T, int64_t k) { return small_group(T, k) && T <= kSmallTokens; }
 
-moe_status check_group_args(int32_t T, int32_t E, int32_t k, const void* offsets, const void* tiles, const void* order,
+moe_status check_group_args(int32_t T, int64_t need, const void* offsets, const void* tiles, const void* order,
                             const void* place, const void* ws, int64_t ws_bytes) {
   if (!offsets || !tiles || (T > 0 && (!order || !place)))
     return fail(MOE_EINVAL, "offsets, tiles, order and place are all needed for grouping");
   if (!aligned_to(offsets, 4) || !aligned_to(tiles, 4) || !aligned_to(order, 4) || !aligned_to(place, 4) || !aligned_to(ws, 4))
     return fail(MOE_EINVAL, "offsets, tiles, order, place and workspace must be 4-byte aligned");
-  const int64_t need = moe_group_workspace(T, k, E);
   if (need > 0 && (!ws || ws_bytes < need))
     return fail(MOE_EINVAL, "workspace holds %lld bytes, %lld are needed", (long long)ws_bytes, (long long)need);
   return MOE_OK;
@@ -604,7 +608,7 @@ using namespace moe;
 extern "C" int64_t moe_grouped_tiles(int64_t P, int32_t E) { return P < 0 || E < 0 ? 0 : (P + 127 * std::min<int64_t>(P, E)) / 128; }
 
 extern "C" int64_t moe_group_workspace(int32_t T, int32_t k, int32_t E) {
-  if (T <= 0 || k < 0 || E < 0 || small_group(T, k)) return 0;
+  if (T <= 0 || k < 0 || E < 0 || small_route(T, k)) return 0;
   const int64_t blocks = (T + tokens_per_block(T) - 1) / tokens_per_block(T);
   return (blocks + 1) * ((int64_t)E + 1) * 4;
 }
@@ -624,7 +628,7 @@ extern "C" moe_status moe_route(int32_t T, int32_t E, int32_t k, int32_t logits_
     return fail(MOE_EINVAL, "n_group = %d (1 to 32) must divide E = %d and topk_group = %d of them hold k = %d experts",
                 n_group, E, topk_group, k);
   const bool group = offsets || tiles || order || place;
-  if (group && (st = check_group_args(T, E, k, offsets, tiles, order, place, workspace, workspace_bytes)) != MOE_OK) return st;
+  if (group && (st = check_group_args(T, moe_group_workspace(T, k, E), offsets, tiles, order, place, workspace, workspace_bytes)) != MOE_OK) return st;
   if (T > 0 && (!logits || !ids || !w)) return fail(MOE_EINVAL, "logits, topk_ids and topk_w must not be NULL");
   if (!aligned_to(logits, logits_dtype == MOE_F32 ? 4 : 2) || !aligned_to(bias, 4) || !aligned_to(ids, 4) || !aligned_to(w, 4))
     return fail(MOE_EINVAL, "logits, bias, topk_ids and topk_w must be aligned to their element size");
@@ -634,7 +638,7 @@ extern "C" moe_status moe_route(int32_t T, int32_t E, int32_t k, int32_t logits_
   a.T = T; a.E = E; a.k = k; a.scoring = scoring; a.n_group = n_group; a.topk_group = topk_group;
   a.renorm = renormalize != 0; a.scale = scale; a.logits = logits; a.bias = bias; a.ids = ids; a.w = w;
   a.offsets = offsets; a.tiles = tiles; a.order = order; a.place = place;
-  const bool small = group && small_group(T, k);
+  const bool small = group && small_route(T, k);
   a.counts = group && !small ? static_cast<int32_t*>(workspace) : nullptr;
   a.tokens_per_block = small ? T : tokens_per_block(T);
   const int blocks = (T + a.tokens_per_block - 1) / a.tokens_per_block;
@@ -651,7 +655,7 @@ extern "C" moe_status moe_group_pairs(int32_t T, int32_t E, int32_t k, const int
                                       int32_t* order, int32_t* place, void* workspace, int64_t workspace_bytes, void* stream) {
   moe_status st = check_sizes(T, E, k);
   if (st != MOE_OK) return st;
-  if ((st = check_group_args(T, E, k, offsets, tiles, order, place, workspace, workspace_bytes)) != MOE_OK) return st;
+  if ((st = check_group_args(T, small_group(T, k) ? 0 : moe_group_workspace(T, k, E), offsets, tiles, order, place, workspace, workspace_bytes)) != MOE_OK) return st;
   if (T > 0 && !ids) return fail(MOE_EINVAL, "topk_ids must not be NULL");
   if (!aligned_to(ids, 4)) return fail(MOE_EINVAL, "topk_ids must be 4-byte aligned");
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -233,3 +233,15 @@ def test_requantised_zeros_under_a_subnormal_matrix_scale(moe, g):
     q = moe.grouped_matmul_fp4(x, moe.quantize_fp4(w, "nvfp4"), gr, act="swiglu", quantize=True, g_out=g)
     v = host(moe.dequantize_fp4(q, out_dtype=torch.float32))
     assert not v[:, :32].any() and np.isfinite(v).all()
+
+
+@pytest.mark.parametrize("T,k", [(16, 8), (32, 8), (33, 7), (64, 4), (65, 3), (128, 2), (256, 1), (257, 1)])
+@pytest.mark.parametrize("E", [60, 1024])
+def test_route_and_group_pairs_of_about_256_pairs(moe, T, k, E):
+    """On both sides of the limits of the one-block forms, 32 tokens and 256 pairs."""
+    z = np.random.default_rng(T * E).permutation(T * E).reshape(T, E).astype(np.float32) / (T * E)      # no two alike
+    ids, w, gr = moe.route(dev(z), k, groups=True)
+    assert np.array_equal(host(ids), np.argsort(-z, axis=1)[:, :k])
+    want = ref.groups(host(ids), E)
+    for g in (gr, moe.group_pairs(ids, E)):
+        assert all(np.array_equal(host(a), b) for a, b in zip((g.offsets, g.tiles, g.order, g.place), want))
