@@ -245,3 +245,82 @@ def test_route_and_group_pairs_of_about_256_pairs(moe, T, k, E):
     want = ref.groups(host(ids), E)
     for g in (gr, moe.group_pairs(ids, E)):
         assert all(np.array_equal(host(a), b) for a, b in zip((g.offsets, g.tiles, g.order, g.place), want))
+
+
+# ---------------------------------------------------------------------------------------------------------
+# long and repeated calls, and the cache behind the router
+# ---------------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("T,E,k,scoring", [(8193, 96, 4, "softmax"), (20000, 64, 6, "sigmoid"), (70001, 8, 2, "softmax")])
+def test_route_of_several_tokens_a_warp(moe, T, E, k, scoring):
+    """Past 8192 tokens a counting block takes more than eight.  Logits of a row are exact steps of 1/64: no two alike."""
+    rng = np.random.default_rng(T)
+    z = (np.argsort(rng.random((T, E)), axis=1) / 64).astype(np.float32)
+    ids, w, gr = moe.route(dev(z), k, scoring=scoring, groups=True)
+    rid = np.argsort(-z, axis=1)[:, :k]
+    assert np.array_equal(host(ids), rid)
+    zt = np.take_along_axis(z, rid, axis=1).astype(np.float64)
+    p = np.exp(zt) if scoring == "softmax" else 1 / (1 + np.exp(-zt))
+    # a term within 4 units, k additions, a division
+    assert np.allclose(host(w), p / p.sum(axis=1, keepdims=True), rtol=(k + 16) * 2 * EPS)
+    want = ref.groups(rid, E)
+    for g in (gr, moe.group_pairs(ids, E)):
+        assert all(np.array_equal(host(a), b) for a, b in zip((g.offsets, g.tiles, g.order, g.place), want))
+
+
+def test_large_calls_give_the_same_bits_again(moe):
+    """A 4-bit layer and a bf16 one of 3000 tokens and 128 experts, ten times each."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    T, E, k, H, I = 3000, 128, 8, 512, 384
+    gu = (torch.randn(E, 2 * I, H, device="cuda", generator=gen) * 0.05).bfloat16()
+    dn = (torch.randn(E, H, I, device="cuda", generator=gen) * 0.05).bfloat16()
+    x = torch.randn(T, H, device="cuda", generator=gen).bfloat16()
+    logits = torch.randn(T, E, device="cuda", generator=gen)
+    gu4, dn4 = (moe.quantize_fp4(w, "nvfp4", g=moe.fp4_scale(w)) for w in (gu, dn))
+    g = torch.full((1,), 0.002, device="cuda")
+
+    def layer4(out):
+        _, w, gr = moe.route(logits, k, groups=True)
+        h = moe.grouped_matmul_fp4(moe.quantize_fp4(x, "nvfp4", g=g, groups=gr), gu4, gr, act="swiglu", quantize=True, g_out=g)
+        return moe.combine(moe.grouped_matmul_fp4(h, dn4, gr, out_dtype=out), gr, w)
+
+    def layer16(out):
+        _, w, gr = moe.route(logits, k, groups=True)
+        h = moe.grouped_matmul(x, gu, gr, act="swiglu", gather=True)
+        return moe.combine(moe.grouped_matmul(h, dn, gr, out_dtype=out), gr, w)
+
+    for layer in (layer4, layer16):
+        for out in (torch.bfloat16, torch.float32):
+            want = layer(out)
+            assert want.isfinite().all() and want.any()
+            for _ in range(9):
+                assert torch.equal(layer(out), want)
+    moe.check_operators()
+
+
+def test_the_cache_decodes_what_the_router_picks(moe):
+    """route's ids and gates as they are, into MoECache.decode: slot maps equal the oracle's, outputs within its tolerance."""
+    from oracle.cache import SlotCache
+    from oracle.ffn import ExpertStore, combine, pair_outputs, relative_max_error
+    from tests.harness import TOL, build_pool, make_cache, torch_act
+    from workloads import activations, config
+    cfg = config("tiny")
+    s = cfg.shape
+    arena, offs, pool = build_pool(cfg)
+    bw = cfg.bw_mbps
+    cache, K = make_cache(cfg, pool, offs, None, bw)
+    ora = SlotCache(s.L, s.E, cfg.capacity, K, bw[0], bw[1])
+    store = ExpertStore(arena, offs, s.wdtype, s.H, s.I, s.blob_bytes)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    out = torch.empty(cfg.T, s.H, device="cuda")
+    slots = torch.empty(cfg.T, s.k, dtype=torch.int32, device="cuda")
+    for step in range(12):
+        logits = torch.randn(cfg.T, s.E, device="cuda", generator=gen).bfloat16()
+        ids, gates, _ = moe.route(logits, s.k, groups=True) if step % 2 else (*moe.route(logits, s.k), None)
+        plan = ora.decode(0, host(ids))
+        x = activations(cfg, step, 0)
+        y = pair_outputs(store, 0, s.E, x, s.adtype, host(ids))
+        cpu = dev(np.where(plan.slot_map[..., None] < 0, y, np.nan).astype(np.float32))
+        cache.decode(0, torch_act(x, "cuda"), ids, gates, out, cpu_part=cpu, slot_map=slots)
+        assert np.array_equal(host(slots), plan.slot_map)
+        assert relative_max_error(host(out), combine(host(gates), y, plan.slot_map, y)) <= TOL
+    cache.close()
