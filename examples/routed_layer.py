@@ -1,6 +1,7 @@
 """A 4-bit MoE layer from bf16 weights: quantise once, then route, multiply and combine prompt chunks and decoded tokens.
 
     python examples/routed_layer.py [--tokens 8192] [--hidden 2048] [--inter 768] [--experts 128] [--top-k 8] [--format nvfp4]
+                                    [--rows bf16]
 
 The layer is what a caller of MoECache.decode has for itself: a router in front (the ids and gates that decode takes), and,
 for experts that all stay on the GPU, the whole layer on tensors it holds.  Prints how far the 4-bit layer is from the bf16 one
@@ -17,10 +18,11 @@ import serving_layer_moe_gb300 as moe  # noqa: E402
 
 
 class RoutedLayer:
-    """One MoE layer: router [E, H] bf16, gate_up [E, 2 I, H] (gate rows, then up rows) and down [E, H, I] bf16."""
+    """One MoE layer: router [E, H] bf16, gate_up [E, 2 I, H] (gate rows, then up rows) and down [E, H, I] bf16.
+    rows: the type of the experts' rows that combine adds up; fp32 rounds them less and moves twice the bytes."""
 
-    def __init__(self, router, gate_up, down, top_k, fmt="nvfp4"):
-        self.router, self.gate_up, self.down, self.k, self.fmt = router, gate_up, down, top_k, fmt
+    def __init__(self, router, gate_up, down, top_k, fmt="nvfp4", rows=torch.bfloat16):
+        self.router, self.gate_up, self.down, self.k, self.fmt, self.rows = router, gate_up, down, top_k, fmt, rows
         scale = moe.fp4_scale if fmt == "nvfp4" else (lambda w: None)
         self.gate_up4 = moe.quantize_fp4(gate_up, fmt, g=scale(gate_up))
         self.down4 = moe.quantize_fp4(down, fmt, g=scale(down))
@@ -38,13 +40,13 @@ class RoutedLayer:
     def bf16(self, x):
         _, w, groups = moe.route(x @ self.router.T, self.k, groups=True)
         h = moe.grouped_matmul(x, self.gate_up, groups, act="swiglu", gather=True)
-        return moe.combine(moe.grouped_matmul(h, self.down, groups), groups, w, out_dtype=torch.bfloat16)
+        return moe.combine(moe.grouped_matmul(h, self.down, groups, out_dtype=self.rows), groups, w, out_dtype=torch.bfloat16)
 
     def __call__(self, x):
         _, w, groups = moe.route(x @ self.router.T, self.k, groups=True)
         xq = moe.quantize_fp4(x, self.fmt, g=self.gx, groups=groups)
         h = moe.grouped_matmul_fp4(xq, self.gate_up4, groups, act="swiglu", quantize=True, g_out=self.gh)
-        return moe.combine(moe.grouped_matmul_fp4(h, self.down4, groups), groups, w, out_dtype=torch.bfloat16)
+        return moe.combine(moe.grouped_matmul_fp4(h, self.down4, groups, out_dtype=self.rows), groups, w, out_dtype=torch.bfloat16)
 
 
 def milliseconds(call, n=20):
@@ -59,7 +61,7 @@ def milliseconds(call, n=20):
     return a.elapsed_time(b) / n
 
 
-def run(tokens=8192, hidden=2048, inter=768, experts=128, top_k=8, fmt="nvfp4", seed=0):
+def run(tokens=8192, hidden=2048, inter=768, experts=128, top_k=8, fmt="nvfp4", seed=0, rows="bf16"):
     """Build a layer with random weights, run it; {relative distance from bf16, ms a chunk, ms a token}."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
 
@@ -67,7 +69,7 @@ def run(tokens=8192, hidden=2048, inter=768, experts=128, top_k=8, fmt="nvfp4", 
         return (torch.randn(shape, generator=gen, device="cuda") * std).bfloat16()
 
     layer = RoutedLayer(normal(experts, hidden, std=hidden ** -0.5), normal(experts, 2 * inter, hidden, std=0.02),
-                        normal(experts, hidden, inter, std=0.02), top_k, fmt)
+                        normal(experts, hidden, inter, std=0.02), top_k, fmt, {"bf16": torch.bfloat16, "f32": torch.float32}[rows])
     x = normal(tokens, hidden, std=1.0)
     layer.calibrate(x[: min(tokens, 256)])
     want, got = layer.bf16(x).float(), layer(x).float()
@@ -96,6 +98,7 @@ if __name__ == "__main__":
     p.add_argument("--experts", type=int, default=128)
     p.add_argument("--top-k", type=int, default=8)
     p.add_argument("--format", choices=("nvfp4", "mxfp4"), default="nvfp4")
+    p.add_argument("--rows", choices=("bf16", "f32"), default="bf16")
     a = p.parse_args()
-    r = run(a.tokens, a.hidden, a.inter, a.experts, a.top_k, a.format)
+    r = run(a.tokens, a.hidden, a.inter, a.experts, a.top_k, a.format, rows=a.rows)
     print(f"{a.format}: {r['distance']:.3f} from bf16, {r['chunk_ms'] * 1e3:.0f} us for {a.tokens} tokens, {r['token_ms'] * 1e3:.1f} us for one")

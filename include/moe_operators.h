@@ -16,7 +16,8 @@
  *  - Every pointer is device memory of the current device, owned by the caller.
  *    Work is enqueued on `stream` (a cudaStream_t passed as void*, NULL = legacy
  *    default stream); the host never waits and nothing is allocated, so every
- *    call can be captured in a CUDA graph.
+ *    call can be captured in a CUDA graph.  The caller orders `stream` behind what
+ *    makes the inputs, and keeps them and the outputs until the work is done.
  *  - Matrices are row-major and contiguous.  int32 / fp32 arrays are 4-byte
  *    aligned, matrices 16-byte aligned where a row of them is a multiple of 16
  *    bytes (MOE_EINVAL otherwise, before anything is enqueued).
@@ -29,7 +30,9 @@
  * Expert order.  A pair p = t * k + j is token t's j-th expert.  Grouped row i
  * holds pair order[i]; the rows of expert e are offsets[e] .. offsets[e + 1] - 1,
  * pairs ascending; place[p] is the row of pair p.  tiles[e] counts the 128-row
- * tiles of the experts before e, each expert's rows starting a new tile.
+ * tiles of the experts before e, each expert's rows starting a new tile.  moe_route and
+ * moe_group_pairs make them from any ids.  The other calls take them as they are: kernels
+ * use what they hold as row numbers and do not check it.
  *
  * 4-bit matrices (MOE_NVFP4, MOE_MXFP4).  codes [rows, K/2]: two e2m1 codes a
  * byte, the even element low.  scales: tiles of 128 rows x 4 blocks, 512 bytes,
@@ -145,8 +148,10 @@ moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const 
  * multiplied by gx * gw[e] (gw_count = 1 or E; NULL = 1).  Their few bits leave such sums nearly
  * exact; where block scales differ widely (by e^2, K = 7168) they are 3e-6 off, for an fp32
  * result 5e-7.  out NULL: with act = 1 the result is quantised again as the 4-bit
- * rows out_codes / out_scales with matrix scale g_out (NULL = 1) from its fp32 values,
- * and N/2 must be a multiple of 32.
+ * rows out_codes / out_scales with matrix scale g_out (NULL = 1), and N/2 must be a multiple
+ * of 32.  It is that of moe_quantize_fp4 on values with a bf16 result's sums and a SwiGLU to
+ * |gate| + 10 units of 2^-23, by products with reciprocals good to three such units: a scale
+ * or code is another one where that carries a value over a rounding edge.
  */
 moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, int32_t K, int32_t wdtype, const uint8_t* x_codes,
                                   const uint8_t* x_scales, const float* gx, const uint8_t* w_codes,

@@ -772,6 +772,8 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
 // us of gate/up (K 2048, N 1536, 128 experts), single and in pairs, by rows an expert: bf16 1 row 75.9 / 73.7, 4 rows 114.3 / 109.1,
 // 64 rows 178.9 / 138.4; rows gathered (before the product for pairs, in it otherwise) 1 row 75.9 / 80.2, 4 rows 119.0 / 118.6,
 // 16 rows 249.7 / 136.0; NVFP4 4 rows 38.0 / 40.1, 64 rows 49.1 / 50.4, 128 rows 66.8 / 56.2 (K 7168, N 4096, 64 rows 32.7 / 28.5).
+// With the same rows for every expert: NVFP4 64 rows 47.1 / 47.0, 256 rows 81.5 / 60.4, MXFP4 45.0 / 45.1 and 78.0 / 57.8; two experts
+// of 2048 x 2048 stay below a wave of SMs, where pairs only start later: 256 rows 6.6 / 8.4.
 // fp32 results take single CTAs (exact_tile): NVFP4, 65536 rows of 128 experts, K 2048, N 1536 184 us, in pairs without the short
 // sums 199; 16384 rows of 32 experts, K 7168, N 4096 327 and 195.
 bool use_pairs(int64_t P, int64_t E, bool fp4) { return P >= (fp4 ? 64 : 4) * E; }
@@ -783,9 +785,9 @@ moe_status launch_product(ProductArgs a, const ProductMem& mem, bool exact, cuda
   return use_pairs(a.P, a.E, FMT != MOE_BF16) ? launch_tiles<FMT, 2, false>(a, mem, s) : launch_tiles<FMT, 1, false>(a, mem, s);
 }
 
-// xs[place[t, j]] = x[t]: a row is read once and stored k times, two 16-byte units a lane of a warp's segment.  A pair's token
+// xs[place[t, j]] = x[t]: a row is read once and stored k times, two 16-byte units a lane of a warp's segment.  A token
 // tile gathered inside the product, once for every weight block, costs more than this pass: 8192 tokens, 8 of 128 experts, K 2048,
-// N 1536 take 277 us from rows in order, 820 gathered by TMA and 710 by cp.async.
+// N 1536 take 280 us from rows in order and 327 with this pass; single CTAs 429 from rows in order and 1488 gathered by TMA.
 constexpr int GATHER_THREADS = 256, GATHER_SEG = 64;
 __global__ void __launch_bounds__(GATHER_THREADS)
 gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ place, int T, int row16, int k, uint4* __restrict__ xs) {

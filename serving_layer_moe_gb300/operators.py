@@ -8,7 +8,9 @@
 
 Argument checks, output tensors and pointers only: the work is in the library's kernels, there is no
 fallback.  Everything is enqueued on `stream` (torch's current stream if None); outputs are allocated for
-that stream.  Wrong arguments raise ValueError before anything is enqueued.
+that stream.  As with torch's own calls, a stream that is not the inputs' own has to be ordered behind what makes
+them (Stream.wait_stream), and they have to stay until it is done (Tensor.record_stream).  Wrong arguments raise
+ValueError before anything is enqueued.
 
 One decoded token runs all five calls in the time of a few launches, so the ordinary call goes straight to
 csrc/operators_host.cpp, which checks, allocates and launches.  What that leaves alone (it returns None) is
@@ -401,7 +403,11 @@ def _columns(groups, E, N, act, out_dtype):
 def grouped_matmul(x, w, groups, *, act="none", gather=False, out_dtype=torch.bfloat16, stream=None):
     """Row i of expert e: x[i] @ w[e].T, w [E, N, K] bf16, x bf16 [P, K] in expert order, or with gather=True
     [T, K] and grouped row i reads x[order[i] // k].  act="swiglu": w holds gate rows, then up rows, and the
-    result has N/2 columns.  K a multiple of 8 (moe_grouped_matmul).  Rows that no pair fills are undefined."""
+    result has N/2 columns.  K a multiple of 8 (moe_grouped_matmul).  Rows that no pair fills are undefined.
+
+    out_dtype: bf16 results are half the bytes on their way to combine.  fp32 ones save a rounding of each expert's
+    row and are summed more exactly: a 4-bit layer on normal weights is then 0.0017 from 64 bits instead of 0.0024.
+    One token takes the same time, 8192 tokens (NVFP4, K 2048, I 768) 441 us instead of 333."""
     if stream is None and isinstance(groups, ExpertGroups) and act in ACTS and out_dtype in _FLOATS:
         out = (_host_module or _host()).matmul(x, w, groups._c, ACTS[act], gather, _FLOATS[out_dtype])
         if out is not None:
@@ -426,7 +432,7 @@ def grouped_matmul(x, w, groups, *, act="none", gather=False, out_dtype=torch.bf
 def grouped_matmul_fp4(x, w, groups, *, act="none", quantize=False, g_out=None, out_dtype=torch.bfloat16, stream=None):
     """grouped_matmul of 4-bit rows x (FP4Rows laid out by these groups) and 4-bit weights w (FP4Rows [E, N, K]) of one
     format.  quantize=True (act="swiglu" only): the result as FP4Rows of that format with the matrix scale g_out
-    [1] (None = 1; "nvfp4" only), rounded from the fp32 values (moe_grouped_matmul_fp4)."""
+    [1] (None = 1; "nvfp4" only), rounded from the fp32 values (moe_grouped_matmul_fp4).  out_dtype: as there."""
     _rows(x, "x")
     _rows(w, "w")
     if stream is None and x.groups is not None and isinstance(groups, ExpertGroups) and act in ACTS and out_dtype in _FLOATS and \
