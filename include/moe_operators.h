@@ -149,9 +149,10 @@ moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_t K, const 
  * exact; where block scales differ widely (by e^2, K = 7168) they are 3e-6 off, for an fp32
  * result 5e-7.  out NULL: with act = 1 the result is quantised again as the 4-bit
  * rows out_codes / out_scales with matrix scale g_out (NULL = 1), and N/2 must be a multiple
- * of 32.  It is that of moe_quantize_fp4 on values with a bf16 result's sums and a SwiGLU to
- * |gate| + 10 units of 2^-23, by products with reciprocals good to three such units: a scale
- * or code is another one where that carries a value over a rounding edge.
+ * of 32.  It is that of moe_quantize_fp4 on values with a bf16 result's sums and SwiGLU (silu
+ * to |gate| + 10 units of 2^-23 of itself or 1e-18 of the gate), by products with reciprocals
+ * good to three such units: a scale or code is another one where that carries a value over a
+ * rounding edge.
  */
 moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, int32_t K, int32_t wdtype, const uint8_t* x_codes,
                                   const uint8_t* x_scales, const float* gx, const uint8_t* w_codes,

@@ -171,10 +171,10 @@ __device__ __forceinline__ void swiglu2(uint32_t gate0, uint32_t gate1, uint32_t
 }
 
 // silu(x) = x / (1 + exp(-x)) of fp32 results, within ten half units.  exp(-x) = 2^t 2^r with t the rounded product -x log2 e and r
-// what the rounding and log2 e's own have left out, |r| < 2^-17: 2^r = 1 + r ln 2.  (65536 rows of 128 experts, K 768, N 2048,
-// MXFP4, fp32 results: 195 us, with expf and a division 293.)  Past -128 the exponential is infinite all the same.
+// what the rounding and log2 e's own have left out, |r| < 2^-16: 2^r = 1 + r ln 2.  (65536 rows of 128 experts, K 768, N 2048,
+// MXFP4, fp32 results: 195 us, with expf and a division 293.)  Past -128 the exponential is infinite all the same, past 128 it is 0.
 __device__ __forceinline__ float silu(float x) {
-  const float c = fmaxf(x, -128.0f), t = c * -1.44269502f, r = fmaf(c, -1.44269502f, -t) - c * 1.92596303e-8f;
+  const float c = fminf(fmaxf(x, -128.0f), 128.0f), t = c * -1.44269502f, r = fmaf(c, -1.44269502f, -t) - c * 1.92596303e-8f;
   float e;
   asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
   if (e < INFINITY) e = fmaf(e, r * 0.693147181f, e);

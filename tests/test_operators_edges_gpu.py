@@ -324,3 +324,18 @@ def test_the_cache_decodes_what_the_router_picks(moe):
         assert np.array_equal(host(slots), plan.slot_map)
         assert relative_max_error(host(out), combine(host(gates), y, plan.slot_map, y)) <= TOL
     cache.close()
+
+
+def test_fp32_swiglu_of_huge_and_infinite_gates(moe):
+    big = float(torch.finfo(torch.bfloat16).max)
+    gates = np.array([big, np.inf, 2.0 ** 100, 2.0 ** 127, -big, -2.0 ** 100, np.nan, 128, 129, -128, -129, 88, -88, 1, 0, -0.0], np.float32)
+    with np.errstate(over="ignore"):
+        want = gates / (1 + np.exp(-gates.astype(np.float64)))
+    # products that are these gates, and ones for up: the first element of K times one, the others zeros
+    w, x = np.zeros((2, 32, 64), np.float32), np.zeros((6, 64), np.float32)
+    w[:, :16, 0], w[:, 16:, 0], x[:, 0] = gates, 1, 1
+    gr = moe.group_pairs(torch.tensor([[0], [1], [1], [0], [1], [0]], dtype=torch.int32, device="cuda"), 2)
+    for row in host(moe.grouped_matmul(dev(x, torch.bfloat16), dev(w, torch.bfloat16), gr, act="swiglu", out_dtype=torch.float32)):
+        assert np.array_equal(np.isnan(row), np.isnan(want)), row
+        ok = ~np.isnan(want)
+        assert np.array_equal(np.isinf(row), np.isinf(want)) and np.allclose(row[ok], want[ok], rtol=12 * EPS, atol=1e-33), row
