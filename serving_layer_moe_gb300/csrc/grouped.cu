@@ -174,7 +174,9 @@ __device__ __forceinline__ void swiglu2(uint32_t gate0, uint32_t gate1, uint32_t
 // what the rounding and log2 e's own have left out, |r| < 2^-16: 2^r = 1 + r ln 2.  (65536 rows of 128 experts, K 768, N 2048,
 // MXFP4, fp32 results: 195 us, with expf and a division 293.)  Past -128 the exponential is infinite all the same, past 128 it is 0.
 __device__ __forceinline__ float silu(float x) {
-  const float c = fminf(fmaxf(x, -128.0f), 128.0f), t = c * -1.44269502f, r = fmaf(c, -1.44269502f, -t) - c * 1.92596303e-8f;
+  constexpr double log2e = 1.4426950408889634;
+  constexpr float near = (float)log2e, rest = (float)(log2e - (double)near);   // in two parts, as Cody and Waite have it
+  const float c = fminf(fmaxf(x, -128.0f), 128.0f), t = c * -near, r = fmaf(c, -near, -t) - c * rest;
   float e;
   asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
   if (e < INFINITY) e = fmaf(e, r * 0.693147181f, e);
