@@ -31,8 +31,8 @@
  * holds pair order[i]; the rows of expert e are offsets[e] .. offsets[e + 1] - 1,
  * pairs ascending; place[p] is the row of pair p.  tiles[e] counts the 128-row
  * tiles of the experts before e, each expert's rows starting a new tile.  moe_route and
- * moe_group_pairs make them from any ids.  The other calls take them as they are: kernels
- * use what they hold as row numbers and do not check it.
+ * moe_group_pairs make them from any ids.  The other calls do not check that what they hold
+ * is a grouping; whatever it is, they read and write inside the arrays of these sizes only.
  *
  * 4-bit matrices (MOE_NVFP4, MOE_MXFP4).  codes [rows, K/2]: two e2m1 codes a
  * byte, the even element low.  scales: tiles of 128 rows x 4 blocks, 512 bytes,

@@ -32,6 +32,7 @@ constexpr int Q_SEG = 32, D_SEG = 128;
 struct QuantArgs {
   int64_t rows;      // input rows (of each matrix)
   int K, E, k, block_groups, g_count;
+  int64_t pairs, pad_rows;   // grouped rows, and the rows of their scale tiles
   const void* x;
   const float* g;
   const int32_t *offsets, *tiles, *place;   // NULL: a stack of matrices
@@ -40,11 +41,12 @@ struct QuantArgs {
 
 struct RowAt { int64_t row, pad; };   // an output row and the padded row of its scales; row < 0: none
 
-// row i of the rows in expert order
+// row i of the rows in expert order; none where i, or what offsets and tiles make of it, is not one of them
 __device__ __forceinline__ RowAt grouped_row(const QuantArgs& a, int i) {
-  if (i < 0) return RowAt{-1, 0};
+  if ((unsigned)i >= (unsigned)a.pairs) return RowAt{-1, 0};
   const int e = expert_of(a.offsets, a.E, i);
-  return RowAt{i, (int64_t)__ldg(a.tiles + e) * 128 + (i - __ldg(a.offsets + e))};
+  const int64_t pad = (int64_t)__ldg(a.tiles + e) * 128 + i - __ldg(a.offsets + e);
+  return RowAt{(uint64_t)pad < (uint64_t)a.pad_rows ? i : -1, pad};
 }
 
 // 16 elements of a row as they are; a row of K starts on 16 elements' bytes from its 16-byte aligned matrix
@@ -162,9 +164,10 @@ __global__ void __launch_bounds__(Q_THREADS) dequantize_kernel(QuantArgs a, O* _
   const int64_t m = blockIdx.z;
   const float g = a.g ? __ldg(a.g + (a.g_count > 1 ? m : 0)) : 1.0f;
   for (int64_t r = (int64_t)blockIdx.x * Q_WARPS + (threadIdx.x >> 5); r < a.rows; r += (int64_t)gridDim.x * Q_WARPS) {
-    const bool none = a.offsets && r >= __ldg(a.offsets + a.E);   // no pair fills the row
     const int64_t row = m * a.rows + r;
-    const int64_t pad = none ? 0 : a.offsets ? grouped_row(a, (int)r).pad : m * ((a.rows + 127) & ~127ll) + r;
+    const RowAt at = !a.offsets ? RowAt{row, m * ((a.rows + 127) & ~127ll) + r} : r < __ldg(a.offsets + a.E) ? grouped_row(a, (int)r) : RowAt{-1, 0};
+    const bool none = at.row < 0;   // no pair fills the row
+    const int64_t pad = at.pad;
     uint32_t q[D_SEG / 32], sc[D_SEG / 32];
 #pragma unroll
     for (int h = 0; h < D_SEG / 32; ++h) {
@@ -299,6 +302,7 @@ extern "C" moe_status moe_quantize_fp4(int32_t G, int32_t N, int32_t K, int32_t 
   a.rows = offsets ? N / k : N; a.K = K; a.E = E; a.g_count = g_count; a.x = x; a.g = g;
   a.block_groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
   a.offsets = offsets; a.tiles = tiles; a.place = offsets ? place : nullptr; a.codes = codes; a.scales = scales;
+  a.pairs = N; a.pad_rows = offsets ? moe_grouped_tiles(N, E) * 128 : 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid = segment_grid(a, G, (K / 16 + 7) / 8 * 8, Q_SEG), block(Q_THREADS);   // whole groups of blocks
   const bool f32 = dtype == MOE_F32, nv = wdtype == MOE_NVFP4;
@@ -328,6 +332,7 @@ extern "C" moe_status moe_dequantize_fp4(int32_t G, int32_t N, int32_t K, int32_
   a.rows = N; a.K = K; a.E = E; a.k = 1; a.g_count = g_count; a.g = g;
   a.block_groups = wdtype == MOE_NVFP4 ? (K + 63) / 64 : (K + 127) / 128;
   a.offsets = offsets; a.tiles = tiles;
+  a.pairs = N; a.pad_rows = offsets ? moe_grouped_tiles(N, E) * 128 : 0;
   a.codes = const_cast<uint8_t*>(codes); a.scales = const_cast<uint8_t*>(scales);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid = segment_grid(a, G, K / 8, D_SEG), block(Q_THREADS);

@@ -59,6 +59,8 @@ constexpr int SMEM_LIMIT = 227 * 1024;
 struct ProductArgs {
   int P, E, N, K, k, cols, groups, gw_count, act, gather, quant, wide, few;
   int m_blocks, kslices, stages, stage_bytes, b_rows, w_tiles, w_parts;   // w_parts: scale tiles one weight tile's rows are in
+  int most_tiles;                // token tiles that P rows of E experts can make
+  int64_t pad_rows;              // rows of the scale tiles that grouped rows have
   const float *gx, *gw, *g_out;
   const int32_t *offsets, *order;
   void* out;
@@ -84,6 +86,9 @@ struct Shape4 {
   static constexpr int BOX = 16 * CG;                   // token rows of a small load; a tile's 128 rows take one
 };
 
+// where expert e's rows start, whatever the offsets hold: a row number of the call's, or P
+__device__ __forceinline__ int row_at(const ProductArgs& a, int e) { return min(max(__ldg(a.offsets + e), 0), a.P); }
+
 // item `it` into o, which holds the one before (tt = -1: none)
 template <int FMT, int CG>
 __device__ __forceinline__ void item_at(const ProductArgs& a, const int32_t* first, int it, Item& o) {
@@ -99,12 +104,12 @@ __device__ __forceinline__ void item_at(const ProductArgs& a, const int32_t* fir
     else hi = mid;
   }
   o.e = lo;
-  const int j = tt - first[lo], r0 = __ldg(a.offsets + lo), n = __ldg(a.offsets + lo + 1) - r0;
+  const int j = tt - first[lo], r0 = row_at(a, lo), n = max(row_at(a, lo + 1), r0) - r0;
   int chunk = S::NMAX;
   if constexpr (!S::FP4) {
     // even shares; 4-bit tiles start on their scales' 128-row tiles
     const int nt = first[lo + 1] - first[lo];
-    chunk = ((n + nt - 1) / nt + 16 * CG - 1) / (16 * CG) * (16 * CG);
+    chunk = min(S::NMAX, ((n + nt - 1) / nt + 16 * CG - 1) / (16 * CG) * (16 * CG));
   }
   o.row0 = r0 + j * chunk;
   o.n = min(chunk, n - j * chunk);
@@ -289,14 +294,15 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     int run = 0;
     for (int b = 0; b < a.E; b += 32) {
       const int e = b + lane;
-      const int c = e < a.E ? (__ldg(a.offsets + e + 1) - __ldg(a.offsets + e) + S::NMAX - 1) / S::NMAX : 0;
+      const int c = e < a.E ? (max(row_at(a, e + 1) - row_at(a, e), 0) + S::NMAX - 1) / S::NMAX : 0;
       int x = c;
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += v;
       }
-      if (e < a.E) first[e] = run + x - c;
-      run += __shfl_sync(0xffffffffu, x, 31);
+      // offsets that do not ascend could make more tiles than the rows do
+      if (e < a.E) first[e] = min(run + x - c, a.most_tiles);
+      run = min(run + __shfl_sync(0xffffffffu, x, 31), a.most_tiles);
     }
     if (lane == 0) first[a.E] = run;
   }
@@ -400,7 +406,7 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       const int row0 = o.row0 + (int)rank * (columns<CG>(o.n) / CG), rows = token_rows<FMT, CG>(a, o);
       if (S::GATHER && a.gather) {
         __syncwarp();
-        for (int r = lane; r < rows; r += 32) gathered[r] = __ldg(a.order + row0 + min(r, o.n - 1)) / a.k;
+        for (int r = lane; r < rows; r += 32) gathered[r] = min(max(__ldg(a.order + row0 + min(r, o.n - 1)) / a.k, 0), a.P / a.k - 1);
         __syncwarp();
       }
       for (int ks = 0; ks < a.kslices; ++ks) {
@@ -505,7 +511,8 @@ product_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       }
       const float go = S::NV && a.quant && a.g_out ? __ldg(a.g_out) : 1.0f, up = fabsf(go) < 1e-30f ? 0x1p64f : 1.0f;
       const float rgo = __frcp_rn(go * up), sixth = kSixth * up;
-      const int64_t pad0 = S::FP4 && a.quant ? (int64_t)__ldg(a.tiles + o.e) * 128 + (o.row0 - __ldg(a.offsets + o.e)) : 0;
+      const int64_t pad0 = !(S::FP4 && a.quant) ? 0
+          : min(max((int64_t)__ldg(a.tiles + o.e) * 128 + (o.row0 - row_at(a, o.e)), (int64_t)0), a.pad_rows - o.n);
       bool ok = warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
       if (S::FP4 && !S::NV && a.quant) ok = named_and(1 + part, 128, ok);   // these four warps wait for one another below
       if (!ok) {
@@ -727,8 +734,10 @@ moe_status launch_tiles(ProductArgs a, const ProductMem& mem, cudaStream_t s) {
   if (!ok) return fail(MOE_ECUDA, "cuTensorMapEncodeTiled failed");
 
   // at most every token tile the rows can make, on every weight block
-  const int64_t most = (a.P + (int64_t)(S::NMAX - 1) * std::min(a.P, a.E)) / S::NMAX * a.m_blocks;
+  const int64_t tiles = (a.P + (int64_t)(S::NMAX - 1) * std::min(a.P, a.E)) / S::NMAX, most = tiles * a.m_blocks;
   if (most > 0x7fffffff) return fail(MOE_EINVAL, "P = %d rows of N = %d columns are too many tiles", a.P, a.N);
+  a.most_tiles = (int)tiles;
+  a.pad_rows = moe_grouped_tiles(a.P, a.E) * 128;
   static bool allowed[64] = {};   // the kernel's shared memory, once per device
   int dev = 0;
   CK(cudaGetDevice(&dev));
@@ -792,7 +801,7 @@ moe_status launch_product(ProductArgs a, const ProductMem& mem, bool exact, cuda
 // N 1536 take 280 us from rows in order and 327 with this pass; single CTAs 429 from rows in order and 1488 gathered by TMA.
 constexpr int GATHER_THREADS = 256, GATHER_SEG = 64;
 __global__ void __launch_bounds__(GATHER_THREADS)
-gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ place, int T, int row16, int k, uint4* __restrict__ xs) {
+gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ place, int T, int row16, int k, int P, uint4* __restrict__ xs) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, c = blockIdx.y * GATHER_SEG + lane;
@@ -803,7 +812,7 @@ gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ place, in
       if (c + 32 * h < row16) v[h] = __ldg(x + (size_t)t * row16 + c + 32 * h);
     for (int j = 0; j < k; ++j) {
       const int row = __ldg(place + (size_t)t * k + j);
-      if (row < 0) continue;
+      if ((unsigned)row >= (unsigned)P) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (c + 32 * h < row16) xs[(size_t)row * row16 + c + 32 * h] = v[h];
@@ -855,7 +864,7 @@ extern "C" moe_status moe_grouped_matmul(int32_t P, int32_t E, int32_t N, int32_
       return fail(MOE_EINVAL, "workspace must hold %lld bytes, 16-byte aligned, holds %lld", (long long)need, (long long)workspace_bytes);
     const int T = P / k, warps = GATHER_THREADS / 32, segs = (K / 8 + GATHER_SEG - 1) / GATHER_SEG;
     const dim3 grid(std::min((T + warps - 1) / warps, std::max(1, operator_sms() * 64 / segs)), segs);
-    CK(launch_pdl(gather_kernel, grid, dim3(GATHER_THREADS), 0, static_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), place, T, K / 8, k,
+    CK(launch_pdl(gather_kernel, grid, dim3(GATHER_THREADS), 0, static_cast<cudaStream_t>(stream), static_cast<const uint4*>(x), place, T, K / 8, k, P,
                   static_cast<uint4*>(workspace)));
     a.gather = 0;
     x = workspace;

@@ -464,7 +464,7 @@ combine_kernel(int T, int k, int N, const Y* __restrict__ y, const int32_t* __re
                const float* __restrict__ w, O* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  const int cols = N / V;
+  const int cols = N / V, rows = T * k;
   const int64_t units = (int64_t)T * cols;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
     // a 64-bit division only where it is needed (4 us of 85)
@@ -483,7 +483,7 @@ combine_kernel(int T, int k, int N, const Y* __restrict__ y, const int32_t* __re
       }
 #pragma unroll
       for (int j = 0; j < COMBINE_ROWS; ++j) {
-        if (row[j] < 0) continue;
+        if ((unsigned)row[j] >= (unsigned)rows) continue;
         const Y* src = y + (size_t)row[j] * N + c;
         if constexpr (sizeof(Y) * V % 16 == 0) {
 #pragma unroll
@@ -495,7 +495,7 @@ combine_kernel(int T, int k, int N, const Y* __restrict__ y, const int32_t* __re
       }
 #pragma unroll
       for (int j = 0; j < COMBINE_ROWS; ++j) {
-        if (row[j] < 0) continue;
+        if ((unsigned)row[j] >= (unsigned)rows) continue;
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = fmaf(g[j], (float)tmp[j][i], acc[i]);
       }

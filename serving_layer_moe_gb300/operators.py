@@ -161,7 +161,7 @@ def _scale(g, name, most, index):
 class ExpertGroups:
     """The (token, expert) pairs of a call in expert order: offsets and tiles [E + 1], order [T * k] and
     place [T, k], all int32 (include/moe_operators.h, "Expert order").  Types and sizes are checked here; the tensors
-    cannot be exchanged after.  What they hold is not looked at: it has to be a grouping, such as route and group_pairs make."""
+    cannot be exchanged after.  What they hold is not: other than a grouping it gives wrong results, inside the arrays."""
 
     __slots__ = ("_c", "_views")
 

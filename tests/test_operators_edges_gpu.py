@@ -339,3 +339,85 @@ def test_fp32_swiglu_of_huge_and_infinite_gates(moe):
         assert np.array_equal(np.isnan(row), np.isnan(want)), row
         ok = ~np.isnan(want)
         assert np.array_equal(np.isinf(row), np.isinf(want)) and np.allclose(row[ok], want[ok], rtol=12 * EPS, atol=1e-33), row
+
+
+# ---------------------------------------------------------------------------------------------------------
+# groups that are none
+# ---------------------------------------------------------------------------------------------------------
+class Guarded:
+    """Memory for an output with as much again on both sides, which has to stay as it is."""
+
+    def __init__(self, n):
+        self.room, self.n = torch.full((n + (2 << 20),), 0x5A, dtype=torch.uint8, device="cuda"), n
+        self.at = self.room.data_ptr() + (1 << 20)
+        assert self.at % 16 == 0
+
+    def kept(self):
+        return bool((self.room[:1 << 20] == 0x5A).all()) and bool((self.room[(1 << 20) + self.n:] == 0x5A).all())
+
+
+def strange_groups(kind, P, E, rng):
+    i32 = np.iinfo(np.int32)
+    if kind == "random":
+        return [rng.integers(i32.min, i32.max, n, dtype=np.int64).astype(np.int32) for n in (E + 1, E + 1, P, P)]
+    if kind == "larger":      # a grouping, of four times the rows
+        ids = rng.integers(0, E, (4 * P, 1))
+        off, tiles, order, place = ref.groups(ids, E)
+        return [np.asarray(a, np.int32) for a in (off, tiles, order[:P], place.reshape(-1)[:P])]
+    if kind == "falling":
+        off = np.linspace(P, 0, E + 1).astype(np.int32)
+        return [off, off, np.arange(P, dtype=np.int32)[::-1].copy(), np.full(P, P, np.int32)]
+    edge = np.array([i32.min, -1, 0, P - 1, P, i32.max])
+    return [rng.choice(edge, n).astype(np.int32) for n in (E + 1, E + 1, P, P)]
+
+
+@pytest.mark.parametrize("kind", ["random", "larger", "falling", "edges"])
+@pytest.mark.parametrize("P,E", [(96, 40), (1200, 6), (640, 5)])
+def test_no_groups_lead_outside_the_arrays(moe, kind, P, E):
+    """Offsets, tiles, orders and places that are no grouping: wrong results, nothing read or written elsewhere, and the next call right."""
+    from serving_layer_moe_gb300.operators import _operators
+    lib, s = _operators(), torch.cuda.current_stream().cuda_stream
+    rng = np.random.default_rng(P + E)
+    k, N, K = 2, 256, 128
+    T = P // k
+    off, tiles, order, place = (dev(a) for a in strange_groups(kind, P, E, rng))
+    x, w = torch.randn(P, K, device="cuda").bfloat16(), torch.randn(E, N, K, device="cuda").bfloat16()
+    y, gates = torch.randn(P, N, device="cuda"), torch.rand(T, k, device="cuda")
+    n_tiles = lib.moe_grouped_tiles(P, E)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    outs = []
+
+    def out(n):
+        outs.append(Guarded(n))
+        return outs[-1].at
+
+    def done(status):
+        assert status == 0, lib.moe_last_error()
+
+    done(lib.moe_combine(T, k, N, 0, p(y), p(place), p(gates), 0, out(T * N * 4), s))
+    for act in (0, 1):
+        for gathered in (False, True):
+            for od, size in ((0, 4), (1, 2)):
+                need = lib.moe_grouped_matmul_workspace(P, E, K, gathered)
+                done(lib.moe_grouped_matmul(P, E, N, K, p(x), T if gathered else P, p(order) if gathered else None, p(place) if gathered else None, k, p(w),
+                                            p(off), p(tiles), act, od, out(P * N // (1 + act) * size), out(need) if need else None, need, s))
+    for fmt, code in (("nvfp4", 3), ("mxfp4", 4)):
+        groups = -(-K // (64 if fmt == "nvfp4" else 128))
+        codes, scales = out(P * K // 2), out(n_tiles * groups * 512)
+        done(lib.moe_quantize_fp4(1, P, K, 1, p(x), code, None, 0, E, k, p(off), p(tiles), p(place), codes, scales, s))
+        done(lib.moe_dequantize_fp4(1, P, K, code, codes, scales, None, 0, E, p(off), p(tiles), 1, out(P * K * 2), s))
+        w4 = moe.quantize_fp4(w, fmt)
+        for act, od, size in ((0, 1, 2), (0, 0, 4), (1, 1, 2), (1, 0, 4)):
+            done(lib.moe_grouped_matmul_fp4(P, E, N, K, code, codes, scales, None, p(w4.codes), p(w4.scales), None, 0, p(off), p(tiles), act, od,
+                                            out(P * N // (1 + act) * size), None, None, None, s))
+        og = -(-N // 2 // (64 if fmt == "nvfp4" else 128))
+        done(lib.moe_grouped_matmul_fp4(P, E, N, K, code, codes, scales, None, p(w4.codes), p(w4.scales), None, 0, p(off), p(tiles), 1, 1, None,
+                                        out(P * N // 4), out(n_tiles * og * 512), None, s))
+    torch.cuda.synchronize()
+    assert all(o.kept() for o in outs)
+    moe.check_operators()
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    gr, (_, _, right, _) = moe.group_pairs(dev(ids), E), ref.groups(ids, E)
+    got = host(moe.grouped_matmul(x[:T].contiguous(), w, gr, gather=True, out_dtype=torch.float32))
+    want = np.einsum("pk,pnk->pn", host(x)[right // k].astype(np.float64), host(w).astype(np.float64)[ids.reshape(-1)[right]])
+    assert distance(got, want) < 1e-6
