@@ -1,16 +1,16 @@
 /*
  * moe_operators.h -- the operators around a cache of experts, for callers that
- * hold their tensors themselves: the router, 4-bit quantisation, products grouped
- * by expert, and the weighted sum of the experts' rows.  Same library as
+ * hold their tensors themselves: the router, 4- and 8-bit quantisation, products grouped
+ * by expert, the weighted sum of the experts' rows, and the norms around a block.  Same library as
  * moe_cache.h (libmoecache.so), same status codes, moe_dtype values and
  * moe_last_error().
  *
  * One layer, router to output, is
  *   moe_route (logits -> ids, gates, pairs in expert order)
- *   moe_quantize_fp4 (rows gathered by expert) or the bf16 rows as they are
- *   moe_grouped_matmul / _fp4 with act = 1 (gate/up product and SwiGLU)
- *   moe_grouped_matmul / _fp4 (down product)
- *   moe_combine (sum over each token's experts)
+ *   moe_quantize_fp4 / _fp8 (rows gathered by expert) or the bf16 rows as they are
+ *   moe_grouped_matmul / _fp4 / _fp8 with act = 1 (gate/up product and SwiGLU)
+ *   moe_grouped_matmul / _fp4 / _fp8 (down product)
+ *   moe_combine (sum over each token's experts), or moe_combine_norm (with the residual and the norms)
  *
  * Conventions for every call:
  *  - Every pointer is device memory of the current device, owned by the caller.
@@ -167,6 +167,61 @@ moe_status moe_grouped_matmul_fp4(int32_t P, int32_t E, int32_t N, int32_t K, in
  */
 moe_status moe_combine(int32_t T, int32_t k, int32_t N, int32_t y_dtype, const void* y, const int32_t* place,
                        const float* topk_w, int32_t out_dtype, void* out, void* stream);
+
+/*
+ * 8-bit blocks.  codes: e4m3.  A block has one fp32 scale: a / 448 (the product of a and the fp32
+ * nearest to 1 / 448), a its largest |x| or 2^-100 if that is more; its codes are e4m3(448 x / a), the
+ * product and the quotient each correctly rounded in 32 bits, nearest even.  A block with a NaN or an
+ * infinity has the scale NaN and codes 0.  K a multiple of 16; a block past K's end is short.
+ *   rows     [R, K]: blocks of 128 elements of a row, scales [ceil(K / 128), R] (the scales of one
+ *            block of all rows together, as a product takes them)
+ *   weights  [G, N, K]: blocks of 128 x 128, scales [G, ceil(N / 128), ceil(K / 128)], as MOE_FP8 experts
+ *            and checkpoints have them
+ * x in dtype MOE_BF16 or MOE_F32.  moe_quantize_fp8: x [T, K]; place NULL (k = 1): row t of the output is row
+ * t of x; otherwise row t becomes the rows place[t, 0 .. k - 1] of T * k, none where that is not a
+ * row.  Rows that no pair fills, and their scales, are left as they are.
+ */
+moe_status moe_quantize_fp8(int32_t T, int32_t K, int32_t dtype, const void* x, int32_t k, const int32_t* place, uint8_t* codes,
+                            float* scales, void* stream);
+moe_status moe_quantize_fp8_weights(int32_t G, int32_t N, int32_t K, int32_t dtype, const void* w, uint8_t* codes, float* scales,
+                                    void* stream);
+
+/* code * scale in fp32, stored in dtype (MOE_BF16 or MOE_F32), of weights [G, N, K] (tiles = 1) or rows [N, K] (tiles = 0, G = 1). */
+moe_status moe_dequantize_fp8(int32_t G, int32_t N, int32_t K, int32_t tiles, const uint8_t* codes, const float* scales, int32_t dtype,
+                              void* out, void* stream);
+
+/*
+ * Products of 8-bit rows and weights: out[i] = x[i] * w[e]^T for the rows i of each expert e, rows in expert order
+ * as offsets [E + 1] has them; offsets NULL (E = 1): all P rows are one matrix's.  K a multiple of 16.
+ *   The products of one block of K are summed in the tensor cores' fp32 accumulators (four additions), multiplied by
+ *   the fp32 product of both scales, and added up over K in fp32.
+ *   act 1: SwiGLU; w holds N/2 gate rows, then N/2 up rows (N a multiple of 128).
+ *   out [P, N or N/2] in out_dtype (MOE_BF16 or MOE_F32); rows from offsets[E] on are left as they are.  silu of fp32
+ *   results is within 11 half units, of others within |gate| + 10 units or 1e-18 of the gate.
+ *   out NULL (act 1): the result as 8-bit rows out_codes [P, N/2], out_scales [ceil(N / 256), P], rounded from the fp32
+ *   values: that of moe_quantize_fp8 up to products with reciprocals good to three units, so a code is another one where
+ *   that carries a value over a rounding edge.
+ */
+moe_status moe_grouped_matmul_fp8(int32_t P, int32_t E, int32_t N, int32_t K, const uint8_t* x_codes, const float* x_scales,
+                                  const uint8_t* w_codes, const float* w_scales, const int32_t* offsets, int32_t act, int32_t out_dtype,
+                                  void* out, uint8_t* out_codes, float* out_scales, void* stream);
+
+/*
+ * The end of a block, and the norm before the next one:
+ *   c = sum_j topk_w[t, j] * y[place[t, j]] (j order, as moe_combine), or y[t] with place NULL (k = 1); 0 with y NULL
+ *   c += shared[t]                              shared [T, N] in y_dtype, or NULL
+ *   c = c / sqrt(mean(c^2) + eps) * post        post [N], or NULL
+ *   c = gate * c                                gate [N], with gate_rows 1 [T]; fp32, or NULL
+ *   h = alpha * residual[t] + c                 stored in r_dtype, unless h is NULL
+ *   z = h / sqrt(mean(h^2) + eps) * pre         stored in z_dtype, of the h before it is rounded; pre and z may be NULL
+ * Everything in between is fp32: a row whose squares overflow that (values past 1e19) has z = 0.  h may be residual itself.
+ * N <= 32768, eps a positive normal number.  shared, post and gate need y; a pair whose place is no row of T * k
+ * contributes nothing.
+ */
+moe_status moe_combine_norm(int32_t T, int32_t k, int32_t N, int32_t y_dtype, const void* y, const int32_t* place, const float* topk_w,
+                            const void* shared, int32_t post_dtype, const void* post, int32_t gate_rows, const float* gate, float alpha,
+                            int32_t r_dtype, const void* residual, int32_t pre_dtype, const void* pre, float eps, void* h, int32_t z_dtype,
+                            void* z, void* stream);
 
 /* Synchronise `stream`; MOE_EDEVICE if a wait inside an operator kernel has run out on this
  * device since the last check (the flag is cleared). */

@@ -10,8 +10,9 @@ import importlib.util as _util
 
 from .binding import (DTYPES, SYMBOLS, MoECache, MoEError, bench_bw, load_library)  # noqa: F401
 
-_OPERATORS = ("OPERATOR_SYMBOLS", "ExpertGroups", "FP4Rows", "check_operators", "combine", "dequantize_fp4", "fp4_scale",
-              "group_pairs", "grouped_matmul", "grouped_matmul_fp4", "quantize_fp4", "route")
+_OPERATORS = ("OPERATOR_SYMBOLS", "ExpertGroups", "FP4Rows", "FP8Rows", "FP8Weights", "check_operators", "combine", "combine_norm",
+              "dequantize_fp4", "dequantize_fp8", "fp4_scale", "group_pairs", "grouped_matmul", "grouped_matmul_fp4", "grouped_matmul_fp8",
+              "matmul_fp8", "quantize_fp4", "quantize_fp8", "quantize_fp8_weights", "residual_norm", "rms_norm", "route")
 
 __all__ = ["MoECache", "MoEError", "bench_bw", "load_library", "DTYPES", "SYMBOLS"]
 if _util.find_spec("torch") is not None:

@@ -49,54 +49,6 @@ __device__ __forceinline__ RowAt grouped_row(const QuantArgs& a, int i) {
   return RowAt{(uint64_t)pad < (uint64_t)a.pad_rows ? i : -1, pad};
 }
 
-// 16 elements of a row as they are; a row of K starts on 16 elements' bytes from its 16-byte aligned matrix
-template <typename X>
-struct Raw16 {
-  static constexpr int W = sizeof(X) == 4 ? 16 : 8;
-  uint32_t w[W];
-  __device__ __forceinline__ void load(const X* p) {
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(p);
-    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {   // 32 bytes an instruction
-#pragma unroll
-      for (int i = 0; i < W; i += 8)
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]), "=r"(w[i + 6]), "=r"(w[i + 7])
-                     : "l"(src + i));
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; i += 4) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + i));
-        w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
-      }
-    }
-  }
-  // bits of the largest |x| as fp32
-  __device__ __forceinline__ uint32_t top() const {
-    uint32_t m = 0u;
-    if constexpr (sizeof(X) == 4) {
-#pragma unroll
-      for (int i = 0; i < W; ++i) m = max(m, w[i] & 0x7fffffffu);
-    } else {   // two at a time: bf16 patterns without their signs order like the values
-#pragma unroll
-      for (int i = 0; i < W; i += 2) m = __vimax3_u16x2(m, w[i] & 0x7fff7fffu, w[i + 1] & 0x7fff7fffu);
-      m = max(m << 16, m & 0xffff0000u);
-    }
-    return m;
-  }
-  __device__ __forceinline__ void values(float (&v)[16]) const {
-    if constexpr (sizeof(X) == 4) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    }
-  }
-};
-
 // GROUPED: rows become the rows of their pairs in expert order; otherwise a stack of matrices.
 // Blocks an SM: loads in flight against registers.  805 MB of bf16 to NVFP4 takes 211 us with 4, 178 with 6 and 214 with 8, where
 // registers spill; to MXFP4 186, 157 and 147 (150 at the copy rate); 403 MB of fp32 84 with 3, 74 with 4, 69 with 5 or 6 (68).

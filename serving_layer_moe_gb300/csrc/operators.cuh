@@ -11,6 +11,9 @@ constexpr int64_t kMaxPairs = 0x70000000;   // T * k: row numbers, and those a b
 // SMs of the current device (looked up once per device).
 int operator_sms();
 
+// Synchronise; whether a wait of the 8-bit products has run out (moe_operators_check).
+moe_status operators_check8(cudaStream_t s);
+
 __host__ __device__ __forceinline__ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // expert of a grouped row, or of a row tile: the e with first[e] <= i < first[e + 1]
@@ -55,6 +58,54 @@ __device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
   asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// 16 elements of a row as they are; a row of K starts on 16 elements' bytes from its 16-byte aligned matrix
+template <typename X>
+struct Raw16 {
+  static constexpr int W = sizeof(X) == 4 ? 16 : 8;
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const X* p) {
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p);
+    if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {   // 32 bytes an instruction
+#pragma unroll
+      for (int i = 0; i < W; i += 8)
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]), "=r"(w[i + 6]), "=r"(w[i + 7])
+                     : "l"(src + i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(src + i));
+        w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+      }
+    }
+  }
+  // bits of the largest |x| as fp32
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0u;
+    if constexpr (sizeof(X) == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) m = max(m, w[i] & 0x7fffffffu);
+    } else {   // two at a time: bf16 patterns without their signs order like the values
+#pragma unroll
+      for (int i = 0; i < W; i += 2) m = __vimax3_u16x2(m, w[i] & 0x7fff7fffu, w[i + 1] & 0x7fff7fffu);
+      m = max(m << 16, m & 0xffff0000u);
+    }
+    return m;
+  }
+  __device__ __forceinline__ void values(float (&v)[16]) const {
+    if constexpr (sizeof(X) == 4) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+};
 
 // Correctly rounded x / d from r = 1 / d rounded to nearest, without a division (Markstein 1990): with q = x r, the
 // remainder x - q d is exact in one fma, and q + remainder * r rounds to the quotient.  Away from the ends of the exponent
@@ -139,6 +190,17 @@ __device__ __forceinline__ uint2 encode16(const float (&v)[16], uint32_t amax_bi
 #pragma unroll
   for (int i = 0; i < 8; ++i) put(i, __fdiv_rn(v[2 * i], step), __fdiv_rn(v[2 * i + 1], step));
   return make_uint2(w[0], w[1]);
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit blocks
+// ---------------------------------------------------------------------------
+constexpr float kLeast8 = 0x1p-100f;   // a block's largest |x| counts as this at least, so that no scale is 0
+// two values -> two e4m3 codes, lo in the low byte
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 }  // namespace moe

@@ -392,6 +392,146 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CATCH
 }
 
+// contiguous fp32 or bf16 of `dim` dimensions on `index`, aligned to 16 bytes where `wide`; its code to *dt.  None is fine where `none`
+bool floats_in(PyObject* o, int dim, int64_t index, bool wide, bool none, int* dt, const void** p) {
+  *dt = MOE_F32;
+  *p = nullptr;
+  if (o == Py_None) return none;
+  const at::Tensor* t = tensor(o, dim, index);
+  if (!t || (*dt = float_code(*t)) < 0) return false;
+  *p = t->data_ptr();
+  return !wide || aligned(*p, 16);
+}
+bool sized(PyObject* o, at::IntArrayRef shape) { return o == Py_None || THPVariable_Unpack(o).sizes() == shape; }
+
+// codes and scales of 8-bit blocks, as they are now: [R, K] with scales [blocks of K, R], or [N, K] / [G, N, K] with a block of 128 x 128 each
+struct Blocks8 { int64_t index, G, N, K; const uint8_t* codes; const float* scales; };
+bool blocks8_in(PyObject* c, PyObject* s, bool rows, int dim, int64_t index, Blocks8& b) {
+  const at::Tensor* codes = typed(c, ScalarType::Float8_e4m3fn, dim, index);
+  if (!codes) return false;
+  b.index = codes->get_device();
+  b.G = dim == 3 ? codes->size(0) : 1;
+  b.N = codes->size(dim - 2);
+  b.K = codes->size(dim - 1);
+  if (b.K < 1 || b.K % 16 || !matrices_fit(b.G, b.N, b.K)) return false;
+  const at::Tensor* scales = typed(s, ScalarType::Float, dim, b.index);
+  const int64_t kb = (b.K + 127) / 128, nb = (b.N + 127) / 128;
+  if (!scales || (dim == 3 && scales->size(0) != b.G) || scales->size(dim - 2) != (rows ? kb : nb) || scales->size(dim - 1) != (rows ? b.N : kb)) return false;
+  if (bytes_from(*codes) < b.G * b.N * b.K || bytes_from(*scales) < scales->numel() * 4) return false;
+  b.codes = static_cast<const uint8_t*>(codes->data_ptr());
+  b.scales = static_cast<const float*>(scales->data_ptr());
+  return aligned(b.codes, 16);
+}
+// room for rows [R, K] and their scales
+PyObject* make_rows8(int64_t R, int64_t K, int64_t index, uint8_t** codes, float** scales) {
+  const int64_t cb = (R * K + 15) / 16 * 16, kb = (K + 127) / 128;
+  const at::Tensor b = room(cb + kb * R * 4, index);
+  *codes = static_cast<uint8_t*>(b.data_ptr());
+  *scales = reinterpret_cast<float*>(*codes + cb);
+  return Py_BuildValue("(NN)", THPVariable_Wrap(on(b, 0, {R, K}, ScalarType::Float8_e4m3fn)), THPVariable_Wrap(on(b, cb, {kb, R}, ScalarType::Float)));
+}
+PyObject* or_raise(moe_status st, PyObject* r) {
+  if (st == MOE_OK) return r;
+  Py_XDECREF(r);
+  return raise(st);
+}
+
+// quantize8(x, groups) -> (codes, scales)
+PyObject* quantize8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  TRY
+  if (n != 2) OTHERWISE;
+  Groups g{};
+  const bool grouped = a[1] != Py_None;
+  if (grouped && !groups_in(a[1], g)) OTHERWISE;
+  const at::Tensor* x = tensor(a[0], 2, grouped ? g.index : -1);
+  if (!x) OTHERWISE;
+  const int dt = float_code(*x);
+  const int64_t T = x->size(0), K = x->size(1), index = x->get_device();
+  void* s;
+  if (dt < 0 || K < 1 || K % 16 || !matrices_fit(1, T, K) || !pairs_fit(T, 1) || (grouped && T != g.T) || (grouped && g.k < 1) || !aligned(x->data_ptr(), 16) ||
+      !here(index, &s))
+    OTHERWISE;
+  uint8_t* codes;
+  float* scales;
+  PyObject* r = make_rows8(grouped ? g.P : T, K, index, &codes, &scales);
+  return or_raise(moe_quantize_fp8((int32_t)T, (int32_t)K, dt, x->data_ptr(), grouped ? (int32_t)g.k : 1, ptr<int32_t>(g.place), codes, scales, s), r);
+  CATCH
+}
+
+// matmul8(x codes, x scales, w codes, w scales, groups, act, quantize, out dtype) -> tensor, or (codes, scales)
+PyObject* matmul8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  TRY
+  if (n != 8) OTHERWISE;
+  Groups g{};
+  Blocks8 x, w;
+  const bool grouped = a[4] != Py_None;
+  if (grouped && !groups_in(a[4], g)) OTHERWISE;
+  if (!blocks8_in(a[2], a[3], false, grouped ? 3 : 2, grouped ? g.index : -1, w) || !blocks8_in(a[0], a[1], true, 2, w.index, x)) OTHERWISE;
+  const long act = PyLong_AsLong(a[5]), od = PyLong_AsLong(a[7]);
+  const int quant = PyObject_IsTrue(a[6]);
+  if (PyErr_Occurred()) return nullptr;
+  const int64_t cols = act ? w.N / 2 : w.N;
+  void* s;
+  if ((grouped && (w.G != g.E || x.N != g.P)) || x.K != w.K || w.N < 1 || !pairs_fit(x.N, 1) || (act && w.N % 128) || (quant && !act) || !here(w.index, &s)) OTHERWISE;
+  PyObject* r;
+  void* out = nullptr;
+  uint8_t* codes = nullptr;
+  float* scales = nullptr;
+  if (quant) {
+    r = make_rows8(x.N, cols, w.index, &codes, &scales);
+  } else {
+    const at::Tensor t = empty({x.N, cols}, float_type(od), w.index);
+    out = t.data_ptr();
+    r = THPVariable_Wrap(t);
+  }
+  if (x.N == 0) return r;   // its memory has no address
+  return or_raise(moe_grouped_matmul_fp8((int32_t)x.N, grouped ? (int32_t)g.E : 1, (int32_t)w.N, (int32_t)w.K, x.codes, x.scales, w.codes, w.scales,
+                                         grouped ? ptr<int32_t>(g.offsets) : nullptr, (int32_t)act, (int32_t)od, out, codes, scales, s), r);
+  CATCH
+}
+
+// block_end(y, groups, topk_w, residual, shared, post, gate, scale, pre, eps, z dtype) -> h, or (h, z); z alone with y None
+PyObject* block_end(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  TRY
+  if (n != 11) OTHERWISE;
+  const at::Tensor* r = tensor(a[3], 2, -1);
+  if (!r) OTHERWISE;
+  const int64_t T = r->size(0), N = r->size(1), index = r->get_device();
+  const bool wide = N % 8 == 0, grouped = a[1] != Py_None, any = a[0] != Py_None, normed = a[8] != Py_None;
+  Groups g{};
+  const at::Tensor* w = nullptr;
+  int yd, rd, sd, pd, qd, gd;
+  const void *y, *res, *shared, *post, *pre, *gate;
+  if (grouped) {
+    if (!any || !groups_in(a[1], g) || g.index != index || g.T != T || g.k < 1) OTHERWISE;
+    w = typed(a[2], ScalarType::Float, 2, index);
+    if (!w || w->size(0) != g.T || w->size(1) != g.k) OTHERWISE;
+  }
+  if (N < 1 || N > 32768 || !pairs_fit(T, 1) || !floats_in(a[3], 2, index, wide, false, &rd, &res) || !floats_in(a[0], 2, index, wide, true, &yd, &y) ||
+      !sized(a[0], {grouped ? g.P : T, N}) || !floats_in(a[4], 2, index, wide, true, &sd, &shared) || !sized(a[4], {T, N}) || (shared && sd != yd) ||
+      !floats_in(a[5], 1, index, wide, true, &pd, &post) || !sized(a[5], {N}) || !floats_in(a[8], 1, index, wide, true, &qd, &pre) || !sized(a[8], {N}) ||
+      (!any && (!normed || shared || post || a[6] != Py_None)))
+    OTHERWISE;
+  const bool per_row = THPVariable_Check(a[6]) && THPVariable_Unpack(a[6]).dim() == 2;
+  if (!floats_in(a[6], per_row ? 2 : 1, index, wide && !per_row, true, &gd, &gate) || gd != MOE_F32 ||
+      !(per_row ? sized(a[6], {T, 1}) : sized(a[6], {N})))
+    OTHERWISE;
+  const double scale = PyFloat_AsDouble(a[7]), eps = PyFloat_AsDouble(a[9]);
+  const long zd = PyLong_AsLong(a[10]);
+  if (PyErr_Occurred()) return nullptr;
+  void* s;
+  if (!(eps >= 1.1754944e-38 && eps <= 3e38) || !(scale >= -3.4e38 && scale <= 3.4e38) || !here(index, &s)) OTHERWISE;
+  at::Tensor h, z;
+  if (any) h = empty({T, N}, float_type(rd), index);
+  if (normed) z = empty({T, N}, float_type(zd), index);
+  PyObject* result = any && normed ? Py_BuildValue("(NN)", THPVariable_Wrap(h), THPVariable_Wrap(z)) : THPVariable_Wrap(any ? h : z);
+  if (T == 0) return result;
+  return or_raise(moe_combine_norm((int32_t)T, grouped ? (int32_t)g.k : 1, (int32_t)N, yd, y, ptr<int32_t>(g.place), w ? w->data_ptr<float>() : nullptr, shared, pd, post,
+                                   per_row, static_cast<const float*>(gate), (float)scale, rd, res, qd, pre, (float)eps, any ? h.data_ptr() : nullptr, (int32_t)zd,
+                                   normed ? z.data_ptr() : nullptr, s), result);
+  CATCH
+}
+
 // views(groups) -> (offsets, tiles, order, place) of groups whose buffer holds them
 PyObject* views(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
@@ -415,7 +555,7 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(init), FAST(groups_of), FAST(rows_of), FAST(route), FAST(quantize), FAST(dequantize), FAST(matmul), FAST(matmul_fp4),
-                         FAST(combine), FAST(views), {nullptr, nullptr, 0, nullptr}};
+                         FAST(combine), FAST(quantize8), FAST(matmul8), FAST(block_end), FAST(views), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operators", "the short way from torch tensors to the operators", -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

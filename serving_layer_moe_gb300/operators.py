@@ -27,14 +27,16 @@ from .binding import DTYPES, _check, load_library
 OPERATOR_SYMBOLS = ("moe_grouped_tiles", "moe_group_workspace", "moe_route", "moe_group_pairs", "moe_fp4_scale",
                     "moe_quantize_fp4", "moe_dequantize_fp4", "moe_grouped_matmul_workspace", "moe_grouped_matmul",
                     "moe_grouped_matmul_fp4",
-                    "moe_combine", "moe_operators_check")
+                    "moe_combine", "moe_operators_check", "moe_quantize_fp8", "moe_quantize_fp8_weights", "moe_dequantize_fp8",
+                    "moe_grouped_matmul_fp8", "moe_combine_norm")
 
 SCORING = {"softmax": 0, "sigmoid": 1}
 ACTS = {None: 0, "none": 0, "swiglu": 1}
 FP4_BLOCK = {"nvfp4": 16, "mxfp4": 32}
 _FLOATS = {torch.float32: DTYPES["f32"], torch.bfloat16: DTYPES["bf16"]}
 _MOST_PAIRS, _MOST_MATRICES, _MOST_ROWS, _MOST_K = 0x70000000, 65535, 0x7FFFFFFF, 1 << 24       # the library's limits
-_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+_F32, _BF16, _I32, _U8, _F8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn
+_MOST_WIDTH = 32768        # of a row of combine_norm
 
 _lib = None
 _host_module = None
@@ -74,6 +76,11 @@ def _operators():
             "moe_grouped_matmul_fp4": [I32, I32, I32, I32, I32, P, P, P, P, P, P, I32, P, P, I32, I32, P, P, P, P, P],
             "moe_combine": [I32, I32, I32, I32, P, P, P, I32, P, P],
             "moe_operators_check": [P],
+            "moe_quantize_fp8": [I32, I32, I32, P, I32, P, P, P, P],
+            "moe_quantize_fp8_weights": [I32, I32, I32, I32, P, P, P, P],
+            "moe_dequantize_fp8": [I32, I32, I32, I32, P, P, I32, P, P],
+            "moe_grouped_matmul_fp8": [I32, I32, I32, I32, P, P, P, P, P, I32, I32, P, P, P, P],
+            "moe_combine_norm": [I32, I32, I32, I32, P, P, P, P, I32, P, I32, P, F32, I32, P, I32, P, F32, P, I32, P, P],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -125,6 +132,11 @@ def _bad(t, name, dtypes, dim, index=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device, is on {t.device}")
     raise ValueError(f"{name} is on {t.device}, the other arguments on cuda:{index}")
+
+
+def _shaped(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, is {tuple(t.shape)}")
 
 
 def _floats(t, name, dim, index=None):
@@ -482,6 +494,257 @@ def combine(y, groups, topk_w, *, out_dtype=torch.float32, stream=None):
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
     return _again(lambda: combine(y, groups, topk_w, out_dtype=out_dtype), index, stream)
+
+
+class _Blocks8:
+    """8-bit codes and the scales of their blocks, of one device.  The tensors cannot be exchanged after."""
+
+    __slots__ = ("_codes", "_scales")
+
+    def __init__(self, codes, scales):
+        self._check(codes, scales)
+        self._codes, self._scales = codes, scales
+
+    @classmethod
+    def _of(cls, codes, scales):
+        """Of the host module's tensors."""
+        self = cls.__new__(cls)
+        self._codes, self._scales = codes, scales
+        return self
+
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    shape = property(lambda self: tuple(self._codes.shape))
+    K = property(lambda self: self._codes.shape[-1])
+    _index = property(lambda self: self._codes.get_device())
+
+
+def _aligned(**tensors):
+    for name, t in tensors.items():
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must be 16-byte aligned")
+
+
+class FP8Rows(_Blocks8):
+    """8-bit rows: codes float8_e4m3fn [R, K] and fp32 scales [ceil(K / 128), R], one for 128 elements of a row
+    (include/moe_operators.h, "8-bit blocks").  Rows in expert order are rows like others."""
+
+    __slots__ = ()
+
+    @staticmethod
+    def _check(codes, scales):
+        _typed(codes, "codes", _F8, 2)
+        _typed(scales, "scales", _F32, 2, codes.get_device())
+        R, K = codes.shape
+        _matrices(1, R, K, 16)
+        _shaped(scales, "scales", (-(-K // 128), R))
+        _aligned(codes=codes)
+
+
+class FP8Weights(_Blocks8):
+    """8-bit weights: codes float8_e4m3fn [N, K] and fp32 scales [ceil(N / 128), ceil(K / 128)], one for 128 x 128 elements, or
+    a stack of G of both (include/moe_operators.h, "8-bit blocks")."""
+
+    __slots__ = ()
+
+    @staticmethod
+    def _check(codes, scales):
+        dim = 3 if isinstance(codes, torch.Tensor) and codes.dim() == 3 else 2
+        _typed(codes, "codes", _F8, dim)
+        _typed(scales, "scales", _F32, dim, codes.get_device())
+        G, N, K = codes.shape if dim == 3 else (1, *codes.shape)
+        _matrices(G, N, K, 16)
+        _shaped(scales, "scales", (*codes.shape[:-2], -(-N // 128), -(-K // 128)))
+        _aligned(codes=codes)
+
+
+def _blocks8(q, name, kind):
+    if not isinstance(q, kind):
+        raise ValueError(f"{name} must be {kind.__name__ if isinstance(kind, type) else 'FP8Rows or FP8Weights'}, is {type(q)}")
+    kind = type(q)
+    kind._check(q._codes, q._scales)      # they may have been resized since
+    return q
+
+
+def quantize_fp8(x, *, groups=None, stream=None):
+    """Rows x [T, K] fp32 or bf16 as FP8Rows, K a multiple of 16 (moe_quantize_fp8).  With groups the result holds row
+    order[i] // k of x at grouped row i; rows that no pair fills are undefined."""
+    if stream is None:
+        r = (_host_module or _host()).quantize8(x, _described(groups))
+        if r is not None:
+            return FP8Rows._of(*r)
+    _floats(x, "x", 2)
+    index = x.get_device()
+    T, K = x.shape
+    _matrices(1, T, K, 16)
+    _aligned(x=x)
+    if groups is not None:
+        _groups_on(groups, index)
+        if groups.T != T:
+            raise ValueError(f"x has {T} rows, groups hold {groups.T} tokens")
+    else:
+        _pairs(T, 1)
+    return _again(lambda: quantize_fp8(x, groups=groups), index, stream)
+
+
+def quantize_fp8_weights(w, *, stream=None):
+    """Weights w [N, K] or [G, N, K], fp32 or bf16, as FP8Weights, K a multiple of 16 (moe_quantize_fp8_weights)."""
+    dim = 3 if isinstance(w, torch.Tensor) and w.dim() == 3 else 2
+    dt = _floats(w, "w", dim)
+    index = w.get_device()
+    G, N, K = w.shape if dim == 3 else (1, *w.shape)
+    _matrices(G, N, K, 16)
+    if -(-N // 128) * -(-K // 128) > _MOST_ROWS:
+        raise ValueError(f"a matrix may have {_MOST_ROWS} blocks at most, got {N} x {K} elements")
+    _aligned(w=w)
+    if stream is not None or index != torch.cuda.current_device():
+        return _again(lambda: quantize_fp8_weights(w), index, stream)
+    codes = torch.empty(w.shape, dtype=_F8, device=w.device)
+    scales = torch.empty(*w.shape[:-2], -(-N // 128), -(-K // 128), dtype=_F32, device=w.device)
+    _check(_operators().moe_quantize_fp8_weights(G, N, K, dt, w.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream(index)))
+    return FP8Weights._of(codes, scales)
+
+
+def dequantize_fp8(q, *, out_dtype=torch.bfloat16, stream=None):
+    """The values that q (FP8Rows or FP8Weights) stands for, in q.shape (moe_dequantize_fp8)."""
+    _blocks8(q, "q", (FP8Rows, FP8Weights))
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
+    index = q._index
+    if stream is not None or index != torch.cuda.current_device():
+        return _again(lambda: dequantize_fp8(q, out_dtype=out_dtype), index, stream)
+    out = torch.empty(q.shape, dtype=out_dtype, device=q.codes.device)
+    G, N, K = q.shape if len(q.shape) == 3 else (1, *q.shape)
+    _check(_operators().moe_dequantize_fp8(G, N, K, isinstance(q, FP8Weights), q.codes.data_ptr(), q.scales.data_ptr(), _FLOATS[out_dtype],
+                                           out.data_ptr(), _stream(index)))
+    return out
+
+
+def _product8(x, w, groups, act, quantize, out_dtype, stream):
+    if stream is None and isinstance(x, FP8Rows) and isinstance(w, FP8Weights) and act in ACTS and out_dtype in _FLOATS:
+        r = (_host_module or _host()).matmul8(x._codes, x._scales, w._codes, w._scales, _described(groups), ACTS[act], quantize, _FLOATS[out_dtype])
+        if r is not None:
+            return FP8Rows._of(*r) if isinstance(r, tuple) else r
+    _blocks8(x, "x", FP8Rows)
+    _blocks8(w, "w", FP8Weights)
+    index = w._index
+    want = 2 if groups is None else 3
+    if len(w.shape) != want:
+        raise ValueError(f"w must be {'[N, K]' if groups is None else '[E, N, K]'}, is {w.shape}")
+    E, N, K = (1, *w.shape) if groups is None else w.shape
+    P = x.shape[0]
+    if groups is not None:
+        _groups_on(groups, index)
+        if groups.E != E:
+            raise ValueError(f"w holds {E} experts, groups {groups.E}")
+        if not 1 <= E <= 4096:
+            raise ValueError(f"1 <= E <= 4096 is needed, got {E}")
+        P = groups.P
+    if x._index != index:
+        raise ValueError(f"x is on cuda:{x._index}, w on cuda:{index}")
+    if x.shape != (P, K):
+        raise ValueError(f"x must be {(P, K)}, is {x.shape}")
+    if N == 0:
+        raise ValueError(f"w must have rows, is {w.shape}")
+    _pairs(P, 1)
+    if act not in ACTS:
+        raise ValueError(f"act must be 'none' or 'swiglu', is {act!r}")
+    if ACTS[act] and N % 128:
+        raise ValueError(f"swiglu needs w rows a multiple of 128, got {N}")
+    if quantize and not ACTS[act]:
+        raise ValueError("quantize needs act='swiglu'")
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
+    return _again(lambda: _product8(x, w, groups, act, quantize, out_dtype, None), index, stream)
+
+
+def matmul_fp8(x, w, *, act="none", quantize=False, out_dtype=torch.bfloat16, stream=None):
+    """x @ w.T of FP8Rows x [R, K] and FP8Weights w [N, K], in out_dtype (moe_grouped_matmul_fp8 of one matrix).
+    act="swiglu": w holds gate rows, then up rows (N a multiple of 128), and the result has N/2 columns; quantize=True: that
+    result as FP8Rows, rounded from the fp32 values."""
+    return _product8(x, w, None, act, quantize, out_dtype, stream)
+
+
+def grouped_matmul_fp8(x, w, groups, *, act="none", quantize=False, out_dtype=torch.bfloat16, stream=None):
+    """matmul_fp8 for rows in expert order: row i of expert e is x[i] @ w[e].T, w FP8Weights [E, N, K] (moe_grouped_matmul_fp8).
+    Rows that no pair fills are undefined."""
+    if not isinstance(groups, ExpertGroups):
+        raise ValueError(f"groups must be ExpertGroups, is {type(groups)}")
+    return _product8(x, w, groups, act, quantize, out_dtype, stream)
+
+
+def _block_end(y, groups, topk_w, residual, shared, post, gate, scale, pre, eps, out_dtype, stream):
+    if stream is None and out_dtype in _FLOATS:
+        r = (_host_module or _host()).block_end(y, _described(groups), topk_w, residual, shared, post, gate, scale, pre, eps, _FLOATS[out_dtype])
+        if r is not None:
+            return r
+    _floats(residual, "residual", 2)
+    index = residual.get_device()
+    T, N = residual.shape
+    if not 1 <= N <= _MOST_WIDTH:
+        raise ValueError(f"rows of 1 to {_MOST_WIDTH} elements are taken, got {N}")
+    if y is not None:
+        _floats(y, "y", 2, index)
+        if groups is not None:
+            _groups_on(groups, index)
+            _typed(topk_w, "topk_w", _F32, 2, index)
+            _shaped(topk_w, "topk_w", (groups.T, groups.k))
+            if groups.T != T:
+                raise ValueError(f"residual has {T} rows, groups hold {groups.T} tokens")
+            if groups.k < 1:
+                raise ValueError("groups hold no experts a token")
+        _shaped(y, "y", (T if groups is None else groups.P, N))
+        _pairs(T, 1 if groups is None else groups.k)
+    else:
+        _pairs(T, 1)
+    if shared is not None:
+        _typed(shared, "shared", y.dtype, 2, index)
+        _shaped(shared, "shared", (T, N))
+    for name, t in (("post", post), ("pre", pre)):
+        if t is not None:
+            _floats(t, name, 1, index)
+            _shaped(t, name, (N,))
+    if gate is not None:
+        _typed(gate, "gate", _F32, 2 if isinstance(gate, torch.Tensor) and gate.dim() == 2 else 1, index)
+        _shaped(gate, "gate", (T, 1) if gate.dim() == 2 else (N,))
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
+    if not 1.1754944e-38 <= eps <= 3e38:
+        raise ValueError(f"eps must be a positive normal number, is {eps}")
+    if not abs(scale) <= 3.4e38:
+        raise ValueError(f"residual_scale must be finite, is {scale}")
+    if N % 8 == 0:
+        for name, t in (("y", y), ("residual", residual), ("shared", shared), ("post", post), ("pre", pre), ("gate", gate)):
+            if t is not None and (name != "gate" or t.dim() == 1) and t.data_ptr() % 16:
+                raise ValueError(f"{name} must be 16-byte aligned where rows are a multiple of 8 elements")
+    return _again(lambda: _block_end(y, groups, topk_w, residual, shared, post, gate, scale, pre, eps, out_dtype, None), index, stream)
+
+
+def combine_norm(y, groups, topk_w, residual, *, shared=None, post=None, gate=None, residual_scale=1.0, pre=None, eps=1e-6,
+                 out_dtype=torch.bfloat16, stream=None):
+    """The end of a block of experts: c = combine(y, groups, topk_w) + shared, its RMS norm with weights post, times gate;
+    h = residual_scale * residual + c, in residual's type; with the next block's norm weights pre also z = its RMS norm,
+    in out_dtype: (h, z), else h (moe_combine_norm).  y [P, N], shared [T, N] in y's type, residual [T, N], fp32 or bf16;
+    post and pre [N], fp32 or bf16; gate fp32, [N] for a value a channel or [T, 1] for one a token."""
+    if not isinstance(groups, ExpertGroups):
+        raise ValueError(f"groups must be ExpertGroups, is {type(groups)}")
+    if y is None:
+        raise ValueError("y must be a tensor, is None")
+    return _block_end(y, groups, topk_w, residual, shared, post, gate, residual_scale, pre, eps, out_dtype, stream)
+
+
+def residual_norm(y, residual, *, post=None, gate=None, residual_scale=1.0, pre=None, eps=1e-6, out_dtype=torch.bfloat16, stream=None):
+    """combine_norm for a block that is no mixture: y [T, N] holds a row for each token."""
+    if y is None:
+        raise ValueError("y must be a tensor, is None")
+    return _block_end(y, None, None, residual, None, post, gate, residual_scale, pre, eps, out_dtype, stream)
+
+
+def rms_norm(x, weight, *, eps=1e-6, out_dtype=torch.bfloat16, stream=None):
+    """x / sqrt(mean(x^2) + eps) * weight of the rows of x [T, N], in out_dtype: the norm before the first block (moe_combine_norm)."""
+    if weight is None:
+        raise ValueError("weight must be a tensor, is None")
+    return _block_end(None, None, None, x, None, None, None, 1.0, weight, eps, out_dtype, stream)
 
 
 def check_operators(stream=None):
