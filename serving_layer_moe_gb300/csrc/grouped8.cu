@@ -2,28 +2,34 @@
 //
 //   out[i, n] = sum_b sx[b, i] sw[n / 128, b] sum_{k in block b} x[i, k] w[n, k],   e4m3 x and w
 //
-// Transposed like the bf16 and 4-bit products (grouped.cu): D[feature, token], a CTA (CG = 1) or
-// a pair (CG = 2) multiplies 128 or 256 weight rows by up to 128 or 256 tokens of one expert,
-// so that ragged tiles and single tokens cost the columns they have.
-//
 // The scales are any fp32 numbers, of every 128 of K, so they cannot be left to the tensor cores
 // (whose block scales are powers of two) nor to the end.  The tensor cores sum one block of K,
 // one slice of the ring, into one of two TMEM accumulators; the epilogue's warps multiply it
-// by its scales and add it up in fp32 registers while the next slice runs.  A tile of 256 x 256
-// is 128 sums a thread, for which the other warps give up registers.  What a slice costs an SM:
-// 512 cycles of products, and beside them 256 of reading TMEM and 256 of fused multiply-adds
-// (two an instruction).
+// by its scales and add it up in fp32 registers while the next slice runs: 128 sums a thread, for
+// which the other warps give up registers.
 //
+// So D[token, feature], unlike the bf16 and 4-bit products (grouped.cu): a TMEM lane is a token, whose scale is
+// one register, and the features of a warp share theirs.  That leaves reading TMEM (32x32b loads, 256 cycles
+// a slice of 128 tokens x 256 features) and the additions (256 more, beside them), under the 512 of the
+// slice's products.  With the features as lanes the columns' scales come from shared memory: 660 cycles with
+// broadcast loads, more with 16x256b loads, which read TMEM at half the rate (709 us for 16384 rows of 8
+// experts, K 7168, N 4096; now 338, 2.85 PFLOP/s, and 301 with nothing added up).  What it costs: a ragged tile of tokens takes a
+// whole one's products.
+//
+// What an epilogue warp does once a slice counts as much: two warps a scheduler hide little of it.  Scales come for four slices at a
+// time (a barrier of their own a slice: 500 us), arrivals are elected without a branch and both accumulators' addresses and
+// phases are registers (410), the warp's number is uniform to the compiler and scales stay single registers until used (338).
+//
+// A CTA (CG = 1) takes up to 128 tokens of one expert, a pair (CG = 2) up to 256, by TILE weight rows.
 // Persistent kernel, one CTA per SM:
 //   warp 0      TMA: weight tiles, into a ring of K slices of 128 bytes a row
 //   warp 1      one lane issues tcgen05.mma kind::f8f6f4
-//   warp 2      TMA: token tiles
-//   warp 3      scales: products of the tokens' and the weights', a slice ahead, into a ring of their own
-//   warps 4-11  sums and epilogue, two warps to a quarter of the TMEM lanes
+//   warp 2      TMA: token tiles, the rows there are; the products of the rows behind them are not looked at
+//   warp 3      scales, some slices ahead, into a ring of groups of slices
+//   warps 4-11  sums and epilogue: a quarter of the lanes, half of the columns each
 //
 // SwiGLU: the weight rows of a tile alternate 16 gate rows and the 16 up rows of the same features, as in
-// grouped.cu.  A requantised result needs the largest of 128 features: both CTAs of a pair have 64 of
-// them and tell one another their maxima, by stores that count on the other's barrier.
+// grouped.cu, so a thread has both.  A requantised block is a token's 128 features: a tile's two halves, in two warps.
 //
 // Every wait is bounded; one that runs out sets the flag moe_operators_check() reads.
 #include "grouped.cuh"
@@ -40,19 +46,20 @@ __device__ uint32_t g_operator_err8;
 
 constexpr int FIRST_EPI = 4, EW = 8;
 constexpr int THREADS = 32 * (FIRST_EPI + EW);
-constexpr int A_BYTES = 128 * 128;             // 128 weight rows, 128 bytes of K each
 constexpr int MAX_STAGES = 12;
-constexpr int SCALE_SLOTS = 8, SCALE_AHEAD = 4;   // slices of scales in the ring, and loaded at a time
-// An epilogue warp's buffer, 32 tokens: rows of 32 bf16 features, or 16 (SwiGLU), with strides that reach all banks
-constexpr int EPI_WARP = 32 * 80, ROW32 = 80, ROW16 = 48;
+constexpr int ACC_COLS = 256;                  // between the accumulators
+constexpr int GROUP = 4;                       // slices whose scales go together
+constexpr int SLOT = GROUP * 128 + 4 * GROUP;  // a group's scales: [slice][token of the CTA], then [half of the columns][even, odd 16 columns][slice]
+constexpr int SCALE_SLOTS = 3;
 constexpr int SMEM_LIMIT = 227 * 1024;
-// registers a thread: launched with LAUNCH_REGS, of which the pair form's epilogue takes EPI_REGS and the four other warps keep OTHER_REGS
-constexpr int LAUNCH_REGS = 168, EPI_REGS = 216, OTHER_REGS = 72;
+// registers a thread: launched with LAUNCH_REGS, of which the epilogue takes EPI_REGS and the four other warps keep OTHER_REGS
+constexpr int LAUNCH_REGS = 168, EPI_REGS = 224, OTHER_REGS = 56;
 static_assert(EPI_REGS * 32 * EW + OTHER_REGS * 32 * FIRST_EPI <= LAUNCH_REGS * THREADS, "the shares are of the launch's registers");
 
 struct Args8 {
-  int P, E, N, K, cols, act, quant, out_f32, wide, few;
-  int m_blocks, kslices, n_blocks, stages, stage_bytes, b_rows, most_tiles;   // n_blocks: 128-row blocks of a matrix, which its scales have
+  int P, E, N, K, cols, act, quant, out_f32, few;
+  int m_blocks, kslices, n_blocks, stages, stage_bytes, box, most_tiles;   // n_blocks: 128-row blocks of a matrix; box: token rows of a load
+  int unit;                     // bytes that a row of out, and out, are multiples of: 32, 16, or less
   const float *sx, *sw;
   const int32_t* offsets;       // NULL: one matrix, all rows
   void* out;
@@ -82,63 +89,104 @@ __device__ __forceinline__ void item_at(const Args8& a, const int32_t* first, in
     else hi = mid;
   }
   o.e = lo;
-  // even shares of the expert's rows
+  // even shares of the expert's rows: they are what is loaded
   const int j = tt - first[lo], r0 = row_at(a, lo), n = max(row_at(a, lo + 1), r0) - r0, nt = first[lo + 1] - first[lo];
-  const int chunk = min(128 * CG, ((n + nt - 1) / nt + 16 * CG - 1) / (16 * CG) * (16 * CG));
+  const int chunk = min(128 * CG, (n + nt - 1) / nt);
   o.row0 = r0 + j * chunk;
   o.n = min(chunk, n - j * chunk);
 }
 
-// token columns of a tile, and the rows of them that one CTA loads
+// of an item's rows: where CTA `rank`'s start, how many it has, how many it loads
 template <int CG>
-__device__ __forceinline__ int columns(int n) { return (n + 16 * CG - 1) / (16 * CG) * (16 * CG); }
-template <int CG>
-__device__ __forceinline__ int token_rows(const Args8& a, const Item8& o) {
-  const int mine = columns<CG>(o.n) / CG;
-  return a.b_rows == 128 && mine > 48 * CG ? 128 : (mine + 16 * CG - 1) / (16 * CG) * (16 * CG);
+__device__ __forceinline__ int rows_from(const Args8& a, const Item8& o, int rank) {
+  return CG == 1 || rank == 0 ? 0 : min(o.n, (((o.n + 1) >> 1) + a.box - 1) / a.box * a.box);
 }
+template <int CG>
+__device__ __forceinline__ int rows_of(const Args8& a, const Item8& o, int rank) {
+  const int split = rows_from<CG>(a, o, 1);
+  return CG == 1 ? o.n : rank == 0 ? split : o.n - split;
+}
+__device__ __forceinline__ int rows_loaded(const Args8& a, int rows) { return (rows + a.box - 1) / a.box * a.box; }
 
-// place of column t's scale in a slot: a thread's eight of a chunk of 32 columns (2 (lane % 4), + 1 of every 8) lie together
-__device__ __forceinline__ int scale_place(int t) { return (t & ~31) + ((t >> 1) & 3) * 8 + ((t >> 3) & 3) * 2 + (t & 1); }
-
+__device__ __forceinline__ void swap(uint32_t (&v)[2]) {
+  const uint32_t t = v[0];
+  v[0] = v[1];
+  v[1] = t;
+}
+// acc += {a, b} * s, behind the wait for a and b
+__device__ __forceinline__ void add2(uint64_t& acc, uint32_t a, uint32_t b, uint64_t s) {
+  asm volatile("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n fma.rn.f32x2 %0, t, %3, %0;\n}\n" : "+l"(acc) : "r"(a), "r"(b), "l"(s));
+}
 __device__ __forceinline__ float2 unpack2(uint64_t p) {
   float2 f;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
   return f;
 }
-
-__device__ __forceinline__ uint32_t pair_bf16(uint64_t p) {
-  const float2 f = unpack2(p);
-  return pack_bf16(f.x, f.y);
+// bytes of a row, `unit` of them a store
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8], int unit) {
+  if (unit == 32) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+                 "r"(v[7]), "l"(to) : "memory");
+  } else {
+    static_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
-__device__ __forceinline__ void put(const Args8& a, size_t row, int col, bool live, float v) {
-  if (!live || col >= a.cols) return;
-  if (a.out_f32) static_cast<float*>(a.out)[row + col] = v;
-  else static_cast<__nv_bfloat16*>(a.out)[row + col] = __float2bfloat16_rn(v);
+// 16 features from column f on of a row that starts at `row`
+__device__ __forceinline__ void put16(const Args8& a, size_t row, int f, const uint64_t (&v)[8]) {
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 p = unpack2(v[i]);
+    x[2 * i] = p.x;
+    x[2 * i + 1] = p.y;
+  }
+  if (a.unit >= 16 && f + 16 <= a.cols) {
+    if (a.out_f32) {
+      uint32_t w[2][8];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i >> 3][i & 7] = __float_as_uint(x[i]);
+      float* to = static_cast<float*>(a.out) + row + f;
+      store32(to, w[0], a.unit);
+      store32(to + 8, w[1], a.unit);
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+      store32(static_cast<__nv_bfloat16*>(a.out) + row + f, w, a.unit);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (f + i >= a.cols) continue;
+    if (a.out_f32) static_cast<float*>(a.out)[row + f + i] = x[i];
+    else static_cast<__nv_bfloat16*>(a.out)[row + f + i] = __float2bfloat16_rn(x[i]);
+  }
 }
 
-template <int CG>
+template <int CG, int TILE>
 __global__ void __launch_bounds__(THREADS, 1)
-product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXall, const Args8 a) {
-  constexpr int NMAX = 128 * CG, CHUNKS = NMAX / 64;     // chunks of 32 columns that a warp has
-  constexpr int SLOT = 2 * NMAX;                         // scales of a slice: for the first and second 16 rows of every 32
+product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Args8 a) {
+  constexpr int HALF = TILE / 2, CHUNKS = HALF / 16;     // a thread's columns: half of the tile's, 16 a chunk
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   const uint32_t ring = smem_u32(smem);
+  constexpr int w_bytes = TILE / CG * 128;     // a stage: the CTA's weight rows, then its token rows
   uint8_t* tail = smem + (size_t)a.stages * a.stage_bytes;
-  uint8_t* ebuf = tail;
-  tail += EW * EPI_WARP;
   float* slots = reinterpret_cast<float*>(tail);
   tail += SCALE_SLOTS * SLOT * 4;
+  uint32_t* tops = reinterpret_cast<uint32_t*>(tail);   // [turn][half of the columns][token]
+  tail += 2 * 2 * 128 * 4;
   const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, sfull = empty + 8 * MAX_STAGES, sempty = sfull + 8 * SCALE_SLOTS,
                  tfull = sempty + 8 * SCALE_SLOTS, tempty = tfull + 16, tops_full = tempty + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 64);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* first = reinterpret_cast<int32_t*>(tmem_slot + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(full + 8 * s, 1);
@@ -152,18 +200,18 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       mbar_init(tfull + 8 * s, 1);
       mbar_init(tempty + 8 * s, EW * CG);
     }
-    for (int s = 0; s < 4; ++s) mbar_init(tops_full + 8 * s, 4);
+    for (int s = 0; s < 4; ++s) mbar_init(tops_full + 8 * s, 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 2 * NMAX);
+  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 2 * ACC_COLS);
   pdl_wait();
   pdl_trigger();
   if (warp == 2) {   // token tiles before each expert
     int run = 0;
     for (int b = 0; b < a.E; b += 32) {
       const int e = b + lane;
-      const int c = e < a.E ? (max(row_at(a, e + 1) - row_at(a, e), 0) + NMAX - 1) / NMAX : 0;
+      const int c = e < a.E ? (max(row_at(a, e + 1) - row_at(a, e), 0) + 128 * CG - 1) / (128 * CG) : 0;
       int x = c;
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, x, o);
@@ -190,23 +238,27 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   o.tt = -1;
 
   if (warp < FIRST_EPI) {
-    if constexpr (CG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
     bool ok = true;
     if (warp == 0) {
-      // ---------------- loads ----------------
+      // ---------------- weights ----------------
       int stage = 0;
       uint32_t phase = 0;
+      constexpr int boxes = (TILE / CG + 127) / 128;
       for (int it = it0; it < it1 && ok; it += step) {
         item_at<CG>(a, first, it, o);
-        const int m = o.mb * CG + (int)rank;      // 128-row weight tile (64 gate + 64 up with SwiGLU)
-        const uint32_t bytes = (uint32_t)CG * (A_BYTES + 128u * token_rows<CG>(a, o));
+        uint32_t bytes = (uint32_t)(CG * w_bytes);
+        for (int r = 0; r < CG; ++r) bytes += 128u * rows_loaded(a, rows_of<CG>(a, o, r));
         for (int ks = 0; ks < a.kslices; ++ks) {
           if (!warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
           if (elect_one()) {
             const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
             if (rank == 0) mbar_expect(full + 8 * stage, bytes);
             // rows of one expert (dimensions K, row, expert), or with SwiGLU (K, 16 rows, gate / up, block of 16, expert)
-            tma_5d<CG>(&tmW, bar, ring + stage * a.stage_bytes, ks * 128, a.act ? 0 : 128 * m, 0, a.act ? 4 * m : 0, o.e);
+            for (int b = 0; b < boxes; ++b) {
+              const int row = o.mb * TILE + rank * (TILE / CG) + 128 * b;
+              tma_5d<CG>(&tmW, bar, ring + stage * a.stage_bytes + b * 128 * 128, ks * 128, a.act ? 0 : row, 0, a.act ? row >> 5 : 0, o.e);
+            }
           }
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
@@ -228,21 +280,20 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       if (rank == 0) {
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
-        const uint64_t da = desc_sw128(ring), db = desc_sw128(ring + A_BYTES);
+        const uint64_t dw = desc_sw128(ring), dx = desc_sw128(ring + w_bytes);
+        // D fp32; e4m3 operands, both K-major; N = TILE; M = 128 CG
+        const uint32_t idesc = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(8 * CG) << 24);
         for (int it = it0; it < it1 && ok; it += step) {
-          item_at<CG>(a, first, it, o);
-          // D fp32; e4m3 operands, both K-major; N; M = 128 CG
-          const uint32_t idesc = (1u << 4) | ((uint32_t)(columns<CG>(o.n) >> 3) << 17) | ((uint32_t)(8 * CG) << 24);
           for (int ks = 0; ks < a.kslices; ++ks) {
             if (!warp_wait(tempty + 8 * acc, acc_phase ^ 1u, abort_flag) || !warp_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
             fence_after();
             if (elect_one()) {
               const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
-              const uint32_t d = tmem + (uint32_t)(acc * NMAX);
+              const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
               const int left = a.K - ks * 128;
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                if (kk * 32 < left) mma_f8<CG>(d, da + at + 2 * kk, db + at + 2 * kk, idesc, (uint32_t)kk);
+                if (kk * 32 < left) mma_f8<CG>(d, dx + at + 2 * kk, dw + at + 2 * kk, idesc, (uint32_t)kk);
               commit<CG>(empty + 8 * stage);
               commit<CG>(tfull + 8 * acc);
             }
@@ -259,15 +310,13 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       uint32_t phase = 0;
       for (int it = it0; it < it1 && ok; it += step) {
         item_at<CG>(a, first, it, o);
-        const int row0 = o.row0 + (int)rank * (columns<CG>(o.n) / CG), rows = token_rows<CG>(a, o);
+        const int row0 = o.row0 + rows_from<CG>(a, o, rank), rows = rows_of<CG>(a, o, rank);
         for (int ks = 0; ks < a.kslices; ++ks) {
           if (!warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
           if (elect_one()) {
-            const uint32_t sb = ring + stage * a.stage_bytes + A_BYTES;
+            const uint32_t sb = ring + stage * a.stage_bytes + w_bytes;
             const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
-            if (a.b_rows == 128 && rows == 128) tma_2d<CG>(&tmXall, bar, sb, ks * 128, row0);
-            else
-              for (int r = 0; r < rows; r += 16 * CG) tma_2d<CG>(&tmX, bar, sb + r * 128, ks * 128, row0 + r);
+            for (int r = 0; r < rows; r += a.box) tma_2d<CG>(&tmX, bar, sb + r * 128, ks * 128, row0 + r);
           }
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
@@ -279,106 +328,134 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       uint32_t phase = 0;
       for (int it = it0; it < it1 && ok; it += step) {
         item_at<CG>(a, first, it, o);
-        const int m = o.mb * CG + (int)rank;
-        // the weights' blocks of the first and second 16 rows of every 32: one block, or the gate rows' and the up rows'
-        const int b0 = min(a.act ? m >> 1 : m, a.n_blocks - 1), b1 = a.act ? min((a.cols + 64 * m) >> 7, a.n_blocks - 1) : b0;
-        const float *w0 = a.sw + ((size_t)o.e * a.n_blocks + b0) * a.kslices, *w1 = a.sw + ((size_t)o.e * a.n_blocks + b1) * a.kslices;
-        const float* x = a.sx + o.row0;
-        for (int k0 = 0; k0 < a.kslices && ok; k0 += SCALE_AHEAD) {
-          float v[SCALE_AHEAD][NMAX / 32], g0[SCALE_AHEAD], g1[SCALE_AHEAD];
+        const int rows = rows_of<CG>(a, o, rank);
+        // lane 8 half + 4 odd + slice: the weights' blocks of each half of the columns, one or the gate rows' and the up rows'
+        const int half = lane >> 3 & 1, odd = lane >> 2 & 1;
+        const int f = a.act ? (o.mb * 2 + half) * (HALF / 2) + odd * a.cols : (o.mb * 2 + half) * HALF;
+        const float* w = a.sw + ((size_t)o.e * a.n_blocks + min(f >> 7, a.n_blocks - 1)) * a.kslices;
+        const float* x = a.sx + o.row0 + rows_from<CG>(a, o, rank);
+        for (int k0 = 0; k0 < a.kslices && ok; k0 += GROUP) {
+          float v[GROUP][4];
 #pragma unroll
-          for (int i = 0; i < SCALE_AHEAD; ++i) {
-            const int ks = k0 + i;
-            g0[i] = ks < a.kslices ? __ldg(w0 + ks) : 0.0f;
-            g1[i] = ks < a.kslices && a.act ? __ldg(w1 + ks) : 0.0f;
+          for (int i = 0; i < GROUP; ++i)
 #pragma unroll
-            for (int c = 0; c < NMAX / 32; ++c) {
-              const int t = 32 * c + lane;
-              v[i][c] = ks < a.kslices && t < o.n ? __ldg(x + (size_t)ks * a.P + t) : 0.0f;
-            }
-          }
+            for (int c = 0; c < 4; ++c)
+              v[i][c] = k0 + i < a.kslices && 32 * c + lane < rows ? __ldg(x + (size_t)(k0 + i) * a.P + 32 * c + lane) : 0.0f;
+          const float g = lane < 4 * GROUP && k0 + (lane & 3) < a.kslices ? __ldg(w + k0 + (lane & 3)) : 0.0f;
+          ok = warp_wait_cta(sempty + 8 * slot, phase ^ 1u, abort_flag);
+          if (!ok) continue;
+          float* to = slots + slot * SLOT + lane;
 #pragma unroll
-          for (int i = 0; i < SCALE_AHEAD; ++i) {
-            if (k0 + i >= a.kslices || !ok) continue;
-            if (!warp_wait(sempty + 8 * slot, phase ^ 1u, abort_flag)) { ok = false; continue; }
-            float* to = slots + slot * SLOT + scale_place(lane);
+          for (int i = 0; i < GROUP; ++i)
 #pragma unroll
-            for (int c = 0; c < NMAX / 32; ++c) {
-              if (32 * c >= o.n) continue;
-              to[32 * c] = v[i][c] * g0[i];
-              if (a.act) to[NMAX + 32 * c] = v[i][c] * g1[i];
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(sfull + 8 * slot);
-            if (++slot == SCALE_SLOTS) { slot = 0; phase ^= 1u; }
-          }
+            for (int c = 0; c < 4; ++c)
+              if (32 * c < rows) to[128 * i + 32 * c] = v[i][c];
+          if (lane < 4 * GROUP) to[GROUP * 128] = g;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfull + 8 * slot);
+          if (++slot == SCALE_SLOTS) { slot = 0; phase ^= 1u; }
         }
       }
       if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
     }
   } else {
-    // ---------------- sums and epilogue: a TMEM lane is a weight row, a column a token ----------------
-    if constexpr (CG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
-    // quarter of the TMEM lanes; which of every two chunks of 32 columns
+    // ---------------- sums and epilogue: a TMEM lane is a token, a column a weight row ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
+    // quarter of the TMEM lanes, half of the columns
     const int q = warp & 3, part = (warp - FIRST_EPI) >> 2;
-    uint8_t* const buf = ebuf + (4 * part + q) * EPI_WARP;
-    int acc = 0, slot = 0, turn = 0;
-    uint32_t acc_phase = 0, slot_phase = 0, tops_phase = 0;
+    int slot = 0, turn = 0;
+    uint32_t slot_phase = 0, tops_phase = 0;
+    // of the accumulator of even and of odd slices: where the warp reads it, its barriers, the phase of the next use
+    uint32_t from[2], ready[2], done[2], phase[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      from[i] = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(i * ACC_COLS + HALF * part);
+      ready[i] = tfull + 8 * i;
+      done[i] = CG == 2 ? in_rank(tempty + 8 * i, 0) : tempty + 8 * i;
+    }
     for (int it = it0; it < it1; it += step) {
       item_at<CG>(a, first, it, o);
-      // Sums of the quarter's rows lane / 4 and + 8 (even and odd pairs) of its first 16 (lo) and second 16 (hi), columns
-      // 2 (lane % 4) and + 1 of every 8, two columns a pair
-      uint64_t lo[CHUNKS][8] = {}, hi[CHUNKS][8] = {};
+      const int rows = rows_of<CG>(a, o, rank);
+      const bool some = 32 * q < rows, mine = 32 * q + lane < rows;
+      uint64_t sum[CHUNKS][8] = {};   // of the thread's token: two columns a pair, 16 a chunk
       bool ok = true;
-      for (int ks = 0; ks < a.kslices; ++ks) {
-        ok = warp_wait(sfull + 8 * slot, slot_phase, abort_flag) && warp_wait(tfull + 8 * acc, acc_phase, abort_flag);
+      for (int k0 = 0; k0 < a.kslices; k0 += GROUP) {
+        ok = warp_wait_cta(sfull + 8 * slot, slot_phase, abort_flag);
         if (!ok) break;
-        fence_after();
-        const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * NMAX + 32 * part);
-        const float* sc = slots + slot * SLOT + 32 * part + 8 * (lane & 3);
+        float s0[GROUP], s1[GROUP];   // of even and odd chunks
+        if (some) {
+          const float* sc = slots + slot * SLOT;
+          const float4 w0 = *reinterpret_cast<const float4*>(sc + GROUP * 128 + 8 * part), w1 = *reinterpret_cast<const float4*>(sc + GROUP * 128 + 8 * part + 4);
+          const float u0[GROUP] = {w0.x, w0.y, w0.z, w0.w}, u1[GROUP] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          if (64 * c + 32 * part >= o.n) continue;
-          uint32_t x[16], y[16];
-          tmem_ld16x4(tbase + 64 * c, x);
-          tmem_ld16x4(tbase + (16u << 16) + 64 * c, y);
-          const ulonglong2 s0 = *reinterpret_cast<const ulonglong2*>(sc + 64 * c), s1 = *reinterpret_cast<const ulonglong2*>(sc + 64 * c + 4);
-          const uint64_t s[4] = {s0.x, s0.y, s1.x, s1.y};
-          uint64_t u[4] = {s0.x, s0.y, s1.x, s1.y};
-          if (a.act) {
-            const ulonglong2 u0 = *reinterpret_cast<const ulonglong2*>(sc + NMAX + 64 * c), u1 = *reinterpret_cast<const ulonglong2*>(sc + NMAX + 64 * c + 4);
-            u[0] = u0.x; u[1] = u0.y; u[2] = u1.x; u[3] = u1.y;
-          }
-          tmem_ld_wait(x, y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            lo[c][i] = fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), s[i >> 1], lo[c][i]);
-            hi[c][i] = fma2(pack2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), u[i >> 1], hi[c][i]);
+          for (int j = 0; j < GROUP; ++j) {
+            const float v = sc[128 * j + 32 * q + lane];
+            s0[j] = u0[j] * v;
+            s1[j] = u1[j] * v;
           }
         }
-        fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (CG == 2) mbar_arrive_cluster(in_rank(tempty + 8 * acc, 0));
-          else mbar_arrive(tempty + 8 * acc);
-          mbar_arrive(sempty + 8 * slot);
-        }
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        arrive_elected<1>(sempty + 8 * slot);
         if (++slot == SCALE_SLOTS) { slot = 0; slot_phase ^= 1u; }
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+          if (k0 + j >= a.kslices) break;
+          ok = warp_wait_cta(ready[j & 1], phase[j & 1], abort_flag);
+          if (!ok) break;
+          phase[j & 1] ^= 1u;
+          fence_after();
+          if (some) {
+            const uint64_t t0 = pack2(s0[j], s0[j]), t1 = pack2(s1[j], s1[j]);
+            uint32_t x[2][16];
+            tmem_ld32(from[j & 1], x[0]);
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+              tmem_wait();
+              if (c + 1 < CHUNKS) {
+                tmem_ld32(from[j & 1] + 16 * (c + 1), x[(c + 1) & 1]);
+              } else {   // the accumulator has been read
+                fence_before();
+                arrive_elected<CG>(done[j & 1]);
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) add2(sum[c][i], x[c & 1][2 * i], x[c & 1][2 * i + 1], c & 1 ? t1 : t0);
+            }
+          } else {
+            fence_before();
+            arrive_elected<CG>(done[j & 1]);
+          }
+        }
+        if (!ok) break;
+      }
+      if (a.kslices & 1) {   // the next item starts with the other accumulator
+        swap(from);
+        swap(ready);
+        swap(done);
+        swap(phase);
       }
       if (!ok) {
         if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
         break;
       }
-      const int m = o.mb * CG + (int)rank, tok = 2 * (lane & 3), feat = lane >> 2;
-      if (a.act) {
-        // lo: gate rows, hi: the up rows of the same 16 features
+      const int token = o.row0 + rows_from<CG>(a, o, rank) + 32 * q + lane;
+      const size_t row = (size_t)token * a.cols;
+      if (!a.act) {
+        const int f0 = o.mb * TILE + part * HALF;
+        if (mine)
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-          if (64 * c + 32 * part >= o.n) continue;
+          for (int c = 0; c < CHUNKS; ++c)
+            if (f0 + 16 * c < a.cols) put16(a, row, f0 + 16 * c, sum[c]);
+        continue;
+      }
+      // gate and up of 16 features alternate
+      const int f0 = (o.mb * 2 + part) * (HALF / 2);
+      uint32_t top = 0u;
+      if (some) {
+#pragma unroll
+        for (int c = 0; c < CHUNKS; c += 2) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 g = unpack2(lo[c][i]), u = unpack2(hi[c][i]);
+            const float2 g = unpack2(sum[c][i]), u = unpack2(sum[c + 1][i]);
             float h0, h1;
             if (a.out_f32) {
               h0 = silu(g.x) * u.x;
@@ -386,138 +463,48 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             } else {
               swiglu2(__float_as_uint(g.x), __float_as_uint(g.y), __float_as_uint(u.x), __float_as_uint(u.y), 1.0f, -1.44269504f, h0, h1);
             }
-            lo[c][i] = pack2(h0, h1);
+            sum[c][i] = pack2(h0, h1);
+            top = __vimax3_u32(top, __float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu);
           }
         }
       }
-      if constexpr (CG == 2) {
-        if (a.quant) {
-          // ---- the largest of the pair's 128 features for every token: [CTA][quarter][column], columns as scales lie in a slot ----
-          uint32_t* const top = reinterpret_cast<uint32_t*>(ebuf) + turn * (8 * NMAX);
-          uint8_t* const bytes = ebuf + 2 * 8 * NMAX * 4 + (4 * part + q) * (32 * 16);
-          const uint32_t bar = tops_full + 8 * (2 * turn + part);
+      if (!a.quant) {
+        if (mine)
 #pragma unroll
-          for (int c = 0; c < CHUNKS; ++c) {
-            if (64 * c + 32 * part >= o.n) continue;
-            uint32_t b[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = unpack2(lo[c][2 * i]), g = unpack2(lo[c][2 * i + 1]);
-              b[2 * i] = max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(g.x) & 0x7fffffffu);
-              b[2 * i + 1] = max(__float_as_uint(f.y) & 0x7fffffffu, __float_as_uint(g.y) & 0x7fffffffu);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int s = 4; s < 32; s <<= 1) b[i] = max(b[i], __shfl_xor_sync(0xffffffffu, b[i], s));
-            if (lane < 4) {
-              uint32_t* const at = top + (4 * (int)rank + q) * NMAX + 64 * c + 32 * part + 8 * lane;
-              const uint32_t v[4] = {b[0], b[1], b[2], b[3]}, w[4] = {b[4], b[5], b[6], b[7]};
-              *reinterpret_cast<uint4*>(at) = make_uint4(v[0], v[1], v[2], v[3]);
-              *reinterpret_cast<uint4*>(at + 4) = make_uint4(w[0], w[1], w[2], w[3]);
-              const uint32_t to = in_rank(smem_u32(at), rank ^ 1u), tobar = in_rank(bar, rank ^ 1u);
-              st_async16(to, tobar, v);
-              st_async16(to + 16, tobar, w);
-            }
-          }
-          __syncwarp();
-          if (lane == 0) {   // four warps arrive; the other CTA's four send 128 bytes a chunk
-            if (q == 0) mbar_expect(bar, (uint32_t)((o.n - 32 * part + 63) / 64) * 4 * 128);
-            else mbar_arrive(bar);
-          }
-          if (!warp_wait(bar, tops_phase, abort_flag)) {
-            if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
-            break;
-          }
-          // Two turns: the other CTA's warps send a turn's next maxima only after these have sent the other turn's, and so read this
-          // one's.
-          if (turn) tops_phase ^= 1u;
-          turn ^= 1;
-          const int f = m * 64 + 16 * q;
-#pragma unroll
-          for (int c = 0; c < CHUNKS; ++c) {
-            const int c0 = 64 * c + 32 * part, left = o.n - c0;
-            if (left <= 0) continue;
-            uint32_t b[8] = {};
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-              const uint4* const at = reinterpret_cast<const uint4*>(top + w * NMAX + c0 + 8 * (lane & 3));
-              const uint4 x = at[0], y = at[1];
-              b[0] = max(b[0], x.x); b[1] = max(b[1], x.y); b[2] = max(b[2], x.z); b[3] = max(b[3], x.w);
-              b[4] = max(b[4], y.x); b[5] = max(b[5], y.y); b[6] = max(b[6], y.z); b[7] = max(b[7], y.w);
-            }
-            float r[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float top_i = fmaxf(__uint_as_float(b[i]), kLeast8);   // NaN counts as kLeast8
-              asm("rcp.approx.f32 %0, %1;" : "=f"(r[i]) : "f"(top_i));
-              r[i] *= 448.0f;
-              const int t = tok + 8 * (i >> 1) + (i & 1);
-              if (rank == 0 && q == 0 && lane < 4 && t < left)
-                a.out_scales[(size_t)o.mb * a.P + o.row0 + c0 + t] = b[i] >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : top_i * (1.0f / 448.0f);
-            }
-            __syncwarp();   // the last chunk's bytes have been read
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 h = unpack2(lo[c][i]);
-              const uint32_t codes = to_e4m3x2(h.x * r[i & ~1], h.y * r[i | 1]);
-              uint8_t* const at = bytes + (tok + 8 * (i >> 1)) * 16 + feat + 8 * (i & 1);
-              at[0] = (uint8_t)codes;
-              at[16] = (uint8_t)(codes >> 8);
-            }
-            __syncwarp();
-            if (lane < left && f < a.cols)
-              *reinterpret_cast<uint4*>(a.out_codes + (size_t)(o.row0 + c0 + lane) * a.cols + f) = *reinterpret_cast<const uint4*>(bytes + lane * 16);
-          }
-          continue;
-        }
+          for (int c = 0; c < CHUNKS; c += 2)
+            if (f0 + 8 * c < a.cols) put16(a, row, f0 + 8 * c, sum[c]);
+        continue;
       }
+      // ---- the largest of the token's 128 features: this warp's 64, and those of the warp with the other half ----
+      uint32_t* const at = tops + turn * 256 + 32 * q + lane;
+      at[128 * part] = top;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tops_full + 8 * q);
+      if (!warp_wait(tops_full + 8 * q, tops_phase, abort_flag)) {
+        if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
+        break;
+      }
+      top = max(top, at[128 * (part ^ 1)]);
+      // two turns: the other warp writes this turn again only after this one has arrived for the next, and so read this
+      tops_phase ^= 1u;
+      turn ^= 1;
+      if (!mine) continue;
+      const float most = fmaxf(__uint_as_float(top), kLeast8);   // NaN counts as kLeast8
+      if (part == 0) a.out_scales[(size_t)o.mb * a.P + token] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : most * (1.0f / 448.0f);
+      float r;
+      asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(most));
+      r *= 448.0f;
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        const int c0 = 64 * c + 32 * part, left = o.n - c0;
-        if (left <= 0) continue;
-        __syncwarp();   // the last chunk's buffer has been read
-        if (a.wide && !a.act) {
-          // bf16: 32 tokens of 32 features through shared memory, transposed 8 x 8 by stmatrix, 16 bytes a lane to memory
-          const uint32_t to = smem_u32(buf) + (lane & 7) * ROW32 + (lane >> 3) * 16;
+      for (int c = 0; c < CHUNKS; c += 4) {
+        if (f0 + 8 * c >= a.cols) continue;
+        uint32_t w[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            stmatrix4_trans(to + 8 * k * ROW32, pair_bf16(lo[c][2 * k]), pair_bf16(lo[c][2 * k + 1]), pair_bf16(hi[c][2 * k]), pair_bf16(hi[c][2 * k + 1]));
-          __syncwarp();
-          const int f = m * 128 + 32 * q + (lane & 3) * 8;
-#pragma unroll
-          for (int r = lane >> 2; r < 32; r += 8)
-            if (r < left && f < a.cols)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c0 + r) * a.cols + f) =
-                  *reinterpret_cast<const uint4*>(buf + r * ROW32 + (lane & 3) * 16);
-        } else if (a.wide) {
-          // matrices: features 0-7 and 8-15 of eight tokens, then of the next eight
-          const uint32_t to = smem_u32(buf) + ((lane & 7) + 8 * (lane >> 4)) * ROW16 + (lane & 8) * 2;
-#pragma unroll
-          for (int k = 0; k < 4; k += 2)
-            stmatrix4_trans(to + 8 * k * ROW16, pair_bf16(lo[c][2 * k]), pair_bf16(lo[c][2 * k + 1]), pair_bf16(lo[c][2 * k + 2]), pair_bf16(lo[c][2 * k + 3]));
-          __syncwarp();
-          const int f = m * 64 + 16 * q + (lane & 1) * 8;
-#pragma unroll
-          for (int r = lane >> 1; r < 32; r += 16)
-            if (r < left && f < a.cols)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (size_t)(o.row0 + c0 + r) * a.cols + f) =
-                  *reinterpret_cast<const uint4*>(buf + r * ROW16 + (lane & 1) * 16);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int t = tok + 8 * (i >> 1), f = feat + 8 * (i & 1);
-            const size_t row = (size_t)(o.row0 + c0 + t) * a.cols;
-            const float2 x = unpack2(lo[c][i]), y = unpack2(hi[c][i]);
-            const int col = a.act ? m * 64 + 16 * q + f : m * 128 + 32 * q + f;
-            put(a, row, col, t < left, x.x);
-            put(a, row + a.cols, col, t + 1 < left, x.y);
-            if (!a.act) {
-              put(a, row, col + 16, t < left, y.x);
-              put(a, row + a.cols, col + 16, t + 1 < left, y.y);
-            }
-          }
+        for (int i = 0; i < 16; ++i) {
+          const float2 h = unpack2(sum[c + 2 * (i >> 3)][i & 7]);
+          const uint32_t two = to_e4m3x2(h.x * r, h.y * r);
+          w[i >> 1] = i & 1 ? w[i >> 1] | two << 16 : two;
         }
+        store32(a.out_codes + row + f0 + 8 * c, w, a.unit);
       }
     }
   }
@@ -527,7 +514,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   if constexpr (CG == 2) cluster_sync();
   if (warp == 1) {
     fence_after();
-    tmem_free<CG>(tmem, 2 * NMAX);
+    tmem_free<CG>(tmem, 2 * ACC_COLS);
   }
 }
 
@@ -536,46 +523,48 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 // ---------------------------------------------------------------------------
 struct Mem8 { const uint8_t *x, *w; };
 
-template <int CG>
+template <int CG, int TILE>
 moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
-  constexpr int NMAX = 128 * CG;
-  const auto kernel = product8_kernel<CG>;
+  const auto kernel = product8_kernel<CG, TILE>;
   const uint64_t K = a.K;
-  a.m_blocks = (int)ceil_div64(a.act ? a.cols : a.N, (a.act ? 64 : 128) * CG);
+  a.m_blocks = (int)ceil_div64(a.N, TILE);
   a.kslices = (a.K + 127) / 128;
   a.n_blocks = (a.N + 127) / 128;
-  a.wide = !a.quant && !a.out_f32 && a.cols % 8 == 0;   // rows of out start on 16 bytes
+  const uintptr_t size = a.quant ? 1 : a.out_f32 ? 4 : 2, base = reinterpret_cast<uintptr_t>(a.quant ? a.out_codes : a.out) | (uintptr_t)a.cols * size;
+  a.unit = base % 32 == 0 ? 32 : base % 16 == 0 ? 16 : 1;
   // rows of the token area: what the largest tile of P rows can need
-  a.b_rows = CG == 2 ? 128 : std::min(128, (a.P + 15) / 16 * 16);
-  a.stage_bytes = A_BYTES + a.b_rows * 128;
-  const int fixed = 1024 + EW * EPI_WARP + SCALE_SLOTS * 2 * NMAX * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 64 + 16 + 4 * (a.E + 1);
+  const int x_rows = CG == 2 ? 128 : std::min(128, (a.P + 15) / 16 * 16);
+  a.box = std::min(32, x_rows & -x_rows);
+  a.stage_bytes = (TILE / CG + x_rows) * 128;
+  // behind the last stage as much as the products read past its token rows
+  const int fixed = 1024 + std::max(SCALE_SLOTS * SLOT * 4 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 64 + 16 + 4 * (a.E + 1), (128 - x_rows) * 128);
   a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 
-  CUtensorMap tw, tx, txall;
+  CUtensorMap tw, tx;
   bool ok;
+  const cuuint32_t w_rows = (cuuint32_t)std::min(128, TILE / CG);
   if (a.act) {
     const cuuint64_t dims[5] = {K, 16, 2, (cuuint64_t)a.cols / 16, (cuuint64_t)a.E};
     const cuuint64_t strides[4] = {K, K * a.cols, K * 16, K * a.N};
-    const cuuint32_t box[5] = {128, 16, 2, 4, 1};
+    const cuuint32_t box[5] = {128, 16, 2, w_rows / 32, 1};
     ok = make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, mem.w, dims, strides, box, true);
   } else {
     const cuuint64_t dims[5] = {K, (cuuint64_t)a.N, 1, 1, (cuuint64_t)a.E};
     const cuuint64_t strides[4] = {K, K * a.N, K * a.N, K * a.N};
-    const cuuint32_t box[5] = {128, 128, 1, 1, 1};
+    const cuuint32_t box[5] = {128, w_rows, 1, 1, 1};
     ok = make_map(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, mem.w, dims, strides, box, true);
   }
   {
     const cuuint64_t dims[2] = {K, (cuuint64_t)a.P};
     const cuuint64_t strides[1] = {K};
-    const cuuint32_t box[2] = {128, 16 * CG}, all[2] = {128, 128};
-    ok = ok && make_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, mem.x, dims, strides, box, true) &&
-         make_map(&txall, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, mem.x, dims, strides, all, true);
+    const cuuint32_t box[2] = {128, (cuuint32_t)a.box};
+    ok = ok && make_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, mem.x, dims, strides, box, true);
   }
   if (!ok) return fail(MOE_ECUDA, "cuTensorMapEncodeTiled failed");
 
   // at most every token tile the rows can make, on every weight block
-  const int64_t tiles = (a.P + (int64_t)(NMAX - 1) * std::min(a.P, a.E)) / NMAX, most = tiles * a.m_blocks;
+  const int64_t tiles = (a.P + (int64_t)(128 * CG - 1) * std::min(a.P, a.E)) / (128 * CG), most = tiles * a.m_blocks;
   if (most > 0x7fffffff) return fail(MOE_EINVAL, "P = %d rows of N = %d columns are too many tiles", a.P, a.N);
   a.most_tiles = (int)tiles;
   static bool allowed[64] = {};   // the kernel's shared memory and registers, once per device
@@ -585,7 +574,7 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   if (!allowed[dev]) {
     cudaFuncAttributes attr;
     CK(cudaFuncGetAttributes(&attr, kernel));
-    if (CG == 2 && attr.numRegs < LAUNCH_REGS) return fail(MOE_ECUDA, "the kernel was built with %d registers, %d are shared out", attr.numRegs, LAUNCH_REGS);
+    if (attr.numRegs < LAUNCH_REGS) return fail(MOE_ECUDA, "the kernel was built with %d registers, %d are shared out", attr.numRegs, LAUNCH_REGS);
     CK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT));
     allowed[dev] = true;
   }
@@ -618,12 +607,12 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   }
   const int units = (int)std::min<int64_t>(most, resident);
   cfg.gridDim = dim3(units * CG);
-  CK(cudaLaunchKernelEx(&cfg, kernel, tw, tx, txall, a));
+  CK(cudaLaunchKernelEx(&cfg, kernel, tw, tx, a));
   return MOE_OK;
 }
 
-// Pairs of CTAs load half of the tokens each; single CTAs start sooner and have twice the units of work.
-bool use_pairs8(int64_t P, int64_t E) { return P >= 16 * E; }
+// Pairs of CTAs take twice the tokens with the same weight rows: from a single CTA's 128 an expert on.
+bool use_pairs8(int64_t P, int64_t E) { return P > 128 * E; }
 
 }  // namespace
 
@@ -670,6 +659,5 @@ extern "C" moe_status moe_grouped_matmul_fp8(int32_t P, int32_t E, int32_t N, in
   a.sx = x_scales; a.sw = w_scales; a.offsets = offsets; a.out = out; a.out_codes = out_codes; a.out_scales = out_scales;
   const Mem8 mem{x_codes, w_codes};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // the block of an 8-bit result is a pair's
-  return a.quant || use_pairs8(P, E) ? launch8<2>(a, mem, s) : launch8<1>(a, mem, s);
+  return use_pairs8(P, E) ? launch8<2, 256>(a, mem, s) : launch8<1, 256>(a, mem, s);
 }

@@ -230,10 +230,30 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[16], uint32_t (&b)[16
                :
                : "memory");
 }
-// 16 bytes into the shared memory of the cluster's CTA that `addr` and `bar` (in_rank) belong to; they count on its barrier
-__device__ __forceinline__ void st_async16(uint32_t addr, uint32_t bar, const uint32_t (&v)[4]) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(bar) : "memory");
+// 32 TMEM lanes x 16 columns, the calling thread's lane; there after tmem_wait(), for what is volatile behind it
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// One lane of a converged warp arrives, on a barrier of the cluster (CG = 2) or of this CTA: without a branch.
+template <int CG>
+__device__ __forceinline__ void arrive_elected(uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n @q mbarrier.arrive.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar) : "memory");
+  else
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar) : "memory");
+}
+// warp_wait on a barrier that only this CTA's threads and its asynchronous copies and products arrive on; inline up to the first test
+__device__ __forceinline__ bool warp_wait_cta(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n vote.sync.all.pred q, p, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0 || warp_wait(bar, parity, abort_flag);
 }
 // four 8 x 8 matrices of 16-bit values, transposed, to rows of 16 bytes whose addresses lanes 8 i .. hold for matrix i
 __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
