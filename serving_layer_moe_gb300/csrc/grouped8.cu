@@ -51,6 +51,15 @@ constexpr int ACC_COLS = 256;                  // between the accumulators
 constexpr int GROUP = 4;                       // slices whose scales go together
 constexpr int SLOT = GROUP * 128 + 4 * GROUP;  // a group's scales: [slice][token of the CTA], then [half of the columns][even, odd 16 columns][slice]
 constexpr int SCALE_SLOTS = 3;
+// What the epilogue has to know of the items (looking it up there, between two items, took 1500 cycles): the scales' warp, SCALE_SLOTS
+// groups ahead at most, leaves it with an item's first group.
+constexpr int HEADS = 8;
+static_assert(HEADS > SCALE_SLOTS + 1, "an item's head stays until its epilogue has read it");
+// An epilogue warp's buffer.  Single CTAs: 64 bytes of 32 tokens' rows, with a stride that reaches all banks; four lanes a row store them.
+// Pairs: two boxes of 32 rows x 128 bytes in the 128-byte swizzle, which TMA stores while the next item's products run (a ragged
+// warp's rows are stored by its lanes).
+constexpr int ROW = 64, ROW_STRIDE = 80, EPI_WARP = 32 * ROW_STRIDE, BOX = 32 * 128;
+template <int CG> constexpr int epi_warp() { return CG == 2 ? 2 * BOX : EPI_WARP; }
 constexpr int SMEM_LIMIT = 227 * 1024;
 // registers a thread: launched with LAUNCH_REGS, of which the epilogue takes EPI_REGS and the four other warps keep OTHER_REGS
 constexpr int LAUNCH_REGS = 168, EPI_REGS = 224, OTHER_REGS = 56;
@@ -59,7 +68,7 @@ static_assert(EPI_REGS * 32 * EW + OTHER_REGS * 32 * FIRST_EPI <= LAUNCH_REGS * 
 struct Args8 {
   int P, E, N, K, cols, act, quant, out_f32, few;
   int m_blocks, kslices, n_blocks, stages, stage_bytes, box, most_tiles;   // n_blocks: 128-row blocks of a matrix; box: token rows of a load
-  int unit;                     // bytes that a row of out, and out, are multiples of: 32, 16, or less
+  int whole;                    // rows of out start on 16 bytes
   const float *sx, *sw;
   const int32_t* offsets;       // NULL: one matrix, all rows
   void* out;
@@ -122,52 +131,111 @@ __device__ __forceinline__ float2 unpack2(uint64_t p) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
   return f;
 }
-// bytes of a row, `unit` of them a store
-__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8], int unit) {
-  if (unit == 32) {
-    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
-                 "r"(v[7]), "l"(to) : "memory");
+// 64 bytes of each lane's row to memory: `rows` rows of `stride` bytes from `out` on, `bytes` of each (64 or less), SIZE bytes an element
+template <int SIZE>
+__device__ __forceinline__ void put_rows(uint8_t* buf, const uint32_t (&w)[16], uint8_t* out, size_t stride, int rows, int bytes, bool whole) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();   // the last rows have been read
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(buf + lane * ROW_STRIDE + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  __syncwarp();
+  if (whole) {
+    const int at = 16 * (lane & 3);
+    uint8_t* to = out + (size_t)(lane >> 2) * stride + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (lane >> 2) + 8 * i;
+      if (r < rows && at < bytes) *reinterpret_cast<uint4*>(to + 8 * i * stride) = *reinterpret_cast<const uint4*>(buf + r * ROW_STRIDE + at);
+    }
   } else {
-    static_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    static_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    constexpr int N = ROW / SIZE;   // elements of a row here
+    const int at = SIZE * (lane % N);
+    for (int r = lane / N; r < rows; r += 32 / N) {
+      if (at >= bytes) continue;
+      if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(out + (size_t)r * stride + at) = *reinterpret_cast<const uint32_t*>(buf + r * ROW_STRIDE + at);
+      else *reinterpret_cast<uint16_t*>(out + (size_t)r * stride + at) = *reinterpret_cast<const uint16_t*>(buf + r * ROW_STRIDE + at);
+    }
   }
 }
-// 16 features from column f on of a row that starts at `row`
-__device__ __forceinline__ void put16(const Args8& a, size_t row, int f, const uint64_t (&v)[8]) {
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 p = unpack2(v[i]);
-    x[2 * i] = p.x;
-    x[2 * i + 1] = p.y;
-  }
-  if (a.unit >= 16 && f + 16 <= a.cols) {
-    if (a.out_f32) {
-      uint32_t w[2][8];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) w[i >> 3][i & 7] = __float_as_uint(x[i]);
-      float* to = static_cast<float*>(a.out) + row + f;
-      store32(to, w[0], a.unit);
-      store32(to + 8, w[1], a.unit);
-    } else {
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-      store32(static_cast<__nv_bfloat16*>(a.out) + row + f, w, a.unit);
-    }
-    return;
-  }
+// 64 bytes of a row: 16 fp32 columns, or 32 bf16 ones of two chunks
+template <int CHUNKS, int STEP>
+__device__ __forceinline__ void pack64(const uint64_t (&v)[CHUNKS][8], int c, bool f32, uint32_t (&w)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    if (f + i >= a.cols) continue;
-    if (a.out_f32) static_cast<float*>(a.out)[row + f + i] = x[i];
-    else static_cast<__nv_bfloat16*>(a.out)[row + f + i] = __float2bfloat16_rn(x[i]);
+    if (f32) {
+      const float2 p = unpack2(v[c * STEP][i >> 1]);
+      w[i] = __float_as_uint(i & 1 ? p.y : p.x);
+    } else {
+      const float2 p = unpack2(v[(c + (i >> 3)) * STEP][i & 7]);
+      w[i] = pack_bf16(p.x, p.y);
+    }
   }
+}
+// The results of a warp's 32 tokens, from `token` on: every STEP-th of CHUNKS chunks of 16 columns, from column f on
+template <int CG, int CHUNKS, int STEP, bool F32>
+__device__ __forceinline__ void put_results(const Args8& a, const CUtensorMap& map, uint8_t* buf, const uint64_t (&v)[CHUNKS][8], int token, int rows, int f) {
+  constexpr int SIZE = F32 ? 4 : 2, ONE = F32 ? 1 : 2, PIECES = CHUNKS / STEP / ONE;   // pieces of 64 bytes
+  const int lane = threadIdx.x & 31;
+  const size_t stride = (size_t)a.cols * SIZE;
+  uint8_t* const out = static_cast<uint8_t*>(a.out) + (size_t)token * stride + (size_t)f * SIZE;
+  const int bytes = (a.cols - f) * SIZE;   // of a row from column f on
+  if constexpr (CG == 2) {
+    if (a.whole) {
+#pragma unroll
+      for (int p0 = 0; p0 < PIECES; p0 += 4) {
+        if (p0 * 64 >= bytes) continue;
+        constexpr int N = PIECES < 4 ? PIECES : 4;
+        store_wait_read();   // the last boxes have been read
+        __syncwarp();
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+          uint32_t w[16];
+          pack64<CHUNKS, STEP>(v, (p0 + p) * ONE, F32, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(buf + (p >> 1) * BOX + lane * 128 + ((4 * (p & 1) + i) ^ (lane & 7)) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        if (rows == 32) {
+          fence_async_proxy();
+          __syncwarp();
+          if (elect_one()) {
+#pragma unroll
+            for (int b = 0; b < (N + 1) / 2; ++b)
+              if ((p0 + 2 * b) * 64 < bytes) tma_store_2d(&map, smem_u32(buf) + b * BOX, f + (p0 + 2 * b) * 64 / SIZE, token);
+            store_commit();
+          }
+          __syncwarp();
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int b = 0; b < (N + 1) / 2; ++b)
+            for (int r = lane >> 3; r < rows; r += 4) {
+              const int at = (p0 + 2 * b) * 64 + 16 * (lane & 7);
+              if (at < bytes && (lane & 7) < 4 * (N - 2 * b))
+                *reinterpret_cast<uint4*>(out + (size_t)r * stride + at) = *reinterpret_cast<const uint4*>(buf + b * BOX + r * 128 + ((lane ^ r) & 7) * 16);
+            }
+        }
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    if (p * 64 >= bytes) continue;
+    uint32_t w[16];
+    pack64<CHUNKS, STEP>(v, p * ONE, F32, w);
+    put_rows<SIZE>(buf, w, out + 64 * p, stride, rows, min(64, bytes - 64 * p), a.whole);
+  }
+}
+template <int CG, int CHUNKS, int STEP>
+__device__ __forceinline__ void put_results(const Args8& a, const CUtensorMap& map, uint8_t* buf, const uint64_t (&v)[CHUNKS][8], int token, int rows, int f) {
+  if (a.out_f32) put_results<CG, CHUNKS, STEP, true>(a, map, buf, v, token, rows, f);
+  else put_results<CG, CHUNKS, STEP, false>(a, map, buf, v, token, rows, f);
 }
 
 template <int CG, int TILE>
 __global__ void __launch_bounds__(THREADS, 1)
-product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Args8 a) {
+product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmO, const Args8 a) {
   constexpr int HALF = TILE / 2, CHUNKS = HALF / 16;     // a thread's columns: half of the tile's, 16 a chunk
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -175,8 +243,12 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   const uint32_t ring = smem_u32(smem);
   constexpr int w_bytes = TILE / CG * 128;     // a stage: the CTA's weight rows, then its token rows
   uint8_t* tail = smem + (size_t)a.stages * a.stage_bytes;
+  uint8_t* ebuf = tail;
+  tail += EW * epi_warp<CG>();
   float* slots = reinterpret_cast<float*>(tail);
   tail += SCALE_SLOTS * SLOT * 4;
+  int4* heads = reinterpret_cast<int4*>(tail);          // an item's first token and number of tokens in this CTA, and its weight block
+  tail += HEADS * 16;
   uint32_t* tops = reinterpret_cast<uint32_t*>(tail);   // [turn][half of the columns][token]
   tail += 2 * 2 * 128 * 4;
   const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, sfull = empty + 8 * MAX_STAGES, sempty = sfull + 8 * SCALE_SLOTS,
@@ -324,9 +396,9 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
     } else {
       // ---------------- scales ----------------
-      int slot = 0;
+      int slot = 0, head = 0;
       uint32_t phase = 0;
-      for (int it = it0; it < it1 && ok; it += step) {
+      for (int it = it0; it < it1 && ok; it += step, head = (head + 1) % HEADS) {
         item_at<CG>(a, first, it, o);
         const int rows = rows_of<CG>(a, o, rank);
         // lane 8 half + 4 odd + slice: the weights' blocks of each half of the columns, one or the gate rows' and the up rows'
@@ -351,6 +423,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
             for (int c = 0; c < 4; ++c)
               if (32 * c < rows) to[128 * i + 32 * c] = v[i][c];
           if (lane < 4 * GROUP) to[GROUP * 128] = g;
+          if (k0 == 0 && lane == 0) heads[head] = make_int4(o.row0 + rows_from<CG>(a, o, rank), rows, o.mb, 0);
           __syncwarp();
           if (lane == 0) mbar_arrive(sfull + 8 * slot);
           if (++slot == SCALE_SLOTS) { slot = 0; phase ^= 1u; }
@@ -363,7 +436,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     // quarter of the TMEM lanes, half of the columns
     const int q = warp & 3, part = (warp - FIRST_EPI) >> 2;
-    int slot = 0, turn = 0;
+    int slot = 0, turn = 0, head = 0;
     uint32_t slot_phase = 0, tops_phase = 0;
     // of the accumulator of even and of odd slices: where the warp reads it, its barriers, the phase of the next use
     uint32_t from[2], ready[2], done[2], phase[2] = {0u, 0u};
@@ -373,18 +446,17 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       ready[i] = tfull + 8 * i;
       done[i] = CG == 2 ? in_rank(tempty + 8 * i, 0) : tempty + 8 * i;
     }
-    for (int it = it0; it < it1; it += step) {
-      item_at<CG>(a, first, it, o);
-      const int rows = rows_of<CG>(a, o, rank);
-      const bool some = 32 * q < rows, mine = 32 * q + lane < rows;
+    uint8_t* const buf = ebuf + (4 * part + q) * epi_warp<CG>();
+    for (int it = it0; it < it1; it += step, head = (head + 1) % HEADS) {
       uint64_t sum[CHUNKS][8] = {};   // of the thread's token: two columns a pair, 16 a chunk
-      bool ok = true;
+      bool ok = true, some = false;   // some: tokens of this warp's
       for (int k0 = 0; k0 < a.kslices; k0 += GROUP) {
         ok = warp_wait_cta(sfull + 8 * slot, slot_phase, abort_flag);
         if (!ok) break;
+        const float* sc = slots + slot * SLOT;
+        if (k0 == 0) some = 32 * q < heads[head].y;
         float s0[GROUP], s1[GROUP];   // of even and odd chunks
         if (some) {
-          const float* sc = slots + slot * SLOT;
           const float4 w0 = *reinterpret_cast<const float4*>(sc + GROUP * 128 + 8 * part), w1 = *reinterpret_cast<const float4*>(sc + GROUP * 128 + 8 * part + 4);
           const float u0[GROUP] = {w0.x, w0.y, w0.z, w0.w}, u1[GROUP] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
@@ -437,18 +509,14 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
         break;
       }
-      const int token = o.row0 + rows_from<CG>(a, o, rank) + 32 * q + lane;
-      const size_t row = (size_t)token * a.cols;
+      const int4 o = heads[head];
+      const int token = o.x + 32 * q, rows = min(32, o.y - 32 * q);   // the warp's
       if (!a.act) {
-        const int f0 = o.mb * TILE + part * HALF;
-        if (mine)
-#pragma unroll
-          for (int c = 0; c < CHUNKS; ++c)
-            if (f0 + 16 * c < a.cols) put16(a, row, f0 + 16 * c, sum[c]);
+        if (some) put_results<CG, CHUNKS, 1>(a, tmO, buf, sum, token, rows, o.z * TILE + part * HALF);
         continue;
       }
       // gate and up of 16 features alternate
-      const int f0 = (o.mb * 2 + part) * (HALF / 2);
+      const int f0 = (o.z * 2 + part) * (HALF / 2);
       uint32_t top = 0u;
       if (some) {
 #pragma unroll
@@ -469,44 +537,40 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         }
       }
       if (!a.quant) {
-        if (mine)
-#pragma unroll
-          for (int c = 0; c < CHUNKS; c += 2)
-            if (f0 + 8 * c < a.cols) put16(a, row, f0 + 8 * c, sum[c]);
+        if (some) put_results<CG, CHUNKS, 2>(a, tmO, buf, sum, token, rows, f0);
         continue;
       }
-      // ---- the largest of the token's 128 features: this warp's 64, and those of the warp with the other half ----
-      uint32_t* const at = tops + turn * 256 + 32 * q + lane;
-      at[128 * part] = top;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tops_full + 8 * q);
-      if (!warp_wait(tops_full + 8 * q, tops_phase, abort_flag)) {
-        if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
-        break;
-      }
-      top = max(top, at[128 * (part ^ 1)]);
-      // two turns: the other warp writes this turn again only after this one has arrived for the next, and so read this
-      tops_phase ^= 1u;
-      turn ^= 1;
-      if (!mine) continue;
-      const float most = fmaxf(__uint_as_float(top), kLeast8);   // NaN counts as kLeast8
-      if (part == 0) a.out_scales[(size_t)o.mb * a.P + token] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : most * (1.0f / 448.0f);
-      float r;
-      asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(most));
-      r *= 448.0f;
+      if constexpr (TILE == 256) {
+        // ---- the largest of the token's 128 features: this warp's 64, and those of the warp with the other half ----
+        uint32_t* const at = tops + turn * 256 + 32 * q + lane;
+        at[128 * part] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tops_full + 8 * q);
+        if (!warp_wait_cta(tops_full + 8 * q, tops_phase, abort_flag)) {
+          if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
+          break;
+        }
+        top = max(top, at[128 * (part ^ 1)]);
+        // two turns: the other warp writes this turn again only after this one has arrived for the next, and so read this
+        tops_phase ^= 1u;
+        turn ^= 1;
+        if (!some || f0 >= a.cols) continue;
+        const float most = fmaxf(__uint_as_float(top), kLeast8);   // NaN counts as kLeast8
+        if (part == 0 && lane < rows) a.out_scales[(size_t)o.z * a.P + token + lane] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : most * (1.0f / 448.0f);
+        float r;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(most));
+        r *= 448.0f;
+        uint32_t w[16];
 #pragma unroll
-      for (int c = 0; c < CHUNKS; c += 4) {
-        if (f0 + 8 * c >= a.cols) continue;
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 h = unpack2(sum[c + 2 * (i >> 3)][i & 7]);
+        for (int i = 0; i < 32; ++i) {
+          const float2 h = unpack2(sum[2 * (i >> 3)][i & 7]);
           const uint32_t two = to_e4m3x2(h.x * r, h.y * r);
           w[i >> 1] = i & 1 ? w[i >> 1] | two << 16 : two;
         }
-        store32(a.out_codes + row + f0 + 8 * c, w, a.unit);
+        put_rows<2>(buf, w, a.out_codes + (size_t)token * a.cols + f0, a.cols, rows, ROW, true);
       }
     }
+    if (CG == 2) store_wait();
   }
   __syncwarp();
   fence_before();
@@ -530,18 +594,17 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   a.m_blocks = (int)ceil_div64(a.N, TILE);
   a.kslices = (a.K + 127) / 128;
   a.n_blocks = (a.N + 127) / 128;
-  const uintptr_t size = a.quant ? 1 : a.out_f32 ? 4 : 2, base = reinterpret_cast<uintptr_t>(a.quant ? a.out_codes : a.out) | (uintptr_t)a.cols * size;
-  a.unit = base % 32 == 0 ? 32 : base % 16 == 0 ? 16 : 1;
+  a.whole = a.cols * (a.out_f32 ? 4 : 2) % 16 == 0;
   // rows of the token area: what the largest tile of P rows can need
   const int x_rows = CG == 2 ? 128 : std::min(128, (a.P + 15) / 16 * 16);
   a.box = std::min(32, x_rows & -x_rows);
   a.stage_bytes = (TILE / CG + x_rows) * 128;
   // behind the last stage as much as the products read past its token rows
-  const int fixed = 1024 + std::max(SCALE_SLOTS * SLOT * 4 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 64 + 16 + 4 * (a.E + 1), (128 - x_rows) * 128);
+  const int fixed = 1024 + std::max(EW * epi_warp<CG>() + SCALE_SLOTS * SLOT * 4 + HEADS * 16 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 64 + 16 + 4 * (a.E + 1), (128 - x_rows) * 128);
   a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 
-  CUtensorMap tw, tx;
+  CUtensorMap tw, tx, to;
   bool ok;
   const cuuint32_t w_rows = (cuuint32_t)std::min(128, TILE / CG);
   if (a.act) {
@@ -560,6 +623,13 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
     const cuuint64_t strides[1] = {K};
     const cuuint32_t box[2] = {128, (cuuint32_t)a.box};
     ok = ok && make_map(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, mem.x, dims, strides, box, true);
+  }
+  to = tx;
+  if (CG == 2 && !a.quant && a.whole) {
+    const int size = a.out_f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.cols, (cuuint64_t)a.P}, strides[1] = {(cuuint64_t)a.cols * size};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32};
+    ok = ok && make_map(&to, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims, strides, box, true);
   }
   if (!ok) return fail(MOE_ECUDA, "cuTensorMapEncodeTiled failed");
 
@@ -607,7 +677,7 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   }
   const int units = (int)std::min<int64_t>(most, resident);
   cfg.gridDim = dim3(units * CG);
-  CK(cudaLaunchKernelEx(&cfg, kernel, tw, tx, a));
+  CK(cudaLaunchKernelEx(&cfg, kernel, tw, tx, to, a));
   return MOE_OK;
 }
 
