@@ -16,7 +16,6 @@ namespace moe {
 
 namespace {
 
-constexpr int MAX_THREADS = 1024;
 constexpr int MAX_WIDTH = 32768;
 
 struct EndArgs {
@@ -30,26 +29,46 @@ struct EndArgs {
   void *h, *z;                                      // either may be NULL
 };
 
-// U consecutive values as fp32
+// U consecutive values (8, 16-byte aligned, or 1) as they are, so that many can be on their way, and as fp32
 template <int U, typename X>
-__device__ __forceinline__ void load(const X* p, float (&v)[U]) {
-  if constexpr (U == 1) {
-    v[0] = (float)*p;
-  } else if constexpr (sizeof(X) == 2) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+struct Raw {
+  static constexpr int Q = U * (int)sizeof(X) / 16;
+  uint4 q[Q];
+  __device__ __forceinline__ void load(const X* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  } else {
+    for (int i = 0; i < Q; ++i) q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void read(const X* p) {   // from shared memory
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
-      v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+    for (int i = 0; i < Q; ++i) q[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void values(float (&v)[U]) const {
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      const uint32_t u[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if constexpr (sizeof(X) == 2) {
+          v[8 * i + 2 * h] = __uint_as_float(u[h] << 16);
+          v[8 * i + 2 * h + 1] = __uint_as_float(u[h] & 0xffff0000u);
+        } else {
+          v[4 * i + h] = __uint_as_float(u[h]);
+        }
+      }
     }
   }
+};
+template <typename X>
+struct Raw<1, X> {
+  X x;
+  __device__ __forceinline__ void load(const X* p) { x = *p; }
+  __device__ __forceinline__ void values(float (&v)[1]) const { v[0] = (float)x; }
+};
+template <int U, typename X>
+__device__ __forceinline__ void load(const X* p, float (&v)[U]) {
+  Raw<U, X> r;
+  r.load(p);
+  r.values(v);
 }
 // of a norm's weights, in either type
 template <int U>
@@ -89,9 +108,9 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
-// V units of U values a thread, unit threadIdx.x first and then every blockDim.x-th
-template <typename Y, typename R, int U, int V>
-__global__ void __launch_bounds__(MAX_THREADS) block_end_kernel(EndArgs a) {
+// V units of U values a thread, unit threadIdx.x first and then every blockDim.x-th; J rows of y on their way at a time
+template <typename Y, typename R, int U, int V, int J, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) block_end_kernel(EndArgs a) {
   __shared__ float parts[2][32];
   pdl_wait();
   pdl_trigger();
@@ -100,124 +119,306 @@ __global__ void __launch_bounds__(MAX_THREADS) block_end_kernel(EndArgs a) {
   const R* residual = static_cast<const R*>(a.residual);
   const float per = 1.0f / (float)a.N;
   for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    float c[V][U] = {}, r[V][U];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int u = threadIdx.x + v * blockDim.x;
-      if (u < units) load(residual + (size_t)t * a.N + u * U, r[v]);
-    }
-    if (y) {
-      const int P = a.place ? a.T * a.k : a.T;
-      for (int j = 0; j < (a.place ? a.k : 1); ++j) {
-        const int row = a.place ? __ldg(a.place + (size_t)t * a.k + j) : t;
-        if ((unsigned)row >= (unsigned)P) continue;
-        const float w = a.place ? __ldg(a.w + (size_t)t * a.k + j) : 1.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int u = threadIdx.x + v * blockDim.x;
-          if (u >= units) continue;
-          float x[U];
-          load(y + (size_t)row * a.N + u * U, x);
-#pragma unroll
-          for (int i = 0; i < U; ++i) c[v][i] = fmaf(w, x[i], c[v][i]);
-        }
-      }
-      if (shared) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int u = threadIdx.x + v * blockDim.x;
-          if (u >= units) continue;
-          float x[U];
-          load(shared + (size_t)t * a.N + u * U, x);
-#pragma unroll
-          for (int i = 0; i < U; ++i) c[v][i] += x[i];
-        }
-      }
-      if (a.post) {
-        float s = 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int i = 0; i < U; ++i) s = fmaf(c[v][i], c[v][i], s);
-        const float inv = rsqrtf(fmaf(block_sum(s, parts[0]), per, a.eps));
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int u = threadIdx.x + v * blockDim.x;
-          if (u >= units) continue;
-          float x[U];
-          load_any(a.post, a.post_bf16, (size_t)u * U, x);
-#pragma unroll
-          for (int i = 0; i < U; ++i) c[v][i] *= inv * x[i];
-        }
-      }
-      if (a.gate) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int u = threadIdx.x + v * blockDim.x;
-          if (u >= units) continue;
-          float x[U];
-          if (a.gate_rows) {
-            const float g = __ldg(a.gate + t);
-#pragma unroll
-            for (int i = 0; i < U; ++i) x[i] = g;
-          } else {
-            load(a.gate + (size_t)u * U, x);
-          }
-#pragma unroll
-          for (int i = 0; i < U; ++i) c[v][i] *= x[i];
-        }
-      }
-    }
-    float s = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int u = threadIdx.x + v * blockDim.x;
-      if (u >= units) continue;
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        c[v][i] = fmaf(a.alpha, r[v][i], c[v][i]);
-        s = fmaf(c[v][i], c[v][i], s);
-      }
-      if (a.h) store(static_cast<R*>(a.h) + (size_t)t * a.N + u * U, c[v]);
-    }
-    if (a.z) {
-      const float inv = rsqrtf(fmaf(block_sum(s, parts[1]), per, a.eps));
+    float c[V][U] = {};
+    Raw<U, R> r[V];
+    auto each = [&](auto f) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int u = threadIdx.x + v * blockDim.x;
-        if (u >= units) continue;
+        if (u < units) f(v, (size_t)u * U);
+      }
+    };
+    if (y) {
+      const int k = a.place ? a.k : 1, P = a.T * k;
+      for (int j0 = 0; j0 < k; j0 += J) {
+        int row[J];
+        float w[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const bool there = j0 + j < k;
+          row[j] = !there ? -1 : a.place ? __ldg(a.place + (size_t)t * k + j0 + j) : t;
+          w[j] = there && a.place ? __ldg(a.w + (size_t)t * k + j0 + j) : 1.0f;
+        }
+        each([&](int v, size_t at) {
+          Raw<U, Y> x[J];
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+            if ((unsigned)row[j] < (unsigned)P) x[j].load(y + (size_t)row[j] * a.N + at);
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            if ((unsigned)row[j] >= (unsigned)P) continue;
+            float f[U];
+            x[j].values(f);
+#pragma unroll
+            for (int i = 0; i < U; ++i) c[v][i] = fmaf(w[j], f[i], c[v][i]);
+          }
+        });
+      }
+      if (shared)
+        each([&](int v, size_t at) {
+          float x[U];
+          load(shared + (size_t)t * a.N + at, x);
+#pragma unroll
+          for (int i = 0; i < U; ++i) c[v][i] += x[i];
+        });
+    }
+    each([&](int v, size_t at) { r[v].load(residual + (size_t)t * a.N + at); });   // on its way during the first mean
+    if (a.post) {
+      float s = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < U; ++i) s = fmaf(c[v][i], c[v][i], s);
+      const float inv = rsqrtf(fmaf(block_sum(s, parts[0]), per, a.eps));
+      each([&](int v, size_t at) {
         float x[U];
-        load_any(a.pre, a.pre_bf16, (size_t)u * U, x);
+        load_any(a.post, a.post_bf16, at, x);
+#pragma unroll
+        for (int i = 0; i < U; ++i) c[v][i] *= inv * x[i];
+      });
+    }
+    if (a.gate) {
+      const float g = a.gate_rows ? __ldg(a.gate + t) : 1.0f;
+      each([&](int v, size_t at) {
+        float x[U];
+        if (!a.gate_rows) load(a.gate + at, x);
+#pragma unroll
+        for (int i = 0; i < U; ++i) c[v][i] *= a.gate_rows ? g : x[i];
+      });
+    }
+    float s = 0.0f;
+    each([&](int v, size_t at) {
+      float x[U];
+      r[v].values(x);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        c[v][i] = fmaf(a.alpha, x[i], c[v][i]);
+        s = fmaf(c[v][i], c[v][i], s);
+      }
+      if (a.h) store(static_cast<R*>(a.h) + (size_t)t * a.N + at, c[v]);
+    });
+    if (a.z) {
+      const float inv = rsqrtf(fmaf(block_sum(s, parts[1]), per, a.eps));
+      each([&](int v, size_t at) {
+        float x[U];
+        load_any(a.pre, a.pre_bf16, at, x);
 #pragma unroll
         for (int i = 0; i < U; ++i) x[i] *= inv * c[v][i];
-        const size_t at = (size_t)t * a.N + u * U;
+        at += (size_t)t * a.N;
         if (a.z_bf16) store(static_cast<__nv_bfloat16*>(a.z) + at, x);
         else store(static_cast<float*>(a.z) + at, x);
-      }
+      });
     }
     __syncthreads();   // the parts have been read
   }
 }
 
-template <typename Y, typename R, int U, int V>
-moe_status launch_end(const EndArgs& a, int threads, cudaStream_t s) {
-  const int grid = (int)std::min<int64_t>(a.T, (int64_t)operator_sms() * std::max(1, 2048 / threads));
-  CK(launch_pdl(block_end_kernel<Y, R, U, V>, dim3(grid), dim3(threads), 0, s, a));
+// ---------------------------------------------------------------------------
+// The same for many tokens: rows come ahead, in a ring of D of them in shared memory, so that loads never wait for a mean.
+// A thread copies what it will read itself (cp.async), so nothing is waited for but its own copies.  A token's rows are
+// its pairs', the shared one, the residual; the norms' weights stay in registers.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) { asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory"); }
+
+// D steps of two rows in the ring.  us of 4096 tokens, N 7168, 8 rows each and all parts (bound 104 bf16, 201 fp32): one row a step 154
+// and 204; two rows, the norms' weights in registers and one block an SM 138 and 202; weights read for each token (KEEP
+// false), registers for two blocks an SM 129 and 237.  Without the ring, bf16: 147 to 203.
+template <typename Y, typename R, int V, int D, bool KEEP, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) block_stream_kernel(EndArgs a) {
+  constexpr int U = 8;
+  extern __shared__ uint4 ring[];
+  __shared__ float parts[2][32];
+  pdl_wait();
+  pdl_trigger();
+  // A unit's place is the same whatever the row's type: it stays the thread's own.
+  constexpr int WIDE = sizeof(Y) > sizeof(R) ? sizeof(Y) : sizeof(R);
+  const int units = a.N / U, lane = threadIdx.x & 31;
+  const int k = a.y ? a.place ? a.k : 1 : 0, sums = k + (a.shared ? 1 : 0), steps = sums / 2 + 1, last = 2 * steps - 1, P = a.T * max(k, 1);
+  const uint32_t row_bytes = (uint32_t)(a.N * WIDE), base = (uint32_t)__cvta_generic_to_shared(ring);
+  const float per = 1.0f / (float)a.N;
+  float post[KEEP ? V : 1][U], pre[KEEP ? V : 1][U], gate[KEEP ? V : 1][U];
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int u = threadIdx.x + v * blockDim.x;
+      if (u < units) f(v, u * U);
+    }
+  };
+  auto load_post = [&](int at, float (&x)[U]) { load_any(a.post, a.post_bf16, (size_t)at, x); };
+  auto load_pre = [&](int at, float (&x)[U]) { load_any(a.pre, a.pre_bf16, (size_t)at, x); };
+  auto load_gate = [&](int at, float (&x)[U]) {
+    if (a.gate && !a.gate_rows) load(a.gate + at, x);
+  };
+  if (KEEP)
+    each([&](int v, int at) {
+      if (a.post) load_post(at, post[v]);
+      if (a.z) load_pre(at, pre[v]);
+      load_gate(at, gate[v]);
+    });
+  // Lane j has row j of a token: its pairs', the shared one, and the residual as the last of the last step.  row_of: the pair's row, as
+  // it is loaded; address: where the row is, 0 where there is none.
+  auto row_of = [&](int t) { return t >= a.T || lane >= k ? -1 : a.place ? __ldg(a.place + (size_t)t * k + lane) : t; };
+  auto address = [&](int t, int row) {
+    return t >= a.T ? 0ull
+           : lane < k ? (unsigned)row < (unsigned)P ? (unsigned long long)(static_cast<const Y*>(a.y) + (size_t)row * a.N) : 0ull
+           : lane < sums ? (unsigned long long)(static_cast<const Y*>(a.shared) + (size_t)t * a.N)
+           : lane == last ? (unsigned long long)(static_cast<const R*>(a.residual) + (size_t)t * a.N) : 0ull;
+  };
+
+  int pt = blockIdx.x, ps = 0, p_slot = 0;   // the next step to copy
+  int p_row = row_of(pt + gridDim.x);
+  unsigned long long p_at = address(pt, row_of(pt));
+  auto copy = [&]() {
+    if (pt < a.T) {
+      const uint32_t to = base + (uint32_t)p_slot * (2 * row_bytes);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const char* from = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, p_at, 2 * ps + h));
+        if (!from) continue;
+        each([&](int, int at) {
+          const int size = h == 1 && sizeof(Y) != sizeof(R) && ps == steps - 1 ? sizeof(R) : sizeof(Y), bytes = sizeof(Y) == sizeof(R) ? (int)sizeof(Y) : size;
+#pragma unroll
+          for (int i = 0; i < WIDE / 2; ++i)
+            if (i < bytes / 2) copy16(to + h * row_bytes + at * WIDE + 16 * i, from + at * bytes + 16 * i);
+        });
+      }
+      if (++ps == steps) {
+        ps = 0;
+        pt += gridDim.x;
+        p_at = address(pt, p_row);
+        p_row = row_of(pt + gridDim.x);
+      }
+      if (++p_slot == D) p_slot = 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < D - 1; ++i) copy();
+
+  int slot = 0, row = row_of(blockIdx.x);
+  auto weight_of = [&](int t) { return t < a.T && lane < k && a.place ? __ldg(a.w + (size_t)t * k + lane) : 1.0f; };
+  float weight = weight_of(blockIdx.x);
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const unsigned there = __ballot_sync(0xffffffffu, lane < k ? (unsigned)row < (unsigned)P : lane < sums);
+    const int next_row = row_of(t + gridDim.x);
+    const float next_weight = weight_of(t + gridDim.x), token_gate = a.gate && a.gate_rows ? __ldg(a.gate + t) : 1.0f;
+    float c[V][U] = {};
+    const uint8_t* from;
+    auto add = [&](int j, const uint8_t* src) {
+      const float w = __shfl_sync(0xffffffffu, weight, j);
+      if (there >> j & 1)
+        each([&](int v, int at) {
+          Raw<U, Y> x;
+          x.read(reinterpret_cast<const Y*>(src + at * WIDE));
+          float f[U];
+          x.values(f);
+#pragma unroll
+          for (int i = 0; i < U; ++i) c[v][i] = fmaf(w, f[i], c[v][i]);
+        });
+    };
+    for (int j = 0; j < steps; ++j) {
+      copy();   // into the slot that was read last
+      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      from = reinterpret_cast<const uint8_t*>(ring) + (size_t)slot * (2 * row_bytes);
+      if (++slot == D) slot = 0;
+      add(2 * j, from);
+      if (j < steps - 1) add(2 * j + 1, from + row_bytes);
+    }
+    float s = 0.0f;
+    if (a.post) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < U; ++i) s = fmaf(c[v][i], c[v][i], s);
+      const float inv = rsqrtf(fmaf(block_sum(s, parts[0]), per, a.eps));
+      each([&](int v, int at) {
+        const int w = KEEP ? v : 0;
+        if (!KEEP) load_post(at, post[w]);
+#pragma unroll
+        for (int i = 0; i < U; ++i) c[v][i] *= inv * post[w][i];
+      });
+    }
+    s = 0.0f;
+    each([&](int v, int at) {
+      Raw<U, R> r;
+      r.read(reinterpret_cast<const R*>(from + row_bytes + at * WIDE));
+      float x[U];
+      r.values(x);
+      const int w = KEEP ? v : 0;
+      if (!KEEP) load_gate(at, gate[w]);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (a.gate) c[v][i] *= a.gate_rows ? token_gate : gate[w][i];
+        c[v][i] = fmaf(a.alpha, x[i], c[v][i]);
+        s = fmaf(c[v][i], c[v][i], s);
+      }
+      if (a.h) store(static_cast<R*>(a.h) + (size_t)t * a.N + at, c[v]);
+    });
+    if (a.z) {
+      const float inv = rsqrtf(fmaf(block_sum(s, parts[1]), per, a.eps));
+      each([&](int v, int at) {
+        float x[U];
+        const int w = KEEP ? v : 0;
+        if (!KEEP) load_pre(at, pre[w]);
+#pragma unroll
+        for (int i = 0; i < U; ++i) x[i] = inv * c[v][i] * pre[w][i];
+        if (a.z_bf16) store(static_cast<__nv_bfloat16*>(a.z) + (size_t)t * a.N + at, x);
+        else store(static_cast<float*>(a.z) + (size_t)t * a.N + at, x);
+      });
+    }
+    if (!(a.post && a.z)) __syncthreads();   // the parts have been read: with two means a token, the other one's barrier says so
+    row = next_row;
+    weight = next_weight;
+  }
+}
+
+template <typename Y, typename R, int V, int D, bool KEEP, int THREADS, int BLOCKS>
+moe_status launch_stream(const EndArgs& a, int threads, cudaStream_t s) {
+  const auto kernel = block_stream_kernel<Y, R, V, D, KEEP, THREADS, BLOCKS>;
+  const size_t smem = (size_t)D * 2 * a.N * std::max(sizeof(Y), sizeof(R));
+  static bool allowed[64] = {};
+  int dev = 0;
+  CK(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(MOE_EINVAL, "device %d is out of range", dev);
+  if (!allowed[dev]) {
+    CK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024));
+    allowed[dev] = true;
+  }
+  int blocks = 1;
+  CK(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem));
+  const int grid = (int)std::min<int64_t>(a.T, (int64_t)operator_sms() * std::max(1, blocks));
+  CK(launch_pdl(kernel, dim3(grid), dim3(threads), smem, s, a));
   return MOE_OK;
 }
 
-// Units a thread: as few as reach the row with 1024 threads, and more, down to 256 threads, when there are tokens for every SM.
+template <typename Y, typename R, int U, int V, int J, int THREADS, int BLOCKS>
+moe_status launch_end(const EndArgs& a, int threads, cudaStream_t s) {
+  const int grid = (int)std::min<int64_t>(a.T, (int64_t)operator_sms() * std::max(1, 2048 / threads));
+  CK(launch_pdl(block_end_kernel<Y, R, U, V, J, THREADS, BLOCKS>, dim3(grid), dim3(threads), 0, s, a));
+  return MOE_OK;
+}
+
 template <typename Y, typename R>
 moe_status run_end(const EndArgs& a, bool wide, cudaStream_t s) {
   const int units = wide ? a.N / 8 : a.N;
-  const int most = a.T >= 2 * operator_sms() ? 256 : MAX_THREADS;
-  int v = 1;
-  while (v < (wide ? 4 : 32) && (units + v - 1) / v > most) v *= 2;
-  const int threads = ((units + v - 1) / v + 31) / 32 * 32;
-  if (wide)
-    return v == 1 ? launch_end<Y, R, 8, 1>(a, threads, s) : v == 2 ? launch_end<Y, R, 8, 2>(a, threads, s) : launch_end<Y, R, 8, 4>(a, threads, s);
-  return v <= 4 ? launch_end<Y, R, 1, 4>(a, ((units + 3) / 4 + 31) / 32 * 32, s) : v == 8 ? launch_end<Y, R, 1, 8>(a, threads, s)
-         : v == 16 ? launch_end<Y, R, 1, 16>(a, threads, s) : launch_end<Y, R, 1, 32>(a, threads, s);
+  auto threads = [&](int v) { return ((units + v - 1) / v + 31) / 32 * 32; };
+  constexpr int H = sizeof(Y) == 2 ? 2 : 1;   // rows on their way: twice as many of half the bytes
+  if (wide) {
+    if (a.T >= 2 * operator_sms() && (!a.place || a.k <= 30)) {   // a lane a row
+      if constexpr (sizeof(Y) + sizeof(R) == 4) {
+        if (units <= 512) return launch_stream<Y, R, 2, 3, false, 256, 4>(a, threads(2), s);
+        if (units <= 1024) return launch_stream<Y, R, 2, 3, false, 512, 2>(a, threads(2), s);
+      } else {
+        if (units <= 256) return launch_stream<Y, R, 1, 3, true, 256, 2>(a, threads(1), s);
+        if (units <= 1024) return launch_stream<Y, R, 2, 3, true, 512, 1>(a, threads(2), s);
+      }
+    }
+    if (units <= 1024) return launch_end<Y, R, 8, 1, 4 * H, 1024, 1>(a, threads(1), s);
+    if (units <= 2048) return launch_end<Y, R, 8, 2, H, 1024, 1>(a, threads(2), s);
+    return launch_end<Y, R, 8, 4, 1, 1024, 1>(a, threads(4), s);
+  }
+  if (units <= 1024) return launch_end<Y, R, 1, 4, 4, 256, 4>(a, threads(4), s);
+  if (units <= 8192) return launch_end<Y, R, 1, 8, 2, 1024, 1>(a, threads(8), s);
+  return launch_end<Y, R, 1, 32, 1, 1024, 1>(a, threads(32), s);
 }
 
 }  // namespace

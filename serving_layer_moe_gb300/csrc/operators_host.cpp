@@ -436,6 +436,55 @@ PyObject* or_raise(moe_status st, PyObject* r) {
   return raise(st);
 }
 
+// blocks8(codes, scales, rows) -> True if they are 8-bit rows, or weights
+PyObject* blocks8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  TRY
+  Blocks8 b;
+  if (n != 3 || !THPVariable_Check(a[0])) OTHERWISE;
+  const bool rows = a[2] == Py_True;
+  if (!blocks8_in(a[0], a[1], rows, !rows && THPVariable_Unpack(a[0]).dim() == 3 ? 3 : 2, -1, b)) OTHERWISE;
+  Py_RETURN_TRUE;
+  CATCH
+}
+
+// dequantize8(codes, scales, rows, out dtype) -> tensor
+PyObject* dequantize8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  TRY
+  Blocks8 b;
+  if (n != 4 || !THPVariable_Check(a[0])) OTHERWISE;
+  const bool rows = a[2] == Py_True;
+  const at::Tensor& codes = THPVariable_Unpack(a[0]);
+  if (!blocks8_in(a[0], a[1], rows, !rows && codes.dim() == 3 ? 3 : 2, -1, b)) OTHERWISE;
+  const long od = PyLong_AsLong(a[3]);
+  void* s;
+  if (PyErr_Occurred()) return nullptr;
+  if (!here(b.index, &s)) OTHERWISE;
+  const at::Tensor out = empty(codes.sizes(), float_type(od), b.index);
+  PyObject* r = THPVariable_Wrap(out);
+  if (out.numel() == 0) return r;
+  return or_raise(moe_dequantize_fp8((int32_t)b.G, (int32_t)b.N, (int32_t)b.K, !rows, b.codes, b.scales, (int32_t)od, out.data_ptr(), s), r);
+  CATCH
+}
+
+// quantize_weights8(w) -> (codes, scales)
+PyObject* quantize_weights8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  TRY
+  if (n != 1 || !THPVariable_Check(a[0])) OTHERWISE;
+  const int dim = THPVariable_Unpack(a[0]).dim() == 3 ? 3 : 2;
+  const at::Tensor* w = tensor(a[0], dim, -1);
+  if (!w) OTHERWISE;
+  const int dt = float_code(*w);
+  const int64_t G = dim == 3 ? w->size(0) : 1, N = w->size(dim - 2), K = w->size(dim - 1), index = w->get_device(), nb = (N + 127) / 128, kb = (K + 127) / 128;
+  void* s;
+  if (dt < 0 || K < 1 || K % 16 || !matrices_fit(G, N, K) || nb * kb > 0x7fffffff || !aligned(w->data_ptr(), 16) || !here(index, &s)) OTHERWISE;
+  const at::Tensor codes = empty(w->sizes(), ScalarType::Float8_e4m3fn, index);
+  const at::Tensor scales = dim == 3 ? empty({G, nb, kb}, ScalarType::Float, index) : empty({nb, kb}, ScalarType::Float, index);
+  PyObject* r = Py_BuildValue("(NN)", THPVariable_Wrap(codes), THPVariable_Wrap(scales));
+  if (w->numel() == 0) return r;
+  return or_raise(moe_quantize_fp8_weights((int32_t)G, (int32_t)N, (int32_t)K, dt, w->data_ptr(), static_cast<uint8_t*>(codes.data_ptr()), scales.data_ptr<float>(), s), r);
+  CATCH
+}
+
 // quantize8(x, groups) -> (codes, scales)
 PyObject* quantize8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TRY
@@ -555,7 +604,7 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(init), FAST(groups_of), FAST(rows_of), FAST(route), FAST(quantize), FAST(dequantize), FAST(matmul), FAST(matmul_fp4),
-                         FAST(combine), FAST(quantize8), FAST(matmul8), FAST(block_end), FAST(views), {nullptr, nullptr, 0, nullptr}};
+                         FAST(combine), FAST(blocks8), FAST(dequantize8), FAST(quantize_weights8), FAST(quantize8), FAST(matmul8), FAST(block_end), FAST(views), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operators", "the short way from torch tensors to the operators", -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -500,9 +500,11 @@ class _Blocks8:
     """8-bit codes and the scales of their blocks, of one device.  The tensors cannot be exchanged after."""
 
     __slots__ = ("_codes", "_scales")
+    _rows = False
 
     def __init__(self, codes, scales):
-        self._check(codes, scales)
+        if not (_host_module or _host()).blocks8(codes, scales, self._rows):
+            self._check(codes, scales)
         self._codes, self._scales = codes, scales
 
     @classmethod
@@ -530,6 +532,7 @@ class FP8Rows(_Blocks8):
     (include/moe_operators.h, "8-bit blocks").  Rows in expert order are rows like others."""
 
     __slots__ = ()
+    _rows = True
 
     @staticmethod
     def _check(codes, scales):
@@ -589,35 +592,31 @@ def quantize_fp8(x, *, groups=None, stream=None):
 
 def quantize_fp8_weights(w, *, stream=None):
     """Weights w [N, K] or [G, N, K], fp32 or bf16, as FP8Weights, K a multiple of 16 (moe_quantize_fp8_weights)."""
+    if stream is None:
+        r = (_host_module or _host()).quantize_weights8(w)
+        if r is not None:
+            return FP8Weights._of(*r)
     dim = 3 if isinstance(w, torch.Tensor) and w.dim() == 3 else 2
-    dt = _floats(w, "w", dim)
+    _floats(w, "w", dim)
     index = w.get_device()
     G, N, K = w.shape if dim == 3 else (1, *w.shape)
     _matrices(G, N, K, 16)
     if -(-N // 128) * -(-K // 128) > _MOST_ROWS:
         raise ValueError(f"a matrix may have {_MOST_ROWS} blocks at most, got {N} x {K} elements")
     _aligned(w=w)
-    if stream is not None or index != torch.cuda.current_device():
-        return _again(lambda: quantize_fp8_weights(w), index, stream)
-    codes = torch.empty(w.shape, dtype=_F8, device=w.device)
-    scales = torch.empty(*w.shape[:-2], -(-N // 128), -(-K // 128), dtype=_F32, device=w.device)
-    _check(_operators().moe_quantize_fp8_weights(G, N, K, dt, w.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream(index)))
-    return FP8Weights._of(codes, scales)
+    return _again(lambda: quantize_fp8_weights(w), index, stream)
 
 
 def dequantize_fp8(q, *, out_dtype=torch.bfloat16, stream=None):
     """The values that q (FP8Rows or FP8Weights) stands for, in q.shape (moe_dequantize_fp8)."""
+    if stream is None and isinstance(q, _Blocks8) and out_dtype in _FLOATS:
+        out = (_host_module or _host()).dequantize8(q._codes, q._scales, q._rows, _FLOATS[out_dtype])
+        if out is not None:
+            return out
     _blocks8(q, "q", (FP8Rows, FP8Weights))
     if out_dtype not in _FLOATS:
         raise ValueError(f"out_dtype must be float32 or bfloat16, is {out_dtype}")
-    index = q._index
-    if stream is not None or index != torch.cuda.current_device():
-        return _again(lambda: dequantize_fp8(q, out_dtype=out_dtype), index, stream)
-    out = torch.empty(q.shape, dtype=out_dtype, device=q.codes.device)
-    G, N, K = q.shape if len(q.shape) == 3 else (1, *q.shape)
-    _check(_operators().moe_dequantize_fp8(G, N, K, isinstance(q, FP8Weights), q.codes.data_ptr(), q.scales.data_ptr(), _FLOATS[out_dtype],
-                                           out.data_ptr(), _stream(index)))
-    return out
+    return _again(lambda: dequantize_fp8(q, out_dtype=out_dtype), q._index, stream)
 
 
 def _product8(x, w, groups, act, quantize, out_dtype, stream):
