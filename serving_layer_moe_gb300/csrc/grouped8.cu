@@ -357,15 +357,20 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const uint32_t idesc = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(8 * CG) << 24);
         for (int it = it0; it < it1 && ok; it += step) {
           for (int ks = 0; ks < a.kslices; ++ks) {
-            if (!warp_wait(tempty + 8 * acc, acc_phase ^ 1u, abort_flag) || !warp_wait(full + 8 * stage, phase, abort_flag)) { ok = false; break; }
+            const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
+            const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
+            const int left = a.K - ks * 128;
+            // The accumulator is what the products wait for, and the epilogue for them: nothing is left to do behind it.  The other CTA's
+            // arrivals stand for its TMEM reads, which the fences order; no memory is handed over.
+            if (!warp_wait_cta(full + 8 * stage, phase, abort_flag) || !warp_wait_cta(tempty + 8 * acc, acc_phase ^ 1u, abort_flag)) { ok = false; break; }
             fence_after();
             if (elect_one()) {
-              const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
-              const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
-              const int left = a.K - ks * 128;
+              if (left >= 128) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                if (kk * 32 < left) mma_f8<CG>(d, dx + at + 2 * kk, dw + at + 2 * kk, idesc, (uint32_t)kk);
+                for (int kk = 0; kk < 4; ++kk) mma_f8<CG>(d, dx + at + 2 * kk, dw + at + 2 * kk, idesc, (uint32_t)kk);
+              } else {
+                for (int kk = 0; kk * 32 < left; ++kk) mma_f8<CG>(d, dx + at + 2 * kk, dw + at + 2 * kk, idesc, (uint32_t)kk);
+              }
               commit<CG>(empty + 8 * stage);
               commit<CG>(tfull + 8 * acc);
             }
