@@ -47,8 +47,11 @@ __device__ uint32_t g_operator_err8;
 constexpr int FIRST_EPI = 4, EW = 8;
 constexpr int THREADS = 32 * (FIRST_EPI + EW);
 constexpr int MAX_STAGES = 12;
-constexpr int ACC_COLS = 256;                  // between the accumulators
-constexpr int GROUP = 4;                       // slices whose scales go together
+// Accumulators, and columns between them: a slice's products and its sums take turns on one, so that with small tiles, whose slices are
+// short, it is the way from one to the other and back that counts.
+template <int TILE> constexpr int accs() { return TILE == 256 ? 2 : 4; }
+constexpr int TMEM_COLS = 512, MAX_ACCS = 4;
+constexpr int GROUP = 4;                       // slices whose scales go together, a multiple of the accumulators
 constexpr int SLOT = GROUP * 128 + 4 * GROUP;  // a group's scales: [slice][token of the CTA], then [half of the columns][even, odd 16 columns][slice]
 constexpr int SCALE_SLOTS = 3;
 // What the epilogue has to know of the items (looking it up there, between two items, took 1500 cycles): the scales' warp, SCALE_SLOTS
@@ -117,10 +120,12 @@ __device__ __forceinline__ int rows_of(const Args8& a, const Item8& o, int rank)
 }
 __device__ __forceinline__ int rows_loaded(const Args8& a, int rows) { return (rows + a.box - 1) / a.box * a.box; }
 
-__device__ __forceinline__ void swap(uint32_t (&v)[2]) {
+template <int N>
+__device__ __forceinline__ void rotate(uint32_t (&v)[N]) {
   const uint32_t t = v[0];
-  v[0] = v[1];
-  v[1] = t;
+#pragma unroll
+  for (int i = 1; i < N; ++i) v[i - 1] = v[i];
+  v[N - 1] = t;
 }
 // acc += {a, b} * s, behind the wait for a and b
 __device__ __forceinline__ void add2(uint64_t& acc, uint32_t a, uint32_t b, uint64_t s) {
@@ -233,10 +238,23 @@ __device__ __forceinline__ void put_results(const Args8& a, const CUtensorMap& m
   else put_results<CG, CHUNKS, STEP, false>(a, map, buf, v, token, rows, f);
 }
 
+// desc_sw128 in two halves: what an address adds is in the lower one
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return (uint32_t)desc_sw128(addr); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) { return (desc_sw128(0) & 0xffffffff00000000ull) | low; }
+// whether both phases are over, for the whole warp; the second test is on its way during the first
+__device__ __forceinline__ bool test_both(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n"
+      " and.pred p, p, q;\n vote.sync.all.pred q, p, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(ok) : "r"(b0), "r"(p0), "r"(b1), "r"(p1) : "memory");
+  return ok != 0;
+}
 template <int CG, int TILE>
 __global__ void __launch_bounds__(THREADS, 1)
 product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmO, const Args8 a) {
   constexpr int HALF = TILE / 2, CHUNKS = HALF / 16;     // a thread's columns: half of the tile's, 16 a chunk
+  constexpr int ACCS = accs<TILE>(), ACC_COLS = TMEM_COLS / ACCS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -252,8 +270,8 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   uint32_t* tops = reinterpret_cast<uint32_t*>(tail);   // [turn][half of the columns][token]
   tail += 2 * 2 * 128 * 4;
   const uint32_t full = smem_u32(tail), empty = full + 8 * MAX_STAGES, sfull = empty + 8 * MAX_STAGES, sempty = sfull + 8 * SCALE_SLOTS,
-                 tfull = sempty + 8 * SCALE_SLOTS, tempty = tfull + 16, tops_full = tempty + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 64);
+                 tfull = sempty + 8 * SCALE_SLOTS, tempty = tfull + 8 * MAX_ACCS, tops_full = tempty + 8 * MAX_ACCS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 16 * MAX_ACCS + 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* first = reinterpret_cast<int32_t*>(tmem_slot + 4);
 
@@ -268,7 +286,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       mbar_init(sfull + 8 * s, 1);
       mbar_init(sempty + 8 * s, EW);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < ACCS; ++s) {
       mbar_init(tfull + 8 * s, 1);
       mbar_init(tempty + 8 * s, EW * CG);
     }
@@ -276,7 +294,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 2 * ACC_COLS);
+  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), TMEM_COLS);
   pdl_wait();
   pdl_trigger();
   if (warp == 2) {   // token tiles before each expert
@@ -351,32 +369,33 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
       // ---------------- products ----------------
       if (rank == 0) {
         int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        const uint64_t dw = desc_sw128(ring), dx = desc_sw128(ring + w_bytes);
+        uint32_t phase = 0, acc_phase = 1, at = 0;
+        const uint32_t lw = desc_low(ring), lx = desc_low(ring + w_bytes);
+        const uint32_t stage_step = (uint32_t)a.stage_bytes >> 4;
+        const int whole = a.K >> 7, rest = a.K & 127;
         // D fp32; e4m3 operands, both K-major; N = TILE; M = 128 CG
-        const uint32_t idesc = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(8 * CG) << 24);
+        constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(8 * CG) << 24);
         for (int it = it0; it < it1 && ok; it += step) {
           for (int ks = 0; ks < a.kslices; ++ks) {
-            const uint64_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
-            const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
-            const int left = a.K - ks * 128;
-            // The accumulator is what the products wait for, and the epilogue for them: nothing is left to do behind it.  The other CTA's
-            // arrivals stand for its TMEM reads, which the fences order; no memory is handed over.
-            if (!warp_wait_cta(full + 8 * stage, phase, abort_flag) || !warp_wait_cta(tempty + 8 * acc, acc_phase ^ 1u, abort_flag)) { ok = false; break; }
+            // The other CTA's arrivals on tempty stand for its TMEM reads, which the fences order; no memory is handed over.
+            if (!test_both(full + 8 * stage, phase, tempty + 8 * acc, acc_phase) &&
+                (!warp_wait(full + 8 * stage, phase, abort_flag) || !warp_wait(tempty + 8 * acc, acc_phase, abort_flag))) { ok = false; break; }
             fence_after();
+            const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
             if (elect_one()) {
-              if (left >= 128) {
+              if (ks < whole) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_f8<CG>(d, dx + at + 2 * kk, dw + at + 2 * kk, idesc, (uint32_t)kk);
+                for (int kk = 0; kk < 4; ++kk) mma_f8<CG>(d, desc_of(lx + at + 2 * kk), desc_of(lw + at + 2 * kk), idesc, (uint32_t)kk);
               } else {
-                for (int kk = 0; kk * 32 < left; ++kk) mma_f8<CG>(d, dx + at + 2 * kk, dw + at + 2 * kk, idesc, (uint32_t)kk);
+                for (int kk = 0; kk * 32 < rest; ++kk) mma_f8<CG>(d, desc_of(lx + at + 2 * kk), desc_of(lw + at + 2 * kk), idesc, (uint32_t)kk);
               }
-              commit<CG>(empty + 8 * stage);
               commit<CG>(tfull + 8 * acc);
+              commit<CG>(empty + 8 * stage);
             }
             __syncwarp();
-            if (++stage == a.stages) { stage = 0; phase ^= 1u; }
-            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            at += stage_step;
+            if (++stage == a.stages) { stage = 0; phase ^= 1u; at = 0; }
+            if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
           }
         }
         if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
@@ -443,10 +462,10 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int q = warp & 3, part = (warp - FIRST_EPI) >> 2;
     int slot = 0, turn = 0, head = 0;
     uint32_t slot_phase = 0, tops_phase = 0;
-    // of the accumulator of even and of odd slices: where the warp reads it, its barriers, the phase of the next use
-    uint32_t from[2], ready[2], done[2], phase[2] = {0u, 0u};
+    // of the accumulator of an item's every ACCS-th slice: where the warp reads it, its barriers, the phase of the next use
+    uint32_t from[ACCS], ready[ACCS], done[ACCS], phase[ACCS] = {};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ACCS; ++i) {
       from[i] = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(i * ACC_COLS + HALF * part);
       ready[i] = tfull + 8 * i;
       done[i] = CG == 2 ? in_rank(tempty + 8 * i, 0) : tempty + 8 * i;
@@ -477,38 +496,38 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < GROUP; ++j) {
           if (k0 + j >= a.kslices) break;
-          ok = warp_wait_cta(ready[j & 1], phase[j & 1], abort_flag);
+          ok = warp_wait_cta(ready[j % ACCS], phase[j % ACCS], abort_flag);
           if (!ok) break;
-          phase[j & 1] ^= 1u;
+          phase[j % ACCS] ^= 1u;
           fence_after();
           if (some) {
             const uint64_t t0 = pack2(s0[j], s0[j]), t1 = pack2(s1[j], s1[j]);
             uint32_t x[2][16];
-            tmem_ld32(from[j & 1], x[0]);
+            tmem_ld32(from[j % ACCS], x[0]);
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c) {
               tmem_wait();
               if (c + 1 < CHUNKS) {
-                tmem_ld32(from[j & 1] + 16 * (c + 1), x[(c + 1) & 1]);
+                tmem_ld32(from[j % ACCS] + 16 * (c + 1), x[(c + 1) & 1]);
               } else {   // the accumulator has been read
                 fence_before();
-                arrive_elected<CG>(done[j & 1]);
+                arrive_elected<CG>(done[j % ACCS]);
               }
 #pragma unroll
               for (int i = 0; i < 8; ++i) add2(sum[c][i], x[c & 1][2 * i], x[c & 1][2 * i + 1], c & 1 ? t1 : t0);
             }
           } else {
             fence_before();
-            arrive_elected<CG>(done[j & 1]);
+            arrive_elected<CG>(done[j % ACCS]);
           }
         }
         if (!ok) break;
       }
-      if (a.kslices & 1) {   // the next item starts with the other accumulator
-        swap(from);
-        swap(ready);
-        swap(done);
-        swap(phase);
+      for (int i = a.kslices % ACCS; i > 0; --i) {   // the accumulator that the next item starts with
+        rotate(from);
+        rotate(ready);
+        rotate(done);
+        rotate(phase);
       }
       if (!ok) {
         if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
@@ -583,7 +602,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
   if constexpr (CG == 2) cluster_sync();
   if (warp == 1) {
     fence_after();
-    tmem_free<CG>(tmem, 2 * ACC_COLS);
+    tmem_free<CG>(tmem, TMEM_COLS);
   }
 }
 
@@ -605,7 +624,7 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   a.box = std::min(32, x_rows & -x_rows);
   a.stage_bytes = (TILE / CG + x_rows) * 128;
   // behind the last stage as much as the products read past its token rows
-  const int fixed = 1024 + std::max(EW * epi_warp<CG>() + SCALE_SLOTS * SLOT * 4 + HEADS * 16 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 64 + 16 + 4 * (a.E + 1), (128 - x_rows) * 128);
+  const int fixed = 1024 + std::max(EW * epi_warp<CG>() + SCALE_SLOTS * SLOT * 4 + HEADS * 16 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 16 * MAX_ACCS + 32 + 16 + 4 * (a.E + 1), (128 - x_rows) * 128);
   a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 
@@ -686,8 +705,21 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   return MOE_OK;
 }
 
-// Pairs of CTAs take twice the tokens with the same weight rows: from a single CTA's 128 an expert on.
-bool use_pairs8(int64_t P, int64_t E) { return P > 128 * E; }
+// Pairs of CTAs take twice the tokens with the same weight rows, single ones waste less on ragged tiles.  us, pairs and single, by
+// rows an expert (128 experts, K 2048, N 1536, requantised): 192 rows 125 / 105, 512 219 / 208, 1024 388 / 359; 32 experts, K 7168,
+// N 4096, SwiGLU: 512 430 / 409, 768 545 / 557, 1024 730 / 756; 2048 rows of 8 experts without SwiGLU 333 / 384.  Pairs store their tiles under the
+// next one's products, which counts when K is short (K 768, N 2048: 256 rows 88 / 82, 512 133 / 144, 1024 232 / 266).
+bool use_pairs8(const Args8& a) { return a.P > (int64_t)(a.act ? a.K >= 4096 ? 704 : 1536 : a.K <= 1024 ? 384 : 704) * a.E; }
+
+// Weight rows of a single CTA's tile: as many as leave items for half of the SMs.  With one tile a unit a call lasts as long as its slices take in
+// turn, a quarter of a microsecond and more.  us with 256, 128 and 64 rows: one row, K 7168, N 4096 23.0 / 17.2 / 15.6; 256 rows, K 2048,
+// N 7168 10.8 / 9.0 / 11.5; one row of 8 experts, K 768, N 2048 7.4 / 6.8 / 7.8.
+int tile8(const Args8& a, int64_t tiles) {
+  if (a.quant) return 256;   // a block of 128 features is one tile's
+  int tile = 256;   // SwiGLU: a warp stores 32 features at least
+  while (tile > (a.act ? 128 : 64) && tiles * ((a.N + tile - 1) / tile) < operator_sms() / 2) tile /= 2;
+  return tile;
+}
 
 }  // namespace
 
@@ -734,5 +766,7 @@ extern "C" moe_status moe_grouped_matmul_fp8(int32_t P, int32_t E, int32_t N, in
   a.sx = x_scales; a.sw = w_scales; a.offsets = offsets; a.out = out; a.out_codes = out_codes; a.out_scales = out_scales;
   const Mem8 mem{x_codes, w_codes};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return use_pairs8(P, E) ? launch8<2, 256>(a, mem, s) : launch8<1, 256>(a, mem, s);
+  if (use_pairs8(a)) return launch8<2, 256>(a, mem, s);
+  const int tile = tile8(a, (P + 127 * (int64_t)std::min(P, E)) / 128);
+  return tile == 256 ? launch8<1, 256>(a, mem, s) : tile == 128 ? launch8<1, 128>(a, mem, s) : launch8<1, 64>(a, mem, s);
 }

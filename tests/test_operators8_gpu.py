@@ -160,6 +160,26 @@ def rough(y, h):
     return (gate + 10) * 2 * EPS * np.abs(h) + gate * up * 2.0 ** -60 * (gate > 41) + 1e-30
 
 
+@pytest.mark.parametrize("counts,N,K", [([1, 0, 1, 1, 0, 1], 384, 2000), ([2, 5, 0, 9], 1000, 1040), ([1], 640, 7168), ([31, 1], 512, 2048), ([64], 300, 656), ([128], 260, 1296),
+                                        ([0, 0, 3], 129, 512)])
+def test_few_items_share_k(moe, counts, N, K):
+    """Calls that leave most SMs idle: several CTAs an item, every form of result."""
+    rng = np.random.default_rng(K)
+    gr, (offsets, _, _, _), P, E, _ = grouping(moe, rng, counts)
+    xc, xs, wc, ws = whole(rng, P, E, N, K)
+    y = product(xc, xs, wc, ws, offsets)
+    x, w = operands(moe, xc, xs, wc, ws)
+    for out in (torch.float32, torch.bfloat16):
+        assert np.array_equal(host(moe.grouped_matmul_fp8(x, w, gr, out_dtype=out)), y if out == torch.float32 else bf16(y))
+    if N % 128 == 0:
+        y = (y / 64).astype(np.float64)
+        x = moe.FP8Rows(x.codes, x.scales / 64)
+        for out in (torch.float32, torch.bfloat16):
+            swiglu_within(host(moe.grouped_matmul_fp8(x, w, gr, act="swiglu", out_dtype=out)), y, out)
+        check_quantized(moe.grouped_matmul_fp8(x, w, gr, act="swiglu", quantize=True), y)
+    moe.check_operators()
+
+
 def swiglu_within(got, y, out):
     """fp32: silu within 11 half units and a product; bf16: what `rough` says, then half a bf16 step."""
     h = ref.swiglu(y)
