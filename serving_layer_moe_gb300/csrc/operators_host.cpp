@@ -392,17 +392,18 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   CATCH
 }
 
-// contiguous fp32 or bf16 of `dim` dimensions on `index`, aligned to 16 bytes where `wide`; its code to *dt.  None is fine where `none`
-bool floats_in(PyObject* o, int dim, int64_t index, bool wide, bool none, int* dt, const void** p) {
+// contiguous fp32 or bf16 of this shape on `index`, its code to *dt; None is fine where `none`
+bool floats_in(PyObject* o, at::IntArrayRef shape, int64_t index, bool none, int* dt) {
   *dt = MOE_F32;
-  *p = nullptr;
   if (o == Py_None) return none;
-  const at::Tensor* t = tensor(o, dim, index);
-  if (!t || (*dt = float_code(*t)) < 0) return false;
-  *p = t->data_ptr();
+  const at::Tensor* t = tensor(o, (int)shape.size(), index);
+  return t && t->sizes() == shape && (*dt = float_code(*t)) >= 0;
+}
+// where it is, once all else is right; false if it is not on 16 bytes where `wide`
+bool pointer(PyObject* o, bool wide, const void** p) {
+  *p = o == Py_None ? nullptr : THPVariable_Unpack(o).data_ptr();
   return !wide || aligned(*p, 16);
 }
-bool sized(PyObject* o, at::IntArrayRef shape) { return o == Py_None || THPVariable_Unpack(o).sizes() == shape; }
 
 // codes and scales of 8-bit blocks, as they are now: [R, K] with scales [blocks of K, R], or [N, K] / [G, N, K] with a block of 128 x 128 each
 struct Blocks8 { int64_t index, G, N, K; const uint8_t* codes; const float* scales; };
@@ -556,23 +557,32 @@ PyObject* block_end(PyObject*, PyObject* const* a, Py_ssize_t n) {
     w = typed(a[2], ScalarType::Float, 2, index);
     if (!w || w->size(0) != g.T || w->size(1) != g.k) OTHERWISE;
   }
-  if (N < 1 || N > 32768 || !pairs_fit(T, 1) || !floats_in(a[3], 2, index, wide, false, &rd, &res) || !floats_in(a[0], 2, index, wide, true, &yd, &y) ||
-      !sized(a[0], {grouped ? g.P : T, N}) || !floats_in(a[4], 2, index, wide, true, &sd, &shared) || !sized(a[4], {T, N}) || (shared && sd != yd) ||
-      !floats_in(a[5], 1, index, wide, true, &pd, &post) || !sized(a[5], {N}) || !floats_in(a[8], 1, index, wide, true, &qd, &pre) || !sized(a[8], {N}) ||
-      (!any && (!normed || shared || post || a[6] != Py_None)))
-    OTHERWISE;
   const bool per_row = THPVariable_Check(a[6]) && THPVariable_Unpack(a[6]).dim() == 2;
-  if (!floats_in(a[6], per_row ? 2 : 1, index, wide && !per_row, true, &gd, &gate) || gd != MOE_F32 ||
-      !(per_row ? sized(a[6], {T, 1}) : sized(a[6], {N})))
+  const int64_t rows[2] = {T, N}, pairs[2] = {grouped ? g.P : T, N}, width[1] = {N}, each[2] = {T, 1};
+  if (N < 1 || N > 32768 || !pairs_fit(T, 1) || !floats_in(a[3], rows, index, false, &rd) || !floats_in(a[0], pairs, index, true, &yd) ||
+      !floats_in(a[4], rows, index, true, &sd) || (a[4] != Py_None && sd != yd) || !floats_in(a[5], width, index, true, &pd) ||
+      !floats_in(a[8], width, index, true, &qd) || !(per_row ? floats_in(a[6], each, index, true, &gd) : floats_in(a[6], width, index, true, &gd)) || gd != MOE_F32 ||
+      (!any && (!normed || a[4] != Py_None || a[5] != Py_None || a[6] != Py_None)))
     OTHERWISE;
   const double scale = PyFloat_AsDouble(a[7]), eps = PyFloat_AsDouble(a[9]);
   const long zd = PyLong_AsLong(a[10]);
   if (PyErr_Occurred()) return nullptr;
   void* s;
-  if (!(eps >= 1.1754944e-38 && eps <= 3e38) || !(scale >= -3.4e38 && scale <= 3.4e38) || !here(index, &s)) OTHERWISE;
+  if (!(eps >= 1.1754944e-38 && eps <= 3e38) || !(scale >= -3.4e38 && scale <= 3.4e38) || !pointer(a[3], wide, &res) || !pointer(a[0], wide, &y) ||
+      !pointer(a[4], wide, &shared) || !pointer(a[5], wide, &post) || !pointer(a[8], wide, &pre) || !pointer(a[6], wide && !per_row, &gate) || !here(index, &s))
+    OTHERWISE;
+  // both in one allocation up to 64 K elements; larger ones apart, so that keeping the stream does not keep what the norm made of it
   at::Tensor h, z;
-  if (any) h = empty({T, N}, float_type(rd), index);
-  if (normed) z = empty({T, N}, float_type(zd), index);
+  if (any && normed && T * N <= 65536) {
+    const ScalarType ht = float_type(rd), zt = float_type(zd);
+    const int64_t hb = (T * N * (rd == MOE_F32 ? 4 : 2) + 15) / 16 * 16;
+    const at::Tensor b = room(hb + T * N * (zd == MOE_F32 ? 4 : 2), index);
+    h = on(b, 0, {T, N}, ht);
+    z = on(b, hb, {T, N}, zt);
+  } else {
+    if (any) h = empty({T, N}, float_type(rd), index);
+    if (normed) z = empty({T, N}, float_type(zd), index);
+  }
   PyObject* result = any && normed ? Py_BuildValue("(NN)", THPVariable_Wrap(h), THPVariable_Wrap(z)) : THPVariable_Wrap(any ? h : z);
   if (T == 0) return result;
   return or_raise(moe_combine_norm((int32_t)T, grouped ? (int32_t)g.k : 1, (int32_t)N, yd, y, ptr<int32_t>(g.place), w ? w->data_ptr<float>() : nullptr, shared, pd, post,

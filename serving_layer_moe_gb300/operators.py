@@ -673,10 +673,7 @@ def grouped_matmul_fp8(x, w, groups, *, act="none", quantize=False, out_dtype=to
 
 
 def _block_end(y, groups, topk_w, residual, shared, post, gate, scale, pre, eps, out_dtype, stream):
-    if stream is None and out_dtype in _FLOATS:
-        r = (_host_module or _host()).block_end(y, _described(groups), topk_w, residual, shared, post, gate, scale, pre, eps, _FLOATS[out_dtype])
-        if r is not None:
-            return r
+    """The calls that the host module has left alone."""
     _floats(residual, "residual", 2)
     index = residual.get_device()
     T, N = residual.shape
@@ -716,7 +713,11 @@ def _block_end(y, groups, topk_w, residual, shared, post, gate, scale, pre, eps,
         for name, t in (("y", y), ("residual", residual), ("shared", shared), ("post", post), ("pre", pre), ("gate", gate)):
             if t is not None and (name != "gate" or t.dim() == 1) and t.data_ptr() % 16:
                 raise ValueError(f"{name} must be 16-byte aligned where rows are a multiple of 8 elements")
-    return _again(lambda: _block_end(y, groups, topk_w, residual, shared, post, gate, scale, pre, eps, out_dtype, None), index, stream)
+    call = _host().block_end
+    r = _again(lambda: call(y, _described(groups), topk_w, residual, shared, post, gate, scale, pre, eps, _FLOATS[out_dtype]), index, stream)
+    if r is None:
+        raise ValueError("the call was not made: tensors that its groups hold were resized, moved or replaced since")
+    return r
 
 
 def combine_norm(y, groups, topk_w, residual, *, shared=None, post=None, gate=None, residual_scale=1.0, pre=None, eps=1e-6,
@@ -729,6 +730,10 @@ def combine_norm(y, groups, topk_w, residual, *, shared=None, post=None, gate=No
         raise ValueError(f"groups must be ExpertGroups, is {type(groups)}")
     if y is None:
         raise ValueError("y must be a tensor, is None")
+    if stream is None and out_dtype in _FLOATS:
+        r = (_host_module or _host()).block_end(y, groups._c, topk_w, residual, shared, post, gate, residual_scale, pre, eps, _FLOATS[out_dtype])
+        if r is not None:
+            return r
     return _block_end(y, groups, topk_w, residual, shared, post, gate, residual_scale, pre, eps, out_dtype, stream)
 
 
@@ -736,6 +741,10 @@ def residual_norm(y, residual, *, post=None, gate=None, residual_scale=1.0, pre=
     """combine_norm for a block that is no mixture: y [T, N] holds a row for each token."""
     if y is None:
         raise ValueError("y must be a tensor, is None")
+    if stream is None and out_dtype in _FLOATS:
+        r = (_host_module or _host()).block_end(y, None, None, residual, None, post, gate, residual_scale, pre, eps, _FLOATS[out_dtype])
+        if r is not None:
+            return r
     return _block_end(y, None, None, residual, None, post, gate, residual_scale, pre, eps, out_dtype, stream)
 
 
@@ -743,6 +752,10 @@ def rms_norm(x, weight, *, eps=1e-6, out_dtype=torch.bfloat16, stream=None):
     """x / sqrt(mean(x^2) + eps) * weight of the rows of x [T, N], in out_dtype: the norm before the first block (moe_combine_norm)."""
     if weight is None:
         raise ValueError("weight must be a tensor, is None")
+    if stream is None and out_dtype in _FLOATS:
+        r = (_host_module or _host()).block_end(None, None, None, x, None, None, None, 1.0, weight, eps, _FLOATS[out_dtype])
+        if r is not None:
+            return r
     return _block_end(None, None, None, x, None, None, None, 1.0, weight, eps, out_dtype, stream)
 
 
