@@ -87,24 +87,34 @@ __device__ __forceinline__ int row_at(const Args8& a, int e) {
   return a.offsets ? min(max(__ldg(a.offsets + e), 0), a.P) : e ? a.P : 0;
 }
 
-// item `it` into o, which holds the one before (tt = -1: none)
+// item `it` into o, which holds the one before (tt = -1: none), by a whole warp.  at[e]: the token tiles, and rows, before expert e.
 template <int CG>
-__device__ __forceinline__ void item_at(const Args8& a, const int32_t* first, int it, Item8& o) {
+__device__ __forceinline__ void item_at(const Args8& a, const int2* at, int it, Item8& o) {
   const int tt = it / a.m_blocks;
   o.mb = it - tt * a.m_blocks;
   if (tt == o.tt) return;
   o.tt = tt;
-  int lo = 0, hi = a.E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= tt) lo = mid;
-    else hi = mid;
+  int lo = 0;
+  if (a.E <= 256) {   // how many experts start at tt or before: the steps of a search would wait for one another
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int b = 0; b < 256; b += 32)
+      if (b < a.E) lo += __popc(__ballot_sync(0xffffffffu, b + lane < a.E && at[b + lane].x <= tt));
+    --lo;
+  } else {
+    int hi = a.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (at[mid].x <= tt) lo = mid;
+      else hi = mid;
+    }
   }
   o.e = lo;
   // even shares of the expert's rows: they are what is loaded
-  const int j = tt - first[lo], r0 = row_at(a, lo), n = max(row_at(a, lo + 1), r0) - r0, nt = first[lo + 1] - first[lo];
-  const int chunk = min(128 * CG, (n + nt - 1) / nt);
-  o.row0 = r0 + j * chunk;
+  const int2 s0 = at[lo], s1 = at[lo + 1];
+  const int n = max(s1.y - s0.y, 0), nt = s1.x - s0.x, j = tt - s0.x;
+  const int chunk = nt == 1 ? min(128 * CG, n) : min(128 * CG, (n + nt - 1) / nt);
+  o.row0 = s0.y + j * chunk;
   o.n = min(chunk, n - j * chunk);
 }
 
@@ -273,7 +283,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                  tfull = sempty + 8 * SCALE_SLOTS, tempty = tfull + 8 * MAX_ACCS, tops_full = tempty + 8 * MAX_ACCS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 16 * MAX_ACCS + 32);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* first = reinterpret_cast<int32_t*>(tmem_slot + 4);
+  int2* first = reinterpret_cast<int2*>(tmem_slot + 4);   // of each expert, and behind the last one: item_at's
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)cluster_rank() : 0;
@@ -295,30 +305,45 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), TMEM_COLS);
+  if (warp == 3 && lane == 0) {
+    prefetch_map(&tmW);
+    prefetch_map(&tmX);
+    prefetch_map(&tmO);
+  }
   pdl_wait();
   pdl_trigger();
-  if (warp == 2) {   // token tiles before each expert
+  if (warp == 2) {   // token tiles and rows before each expert, four experts a lane
     int run = 0;
-    for (int b = 0; b < a.E; b += 32) {
-      const int e = b + lane;
-      const int c = e < a.E ? (max(row_at(a, e + 1) - row_at(a, e), 0) + 128 * CG - 1) / (128 * CG) : 0;
-      int x = c;
+    for (int b = 4 * lane; b < a.E + 1 + 4 * lane; b += 128) {
+      int row[5], tiles[4], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) row[i] = b + i <= a.E ? row_at(a, b + i) : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        tiles[i] = b + i < a.E ? (max(row[i + 1] - row[i], 0) + 128 * CG - 1) / (128 * CG) : 0;
+        sum += tiles[i];
+      }
+      int x = sum;
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += v;
       }
-      // offsets that do not ascend could make more tiles than the rows do
-      if (e < a.E) first[e] = min(run + x - c, a.most_tiles);
+      int before = run + x - sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // offsets that do not ascend could make more tiles than the rows do
+        if (b + i <= a.E) first[b + i] = make_int2(min(before, a.most_tiles), row[i]);
+        before += tiles[i];
+      }
       run = min(run + __shfl_sync(0xffffffffu, x, 31), a.most_tiles);
     }
-    if (lane == 0) first[a.E] = run;
   }
   fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int total = first[a.E] * a.m_blocks;
+  const int total = first[a.E].x * a.m_blocks;
   // Every so many-th item; with few rows an expert, runs of items, mostly weight blocks of one token tile (as in grouped.cu)
   const int units = gridDim.x / CG, unit = blockIdx.x / CG, share = total / units, more = total % units;
   const bool runs = CG == 1 && a.few;
@@ -624,7 +649,7 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   a.box = std::min(32, x_rows & -x_rows);
   a.stage_bytes = (TILE / CG + x_rows) * 128;
   // behind the last stage as much as the products read past its token rows
-  const int fixed = 1024 + std::max(EW * epi_warp<CG>() + SCALE_SLOTS * SLOT * 4 + HEADS * 16 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 16 * MAX_ACCS + 32 + 16 + 4 * (a.E + 1), (128 - x_rows) * 128);
+  const int fixed = 1024 + std::max(EW * epi_warp<CG>() + SCALE_SLOTS * SLOT * 4 + HEADS * 16 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 16 * MAX_ACCS + 32 + 16 + 8 * (a.E + 1), (128 - x_rows) * 128);
   a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 
