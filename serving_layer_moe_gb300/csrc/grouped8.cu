@@ -22,9 +22,10 @@
 //
 // A CTA (CG = 1) takes up to 128 tokens of one expert, a pair (CG = 2) up to 256, by TILE weight rows.
 // Persistent kernel, one CTA per SM:
-//   warp 0      TMA: weight tiles, into a ring of K slices of 128 bytes a row
-//   warp 1      one lane issues tcgen05.mma kind::f8f6f4
-//   warp 2      TMA: token tiles, the rows there are; the products of the rows behind them are not looked at
+//   warp 0      TMA: weight tiles, and the token rows there are (the products of the rows behind them are not looked at), into a ring of
+//               K slices of 128 bytes a row
+//   warps 1-2   one lane each issues tcgen05.mma kind::f8f6f4, for every other slice: waiting for a slice and issuing it takes 500 to
+//               650 cycles, more than the products of a small tile
 //   warp 3      scales, some slices ahead, into a ring of groups of slices
 //   warps 4-11  sums and epilogue: a quarter of the lanes, half of the columns each
 //
@@ -181,7 +182,7 @@ __device__ __forceinline__ void pack64(const uint64_t (&v)[CHUNKS][8], int c, bo
       const float2 p = unpack2(v[c * STEP][i >> 1]);
       w[i] = __float_as_uint(i & 1 ? p.y : p.x);
     } else {
-      const float2 p = unpack2(v[(c + (i >> 3)) * STEP][i & 7]);
+      const float2 p = (c + (i >> 3)) * STEP < CHUNKS ? unpack2(v[(c + (i >> 3)) * STEP < CHUNKS ? (c + (i >> 3)) * STEP : 0][i & 7]) : make_float2(0.0f, 0.0f);
       w[i] = pack_bf16(p.x, p.y);
     }
   }
@@ -189,11 +190,11 @@ __device__ __forceinline__ void pack64(const uint64_t (&v)[CHUNKS][8], int c, bo
 // The results of a warp's 32 tokens, from `token` on: every STEP-th of CHUNKS chunks of 16 columns, from column f on
 template <int CG, int CHUNKS, int STEP, bool F32>
 __device__ __forceinline__ void put_results(const Args8& a, const CUtensorMap& map, uint8_t* buf, const uint64_t (&v)[CHUNKS][8], int token, int rows, int f) {
-  constexpr int SIZE = F32 ? 4 : 2, ONE = F32 ? 1 : 2, PIECES = CHUNKS / STEP / ONE;   // pieces of 64 bytes
+  constexpr int SIZE = F32 ? 4 : 2, ONE = F32 ? 1 : 2, PIECES = (CHUNKS / STEP + ONE - 1) / ONE;   // pieces of 64 bytes
   const int lane = threadIdx.x & 31;
   const size_t stride = (size_t)a.cols * SIZE;
   uint8_t* const out = static_cast<uint8_t*>(a.out) + (size_t)token * stride + (size_t)f * SIZE;
-  const int bytes = (a.cols - f) * SIZE;   // of a row from column f on
+  const int bytes = min(a.cols - f, CHUNKS / STEP * 16) * SIZE;   // of a row from column f on
   if constexpr (CG == 2) {
     if (a.whole) {
 #pragma unroll
@@ -356,7 +357,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
     bool ok = true;
     if (warp == 0) {
-      // ---------------- weights ----------------
+      // ---------------- loads ----------------
       int stage = 0;
       uint32_t phase = 0;
       constexpr int boxes = (TILE / CG + 127) / 128;
@@ -364,16 +365,18 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         item_at<CG>(a, first, it, o);
         uint32_t bytes = (uint32_t)(CG * w_bytes);
         for (int r = 0; r < CG; ++r) bytes += 128u * rows_loaded(a, rows_of<CG>(a, o, r));
+        const int row0 = o.row0 + rows_from<CG>(a, o, rank), rows = rows_of<CG>(a, o, rank);
         for (int ks = 0; ks < a.kslices; ++ks) {
           if (!warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
           if (elect_one()) {
-            const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
+            const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage, to = ring + stage * a.stage_bytes;
             if (rank == 0) mbar_expect(full + 8 * stage, bytes);
             // rows of one expert (dimensions K, row, expert), or with SwiGLU (K, 16 rows, gate / up, block of 16, expert)
             for (int b = 0; b < boxes; ++b) {
               const int row = o.mb * TILE + rank * (TILE / CG) + 128 * b;
-              tma_5d<CG>(&tmW, bar, ring + stage * a.stage_bytes + b * 128 * 128, ks * 128, a.act ? 0 : row, 0, a.act ? row >> 5 : 0, o.e);
+              tma_5d<CG>(&tmW, bar, to + b * 128 * 128, ks * 128, a.act ? 0 : row, 0, a.act ? row >> 5 : 0, o.e);
             }
+            for (int r = 0; r < rows; r += a.box) tma_2d<CG>(&tmX, bar, to + w_bytes + r * 128, ks * 128, row0 + r);
           }
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
@@ -390,59 +393,41 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag);
         if (++stage == a.stages) { stage = 0; phase ^= 1u; }
       }
-    } else if (warp == 1) {
-      // ---------------- products ----------------
+    } else if (warp < 3) {
+      // ---------------- products: every other slice ----------------
       if (rank == 0) {
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 1, at = 0;
+        const int p = warp - 1, items = it0 < it1 ? (it1 - it0 + step - 1) / step : 0, slices = items * a.kslices;
+        int stage = p, acc = p, ks = p;
+        uint32_t phase = 0, acc_phase = 1;
         const uint32_t lw = desc_low(ring), lx = desc_low(ring + w_bytes);
-        const uint32_t stage_step = (uint32_t)a.stage_bytes >> 4;
         const int whole = a.K >> 7, rest = a.K & 127;
         // D fp32; e4m3 operands, both K-major; N = TILE; M = 128 CG
         constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(TILE >> 3) << 17) | ((uint32_t)(8 * CG) << 24);
-        for (int it = it0; it < it1 && ok; it += step) {
-          for (int ks = 0; ks < a.kslices; ++ks) {
-            // The other CTA's arrivals on tempty stand for its TMEM reads, which the fences order; no memory is handed over.
-            if (!test_both(full + 8 * stage, phase, tempty + 8 * acc, acc_phase) &&
-                (!warp_wait(full + 8 * stage, phase, abort_flag) || !warp_wait(tempty + 8 * acc, acc_phase, abort_flag))) { ok = false; break; }
-            fence_after();
-            const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
-            if (elect_one()) {
-              if (ks < whole) {
+        for (int g = p; g < slices; g += 2) {
+          while (ks >= a.kslices) ks -= a.kslices;   // of its item
+          const uint32_t at = (uint32_t)(stage * a.stage_bytes) >> 4;
+          // The other CTA's arrivals on tempty stand for its TMEM reads, which the fences order; no memory is handed over.
+          if (!test_both(full + 8 * stage, phase, tempty + 8 * acc, acc_phase) &&
+              (!warp_wait(full + 8 * stage, phase, abort_flag) || !warp_wait(tempty + 8 * acc, acc_phase, abort_flag))) { ok = false; break; }
+          fence_after();
+          const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
+          if (elect_one()) {
+            if (ks < whole) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_f8<CG>(d, desc_of(lx + at + 2 * kk), desc_of(lw + at + 2 * kk), idesc, (uint32_t)kk);
-              } else {
-                for (int kk = 0; kk * 32 < rest; ++kk) mma_f8<CG>(d, desc_of(lx + at + 2 * kk), desc_of(lw + at + 2 * kk), idesc, (uint32_t)kk);
-              }
-              commit<CG>(tfull + 8 * acc);
-              commit<CG>(empty + 8 * stage);
+              for (int kk = 0; kk < 4; ++kk) mma_f8<CG>(d, desc_of(lx + at + 2 * kk), desc_of(lw + at + 2 * kk), idesc, (uint32_t)kk);
+            } else {
+              for (int kk = 0; kk * 32 < rest; ++kk) mma_f8<CG>(d, desc_of(lx + at + 2 * kk), desc_of(lw + at + 2 * kk), idesc, (uint32_t)kk);
             }
-            __syncwarp();
-            at += stage_step;
-            if (++stage == a.stages) { stage = 0; phase ^= 1u; at = 0; }
-            if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
+            commit<CG>(tfull + 8 * acc);
+            commit<CG>(empty + 8 * stage);
           }
+          __syncwarp();
+          ks += 2;
+          if ((stage += 2) >= a.stages) { stage -= a.stages; phase ^= 1u; }
+          if ((acc += 2) >= ACCS) { acc -= ACCS; acc_phase ^= 1u; }
         }
         if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
       }
-    } else if (warp == 2) {
-      // ---------------- tokens ----------------
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int it = it0; it < it1 && ok; it += step) {
-        item_at<CG>(a, first, it, o);
-        const int row0 = o.row0 + rows_from<CG>(a, o, rank), rows = rows_of<CG>(a, o, rank);
-        for (int ks = 0; ks < a.kslices; ++ks) {
-          if (!warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag)) { ok = false; break; }
-          if (elect_one()) {
-            const uint32_t sb = ring + stage * a.stage_bytes + w_bytes;
-            const uint32_t bar = CG == 2 ? in_rank(full + 8 * stage, 0) : full + 8 * stage;
-            for (int r = 0; r < rows; r += a.box) tma_2d<CG>(&tmX, bar, sb + r * 128, ks * 128, row0 + r);
-          }
-          if (++stage == a.stages) { stage = 0; phase ^= 1u; }
-        }
-      }
-      if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
     } else {
       // ---------------- scales ----------------
       int slot = 0, head = 0;
@@ -741,8 +726,8 @@ bool use_pairs8(const Args8& a) { return a.P > (int64_t)(a.act ? a.K >= 4096 ? 7
 // N 7168 10.8 / 9.0 / 11.5; one row of 8 experts, K 768, N 2048 7.4 / 6.8 / 7.8.
 int tile8(const Args8& a, int64_t tiles) {
   if (a.quant) return 256;   // a block of 128 features is one tile's
-  int tile = 256;   // SwiGLU: a warp stores 32 features at least
-  while (tile > (a.act ? 128 : 64) && tiles * ((a.N + tile - 1) / tile) < operator_sms() / 2) tile /= 2;
+  int tile = 256;
+  while (tile > 64 && tiles * ((a.N + tile - 1) / tile) < operator_sms() / 2) tile /= 2;
   return tile;
 }
 
