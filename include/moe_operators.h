@@ -175,8 +175,8 @@ moe_status moe_combine(int32_t T, int32_t k, int32_t N, int32_t y_dtype, const v
  * infinity has the scale NaN and codes 0.  K a multiple of 16; a block past K's end is short.
  *   rows     [R, K]: blocks of 128 elements of a row, scales [ceil(K / 128), R] (the scales of one
  *            block of all rows together, as a product takes them)
- *   weights  [G, N, K]: blocks of 128 x 128, scales [G, ceil(N / 128), ceil(K / 128)], as MOE_FP8 experts
- *            and checkpoints have them
+ *   weights  [G, N, K]: blocks of 128 x 128, scales [G, ceil(N / 128), ceil(K / 128)], as MOE_FP8E4M3_B128
+ *            experts and checkpoints have them
  * x in dtype MOE_BF16 or MOE_F32.  moe_quantize_fp8: x [T, K]; place NULL (k = 1): row t of the output is row
  * t of x; otherwise row t becomes the rows place[t, 0 .. k - 1] of T * k, none where that is not a
  * row.  Rows that no pair fills, and their scales, are left as they are.
@@ -194,7 +194,8 @@ moe_status moe_dequantize_fp8(int32_t G, int32_t N, int32_t K, int32_t tiles, co
  * Products of 8-bit rows and weights: out[i] = x[i] * w[e]^T for the rows i of each expert e, rows in expert order
  * as offsets [E + 1] has them; offsets NULL (E = 1): all P rows are one matrix's.  K a multiple of 16.
  *   The products of one block of K are summed in the tensor cores' fp32 accumulators (four additions), multiplied by
- *   the fp32 product of both scales, and added up over K in fp32.
+ *   the fp32 product of both scales, and added up over K in fp32, block after block: a row's result does not depend on
+ *   the rows beside it.
  *   act 1: SwiGLU; w holds N/2 gate rows, then N/2 up rows (N a multiple of 128).
  *   out [P, N or N/2] in out_dtype (MOE_BF16 or MOE_F32); rows from offsets[E] on are left as they are.  silu of fp32
  *   results is within 11 half units, of others within |gate| + 10 units or 1e-18 of the gate.

@@ -462,3 +462,27 @@ def test_no_tokens(moe, E):
     else:
         h, z = moe.residual_norm(x, x, pre=one)
     assert h.shape == z.shape == moe.rms_norm(x, one).shape == (0, 256)
+
+
+@pytest.mark.parametrize("act,quant", [("none", False), ("swiglu", False), ("swiglu", True)])
+def test_a_rows_result_does_not_depend_on_the_rows_beside_it(moe, act, quant):
+    """The same row alone, in small calls and in large ones, whose tiles differ."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    K, N = 1040, 512
+    x, w = torch.randn(3000, K, generator=gen, device="cuda").bfloat16(), moe.quantize_fp8_weights(torch.randn(N, K, generator=gen, device="cuda").bfloat16())
+
+    def rows(n):
+        r = moe.matmul_fp8(moe.quantize_fp8(x[:n]), w, act=act, quantize=quant)
+        return r.codes.view(torch.uint8) if quant else r
+    want = rows(3000)
+    for n in (1, 16, 40, 128, 129, 700):
+        assert torch.equal(rows(n), want[:n]), n
+
+
+def test_the_example_runs(moe):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import routed_layer
+    r = routed_layer.run(tokens=300, hidden=512, inter=256, experts=16, top_k=4, fmt="fp8")
+    assert np.isfinite(r["distance"]) and r["chunk_ms"] > 0 and r["token_ms"] > 0
