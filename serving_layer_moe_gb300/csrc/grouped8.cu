@@ -52,6 +52,13 @@ constexpr int MAX_STAGES = 12;
 // short, it is the way from one to the other and back that counts.
 template <int TILE> constexpr int accs() { return TILE == 256 ? 2 : 4; }
 constexpr int TMEM_COLS = 512, MAX_ACCS = 4;
+// Stages, of `room` that fit.  Two warps issue alternate slices, so an odd number makes them share each stage, and a warp may test slice g's
+// data while its stage's use before that, the other warp's slice g - stages, has not landed: by parity, that looks like data that has.  With
+// ACCS + 2 stages it has landed: the warp is done with slice g - 2, so the sums with g - 2 - ACCS.  With fewer each warp keeps its own stages.
+template <int TILE> int stages_of(int room) {
+  const int n = std::min(MAX_STAGES, room);
+  return n >= accs<TILE>() + 2 ? n : n & ~1;
+}
 constexpr int GROUP = 4;                       // slices whose scales go together, a multiple of the accumulators
 constexpr int SLOT = GROUP * 128 + 4 * GROUP;  // a group's scales: [slice][token of the CTA], then [half of the columns][even, odd 16 columns][slice]
 constexpr int SCALE_SLOTS = 3;
@@ -252,7 +259,8 @@ __device__ __forceinline__ void put_results(const Args8& a, const CUtensorMap& m
 // desc_sw128 in two halves: what an address adds is in the lower one
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return (uint32_t)desc_sw128(addr); }
 __device__ __forceinline__ uint64_t desc_of(uint32_t low) { return (desc_sw128(0) & 0xffffffff00000000ull) | low; }
-// whether both phases are over, for the whole warp; the second test is on its way during the first
+// whether both phases are over, for the whole warp.  Both tests are on their way at once, and each may be held until its phase ends: an outcome
+// can be older than the other one's (stages_of).
 __device__ __forceinline__ bool test_both(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {
   uint32_t ok;
   asm volatile(
@@ -381,17 +389,17 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
           if (++stage == a.stages) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) {
-        if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
-        // copies in flight land long before this bound
-        const unsigned long long t0 = gtimer();
-        while (gtimer() - t0 < 1000000ull) {
-        }
-      }
       // every slice has been used, and no arrival on this CTA's barriers is outstanding, before it ends
       for (int i = 0; i < a.stages && ok; ++i) {
         ok = warp_wait(empty + 8 * stage, phase ^ 1u, abort_flag);
         if (++stage == a.stages) { stage = 0; phase ^= 1u; }
+      }
+      if (!ok) {
+        if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
+        // copies and products in flight end long before this bound
+        const unsigned long long t0 = gtimer();
+        while (gtimer() - t0 < 1000000ull) {
+        }
       }
     } else if (warp < 3) {
       // ---------------- products: every other slice ----------------
@@ -635,7 +643,7 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   a.stage_bytes = (TILE / CG + x_rows) * 128;
   // behind the last stage as much as the products read past its token rows
   const int fixed = 1024 + std::max(EW * epi_warp<CG>() + SCALE_SLOTS * SLOT * 4 + HEADS * 16 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 16 * MAX_ACCS + 32 + 16 + 8 * (a.E + 1), (128 - x_rows) * 128);
-  a.stages = std::min(MAX_STAGES, (SMEM_LIMIT - fixed) / a.stage_bytes);
+  a.stages = stages_of<TILE>((SMEM_LIMIT - fixed) / a.stage_bytes);
   const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
 
   CUtensorMap tw, tx, to;

@@ -42,6 +42,26 @@ def test_many_experts(moe, E, most, N, K):
     moe.check_operators()
 
 
+@pytest.mark.parametrize("E,counts,N,K", [(1500, [1] * 60 + [0] * 1380 + [3] * 60, 512, 2048), (4096, [0] * 4040 + [2] * 56, 256, 1040), (1500, [0] * 1492 + [300] * 8, 640, 1936)])
+def test_many_experts_and_many_slices(moe, E, counts, N, K):
+    """The experts' table leaves room for three stages, an odd number, for two warps, and the weights come from memory."""
+    rng = np.random.default_rng(E + N)
+    gr, (offsets, _, _, _), P, E, _ = grouping(moe, rng, counts)
+    used = np.array(counts) > 0
+    xc, xs, few, scales = whole(rng, P, int(used.sum()), N, K)
+    xs = xs / 8
+    y = product(xc, xs, few, scales, np.concatenate([[0], np.cumsum(np.array(counts)[used])]))
+    wc, ws = np.zeros((E, *few.shape[1:]), few.dtype), np.ones((E, *scales.shape[1:]), scales.dtype)
+    wc[used], ws[used] = few, scales
+    x, w = operands(moe, xc, xs, wc, ws)
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(8):
+        big.zero_()   # the weights are in memory, not in the cache
+        assert np.array_equal(host(moe.grouped_matmul_fp8(x, w, gr, out_dtype=torch.float32)), y)
+    check_quantized(moe.grouped_matmul_fp8(x, w, gr, act="swiglu", quantize=True), y.astype(np.float64))
+    moe.check_operators()
+
+
 @pytest.mark.parametrize("N", [7, 24, 130, 136, 257, 1000])
 @pytest.mark.parametrize("counts", [[900, 1], [5, 0, 31]])
 def test_widths_of_results(moe, N, counts):
