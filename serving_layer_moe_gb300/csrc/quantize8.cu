@@ -144,23 +144,46 @@ __global__ void __launch_bounds__(Q_THREADS) dequantize8_kernel(const uint8_t* _
                                                                 int64_t rows, int K, O* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  const int units = K / 16, c = (int)blockIdx.y * Q_SEG + (threadIdx.x & 31);
   const int64_t g = blockIdx.z;
-  if (c >= units) return;
-  for (int64_t r = (int64_t)blockIdx.x * Q_WARPS + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * Q_WARPS) {
-    const size_t at = (size_t)(g * rows + r) * K + c * 16;
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(codes + at));
-    const float s = __ldg(scales + g * sc.per + r / sc.high * sc.rs + (c >> 3) * sc.bs);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    O res[16];
+  if constexpr (sizeof(O) == 4) {
+    // four elements of each of four blocks a lane, so that a store's 512 bytes are in one place (32 x 4096 x 2000: 267 us with 16 in a row, now 195)
+    const int e0 = (int)blockIdx.y * (Q_SEG * 16) + 4 * (threadIdx.x & 31);
+    for (int64_t r = (int64_t)blockIdx.x * Q_WARPS + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * Q_WARPS) {
+      const size_t at = (size_t)(g * rows + r) * K + e0;
+      const float* sp = scales + g * sc.per + r / sc.high * sc.rs + (e0 >> 7) * sc.bs;
+      uint32_t w[4];
+      float s[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 x = e4m3x2_values((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-      res[2 * i] = (O)(x.x * s);
-      res[2 * i + 1] = (O)(x.y * s);
+      for (int i = 0; i < 4; ++i)
+        if (e0 + 128 * i < K) {
+          w[i] = __ldg(reinterpret_cast<const uint32_t*>(codes + at + 128 * i));
+          s[i] = __ldg(sp + i * sc.bs);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (e0 + 128 * i < K) {
+          const float2 x = e4m3x2_values(w[i] & 0xffffu), y = e4m3x2_values(w[i] >> 16);
+          *reinterpret_cast<float4*>(out + at + 128 * i) = make_float4(x.x * s[i], x.y * s[i], y.x * s[i], y.y * s[i]);
+        }
     }
+  } else {
+    const int units = K / 16, c = (int)blockIdx.y * Q_SEG + (threadIdx.x & 31);
+    if (c >= units) return;
+    for (int64_t r = (int64_t)blockIdx.x * Q_WARPS + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * Q_WARPS) {
+      const size_t at = (size_t)(g * rows + r) * K + c * 16;
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(codes + at));
+      const float s = __ldg(scales + g * sc.per + r / sc.high * sc.rs + (c >> 3) * sc.bs);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      O res[16];
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(O); ++i) reinterpret_cast<uint4*>(out + at)[i] = reinterpret_cast<const uint4*>(res)[i];
+      for (int i = 0; i < 8; ++i) {
+        const float2 x = e4m3x2_values((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+        res[2 * i] = (O)(x.x * s);
+        res[2 * i + 1] = (O)(x.y * s);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(out + at)[i] = reinterpret_cast<const uint4*>(res)[i];
+    }
   }
 }
 
