@@ -13,12 +13,13 @@
 // a slice of 128 tokens x 256 features) and the additions (256 more, beside them), under the 512 of the
 // slice's products.  With the features as lanes the columns' scales come from shared memory: 660 cycles with
 // broadcast loads, more with 16x256b loads, which read TMEM at half the rate (709 us for 16384 rows of 8
-// experts, K 7168, N 4096; now 338, 2.85 PFLOP/s, and 301 with nothing added up).  What it costs: a ragged tile of tokens takes a
+// experts, K 7168, N 4096; now 317, 3.0 PFLOP/s, and 301 with nothing added up).  What it costs: a ragged tile of tokens takes a
 // whole one's products.
 //
 // What an epilogue warp does once a slice counts as much: two warps a scheduler hide little of it.  Scales come for four slices at a
 // time (a barrier of their own a slice: 500 us), arrivals are elected without a branch and both accumulators' addresses and
-// phases are registers (410), the warp's number is uniform to the compiler and scales stay single registers until used (338).
+// phases are registers (410), the warp's number is uniform to the compiler and scales stay single registers until used (338); the second
+// issuing warp took it to 317.
 //
 // A CTA (CG = 1) takes up to 128 tokens of one expert, a pair (CG = 2) up to 256, by TILE weight rows.
 // Persistent kernel, one CTA per SM:

@@ -405,6 +405,9 @@ moe_status run_end(const EndArgs& a, bool wide, cudaStream_t s) {
   if (wide) {
     if (a.T >= 2 * operator_sms() && (!a.place || a.k <= 30)) {   // a lane a row
       if constexpr (sizeof(Y) + sizeof(R) == 4) {
+        // with few rows a token three weights a channel, read each time, hold it up: us, kept in registers / read, 8192 dense rows of 7168
+        // with all parts 107 / 118, 16384 of 2048 54 / 63; without post 86 / 79 and 43 / 45; 8192 tokens of 2 rows, N 7168 142 / 108
+        if (!a.place && a.post && units <= 1024) return launch_stream<Y, R, 2, 3, true, 512, 1>(a, threads(2), s);
         if (units <= 512) return launch_stream<Y, R, 2, 3, false, 256, 4>(a, threads(2), s);
         if (units <= 1024) return launch_stream<Y, R, 2, 3, false, 512, 2>(a, threads(2), s);
       } else {

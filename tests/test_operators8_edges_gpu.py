@@ -133,6 +133,22 @@ def test_combine_norm_on_both_sides_of_its_forms(moe, T, k, N):
                 end_within(host(gz), z, mz + np.abs(z), k, N, torch.float32, 2)
 
 
+@pytest.mark.parametrize("T,N", [(304, 8), (310, 2056), (350, 7168), (306, 8192), (303, 2048)])
+def test_many_dense_rows(moe, T, N):
+    """A row a token, as many tokens as the form for many of them takes and one fewer, with and without each part."""
+    rng = np.random.default_rng(T + N)
+    r = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+    y, res, post, pre, gate, gate_t = bf16(r(T, N)), bf16(r(T, N)), 1 + r(N) / 8, bf16(1 + r(N) / 8), r(N), r(T, 1)
+    for yt, rt in ((torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32)):
+        for kw in (dict(post=post, gate=gate, pre=pre), dict(post=post, gate=gate_t, pre=pre), dict(post=post), dict(post=pre, pre=post), dict(gate=gate, pre=pre)):
+            h, z, mh, mz = ref8.block_end(y, None, None, res, scale=0.5, **kw)
+            got = moe.residual_norm(dev(y, yt), dev(res, rt), residual_scale=0.5, out_dtype=torch.float32, **{n: dev(v, torch.bfloat16 if v is pre else None) for n, v in kw.items()})
+            gh, gz = got if z is not None else (got, None)
+            end_within(host(gh), h, mh, 1, N, rt, "post" in kw)
+            if z is not None:
+                end_within(host(gz), z, mz + np.abs(z), 1, N, torch.float32, 2)
+
+
 def test_the_stream_may_be_updated_in_place(moe):
     """The C call's h is the residual itself: rows of other tokens are read before or after, never half way."""
     from serving_layer_moe_gb300.operators import _operators
