@@ -5,7 +5,7 @@
 //   c = sum_j w[j] y[place[j]] + shared;   c = c / sqrt(mean c^2 + eps) * post;   c = gate c
 //   h = alpha r + c;                       z = h / sqrt(mean h^2 + eps) * pre
 //
-// A block of threads holds a token's row in fp32 registers from the first load to the last
+// A block of threads holds a token's row in fp32, in registers or shared memory, from the first load to the last
 // store, so each row is read and written once.  The two means are the only points where its
 // threads wait for one another; other blocks' loads fill that time.  Bound by memory.
 #include "operators.cuh"
@@ -29,7 +29,7 @@ struct EndArgs {
   void *h, *z;                                      // either may be NULL
 };
 
-// U consecutive values (8, 16-byte aligned, or 1) as they are, so that many can be on their way, and as fp32
+// U consecutive values (8, 16-byte aligned) as they are, so that many can be on their way, and as fp32
 template <int U, typename X>
 struct Raw {
   static constexpr int Q = U * (int)sizeof(X) / 16;
@@ -58,12 +58,6 @@ struct Raw {
     }
   }
 };
-template <typename X>
-struct Raw<1, X> {
-  X x;
-  __device__ __forceinline__ void load(const X* p) { x = *p; }
-  __device__ __forceinline__ void values(float (&v)[1]) const { v[0] = (float)x; }
-};
 template <int U, typename X>
 __device__ __forceinline__ void load(const X* p, float (&v)[U]) {
   Raw<U, X> r;
@@ -78,9 +72,7 @@ __device__ __forceinline__ void load_any(const void* p, int bf16, size_t at, flo
 }
 template <int U, typename X>
 __device__ __forceinline__ void store(X* p, const float (&v)[U]) {
-  if constexpr (U == 1) {
-    *p = (X)v[0];
-  } else if constexpr (sizeof(X) == 2) {
+  if constexpr (sizeof(X) == 2) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -108,9 +100,10 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
-// V units of U values a thread, unit threadIdx.x first and then every blockDim.x-th; J rows of y on their way at a time
-template <typename Y, typename R, int U, int V, int J, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) block_end_kernel(EndArgs a) {
+// V units of 8 values a thread, unit threadIdx.x first and then every blockDim.x-th; J rows of y on their way at a time
+template <typename Y, typename R, int V, int J>
+__global__ void __launch_bounds__(1024, 1) block_end_kernel(EndArgs a) {
+  constexpr int U = 8;
   __shared__ float parts[2][32];
   pdl_wait();
   pdl_trigger();
@@ -128,6 +121,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_end_kernel(EndArgs a) {
         if (u < units) f(v, (size_t)u * U);
       }
     };
+    // Rows are loaded without a test of the width, so that a row's loads do not wait for one another: behind it, its last unit again.
+    // us of 250 tokens, N 7168, 8 rows each and all parts 12.4 with the test, 10.3 without.
+    auto place_of = [&](int v) { return (size_t)min((int)(threadIdx.x + v * blockDim.x), units - 1) * U; };
     if (y) {
       const int k = a.place ? a.k : 1, P = a.T * k;
       for (int j0 = 0; j0 < k; j0 += J) {
@@ -137,38 +133,47 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_end_kernel(EndArgs a) {
         for (int j = 0; j < J; ++j) {
           const bool there = j0 + j < k;
           row[j] = !there ? -1 : a.place ? __ldg(a.place + (size_t)t * k + j0 + j) : t;
+          if ((unsigned)row[j] >= (unsigned)P) row[j] = -1;
           w[j] = there && a.place ? __ldg(a.w + (size_t)t * k + j0 + j) : 1.0f;
         }
-        each([&](int v, size_t at) {
-          Raw<U, Y> x[J];
+        Raw<U, Y> x[J][V];
 #pragma unroll
-          for (int j = 0; j < J; ++j)
-            if ((unsigned)row[j] < (unsigned)P) x[j].load(y + (size_t)row[j] * a.N + at);
+        for (int j = 0; j < J; ++j)
+          if (row[j] >= 0)
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            if ((unsigned)row[j] >= (unsigned)P) continue;
-            float f[U];
-            x[j].values(f);
+            for (int v = 0; v < V; ++v) x[j][v].load(y + (size_t)row[j] * a.N + place_of(v));
 #pragma unroll
-            for (int i = 0; i < U; ++i) c[v][i] = fmaf(w[j], f[i], c[v][i]);
-          }
-        });
+        for (int j = 0; j < J; ++j)
+          if (row[j] >= 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              float f[U];
+              x[j][v].values(f);
+#pragma unroll
+              for (int i = 0; i < U; ++i) c[v][i] = fmaf(w[j], f[i], c[v][i]);
+            }
       }
-      if (shared)
-        each([&](int v, size_t at) {
-          float x[U];
-          load(shared + (size_t)t * a.N + at, x);
+      if (shared) {
+        Raw<U, Y> x[V];
 #pragma unroll
-          for (int i = 0; i < U; ++i) c[v][i] += x[i];
-        });
+        for (int v = 0; v < V; ++v) x[v].load(shared + (size_t)t * a.N + place_of(v));
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float f[U];
+          x[v].values(f);
+#pragma unroll
+          for (int i = 0; i < U; ++i) c[v][i] += f[i];
+        }
+      }
     }
-    each([&](int v, size_t at) { r[v].load(residual + (size_t)t * a.N + at); });   // on its way during the first mean
+#pragma unroll
+    for (int v = 0; v < V; ++v) r[v].load(residual + (size_t)t * a.N + place_of(v));   // on its way during the first mean
     if (a.post) {
       float s = 0.0f;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
+      each([&](int v, size_t) {
 #pragma unroll
         for (int i = 0; i < U; ++i) s = fmaf(c[v][i], c[v][i], s);
+      });
       const float inv = rsqrtf(fmaf(block_sum(s, parts[0]), per, a.eps));
       each([&](int v, size_t at) {
         float x[U];
@@ -207,6 +212,120 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) block_end_kernel(EndArgs a) {
         at += (size_t)t * a.N;
         if (a.z_bf16) store(static_cast<__nv_bfloat16*>(a.z) + at, x);
         else store(static_cast<float*>(a.z) + at, x);
+      });
+    }
+    __syncthreads();   // the parts have been read
+  }
+}
+
+// Any width: single values, which start anywhere.  The row is in shared memory as fp32, each value its thread's own, so that a thread needs
+// few registers, none of them for values it has yet to use, and has W loads on their way.  us with the row in registers / so: 4096 tokens, N
+// 1001, 2 rows each and all parts 26 / 23; 2000 tokens, N 8191 150 / 105 (bound 29); 1000 tokens, N 16383 414 / 108; one token, N 8191 15 / 13.
+// Four values of two rows at a time 25, 107, 112 and 14, eight of two rows 39, 158, 164 and 18 (spilled).
+constexpr int ANY_THREADS = 512, ANY_VALUES = 8;
+template <typename Y, typename R>
+__global__ void __launch_bounds__(ANY_THREADS, 2) block_end_any_kernel(EndArgs a) {
+  constexpr int W = ANY_VALUES;
+  extern __shared__ float c_row[];
+  __shared__ float parts[2][32];
+  pdl_wait();
+  pdl_trigger();
+  const Y *y = static_cast<const Y*>(a.y), *shared = static_cast<const Y*>(a.shared);
+  const R* residual = static_cast<const R*>(a.residual);
+  const float per = 1.0f / (float)a.N;
+  const int k = a.place ? a.k : 1, P = a.T * k, stride = blockDim.x;
+  // f(values' places, of which the thread's i-th is there if there[i]; behind the row's end they are its last one)
+  auto each = [&](auto f) {
+    for (int u0 = threadIdx.x; u0 < a.N; u0 += W * stride) {
+      int at[W];
+      bool there[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        there[i] = u0 + i * stride < a.N;
+        at[i] = min(u0 + i * stride, a.N - 1);
+      }
+      f(at, there);
+    }
+  };
+  auto weights = [&](const void* p, int bf16, const int (&at)[W], float (&x)[W]) {
+    if (bf16)
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = (float)static_cast<const __nv_bfloat16*>(p)[at[i]];
+    else
+#pragma unroll
+      for (int i = 0; i < W; ++i) x[i] = static_cast<const float*>(p)[at[i]];
+  };
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const size_t row0 = (size_t)t * a.N;
+    float s = 0.0f;
+    if (y)
+      each([&](const int (&at)[W], const bool (&there)[W]) {
+        float c[W] = {};
+        for (int j = 0; j < k; ++j) {
+          const int row = a.place ? __ldg(a.place + (size_t)t * k + j) : t;
+          if ((unsigned)row >= (unsigned)P) continue;
+          const float w = a.place ? __ldg(a.w + (size_t)t * k + j) : 1.0f;
+          Y x[W];
+#pragma unroll
+          for (int i = 0; i < W; ++i) x[i] = y[(size_t)row * a.N + at[i]];
+#pragma unroll
+          for (int i = 0; i < W; ++i) c[i] = fmaf(w, (float)x[i], c[i]);
+        }
+        if (shared) {
+          Y x[W];
+#pragma unroll
+          for (int i = 0; i < W; ++i) x[i] = shared[row0 + at[i]];
+#pragma unroll
+          for (int i = 0; i < W; ++i) c[i] += (float)x[i];
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (there[i]) {
+            c_row[at[i]] = c[i];
+            s = fmaf(c[i], c[i], s);
+          }
+      });
+    const float inv_post = a.post ? rsqrtf(fmaf(block_sum(s, parts[0]), per, a.eps)) : 1.0f, token_gate = a.gate && a.gate_rows ? __ldg(a.gate + t) : 1.0f;
+    s = 0.0f;
+    each([&](const int (&at)[W], const bool (&there)[W]) {
+      R r[W];
+      float c[W] = {}, x[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) r[i] = residual[row0 + at[i]];
+      if (y)
+#pragma unroll
+        for (int i = 0; i < W; ++i) c[i] = there[i] ? c_row[at[i]] : 0.0f;
+      if (a.post) {
+        weights(a.post, a.post_bf16, at, x);
+#pragma unroll
+        for (int i = 0; i < W; ++i) c[i] *= inv_post * x[i];
+      }
+      if (a.gate) {
+        if (!a.gate_rows) weights(a.gate, 0, at, x);
+#pragma unroll
+        for (int i = 0; i < W; ++i) c[i] *= a.gate_rows ? token_gate : x[i];
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float h = fmaf(a.alpha, (float)r[i], c[i]);
+        if (!there[i]) continue;
+        if (a.h) static_cast<R*>(a.h)[row0 + at[i]] = (R)h;
+        if (a.z) c_row[at[i]] = h;
+        s = fmaf(h, h, s);
+      }
+    });
+    if (a.z) {
+      const float inv = rsqrtf(fmaf(block_sum(s, parts[1]), per, a.eps));
+      each([&](const int (&at)[W], const bool (&there)[W]) {
+        float x[W];
+        weights(a.pre, a.pre_bf16, at, x);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (there[i]) {
+            const float z = x[i] * (inv * c_row[at[i]]);
+            if (a.z_bf16) static_cast<__nv_bfloat16*>(a.z)[row0 + at[i]] = (__nv_bfloat16)z;
+            else static_cast<float*>(a.z)[row0 + at[i]] = z;
+          }
       });
     }
     __syncthreads();   // the parts have been read
@@ -390,16 +509,36 @@ moe_status launch_stream(const EndArgs& a, int threads, cudaStream_t s) {
   return MOE_OK;
 }
 
-template <typename Y, typename R, int U, int V, int J, int THREADS, int BLOCKS>
+template <typename Y, typename R, int V, int J>
 moe_status launch_end(const EndArgs& a, int threads, cudaStream_t s) {
   const int grid = (int)std::min<int64_t>(a.T, (int64_t)operator_sms() * std::max(1, 2048 / threads));
-  CK(launch_pdl(block_end_kernel<Y, R, U, V, J, THREADS, BLOCKS>, dim3(grid), dim3(threads), 0, s, a));
+  CK(launch_pdl(block_end_kernel<Y, R, V, J>, dim3(grid), dim3(threads), 0, s, a));
+  return MOE_OK;
+}
+
+template <typename Y, typename R>
+moe_status launch_any(const EndArgs& a, cudaStream_t s) {
+  const auto kernel = block_end_any_kernel<Y, R>;
+  const int threads = std::min(ANY_THREADS, ((a.N + ANY_VALUES - 1) / ANY_VALUES + 31) / 32 * 32);
+  const size_t smem = (size_t)a.N * 4;
+  static bool allowed[64] = {};
+  int dev = 0;
+  CK(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(MOE_EINVAL, "device %d is out of range", dev);
+  if (!allowed[dev]) {
+    CK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_WIDTH * 4));
+    allowed[dev] = true;
+  }
+  int blocks = 1;
+  CK(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem));
+  const int grid = (int)std::min<int64_t>(a.T, (int64_t)operator_sms() * std::max(1, blocks));
+  CK(launch_pdl(kernel, dim3(grid), dim3(threads), smem, s, a));
   return MOE_OK;
 }
 
 template <typename Y, typename R>
 moe_status run_end(const EndArgs& a, bool wide, cudaStream_t s) {
-  const int units = wide ? a.N / 8 : a.N;
+  const int units = a.N / 8;
   auto threads = [&](int v) { return ((units + v - 1) / v + 31) / 32 * 32; };
   constexpr int H = sizeof(Y) == 2 ? 2 : 1;   // rows on their way: twice as many of half the bytes
   if (wide) {
@@ -415,13 +554,11 @@ moe_status run_end(const EndArgs& a, bool wide, cudaStream_t s) {
         if (units <= 1024) return launch_stream<Y, R, 2, 3, true, 512, 1>(a, threads(2), s);
       }
     }
-    if (units <= 1024) return launch_end<Y, R, 8, 1, 4 * H, 1024, 1>(a, threads(1), s);
-    if (units <= 2048) return launch_end<Y, R, 8, 2, H, 1024, 1>(a, threads(2), s);
-    return launch_end<Y, R, 8, 4, 1, 1024, 1>(a, threads(4), s);
+    if (units <= 1024) return launch_end<Y, R, 1, 4 * H>(a, threads(1), s);
+    if (units <= 2048) return launch_end<Y, R, 2, H>(a, threads(2), s);
+    return launch_end<Y, R, 4, 1>(a, threads(4), s);
   }
-  if (units <= 1024) return launch_end<Y, R, 1, 4, 4, 256, 4>(a, threads(4), s);
-  if (units <= 8192) return launch_end<Y, R, 1, 8, 2, 1024, 1>(a, threads(8), s);
-  return launch_end<Y, R, 1, 32, 1, 1024, 1>(a, threads(32), s);
+  return launch_any<Y, R>(a, s);
 }
 
 }  // namespace
