@@ -598,8 +598,9 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         tops_phase ^= 1u;
         turn ^= 1;
         if (!some || f0 >= a.cols) continue;
-        const float most = fmaxf(__uint_as_float(top), kLeast8);   // NaN counts as kLeast8
-        if (part == 0 && lane < rows) a.out_scales[(size_t)o.z * a.P + token + lane] = top >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : most * (1.0f / 448.0f);
+        const float most = fmaxf(__uint_as_float(top), kLeast8);
+        const bool bad = top >= 0x7f800000u;   // a NaN or an infinity: scale NaN, codes 0
+        if (part == 0 && lane < rows) a.out_scales[(size_t)o.z * a.P + token + lane] = bad ? __uint_as_float(0x7fffffffu) : most * (1.0f / 448.0f);
         float r;
         asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(most));
         r *= 448.0f;
@@ -608,7 +609,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         for (int i = 0; i < 32; ++i) {
           const float2 h = unpack2(sum[2 * (i >> 3)][i & 7]);
           const uint32_t two = to_e4m3x2(h.x * r, h.y * r);
-          w[i >> 1] = i & 1 ? w[i >> 1] | two << 16 : two;
+          w[i >> 1] = bad ? 0u : i & 1 ? w[i >> 1] | two << 16 : two;
         }
         put_rows<2>(buf, w, a.out_codes + (size_t)token * a.cols + f0, a.cols, rows, ROW, true);
       }
