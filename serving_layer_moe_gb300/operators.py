@@ -119,7 +119,7 @@ def _stream(index):
 def _again(call, index, stream):
     """Make a call that was left alone again, on its own device and stream, now that its arguments are right."""
     if stream is None and index == torch.cuda.current_device():
-        raise ValueError("the call was not made: tensors that its groups or 4-bit rows hold were resized, moved or replaced since")
+        raise ValueError("the call was not made: tensors that its arguments hold were resized, moved or replaced since")
     with _On(index, stream):
         return call()
 
@@ -585,6 +585,8 @@ def quantize_fp8(x, *, groups=None, stream=None):
         _groups_on(groups, index)
         if groups.T != T:
             raise ValueError(f"x has {T} rows, groups hold {groups.T} tokens")
+        if groups.k < 1:
+            raise ValueError("groups hold no experts a token")
     else:
         _pairs(T, 1)
     return _again(lambda: quantize_fp8(x, groups=groups), index, stream)
