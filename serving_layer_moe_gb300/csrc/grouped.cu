@@ -777,6 +777,18 @@ moe_status check_product(int32_t P, int32_t E, int32_t N, int32_t K, int32_t qua
 
 }  // namespace
 
+uint32_t* operator_flag() {
+  static uint32_t* at[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  if (!at[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_operator_err) != cudaSuccess) return nullptr;
+    at[dev] = static_cast<uint32_t*>(p);
+  }
+  return at[dev];
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -855,8 +867,7 @@ extern "C" moe_status moe_operators_check(void* stream) {
   uint32_t err = 0;
   CK(cudaMemcpyFromSymbolAsync(&err, g_operator_err, sizeof(err), 0, cudaMemcpyDeviceToHost, s));
   CK(cudaStreamSynchronize(s));
-  const moe_status st = operators_check8(s);
-  if (!err) return st;
+  if (!err) return MOE_OK;
   err = 0;
   CK(cudaMemcpyToSymbolAsync(g_operator_err, &err, sizeof(err), 0, cudaMemcpyHostToDevice, s));
   CK(cudaStreamSynchronize(s));

@@ -44,8 +44,6 @@ namespace {
 
 using namespace tc;
 
-__device__ uint32_t g_operator_err8;
-
 constexpr int FIRST_EPI = 4, EW = 8;
 constexpr int THREADS = 32 * (FIRST_EPI + EW);
 constexpr int MAX_STAGES = 12;
@@ -86,6 +84,7 @@ struct Args8 {
   void* out;
   uint8_t* out_codes;
   float* out_scales;
+  uint32_t* err;                // operator_flag()
 };
 
 // expert, first row, rows, weight block; tt: token tile, of all experts
@@ -396,7 +395,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         if (++stage == a.stages) { stage = 0; phase ^= 1u; }
       }
       if (!ok) {
-        if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
+        if (lane == 0) { *abort_flag = 1; atomicOr(a.err, 1u); }
         // copies and products in flight end long before this bound
         const unsigned long long t0 = gtimer();
         while (gtimer() - t0 < 1000000ull) {
@@ -435,7 +434,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
           if ((stage += 2) >= a.stages) { stage -= a.stages; phase ^= 1u; }
           if ((acc += 2) >= ACCS) { acc -= ACCS; acc_phase ^= 1u; }
         }
-        if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
+        if (!ok && lane == 0) { *abort_flag = 1; atomicOr(a.err, 1u); }
       }
     } else {
       // ---------------- scales ----------------
@@ -472,7 +471,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
           if (++slot == SCALE_SLOTS) { slot = 0; phase ^= 1u; }
         }
       }
-      if (!ok && lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
+      if (!ok && lane == 0) { *abort_flag = 1; atomicOr(a.err, 1u); }
     }
   } else {
     // ---------------- sums and epilogue: a TMEM lane is a token, a column a weight row ----------------
@@ -549,7 +548,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         rotate(phase);
       }
       if (!ok) {
-        if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
+        if (lane == 0) { *abort_flag = 1; atomicOr(a.err, 1u); }
         break;
       }
       const int4 o = heads[head];
@@ -590,7 +589,7 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(tops_full + 8 * q);
         if (!warp_wait_cta(tops_full + 8 * q, tops_phase, abort_flag)) {
-          if (lane == 0) { *abort_flag = 1; atomicOr(&g_operator_err8, 1u); }
+          if (lane == 0) { *abort_flag = 1; atomicOr(a.err, 1u); }
           break;
         }
         top = max(top, at[128 * (part ^ 1)]);
@@ -743,17 +742,6 @@ int tile8(const Args8& a, int64_t tiles) {
 
 }  // namespace
 
-moe_status operators_check8(cudaStream_t s) {
-  uint32_t err = 0;
-  CK(cudaMemcpyFromSymbolAsync(&err, g_operator_err8, sizeof(err), 0, cudaMemcpyDeviceToHost, s));
-  CK(cudaStreamSynchronize(s));
-  if (!err) return MOE_OK;
-  err = 0;
-  CK(cudaMemcpyToSymbolAsync(g_operator_err8, &err, sizeof(err), 0, cudaMemcpyHostToDevice, s));
-  CK(cudaStreamSynchronize(s));
-  return fail(MOE_EDEVICE, "a wait inside an operator kernel ran out");
-}
-
 }  // namespace moe
 
 using namespace moe;
@@ -784,6 +772,8 @@ extern "C" moe_status moe_grouped_matmul_fp8(int32_t P, int32_t E, int32_t N, in
   a.P = P; a.E = E; a.N = N; a.K = K; a.act = act; a.cols = act ? N / 2 : N; a.quant = !out; a.out_f32 = out && out_dtype == MOE_F32;
   a.few = P < 64 * (int64_t)E;
   a.sx = x_scales; a.sw = w_scales; a.offsets = offsets; a.out = out; a.out_codes = out_codes; a.out_scales = out_scales;
+  a.err = operator_flag();
+  if (!a.err) return fail(MOE_ECUDA, "the library's flag has no address on this device");
   const Mem8 mem{x_codes, w_codes};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (use_pairs8(a)) return launch8<2, 256>(a, mem, s);

@@ -11,8 +11,9 @@ constexpr int64_t kMaxPairs = 0x70000000;   // T * k: row numbers, and those a b
 // SMs of the current device (looked up once per device).
 int operator_sms();
 
-// Synchronise; whether a wait of the 8-bit products has run out (moe_operators_check).
-moe_status operators_check8(cudaStream_t s);
+// Address of the current device's flag that waits which run out set, for kernels outside grouped.cu (looked up once per device;
+// NULL where that fails).  One flag, so that moe_operators_check waits for one copy.
+uint32_t* operator_flag();
 
 __host__ __device__ __forceinline__ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
