@@ -630,6 +630,19 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 // ---------------------------------------------------------------------------
 struct Mem8 { const uint8_t *x, *w; };
 
+// Shared memory of a CTA: rows of the token area, what the largest tile of P rows can need; bytes of a stage, and of all else; stages
+struct Room8 { int x_rows, stage_bytes, fixed, stages; };
+template <int CG, int TILE>
+Room8 room8(int P, int E) {
+  Room8 m;
+  m.x_rows = CG == 2 ? 128 : std::min(128, (int)(((int64_t)P + 15) / 16 * 16));
+  m.stage_bytes = (TILE / CG + m.x_rows) * 128;
+  // behind the last stage as much as the products read past its token rows
+  m.fixed = 1024 + std::max(EW * epi_warp<CG>() + SCALE_SLOTS * SLOT * 4 + HEADS * 16 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 16 * MAX_ACCS + 32 + 16 + 8 * (E + 1), (128 - m.x_rows) * 128);
+  m.stages = stages_of<TILE>((SMEM_LIMIT - m.fixed) / m.stage_bytes);
+  return m;
+}
+
 template <int CG, int TILE>
 moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   const auto kernel = product8_kernel<CG, TILE>;
@@ -638,14 +651,12 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   a.kslices = (a.K + 127) / 128;
   a.n_blocks = (a.N + 127) / 128;
   a.whole = a.cols * (a.out_f32 ? 4 : 2) % 16 == 0;
-  // rows of the token area: what the largest tile of P rows can need
-  const int x_rows = CG == 2 ? 128 : std::min(128, (a.P + 15) / 16 * 16);
-  a.box = std::min(32, x_rows & -x_rows);
-  a.stage_bytes = (TILE / CG + x_rows) * 128;
-  // behind the last stage as much as the products read past its token rows
-  const int fixed = 1024 + std::max(EW * epi_warp<CG>() + SCALE_SLOTS * SLOT * 4 + HEADS * 16 + 2 * 2 * 128 * 4 + 16 * MAX_STAGES + 16 * SCALE_SLOTS + 16 * MAX_ACCS + 32 + 16 + 8 * (a.E + 1), (128 - x_rows) * 128);
-  a.stages = stages_of<TILE>((SMEM_LIMIT - fixed) / a.stage_bytes);
-  const size_t smem = (size_t)fixed + (size_t)a.stages * a.stage_bytes;
+  const Room8 m = room8<CG, TILE>(a.P, a.E);
+  if (m.stages < 2) return fail(MOE_EINVAL, "the table of E = %d experts leaves no room for two stages", a.E);   // a warp that issues starts at its own
+  a.box = std::min(32, m.x_rows & -m.x_rows);
+  a.stage_bytes = m.stage_bytes;
+  a.stages = m.stages;
+  const size_t smem = (size_t)m.fixed + (size_t)a.stages * a.stage_bytes;
 
   CUtensorMap tw, tx, to;
   bool ok;
@@ -733,11 +744,18 @@ bool use_pairs8(const Args8& a) { return a.P > (int64_t)(a.act ? a.K >= 4096 ? 7
 // Weight rows of a single CTA's tile: as many as leave items for half of the SMs.  With one tile a unit a call lasts as long as its slices take in
 // turn, a quarter of a microsecond and more.  us with 256, 128 and 64 rows: one row, K 7168, N 4096 23.0 / 17.2 / 15.6; 256 rows, K 2048,
 // N 7168 10.8 / 9.0 / 11.5; one row of 8 experts, K 768, N 2048 7.4 / 6.8 / 7.8.
-int tile8(const Args8& a, int64_t tiles) {
+int tile8(const Args8& a, int64_t tiles, int sms) {
   if (a.quant) return 256;   // a block of 128 features is one tile's
   int tile = 256;
-  while (tile > 64 && tiles * ((a.N + tile - 1) / tile) < operator_sms() / 2) tile /= 2;
+  while (tile > 64 && tiles * ((a.N + tile - 1) / tile) < sms / 2) tile /= 2;
   return tile;
+}
+
+// what a call runs on a device of so many SMs
+struct Form8 { int ctas, tile; };
+Form8 form8(const Args8& a, int sms) {
+  if (use_pairs8(a)) return Form8{2, 256};
+  return Form8{1, tile8(a, (a.P + 127 * (int64_t)std::min(a.P, a.E)) / 128, sms)};
 }
 
 }  // namespace
@@ -776,7 +794,17 @@ extern "C" moe_status moe_grouped_matmul_fp8(int32_t P, int32_t E, int32_t N, in
   if (!a.err) return fail(MOE_ECUDA, "the library's flag has no address on this device");
   const Mem8 mem{x_codes, w_codes};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (use_pairs8(a)) return launch8<2, 256>(a, mem, s);
-  const int tile = tile8(a, (P + 127 * (int64_t)std::min(P, E)) / 128);
-  return tile == 256 ? launch8<1, 256>(a, mem, s) : tile == 128 ? launch8<1, 128>(a, mem, s) : launch8<1, 64>(a, mem, s);
+  const Form8 f = form8(a, operator_sms());
+  return f.ctas == 2 ? launch8<2, 256>(a, mem, s) : f.tile == 256 ? launch8<1, 256>(a, mem, s) : f.tile == 128 ? launch8<1, 128>(a, mem, s) : launch8<1, 64>(a, mem, s);
+}
+
+extern "C" void moe_product8_form(int32_t P, int32_t E, int32_t N, int32_t K, int32_t act, int32_t quant, int32_t sms, int32_t* form) {
+  Args8 a{};
+  a.P = P; a.E = E; a.N = N; a.K = K; a.act = act; a.quant = quant;
+  const Form8 f = form8(a, sms);
+  const Room8 m = f.ctas == 2 ? room8<2, 256>(P, E) : f.tile == 256 ? room8<1, 256>(P, E) : f.tile == 128 ? room8<1, 128>(P, E) : room8<1, 64>(P, E);
+  form[0] = f.ctas;
+  form[1] = f.tile;
+  form[2] = m.stages;
+  form[3] = f.tile == 256 ? accs<256>() : f.tile == 128 ? accs<128>() : accs<64>();
 }

@@ -15,6 +15,10 @@ int operator_sms();
 // NULL where that fails).  One flag, so that moe_operators_check waits for one copy.
 uint32_t* operator_flag();
 
+// For tests, outside the ABI: what moe_grouped_matmul_fp8 runs for such a call on a device of so many SMs, as {CTAs a tile, weight
+// rows of a tile, stages of the ring, accumulators}.
+extern "C" void moe_product8_form(int32_t P, int32_t E, int32_t N, int32_t K, int32_t act, int32_t quant, int32_t sms, int32_t* form);
+
 __host__ __device__ __forceinline__ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // expert of a grouped row, or of a row tile: the e with first[e] <= i < first[e + 1]
