@@ -133,7 +133,8 @@ moe_status moe_dequantize_fp4(int32_t G, int32_t N, int32_t K, int32_t wdtype, c
  *   Sums are fp32 in the tensor cores' accumulators, which truncate what is added to them.  A
  *   bf16 result is one such sum over K, rounded once (2e-6 off before that at K = 2000).  For an
  *   fp32 result the accumulators take K by 256 elements, and these sums are added up with
- *   rounding (2.5e-7 off, at K = 7168 too); its SwiGLU is within 11 half units of fp32.
+ *   rounding (2.5e-7 off, at K = 7168 too); its SwiGLU is within 11 half units of fp32, or 0 where
+ *   the gate is below -87.3 and its silu under 1.1e-36.
  *   workspace: moe_grouped_matmul_workspace(P, E, K, order != NULL) bytes (0 or the rows
  *   gathered, for many rows per expert), 16-byte aligned.
  */
@@ -198,7 +199,8 @@ moe_status moe_dequantize_fp8(int32_t G, int32_t N, int32_t K, int32_t tiles, co
  *   the rows beside it.
  *   act 1: SwiGLU; w holds N/2 gate rows, then N/2 up rows (N a multiple of 128).
  *   out [P, N or N/2] in out_dtype (MOE_BF16 or MOE_F32); rows from offsets[E] on are left as they are.  silu of fp32
- *   results is within 11 half units, of others within |gate| + 10 units or 1e-18 of the gate.
+ *   results is within 11 half units, or 0 at gates below -87.3 (where it is under 1.1e-36); of others within |gate| + 10
+ *   units or 1e-18 of the gate.
  *   out NULL (act 1): the result as 8-bit rows out_codes [P, N/2], out_scales [ceil(N / 256), P], rounded from the fp32
  *   values: that of moe_quantize_fp8 up to products with reciprocals good to three units, so a code is another one where
  *   that carries a value over a rounding edge.

@@ -27,6 +27,7 @@ __device__ __forceinline__ void swiglu2(uint32_t gate0, uint32_t gate1, uint32_t
 // silu(x) = x / (1 + exp(-x)) of fp32 results, within ten half units.  exp(-x) = 2^t 2^r with t the rounded product -x log2 e and r
 // what the rounding and log2 e's own have left out, |r| < 2^-16: 2^r = 1 + r ln 2.  (65536 rows of 128 experts, K 768, N 2048,
 // MXFP4, fp32 results: 195 us, with expf and a division 293.)  Past -128 the exponential is infinite all the same, past 128 it is 0.
+// __fdividef gives 0 for a divisor past 2^126: x below -87.3, where silu is under 1.1e-36.
 __device__ __forceinline__ float silu(float x) {
   constexpr double log2e = 1.4426950408889634;
   constexpr float near = (float)log2e, rest = (float)(log2e - (double)near);   // in two parts, as Cody and Waite have it
