@@ -16,12 +16,13 @@ def test_the_check_waits_for_one_copy():
     assert len(re.findall("cudaMemcpyFromSymbolAsync", text)) == 1
 
 
-# The flag's address is looked up by a process's first 8-bit product: here that one is captured, on a stream that is not torch's own.
+# The flag's address, and how many pairs of CTAs a device holds, are looked up by a process's first 8-bit product: here that one is captured,
+# on a stream that is not torch's own.
 FIRST_CALL = """
-import torch
+import sys, torch
 import serving_layer_moe_gb300 as moe
 gen = torch.Generator(device="cuda").manual_seed(1)
-x, w = moe.quantize_fp8(torch.randn(40, 272, device="cuda", generator=gen)), moe.quantize_fp8_weights(torch.randn(384, 272, device="cuda", generator=gen))
+x, w = moe.quantize_fp8(torch.randn(int(sys.argv[1]), 272, device="cuda", generator=gen)), moe.quantize_fp8_weights(torch.randn(384, 272, device="cuda", generator=gen))
 torch.cuda.synchronize()
 g = torch.cuda.CUDAGraph()
 with torch.cuda.graph(g):
@@ -34,8 +35,10 @@ print("right")
 
 
 @pytest.mark.gpu
-def test_the_first_product_may_be_captured():
-    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=ROOT, capture_output=True, text=True, timeout=300)
+@pytest.mark.parametrize("rows", [40, 1000])
+def test_the_first_product_may_be_captured(rows):
+    """Single CTAs, and pairs."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL, str(rows)], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "right", (r.stdout[-300:], r.stderr[-2000:])
 
 
