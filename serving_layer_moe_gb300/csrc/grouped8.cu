@@ -14,7 +14,9 @@
 // slice's products.  With the features as lanes the columns' scales come from shared memory: 660 cycles with
 // broadcast loads, more with 16x256b loads, which read TMEM at half the rate (709 us for 16384 rows of 8
 // experts, K 7168, N 4096; now 317, 3.0 PFLOP/s, and 301 with nothing added up).  What it costs: a ragged tile of tokens takes a
-// whole one's products.
+// whole one's products.  These are bursts, at 1785 MHz and 727 cycles a slice; in loops of seconds power leaves 1567 MHz, 723 cycles,
+// 362 us.  Single CTAs take 736 to 777 cycles a slice at 1.33 to 1.66 GHz; with six slices a tile (K 768) it is 1240 to 1310, start and
+// end of the tile among them.
 //
 // What an epilogue warp does once a slice counts as much: two warps a scheduler hide little of it.  Scales come for four slices at a
 // time (a barrier of their own a slice: 500 us), arrivals are elected without a branch and both accumulators' addresses and
@@ -600,6 +602,8 @@ product8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const float most = fmaxf(__uint_as_float(top), kLeast8);
         const bool bad = top >= 0x7f800000u;   // a NaN or an infinity: scale NaN, codes 0
         if (part == 0 && lane < rows) a.out_scales[(size_t)o.z * a.P + token + lane] = bad ? __uint_as_float(0x7fffffffu) : most * (1.0f / 448.0f);
+        // Codes by a reciprocal good to three units, not the quantiser's rounded quotient: h carries the sums' and SwiGLU's errors, so no tie
+        // of the 8-bit grid is exact here (512 x 2048 results of K 7168: the codes are those of quantising the fp32 results, each one).
         float r;
         asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(most));
         r *= 448.0f;
@@ -735,10 +739,17 @@ moe_status launch8(Args8 a, const Mem8& mem, cudaStream_t s) {
   return MOE_OK;
 }
 
-// Pairs of CTAs take twice the tokens with the same weight rows, single ones waste less on ragged tiles.  us, pairs and single, by
-// rows an expert (128 experts, K 2048, N 1536, requantised): 192 rows 125 / 105, 512 219 / 208, 1024 388 / 359; 32 experts, K 7168,
-// N 4096, SwiGLU: 512 430 / 409, 768 545 / 557, 1024 730 / 756; 2048 rows of 8 experts without SwiGLU 333 / 384.  Pairs store their tiles under the
-// next one's products, which counts when K is short (K 768, N 2048: 256 rows 88 / 82, 512 133 / 144, 1024 232 / 266).
+// Pairs of CTAs take twice the tokens with the same weight rows, and store their tiles under the next one's products; single ones waste less on
+// ragged tiles.  us, pairs / single, by the experts' mean rows, spread as a router spreads them (bursts; in brackets loops of 0.7 s,
+// where power bounds both and pairs gain):
+//   K 768, N 2048, 128 experts                256 86 / 81, 384 111 / 112, 512 136 / 143, 1024 233 / 267
+//   K 2048, N 2048, 128                       384 217 / 211, 704 347 / 346 (387 / 406), 1024 466 / 482
+//   K 7168, N 4096, 32                        512 416 / 405, 704 531 / 519 (604 / 615), 1024 733 / 734 (829 / 873)
+//   K 7168, N 4096, 32, SwiGLU                512 445 / 415, 704 539 / 538 (608 / 638), 1024 749 / 729 (857 / 866)
+//   K 2048, N 1536, 128, requantised          512 219 / 201, 1024 385 / 369 (416 / 418), 1536 552 / 533 (597 / 599), 2048 709 / 696 (766 / 783)
+// Experts of 512 rows each, no tile ragged, are faster in pairs already (111 / 133, 222 / 241, 350 / 374, 355 / 373 in the order above); a
+// rule on sizes does not see that.  Nor does this one see how many items there are: one matrix of 1001 rows, K 7168, N 2048 takes
+// 26 us in 32 pairs, 19 single.
 bool use_pairs8(const Args8& a) { return a.P > (int64_t)(a.act ? a.K >= 4096 ? 704 : 1536 : a.K <= 1024 ? 384 : 704) * a.E; }
 
 // Weight rows of a single CTA's tile: as many as leave items for half of the SMs.  With one tile a unit a call lasts as long as its slices take in

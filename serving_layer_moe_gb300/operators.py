@@ -662,13 +662,17 @@ def _product8(x, w, groups, act, quantize, out_dtype, stream):
 def matmul_fp8(x, w, *, act="none", quantize=False, out_dtype=torch.bfloat16, stream=None):
     """x @ w.T of FP8Rows x [R, K] and FP8Weights w [N, K], in out_dtype (moe_grouped_matmul_fp8 of one matrix).
     act="swiglu": w holds gate rows, then up rows (N a multiple of 128), and the result has N/2 columns; quantize=True: that
-    result as FP8Rows, rounded from the fp32 values."""
+    result as FP8Rows, rounded from the fp32 values.
+
+    out_dtype: bf16 results are half the bytes on their way to combine_norm, and each is off by up to half a bf16 step.  The sum of
+    eight experts' rows (K 768, N 2048) is 0.0017 from 64 bits with bf16 rows and 9e-8 with fp32 ones; 8192 tokens' product takes
+    136 us and 173."""
     return _product8(x, w, None, act, quantize, out_dtype, stream)
 
 
 def grouped_matmul_fp8(x, w, groups, *, act="none", quantize=False, out_dtype=torch.bfloat16, stream=None):
     """matmul_fp8 for rows in expert order: row i of expert e is x[i] @ w[e].T, w FP8Weights [E, N, K] (moe_grouped_matmul_fp8).
-    Rows that no pair fills are undefined."""
+    Rows that no pair fills are undefined.  out_dtype: as there."""
     if not isinstance(groups, ExpertGroups):
         raise ValueError(f"groups must be ExpertGroups, is {type(groups)}")
     return _product8(x, w, groups, act, quantize, out_dtype, stream)
